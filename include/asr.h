@@ -245,6 +245,136 @@ asr_status asr_gemm_bf16_sr(const uint16_t *a, const uint16_t *b, uint16_t *c, f
                             uint64_t n, uint64_t k, uint32_t rounding, uint32_t step, uint64_t seed,
                             asr_stream_t stream);
 
+/* ------------------------------------------- orthogonalised updates (Muon)
+ *
+ * Newton-Schulz orthogonalisation.  For a matrix G (rows x cols):
+ *   X_0 = G / max(|G|_F, eps);   then `steps` times
+ *   X <- a X + (b S + c S S) X with S = X X^T        (rows <= cols)
+ *   X <- a X + X (b S + c S S) with S = X^T X        (rows >  cols)
+ * which moves every singular value towards 1 and keeps the singular vectors.
+ * The products run on the tensor cores with f16 operands (2^12 times the
+ * matrices' values) and binary32 sums; the result is rounded to bf16 once.
+ * Coefficients must keep what is stored in range: starting from singular
+ * values in [0, 1], the polynomial a x + b x^3 + c x^5 and its square, and
+ * a + b x^2 + c x^4, must stay within 8 over all steps, otherwise
+ * ASR_ERR_INVALID_VALUE (the usual 3.4445, -4.7750, 2.0315 stay below 3.5).
+ * A zero matrix gives zeros; one that holds an infinity or a NaN, or whose sum
+ * of squares overflows binary32, gives NaN throughout.  1 <= steps <= 100,
+ * 1e-30 <= eps <= 1e30, rows and cols at most 2^20. */
+typedef struct {
+    double a, b, c;
+    double eps;
+    uint32_t steps;
+    uint32_t reserved;      /* 0 */
+} asr_ns_params;
+
+/* A stack of `count` matrices: x_stride (out_stride) elements between
+ * matrices, x_ld (out_ld) between rows, both >= cols; columns contiguous. */
+typedef struct {
+    const void *x;          /* x_dtype, read only                            */
+    uint16_t *out;          /* bf16 patterns                                 */
+    uint64_t count, rows, cols;
+    uint64_t x_ld, x_stride;
+    uint64_t out_ld, out_stride;
+    int32_t x_dtype;        /* asr_dtype */
+    int32_t reserved;       /* 0 */
+} asr_matrix_desc;
+
+/* Orthogonalises every matrix of the table.  Matrices of one shape, type and
+ * row pitch are worked on together, whichever descriptors they come from.
+ * table: HOST array, read during the call only; empty descriptors are skipped.
+ * workspace: device, 256-byte aligned, at least asr_newton_schulz_workspace's
+ * bytes, not shared with work that may run at the same time; its contents
+ * are not kept between calls. */
+asr_status asr_newton_schulz(const asr_matrix_desc *table, int32_t n, const asr_ns_params *params,
+                             void *workspace, uint64_t workspace_bytes, asr_stream_t stream);
+
+/* Workspace of that call in bytes (host only; pointers are checked for
+ * alignment, which decides how matrices are grouped, but not read). */
+asr_status asr_newton_schulz_workspace(const asr_matrix_desc *table, int32_t n, uint64_t *bytes);
+
+/* How a Muon step's rate follows a matrix's shape. */
+typedef enum {
+    ASR_MUON_ADJUST_NONE = 0,       /* 1 */
+    ASR_MUON_ADJUST_SPECTRAL = 1,   /* sqrt(max(1, rows / cols)) */
+    ASR_MUON_ADJUST_RMS = 2         /* 0.2 sqrt(max(rows, cols)): AdamW's usual update size */
+} asr_muon_adjust;
+
+/* lr, weight_decay finite and >= 0; 0 <= momentum < 1; step >= 1 (Philox
+ * counter word 2). */
+typedef struct {
+    double lr, momentum, weight_decay;
+    asr_ns_params ns;
+    uint32_t nesterov;      /* 0 or 1 */
+    uint32_t adjust;        /* asr_muon_adjust */
+    uint32_t step;
+    uint32_t rounding;      /* asr_rounding */
+    uint64_t seed;
+} asr_muon_hparams;
+
+/* A stack of `count` contiguous rows x cols parameters that follow one
+ * another, their gradients and momentum buffers likewise. */
+typedef struct {
+    void *param;            /* param_dtype, updated in place                 */
+    const void *grad;       /* grad_dtype, read only                         */
+    float *momentum;        /* binary32, updated in place                    */
+    uint64_t count, rows, cols;
+    uint64_t base_index;    /* global parameter position of element 0        */
+    int32_t param_dtype;    /* asr_dtype */
+    int32_t grad_dtype;     /* asr_dtype */
+} asr_muon_desc;
+
+/* One Muon step of every matrix of the table.  With mu the momentum:
+ *   m <- m + (1 - mu) (g - m);   u = nesterov ? g + mu (m - g) : m;
+ *   O = Newton-Schulz(u) (above; kept in binary32 here, not rounded);
+ *   p <- p (1 - lr weight_decay) - (lr adjust) O
+ * the momentum in binary32 with every operation rounded on its own in this
+ * order; p is written as computed (f32) or rounded to bf16 with the random
+ * bits of its global index (stochastic, or nearest-even), as the AdamW step
+ * rounds it.  Workspace: as above, asr_muon_workspace's bytes. */
+asr_status asr_muon_sr_multi_tensor(const asr_muon_desc *table, int32_t n, const asr_muon_hparams *hp,
+                                    void *workspace, uint64_t workspace_bytes, asr_stream_t stream);
+
+asr_status asr_muon_workspace(const asr_muon_desc *table, int32_t n, uint64_t *bytes);
+
+/* ------------------------------------------------ 8-bit integer products
+ *
+ * Symmetric quantisation with one scale a row (a token, or a channel of a
+ * weight) or a column.  For each row (column) of x, rows x cols, x_ld elements
+ * between rows: top = max |x|, scale = top / 127, y = x (127 / top), and
+ *   q = rint(y)                                        ASR_ROUND_RNE
+ *   q = floor(y) + (65536 (y - floor(y)) > r)          ASR_ROUND_SR
+ * in binary32 (rows with top < 2^-64 are raised by 2^64 first), |q| <= 127;
+ * r is the low 16 bits of the Philox word of global index base_index +
+ * i * cols + j at (seed, step).  A row of zeros gives scale 0 and zeros; one
+ * that holds an infinity or a NaN gives zeros and a scale that is not finite,
+ * so that its products are NaN.
+ * ASR_ROWS: q is rows x cols, q_ld >= cols bytes between rows, scale has `rows`
+ * entries.  ASR_COLUMNS: q is stored transposed, cols x rows, q_ld >= rows, and
+ * scale has `cols` entries.  Bytes between a row's end and the next row are
+ * not written. */
+typedef enum { ASR_ROWS = 0, ASR_COLUMNS = 1 } asr_axis;
+
+asr_status asr_quantize_int8(const void *x, int32_t x_dtype, uint64_t rows, uint64_t cols, uint64_t x_ld,
+                             int32_t axis, int8_t *q, uint64_t q_ld, float *scale, uint32_t rounding,
+                             uint64_t base_index, uint32_t step, uint64_t seed, asr_stream_t stream);
+
+/* C = A . B^T in 8-bit integers: c(i, j) = (sum over k of a(i, k) b(j, k)) *
+ * a_scale[i] * b_scale[j], the sum exact, the rest in binary32 in this order.
+ * a: m x k, b: n x k (lda, ldb >= k bytes between rows); c: m x n of c_dtype,
+ * ldc elements between rows; a bf16 c is rounded as element i*n + j of
+ * asr_stochastic_round_bf16 with base index 0 at (seed, step), or to
+ * nearest-even.  1 <= k <= 131071, m and n at most 2^24; any alignment and
+ * pitch (16-byte aligned operands with pitches a multiple of 16 are read
+ * faster).  m == 0 or n == 0 is a no-op.  workspace: device, 256-byte aligned,
+ * at least asr_gemm_int8_workspace's bytes. */
+asr_status asr_gemm_int8_sr(const int8_t *a, uint64_t lda, const int8_t *b, uint64_t ldb,
+                            const float *a_scale, const float *b_scale, void *c, uint64_t ldc, int32_t c_dtype,
+                            uint64_t m, uint64_t n, uint64_t k, uint32_t rounding, uint32_t step, uint64_t seed,
+                            void *workspace, uint64_t workspace_bytes, asr_stream_t stream);
+
+asr_status asr_gemm_int8_workspace(uint64_t m, uint64_t n, uint64_t k, uint64_t *bytes);
+
 /* Static description of a status code. */
 const char *asr_status_string(asr_status status);
 
@@ -330,7 +460,11 @@ typedef enum {
     ASR_KERNEL_ROUND = 5,                    /* asr_stochastic_round_bf16 */
     ASR_KERNEL_PHILOX = 6,                   /* asr_philox4x32 */
     ASR_KERNEL_GEMM = 7,                     /* asr_gemm_bf16_sr */
-    ASR_KERNEL_KINDS = 8
+    ASR_KERNEL_MATRIX_PREP = 8,              /* Newton-Schulz and Muon: momentum, norm, scaled f16 copy */
+    ASR_KERNEL_PRODUCT = 9,                  /* f16-operand products of Newton-Schulz, Muon and the 8-bit GEMM */
+    ASR_KERNEL_QUANTIZE = 10,                /* 8-bit quantiser, and the 8-bit GEMM's widening of its operands */
+    ASR_KERNEL_INT8_FEW_ROWS = 11,           /* the 8-bit GEMM with few rows */
+    ASR_KERNEL_KINDS = 12
 } asr_kernel_kind;
 
 /* Diagnostic (no counterpart on the pages): copies into counts[k], for

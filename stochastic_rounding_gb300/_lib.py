@@ -26,10 +26,14 @@ EXPORTS = ("asr_philox4x32", "asr_stochastic_round_bf16", "asr_adamw_prepare",
            "asr_adamw_sr_step", "asr_adamw_sr_multi_tensor", "asr_status_string",
            "asr_last_cuda_error", "asr_take_device_error", "asr_selftest_wait_timeout",
            "asr_adamw_sr_multi_tensor_static", "asr_gemm_bf16_sr", "asr_take_device_error_async",
-           "asr_kernel_launches", "asr_adamw_sr_multi_tensor_host")
+           "asr_kernel_launches", "asr_adamw_sr_multi_tensor_host",
+           "asr_newton_schulz", "asr_newton_schulz_workspace", "asr_muon_sr_multi_tensor", "asr_muon_workspace",
+           "asr_quantize_int8", "asr_gemm_int8_sr", "asr_gemm_int8_workspace")
 # asr_kernel_kind, in order
 KERNEL_KINDS = ("adamw_scalar", "adamw_vector", "adamw_pipelined", "adamw_pipelined_any_base", "adamw_static",
-                "round", "philox", "gemm")
+                "round", "philox", "gemm", "matrix_prep", "product", "quantize", "int8_few_rows")
+ASR_MUON_ADJUST_NONE, ASR_MUON_ADJUST_SPECTRAL, ASR_MUON_ADJUST_RMS = 0, 1, 2
+ASR_ROWS, ASR_COLUMNS = 0, 1
 ASR_STATIC_TABLE_MAX = 4096
 
 
@@ -54,6 +58,30 @@ class TensorDesc(ctypes.Structure):
 
 class HostTensorDesc(ctypes.Structure):
     _fields_ = [("dev", TensorDesc), ("grad_host", ctypes.c_void_p), ("param_host", ctypes.c_void_p)]
+
+
+class NsParams(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_double), ("b", ctypes.c_double), ("c", ctypes.c_double), ("eps", ctypes.c_double),
+                ("steps", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class MatrixDesc(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("count", ctypes.c_uint64),
+                ("rows", ctypes.c_uint64), ("cols", ctypes.c_uint64), ("x_ld", ctypes.c_uint64),
+                ("x_stride", ctypes.c_uint64), ("out_ld", ctypes.c_uint64), ("out_stride", ctypes.c_uint64),
+                ("x_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class MuonHparams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("ns", NsParams), ("nesterov", ctypes.c_uint32), ("adjust", ctypes.c_uint32),
+                ("step", ctypes.c_uint32), ("rounding", ctypes.c_uint32), ("seed", ctypes.c_uint64)]
+
+
+class MuonDesc(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("momentum", ctypes.c_void_p),
+                ("count", ctypes.c_uint64), ("rows", ctypes.c_uint64), ("cols", ctypes.c_uint64),
+                ("base_index", ctypes.c_uint64), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
 
 
 class AsrError(RuntimeError):
@@ -90,6 +118,18 @@ def lib() -> ctypes.CDLL:
         L.asr_adamw_sr_multi_tensor_host.restype = ctypes.c_int
         L.asr_gemm_bf16_sr.argtypes = [vp, vp, vp, vp, u64, u64, u64, u32, u32, u64, vp]
         L.asr_gemm_bf16_sr.restype = ctypes.c_int
+        pu64 = ctypes.POINTER(u64)
+        L.asr_newton_schulz.argtypes = [ctypes.POINTER(MatrixDesc), i32, ctypes.POINTER(NsParams), vp, u64, vp]
+        L.asr_newton_schulz_workspace.argtypes = [ctypes.POINTER(MatrixDesc), i32, pu64]
+        L.asr_muon_sr_multi_tensor.argtypes = [ctypes.POINTER(MuonDesc), i32, ctypes.POINTER(MuonHparams), vp, u64, vp]
+        L.asr_muon_workspace.argtypes = [ctypes.POINTER(MuonDesc), i32, pu64]
+        L.asr_quantize_int8.argtypes = [vp, i32, u64, u64, u64, i32, vp, u64, vp, u32, u64, u32, u64, vp]
+        L.asr_gemm_int8_sr.argtypes = [vp, u64, vp, u64, vp, vp, vp, u64, i32, u64, u64, u64, u32, u32, u64, vp, u64,
+                                       vp]
+        L.asr_gemm_int8_workspace.argtypes = [u64, u64, u64, pu64]
+        for f in ("asr_newton_schulz", "asr_newton_schulz_workspace", "asr_muon_sr_multi_tensor",
+                  "asr_muon_workspace", "asr_quantize_int8", "asr_gemm_int8_sr", "asr_gemm_int8_workspace"):
+            getattr(L, f).restype = ctypes.c_int
         for f in ("asr_philox4x32", "asr_stochastic_round_bf16", "asr_adamw_prepare",
                   "asr_adamw_sr_step", "asr_adamw_sr_multi_tensor",
                   "asr_adamw_sr_multi_tensor_static"):
@@ -495,4 +535,248 @@ def asr_gemm_bf16_sr(a, b, c, c_f32=None, *, rounding="sr", step=0, seed=0, stre
         _check(lib().asr_gemm_bf16_sr(pa, pb, pc, pf, m, n, k, r, int(step) & 0xFFFFFFFF,
                                       int(seed) & (2**64 - 1), _stream_handle(a.device, stream)),
                "asr_gemm_bf16_sr")
+    return c
+
+
+# ------------------------------------------- orthogonalised updates (Muon)
+
+NS_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+_ADJUST = {None: ASR_MUON_ADJUST_NONE, "none": ASR_MUON_ADJUST_NONE, "original": ASR_MUON_ADJUST_SPECTRAL,
+           "match_rms_adamw": ASR_MUON_ADJUST_RMS}
+
+
+def _strided_ptr(t, name, dtypes, device=None):
+    """As ``_dev_ptr`` for a 2-D or 3-D tensor whose last dimension is
+    contiguous: (pointer, count, rows, cols, row pitch, matrix pitch)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}; the call's other tensors are on cuda:{device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}; expected one of {dtypes}")
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be a matrix or a stack of matrices (2-D or 3-D), not {t.dim()}-D")
+    rows, cols = t.shape[-2], t.shape[-1]
+    count = t.shape[0] if t.dim() == 3 else 1
+    ld = t.stride(-2) if rows > 1 else cols
+    stride = t.stride(0) if t.dim() == 3 and count > 1 else 0
+    if (cols > 1 and t.stride(-1) != 1) or ld < cols:
+        raise ValueError(f"{name}'s rows must be contiguous and must not overlap")
+    return t.data_ptr(), count, rows, cols, ld, stride
+
+
+def _workspace(workspace, need, device, stream):
+    """(pointer, bytes) of the caller's workspace, or of a new one: torch
+    memory of the call's stream, given back to torch's allocator after the
+    call (which hands it out again only to later work of that stream)."""
+    torch = _torch()
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+            raise TypeError("workspace must be a contiguous CUDA tensor")
+        if workspace.device.index != device.index:
+            raise ValueError(f"workspace is on {workspace.device}; the call's tensors are on {device}")
+        size = workspace.numel() * workspace.element_size()
+        if size < need:
+            raise ValueError(f"workspace has {size} bytes; the call needs {need}")
+        return workspace, workspace.data_ptr(), size
+    if stream is None:
+        buf = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(s):
+            buf = torch.empty(need, dtype=torch.uint8, device=device)
+    return buf, buf.data_ptr(), need
+
+
+def _ns_params(steps, coefficients, eps) -> NsParams:
+    a, b, c = (float(v) for v in coefficients)
+    steps = int(steps)
+    if not 1 <= steps <= 100:
+        raise ValueError(f"steps must be between 1 and 100, not {steps}")
+    return NsParams(a, b, c, float(eps), steps, 0)
+
+
+def _matrix_table(pairs):
+    torch = _torch()
+    arr = (MatrixDesc * len(pairs))()
+    dev = None
+    for i, (x, out) in enumerate(pairs):
+        px, count, rows, cols, ld, stride = _strided_ptr(x, f"x[{i}]", (torch.float32, torch.bfloat16), dev)
+        dev = x.get_device()
+        po, *shape, out_ld, out_stride = _strided_ptr(out, f"out[{i}]", (torch.bfloat16,), dev)
+        if tuple(x.shape) != tuple(out.shape):
+            raise ValueError(f"out[{i}] has shape {tuple(out.shape)}; x[{i}] has {tuple(x.shape)}")
+        if count > 1 and rows * cols and abs(out_stride) < (rows - 1) * out_ld + cols:
+            raise ValueError(f"out[{i}]'s matrices must not overlap")
+        if stride < 0 or out_stride < 0:
+            raise ValueError("negative strides are not supported")
+        arr[i] = MatrixDesc(px, po, count, rows, cols, ld, stride, out_ld, out_stride, _dt(x), 0)
+    return arr
+
+
+def asr_newton_schulz_workspace(pairs) -> int:
+    """Bytes of workspace that ``asr_newton_schulz`` needs for these pairs."""
+    need = ctypes.c_uint64(0)
+    table = pairs if isinstance(pairs, ctypes.Array) else _matrix_table(pairs)
+    _check(lib().asr_newton_schulz_workspace(table, len(table), ctypes.byref(need)), "asr_newton_schulz_workspace")
+    return int(need.value)
+
+
+def asr_newton_schulz(pairs, *, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, workspace=None, stream=None):
+    """Orthogonalise matrices by Newton-Schulz products.  ``pairs``: (x, out)
+    tuples of CUDA tensors of one shape, 2-D, or 3-D for a stack of matrices;
+    x float32 or bfloat16, out bfloat16, rows contiguous (any pitch).
+    Matrices of one shape and type are worked on together.  ``workspace``: a
+    CUDA tensor of at least ``asr_newton_schulz_workspace(pairs)`` bytes to use
+    instead of memory from torch's allocator."""
+    torch = _torch()
+    ns = _ns_params(steps, coefficients, eps)
+    table = _matrix_table(pairs)
+    dev = pairs[0][0].device if len(pairs) else torch.device("cuda")
+    need = asr_newton_schulz_workspace(table)
+    if need == 0:
+        _check(lib().asr_newton_schulz(table, len(table), ctypes.byref(ns), None, 0, None), "asr_newton_schulz")
+        return
+    with _on_device(dev):
+        buf, p, size = _workspace(workspace, need, dev, stream)
+        _check(lib().asr_newton_schulz(table, len(table), ctypes.byref(ns), p, size, _stream_handle(dev, stream)),
+               "asr_newton_schulz")
+
+
+def _muon_table(tensors):
+    torch = _torch()
+    arr = (MuonDesc * len(tensors))()
+    dev = None
+    for i, (p, g, m, base) in enumerate(tensors):
+        pp = _dev_ptr(p, f"param[{i}]", (torch.float32, torch.bfloat16), None, dev)
+        dev = p.get_device()
+        if p.dim() not in (2, 3):
+            raise ValueError(f"param[{i}] must be a matrix or a stack of matrices (2-D or 3-D), not {p.dim()}-D")
+        for t, what in ((g, "grad"), (m, "momentum")):
+            if tuple(t.shape) != tuple(p.shape):
+                raise ValueError(f"{what}[{i}] has shape {tuple(t.shape)}; param[{i}] has {tuple(p.shape)}")
+        arr[i] = MuonDesc(pp, _dev_ptr(g, f"grad[{i}]", (torch.float32, torch.bfloat16), None, dev),
+                          _dev_ptr(m, f"momentum[{i}]", (torch.float32,), None, dev),
+                          p.shape[0] if p.dim() == 3 else 1, p.shape[-2], p.shape[-1], int(base), _dt(p), _dt(g))
+    return arr
+
+
+def asr_muon_workspace(tensors) -> int:
+    """Bytes of workspace that ``asr_muon_sr_multi_tensor`` needs for these tensors."""
+    need = ctypes.c_uint64(0)
+    table = tensors if isinstance(tensors, ctypes.Array) else _muon_table(tensors)
+    _check(lib().asr_muon_workspace(table, len(table), ctypes.byref(need)), "asr_muon_workspace")
+    return int(need.value)
+
+
+def asr_muon_sr_multi_tensor(tensors, *, lr, momentum=0.95, weight_decay=0.1, nesterov=True, steps=5,
+                             coefficients=NS_COEFFICIENTS, eps=1e-7, adjust="original", step, seed=0, rounding="sr",
+                             workspace=None, stream=None):
+    """One Muon step in place over many matrices.  ``tensors``: (param, grad,
+    momentum, base_index) tuples of contiguous CUDA tensors of one shape, 2-D,
+    or 3-D for a stack of matrices; param and grad float32 or bfloat16,
+    momentum float32.  ``adjust`` scales lr by a matrix's shape: ``"original"``
+    (sqrt(max(1, rows/cols))), ``"match_rms_adamw"`` (0.2 sqrt(max(rows,
+    cols))) or None."""
+    torch = _torch()
+    r = _ROUNDING.get(rounding)
+    if r is None:
+        raise ValueError(f"rounding must be 'sr' or 'rne', not {rounding!r}")
+    if adjust not in _ADJUST:
+        raise ValueError(f"adjust must be 'original', 'match_rms_adamw' or None, not {adjust!r}")
+    if not 0 <= int(step) < 2**32:
+        raise ValueError("hyperparameters out of range: step must fit in 32 bits")
+    hp = MuonHparams(float(lr), float(momentum), float(weight_decay), _ns_params(steps, coefficients, eps),
+                     1 if nesterov else 0, _ADJUST[adjust], int(step), r, int(seed) & (2**64 - 1))
+    table = _muon_table(tensors)
+    dev = tensors[0][0].device if len(tensors) else torch.device("cuda")
+    need = asr_muon_workspace(table)
+    if need == 0:
+        _check(lib().asr_muon_sr_multi_tensor(table, len(table), ctypes.byref(hp), None, 0, None),
+               "asr_muon_sr_multi_tensor")
+        return
+    with _on_device(dev):
+        buf, p, size = _workspace(workspace, need, dev, stream)
+        _check(lib().asr_muon_sr_multi_tensor(table, len(table), ctypes.byref(hp), p, size,
+                                              _stream_handle(dev, stream)), "asr_muon_sr_multi_tensor")
+
+
+# ------------------------------------------------- 8-bit integer products
+
+_AXIS = {"rows": ASR_ROWS, "columns": ASR_COLUMNS}
+
+
+def _matrix_ptr(t, name, dtypes, device=None):
+    p, count, rows, cols, ld, _ = _strided_ptr(t, name, dtypes, device)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return p, rows, cols, ld
+
+
+def int8_empty(rows: int, cols: int, device="cuda"):
+    """An uninitialised int8 matrix whose rows start a multiple of 16 bytes
+    apart, as the 8-bit product reads fastest."""
+    torch = _torch()
+    return torch.empty(int(rows), (int(cols) + 15) // 16 * 16, dtype=torch.int8, device=device)[:, :int(cols)]
+
+
+def asr_quantize_int8(x, q, scale, *, axis="rows", rounding="rne", base_index: int = 0, step: int = 0, seed: int = 0,
+                      stream=None):
+    """Quantise the rows of ``x`` (float32 or bfloat16, 2-D) to 8-bit integers
+    with one scale each into ``q`` (int8, x's shape) and ``scale`` (float32);
+    with ``axis="columns"`` its columns, ``q`` being x's shape transposed.
+    ``rounding="sr"`` rounds stochastically."""
+    torch = _torch()
+    px, rows, cols, ld = _matrix_ptr(x, "x", (torch.float32, torch.bfloat16))
+    d = x.get_device()
+    pq, qrows, qcols, qld = _matrix_ptr(q, "q", (torch.int8,), d)
+    if axis not in _AXIS:
+        raise ValueError(f"axis must be 'rows' or 'columns', not {axis!r}")
+    r = _ROUNDING.get(rounding)
+    if r is None:
+        raise ValueError(f"rounding must be 'sr' or 'rne', not {rounding!r}")
+    want = (rows, cols) if axis == "rows" else (cols, rows)
+    if (qrows, qcols) != want:
+        raise ValueError(f"q has shape {(qrows, qcols)}; expected {want}")
+    ps = _dev_ptr(scale, "scale", (torch.float32,), want[0], d)
+    with _on_device(x.device):
+        _check(lib().asr_quantize_int8(px, _dt(x), rows, cols, ld, _AXIS[axis], pq, qld, ps, r,
+                                       int(base_index) & (2**64 - 1), int(step) & 0xFFFFFFFF, int(seed) & (2**64 - 1),
+                                       _stream_handle(x.device, stream)), "asr_quantize_int8")
+    return q, scale
+
+
+def asr_gemm_int8_workspace(m: int, n: int, k: int) -> int:
+    """Bytes of workspace that ``asr_gemm_int8_sr`` needs at these sizes."""
+    need = ctypes.c_uint64(0)
+    _check(lib().asr_gemm_int8_workspace(int(m), int(n), int(k), ctypes.byref(need)), "asr_gemm_int8_workspace")
+    return int(need.value)
+
+
+def asr_gemm_int8_sr(a, b, a_scale, b_scale, c, *, rounding="sr", step: int = 0, seed: int = 0, workspace=None,
+                     stream=None):
+    """C = A . B^T of 8-bit integer matrices with one scale a row of each:
+    a (m, k), b (n, k) int8, a_scale (m), b_scale (n) float32, c (m, n)
+    bfloat16 or float32; rows contiguous, any pitch."""
+    torch = _torch()
+    pa, m, k, lda = _matrix_ptr(a, "a", (torch.int8,))
+    d = a.get_device()
+    pb, n, kb, ldb = _matrix_ptr(b, "b", (torch.int8,), d)
+    pc, mc, nc, ldc = _matrix_ptr(c, "c", (torch.float32, torch.bfloat16), d)
+    if kb != k or (mc, nc) != (m, n):
+        raise ValueError(f"shapes do not chain: a {tuple(a.shape)}, b {tuple(b.shape)}, c {tuple(c.shape)}")
+    psa = _dev_ptr(a_scale, "a_scale", (torch.float32,), m, d)
+    psb = _dev_ptr(b_scale, "b_scale", (torch.float32,), n, d)
+    r = _ROUNDING.get(rounding)
+    if r is None:
+        raise ValueError(f"rounding must be 'sr' or 'rne', not {rounding!r}")
+    need = asr_gemm_int8_workspace(m, n, k)
+    with _on_device(a.device):
+        buf, pw, size = _workspace(workspace, need, a.device, stream)
+        _check(lib().asr_gemm_int8_sr(pa, lda, pb, ldb, psa, psb, pc, ldc, _dt(c), m, n, k, r,
+                                      int(step) & 0xFFFFFFFF, int(seed) & (2**64 - 1), pw, size,
+                                      _stream_handle(a.device, stream)), "asr_gemm_int8_sr")
     return c

@@ -32,8 +32,10 @@
 // This file holds the host side: argument checks, launch shapes and the C ABI.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -578,6 +580,21 @@ std::atomic<uint64_t> g_philox_ready{0}, g_round_ready{0};
 #include "host_pipeline.cuh"
 #include "static_table.cuh"
 #include "gemm_sr.cuh"
+#include "product.cuh"
+#include "muon.cuh"
+#include "int8.cuh"
+
+// The entry points that hold host tables in containers: out of host memory is
+// a status there too.
+template <typename F>
+asr_status guarded(F f)
+{
+    try {
+        return f();
+    } catch (...) {
+        return cuda_fail(cudaErrorMemoryAllocation);
+    }
+}
 
 }  // namespace
 
@@ -770,6 +787,57 @@ asr_status asr_gemm_bf16_sr(const uint16_t *a, const uint16_t *b, uint16_t *c, f
                             uint64_t k, uint32_t rounding, uint32_t step, uint64_t seed, asr_stream_t stream)
 {
     return gemm::run(a, b, c, c_f32, m, n, k, rounding, step, seed, reinterpret_cast<cudaStream_t>(stream));
+}
+
+asr_status asr_newton_schulz(const asr_matrix_desc *table, int32_t n, const asr_ns_params *params, void *workspace,
+                             uint64_t workspace_bytes, asr_stream_t stream)
+{
+    return guarded([&] {
+        return muon::newton_schulz(table, n, params, workspace, workspace_bytes,
+                                   reinterpret_cast<cudaStream_t>(stream));
+    });
+}
+
+asr_status asr_newton_schulz_workspace(const asr_matrix_desc *table, int32_t n, uint64_t *bytes)
+{
+    return guarded([&] { return muon::workspace_of(table, n, bytes); });
+}
+
+asr_status asr_muon_sr_multi_tensor(const asr_muon_desc *table, int32_t n, const asr_muon_hparams *hp, void *workspace,
+                                    uint64_t workspace_bytes, asr_stream_t stream)
+{
+    return guarded([&] {
+        return muon::step(table, n, hp, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+    });
+}
+
+asr_status asr_muon_workspace(const asr_muon_desc *table, int32_t n, uint64_t *bytes)
+{
+    return guarded([&] { return muon::workspace_of(table, n, bytes); });
+}
+
+asr_status asr_quantize_int8(const void *x, int32_t x_dtype, uint64_t rows, uint64_t cols, uint64_t x_ld, int32_t axis,
+                             int8_t *q, uint64_t q_ld, float *scale, uint32_t rounding, uint64_t base_index,
+                             uint32_t step, uint64_t seed, asr_stream_t stream)
+{
+    return int8::quantize(x, x_dtype, rows, cols, x_ld, axis, q, q_ld, scale, rounding, base_index, step, seed,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+asr_status asr_gemm_int8_sr(const int8_t *a, uint64_t lda, const int8_t *b, uint64_t ldb, const float *a_scale,
+                            const float *b_scale, void *c, uint64_t ldc, int32_t c_dtype, uint64_t m, uint64_t n,
+                            uint64_t k, uint32_t rounding, uint32_t step, uint64_t seed, void *workspace,
+                            uint64_t workspace_bytes, asr_stream_t stream)
+{
+    return int8::gemm(a, lda, b, ldb, a_scale, b_scale, c, ldc, c_dtype, m, n, k, rounding, step, seed, workspace,
+                      workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+asr_status asr_gemm_int8_workspace(uint64_t m, uint64_t n, uint64_t k, uint64_t *bytes)
+{
+    if (!bytes || !int8::sizes_ok(m, n, k)) return ASR_ERR_INVALID_VALUE;
+    *bytes = m && n && k ? int8::layout(m, n, k).bytes : 0;
+    return ASR_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,656 @@
+// product.cuh -- batched matrix products with f16 operands on the
+// 5th-generation tensor cores, the core of the Newton-Schulz orthogonalisation
+// (muon.cuh) and of the 8-bit integer product (int8.cuh).  Included into
+// asr.cu (inside its anonymous namespace), after gemm_sr.cuh, whose cluster,
+// barrier and tensor-map helpers it uses.
+//
+// out_z = epilogue(A_z . B_z^T) for the matrices z of a stack, with binary32
+// sums.  The shape is gemm_sr.cuh's two-SM kernel: 256 x 256 tiles on clusters
+// of two CTAs, tcgen05.mma.cta_group::2 (kind::f16), 128-deep K slices in a
+// 3-stage ring of 64 KB, two TMEM accumulators.  What differs:
+//   - operands are f16, in a workspace that the library lays out itself (rows
+//     a multiple of 32 bytes apart), so every size and alignment of the
+//     caller's matrices takes this one path;
+//   - an operand is stored with the contraction contiguous ("K-major") or
+//     across it ("MN-major"): X X^T and B X, or X^T X and X B, are formed from
+//     the one row-major X, and nothing is ever transposed in memory;
+//   - a product whose result is symmetric computes the tiles on and above the
+//     diagonal and writes each of the others as a mirror image: half the work;
+//   - the sum over K may be cut into chunks, each accumulated on its own and
+//     added up by the epilogue in int32 (8-bit integers, whose chunk sums are
+//     exact in binary32).
+//
+// A K-half of a stage (64 of K, 16 KB an operand and CTA) in shared memory:
+//   K-major    128 rows of 128 bytes, 128-byte swizzle; a K=16 step is 32 bytes;
+//   MN-major   two blocks of 64 rows' columns: 64 K-lines of 128 bytes each
+//              (64 values across), 128-byte swizzle; groups of 8 K-lines are
+//              1,024 bytes apart (stride offset), the blocks 8,192 (leading
+//              offset); a K=16 step is 2,048 bytes.
+
+namespace prod {
+
+using gemm::cluster_rank;
+using gemm::cluster_sync;
+using gemm::mbar_arrive_remote;
+using gemm::mbar_wait_cluster;
+using gemm::mma_bf16_pair;          // the instruction descriptor names the operand type
+using gemm::mma_commit_pair;
+using gemm::pair_wait;
+using gemm::peer_addr;
+using gemm::st_global_v8;
+using gemm::tile_coords;
+
+constexpr int kTile = 256;                      // tile rows and columns of a CTA pair
+constexpr int kBK = 128;                        // K per stage, two halves of 64
+constexpr int kStages = 3;
+constexpr int kEpi = 8;                         // epilogue warps: two per TMEM lane quarter
+constexpr int kThreads = 64 + 32 * kEpi;
+constexpr int kSpan = kTile / (kEpi / 4);       // columns per epilogue warp
+constexpr uint32_t kHalfBytes = 128 * 64 * 2;   // a K-half of one operand in one CTA
+constexpr uint32_t kStageBytes = 4 * kHalfBytes;
+constexpr int kAccBufs = 2;
+constexpr uint32_t kTmemCols = kTile * kAccBufs;
+constexpr int kBars = kStages * 3 + 2 * kAccBufs + 1;
+constexpr int kSmem = 1024 + kStages * kStageBytes + kBars * 8 + 16;
+constexpr int kGroupM = 8;
+constexpr int kMaxBatch = 64;                   // matrices per launch
+
+// What the epilogue makes of a sum.  "Stored" values are f16 at 2^12 times the
+// matrix (see muon.cuh).
+enum Op {
+    kGram,      // stored S = alpha * sum, symmetric
+    kPoly,      // stored P = alpha * sum + beta * (stored S) + diag on the diagonal, symmetric
+    kNext,      // stored X' = alpha * sum
+    kOut,       // caller's bf16 matrix = alpha * sum, to nearest
+    kParam,     // caller's parameter p = p * beta - alpha * sum, f32 or rounded to bf16
+    kInt8       // caller's matrix = sum * row scale * column scale
+};
+
+struct Slot {                       // one matrix of the stack: the caller's
+    void *ptr;
+    uint64_t base;                  // global index of its first element (kParam)
+};
+
+struct Params {
+    uint32_t m, n, k, batch;
+    uint32_t tiles_m, tiles_n, per_matrix;
+    uint32_t wide, narrow;          // work items: whole tiles, then halves of the last ones
+    uint32_t chunk;                 // K slices per accumulation
+    float alpha, beta, diag;
+    uint32_t ld;                    // stored output (and S): elements between rows
+    uint64_t stride;                // and between matrices
+    __half *out;
+    const __half *aux;
+    // the caller's output
+    uint64_t out_ld;
+    uint32_t out_dtype;             // asr_dtype
+    uint32_t rounding;              // asr_rounding
+    uint32_t vec;                   // rows are 32-byte aligned throughout: 256-bit accesses
+    uint32_t step;
+    const float *row_scale, *col_scale;
+    RoundKeys keys;
+    Slot slot[kMaxBatch];
+};
+
+__host__ __device__ constexpr uint32_t instr_desc(uint32_t n, bool a_mn, bool b_mn)
+{
+    return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((n >> 3) << 17) |
+           (uint32_t(kTile >> 4) << 24);
+}
+
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr)
+{
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(MN ? 8192u >> 4 : 1u) << 16) |
+           ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z,
+                                                 uint32_t cluster_bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(cluster_bar)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float2 unpack_f16(uint32_t w)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// Tile w of a matrix whose result is symmetric: column nt of the upper
+// triangle holds nt + 1 tiles.
+__device__ __forceinline__ void triangle_coords(uint32_t w, uint32_t &mt, uint32_t &nt)
+{
+    uint32_t c = static_cast<uint32_t>((sqrtf(8.0f * static_cast<float>(w) + 1.0f) - 1.0f) * 0.5f);
+    while (c * (c + 1) / 2 > w) --c;
+    while ((c + 1) * (c + 2) / 2 <= w) ++c;
+    nt = c;
+    mt = w - c * (c + 1) / 2;
+}
+
+struct Item {
+    uint32_t z, m0, n0, width;
+    bool mirror;
+};
+
+template <bool SYM>
+__device__ __forceinline__ Item work_item(const Params &P, uint32_t t)
+{
+    Item it;
+    uint32_t whole = t, half = 0;
+    it.width = kTile;
+    if (t >= P.wide) {
+        whole = P.wide + (t - P.wide) / 2;
+        half = (t - P.wide) & 1u;
+        it.width = kTile / 2;
+    }
+    it.z = whole / P.per_matrix;
+    uint32_t mt, nt;
+    if (SYM) triangle_coords(whole % P.per_matrix, mt, nt);
+    else tile_coords(whole % P.per_matrix, P.tiles_m, P.tiles_n, mt, nt, kGroupM);
+    it.m0 = mt * kTile;
+    it.n0 = nt * kTile + half * (kTile / 2);
+    it.mirror = SYM && mt != nt;
+    return it;
+}
+
+// The 16 random words of elements e .. e+15.
+__device__ __forceinline__ void words16(uint64_t e, uint32_t step, const RoundKeys &K, uint32_t r[16])
+{
+    if ((e & 3u) == 0) {
+        unit_words<true>(e, 0, step, K, r);
+        unit_words<true>(e + 8, 0, step, K, r + 8);
+    } else {
+        unit_words<false>(e, 0, step, K, r);
+        unit_words<false>(e + 8, 0, step, K, r + 8);
+    }
+}
+
+__device__ __forceinline__ void ld_global_v8(const void *p, uint32_t w[8])
+{
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p)
+                 : "memory");
+}
+
+// 16 values of one row to a bf16 matrix (dst: their place in it); `live` of
+// them are inside the matrix; random bits of elements e .. e+15.
+__device__ __forceinline__ void store_bf16(uint16_t *dst, const float x[16], int live, bool vec, uint32_t rounding,
+                                           uint64_t e, uint32_t step, const RoundKeys &K)
+{
+    uint32_t w[8];
+    if (rounding == ASR_ROUND_SR) {
+        uint32_t r[16];
+        words16(e, step, K, r);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) w[q] = sr_pack2<true>(x[2 * q], x[2 * q + 1], r[2 * q], r[2 * q + 1]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) w[q] = pack_bf16(round_rne(x[2 * q]), round_rne(x[2 * q + 1]));
+    }
+    if (vec && live >= 16) {
+        st_global_v8(dst, w);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+            if (q < live) dst[q] = static_cast<uint16_t>(w[q >> 1] >> ((q & 1) * 16));
+    }
+}
+
+__device__ __forceinline__ void store_f32(float *dst, const float x[16], int live, bool vec)
+{
+    if (vec && live >= 16) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            reinterpret_cast<float4 *>(dst)[q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+            if (q < live) dst[q] = x[q];
+    }
+}
+
+// 16 sums of row `row`, columns col .. col+15, to the output.  Sums of
+// columns past n (operands read as zeros there) are zero; rows past m are
+// skipped by the caller.
+template <int OP>
+__device__ __forceinline__ void store_sums(const Params &P, const Item &it, uint32_t row, uint32_t col, float x[16])
+{
+    if constexpr (OP == kGram || OP == kPoly || OP == kNext) {
+        __half *mat = P.out + it.z * P.stride;
+        const uint64_t at = static_cast<uint64_t>(row) * P.ld + col;
+        if constexpr (OP == kPoly) {
+            uint32_t s[8];
+            ld_global_v8(P.aux + it.z * P.stride + at, s);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const float2 v = unpack_f16(s[q]);
+                x[2 * q] = fmaf(P.alpha, x[2 * q], P.beta * v.x);
+                x[2 * q + 1] = fmaf(P.alpha, x[2 * q + 1], P.beta * v.y);
+            }
+            const uint32_t d = row - col;
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                if (d == static_cast<uint32_t>(q)) x[q] += P.diag;
+        } else {
+#pragma unroll
+            for (int q = 0; q < 16; ++q) x[q] *= P.alpha;
+        }
+        uint32_t w[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) w[q] = pack_f16(x[2 * q], x[2 * q + 1]);
+        st_global_v8(mat + at, w);
+        if (OP != kNext && it.mirror) {
+            uint16_t *dst = reinterpret_cast<uint16_t *>(mat) + static_cast<uint64_t>(col) * P.ld + row;
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                if (col + q < P.n) dst[static_cast<uint64_t>(q) * P.ld] = static_cast<uint16_t>(w[q >> 1] >> ((q & 1) * 16));
+        }
+    } else {
+        const int live = P.n - col < 16 ? static_cast<int>(P.n - col) : 16;
+        const Slot &S = P.slot[it.z];
+        const uint64_t at = static_cast<uint64_t>(row) * P.out_ld + col;
+        const uint64_t e = S.base + static_cast<uint64_t>(row) * P.n + col;
+        if constexpr (OP == kParam) {
+            if (P.out_dtype == ASR_BF16) {
+                uint16_t *p = static_cast<uint16_t *>(S.ptr) + at;
+                uint32_t w[8];
+                if (P.vec && live >= 16) {
+                    ld_global_v8(p, w);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        w[q] = (2 * q < live ? p[2 * q] : 0u) | (2 * q + 1 < live ? static_cast<uint32_t>(p[2 * q + 1]) << 16 : 0u);
+                }
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    x[2 * q] = __fsub_rn(__fmul_rn(bf16_lo(w[q]), P.beta), __fmul_rn(P.alpha, x[2 * q]));
+                    x[2 * q + 1] = __fsub_rn(__fmul_rn(bf16_hi(w[q]), P.beta), __fmul_rn(P.alpha, x[2 * q + 1]));
+                }
+                store_bf16(p, x, live, P.vec, P.rounding, e, P.step, P.keys);
+            } else {
+                float *p = static_cast<float *>(S.ptr) + at;
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+                    x[q] = __fsub_rn(__fmul_rn(q < live ? p[q] : 0.0f, P.beta), __fmul_rn(P.alpha, x[q]));
+                store_f32(p, x, live, P.vec);
+            }
+        } else {
+            if constexpr (OP == kInt8) {
+                const float rs = P.row_scale[row];
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+                    x[q] = __fmul_rn(__fmul_rn(x[q], rs), q < live ? __ldg(P.col_scale + col + q) : 0.0f);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 16; ++q) x[q] *= P.alpha;
+            }
+            if (P.out_dtype == ASR_BF16)
+                store_bf16(static_cast<uint16_t *>(S.ptr) + at, x, live, P.vec, P.rounding, e, P.step, P.keys);
+            else
+                store_f32(static_cast<float *>(S.ptr) + at, x, live, P.vec);
+        }
+    }
+}
+
+// Persistent over work items: cluster c takes items c, c + clusters, ...
+// The roles and barriers are those of gemm_sr.cuh's pair kernel.
+template <bool A_MN, bool B_MN, int OP>
+__global__ void __launch_bounds__(kThreads, 1)
+product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+               const __grid_constant__ CUtensorMap map_b_half, const __grid_constant__ Params P, uint64_t limit_ns)
+{
+    constexpr bool kSym = OP == kGram || OP == kPoly;
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    const uint32_t bars = base + kStages * kStageBytes;
+    auto full = [&](int s) { return bars + 8u * s; };
+    auto empty = [&](int s, int j) { return bars + 8u * (kStages + 2 * s + j); };
+    auto acc_full = [&](int b) { return bars + 8u * (3 * kStages + b); };
+    auto acc_empty = [&](int b) { return bars + 8u * (3 * kStages + kAccBufs + b); };
+    const uint32_t drained = bars + 8u * (kBars - 1);
+    const uint32_t tmem_slot = drained + 8u;
+    const uint32_t *tmem_slot_ptr = reinterpret_cast<const uint32_t *>(smem_raw + (tmem_slot - raw));
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const bool leader = rank == 0;
+    const uint32_t cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+    const uint32_t items = P.wide + P.narrow;
+    const uint32_t kblocks = (P.k + kBK - 1) / kBK;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s, 0), 1);
+            mbar_init(empty(s, 1), 1);
+        }
+        for (int b = 0; b < kAccBufs; ++b) {
+            mbar_init(acc_full(b), 1);
+            mbar_init(acc_empty(b), 2 * kEpi);
+        }
+        mbar_init(drained, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tmem_slot),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    }
+    cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = *tmem_slot_ptr;
+    // the operands may be the previous kernel's output
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------------- producer
+        uint32_t g = 0, s = 0, phase = 0;
+        bool wrapped = false, ok = true;
+        const uint32_t full0 = peer_addr(full(0), 0);
+        for (uint32_t t = cluster; ok && t < items; t += clusters) {
+            const Item it = work_item<kSym>(P, t);
+            const bool half = it.width != kTile;
+            uint32_t ra = it.m0 + rank * 128, rb = it.n0 + rank * (it.width / 2);
+            // rows wholly past the matrix: any rows do, their sums are not stored
+            const bool a2 = ra + 64 < P.m, b2 = rb + 64 < P.n;
+            if (ra >= P.m) ra = 0;
+            if (rb >= P.n) rb = 0;
+            const uint32_t bytes = 4 * (kHalfBytes + (half ? kHalfBytes / 2 : kHalfBytes));
+            const int32_t z = static_cast<int32_t>(it.z);
+            for (uint32_t kb = 0; kb < kblocks; ++kb, ++g) {
+                const uint32_t bar = full0 + 8u * s;
+                const uint32_t dst = base + s * kStageBytes;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (wrapped && !pair_wait(empty(s, j), phase ^ 1u, limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    if (j == 0 && leader) mbar_arrive_expect_tx(full(s), bytes);
+                    const int32_t k0 = static_cast<int32_t>(kb * kBK + j * 64);
+                    const uint32_t da = dst + j * kHalfBytes, db = dst + (2 + j) * kHalfBytes;
+                    if (A_MN) {
+                        tma_load_3d_pair(da, &map_a, static_cast<int32_t>(ra), k0, z, bar);
+                        tma_load_3d_pair(da + 8192, &map_a, static_cast<int32_t>(a2 ? ra + 64 : ra), k0, z, bar);
+                    } else {
+                        tma_load_3d_pair(da, &map_a, k0, static_cast<int32_t>(ra), z, bar);
+                    }
+                    if (B_MN) {
+                        tma_load_3d_pair(db, &map_b, static_cast<int32_t>(rb), k0, z, bar);
+                        if (!half)
+                            tma_load_3d_pair(db + 8192, &map_b, static_cast<int32_t>(b2 ? rb + 64 : rb), k0, z, bar);
+                    } else {
+                        tma_load_3d_pair(db, half ? &map_b_half : &map_b, k0, static_cast<int32_t>(rb), z, bar);
+                    }
+                }
+                if (!ok) break;
+                if (++s == kStages) {
+                    s = 0;
+                    phase ^= 1u;
+                    wrapped = true;
+                }
+            }
+        }
+        for (uint32_t q = 0; q < static_cast<uint32_t>(kStages) && q < g; ++q) {
+            const uint32_t last_use = (g - 1 - q) / kStages;
+            for (int j = 0; j < 2; ++j) pair_wait(empty(static_cast<int>(q), j), last_use & 1u, limit_ns);
+        }
+    } else if (warp == 1 && lane == 0 && leader) {
+        // ------------------------------------------------------ MMA issuer
+        uint32_t s = 0, phase = 0, i = 0;
+        bool ok = true;
+        constexpr uint32_t kDescWide = instr_desc(kTile, A_MN, B_MN), kDescNarrow = instr_desc(kTile / 2, A_MN, B_MN);
+        const uint64_t desc_a0 = operand_desc<A_MN>(base), desc_b0 = operand_desc<B_MN>(base + 2 * kHalfBytes);
+        constexpr uint64_t kDescStage = kStageBytes >> 4, kDescHalf = kHalfBytes >> 4;
+        constexpr uint64_t kStepA = A_MN ? 2048 >> 4 : 32 >> 4, kStepB = B_MN ? 2048 >> 4 : 32 >> 4;
+        for (uint32_t t = cluster; ok && t < items; t += clusters) {
+            const uint32_t idesc = t < P.wide ? kDescWide : kDescNarrow;
+            for (uint32_t kc = 0; ok && kc < kblocks; kc += P.chunk, ++i) {
+                const int b = static_cast<int>(i % kAccBufs);
+                const uint32_t ub = i / kAccBufs;
+                if (ub > 0 && !mbar_wait_cluster(acc_empty(b), (ub - 1) & 1u, limit_ns)) {
+                    ok = false;
+                    break;
+                }
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t d = tmem + static_cast<uint32_t>(b * kTile);
+                const uint32_t kend = kblocks - kc < P.chunk ? kblocks : kc + P.chunk;
+                for (uint32_t kb = kc; kb < kend; ++kb) {
+                    if (!pair_wait(full(s), phase, limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint64_t ad = desc_a0 + s * kDescStage, bd = desc_b0 + s * kDescStage;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint64_t aj = ad + j * kDescHalf, bj = bd + j * kDescHalf;
+                        mma_bf16_pair(d, aj, bj, idesc, (kb != kc || j != 0) ? 1u : 0u);
+                        mma_bf16_pair(d, aj + kStepA, bj + kStepB, idesc, 1u);
+                        mma_bf16_pair(d, aj + 2 * kStepA, bj + 2 * kStepB, idesc, 1u);
+                        mma_bf16_pair(d, aj + 3 * kStepA, bj + 3 * kStepB, idesc, 1u);
+                        mma_commit_pair(empty(s, j));
+                    }
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+                mma_commit_pair(acc_full(b));
+            }
+        }
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(drained)
+                     : "memory");
+        pair_wait(drained, 0, limit_ns);
+    } else if (warp >= 2) {
+        // ------------------------------------------------------- epilogue
+        const int quarter = warp & 3;
+        const uint32_t c_lo = static_cast<uint32_t>((warp - 2) / 4) * kSpan;
+        uint32_t i = 0;
+        bool ok = true;
+        for (uint32_t t = cluster; ok && t < items; t += clusters) {
+            const Item it = work_item<kSym>(P, t);
+            const uint32_t row = it.m0 + rank * 128 + quarter * 32 + lane;
+            const uint32_t ncols = it.n0 >= P.n ? 0 : P.n - it.n0 < it.width ? P.n - it.n0 : it.width;
+            const uint32_t c_hi = ncols < c_lo + kSpan ? ncols : c_lo + kSpan;
+            int32_t acc[OP == kInt8 ? kSpan : 1];
+            for (uint32_t kc = 0; kc < kblocks; kc += P.chunk, ++i) {
+                const int b = static_cast<int>(i % kAccBufs);
+                if (!__all_sync(0xFFFFFFFFu, pair_wait(acc_full(b), (i / kAccBufs) & 1u, limit_ns))) {
+                    ok = false;
+                    break;
+                }
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t tq =
+                    tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(b * kTile) + c_lo;
+                const bool last = kblocks - kc <= P.chunk;
+#pragma unroll
+                for (int c = 0; c < kSpan; c += 16) {
+                    if (c_lo + c >= c_hi) continue;             // the same for the whole warp
+                    uint32_t v[16];
+                    gemm::tmem_ld16(tq + c, v);
+                    float x[16];
+                    if constexpr (OP == kInt8) {
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            const int32_t a = __float2int_rn(__uint_as_float(v[q]));
+                            acc[c + q] = kc == 0 ? a : acc[c + q] + a;
+                        }
+                        if (!last) continue;
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) x[q] = __int2float_rn(acc[c + q]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) x[q] = __uint_as_float(v[q]);
+                    }
+                    if (row < P.m) store_sums<OP>(P, it, row, it.n0 + c_lo + c, x);
+                }
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(peer_addr(acc_empty(b), 0));
+            }
+        }
+    }
+    // ------------------------------------------------------------ cleanup
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncwarp();
+    cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
+                     : "memory");
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+// Shared-memory opt-in and resident pairs, set up for every form of the kernel
+// on a device's first product, so that later ones may be captured into graphs.
+std::mutex g_prod_mu;
+bool g_prod_ready[kMaxDevices];
+int g_prod_pairs[kMaxDevices];
+
+template <bool A_MN, bool B_MN, int OP>
+cudaError_t setup_one(int sms, int *pairs)
+{
+    cudaError_t e = cudaFuncSetAttribute(product_kernel<A_MN, B_MN, OP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(sms & ~1), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, product_kernel<A_MN, B_MN, OP>, &cfg);
+    if (e == cudaSuccess && (*pairs == 0 || n < *pairs)) *pairs = n;
+    return e;
+}
+
+asr_status setup(int *pairs)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (dev < 0 || dev >= kMaxDevices) return ASR_ERR_INVALID_VALUE;
+    std::lock_guard<std::mutex> lk(g_prod_mu);
+    if (!g_prod_ready[dev]) {
+        int sms = 0, n = 0;
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess) e = setup_one<false, false, kGram>(sms, &n);
+        if (e == cudaSuccess) e = setup_one<true, true, kGram>(sms, &n);
+        if (e == cudaSuccess) e = setup_one<false, false, kPoly>(sms, &n);
+        if (e == cudaSuccess) e = setup_one<false, true, kNext>(sms, &n);
+        if (e == cudaSuccess) e = setup_one<false, false, kNext>(sms, &n);
+        if (e == cudaSuccess) e = setup_one<false, true, kOut>(sms, &n);
+        if (e == cudaSuccess) e = setup_one<false, false, kOut>(sms, &n);
+        if (e == cudaSuccess) e = setup_one<false, true, kParam>(sms, &n);
+        if (e == cudaSuccess) e = setup_one<false, false, kParam>(sms, &n);
+        if (e == cudaSuccess) e = setup_one<false, false, kInt8>(sms, &n);
+        if (e != cudaSuccess) return cuda_fail(e);
+        if (n < 1) return cuda_fail(cudaErrorNotSupported);
+        g_prod_pairs[dev] = n;
+        g_prod_ready[dev] = true;
+    }
+    *pairs = g_prod_pairs[dev];
+    return ASR_OK;
+}
+
+// A stack of row-major f16 matrices (rows x cols, ld elements between rows,
+// stride between matrices) in boxes of box_rows x 64.
+asr_status make_map(CUtensorMap *map, const void *ptr, uint64_t rows, uint64_t cols, uint64_t ld, uint64_t stride,
+                    uint64_t batch, uint32_t box_rows)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    asr_status st = gemm::encoder(&enc);
+    if (st != ASR_OK) return st;
+    const cuuint64_t dims[3] = {cols, rows, batch};
+    const cuuint64_t strides[2] = {ld * 2, stride * 2};
+    const cuuint32_t box[3] = {64, box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? ASR_OK : ASR_ERR_INVALID_VALUE;
+}
+
+// One stored stack of matrices: f16, rows a multiple of 32 bytes apart.
+struct Stored {
+    __half *ptr;
+    uint64_t rows, cols, ld, stride;
+};
+
+// Launches the product of a (m x k, or k x m where A_MN) and b (n x k, or
+// k x n where B_MN); P's sizes and schedule are filled in here.
+template <bool A_MN, bool B_MN, int OP>
+asr_status launch(const Stored &a, const Stored &b, Params &P, int kind, cudaStream_t stream)
+{
+    int pairs = 0;
+    asr_status st = setup(&pairs);
+    if (st != ASR_OK) return st;
+    P.m = static_cast<uint32_t>(A_MN ? a.cols : a.rows);
+    P.k = static_cast<uint32_t>(A_MN ? a.rows : a.cols);
+    P.n = static_cast<uint32_t>(B_MN ? b.cols : b.rows);
+    P.tiles_m = (P.m + kTile - 1) / kTile;
+    P.tiles_n = (P.n + kTile - 1) / kTile;
+    constexpr bool kSym = OP == kGram || OP == kPoly;
+    const uint64_t per = kSym ? static_cast<uint64_t>(P.tiles_m) * (P.tiles_m + 1) / 2
+                              : static_cast<uint64_t>(P.tiles_m) * P.tiles_n;
+    const uint64_t tiles = per * P.batch;
+    if (tiles >= (1ull << 30)) return ASR_ERR_INVALID_VALUE;
+    P.per_matrix = static_cast<uint32_t>(per);
+    // as in gemm_sr.cuh: the tiles of a last round that is at most half full go as halves
+    uint64_t rest = tiles % static_cast<uint64_t>(pairs);
+    if (2 * rest > static_cast<uint64_t>(pairs)) rest = 0;
+    P.wide = static_cast<uint32_t>(tiles - rest);
+    P.narrow = static_cast<uint32_t>(2 * rest);
+    const uint64_t items = P.wide + static_cast<uint64_t>(P.narrow);
+    const unsigned clusters = static_cast<unsigned>(items < static_cast<uint64_t>(pairs) ? items : pairs);
+    CUtensorMap ma, mb, mbh;
+    st = make_map(&ma, a.ptr, a.rows, a.cols, a.ld, a.stride, P.batch, A_MN ? 64 : 128);
+    if (st == ASR_OK) st = make_map(&mb, b.ptr, b.rows, b.cols, b.ld, b.stride, P.batch, B_MN ? 64 : 128);
+    if (st == ASR_OK) st = make_map(&mbh, b.ptr, b.rows, b.cols, b.ld, b.stride, P.batch, 64);
+    if (st != ASR_OK) return st;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(2 * clusters, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const uint64_t limit = kWaitLimitNs;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, product_kernel<A_MN, B_MN, OP>, ma, mb, mbh, P, limit);
+    if (e != cudaSuccess) return cuda_fail(e);
+    return launched(kind);
+}
+
+}  // namespace prod

@@ -1,0 +1,94 @@
+"""A linear layer whose three products run in 8-bit integers.
+
+    y  = x W^T       tokens and weight rows quantised, one scale each, to nearest
+    dx = dy W        dy's rows and W's columns
+    dw = dy^T x      dy's columns and x's columns
+
+The gradient operand is rounded stochastically, so that what it contributes is
+unbiased; the others to nearest.  Sums of integers are exact; outputs are bf16.
+The weight itself stays bf16 (or float32) and is what an optimizer of this
+package updates.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _lib
+from ._lib import asr_gemm_int8_sr, asr_quantize_int8, int8_empty
+
+
+def _quantised(x, axis="rows", **kw):
+    rows, cols = x.shape if axis == "rows" else (x.shape[1], x.shape[0])
+    q = int8_empty(rows, cols, x.device)
+    scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    return asr_quantize_int8(x, q, scale, axis=axis, **kw)
+
+
+def int8_linear(x, qweight, weight_scale, *, rounding="rne", step: int = 0, seed: int = 0, out=None):
+    """``x`` (tokens, k), float32 or bfloat16, times the transpose of an int8
+    weight (n, k) with one scale a row: (tokens, n), bfloat16 unless ``out`` says
+    otherwise.  ``rounding="sr"`` rounds the outputs stochastically."""
+    if out is None:
+        out = torch.empty(x.shape[0], qweight.shape[0], dtype=torch.bfloat16, device=x.device)
+    q, scale = _quantised(x)
+    return asr_gemm_int8_sr(q, qweight, scale, weight_scale, out, rounding=rounding, step=step, seed=seed)
+
+
+def int8_linear_grads(dy, x, weight, *, step: int = 0, seed: int = 0, need_dx=True, need_dw=True):
+    """Gradients of ``y = x weight^T`` from ``dy`` (tokens, n): (dx, dw) in
+    bfloat16, either None where it is not needed."""
+    dx = dw = None
+    tokens, n = dy.shape
+    k = x.shape[1]
+    if need_dx:
+        dx = torch.empty(tokens, k, dtype=torch.bfloat16, device=dy.device)
+        q, s = _quantised(dy, rounding="sr", step=step, seed=seed)
+        v, t = _quantised(weight, "columns")
+        asr_gemm_int8_sr(q, v, s, t, dx, rounding="rne")
+    if need_dw:
+        dw = torch.empty(n, k, dtype=torch.bfloat16, device=dy.device)
+        q, s = _quantised(dy, "columns", rounding="sr", step=step, seed=seed)
+        v, t = _quantised(x, "columns")
+        asr_gemm_int8_sr(q, v, s, t, dw, rounding="rne")
+    return dx, dw
+
+
+class _Int8LinearFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, step, seed):
+        ctx.save_for_backward(x, weight)
+        ctx.key = (step, seed)
+        q, scale = _quantised(weight)
+        return int8_linear(x, q, scale)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight = ctx.saved_tensors
+        step, seed = ctx.key
+        dx, dw = int8_linear_grads(dy.contiguous(), x, weight, step=step, seed=seed, need_dx=ctx.needs_input_grad[0],
+                                   need_dw=ctx.needs_input_grad[1])
+        return (dx.to(x.dtype) if dx is not None else None, dw.to(weight.dtype) if dw is not None else None, None,
+                None)
+
+
+class Int8Linear(torch.nn.Module):
+    """``torch.nn.Linear`` without a bias on the 8-bit products: a bf16 (or
+    float32) weight of shape (out_features, in_features), quantised in every
+    forward pass.  ``seed`` keys the stochastic rounding of the gradients; it
+    is drawn anew for every forward pass of the layer (the pass's number is the
+    Philox step), so a run repeats bit for bit."""
+
+    def __init__(self, in_features: int, out_features: int, *, seed: int = 0, device=None, dtype=torch.bfloat16):
+        super().__init__()
+        self.in_features, self.out_features, self.seed, self.calls = in_features, out_features, int(seed), 0
+        self.weight = torch.nn.Parameter(torch.empty(out_features, in_features, device=device, dtype=dtype))
+        torch.nn.init.normal_(self.weight, std=in_features ** -0.5)
+
+    def forward(self, x):
+        self.calls += 1
+        flat = x.reshape(-1, self.in_features)
+        y = _Int8LinearFunction.apply(flat, self.weight, self.calls, self.seed)
+        return y.reshape(*x.shape[:-1], self.out_features)
+
+    def extra_repr(self):
+        return f"in_features={self.in_features}, out_features={self.out_features}, seed={self.seed}"
