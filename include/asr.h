@@ -367,13 +367,40 @@ asr_status asr_quantize_int8(const void *x, int32_t x_dtype, uint64_t rows, uint
  * nearest-even.  1 <= k <= 131071, m and n at most 2^24; any alignment and
  * pitch (16-byte aligned operands with pitches a multiple of 16 are read
  * faster).  m == 0 or n == 0 is a no-op.  workspace: device, 256-byte aligned,
- * at least asr_gemm_int8_workspace's bytes. */
+ * at least asr_gemm_int8_workspace's bytes (none, and NULL, up to 64 rows). */
 asr_status asr_gemm_int8_sr(const int8_t *a, uint64_t lda, const int8_t *b, uint64_t ldb,
                             const float *a_scale, const float *b_scale, void *c, uint64_t ldc, int32_t c_dtype,
                             uint64_t m, uint64_t n, uint64_t k, uint32_t rounding, uint32_t step, uint64_t seed,
                             void *workspace, uint64_t workspace_bytes, asr_stream_t stream);
 
 asr_status asr_gemm_int8_workspace(uint64_t m, uint64_t n, uint64_t k, uint64_t *bytes);
+
+/* A linear layer on these products.  Forward: y = x . W^T for tokens x (m x k)
+ * and a quantised weight (n x k, one scale a row): the rows of x are quantised
+ * to nearest inside the call, then as asr_gemm_int8_sr; bitwise what the two
+ * calls give. */
+asr_status asr_linear_int8(const void *x, int32_t x_dtype, uint64_t x_ld, const int8_t *weight, uint64_t ldw,
+                           const float *weight_scale, void *y, uint64_t ldy, int32_t y_dtype, uint64_t m,
+                           uint64_t n, uint64_t k, uint32_t rounding, uint32_t step, uint64_t seed,
+                           void *workspace, uint64_t workspace_bytes, asr_stream_t stream);
+
+asr_status asr_linear_int8_workspace(uint64_t m, uint64_t n, uint64_t k, uint64_t *bytes);
+
+/* Backward, from dy (tokens x n), x (tokens x k) and the weight (n x k), each
+ * f32 or bf16:
+ *   dx = dy . W     dy's rows rounded stochastically (base index 0), W's columns to nearest
+ *   dw = dy^T . x   dy's columns rounded stochastically, x's columns to nearest
+ * both bf16, to nearest; bitwise what the quantiser and the product give.
+ * dx or dw may be NULL where it is not needed (then w, or x, may be NULL).
+ * tokens, n and k between 1 and 131071. */
+asr_status asr_linear_int8_grads(const void *dy, int32_t dy_dtype, uint64_t dy_ld, const void *x, int32_t x_dtype,
+                                 uint64_t x_ld, const void *w, int32_t w_dtype, uint64_t w_ld, uint16_t *dx,
+                                 uint64_t dx_ld, uint16_t *dw, uint64_t dw_ld, uint64_t tokens, uint64_t n,
+                                 uint64_t k, uint32_t step, uint64_t seed, void *workspace,
+                                 uint64_t workspace_bytes, asr_stream_t stream);
+
+/* Workspace of that call for both gradients. */
+asr_status asr_linear_int8_grads_workspace(uint64_t tokens, uint64_t n, uint64_t k, uint64_t *bytes);
 
 /* Static description of a status code. */
 const char *asr_status_string(asr_status status);

@@ -11,7 +11,8 @@ from ._lib import (  # noqa: F401
     asr_stochastic_round_bf16, asr_take_device_error, asr_take_device_error_async, asr_selftest_wait_timeout,
     asr_kernel_launches, asr_adamw_sr_multi_tensor_host, lib, make_host_table, make_table,
     asr_gemm_int8_sr, asr_gemm_int8_workspace, asr_muon_sr_multi_tensor, asr_muon_workspace, asr_newton_schulz,
-    asr_newton_schulz_workspace, asr_quantize_int8, int8_empty,
+    asr_newton_schulz_workspace, asr_quantize_int8, int8_empty, asr_linear_int8, asr_linear_int8_workspace,
+    asr_linear_int8_grads, asr_linear_int8_grads_workspace,
 )
 from .int8 import Int8Linear, int8_linear, int8_linear_grads  # noqa: F401,E402
 from .optim import AdamWSR, DeviceError  # noqa: F401,E402

@@ -28,7 +28,8 @@ EXPORTS = ("asr_philox4x32", "asr_stochastic_round_bf16", "asr_adamw_prepare",
            "asr_adamw_sr_multi_tensor_static", "asr_gemm_bf16_sr", "asr_take_device_error_async",
            "asr_kernel_launches", "asr_adamw_sr_multi_tensor_host",
            "asr_newton_schulz", "asr_newton_schulz_workspace", "asr_muon_sr_multi_tensor", "asr_muon_workspace",
-           "asr_quantize_int8", "asr_gemm_int8_sr", "asr_gemm_int8_workspace")
+           "asr_quantize_int8", "asr_gemm_int8_sr", "asr_gemm_int8_workspace", "asr_linear_int8",
+           "asr_linear_int8_workspace", "asr_linear_int8_grads", "asr_linear_int8_grads_workspace")
 # asr_kernel_kind, in order
 KERNEL_KINDS = ("adamw_scalar", "adamw_vector", "adamw_pipelined", "adamw_pipelined_any_base", "adamw_static",
                 "round", "philox", "gemm", "matrix_prep", "product", "quantize", "int8_few_rows")
@@ -127,8 +128,16 @@ def lib() -> ctypes.CDLL:
         L.asr_gemm_int8_sr.argtypes = [vp, u64, vp, u64, vp, vp, vp, u64, i32, u64, u64, u64, u32, u32, u64, vp, u64,
                                        vp]
         L.asr_gemm_int8_workspace.argtypes = [u64, u64, u64, pu64]
+        L.asr_linear_int8.argtypes = [vp, i32, u64, vp, u64, vp, vp, u64, i32, u64, u64, u64, u32, u32, u64, vp, u64,
+                                      vp]
+        L.asr_linear_int8_workspace.argtypes = [u64, u64, u64, pu64]
+        L.asr_linear_int8_grads.argtypes = [vp, i32, u64, vp, i32, u64, vp, i32, u64, vp, u64, vp, u64, u64, u64, u64,
+                                            u32, u64, vp, u64, vp]
+        L.asr_linear_int8_grads_workspace.argtypes = [u64, u64, u64, pu64]
         for f in ("asr_newton_schulz", "asr_newton_schulz_workspace", "asr_muon_sr_multi_tensor",
-                  "asr_muon_workspace", "asr_quantize_int8", "asr_gemm_int8_sr", "asr_gemm_int8_workspace"):
+                  "asr_muon_workspace", "asr_quantize_int8", "asr_gemm_int8_sr", "asr_gemm_int8_workspace",
+                  "asr_linear_int8", "asr_linear_int8_workspace", "asr_linear_int8_grads",
+                  "asr_linear_int8_grads_workspace"):
             getattr(L, f).restype = ctypes.c_int
         for f in ("asr_philox4x32", "asr_stochastic_round_bf16", "asr_adamw_prepare",
                   "asr_adamw_sr_step", "asr_adamw_sr_multi_tensor",
@@ -780,3 +789,89 @@ def asr_gemm_int8_sr(a, b, a_scale, b_scale, c, *, rounding="sr", step: int = 0,
                                       int(step) & 0xFFFFFFFF, int(seed) & (2**64 - 1), pw, size,
                                       _stream_handle(a.device, stream)), "asr_gemm_int8_sr")
     return c
+
+
+def asr_linear_int8_workspace(m: int, n: int, k: int) -> int:
+    """Bytes of workspace that ``asr_linear_int8`` needs at these sizes."""
+    need = ctypes.c_uint64(0)
+    _check(lib().asr_linear_int8_workspace(int(m), int(n), int(k), ctypes.byref(need)), "asr_linear_int8_workspace")
+    return int(need.value)
+
+
+def asr_linear_int8(x, weight, weight_scale, y, *, rounding="rne", step: int = 0, seed: int = 0, workspace=None,
+                    stream=None):
+    """y = x . W^T: ``x`` (tokens, k) float32 or bfloat16, its rows quantised
+    inside the call; ``weight`` (n, k) int8 with ``weight_scale`` (n) float32;
+    ``y`` (tokens, n) bfloat16 or float32."""
+    torch = _torch()
+    px, m, k, x_ld = _matrix_ptr(x, "x", (torch.bfloat16, torch.float32))
+    d = x.get_device()
+    pw, n, kw, ldw = _matrix_ptr(weight, "weight", (torch.int8,), d)
+    py, my, ny, ldy = _matrix_ptr(y, "y", (torch.bfloat16, torch.float32), d)
+    if kw != k or my != m or ny != n:
+        raise ValueError(f"shapes do not chain: x {tuple(x.shape)}, weight {tuple(weight.shape)}, y {tuple(y.shape)}")
+    ps = _dev_ptr(weight_scale, "weight_scale", (torch.float32,), n, d)
+    r = _ROUNDING.get(rounding)
+    if r is None:
+        raise ValueError(f"rounding must be 'sr' or 'rne', not {rounding!r}")
+    need = asr_linear_int8_workspace(m, n, k)
+    device = x.device
+    with _on_device(device):
+        buf, pws, size = _workspace(workspace, need, device, stream)
+        _check(lib().asr_linear_int8(px, _dt(x), x_ld, pw, ldw, ps, py, ldy, _dt(y), m, n, k, r,
+                                     int(step) & 0xFFFFFFFF, int(seed) & (2**64 - 1), pws, size,
+                                     _stream_handle(device, stream)), "asr_linear_int8")
+    return y
+
+
+def asr_linear_int8_grads_workspace(tokens: int, n: int, k: int) -> int:
+    """Bytes of workspace that ``asr_linear_int8_grads`` needs at these sizes."""
+    need = ctypes.c_uint64(0)
+    _check(lib().asr_linear_int8_grads_workspace(int(tokens), int(n), int(k), ctypes.byref(need)),
+           "asr_linear_int8_grads_workspace")
+    return int(need.value)
+
+
+def asr_linear_int8_grads(dy, x, w, dx, dw, *, step: int = 0, seed: int = 0, workspace=None, stream=None):
+    """Gradients of ``y = x w^T`` in 8-bit products: ``dy`` (tokens, n), ``x``
+    (tokens, k), ``w`` (n, k), each float32 or bfloat16; ``dx`` and ``dw``
+    bfloat16, either None where it is not needed (then w, or x, may be None)."""
+    torch = _torch()
+    types = (torch.bfloat16, torch.float32)
+    pg, t, n, g_ld = _matrix_ptr(dy, "dy", types)
+    d = dy.get_device()
+    given = [v for v in (x, w) if v is not None]
+    if (dw is not None and x is None) or (dx is not None and w is None):
+        raise ValueError("dw needs x and dx needs w")
+    k = given[0].shape[-1] if given else 0
+    args = []
+    for v, name, rows in ((x, "x", t), (w, "w", n)):
+        if v is None:
+            args += [None, ASR_BF16, k]
+            continue
+        p, r, c, ld = _matrix_ptr(v, name, types, d)
+        if r != rows or c != k:
+            raise ValueError(f"{name} has shape {(r, c)}; expected {(rows, k)}")
+        args += [p, _dt(v), ld]
+    for v, name, rows in ((dx, "dx", t), (dw, "dw", n)):
+        if v is None:
+            args += [None, k]
+            continue
+        p, r, c, ld = _matrix_ptr(v, name, (torch.bfloat16,), d)
+        if r != rows or c != k:
+            raise ValueError(f"{name} has shape {(r, c)}; expected {(rows, k)}")
+        args += [p, ld]
+    if dx is None and dw is None:
+        return
+    if t == 0 or n == 0 or k == 0:                  # sums over nothing
+        for v in (dx, dw):
+            if v is not None:
+                v.zero_()
+        return
+    need = asr_linear_int8_grads_workspace(t, n, k)
+    device = dy.device
+    with _on_device(device):
+        buf, pws, size = _workspace(workspace, need, device, stream)
+        _check(lib().asr_linear_int8_grads(pg, _dt(dy), g_ld, *args, t, n, k, int(step) & 0xFFFFFFFF,
+                                           int(seed) & (2**64 - 1), pws, size, _stream_handle(device, stream)),
+               "asr_linear_int8_grads")

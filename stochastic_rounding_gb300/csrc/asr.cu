@@ -582,6 +582,7 @@ std::atomic<uint64_t> g_philox_ready{0}, g_round_ready{0};
 #include "gemm_sr.cuh"
 #include "product.cuh"
 #include "muon.cuh"
+#include "int8_few.cuh"
 #include "int8.cuh"
 
 // The entry points that hold host tables in containers: out of host memory is
@@ -829,14 +830,49 @@ asr_status asr_gemm_int8_sr(const int8_t *a, uint64_t lda, const int8_t *b, uint
                             uint64_t k, uint32_t rounding, uint32_t step, uint64_t seed, void *workspace,
                             uint64_t workspace_bytes, asr_stream_t stream)
 {
-    return int8::gemm(a, lda, b, ldb, a_scale, b_scale, c, ldc, c_dtype, m, n, k, rounding, step, seed, workspace,
-                      workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+    const int8::Output o{c, ldc, c_dtype, rounding, step, seed};
+    return int8::gemm(a, lda, b, ldb, a_scale, b_scale, o, m, n, k, workspace, workspace_bytes,
+                      reinterpret_cast<cudaStream_t>(stream));
 }
 
 asr_status asr_gemm_int8_workspace(uint64_t m, uint64_t n, uint64_t k, uint64_t *bytes)
 {
     if (!bytes || !int8::sizes_ok(m, n, k)) return ASR_ERR_INVALID_VALUE;
     *bytes = m && n && k ? int8::layout(m, n, k).bytes : 0;
+    return ASR_OK;
+}
+
+asr_status asr_linear_int8(const void *x, int32_t x_dtype, uint64_t x_ld, const int8_t *weight, uint64_t ldw,
+                           const float *weight_scale, void *y, uint64_t ldy, int32_t y_dtype, uint64_t m, uint64_t n,
+                           uint64_t k, uint32_t rounding, uint32_t step, uint64_t seed, void *workspace,
+                           uint64_t workspace_bytes, asr_stream_t stream)
+{
+    const int8::Output o{y, ldy, y_dtype, rounding, step, seed};
+    return int8::linear(x, x_dtype, x_ld, weight, ldw, weight_scale, o, m, n, k, workspace, workspace_bytes,
+                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+asr_status asr_linear_int8_workspace(uint64_t m, uint64_t n, uint64_t k, uint64_t *bytes)
+{
+    if (!bytes || !int8::sizes_ok(m, n, k)) return ASR_ERR_INVALID_VALUE;
+    *bytes = m && n && k ? int8::linear_layout(m, n, k).bytes : 0;
+    return ASR_OK;
+}
+
+asr_status asr_linear_int8_grads(const void *dy, int32_t dy_dtype, uint64_t dy_ld, const void *x, int32_t x_dtype,
+                                 uint64_t x_ld, const void *w, int32_t w_dtype, uint64_t w_ld, uint16_t *dx,
+                                 uint64_t dx_ld, uint16_t *dw, uint64_t dw_ld, uint64_t tokens, uint64_t n, uint64_t k,
+                                 uint32_t step, uint64_t seed, void *workspace, uint64_t workspace_bytes,
+                                 asr_stream_t stream)
+{
+    return int8::grads({dy, dy_ld, dy_dtype}, {x, x_ld, x_dtype}, {w, w_ld, w_dtype}, dx, dx_ld, dw, dw_ld, tokens, n,
+                       k, step, seed, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+asr_status asr_linear_int8_grads_workspace(uint64_t tokens, uint64_t n, uint64_t k, uint64_t *bytes)
+{
+    if (!bytes || !int8::grad_sizes_ok(tokens, n, k)) return ASR_ERR_INVALID_VALUE;
+    *bytes = int8::grad_layout(tokens, n, k, true, true).bytes;
     return ASR_OK;
 }
 

@@ -21,16 +21,67 @@ constexpr int kThreads = 256;
 constexpr uint64_t kMaxK = 131071;              // 128^2 K < 2^31
 constexpr uint32_t kChunk = 1024 / prod::kBK;
 
-struct QuantParams {
-    const void *x;
-    int8_t *q;
-    float *scale;
-    uint64_t rows, cols, x_ld, q_ld;
-    uint64_t base;
-    uint32_t dtype, rounding, step;
-    uint32_t vec;                               // 8-element units of x are 16-byte aligned
-    RoundKeys keys;
+struct WidenParams {
+    const int8_t *src[2];
+    __half *dst[2];
+    uint64_t rows[2], src_ld[2];
+    uint64_t cols, dst_ld;                      // dst_ld: cols up to a multiple of 16
+    uint32_t vec[2];
 };
+
+// 8-bit integers to f16, block `block` of `blocks`: a warp a span of 512
+// columns, 16 a lane.
+__device__ __forceinline__ void widen_block(const WidenParams &P, uint32_t block, uint32_t blocks)
+{
+    const uint32_t lane = threadIdx.x & 31;
+    muon::Walk k(P.rows[0] + P.rows[1], (P.cols + 1) / 2, block * 8ull + (threadIdx.x >> 5), blocks * 8ull);
+    for (; k.more(); k.next()) {
+        const int which = k.row >= P.rows[0];
+        const uint64_t row = which ? k.row - P.rows[0] : k.row, col = k.span * 512ull + lane * 16;
+        if (col >= P.cols) continue;
+        const int8_t *src = P.src[which] + row * P.src_ld[which] + col;
+        uint32_t a[4] = {0, 0, 0, 0};
+        if (P.vec[which] && P.cols - col >= 16) {
+            const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(src));
+            a[0] = w.x, a[1] = w.y, a[2] = w.z, a[3] = w.w;
+        } else {
+            const int live = P.cols - col < 16 ? static_cast<int>(P.cols - col) : 16;
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                if (q < live) a[q >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(src[q])) << (8 * (q & 3));
+        }
+        uint32_t h[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) int8few::widen4(a[q], h[2 * q], h[2 * q + 1]);
+        gemm::st_global_v8(P.dst[which] + row * P.dst_ld + col, h);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__ WidenParams P)
+{
+    widen_block(P, blockIdx.x, gridDim.x);
+}
+
+__device__ __forceinline__ uint4 pack8(const float x[8])
+{
+    return make_uint4(prod::pack_f16(x[0], x[1]), prod::pack_f16(x[2], x[3]), prod::pack_f16(x[4], x[5]),
+                      prod::pack_f16(x[6], x[7]));
+}
+
+__device__ __forceinline__ void store_int8(int8_t *dst, const float x[8], int live)
+{
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        w[q >> 2] |= static_cast<uint32_t>(__float2int_rn(x[q]) & 0xFF) << (8 * (q & 3));
+    if (live == 8 && (reinterpret_cast<uintptr_t>(dst) & 7u) == 0) {
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (q < live) dst[q] = static_cast<int8_t>(w[q >> 2] >> (8 * (q & 3)));
+    }
+}
 
 // How a row's values become integers: y = (x * pre) * inv.  A row whose largest
 // value is so small that 127 / max would overflow is raised by 2^64 first (exact);
@@ -48,17 +99,20 @@ __device__ __forceinline__ Levels levels_of(float top)
     return L;
 }
 
+// The integer of x, as a float.
 template <bool SR>
-__device__ __forceinline__ int quantise(float x, const Levels &L, uint32_t r)
+__device__ __forceinline__ float quantise(float x, const Levels &L, uint32_t r)
 {
     const float y = __fmul_rn(__fmul_rn(x, L.pre), L.inv);
+    float q;
     if (!SR) {
-        const int q = __float2int_rn(y);
-        return L.inv == 0.0f ? 0 : q;           // |y| <= 127 (1 + 2^-23): rounds to at most 127
+        q = rintf(y);                           // |y| <= 127 (1 + 2^-23): rounds to at most 127
+    } else {
+        const float low = floorf(y);
+        q = low + (__fmul_rn(__fsub_rn(y, low), 65536.0f) > static_cast<float>(r & 0xFFFFu) ? 1.0f : 0.0f);
+        q = fmaxf(-127.0f, fminf(127.0f, q));
     }
-    const float low = floorf(y);
-    const int q = static_cast<int>(low) + (__fmul_rn(__fsub_rn(y, low), 65536.0f) > static_cast<float>(r & 0xFFFFu));
-    return L.inv == 0.0f ? 0 : max(-127, min(127, q));
+    return L.inv == 0.0f ? 0.0f : q;
 }
 
 __device__ __forceinline__ uint32_t absbits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
@@ -73,12 +127,36 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *part)
     return v;
 }
 
-// One block a row.
-template <bool SR>
-__global__ void __launch_bounds__(kThreads) quantise_rows_kernel(const __grid_constant__ QuantParams P)
+__device__ __forceinline__ void words8(uint64_t base, uint64_t e, uint32_t step, const RoundKeys &K, uint32_t r[8])
 {
+    if (((base + e) & 3u) == 0) unit_words<true>(base, e, step, K, r);
+    else unit_words<false>(base, e, step, K, r);
+}
+
+struct RowParams {
+    const void *x;
+    void *q;                                    // int8, or f16 rows a multiple of 16 apart (WIDE)
+    float *scale;
+    uint64_t rows, cols, x_ld, q_ld;
+    uint64_t base;
+    uint32_t dtype, step;
+    uint32_t vec;                               // 8-element units of x are 16-byte aligned
+    RoundKeys keys;
+    WidenParams w;                              // WIDE: the other operand, widened by the blocks past `rows`
+};
+
+// Rows: one block each, the second pass over the row out of the cache.
+template <bool SR, bool WIDE>
+__global__ void __launch_bounds__(kThreads) quantise_rows_kernel(const __grid_constant__ RowParams P, uint32_t row_blocks)
+{
+    // the product that follows may start on what does not depend on this
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (WIDE && blockIdx.x >= row_blocks) {
+        widen_block(P.w, blockIdx.x - row_blocks, gridDim.x - row_blocks);
+        return;
+    }
     __shared__ uint32_t part[kThreads / 32];
-    for (uint64_t row = blockIdx.x; row < P.rows; row += gridDim.x) {
+    for (uint64_t row = blockIdx.x; row < P.rows; row += row_blocks) {
         uint32_t top = 0;                       // the order of non-negative floats is that of their bits; a NaN is above all
         for (uint64_t col = threadIdx.x * 8ull; col < P.cols; col += kThreads * 8ull) {
             const int live = P.cols - col < 8 ? static_cast<int>(P.cols - col) : 8;
@@ -95,115 +173,217 @@ __global__ void __launch_bounds__(kThreads) quantise_rows_kernel(const __grid_co
             float x[8];
             muon::load8(P.x, P.dtype, row * P.x_ld + col, live, P.vec, x);
             uint32_t r[8];
-            if (SR) unit_words<false>(P.base + row * P.cols, col, P.step, P.keys, r);
-            uint32_t w[2] = {0, 0};
+            if (SR) words8(P.base, row * P.cols + col, P.step, P.keys, r);
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                w[q >> 2] |= static_cast<uint32_t>(quantise<SR>(x[q], L, SR ? r[q] : 0u) & 0xFF) << (8 * (q & 3));
-            int8_t *dst = P.q + row * P.q_ld + col;
-            if (live == 8 && (reinterpret_cast<uintptr_t>(dst) & 7u) == 0) {
-                *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+            for (int q = 0; q < 8; ++q) x[q] = quantise<SR>(x[q], L, SR ? r[q] : 0u);
+            if (WIDE) {
+                *reinterpret_cast<uint4 *>(static_cast<__half *>(P.q) + row * P.q_ld + col) = pack8(x);
             } else {
-                for (int q = 0; q < live; ++q) dst[q] = static_cast<int8_t>(w[q >> 2] >> (8 * (q & 3)));
+                store_int8(static_cast<int8_t *>(P.q) + row * P.q_ld + col, x, live);
             }
         }
         __syncthreads();
     }
 }
 
-// Columns: the largest value of each (bits, in `scale`, zeroed before) ...
-__global__ void __launch_bounds__(kThreads) column_max_kernel(const __grid_constant__ QuantParams P)
+// Maxima along columns, or along both, of up to three matrices in one launch:
+// blocks of kTileRows x 256, a warp every eighth row, eight columns a lane.
+// `row_max` and `col_max` hold bits of non-negative floats, zero at the start;
+// integer maxima are the same whatever their order.
+constexpr int kTileRows = 64;
+
+struct Side {
+    const void *x;
+    uint64_t rows, cols, x_ld;
+    uint32_t *row_max, *col_max;                // row_max may be null
+    uint32_t vec, dtype;
+    uint32_t tiles_x, first;                    // first block of this matrix
+    // what becomes of it in `wide_kernel`: f16 integers in place, scaled by columns and (with row_max) by rows
+    __half *by_row, *by_col;
+    float *row_scale, *col_scale;
+    uint64_t q_ld;
+};
+
+struct SideParams {
+    Side s[3];
+    uint32_t count, blocks;
+    uint32_t step;
+    RoundKeys keys;
+};
+
+__device__ __forceinline__ const Side &side_of(const SideParams &P, uint32_t block)
 {
-    const uint64_t col = (blockIdx.x * 32ull + (threadIdx.x & 31)) * 8;
-    if (col >= P.cols) return;
-    const int live = P.cols - col < 8 ? static_cast<int>(P.cols - col) : 8;
-    uint32_t top[8] = {};
-    for (uint64_t row = blockIdx.y * 8ull + (threadIdx.x >> 5); row < P.rows; row += gridDim.y * 8ull) {
-        float x[8];
-        muon::load8(P.x, P.dtype, row * P.x_ld + col, live, P.vec, x);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) top[q] = max(top[q], absbits(x[q]));
-    }
-    // integer maxima: the same whatever their order
-    for (int q = 0; q < live; ++q) atomicMax(reinterpret_cast<uint32_t *>(P.scale) + col + q, top[q]);
+    return P.s[P.count > 2 && block >= P.s[2].first ? 2 : P.count > 1 && block >= P.s[1].first ? 1 : 0];
 }
 
-// ... the integers, 64 x 64 tiles turned in shared memory ...
+__global__ void __launch_bounds__(kThreads) max_kernel(const __grid_constant__ SideParams P)
+{
+    __shared__ uint32_t part[8][256];
+    const Side &S = side_of(P, blockIdx.x);
+    const uint32_t tile = blockIdx.x - S.first, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t r0 = static_cast<uint64_t>(tile / S.tiles_x) * kTileRows;
+    const uint64_t c0 = static_cast<uint64_t>(tile % S.tiles_x) * 256, col = c0 + lane * 8;
+    const int live = col >= S.cols ? 0 : S.cols - col < 8 ? static_cast<int>(S.cols - col) : 8;
+    uint32_t top[8] = {};
+#pragma unroll 4
+    for (int i = 0; i < kTileRows / 8; ++i) {
+        const uint64_t row = r0 + i * 8 + warp;
+        if (row >= S.rows) break;
+        uint32_t most = 0;
+        if (live) {
+            float x[8];
+            muon::load8(S.x, S.dtype, row * S.x_ld + col, live, S.vec, x);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const uint32_t b = absbits(x[q]);
+                top[q] = max(top[q], b);
+                most = max(most, b);
+            }
+        }
+        if (S.row_max) {
+            most = __reduce_max_sync(0xFFFFFFFFu, most);
+            if (lane == 0) atomicMax(S.row_max + row, most);
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) part[warp][q * 32 + lane] = top[q];     // column lane * 8 + q
+    __syncthreads();
+    uint32_t v = part[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) v = max(v, part[w][threadIdx.x]);
+    const uint64_t c = c0 + (threadIdx.x & 31) * 8 + (threadIdx.x >> 5);
+    if (c < S.cols) atomicMax(S.col_max + c, v);
+}
+
+// The integers of every matrix of the call, as f16, where they lie (the
+// products read them across): side 0 (dy) stochastically, by its rows' and by
+// its columns' maxima with the same random bits; the others to nearest, by
+// columns.  The first tiles write the scales.
+__global__ void __launch_bounds__(kThreads) wide_kernel(const __grid_constant__ SideParams P)
+{
+    const Side &S = side_of(P, blockIdx.x);
+    const uint32_t tile = blockIdx.x - S.first, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t r0 = static_cast<uint64_t>(tile / S.tiles_x) * kTileRows;
+    const uint64_t c0 = static_cast<uint64_t>(tile % S.tiles_x) * 256, col = c0 + lane * 8;
+    const int live = col >= S.cols ? 0 : S.cols - col < 8 ? static_cast<int>(S.cols - col) : 8;
+    if (r0 == 0 && c0 + threadIdx.x < S.cols)
+        S.col_scale[c0 + threadIdx.x] = __fdiv_rn(__uint_as_float(S.col_max[c0 + threadIdx.x]), 127.0f);
+    if (S.row_max && c0 == 0 && threadIdx.x < kTileRows && r0 + threadIdx.x < S.rows)
+        S.row_scale[r0 + threadIdx.x] = __fdiv_rn(__uint_as_float(S.row_max[r0 + threadIdx.x]), 127.0f);
+    if (!live) return;
+    Levels L[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) L[q] = levels_of(q < live ? __uint_as_float(S.col_max[col + q]) : 0.0f);
+    for (int i = 0; i < kTileRows / 8; ++i) {
+        const uint64_t row = r0 + i * 8 + warp;
+        if (row >= S.rows) break;
+        float x[8], y[8];
+        muon::load8(S.x, S.dtype, row * S.x_ld + col, live, S.vec, x);
+        if (S.row_max) {
+            uint32_t r[8];
+            words8(0, row * S.cols + col, P.step, P.keys, r);
+            const Levels R = levels_of(__uint_as_float(S.row_max[row]));
+            if (S.by_row) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) y[q] = quantise<true>(x[q], R, r[q]);
+                *reinterpret_cast<uint4 *>(S.by_row + row * S.q_ld + col) = pack8(y);
+            }
+            if (S.by_col) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) y[q] = quantise<true>(x[q], L[q], r[q]);
+                *reinterpret_cast<uint4 *>(S.by_col + row * S.q_ld + col) = pack8(y);
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) y[q] = quantise<false>(x[q], L[q], 0u);
+            *reinterpret_cast<uint4 *>(S.by_col + row * S.q_ld + col) = pack8(y);
+        }
+    }
+}
+
+struct ColumnParams {
+    const void *x;
+    int8_t *q;
+    const uint32_t *col_max;                    // in `scale`, until the scales are written
+    uint64_t rows, cols, x_ld, q_ld;
+    uint64_t base;
+    uint32_t dtype, step, vec;
+    RoundKeys keys;
+};
+
+// Columns, stored transposed: 64 x 64 tiles turned in shared memory.
 template <bool SR>
-__global__ void __launch_bounds__(kThreads) quantise_columns_kernel(const __grid_constant__ QuantParams P)
+__global__ void __launch_bounds__(kThreads) quantise_columns_kernel(const __grid_constant__ ColumnParams P)
 {
     __shared__ int8_t tile[64][68];
     const uint64_t r0 = blockIdx.y * 64ull, c0 = blockIdx.x * 64ull;
-    for (int i = threadIdx.x; i < 64 * 8; i += kThreads) {
-        const uint64_t row = r0 + (i >> 3), col = c0 + (i & 7) * 8;
-        if (row >= P.rows || col >= P.cols) continue;
-        const int live = P.cols - col < 8 ? static_cast<int>(P.cols - col) : 8;
+    const uint64_t col = c0 + (threadIdx.x & 7) * 8;
+    const int live = col >= P.cols ? 0 : P.cols - col < 8 ? static_cast<int>(P.cols - col) : 8;
+    Levels L[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) L[q] = levels_of(q < live ? __uint_as_float(P.col_max[col + q]) : 0.0f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int tr = (threadIdx.x >> 3) + i * 32;
+        const uint64_t row = r0 + tr;
+        if (row >= P.rows || !live) continue;
         float x[8];
         muon::load8(P.x, P.dtype, row * P.x_ld + col, live, P.vec, x);
         uint32_t r[8];
-        if (SR) unit_words<false>(P.base + row * P.cols, col, P.step, P.keys, r);
+        if (SR) words8(P.base, row * P.cols + col, P.step, P.keys, r);
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-            if (q < live)
-                tile[(i & 7) * 8 + q][i >> 3] =
-                    static_cast<int8_t>(quantise<SR>(x[q], levels_of(P.scale[col + q]), SR ? r[q] : 0u));
+            tile[(threadIdx.x & 7) * 8 + q][tr] = static_cast<int8_t>(__float2int_rn(quantise<SR>(x[q], L[q], SR ? r[q] : 0u)));
     }
     __syncthreads();
     for (int i = threadIdx.x; i < 64 * 64; i += kThreads) {
-        const uint64_t col = c0 + (i >> 6), row = r0 + (i & 63);
-        if (row < P.rows && col < P.cols) P.q[col * P.q_ld + row] = tile[i >> 6][i & 63];
+        const uint64_t c = c0 + (i >> 6), row = r0 + (i & 63);
+        if (row < P.rows && c < P.cols) P.q[c * P.q_ld + row] = tile[i >> 6][i & 63];
     }
 }
 
-// ... and the scales.
 __global__ void __launch_bounds__(kThreads) column_scale_kernel(float *scale, uint64_t n)
 {
     const uint64_t i = blockIdx.x * static_cast<uint64_t>(kThreads) + threadIdx.x;
     if (i < n) scale[i] = __fdiv_rn(scale[i], 127.0f);
 }
 
-struct WidenParams {
-    const int8_t *src[2];
-    __half *dst[2];
-    uint64_t rows[2], src_ld[2];
-    uint64_t cols, dst_ld;                      // dst_ld: cols up to a multiple of 16
-    uint32_t vec[2];
-};
-
-__device__ __forceinline__ uint32_t widen2(int lo, int hi)
-{
-    const __half2 h = __halves2half2(__int2half_rn(lo), __int2half_rn(hi));
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// 8-bit integers to f16: 16 a thread.
-__global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__ WidenParams P)
-{
-    const uint64_t per_row = P.dst_ld / 16, first = P.rows[0] * per_row, units = first + P.rows[1] * per_row;
-    for (uint64_t u = blockIdx.x * static_cast<uint64_t>(kThreads) + threadIdx.x; u < units;
-         u += static_cast<uint64_t>(gridDim.x) * kThreads) {
-        const int which = u >= first;
-        const uint64_t v = which ? u - first : u;
-        const uint64_t row = v / per_row, col = (v - row * per_row) * 16;
-        const int live = P.cols - col < 16 ? static_cast<int>(P.cols - col) : 16;
-        const int8_t *src = P.src[which] + row * P.src_ld[which] + col;
-        int x[16];
-        if (P.vec[which] && live == 16) {
-            const int4 w = *reinterpret_cast<const int4 *>(src);
-            const int a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int q = 0; q < 16; ++q) x[q] = static_cast<int8_t>(a[q >> 2] >> (8 * (q & 3)));
-        } else {
-#pragma unroll
-            for (int q = 0; q < 16; ++q) x[q] = q < live ? src[q] : 0;
-        }
-        uint4 *dst = reinterpret_cast<uint4 *>(P.dst[which] + row * P.dst_ld + col);
-        dst[0] = make_uint4(widen2(x[0], x[1]), widen2(x[2], x[3]), widen2(x[4], x[5]), widen2(x[6], x[7]));
-        dst[1] = make_uint4(widen2(x[8], x[9]), widen2(x[10], x[11]), widen2(x[12], x[13]), widen2(x[14], x[15]));
-    }
-}
-
 // ------------------------------------------------------------------ host
+
+unsigned blocks_for(uint64_t units, uint64_t per_block, uint64_t most)
+{
+    const uint64_t b = (units + per_block - 1) / per_block;
+    return static_cast<unsigned>(b < 1 ? 1 : b < most ? b : most);
+}
+
+bool pitch_ok(uint64_t ld, uint64_t least) { return ld >= least && ld <= (1ull << 32); }
+
+// A row and column range of the tiles that the column kernels walk must be countable in a launch.
+bool quantisable(uint64_t rows, uint64_t cols)
+{
+    return rows <= (1u << 30) && cols <= (1u << 30) &&
+           ((rows + kTileRows - 1) / kTileRows) * ((cols + 255) / 256) < (1ull << 28);
+}
+
+Side side(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t first)
+{
+    Side S;
+    std::memset(&S, 0, sizeof(S));
+    S.x = x;
+    S.rows = rows;
+    S.cols = cols;
+    S.x_ld = ld;
+    S.vec = muon::units_aligned(x, ld, 0);
+    S.dtype = static_cast<uint32_t>(dtype);
+    S.tiles_x = static_cast<uint32_t>((cols + 255) / 256);
+    S.first = first;
+    return S;
+}
+
+uint32_t side_blocks(const Side &S)
+{
+    return static_cast<uint32_t>((S.rows + kTileRows - 1) / kTileRows) * S.tiles_x;
+}
 
 asr_status quantize(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, uint64_t x_ld, int32_t axis, int8_t *q,
                     uint64_t q_ld, float *scale, uint32_t rounding, uint64_t base, uint32_t step, uint64_t seed,
@@ -215,37 +395,54 @@ asr_status quantize(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, 
     if (rows == 0 || cols == 0) return ASR_OK;
     if (!x || !q || !scale || !muon::element_aligned(x, dtype) || !muon::element_aligned(scale, ASR_F32))
         return ASR_ERR_INVALID_VALUE;
-    if (rows > (1u << 30) || cols > (1u << 30) || x_ld < cols || x_ld > (1ull << 32) || q_ld > (1ull << 32) ||
-        q_ld < (axis == ASR_ROWS ? cols : rows) || base > UINT64_MAX - rows * cols)
+    if (!quantisable(rows, cols) || !pitch_ok(x_ld, cols) || !pitch_ok(q_ld, axis == ASR_ROWS ? cols : rows) ||
+        base > UINT64_MAX - rows * cols)
         return ASR_ERR_INVALID_VALUE;
-    QuantParams P;
+    const bool sr = rounding == ASR_ROUND_SR;
+    if (axis == ASR_ROWS) {
+        RowParams P;
+        std::memset(&P, 0, sizeof(P));
+        P.x = x;
+        P.q = q;
+        P.scale = scale;
+        P.rows = rows;
+        P.cols = cols;
+        P.x_ld = x_ld;
+        P.q_ld = q_ld;
+        P.base = base;
+        P.dtype = static_cast<uint32_t>(dtype);
+        P.step = step;
+        P.vec = muon::units_aligned(x, x_ld, 0);
+        P.keys = make_keys(seed);
+        const unsigned grid = blocks_for(rows, 1, 65536);
+        if (sr) quantise_rows_kernel<true, false><<<grid, kThreads, 0, stream>>>(P, grid);
+        else quantise_rows_kernel<false, false><<<grid, kThreads, 0, stream>>>(P, grid);
+        return launched(ASR_KERNEL_QUANTIZE);
+    }
+    if ((rows + 63) / 64 > 65535) return ASR_ERR_INVALID_VALUE;
+    const cudaError_t e = cudaMemsetAsync(scale, 0, cols * sizeof(float), stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+    SideParams M;
+    std::memset(&M, 0, sizeof(M));
+    M.s[0] = side(x, dtype, rows, cols, x_ld, 0);
+    M.s[0].col_max = reinterpret_cast<uint32_t *>(scale);
+    M.count = 1;
+    max_kernel<<<side_blocks(M.s[0]), kThreads, 0, stream>>>(M);
+    asr_status st = launched(ASR_KERNEL_QUANTIZE);
+    if (st != ASR_OK) return st;
+    ColumnParams P;
     P.x = x;
     P.q = q;
-    P.scale = scale;
+    P.col_max = reinterpret_cast<const uint32_t *>(scale);
     P.rows = rows;
     P.cols = cols;
     P.x_ld = x_ld;
     P.q_ld = q_ld;
     P.base = base;
     P.dtype = static_cast<uint32_t>(dtype);
-    P.rounding = rounding;
     P.step = step;
     P.vec = muon::units_aligned(x, x_ld, 0);
     P.keys = make_keys(seed);
-    const bool sr = rounding == ASR_ROUND_SR;
-    if (axis == ASR_ROWS) {
-        const unsigned grid = static_cast<unsigned>(rows < 65536 ? rows : 65536);
-        if (sr) quantise_rows_kernel<true><<<grid, kThreads, 0, stream>>>(P);
-        else quantise_rows_kernel<false><<<grid, kThreads, 0, stream>>>(P);
-        return launched(ASR_KERNEL_QUANTIZE);
-    }
-    if ((rows + 63) / 64 > 65535) return ASR_ERR_INVALID_VALUE;
-    cudaError_t e = cudaMemsetAsync(scale, 0, cols * sizeof(float), stream);
-    if (e != cudaSuccess) return cuda_fail(e);
-    const uint64_t strips = (cols + 255) / 256, chunks = (rows + 63) / 64;
-    column_max_kernel<<<dim3(static_cast<unsigned>(strips), static_cast<unsigned>(chunks)), kThreads, 0, stream>>>(P);
-    asr_status st = launched(ASR_KERNEL_QUANTIZE);
-    if (st != ASR_OK) return st;
     const dim3 grid(static_cast<unsigned>((cols + 63) / 64), static_cast<unsigned>((rows + 63) / 64));
     if (sr) quantise_columns_kernel<true><<<grid, kThreads, 0, stream>>>(P);
     else quantise_columns_kernel<false><<<grid, kThreads, 0, stream>>>(P);
@@ -255,46 +452,118 @@ asr_status quantize(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, 
     return launched(ASR_KERNEL_QUANTIZE);
 }
 
+bool sizes_ok(uint64_t m, uint64_t n, uint64_t k)
+{
+    return m <= (1u << 24) && n <= (1u << 24) && k <= kMaxK;
+}
+
+bool few(uint64_t m) { return m <= static_cast<uint64_t>(int8few::kMaxTokens); }
+
+// Workspace of the product: the widened operands, or nothing where A has few rows.
 struct Layout {
     uint64_t a, b, bytes, ld;
 };
 
 Layout layout(uint64_t m, uint64_t n, uint64_t k)
 {
-    Layout L;
-    L.ld = muon::up(k, 16);
-    L.a = 0;
+    Layout L{0, 0, 0, muon::up(k, 16)};
+    if (few(m)) return L;
     L.b = muon::up(m * L.ld * 2, 256);
     L.bytes = L.b + muon::up(n * L.ld * 2, 256);
     return L;
 }
 
-bool sizes_ok(uint64_t m, uint64_t n, uint64_t k)
+struct Output {
+    void *c;
+    uint64_t ld;
+    int32_t dtype;
+    uint32_t rounding, step;
+    uint64_t seed;
+};
+
+bool output_ok(const Output &o, uint64_t n)
 {
-    return m <= (1u << 24) && n <= (1u << 24) && k <= kMaxK;
+    return o.c && pitch_ok(o.ld, n) && muon::element_aligned(o.c, o.dtype);
 }
 
-asr_status gemm(const int8_t *a, uint64_t lda, const int8_t *b, uint64_t ldb, const float *sa, const float *sb, void *c,
-                uint64_t ldc, int32_t c_dtype, uint64_t m, uint64_t n, uint64_t k, uint32_t rounding, uint32_t step,
-                uint64_t seed, void *ws, uint64_t ws_bytes, cudaStream_t stream)
+asr_status output_kind(const Output &o)
 {
-    if (c_dtype != ASR_F32 && c_dtype != ASR_BF16) return ASR_ERR_UNSUPPORTED_DTYPE;
-    if (rounding != ASR_ROUND_SR && rounding != ASR_ROUND_RNE) return ASR_ERR_UNSUPPORTED_DTYPE;
+    if (o.dtype != ASR_F32 && o.dtype != ASR_BF16) return ASR_ERR_UNSUPPORTED_DTYPE;
+    if (o.rounding != ASR_ROUND_SR && o.rounding != ASR_ROUND_RNE) return ASR_ERR_UNSUPPORTED_DTYPE;
+    return ASR_OK;
+}
+
+// The product of widened operands.
+template <bool A_MN, bool B_MN>
+asr_status product(const prod::Stored &a, const prod::Stored &b, const float *sa, const float *sb, const Output &o,
+                   cudaStream_t stream)
+{
+    prod::Params P;
+    std::memset(&P, 0, sizeof(P));
+    P.batch = 1;
+    P.chunk = kChunk;
+    P.out_ld = o.ld;
+    P.out_dtype = static_cast<uint32_t>(o.dtype);
+    P.rounding = o.rounding;
+    P.vec = muon::aligned32(o.c) && o.ld % 16 == 0;
+    P.step = o.step;
+    P.row_scale = sa;
+    P.col_scale = sb;
+    P.keys = make_keys(o.seed);
+    P.slot[0].ptr = o.c;
+    return prod::launch<A_MN, B_MN, prod::kInt8>(a, b, P, ASR_KERNEL_PRODUCT, stream);
+}
+
+prod::Stored stored(__half *p, uint64_t rows, uint64_t cols, uint64_t ld)
+{
+    return prod::Stored{p, rows, cols, ld, muon::up(rows * ld * 2, 256) / 2};
+}
+
+asr_status few_rows(const int8_t *a, uint64_t lda, const int8_t *b, uint64_t ldb, const float *sa, const float *sb,
+                    const Output &o, uint64_t m, uint64_t n, uint64_t k, bool early, cudaStream_t stream)
+{
+    int8few::Params P;
+    std::memset(&P, 0, sizeof(P));
+    P.a = a;
+    P.b = b;
+    P.row_scale = sa;
+    P.col_scale = sb;
+    P.c = o.c;
+    P.lda = lda;
+    P.ldb = ldb;
+    P.ldc = o.ld;
+    P.m = static_cast<uint32_t>(m);
+    P.n = static_cast<uint32_t>(n);
+    P.k = static_cast<uint32_t>(k);
+    P.a_vec = aligned16(a) && lda % 16 == 0;
+    P.b_vec = aligned16(b) && ldb % 16 == 0;
+    P.c_dtype = static_cast<uint32_t>(o.dtype);
+    P.rounding = o.rounding;
+    P.step = o.step;
+    P.early = early;
+    P.keys = make_keys(o.seed);
+    return int8few::run(P, stream);
+}
+
+asr_status gemm(const int8_t *a, uint64_t lda, const int8_t *b, uint64_t ldb, const float *sa, const float *sb,
+                const Output &o, uint64_t m, uint64_t n, uint64_t k, void *ws, uint64_t ws_bytes, cudaStream_t stream)
+{
+    asr_status st = output_kind(o);
+    if (st != ASR_OK) return st;
     if (m == 0 || n == 0) return ASR_OK;
     if (!sizes_ok(m, n, k) || k == 0) return ASR_ERR_INVALID_VALUE;
-    if (!a || !b || !sa || !sb || !c || lda < k || ldb < k || ldc < n || lda > (1ull << 32) || ldb > (1ull << 32) ||
-        ldc > (1ull << 32))
+    if (!a || !b || !sa || !sb || !pitch_ok(lda, k) || !pitch_ok(ldb, k) || !output_ok(o, n) ||
+        !muon::element_aligned(sa, ASR_F32) || !muon::element_aligned(sb, ASR_F32))
         return ASR_ERR_INVALID_VALUE;
-    if (!muon::element_aligned(sa, ASR_F32) || !muon::element_aligned(sb, ASR_F32) ||
-        !muon::element_aligned(c, c_dtype))
-        return ASR_ERR_INVALID_VALUE;
+    if (few(m)) return few_rows(a, lda, b, ldb, sa, sb, o, m, n, k, false, stream);
     const Layout L = layout(m, n, k);
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < L.bytes) return ASR_ERR_INVALID_VALUE;
     int pairs = 0;
-    asr_status st = prod::setup(&pairs);
+    st = prod::setup(&pairs);
     if (st != ASR_OK) return st;
     char *w = static_cast<char *>(ws);
     WidenParams W;
+    std::memset(&W, 0, sizeof(W));
     W.src[0] = a;
     W.src[1] = b;
     W.dst[0] = reinterpret_cast<__half *>(w + L.a);
@@ -307,26 +576,196 @@ asr_status gemm(const int8_t *a, uint64_t lda, const int8_t *b, uint64_t ldb, co
     W.dst_ld = L.ld;
     W.vec[0] = aligned16(a) && lda % 16 == 0;
     W.vec[1] = aligned16(b) && ldb % 16 == 0;
-    const uint64_t blocks = ((m + n) * (L.ld / 16) + kThreads - 1) / kThreads;
-    widen_kernel<<<static_cast<unsigned>(blocks < 65536 ? blocks : 65536), kThreads, 0, stream>>>(W);
+    widen_kernel<<<blocks_for((m + n) * ((k + 511) / 512), 8, 1216), kThreads, 0, stream>>>(W);
     st = launched(ASR_KERNEL_QUANTIZE);
     if (st != ASR_OK) return st;
-    prod::Params P;
+    return product<false, false>(stored(W.dst[0], m, k, L.ld), stored(W.dst[1], n, k, L.ld), sa, sb, o, stream);
+}
+
+// ---- the linear layer's calls
+
+struct LinearLayout {
+    uint64_t scale, a, b, bytes, ld;
+};
+
+LinearLayout linear_layout(uint64_t m, uint64_t n, uint64_t k)
+{
+    LinearLayout L;
+    L.ld = muon::up(k, 16);
+    L.scale = 0;
+    L.a = muon::up(m * sizeof(float), 256);
+    L.b = L.a + muon::up(m * L.ld * (few(m) ? 1 : 2), 256);
+    L.bytes = few(m) ? L.b : L.b + muon::up(n * L.ld * 2, 256);
+    return L;
+}
+
+asr_status linear(const void *x, int32_t x_dtype, uint64_t x_ld, const int8_t *qw, uint64_t ldw, const float *sw,
+                  const Output &o, uint64_t m, uint64_t n, uint64_t k, void *ws, uint64_t ws_bytes,
+                  cudaStream_t stream)
+{
+    if (x_dtype != ASR_F32 && x_dtype != ASR_BF16) return ASR_ERR_UNSUPPORTED_DTYPE;
+    asr_status st = output_kind(o);
+    if (st != ASR_OK) return st;
+    if (m == 0 || n == 0) return ASR_OK;
+    if (!sizes_ok(m, n, k) || k == 0) return ASR_ERR_INVALID_VALUE;
+    if (!x || !qw || !sw || !pitch_ok(x_ld, k) || !pitch_ok(ldw, k) || !output_ok(o, n) ||
+        !muon::element_aligned(x, x_dtype) || !muon::element_aligned(sw, ASR_F32))
+        return ASR_ERR_INVALID_VALUE;
+    const LinearLayout L = linear_layout(m, n, k);
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < L.bytes) return ASR_ERR_INVALID_VALUE;
+    int pairs = 0;
+    st = prod::setup(&pairs);
+    if (st != ASR_OK) return st;
+    char *w = static_cast<char *>(ws);
+    RowParams P;
     std::memset(&P, 0, sizeof(P));
-    P.batch = 1;
-    P.chunk = kChunk;
-    P.out_ld = ldc;
-    P.out_dtype = static_cast<uint32_t>(c_dtype);
-    P.rounding = rounding;
-    P.vec = muon::aligned32(c) && ldc % 16 == 0;
-    P.step = step;
-    P.row_scale = sa;
-    P.col_scale = sb;
-    P.keys = make_keys(seed);
-    P.slot[0].ptr = c;
-    const prod::Stored A{W.dst[0], m, k, L.ld, muon::up(m * L.ld * 2, 256) / 2};
-    const prod::Stored B{W.dst[1], n, k, L.ld, muon::up(n * L.ld * 2, 256) / 2};
-    return prod::launch<false, false, prod::kInt8>(A, B, P, ASR_KERNEL_PRODUCT, stream);
+    P.x = x;
+    P.q = w + L.a;
+    P.scale = reinterpret_cast<float *>(w + L.scale);
+    P.rows = m;
+    P.cols = k;
+    P.x_ld = x_ld;
+    P.q_ld = L.ld;
+    P.dtype = static_cast<uint32_t>(x_dtype);
+    P.vec = muon::units_aligned(x, x_ld, 0);
+    const unsigned row_blocks = blocks_for(m, 1, 65536);
+    if (few(m)) {
+        quantise_rows_kernel<false, false><<<row_blocks, kThreads, 0, stream>>>(P, row_blocks);
+        st = launched(ASR_KERNEL_QUANTIZE);
+        if (st != ASR_OK) return st;
+        // the weight is older than the quantiser's kernel, so it may be read while that runs
+        return few_rows(static_cast<const int8_t *>(P.q), L.ld, qw, ldw, P.scale, sw, o, m, n, k, true, stream);
+    }
+    P.w.src[0] = qw;
+    P.w.dst[0] = reinterpret_cast<__half *>(w + L.b);
+    P.w.rows[0] = n;
+    P.w.src_ld[0] = ldw;
+    P.w.cols = k;
+    P.w.dst_ld = L.ld;
+    P.w.vec[0] = aligned16(qw) && ldw % 16 == 0;
+    const unsigned more = blocks_for(n * ((k + 511) / 512), 8, 1216);
+    quantise_rows_kernel<false, true><<<row_blocks + more, kThreads, 0, stream>>>(P, row_blocks);
+    st = launched(ASR_KERNEL_QUANTIZE);
+    if (st != ASR_OK) return st;
+    return product<false, false>(stored(static_cast<__half *>(P.q), m, k, L.ld), stored(P.w.dst[0], n, k, L.ld),
+                                 P.scale, sw, o, stream);
+}
+
+struct GradLayout {
+    // maxima (zeroed together), scales, and the widened matrices
+    uint64_t max_row, max_dy, max_w, max_x, zeroed;
+    uint64_t row, col_dy, col_w, col_x;
+    uint64_t dy_row, dy_col, w, x, bytes, ldn, ldk;
+};
+
+GradLayout grad_layout(uint64_t t, uint64_t n, uint64_t k, bool dx, bool dw)
+{
+    GradLayout L;
+    L.ldn = muon::up(n, 16);
+    L.ldk = muon::up(k, 16);
+    uint64_t at = 0;
+    auto take = [&](uint64_t bytes) {
+        const uint64_t was = at;
+        at += muon::up(bytes, 256);
+        return was;
+    };
+    L.max_row = take(t * 4);
+    L.max_dy = take(n * 4);
+    L.max_w = take(dx ? k * 4 : 0);
+    L.max_x = take(dw ? k * 4 : 0);
+    L.zeroed = at;
+    L.row = take(t * 4);
+    L.col_dy = take(n * 4);
+    L.col_w = take(dx ? k * 4 : 0);
+    L.col_x = take(dw ? k * 4 : 0);
+    L.dy_row = take(dx ? t * L.ldn * 2 : 0);
+    L.dy_col = take(dw ? t * L.ldn * 2 : 0);
+    L.w = take(dx ? n * L.ldk * 2 : 0);
+    L.x = take(dw ? t * L.ldk * 2 : 0);
+    L.bytes = at;
+    return L;
+}
+
+bool grad_sizes_ok(uint64_t t, uint64_t n, uint64_t k)
+{
+    return sizes_ok(t, n, k) && n <= kMaxK && t <= kMaxK && k <= kMaxK;
+}
+
+struct GradSource {
+    const void *p;
+    uint64_t ld;
+    int32_t dtype;
+};
+
+asr_status grads(const GradSource &dy, const GradSource &x, const GradSource &w, uint16_t *dx, uint64_t dx_ld,
+                 uint16_t *dw, uint64_t dw_ld, uint64_t t, uint64_t n, uint64_t k, uint32_t step, uint64_t seed,
+                 void *ws, uint64_t ws_bytes, cudaStream_t stream)
+{
+    auto known = [](const GradSource &s) { return s.dtype == ASR_F32 || s.dtype == ASR_BF16; };
+    if (!known(dy) || (dw && !known(x)) || (dx && !known(w))) return ASR_ERR_UNSUPPORTED_DTYPE;
+    if (!dx && !dw) return ASR_OK;
+    if (t == 0 || n == 0 || k == 0 || !grad_sizes_ok(t, n, k)) return ASR_ERR_INVALID_VALUE;
+    const Output ox{dx, dx_ld, ASR_BF16, ASR_ROUND_RNE, 0, 0}, ow{dw, dw_ld, ASR_BF16, ASR_ROUND_RNE, 0, 0};
+    if (!dy.p || !pitch_ok(dy.ld, n) || !muon::element_aligned(dy.p, dy.dtype)) return ASR_ERR_INVALID_VALUE;
+    if (dx && (!w.p || !pitch_ok(w.ld, k) || !muon::element_aligned(w.p, w.dtype) || !output_ok(ox, k)))
+        return ASR_ERR_INVALID_VALUE;
+    if (dw && (!x.p || !pitch_ok(x.ld, k) || !muon::element_aligned(x.p, x.dtype) || !output_ok(ow, k)))
+        return ASR_ERR_INVALID_VALUE;
+    const GradLayout L = grad_layout(t, n, k, dx != nullptr, dw != nullptr);
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < L.bytes) return ASR_ERR_INVALID_VALUE;
+    int pairs = 0;
+    asr_status st = prod::setup(&pairs);
+    if (st != ASR_OK) return st;
+    char *b = static_cast<char *>(ws);
+    auto words = [&](uint64_t at) { return reinterpret_cast<uint32_t *>(b + at); };
+    auto floats = [&](uint64_t at) { return reinterpret_cast<float *>(b + at); };
+    auto halves = [&](uint64_t at) { return reinterpret_cast<__half *>(b + at); };
+    const cudaError_t e = cudaMemsetAsync(ws, 0, L.zeroed, stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+    SideParams M;
+    std::memset(&M, 0, sizeof(M));
+    M.step = step;
+    M.keys = make_keys(seed);
+    Side &D = M.s[M.count++];
+    D = side(dy.p, dy.dtype, t, n, dy.ld, 0);
+    D.row_max = words(L.max_row);
+    D.col_max = words(L.max_dy);
+    D.row_scale = floats(L.row);
+    D.col_scale = floats(L.col_dy);
+    D.by_row = dx ? halves(L.dy_row) : nullptr;
+    D.by_col = dw ? halves(L.dy_col) : nullptr;
+    D.q_ld = L.ldn;
+    M.blocks = side_blocks(D);
+    if (dx) {
+        Side &W = M.s[M.count++];
+        W = side(w.p, w.dtype, n, k, w.ld, M.blocks);
+        W.col_max = words(L.max_w);
+        W.col_scale = floats(L.col_w);
+        W.by_col = halves(L.w);
+        W.q_ld = L.ldk;
+        M.blocks += side_blocks(W);
+    }
+    if (dw) {
+        Side &X = M.s[M.count++];
+        X = side(x.p, x.dtype, t, k, x.ld, M.blocks);
+        X.col_max = words(L.max_x);
+        X.col_scale = floats(L.col_x);
+        X.by_col = halves(L.x);
+        X.q_ld = L.ldk;
+        M.blocks += side_blocks(X);
+    }
+    max_kernel<<<M.blocks, kThreads, 0, stream>>>(M);
+    st = launched(ASR_KERNEL_QUANTIZE);
+    if (st != ASR_OK) return st;
+    wide_kernel<<<M.blocks, kThreads, 0, stream>>>(M);
+    st = launched(ASR_KERNEL_QUANTIZE);
+    if (st == ASR_OK && dx)
+        st = product<false, true>(stored(halves(L.dy_row), t, n, L.ldn), stored(halves(L.w), n, k, L.ldk),
+                                  floats(L.row), floats(L.col_w), ox, stream);
+    if (st == ASR_OK && dw)
+        st = product<true, true>(stored(halves(L.dy_col), t, n, L.ldn), stored(halves(L.x), t, k, L.ldk),
+                                 floats(L.col_dy), floats(L.col_x), ow, stream);
+    return st;
 }
 
 }  // namespace int8

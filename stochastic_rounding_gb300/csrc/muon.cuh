@@ -29,7 +29,8 @@
 namespace muon {
 
 constexpr int kThreads = 256;
-constexpr int kPartBlocks = 256;            // partial sums a matrix at most
+constexpr int kPartBlocks = 1024;           // partial sums a matrix at most
+constexpr int kSpan = 256;                  // columns a warp takes at a time, eight a lane
 constexpr float kStore = 4096.0f;
 constexpr double kLargest = 8.0;            // bound of every stored value / 2^12
 
@@ -83,16 +84,44 @@ __device__ __forceinline__ float update_of(const PrepParams &P, float g, float m
     return P.nesterov ? __fadd_rn(g, __fmul_rn(P.mu, __fsub_rn(m, g))) : m;
 }
 
+// A warp's way through a matrix in spans of kSpan columns: span `at` counted
+// along the rows, then every `stride`-th.  One division at the start instead of
+// one an element.
+struct Walk {
+    uint64_t row, rows;
+    uint32_t span, spans, dspan;
+    uint64_t drow;
+    __device__ Walk(uint64_t rows_, uint64_t cols, uint64_t at, uint64_t stride)
+    {
+        rows = rows_;
+        spans = static_cast<uint32_t>((cols + kSpan - 1) / kSpan);
+        row = at / spans;
+        span = static_cast<uint32_t>(at % spans);
+        drow = stride / spans;
+        dspan = static_cast<uint32_t>(stride % spans);
+    }
+    __device__ bool more() const { return row < rows; }
+    __device__ void next()
+    {
+        row += drow;
+        span += dspan;
+        if (span >= spans) {
+            span -= spans;
+            ++row;
+        }
+    }
+};
+
 // First pass: m <- m + (1 - mu)(g - m) (MUON), and each block's sum of squares.
 template <bool MUON>
 __global__ void __launch_bounds__(kThreads) square_sum_kernel(const __grid_constant__ PrepParams P)
 {
     const Matrix M = P.m[blockIdx.y];
-    const uint64_t per_row = (P.cols + 7) / 8, units = P.rows * per_row;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float sum = 0.0f;
-    for (uint64_t u = blockIdx.x * static_cast<uint64_t>(kThreads) + threadIdx.x; u < units;
-         u += static_cast<uint64_t>(P.blocks) * kThreads) {
-        const uint64_t row = u / per_row, col = (u - row * per_row) * 8;
+    for (Walk k(P.rows, P.cols, blockIdx.x * 8ull + warp, P.blocks * 8ull); k.more(); k.next()) {
+        const uint64_t row = k.row, col = k.span * static_cast<uint64_t>(kSpan) + lane * 8;
+        if (col >= P.cols) continue;
         const int live = P.cols - col < 8 ? static_cast<int>(P.cols - col) : 8;
         float x[8];
         load8(M.src, P.src_dtype, row * P.src_ld + col, live, P.vec, x);
@@ -120,7 +149,7 @@ __global__ void __launch_bounds__(kThreads) square_sum_kernel(const __grid_const
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     __shared__ float part[kThreads / 32];
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
+    if (lane == 0) part[warp] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int w = 1; w < kThreads / 32; ++w) sum += part[w];
@@ -135,25 +164,22 @@ template <bool MUON>
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ PrepParams P)
 {
     const Matrix M = P.m[blockIdx.y];
-    __shared__ float factor;
-    if (threadIdx.x < 32) {
-        double sum = 0.0;
-        for (uint32_t i = threadIdx.x; i < P.blocks; i += 32) sum += P.partial[blockIdx.y * P.blocks + i];
+    __shared__ float part[kThreads / 32];
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float sum = 0.0f;
+    for (uint32_t i = threadIdx.x; i < P.blocks; i += kThreads) sum += P.partial[blockIdx.y * P.blocks + i];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        if (threadIdx.x == 0) {
-            const double norm = sqrt(sum);
-            factor = norm <= 3.0e38 ? static_cast<float>(static_cast<double>(kStore) / fmax(norm, static_cast<double>(P.eps)))
-                                    : __int_as_float(0x7FC00000);
-        }
-    }
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (lane == 0) part[warp] = sum;
     __syncthreads();
-    const float f = factor;
-    const uint64_t per_row = (P.cols + 7) / 8, units = P.rows * per_row;
+    sum = 0.0f;
+    for (int w = 0; w < kThreads / 32; ++w) sum += part[w];
+    const float norm = __fsqrt_rn(sum);
+    const float f = norm <= 3.402823466e38f ? __fdiv_rn(kStore, fmaxf(norm, P.eps)) : __int_as_float(0x7FC00000);
     __half *out = P.out + blockIdx.y * P.out_stride;
-    for (uint64_t u = blockIdx.x * static_cast<uint64_t>(kThreads) + threadIdx.x; u < units;
-         u += static_cast<uint64_t>(gridDim.x) * kThreads) {
-        const uint64_t row = u / per_row, col = (u - row * per_row) * 8;
+    for (Walk k(P.rows, P.cols, blockIdx.x * 8ull + warp, gridDim.x * 8ull); k.more(); k.next()) {
+        const uint64_t row = k.row, col = k.span * static_cast<uint64_t>(kSpan) + lane * 8;
+        if (col >= P.cols) continue;
         const int live = P.cols - col < 8 ? static_cast<int>(P.cols - col) : 8;
         float x[8];
         load8(M.src, P.src_dtype, row * P.src_ld + col, live, P.vec, x);
@@ -267,9 +293,11 @@ asr_status prep(const Group &G, const NsParams &ns, const Layout &L, char *ws, f
     P.src_ld = G.src_ld;
     P.src_dtype = G.src_dtype;
     P.vec = G.vec_in;
-    const uint64_t units = G.rows * ((G.cols + 7) / 8);
-    const uint64_t want = (units + kThreads - 1) / kThreads;
-    P.blocks = static_cast<uint32_t>(want < kPartBlocks ? want : kPartBlocks);
+    // eight spans a block at least, and no more blocks than fill the GPU (152
+    // SMs, eight a SM) or make enough partial sums
+    const uint64_t want = (G.rows * ((G.cols + kSpan - 1) / kSpan) + 7) / 8;
+    const uint64_t fill = std::max<uint64_t>(16, std::min<uint64_t>(kPartBlocks, 1216 / G.batch));
+    P.blocks = static_cast<uint32_t>(want < fill ? want : fill);
     P.nesterov = nesterov;
     P.mu = mu;
     P.omu = static_cast<float>(1.0 - static_cast<double>(mu));
@@ -283,8 +311,7 @@ asr_status prep(const Group &G, const NsParams &ns, const Layout &L, char *ws, f
     square_sum_kernel<MUON><<<grid, kThreads, 0, stream>>>(P);
     asr_status st = launched(ASR_KERNEL_MATRIX_PREP);
     if (st != ASR_OK) return st;
-    const dim3 grid2(static_cast<unsigned>(want < 2048 ? want : 2048), G.batch, 1);
-    scale_kernel<MUON><<<grid2, kThreads, 0, stream>>>(P);
+    scale_kernel<MUON><<<grid, kThreads, 0, stream>>>(P);
     return launched(ASR_KERNEL_MATRIX_PREP);
 }
 

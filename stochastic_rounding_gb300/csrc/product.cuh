@@ -51,7 +51,12 @@ constexpr uint32_t kStageBytes = 4 * kHalfBytes;
 constexpr int kAccBufs = 2;
 constexpr uint32_t kTmemCols = kTile * kAccBufs;
 constexpr int kBars = kStages * 3 + 2 * kAccBufs + 1;
-constexpr int kSmem = 1024 + kStages * kStageBytes + kBars * 8 + 16;
+// Per epilogue warp, 32 rows x 32 columns of binary32 on their way out, rows 33
+// words apart so that neither rows nor columns collide in a bank.
+constexpr int kPitch = 33;
+constexpr uint32_t kWarpStage = 32 * kPitch * 4;
+constexpr int kBarBytes = (kBars * 8 + 16 + 127) / 128 * 128;
+constexpr int kSmem = 1024 + kStages * kStageBytes + kBarBytes + kEpi * kWarpStage;
 constexpr int kGroupM = 8;
 constexpr int kMaxBatch = 64;                   // matrices per launch
 
@@ -163,18 +168,6 @@ __device__ __forceinline__ Item work_item(const Params &P, uint32_t t)
     return it;
 }
 
-// The 16 random words of elements e .. e+15.
-__device__ __forceinline__ void words16(uint64_t e, uint32_t step, const RoundKeys &K, uint32_t r[16])
-{
-    if ((e & 3u) == 0) {
-        unit_words<true>(e, 0, step, K, r);
-        unit_words<true>(e + 8, 0, step, K, r + 8);
-    } else {
-        unit_words<false>(e, 0, step, K, r);
-        unit_words<false>(e + 8, 0, step, K, r + 8);
-    }
-}
-
 __device__ __forceinline__ void ld_global_v8(const void *p, uint32_t w[8])
 {
     asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -183,123 +176,197 @@ __device__ __forceinline__ void ld_global_v8(const void *p, uint32_t w[8])
                  : "memory");
 }
 
-// 16 values of one row to a bf16 matrix (dst: their place in it); `live` of
-// them are inside the matrix; random bits of elements e .. e+15.
-__device__ __forceinline__ void store_bf16(uint16_t *dst, const float x[16], int live, bool vec, uint32_t rounding,
-                                           uint64_t e, uint32_t step, const RoundKeys &K)
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t v[32])
 {
-    uint32_t w[8];
-    if (rounding == ASR_ROUND_SR) {
-        uint32_t r[16];
-        words16(e, step, K, r);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) w[q] = sr_pack2<true>(x[2 * q], x[2 * q + 1], r[2 * q], r[2 * q + 1]);
-    } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) w[q] = pack_bf16(round_rne(x[2 * q]), round_rne(x[2 * q + 1]));
-    }
-    if (vec && live >= 16) {
-        st_global_v8(dst, w);
-    } else {
-#pragma unroll
-        for (int q = 0; q < 16; ++q)
-            if (q < live) dst[q] = static_cast<uint16_t>(w[q >> 1] >> ((q & 1) * 16));
-    }
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void store_f32(float *dst, const float x[16], int live, bool vec)
-{
-    if (vec && live >= 16) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            reinterpret_cast<float4 *>(dst)[q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-    } else {
-#pragma unroll
-        for (int q = 0; q < 16; ++q)
-            if (q < live) dst[q] = x[q];
-    }
-}
-
-// 16 sums of row `row`, columns col .. col+15, to the output.  Sums of
-// columns past n (operands read as zeros there) are zero; rows past m are
-// skipped by the caller.
+// 32 sums of this lane's row `row`, columns col .. col+31, to a stored matrix.
+// Rows past m are not written; columns are, up to the row's padding (their
+// sums are zero: operands read as zeros there).  Where the tile has a mirror
+// image, the block goes out a second time, turned in the warp's staging area.
 template <int OP>
-__device__ __forceinline__ void store_sums(const Params &P, const Item &it, uint32_t row, uint32_t col, float x[16])
+__device__ __forceinline__ void store_stored(const Params &P, const Item &it, uint32_t row, uint32_t col, float x[32],
+                                             float *stage, int lane)
 {
-    if constexpr (OP == kGram || OP == kPoly || OP == kNext) {
-        __half *mat = P.out + it.z * P.stride;
-        const uint64_t at = static_cast<uint64_t>(row) * P.ld + col;
-        if constexpr (OP == kPoly) {
-            uint32_t s[8];
-            ld_global_v8(P.aux + it.z * P.stride + at, s);
+    __half *mat = P.out + it.z * P.stride;
+    const uint64_t at = static_cast<uint64_t>(row) * P.ld + col;
+    const bool in = row < P.m;
+    if constexpr (OP == kPoly) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t s[8] = {};
+            if (in && col + 16 * h < P.n) ld_global_v8(P.aux + it.z * P.stride + at + 16 * h, s);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 const float2 v = unpack_f16(s[q]);
-                x[2 * q] = fmaf(P.alpha, x[2 * q], P.beta * v.x);
-                x[2 * q + 1] = fmaf(P.alpha, x[2 * q + 1], P.beta * v.y);
+                x[16 * h + 2 * q] = fmaf(P.alpha, x[16 * h + 2 * q], P.beta * v.x);
+                x[16 * h + 2 * q + 1] = fmaf(P.alpha, x[16 * h + 2 * q + 1], P.beta * v.y);
             }
+        }
+        if (!it.mirror) {
             const uint32_t d = row - col;
 #pragma unroll
-            for (int q = 0; q < 16; ++q)
+            for (int q = 0; q < 32; ++q)
                 if (d == static_cast<uint32_t>(q)) x[q] += P.diag;
-        } else {
-#pragma unroll
-            for (int q = 0; q < 16; ++q) x[q] *= P.alpha;
-        }
-        uint32_t w[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) w[q] = pack_f16(x[2 * q], x[2 * q + 1]);
-        st_global_v8(mat + at, w);
-        if (OP != kNext && it.mirror) {
-            uint16_t *dst = reinterpret_cast<uint16_t *>(mat) + static_cast<uint64_t>(col) * P.ld + row;
-#pragma unroll
-            for (int q = 0; q < 16; ++q)
-                if (col + q < P.n) dst[static_cast<uint64_t>(q) * P.ld] = static_cast<uint16_t>(w[q >> 1] >> ((q & 1) * 16));
         }
     } else {
-        const int live = P.n - col < 16 ? static_cast<int>(P.n - col) : 16;
-        const Slot &S = P.slot[it.z];
-        const uint64_t at = static_cast<uint64_t>(row) * P.out_ld + col;
-        const uint64_t e = S.base + static_cast<uint64_t>(row) * P.n + col;
-        if constexpr (OP == kParam) {
-            if (P.out_dtype == ASR_BF16) {
-                uint16_t *p = static_cast<uint16_t *>(S.ptr) + at;
+#pragma unroll
+        for (int q = 0; q < 32; ++q) x[q] *= P.alpha;
+    }
+    if (in) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t w[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) w[q] = pack_f16(x[16 * h + 2 * q], x[16 * h + 2 * q + 1]);
+            if (col + 16 * h < P.n) st_global_v8(mat + at + 16 * h, w);
+        }
+    }
+    if (OP != kNext && it.mirror) {
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 32; ++q) stage[lane * kPitch + q] = x[q];
+        __syncwarp();
+        if (col + lane < P.n) {
+            const uint32_t row0 = row - lane;        // row col + lane of the image, its columns row0 .. row0+31
+            __half *dst = mat + static_cast<uint64_t>(col + lane) * P.ld + row0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
                 uint32_t w[8];
-                if (P.vec && live >= 16) {
-                    ld_global_v8(p, w);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    w[q] = pack_f16(stage[(16 * h + 2 * q) * kPitch + lane], stage[(16 * h + 2 * q + 1) * kPitch + lane]);
+                if (row0 + 16 * h < P.m) st_global_v8(dst + 16 * h, w);
+            }
+        }
+    }
+}
+
+// A 32 x 32 block of sums in the warp's staging area (lane r wrote row r), first
+// row row0 and column col, to the caller's matrix.  Each lane finishes its own
+// row, eight columns at a time; full blocks of aligned matrices are stored from
+// there (and parameters read), others pass through the staging area once more,
+// so that the lanes lie along a row in memory whatever the row pitch.
+template <int OP>
+__device__ __forceinline__ void finish_block(const Params &P, uint32_t z, uint32_t row0, uint32_t col, float *stage)
+{
+    const int lane = threadIdx.x & 31;
+    const uint32_t row = row0 + lane;
+    const uint32_t live = P.n - col < 32 ? P.n - col : 32, rows = P.m - row0 < 32 ? P.m - row0 : 32;
+    const bool direct = P.vec && live == 32, bf16 = P.out_dtype == ASR_BF16;
+    const Slot S = P.slot[z];
+    uint16_t *out16 = static_cast<uint16_t *>(S.ptr);
+    float *out32 = static_cast<float *>(S.ptr);
+    const uint64_t at0 = static_cast<uint64_t>(row0) * P.out_ld + col;
+    float *own = stage + lane * kPitch;
+    float p[32];
+    if constexpr (OP == kParam) {
+        // the parameters, into this lane's registers
+        if (direct) {
+            if (row < P.m) {
+                const uint64_t at = at0 + lane * P.out_ld;
+                if (bf16) {
+                    uint32_t w[16];
+                    ld_global_v8(out16 + at, w);
+                    ld_global_v8(out16 + at + 16, w + 8);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) p[2 * q] = bf16_lo(w[q]), p[2 * q + 1] = bf16_hi(w[q]);
                 } else {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        w[q] = (2 * q < live ? p[2 * q] : 0u) | (2 * q + 1 < live ? static_cast<uint32_t>(p[2 * q + 1]) << 16 : 0u);
-                }
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t w[8];
+                        ld_global_v8(out32 + at + 8 * h, w);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    x[2 * q] = __fsub_rn(__fmul_rn(bf16_lo(w[q]), P.beta), __fmul_rn(P.alpha, x[2 * q]));
-                    x[2 * q + 1] = __fsub_rn(__fmul_rn(bf16_hi(w[q]), P.beta), __fmul_rn(P.alpha, x[2 * q + 1]));
+                        for (int q = 0; q < 8; ++q) p[8 * h + q] = __uint_as_float(w[q]);
+                    }
                 }
-                store_bf16(p, x, live, P.vec, P.rounding, e, P.step, P.keys);
-            } else {
-                float *p = static_cast<float *>(S.ptr) + at;
-#pragma unroll
-                for (int q = 0; q < 16; ++q)
-                    x[q] = __fsub_rn(__fmul_rn(q < live ? p[q] : 0.0f, P.beta), __fmul_rn(P.alpha, x[q]));
-                store_f32(p, x, live, P.vec);
             }
         } else {
-            if constexpr (OP == kInt8) {
-                const float rs = P.row_scale[row];
+            float sum[32];
 #pragma unroll
-                for (int q = 0; q < 16; ++q)
-                    x[q] = __fmul_rn(__fmul_rn(x[q], rs), q < live ? __ldg(P.col_scale + col + q) : 0.0f);
+            for (int q = 0; q < 32; ++q) sum[q] = own[q];
+            __syncwarp();
+#pragma unroll 8
+            for (uint32_t r = 0; r < 32; ++r) {
+                const uint64_t at = at0 + r * P.out_ld + lane;
+                if (r < rows && lane < live) stage[r * kPitch + lane] = bf16 ? bf16_lo(out16[at]) : out32[at];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 32; ++q) {
+                p[q] = own[q];
+                own[q] = sum[q];
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 32; ++q) own[q] = __fsub_rn(__fmul_rn(p[q], P.beta), __fmul_rn(P.alpha, own[q]));
+    }
+    const float rs = OP == kInt8 && row < P.m ? P.row_scale[row] : 0.0f;
+    const uint64_t e = S.base + static_cast<uint64_t>(row) * P.n + col;
+    uint32_t w[4];
+#pragma unroll 1
+    for (int u = 0; u < 4; ++u) {
+        float x[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            x[q] = own[8 * u + q];
+            if constexpr (OP == kInt8)
+                x[q] = __fmul_rn(__fmul_rn(x[q], rs), 8 * u + q < live ? __ldg(P.col_scale + col + 8 * u + q) : 0.0f);
+            if constexpr (OP == kOut) x[q] *= P.alpha;
+        }
+        if (bf16) {
+            uint32_t h[8];
+            if (P.rounding == ASR_ROUND_SR) {
+                uint32_t r[8];
+                if ((e & 3u) == 0) unit_words<true>(e, 8 * u, P.step, P.keys, r);
+                else unit_words<false>(e, 8 * u, P.step, P.keys, r);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) h[q] = round_sr(x[q], r[q]);
             } else {
 #pragma unroll
-                for (int q = 0; q < 16; ++q) x[q] *= P.alpha;
+                for (int q = 0; q < 8; ++q) h[q] = round_rne(x[q]);
             }
-            if (P.out_dtype == ASR_BF16)
-                store_bf16(static_cast<uint16_t *>(S.ptr) + at, x, live, P.vec, P.rounding, e, P.step, P.keys);
-            else
-                store_f32(static_cast<float *>(S.ptr) + at, x, live, P.vec);
+            if (direct) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) w[q] = pack_bf16(h[2 * q], h[2 * q + 1]);
+                if (row < P.m)
+                    *reinterpret_cast<uint4 *>(out16 + at0 + lane * P.out_ld + 8 * u) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) own[8 * u + q] = __uint_as_float(h[q]);
+            }
+        } else if (direct) {
+            uint32_t v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = __float_as_uint(x[q]);
+            if (row < P.m) st_global_v8(out32 + at0 + lane * P.out_ld + 8 * u, v);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) own[8 * u + q] = x[q];
         }
+    }
+    __syncwarp();
+    if (!direct) {
+#pragma unroll 8
+        for (uint32_t r = 0; r < 32; ++r) {
+            const uint64_t at = at0 + r * P.out_ld + lane;
+            if (r < rows && lane < live) {
+                const float v = stage[r * kPitch + lane];
+                if (bf16) out16[at] = static_cast<uint16_t>(__float_as_uint(v));
+                else out32[at] = v;
+            }
+        }
+        __syncwarp();
     }
 }
 
@@ -461,6 +528,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         // ------------------------------------------------------- epilogue
         const int quarter = warp & 3;
         const uint32_t c_lo = static_cast<uint32_t>((warp - 2) / 4) * kSpan;
+        float *stage = reinterpret_cast<float *>(smem_raw + (bars + kBarBytes - raw) + (warp - 2) * kWarpStage);
         uint32_t i = 0;
         bool ok = true;
         for (uint32_t t = cluster; ok && t < items; t += clusters) {
@@ -468,6 +536,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             const uint32_t row = it.m0 + rank * 128 + quarter * 32 + lane;
             const uint32_t ncols = it.n0 >= P.n ? 0 : P.n - it.n0 < it.width ? P.n - it.n0 : it.width;
             const uint32_t c_hi = ncols < c_lo + kSpan ? ncols : c_lo + kSpan;
+            constexpr bool kStored = OP == kGram || OP == kPoly || OP == kNext;
             int32_t acc[OP == kInt8 ? kSpan : 1];
             for (uint32_t kc = 0; kc < kblocks; kc += P.chunk, ++i) {
                 const int b = static_cast<int>(i % kAccBufs);
@@ -478,31 +547,62 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t tq =
                     tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(b * kTile) + c_lo;
-                const bool last = kblocks - kc <= P.chunk;
+                // this warp has read its part of accumulator b
+                auto release = [&]() {
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(peer_addr(acc_empty(b), 0));
+                };
+                if constexpr (OP == kInt8) {
 #pragma unroll
-                for (int c = 0; c < kSpan; c += 16) {
-                    if (c_lo + c >= c_hi) continue;             // the same for the whole warp
-                    uint32_t v[16];
-                    gemm::tmem_ld16(tq + c, v);
-                    float x[16];
-                    if constexpr (OP == kInt8) {
+                    for (int c = 0; c < kSpan; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(tq + c, v);
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) {
+                        for (int q = 0; q < 32; ++q) {
                             const int32_t a = __float2int_rn(__uint_as_float(v[q]));
                             acc[c + q] = kc == 0 ? a : acc[c + q] + a;
                         }
-                        if (!last) continue;
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) x[q] = __int2float_rn(acc[c + q]);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) x[q] = __uint_as_float(v[q]);
                     }
-                    if (row < P.m) store_sums<OP>(P, it, row, it.n0 + c_lo + c, x);
+                    release();
+                } else {
+#pragma unroll (kStored ? kSpan / 32 : 1)
+                    for (int c = 0; c < kSpan; c += 32) {
+                        uint32_t v[32];
+                        const bool have = c_lo + c < c_hi;      // the same for the whole warp
+                        if (have) tmem_ld32(tq + c, v);
+                        if (c + 32 == kSpan) release();
+                        if (!have) continue;
+                        float x[32];
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) x[q] = __uint_as_float(v[q]);
+                        if constexpr (kStored) {
+                            store_stored<OP>(P, it, row, it.n0 + c_lo + c, x, stage, lane);
+                        } else if (row - lane < P.m) {
+#pragma unroll
+                            for (int q = 0; q < 32; ++q) stage[lane * kPitch + q] = x[q];
+                            __syncwarp();
+                            finish_block<OP>(P, it.z, row - lane, it.n0 + c_lo + c, stage);
+                        }
+                    }
                 }
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(peer_addr(acc_empty(b), 0));
+            }
+            if constexpr (OP == kInt8) {
+                if (ok && row - lane < P.m) {
+                    // one copy of the finishing code for the four blocks
+#pragma unroll 1
+                    for (int c = 0; c < kSpan; c += 32) {
+                        if (c_lo + c >= c_hi) break;
+#pragma unroll
+                        for (int d = 0; d < kSpan; d += 32) {
+                            if (c != d) continue;
+#pragma unroll
+                            for (int q = 0; q < 32; ++q) stage[lane * kPitch + q] = __int2float_rn(acc[d + q]);
+                        }
+                        __syncwarp();
+                        finish_block<OP>(P, it.z, row - lane, it.n0 + c_lo + c, stage);
+                    }
+                }
             }
         }
     }
@@ -569,6 +669,8 @@ asr_status setup(int *pairs)
         if (e == cudaSuccess) e = setup_one<false, true, kParam>(sms, &n);
         if (e == cudaSuccess) e = setup_one<false, false, kParam>(sms, &n);
         if (e == cudaSuccess) e = setup_one<false, false, kInt8>(sms, &n);
+        if (e == cudaSuccess) e = setup_one<false, true, kInt8>(sms, &n);
+        if (e == cudaSuccess) e = setup_one<true, true, kInt8>(sms, &n);
         if (e != cudaSuccess) return cuda_fail(e);
         if (n < 1) return cuda_fail(cudaErrorNotSupported);
         g_prod_pairs[dev] = n;

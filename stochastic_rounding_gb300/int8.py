@@ -13,15 +13,7 @@ from __future__ import annotations
 
 import torch
 
-from . import _lib
-from ._lib import asr_gemm_int8_sr, asr_quantize_int8, int8_empty
-
-
-def _quantised(x, axis="rows", **kw):
-    rows, cols = x.shape if axis == "rows" else (x.shape[1], x.shape[0])
-    q = int8_empty(rows, cols, x.device)
-    scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-    return asr_quantize_int8(x, q, scale, axis=axis, **kw)
+from ._lib import asr_linear_int8, asr_linear_int8_grads, asr_quantize_int8, int8_empty
 
 
 def int8_linear(x, qweight, weight_scale, *, rounding="rne", step: int = 0, seed: int = 0, out=None):
@@ -30,26 +22,15 @@ def int8_linear(x, qweight, weight_scale, *, rounding="rne", step: int = 0, seed
     otherwise.  ``rounding="sr"`` rounds the outputs stochastically."""
     if out is None:
         out = torch.empty(x.shape[0], qweight.shape[0], dtype=torch.bfloat16, device=x.device)
-    q, scale = _quantised(x)
-    return asr_gemm_int8_sr(q, qweight, scale, weight_scale, out, rounding=rounding, step=step, seed=seed)
+    return asr_linear_int8(x, qweight, weight_scale, out, rounding=rounding, step=step, seed=seed)
 
 
 def int8_linear_grads(dy, x, weight, *, step: int = 0, seed: int = 0, need_dx=True, need_dw=True):
     """Gradients of ``y = x weight^T`` from ``dy`` (tokens, n): (dx, dw) in
     bfloat16, either None where it is not needed."""
-    dx = dw = None
-    tokens, n = dy.shape
-    k = x.shape[1]
-    if need_dx:
-        dx = torch.empty(tokens, k, dtype=torch.bfloat16, device=dy.device)
-        q, s = _quantised(dy, rounding="sr", step=step, seed=seed)
-        v, t = _quantised(weight, "columns")
-        asr_gemm_int8_sr(q, v, s, t, dx, rounding="rne")
-    if need_dw:
-        dw = torch.empty(n, k, dtype=torch.bfloat16, device=dy.device)
-        q, s = _quantised(dy, "columns", rounding="sr", step=step, seed=seed)
-        v, t = _quantised(x, "columns")
-        asr_gemm_int8_sr(q, v, s, t, dw, rounding="rne")
+    dx = torch.empty(x.shape, dtype=torch.bfloat16, device=dy.device) if need_dx else None
+    dw = torch.empty(weight.shape, dtype=torch.bfloat16, device=dy.device) if need_dw else None
+    asr_linear_int8_grads(dy, x, weight, dx, dw, step=step, seed=seed)
     return dx, dw
 
 
@@ -58,7 +39,9 @@ class _Int8LinearFunction(torch.autograd.Function):
     def forward(ctx, x, weight, step, seed):
         ctx.save_for_backward(x, weight)
         ctx.key = (step, seed)
-        q, scale = _quantised(weight)
+        q = int8_empty(*weight.shape, weight.device)
+        scale = torch.empty(weight.shape[0], dtype=torch.float32, device=weight.device)
+        asr_quantize_int8(weight, q, scale)
         return int8_linear(x, q, scale)
 
     @staticmethod

@@ -245,6 +245,31 @@ def test_linear_and_its_gradients(asr):
         assert_same_bits(host(got), host(_want_product(a, b, sa, sb).bfloat16()))
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("size", [(1, 300, 515), (40, 64, 1000), (200, 130, 77), (513, 1001, 257)])
+def test_linear_from_either_type_strided(asr, dtype, size):
+    """The one call gives what the quantiser and the product give, on strided
+    views; each gradient alone as both together."""
+    import torch
+    torch.manual_seed(size[1])
+    t, n, k = size
+    mk = lambda r, c: torch.randn(r + 1, c + 5, device="cuda").to(getattr(torch, dtype))[1:, 2:c + 2]  # noqa: E731
+    x, w, dy = mk(t, k), mk(n, k), mk(t, n)
+    qw, sw = asr.asr_quantize_int8(w, asr.int8_empty(n, k), torch.empty(n, device="cuda"))
+    qx, sx = asr.asr_quantize_int8(x, asr.int8_empty(t, k), torch.empty(t, device="cuda"))
+    y = torch.empty(t, n, device="cuda")
+    asr.int8_linear(x, qw, sw, out=y)
+    assert_same_bits(host(y), host(_want_product(qx, qw, sx, sw)))
+    dx, dw = asr.int8_linear_grads(dy, x, w, step=1, seed=2)
+    a, sa = asr.asr_quantize_int8(dy, asr.int8_empty(t, n), torch.empty(t, device="cuda"), rounding="sr", step=1, seed=2)
+    b, sb = asr.asr_quantize_int8(w, asr.int8_empty(k, n), torch.empty(k, device="cuda"), axis="columns")
+    assert_same_bits(host(dx), host(_want_product(a, b, sa, sb).bfloat16()))
+    only, none = asr.int8_linear_grads(dy, x, w, step=1, seed=2, need_dw=False)
+    assert none is None and torch.equal(only, dx)
+    none, only = asr.int8_linear_grads(dy, x, w, step=1, seed=2, need_dx=False)
+    assert none is None and torch.equal(only, dw)
+
+
 def test_linear_module_gradients_against_differences(asr):
     """Int8Linear's gradients along a direction against differences of the
     unquantised layer.  One entry of an operand is off by at most half a step
@@ -298,8 +323,10 @@ def test_refusals(asr):
         asr.asr_gemm_int8_sr(a.cpu(), b, sa, sb, c)
     with pytest.raises(ValueError):
         asr.asr_gemm_int8_sr(a, b, sa, sb, c.t().contiguous().t())
+    a2, b2, sa2, sb2 = _operands(100, 6, 32, 1)      # with many rows the product needs a workspace
     with pytest.raises(ValueError):
-        asr.asr_gemm_int8_sr(a, b, sa, sb, c, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        asr.asr_gemm_int8_sr(a2, b2, sa2, sb2, torch.empty(100, 6, device="cuda"),
+                             workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         asr.asr_quantize_int8(c, asr.int8_empty(4, 6), sa, axis="both")
     with pytest.raises(ValueError):
