@@ -367,7 +367,7 @@ asr_status asr_quantize_int8(const void *x, int32_t x_dtype, uint64_t rows, uint
  * nearest-even.  1 <= k <= 131071, m and n at most 2^24; any alignment and
  * pitch (16-byte aligned operands with pitches a multiple of 16 are read
  * faster).  m == 0 or n == 0 is a no-op.  workspace: device, 256-byte aligned,
- * at least asr_gemm_int8_workspace's bytes (none, and NULL, up to 64 rows). */
+ * at least asr_gemm_int8_workspace's bytes. */
 asr_status asr_gemm_int8_sr(const int8_t *a, uint64_t lda, const int8_t *b, uint64_t ldb,
                             const float *a_scale, const float *b_scale, void *c, uint64_t ldc, int32_t c_dtype,
                             uint64_t m, uint64_t n, uint64_t k, uint32_t rounding, uint32_t step, uint64_t seed,

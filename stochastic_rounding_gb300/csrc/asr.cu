@@ -855,7 +855,7 @@ asr_status asr_linear_int8(const void *x, int32_t x_dtype, uint64_t x_ld, const 
 asr_status asr_linear_int8_workspace(uint64_t m, uint64_t n, uint64_t k, uint64_t *bytes)
 {
     if (!bytes || !int8::sizes_ok(m, n, k)) return ASR_ERR_INVALID_VALUE;
-    *bytes = m && n && k ? int8::linear_layout(m, n, k).bytes : 0;
+    *bytes = m && n && k ? int8::layout(m, n, k).bytes : 0;
     return ASR_OK;
 }
 

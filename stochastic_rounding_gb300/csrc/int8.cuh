@@ -186,6 +186,84 @@ __global__ void __launch_bounds__(kThreads) quantise_rows_kernel(const __grid_co
     }
 }
 
+// What the product with few rows needs before it: the tokens widened (quantised
+// here from f32 or bf16, or given as integers), their scales, and zeros in its
+// sums.  Blocks below `rows` take a row each, a few units a thread held in
+// registers between the two passes; the others zero.
+constexpr int kFewThreads = 1024;
+constexpr int kFewUnits = 4;                    // rows of up to 4 * 8 * 1,024 values stay in registers
+
+struct FewPrepParams {
+    const void *x;
+    __half *out;
+    float *scale;                               // null: x is int8
+    uint4 *zero;
+    uint64_t rows, cols, x_ld, out_ld, zero_units;
+    uint32_t dtype, vec;
+};
+
+__global__ void __launch_bounds__(kFewThreads) few_prep_kernel(const __grid_constant__ FewPrepParams P)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x >= P.rows) {
+        for (uint64_t i = (blockIdx.x - P.rows) * kFewThreads + threadIdx.x; i < P.zero_units;
+             i += (gridDim.x - P.rows) * kFewThreads)
+            P.zero[i] = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    const uint64_t row = blockIdx.x;
+    __half *out = P.out + row * P.out_ld;
+    if (!P.scale) {
+        const int8_t *src = static_cast<const int8_t *>(P.x) + row * P.x_ld;
+        for (uint64_t col = threadIdx.x * 8ull; col < P.out_ld; col += kFewThreads * 8ull) {
+            float x[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) x[q] = col + q < P.cols ? static_cast<float>(src[col + q]) : 0.0f;
+            *reinterpret_cast<uint4 *>(out + col) = pack8(x);
+        }
+        return;
+    }
+    __shared__ uint32_t part[kFewThreads / 32];
+    float x[kFewUnits][8];
+    uint32_t top = 0;
+    auto fetch = [&](uint64_t col, float v[8]) {
+        const int live = col >= P.cols ? 0 : P.cols - col < 8 ? static_cast<int>(P.cols - col) : 8;
+        muon::load8(P.x, P.dtype, row * P.x_ld + col, live, P.vec, v);
+    };
+#pragma unroll
+    for (int u = 0; u < kFewUnits; ++u) {
+        fetch((u * kFewThreads + threadIdx.x) * 8ull, x[u]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) top = max(top, absbits(x[u][q]));
+    }
+    for (uint64_t col = (kFewUnits * kFewThreads + threadIdx.x) * 8ull; col < P.cols; col += kFewThreads * 8ull) {
+        float v[8];
+        fetch(col, v);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) top = max(top, absbits(v[q]));
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+    __syncthreads();
+    const float amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, part[threadIdx.x & 31]));
+    const Levels L = levels_of(amax);
+    if (threadIdx.x == 0) P.scale[row] = __fdiv_rn(amax, 127.0f);
+#pragma unroll
+    for (int u = 0; u < kFewUnits; ++u) {
+        const uint64_t col = (u * kFewThreads + threadIdx.x) * 8ull;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[u][q] = quantise<false>(x[u][q], L, 0u);
+        if (col < P.out_ld) *reinterpret_cast<uint4 *>(out + col) = pack8(x[u]);
+    }
+    for (uint64_t col = (kFewUnits * kFewThreads + threadIdx.x) * 8ull; col < P.out_ld; col += kFewThreads * 8ull) {
+        float v[8];
+        fetch(col, v);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = quantise<false>(v[q], L, 0u);
+        *reinterpret_cast<uint4 *>(out + col) = pack8(v);
+    }
+}
+
 // Maxima along columns, or along both, of up to three matrices in one launch:
 // blocks of kTileRows x 256, a warp every eighth row, eight columns a lane.
 // `row_max` and `col_max` hold bits of non-negative floats, zero at the start;
@@ -457,20 +535,42 @@ bool sizes_ok(uint64_t m, uint64_t n, uint64_t k)
     return m <= (1u << 24) && n <= (1u << 24) && k <= kMaxK;
 }
 
-bool few(uint64_t m) { return m <= static_cast<uint64_t>(int8few::kMaxTokens); }
+#ifndef ASR_FEW_TOKENS
+#define ASR_FEW_TOKENS 48
+#endif
+bool few(uint64_t m) { return m <= ASR_FEW_TOKENS; }
 
-// Workspace of the product: the widened operands, or nothing where A has few rows.
+// Workspace: with few rows of A the widened rows, their scales and the sums;
+// otherwise the scales and both operands, widened.
 struct Layout {
-    uint64_t a, b, bytes, ld;
+    uint64_t scale, zero, zero_bytes, counts, a, b, bytes, ld;
 };
 
 Layout layout(uint64_t m, uint64_t n, uint64_t k)
 {
-    Layout L{0, 0, 0, muon::up(k, 16)};
-    if (few(m)) return L;
-    L.b = muon::up(m * L.ld * 2, 256);
-    L.bytes = L.b + muon::up(n * L.ld * 2, 256);
+    Layout L;
+    L.ld = muon::up(k, 16);
+    L.scale = 0;
+    L.zero = muon::up(m * sizeof(float), 256);
+    L.zero_bytes = 0;
+    L.counts = L.zero;
+    if (few(m)) {
+        const uint64_t tiles = (n + int8few::kRows - 1) / int8few::kRows;
+        L.counts = L.zero + tiles * m * int8few::kRows * sizeof(int32_t);
+        L.zero_bytes = muon::up(L.counts - L.zero + tiles * int8few::groups(m) * sizeof(uint32_t), 256);
+    }
+    L.a = L.zero + L.zero_bytes;
+    L.b = L.a + muon::up(m * L.ld * 2, 256);
+    L.bytes = few(m) ? L.b : L.b + muon::up(n * L.ld * 2, 256);
     return L;
+}
+
+// Every kernel of the products ready on this device, whichever a call takes.
+asr_status setup()
+{
+    int pairs = 0, sms = 0;
+    const asr_status st = prod::setup(&pairs);
+    return st == ASR_OK ? int8few::setup(&sms) : st;
 }
 
 struct Output {
@@ -519,28 +619,49 @@ prod::Stored stored(__half *p, uint64_t rows, uint64_t cols, uint64_t ld)
     return prod::Stored{p, rows, cols, ld, muon::up(rows * ld * 2, 256) / 2};
 }
 
-asr_status few_rows(const int8_t *a, uint64_t lda, const int8_t *b, uint64_t ldb, const float *sa, const float *sb,
-                    const Output &o, uint64_t m, uint64_t n, uint64_t k, bool early, cudaStream_t stream)
+// The product with few rows: x is the tokens (quantised here), or, with `sa`,
+// 8-bit integers with those scales.
+asr_status few_rows(const void *x, int32_t x_dtype, uint64_t x_ld, const float *sa, const int8_t *b, uint64_t ldb,
+                    const float *sb, const Output &o, uint64_t m, uint64_t n, uint64_t k, char *ws, const Layout &L,
+                    cudaStream_t stream)
 {
+    FewPrepParams F;
+    std::memset(&F, 0, sizeof(F));
+    F.x = x;
+    F.out = reinterpret_cast<__half *>(ws + L.a);
+    F.scale = sa ? nullptr : reinterpret_cast<float *>(ws + L.scale);
+    F.zero = reinterpret_cast<uint4 *>(ws + L.zero);
+    F.rows = m;
+    F.cols = k;
+    F.x_ld = x_ld;
+    F.out_ld = L.ld;
+    F.zero_units = L.zero_bytes / 16;
+    F.dtype = static_cast<uint32_t>(x_dtype);
+    F.vec = !sa && muon::units_aligned(x, x_ld, 0);
+    few_prep_kernel<<<static_cast<unsigned>(m) + blocks_for(F.zero_units, 4 * kFewThreads, 64), kFewThreads, 0,
+                      stream>>>(F);
+    asr_status st = launched(ASR_KERNEL_QUANTIZE);
+    if (st != ASR_OK) return st;
     int8few::Params P;
     std::memset(&P, 0, sizeof(P));
-    P.a = a;
+    P.a = F.out;
     P.b = b;
-    P.row_scale = sa;
+    P.row_scale = sa ? sa : F.scale;
     P.col_scale = sb;
     P.c = o.c;
-    P.lda = lda;
+    P.sums = reinterpret_cast<int32_t *>(ws + L.zero);
+    P.counts = reinterpret_cast<uint32_t *>(ws + L.counts);
+    P.lda = L.ld;
     P.ldb = ldb;
     P.ldc = o.ld;
     P.m = static_cast<uint32_t>(m);
     P.n = static_cast<uint32_t>(n);
     P.k = static_cast<uint32_t>(k);
-    P.a_vec = aligned16(a) && lda % 16 == 0;
     P.b_vec = aligned16(b) && ldb % 16 == 0;
     P.c_dtype = static_cast<uint32_t>(o.dtype);
     P.rounding = o.rounding;
     P.step = o.step;
-    P.early = early;
+    P.early = 1;                                // the weight is older than the kernel above, which no other overlaps
     P.keys = make_keys(o.seed);
     return int8few::run(P, stream);
 }
@@ -555,13 +676,12 @@ asr_status gemm(const int8_t *a, uint64_t lda, const int8_t *b, uint64_t ldb, co
     if (!a || !b || !sa || !sb || !pitch_ok(lda, k) || !pitch_ok(ldb, k) || !output_ok(o, n) ||
         !muon::element_aligned(sa, ASR_F32) || !muon::element_aligned(sb, ASR_F32))
         return ASR_ERR_INVALID_VALUE;
-    if (few(m)) return few_rows(a, lda, b, ldb, sa, sb, o, m, n, k, false, stream);
     const Layout L = layout(m, n, k);
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < L.bytes) return ASR_ERR_INVALID_VALUE;
-    int pairs = 0;
-    st = prod::setup(&pairs);
+    st = setup();
     if (st != ASR_OK) return st;
     char *w = static_cast<char *>(ws);
+    if (few(m)) return few_rows(a, 0, lda, sa, b, ldb, sb, o, m, n, k, w, L, stream);
     WidenParams W;
     std::memset(&W, 0, sizeof(W));
     W.src[0] = a;
@@ -584,21 +704,6 @@ asr_status gemm(const int8_t *a, uint64_t lda, const int8_t *b, uint64_t ldb, co
 
 // ---- the linear layer's calls
 
-struct LinearLayout {
-    uint64_t scale, a, b, bytes, ld;
-};
-
-LinearLayout linear_layout(uint64_t m, uint64_t n, uint64_t k)
-{
-    LinearLayout L;
-    L.ld = muon::up(k, 16);
-    L.scale = 0;
-    L.a = muon::up(m * sizeof(float), 256);
-    L.b = L.a + muon::up(m * L.ld * (few(m) ? 1 : 2), 256);
-    L.bytes = few(m) ? L.b : L.b + muon::up(n * L.ld * 2, 256);
-    return L;
-}
-
 asr_status linear(const void *x, int32_t x_dtype, uint64_t x_ld, const int8_t *qw, uint64_t ldw, const float *sw,
                   const Output &o, uint64_t m, uint64_t n, uint64_t k, void *ws, uint64_t ws_bytes,
                   cudaStream_t stream)
@@ -611,12 +716,12 @@ asr_status linear(const void *x, int32_t x_dtype, uint64_t x_ld, const int8_t *q
     if (!x || !qw || !sw || !pitch_ok(x_ld, k) || !pitch_ok(ldw, k) || !output_ok(o, n) ||
         !muon::element_aligned(x, x_dtype) || !muon::element_aligned(sw, ASR_F32))
         return ASR_ERR_INVALID_VALUE;
-    const LinearLayout L = linear_layout(m, n, k);
+    const Layout L = layout(m, n, k);
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < L.bytes) return ASR_ERR_INVALID_VALUE;
-    int pairs = 0;
-    st = prod::setup(&pairs);
+    st = setup();
     if (st != ASR_OK) return st;
     char *w = static_cast<char *>(ws);
+    if (few(m)) return few_rows(x, x_dtype, x_ld, nullptr, qw, ldw, sw, o, m, n, k, w, L, stream);
     RowParams P;
     std::memset(&P, 0, sizeof(P));
     P.x = x;
@@ -629,13 +734,6 @@ asr_status linear(const void *x, int32_t x_dtype, uint64_t x_ld, const int8_t *q
     P.dtype = static_cast<uint32_t>(x_dtype);
     P.vec = muon::units_aligned(x, x_ld, 0);
     const unsigned row_blocks = blocks_for(m, 1, 65536);
-    if (few(m)) {
-        quantise_rows_kernel<false, false><<<row_blocks, kThreads, 0, stream>>>(P, row_blocks);
-        st = launched(ASR_KERNEL_QUANTIZE);
-        if (st != ASR_OK) return st;
-        // the weight is older than the quantiser's kernel, so it may be read while that runs
-        return few_rows(static_cast<const int8_t *>(P.q), L.ld, qw, ldw, P.scale, sw, o, m, n, k, true, stream);
-    }
     P.w.src[0] = qw;
     P.w.dst[0] = reinterpret_cast<__half *>(w + L.b);
     P.w.rows[0] = n;
@@ -713,8 +811,7 @@ asr_status grads(const GradSource &dy, const GradSource &x, const GradSource &w,
         return ASR_ERR_INVALID_VALUE;
     const GradLayout L = grad_layout(t, n, k, dx != nullptr, dw != nullptr);
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < L.bytes) return ASR_ERR_INVALID_VALUE;
-    int pairs = 0;
-    asr_status st = prod::setup(&pairs);
+    asr_status st = setup();
     if (st != ASR_OK) return st;
     char *b = static_cast<char *>(ws);
     auto words = [&](uint64_t at) { return reinterpret_cast<uint32_t *>(b + at); };
