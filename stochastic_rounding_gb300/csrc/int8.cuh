@@ -190,40 +190,48 @@ __global__ void __launch_bounds__(kThreads) quantise_rows_kernel(const __grid_co
 // here from f32 or bf16, or given as integers), their scales, and zeros in its
 // sums.  Blocks below `rows` take a row each, a few units a thread held in
 // registers between the two passes; the others zero.
-constexpr int kFewThreads = 1024;
+constexpr int kPrepThreads = 1024;
 constexpr int kFewUnits = 4;                    // rows of up to 4 * 8 * 1,024 values stay in registers
 
 struct FewPrepParams {
     const void *x;
-    __half *out;
+    void *out;                                  // f16, or int8 (DOTS)
     float *scale;                               // null: x is int8
     uint4 *zero;
     uint64_t rows, cols, x_ld, out_ld, zero_units;
     uint32_t dtype, vec;
 };
 
-__global__ void __launch_bounds__(kFewThreads) few_prep_kernel(const __grid_constant__ FewPrepParams P)
+template <bool DOTS>
+__device__ __forceinline__ void store_few(void *row, uint64_t col, const float x[8])
+{
+    if (DOTS) store_int8(static_cast<int8_t *>(row) + col, x, 8);
+    else *reinterpret_cast<uint4 *>(static_cast<__half *>(row) + col) = pack8(x);
+}
+
+template <bool DOTS>
+__global__ void __launch_bounds__(kPrepThreads) few_prep_kernel(const __grid_constant__ FewPrepParams P)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x >= P.rows) {
-        for (uint64_t i = (blockIdx.x - P.rows) * kFewThreads + threadIdx.x; i < P.zero_units;
-             i += (gridDim.x - P.rows) * kFewThreads)
+        for (uint64_t i = (blockIdx.x - P.rows) * kPrepThreads + threadIdx.x; i < P.zero_units;
+             i += (gridDim.x - P.rows) * kPrepThreads)
             P.zero[i] = make_uint4(0, 0, 0, 0);
         return;
     }
     const uint64_t row = blockIdx.x;
-    __half *out = P.out + row * P.out_ld;
+    void *out = static_cast<char *>(P.out) + row * P.out_ld * (DOTS ? 1 : 2);
     if (!P.scale) {
         const int8_t *src = static_cast<const int8_t *>(P.x) + row * P.x_ld;
-        for (uint64_t col = threadIdx.x * 8ull; col < P.out_ld; col += kFewThreads * 8ull) {
+        for (uint64_t col = threadIdx.x * 8ull; col < P.out_ld; col += kPrepThreads * 8ull) {
             float x[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) x[q] = col + q < P.cols ? static_cast<float>(src[col + q]) : 0.0f;
-            *reinterpret_cast<uint4 *>(out + col) = pack8(x);
+            store_few<DOTS>(out, col, x);
         }
         return;
     }
-    __shared__ uint32_t part[kFewThreads / 32];
+    __shared__ uint32_t part[kPrepThreads / 32];
     float x[kFewUnits][8];
     uint32_t top = 0;
     auto fetch = [&](uint64_t col, float v[8]) {
@@ -232,11 +240,11 @@ __global__ void __launch_bounds__(kFewThreads) few_prep_kernel(const __grid_cons
     };
 #pragma unroll
     for (int u = 0; u < kFewUnits; ++u) {
-        fetch((u * kFewThreads + threadIdx.x) * 8ull, x[u]);
+        fetch((u * kPrepThreads + threadIdx.x) * 8ull, x[u]);
 #pragma unroll
         for (int q = 0; q < 8; ++q) top = max(top, absbits(x[u][q]));
     }
-    for (uint64_t col = (kFewUnits * kFewThreads + threadIdx.x) * 8ull; col < P.cols; col += kFewThreads * 8ull) {
+    for (uint64_t col = (kFewUnits * kPrepThreads + threadIdx.x) * 8ull; col < P.cols; col += kPrepThreads * 8ull) {
         float v[8];
         fetch(col, v);
 #pragma unroll
@@ -250,17 +258,17 @@ __global__ void __launch_bounds__(kFewThreads) few_prep_kernel(const __grid_cons
     if (threadIdx.x == 0) P.scale[row] = __fdiv_rn(amax, 127.0f);
 #pragma unroll
     for (int u = 0; u < kFewUnits; ++u) {
-        const uint64_t col = (u * kFewThreads + threadIdx.x) * 8ull;
+        const uint64_t col = (u * kPrepThreads + threadIdx.x) * 8ull;
 #pragma unroll
         for (int q = 0; q < 8; ++q) x[u][q] = quantise<false>(x[u][q], L, 0u);
-        if (col < P.out_ld) *reinterpret_cast<uint4 *>(out + col) = pack8(x[u]);
+        if (col < P.out_ld) store_few<DOTS>(out, col, x[u]);
     }
-    for (uint64_t col = (kFewUnits * kFewThreads + threadIdx.x) * 8ull; col < P.out_ld; col += kFewThreads * 8ull) {
+    for (uint64_t col = (kFewUnits * kPrepThreads + threadIdx.x) * 8ull; col < P.out_ld; col += kPrepThreads * 8ull) {
         float v[8];
         fetch(col, v);
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[q] = quantise<false>(v[q], L, 0u);
-        *reinterpret_cast<uint4 *>(out + col) = pack8(v);
+        store_few<DOTS>(out, col, v);
     }
 }
 
@@ -536,7 +544,7 @@ bool sizes_ok(uint64_t m, uint64_t n, uint64_t k)
 }
 
 #ifndef ASR_FEW_TOKENS
-#define ASR_FEW_TOKENS 48
+#define ASR_FEW_TOKENS 128
 #endif
 bool few(uint64_t m) { return m <= ASR_FEW_TOKENS; }
 
@@ -557,7 +565,7 @@ Layout layout(uint64_t m, uint64_t n, uint64_t k)
     if (few(m)) {
         const uint64_t tiles = (n + int8few::kRows - 1) / int8few::kRows;
         L.counts = L.zero + tiles * m * int8few::kRows * sizeof(int32_t);
-        L.zero_bytes = muon::up(L.counts - L.zero + tiles * int8few::groups(m) * sizeof(uint32_t), 256);
+        L.zero_bytes = muon::up(L.counts - L.zero + tiles * int8few::passes(m) * sizeof(uint32_t), 256);
     }
     L.a = L.zero + L.zero_bytes;
     L.b = L.a + muon::up(m * L.ld * 2, 256);
@@ -628,7 +636,7 @@ asr_status few_rows(const void *x, int32_t x_dtype, uint64_t x_ld, const float *
     FewPrepParams F;
     std::memset(&F, 0, sizeof(F));
     F.x = x;
-    F.out = reinterpret_cast<__half *>(ws + L.a);
+    F.out = ws + L.a;
     F.scale = sa ? nullptr : reinterpret_cast<float *>(ws + L.scale);
     F.zero = reinterpret_cast<uint4 *>(ws + L.zero);
     F.rows = m;
@@ -638,8 +646,9 @@ asr_status few_rows(const void *x, int32_t x_dtype, uint64_t x_ld, const float *
     F.zero_units = L.zero_bytes / 16;
     F.dtype = static_cast<uint32_t>(x_dtype);
     F.vec = !sa && muon::units_aligned(x, x_ld, 0);
-    few_prep_kernel<<<static_cast<unsigned>(m) + blocks_for(F.zero_units, 4 * kFewThreads, 64), kFewThreads, 0,
-                      stream>>>(F);
+    const unsigned blocks = static_cast<unsigned>(m) + blocks_for(F.zero_units, 4 * kPrepThreads, 64);
+    if (int8few::dots(m)) few_prep_kernel<true><<<blocks, kPrepThreads, 0, stream>>>(F);
+    else few_prep_kernel<false><<<blocks, kPrepThreads, 0, stream>>>(F);
     asr_status st = launched(ASR_KERNEL_QUANTIZE);
     if (st != ASR_OK) return st;
     int8few::Params P;
@@ -661,7 +670,6 @@ asr_status few_rows(const void *x, int32_t x_dtype, uint64_t x_ld, const float *
     P.c_dtype = static_cast<uint32_t>(o.dtype);
     P.rounding = o.rounding;
     P.step = o.step;
-    P.early = 1;                                // the weight is older than the kernel above, which no other overlaps
     P.keys = make_keys(o.seed);
     return int8few::run(P, stream);
 }

@@ -2,51 +2,48 @@
 // bounds it is reading B (the weight) once.  Included into asr.cu (inside its
 // anonymous namespace), before int8.cuh.
 //
-// The work is cut into slabs, 128 rows of B by 512 of K, and every CTA (one on
-// each SM) takes the same number of consecutive slabs, across row blocks where
-// they end: all SMs read the same share of the weight, whatever its shape.
-// Sixteen warps: four blocks of 32 rows, four quarters of a slab's K.  A warp
-// streams its rows from global memory straight into registers, 16 bytes a lane
-// and row, a slab ahead, and widens them to f16 there; the tokens (f16 already)
-// come into shared memory by asynchronous copies, two slabs ahead.  The sums of
-// a row block's part are added up over the warps in shared memory, in int32,
-// and where several CTAs share the block, over them in the workspace: the CTA
-// that completes the block's count of slabs writes the outputs.  Integer sums
-// are the same in every order, and nobody waits for anybody.
+// The work is cut into pieces, 128 rows of B by a stretch of K, and every CTA
+// (one on each SM) takes the same number of consecutive ones, across row blocks
+// where they end: all SMs read the same share of the weight, whatever its shape.
+// The int32 sums of a row block that several CTAs share are added up in the
+// workspace, and the CTA that completes the block's count of pieces writes its
+// outputs.  Integer sums are the same in every order, and nobody waits for
+// anybody.  A warp streams its rows of the weight from global memory straight
+// into registers, several pieces ahead.
 //
-// The products are mma.sync m16n8k16 (f16, binary32 sums): B's rows are the 16,
-// tokens the 8.  Measured on GB300, an SM does one in two cycles; with up to 48
-// tokens (6 products for 256 bytes of B, so 23 bytes a cycle) that keeps pace
-// with the SM's share of the memory rate (23 bytes a cycle), and with operands
-// in registers the weight never passes through shared memory, where widening it
-// for tcgen05 would cost three bytes' traffic for each.  The order of K inside a
-// product is free, so a lane's 16 contiguous bytes serve as its fragments of
-// four consecutive steps.  At most 1,024 products are added in binary32, which
-// is exact.
+// Two kernels:
+//   few_dots_kernel    up to 4 tokens: dot products of four bytes (dp4a), 16
+//                      instructions for a lane's four rows of 16 bytes;
+//   few_rows_kernel    up to 128 tokens a pass: tcgen05.mma with the weight as
+//                      the 128 rows of A.  The weight's bytes are widened to f16
+//                      in registers and stored into tensor memory, from which
+//                      the product reads them: through shared memory each byte
+//                      would cost four bytes' traffic, and 23 bytes a cycle
+//                      arrive.  The tokens are the B operand, from shared memory.
+//                      mma.sync takes 2 cycles an SM for 256 bytes and 8 tokens
+//                      (measured: 1.05 ns), so beyond 16 tokens it falls behind
+//                      the memory: 40 us against 58.7 MB and 33 tokens.
+// At most 1,024 products are added in binary32, which is exact; int32 then.
 
 namespace int8few {
 
-constexpr int kThreads = 512;
-constexpr int kRows = 128;                  // rows of B a slab
-constexpr int kSlab = 512;                  // K a slab, a quarter of it a warp
-constexpr int kPitch = kSlab * 2 + 16;      // bytes between tokens in shared memory: 8 lanes' 16 bytes never collide
-constexpr int kSumPitch = kRows + 4;        // words between tokens' sums
-constexpr int kMaxTokens = 48;              // of a pass over B
-constexpr uint32_t kMaxRun = 1024 / (kSlab / 4);    // slabs added up in binary32
-constexpr int kStages = 3;                  // slabs of tokens in shared memory
+constexpr int kRows = 128;                  // rows of B a piece
+constexpr int kDotTokens = 4;               // up to this many, dot products
+constexpr int kMaxTokens = 128;             // of a pass over B
 
 struct Params {
-    const __half *a;                        // tokens, widened: m x k, rows a multiple of 32 bytes apart
+    const void *a;                          // tokens, m x k: widened, rows a multiple of 16 values apart and zero
+                                            // past k (dot products: integers, likewise)
     const int8_t *b;                        // weight, n x k
     const float *row_scale, *col_scale;
     void *c;
     int32_t *sums;                          // [row block][token][128], zero at the start
-    uint32_t *counts;                       // [token group][row block], zero at the start
+    uint32_t *counts;                       // [pass][row block], zero at the start
     uint64_t lda, ldb, ldc;
-    uint32_t m, n, k, tiles, slabs;         // row blocks, slabs of each
+    uint32_t m, n, k, tiles, pieces;        // row blocks, pieces of each
+    uint32_t each;                          // tokens a pass, a multiple of 16 (tcgen05)
     uint32_t b_vec;                         // rows of B in 16-byte aligned units
     uint32_t c_dtype, rounding, step;
-    uint32_t early;                         // B may be read before the previous kernel has finished
     RoundKeys keys;
 };
 
@@ -76,127 +73,151 @@ __device__ __noinline__ uint4 load16_slow(const int8_t *p, uint32_t count)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ void mma16816(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1)
+// The outputs of one column and COUNT tokens (`live` of them) from their integer
+// sums.  Loads first: with a load before each store a row block took one trip to
+// L2 a token.
+template <int COUNT>
+__device__ __forceinline__ void store_outputs(const Params &P, uint32_t token, uint32_t col, const int32_t sum[COUNT],
+                                              uint32_t live)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-template <int NB>
-constexpr int smem_bytes()
-{
-    return kStages * 8 * NB * kPitch + 8 * NB * kSumPitch * 4;
-}
-
-// One output from its integer sum.
-__device__ __forceinline__ void store_output(const Params &P, uint32_t token, uint32_t col, int32_t sum)
-{
-    const float y = __fmul_rn(__fmul_rn(__int2float_rn(sum), P.row_scale[token]), __ldg(P.col_scale + col));
-    const uint64_t dst = token * P.ldc + col;
-    if (P.c_dtype == ASR_F32) {
-        static_cast<float *>(P.c)[dst] = y;
-        return;
+    const float cs = __ldg(P.col_scale + col);
+    float y[COUNT];
+#pragma unroll
+    for (int q = 0; q < COUNT; ++q)
+        y[q] = static_cast<uint32_t>(q) < live ? __ldg(P.row_scale + token + q) : 0.0f;
+#pragma unroll
+    for (int q = 0; q < COUNT; ++q) y[q] = __fmul_rn(__fmul_rn(__int2float_rn(sum[q]), y[q]), cs);
+#pragma unroll
+    for (int q = 0; q < COUNT; ++q) {
+        if (static_cast<uint32_t>(q) >= live) continue;
+        const uint64_t dst = (token + q) * P.ldc + col;
+        if (P.c_dtype == ASR_F32) {
+            static_cast<float *>(P.c)[dst] = y[q];
+            continue;
+        }
+        uint32_t h;
+        if (P.rounding == ASR_ROUND_SR) {
+            const uint64_t e = static_cast<uint64_t>(token + q) * P.n + col;
+            uint32_t r[4];
+            philox_q(e >> 2, P.step, P.keys, r);
+            const uint32_t sel = static_cast<uint32_t>(e & 3u);
+            h = round_sr(y[q], sel == 0 ? r[0] : sel == 1 ? r[1] : sel == 2 ? r[2] : r[3]);
+        } else {
+            h = round_rne(y[q]);
+        }
+        static_cast<uint16_t *>(P.c)[dst] = static_cast<uint16_t>(h);
     }
-    uint32_t h;
-    if (P.rounding == ASR_ROUND_SR) {
-        const uint64_t e = static_cast<uint64_t>(token) * P.n + col;
-        uint32_t r[4];
-        philox_q(e >> 2, P.step, P.keys, r);
-        const uint32_t sel = static_cast<uint32_t>(e & 3u);
-        h = round_sr(y, sel == 0 ? r[0] : sel == 1 ? r[1] : sel == 2 ? r[2] : r[3]);
-    } else {
-        h = round_rne(y);
-    }
-    static_cast<uint16_t *>(P.c)[dst] = static_cast<uint16_t>(h);
 }
 
-// Tokens 8 * NB * blockIdx.y and on.
-template <int NB>
-__global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_constant__ Params P)
+// ------------------------------------------------------------ dot products
+//
+// Sixteen warps: four blocks of 32 rows, four quarters of a piece's 512 of K.
+// The tokens come into a ring in shared memory by bulk copies.
+
+constexpr int kThreads = 512;
+constexpr int kSlab = 512;                  // K a piece, a quarter of it a warp
+constexpr int kTokenPitch = kSlab + 16;
+constexpr int kSumPitch = kRows + 4;        // words between tokens' sums
+constexpr int kStages = 8;                  // pieces of tokens in shared memory
+constexpr int kAhead = kStages / 2;
+
+__global__ void __launch_bounds__(kThreads, 1) few_dots_kernel(const __grid_constant__ Params P, uint64_t limit_ns)
 {
-    constexpr int kTokens = 8 * NB;
-    extern __shared__ __align__(128) unsigned char smem[];
-    int32_t *sums = reinterpret_cast<int32_t *>(smem + kStages * kTokens * kPitch);   // [kTokens][kSumPitch]
+    __shared__ __align__(16) unsigned char ring[kStages * kDotTokens * kTokenPitch];
+    __shared__ int32_t sums[kDotTokens * kSumPitch];
+    __shared__ __align__(8) uint64_t bar[2 * kStages];
     __shared__ uint32_t done;
-    const uint32_t xs = smem_addr(smem);
+    const uint32_t xs = smem_addr(ring), bars = smem_addr(bar);
+    auto full = [&](uint32_t i) { return bars + 8u * i; };
+    auto empty = [&](uint32_t i) { return bars + 8u * (kStages + i); };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3, quarter = warp & 3, wr = warp >> 2;
-    const uint32_t token0 = blockIdx.y * kTokens, tokens = min(static_cast<uint32_t>(kTokens), P.m - token0);
-    const uint32_t total = P.tiles * P.slabs;
+    const uint32_t total = P.tiles * P.pieces;
     const uint32_t first = static_cast<uint32_t>(static_cast<uint64_t>(total) * blockIdx.x / gridDim.x);
     const uint32_t end = static_cast<uint32_t>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / gridDim.x);
 
-    if (!P.early) asm volatile("griddepcontrol.wait;" ::: "memory");
-
-    // the weight of slab (tile, s): rows g, g + 8, g + 16, g + 24 of the warp's 32, two 64-wide pieces
+    // the weight of piece (tile, s): rows g, g + 8, g + 16, g + 24 of the warp's 32, two 64-wide parts
     uint4 w[2][4];
+    const uint64_t ldb8 = 8 * P.ldb;
     auto weight = [&](uint32_t tile, uint32_t s, int i) {
         const uint32_t row = tile * kRows + wr * 32 + g, k = s * kSlab + quarter * (kSlab / 4) + i * 64 + t * 16;
         const int8_t *p = P.b + row * P.ldb + k;
+        if (P.b_vec && (tile + 1) * kRows <= P.n && (s + 1) * kSlab <= P.k) {     // the same for the whole CTA
 #pragma unroll
-        for (int r = 0; r < 4; ++r, p += 8 * P.ldb) {
-            w[i][r] = make_uint4(0, 0, 0, 0);
-            if (row + 8 * r < P.n && k < P.k) {
-                if (P.b_vec && k + 16 <= P.k) w[i][r] = __ldcs(reinterpret_cast<const uint4 *>(p));
-                else w[i][r] = load16_slow(p, P.k - k);
+            for (int r = 0; r < 4; ++r) w[i][r] = __ldcs(reinterpret_cast<const uint4 *>(p + r * ldb8));
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                w[i][r] = make_uint4(0, 0, 0, 0);
+                if (row + 8 * r < P.n && k < P.k) {
+                    if (P.b_vec && k + 16 <= P.k) w[i][r] = __ldcs(reinterpret_cast<const uint4 *>(p + r * ldb8));
+                    else w[i][r] = load16_slow(p + r * ldb8, P.k - k);
+                }
             }
         }
     };
-    // the tokens of a slab: copies of 16 bytes, zeros past their end (rows are padded to 16 values, the last
-    // unit's padding is zero)
+    // the tokens of a piece (warp 0, a token a lane); what a short last piece leaves in its stage meets weights
+    // that are zero there
     auto fetch = [&](uint32_t s, uint32_t stage) {
-#pragma unroll
-        for (int q = 0; q < NB; ++q) {
-            const uint32_t u = q * kThreads + threadIdx.x, token = u >> 6, k = s * kSlab + (u & 63) * 8;
-            const bool in = token < tokens && k < P.k;
-            const __half *src = P.a + (in ? static_cast<uint64_t>(token0 + token) * P.lda + k : 0);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(xs + (stage * kTokens + token) * kPitch +
-                                                                               (u & 63) * 16),
-                         "l"(src), "r"(in ? 16 : 0)
+        const uint64_t k = static_cast<uint64_t>(s) * kSlab;
+        const uint32_t bytes = P.lda - k < kSlab ? static_cast<uint32_t>(P.lda - k) : kSlab;
+        if (lane == 0) mbar_arrive_expect_tx(full(stage), bytes * P.m);
+        __syncwarp();
+        if (lane < static_cast<int>(P.m)) {
+            const int8_t *src = static_cast<const int8_t *>(P.a) + lane * P.lda + k;
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             xs + (stage * kDotTokens + lane) * kTokenPitch),
+                         "l"(src), "r"(bytes), "r"(full(stage))
                          : "memory");
         }
     };
 
-    uint32_t tile = first / P.slabs, s = first % P.slabs;
+    uint32_t tile = first / P.pieces, s = first % P.pieces;
     if (first < end) {
         weight(tile, s, 0);
         weight(tile, s, 1);
     }
-    if (P.early) asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int i = threadIdx.x; i < kDotTokens * kSumPitch; i += kThreads) sums[i] = 0;
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < kStages; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), kThreads / 32);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    // the weight is older than the previous kernel on the stream; the tokens and the sums are its output
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-    for (int i = threadIdx.x; i < kTokens * kSumPitch; i += kThreads) sums[i] = 0;
-    // slab numbers of the copies run ahead of those of the products
-    uint32_t fs = s, fetched = first;
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-        if (fetched < end) fetch(fs, static_cast<uint32_t>(i));
-        ++fetched;
-        fs = fs + 1 == P.slabs ? 0 : fs + 1;
-        asm volatile("cp.async.commit_group;" ::: "memory");
+    uint32_t fs = s, fetched = first, ahead = 0;
+    if (warp == 0) {
+        for (int i = 0; i < kAhead && fetched < end; ++i, ++fetched) {
+            fetch(fs, ahead++);
+            fs = fs + 1 == P.pieces ? 0 : fs + 1;
+        }
     }
 
-    float acc[2][NB][4];
+    int32_t dot[4][kDotTokens];                 // rows g + 8 r, this lane's part of K
 #pragma unroll
-    for (int mb = 0; mb < 2; ++mb)
+    for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) acc[mb][nb][q] = 0.0f;
+        for (int q = 0; q < kDotTokens; ++q) dot[r][q] = 0;
 
-    uint32_t run = 0, stage = 0, ahead = kStages - 1;
+    uint32_t run = 0, stage = 0, phase = 0;
     for (uint32_t at = first; at < end; ++at) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-        __syncthreads();                        // this slab's tokens are here, and the stage two ahead is free
-        if (fetched < end) fetch(fs, ahead);
-        ++fetched;
-        fs = fs + 1 == P.slabs ? 0 : fs + 1;
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        const uint32_t ns = s + 1 == P.slabs ? 0 : s + 1, nt = s + 1 == P.slabs ? tile + 1 : tile;
-        const unsigned char *x = smem + (stage * kTokens + g) * kPitch + quarter * (kSlab / 2) + t * 32;
+        if (warp == 0 && fetched < end) {
+            // the stage's last use was piece fetched - kStages of this CTA's
+            const uint32_t use = (fetched - first) / kStages;
+            if (use > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(empty(ahead), (use - 1) & 1u, limit_ns))) break;
+            fetch(fs, ahead);
+            ++fetched;
+            fs = fs + 1 == P.pieces ? 0 : fs + 1;
+            ahead = ahead + 1 == kStages ? 0 : ahead + 1;
+        }
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(full(stage), phase, limit_ns))) break;
+        const uint32_t ns = s + 1 == P.pieces ? 0 : s + 1, nt = s + 1 == P.pieces ? tile + 1 : tile;
+        const unsigned char *x = ring + stage * kDotTokens * kTokenPitch + quarter * (kSlab / 4) + t * 16;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             uint32_t v[4][4];
@@ -204,83 +225,401 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
             for (int r = 0; r < 4; ++r) v[r][0] = w[i][r].x, v[r][1] = w[i][r].y, v[r][2] = w[i][r].z, v[r][3] = w[i][r].w;
             if (at + 1 < end) weight(nt, ns, i);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {        // two steps of 16
-                uint32_t a[2][2][4];             // [step][row block][fragment]
+            for (int q = 0; q < kDotTokens; ++q) {
+                if (q > 0 && q >= static_cast<int>(P.m)) break;
+                const int4 b = *reinterpret_cast<const int4 *>(x + q * kTokenPitch + i * 64);
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) widen4(v[r][2 * h + q], a[q][r >> 1][r & 1], a[q][r >> 1][(r & 1) + 2]);
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    const uint4 b = *reinterpret_cast<const uint4 *>(x + nb * 8 * kPitch + i * 128 + h * 16);
-                    mma16816(acc[0][nb], a[0][0], b.x, b.y);
-                    mma16816(acc[1][nb], a[0][1], b.x, b.y);
-                    mma16816(acc[0][nb], a[1][0], b.z, b.w);
-                    mma16816(acc[1][nb], a[1][1], b.z, b.w);
+                for (int r = 0; r < 4; ++r) {
+                    dot[r][q] = __dp4a(static_cast<int>(v[r][0]), b.x, dot[r][q]);
+                    dot[r][q] = __dp4a(static_cast<int>(v[r][1]), b.y, dot[r][q]);
+                    dot[r][q] = __dp4a(static_cast<int>(v[r][2]), b.z, dot[r][q]);
+                    dot[r][q] = __dp4a(static_cast<int>(v[r][3]), b.w, dot[r][q]);
                 }
             }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(stage));
         ++run;
-        if (at + 1 == end || s + 1 == P.slabs || run == kMaxRun) {
+        if (at + 1 == end || s + 1 == P.pieces) {
             // add the warps' sums up
 #pragma unroll
-            for (int mb = 0; mb < 2; ++mb)
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int token = nb * 8 + 2 * t + (q & 1), row = wr * 32 + mb * 16 + g + (q >> 1) * 8;
-                        atomicAdd(sums + token * kSumPitch + row, __float2int_rn(acc[mb][nb][q]));
-                        acc[mb][nb][q] = 0.0f;
-                    }
-            __syncthreads();
-            const bool whole = run == P.slabs;      // the block's only part
-            const uint32_t row = threadIdx.x % kRows, col = tile * kRows + row;
-            for (uint32_t token = threadIdx.x / kRows; token < tokens; token += kThreads / kRows) {
-                int32_t *p = sums + token * kSumPitch + row;
-                const int32_t sum = *p;
-                *p = 0;
-                if (whole) {
-                    if (col < P.n) store_output(P, token0 + token, col, sum);
-                } else {
-                    atomicAdd(P.sums + (static_cast<uint64_t>(tile) * P.m + token0 + token) * kRows + row, sum);
+                for (int q = 0; q < kDotTokens; ++q) {
+                    int32_t v = dot[r][q];
+                    v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+                    v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+                    if (t == q) atomicAdd(sums + q * kSumPitch + wr * 32 + r * 8 + g, v);
+                    dot[r][q] = 0;
                 }
+            __syncthreads();
+            const bool whole = run == P.pieces;     // the block's only part
+            const uint32_t row = threadIdx.x % kRows, col = tile * kRows + row, token = threadIdx.x / kRows;
+            int32_t *mine = P.sums + (static_cast<uint64_t>(tile) * P.m + token) * kRows + row;
+            if (token < P.m) {
+                const int32_t sum = sums[token * kSumPitch + row];
+                sums[token * kSumPitch + row] = 0;
+                if (!whole) atomicAdd(mine, sum);
+                else if (col < P.n) store_outputs<1>(P, token, col, &sum, 1);
             }
             if (!whole) {
                 __threadfence();
                 __syncthreads();
-                if (threadIdx.x == 0) done = atomicAdd(P.counts + blockIdx.y * P.tiles + tile, run) + run;
+                if (threadIdx.x == 0) done = atomicAdd(P.counts + tile, run) + run;
                 __syncthreads();
-                if (done == P.slabs) {
+                if (done == P.pieces) {
                     __threadfence();
-                    for (uint32_t token = threadIdx.x / kRows; token < tokens; token += kThreads / kRows)
-                        if (col < P.n)
-                            store_output(P, token0 + token, col,
-                                         __ldcg(P.sums + (static_cast<uint64_t>(tile) * P.m + token0 + token) * kRows + row));
+                    if (token < P.m && col < P.n) {
+                        const int32_t sum = __ldcg(mine);
+                        store_outputs<1>(P, token, col, &sum, 1);
+                    }
                 }
             }
             run = 0;
-            // the sums are zero again before any warp adds to them: the next slab begins with a barrier, and
-            // they are added to at its end
+            __syncthreads();                        // the sums are zero again before any warp adds to them
         }
         s = ns;
         tile = nt;
-        stage = stage + 1 == kStages ? 0 : stage + 1;
-        ahead = ahead + 1 == kStages ? 0 : ahead + 1;
+        if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+        }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    // after a wait that gave up: the copies issued here have landed before the CTA leaves
+    if (warp == 0)
+        for (uint32_t i = 0; i < kStages && i < fetched - first; ++i)
+            mbar_wait(full(i), ((fetched - first - 1 - i) / kStages) & 1u, limit_ns);
+}
+
+// ------------------------------------------------------------------ tcgen05
+//
+// A piece is 128 rows by 128 of K.  Warp 0 brings the tokens (two boxes of 64
+// of K, 128-byte swizzle), warp 14 the weight's bytes (one box of 128 x 128,
+// likewise), warp 1 issues the products, warps 2 to 5 read the sums (after 1,024
+// of K or at the end of a row block) and finish them, warps 6 to 13 widen the
+// weight: four of them, one for each quarter of the tensor memory's lanes, take
+// every other piece.  A lane is a row: 128 bytes of it a piece, which become 64
+// columns.  (Loading a lane's row straight into its registers, 32 rows a load
+// instruction, left the memory at 4.2 TB/s, and at less with more loads in
+// flight: a line's four sectors came in four requests.)
+constexpr int kPiece = 128;
+constexpr int kSets = 2;                        // of four widening warps
+constexpr int kWidener = 6;                     // first widening warp
+constexpr int kFewThreads = 32 * (kWidener + 4 * kSets + 1);
+constexpr uint32_t kRing = 4;                   // pieces in tensor memory
+constexpr uint32_t kRun = 1024 / kPiece;        // pieces added up in binary32
+constexpr uint32_t kAccAt = kRing * kPiece / 2; // columns: the weight, then two accumulators
+constexpr uint32_t kFewSmem = 226 * 1024;      // of the 227 KB, some static
+constexpr uint32_t kMaxRing = 8;                // stages of a ring in shared memory
+constexpr uint32_t kPieceBytes = kRows * kPiece;
+constexpr int kBars = 4 * kMaxRing + 2 * kRing + 4 + 3;
+
+// Shared memory for a pass of `each` tokens: rings of the tokens and of the
+// weight's bytes, and the sums of a part longer than 1,024 of K.
+struct FewShape {
+    uint32_t x_ring, w_ring, x_bytes, sums_at, w_at, bars_at, bytes;
+};
+
+__host__ __device__ constexpr FewShape few_shape(uint32_t each)
+{
+    FewShape f{};
+    f.x_bytes = each * kPiece * 2;
+    f.x_ring = each <= 64 ? 4 : 2;
+    f.w_at = f.x_ring * f.x_bytes;              // 1,024-byte multiples: each is a multiple of 16
+    const uint32_t left = kFewSmem - 16 - 1024 - f.w_at - each * kRows * 4 - kBars * 8;
+    f.w_ring = left / kPieceBytes < kMaxRing ? left / kPieceBytes : kMaxRing;
+    f.sums_at = f.w_at + f.w_ring * kPieceBytes;
+    f.bars_at = f.sums_at + each * kRows * 4;
+    f.bytes = 1024 + f.bars_at + kBars * 8 + 16;
+    return f;
+}
+
+__device__ __forceinline__ void mma_from_tmem(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t v[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// Where piece `at` of a CTA's stretch ends a run (its sums are read) and a part
+// (of a row block); the same for every role.
+struct Place {
+    uint32_t tile, s, run, part;
+    __device__ Place(uint32_t at, uint32_t pieces) : tile(at / pieces), s(at % pieces), run(0), part(0) {}
+    __device__ bool ends_part(uint32_t at, uint32_t end, uint32_t pieces) const { return at + 1 == end || s + 1 == pieces; }
+    __device__ bool ends_run(uint32_t at, uint32_t end, uint32_t pieces) const
+    {
+        return run + 1 == kRun || ends_part(at, end, pieces);
+    }
+    __device__ void next(uint32_t at, uint32_t end, uint32_t pieces)
+    {
+        const bool p = ends_part(at, end, pieces), r = ends_run(at, end, pieces);
+        run = r ? 0 : run + 1;
+        part = p ? 0 : part + 1;
+        if (++s == pieces) {
+            s = 0;
+            ++tile;
+        }
+    }
+};
+
+__global__ void __launch_bounds__(kFewThreads, 1)
+few_rows_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                const __grid_constant__ Params P, uint64_t limit_ns)
+{
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    __shared__ uint32_t done;
+    const FewShape F = few_shape(P.each);
+    const uint32_t raw = smem_addr(smem_raw), xs = (raw + 1023u) & ~1023u, ws = xs + F.w_at;
+    const uint32_t each = P.each, box = each * 128;
+    int32_t *sums = reinterpret_cast<int32_t *>(smem_raw + (xs - raw) + F.sums_at);     // [token][row]
+    const uint32_t bars = xs + F.bars_at;
+    auto full_x = [&](uint32_t i) { return bars + 8u * i; };
+    auto empty_x = [&](uint32_t i) { return bars + 8u * (kMaxRing + i); };
+    auto full_w = [&](uint32_t i) { return bars + 8u * (2 * kMaxRing + i); };
+    auto empty_w = [&](uint32_t i) { return bars + 8u * (3 * kMaxRing + i); };
+    auto full_a = [&](uint32_t i) { return bars + 8u * (4 * kMaxRing + i); };
+    auto empty_a = [&](uint32_t i) { return bars + 8u * (4 * kMaxRing + kRing + i); };
+    auto acc_full = [&](uint32_t i) { return bars + 8u * (4 * kMaxRing + 2 * kRing + i); };
+    auto acc_empty = [&](uint32_t i) { return bars + 8u * (4 * kMaxRing + 2 * kRing + 2 + i); };
+    const uint32_t added = bars + 8u * (kBars - 3), counted = added + 8u, drained = added + 16u, tmem_slot = drained + 8u;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t token0 = blockIdx.y * each, tokens = min(each, P.m - token0);
+    const uint32_t total = P.tiles * P.pieces;
+    const uint32_t first = static_cast<uint32_t>(static_cast<uint64_t>(total) * blockIdx.x / gridDim.x);
+    const uint32_t end = static_cast<uint32_t>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / gridDim.x);
+
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < kMaxRing; ++i) {
+            mbar_init(full_x(i), 1);
+            mbar_init(empty_x(i), 1);
+            mbar_init(full_w(i), 1);
+            mbar_init(empty_w(i), 4);
+        }
+        for (uint32_t i = 0; i < kRing; ++i) {
+            mbar_init(full_a(i), 4);
+            mbar_init(empty_a(i), 1);
+        }
+        for (uint32_t i = 0; i < 2; ++i) {
+            mbar_init(acc_full(i), 1);
+            mbar_init(acc_empty(i), 4);
+        }
+        mbar_init(added, 4);
+        mbar_init(counted, 1);
+        mbar_init(drained, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tmem_slot), "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    }
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = *reinterpret_cast<const uint32_t *>(smem_raw + (tmem_slot - raw));
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------------- tokens
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        uint32_t s = first % P.pieces, i = 0;
+        for (uint32_t at = first; at < end; ++at, ++i) {
+            const uint32_t st = i % F.x_ring, use = i / F.x_ring;
+            if (use > 0 && !mbar_wait(empty_x(st), (use - 1) & 1u, limit_ns)) break;
+            mbar_arrive_expect_tx(full_x(st), F.x_bytes);
+            const uint32_t dst = xs + st * F.x_bytes;
+            gemm::tma_load_2d(dst, &map_x, static_cast<int32_t>(s * kPiece), static_cast<int32_t>(token0), full_x(st));
+            gemm::tma_load_2d(dst + box, &map_x, static_cast<int32_t>(s * kPiece + 64), static_cast<int32_t>(token0),
+                              full_x(st));
+            s = s + 1 == P.pieces ? 0 : s + 1;
+        }
+        for (uint32_t q = 0; q < F.x_ring && q < i; ++q) mbar_wait(full_x(q), ((i - 1 - q) / F.x_ring) & 1u, limit_ns);
+    } else if (warp == kWidener + 4 * kSets) {
+        // ------------------------------------------------------- weight
+        // older than the previous kernel on the stream, so nothing to wait for
+        if (lane == 0 && P.b_vec) {
+            uint32_t tile = first / P.pieces, s = first % P.pieces, i = 0;
+            for (uint32_t at = first; at < end; ++at, ++i) {
+                const uint32_t st = i % F.w_ring, use = i / F.w_ring;
+                if (use > 0 && !mbar_wait(empty_w(st), (use - 1) & 1u, limit_ns)) break;
+                mbar_arrive_expect_tx(full_w(st), kPieceBytes);
+                gemm::tma_load_2d(ws + st * kPieceBytes, &map_w, static_cast<int32_t>(s * kPiece),
+                                  static_cast<int32_t>(tile * kRows), full_w(st));
+                if (++s == P.pieces) {
+                    s = 0;
+                    ++tile;
+                }
+            }
+            for (uint32_t q = 0; q < F.w_ring && q < i; ++q)
+                mbar_wait(full_w(q), ((i - 1 - q) / F.w_ring) & 1u, limit_ns);
+        }
+    } else if (warp == 1 && lane == 0) {
+        // ------------------------------------------------------- products
+        const uint32_t idesc = (1u << 4) | ((each >> 3) << 17) | ((128u >> 4) << 24);
+        Place pl(first, P.pieces);
+        uint32_t i = 0, r = 0;
+        bool ok = true;
+        for (uint32_t at = first; ok && at < end; ++at, ++i) {
+            const uint32_t st = i % kRing, sx = i % F.x_ring, b = r & 1u;
+            if (pl.run == 0 && r >= 2) ok = mbar_wait(acc_empty(b), ((r >> 1) - 1) & 1u, limit_ns);
+            ok = ok && mbar_wait(full_x(sx), (i / F.x_ring) & 1u, limit_ns) &&
+                 mbar_wait(full_a(st), (i / kRing) & 1u, limit_ns);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t d = tmem + kAccAt + b * kMaxTokens, a = tmem + st * (kPiece / 2);
+            const uint64_t x = gemm::smem_desc(xs + sx * F.x_bytes), x2 = gemm::smem_desc(xs + sx * F.x_bytes + box);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                mma_from_tmem(d, a + q * 8, (q < 4 ? x : x2) + (q & 3) * 2, idesc, pl.run != 0 || q != 0);
+            gemm::mma_commit(empty_a(st));
+            gemm::mma_commit(empty_x(sx));
+            if (pl.ends_run(at, end, P.pieces)) {
+                gemm::mma_commit(acc_full(b));
+                ++r;
+            }
+            pl.next(at, end, P.pieces);
+        }
+        gemm::mma_commit(drained);
+        mbar_wait(drained, 0, limit_ns);
+    } else if (warp >= 2 && warp < 6) {
+        // ------------------------------------------------------- sums
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        const uint32_t quarter = warp & 3u, row = quarter * 32 + lane;
+        Place pl(first, P.pieces);
+        uint32_t r = 0, shares = 0;
+        bool held = false;                              // sums of this part in shared memory already
+        for (uint32_t at = first; at < end; ++at) {
+            if (pl.ends_run(at, end, P.pieces)) {
+                const uint32_t b = r & 1u;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_full(b), (r >> 1) & 1u, limit_ns))) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const bool last = pl.ends_part(at, end, P.pieces), whole = last && pl.part + 1 == P.pieces;
+                const uint32_t tq = tmem + ((quarter * 32) << 16) + kAccAt + b * kMaxTokens, col = pl.tile * kRows + row;
+                int32_t *shared = P.sums + (static_cast<uint64_t>(pl.tile) * P.m + token0) * kRows + row;
+#pragma unroll 1
+                for (uint32_t c = 0; c < tokens; c += 16) {
+                    uint32_t v[16];
+                    int32_t sum[16];
+                    gemm::tmem_ld16(tq + c, v);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+                        sum[q] = __float2int_rn(__uint_as_float(v[q]));
+                        if (held) sum[q] += sums[(c + q) * kRows + row];
+                    }
+                    if (!last) {
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) sums[(c + q) * kRows + row] = sum[q];
+                    } else if (!whole) {
+#pragma unroll
+                        for (int q = 0; q < 16; ++q)
+                            if (c + q < tokens) atomicAdd(shared + (c + q) * kRows, sum[q]);
+                    } else if (col < P.n) {
+                        store_outputs<16>(P, token0 + c, col, sum, tokens - c);
+                    }
+                }
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acc_empty(b));
+                held = !last;
+                if (last && !whole) {
+                    // the last CTA to add its part finishes the row block
+                    __threadfence();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(added);
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(added, shares & 1u, limit_ns))) break;
+                    if (threadIdx.x == 64) {
+                        const uint32_t run = pl.part + 1;
+                        done = atomicAdd(P.counts + blockIdx.y * P.tiles + pl.tile, run) + run;
+                        mbar_arrive(counted);
+                    }
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(counted, shares & 1u, limit_ns))) break;
+                    ++shares;
+                    if (done == P.pieces) {
+                        __threadfence();
+#pragma unroll 1
+                        for (uint32_t c = 0; c < tokens && col < P.n; c += 16) {
+                            int32_t sum[16];
+#pragma unroll
+                            for (int q = 0; q < 16; ++q) sum[q] = c + q < tokens ? __ldcg(shared + (c + q) * kRows) : 0;
+                            store_outputs<16>(P, token0 + c, col, sum, tokens - c);
+                        }
+                    }
+                }
+                ++r;
+            }
+            pl.next(at, end, P.pieces);
+        }
+    } else if (warp >= kWidener && warp < kWidener + 4 * kSets) {
+        // ------------------------------------------------------- widening
+        const uint32_t quarter = warp & 3u, row = quarter * 32 + lane;
+        const unsigned char *mine = smem_raw + (ws - raw) + row * kPiece;
+        uint32_t i = (warp - kWidener) >> 2;
+        for (uint32_t at = first + i; at < end; at += kSets, i += kSets) {
+            uint4 w[8];
+            if (P.b_vec) {
+                const uint32_t sw = i % F.w_ring;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(full_w(sw), (i / F.w_ring) & 1u, limit_ns))) break;
+                // 16-byte unit q of a row lies at q ^ (row & 7) of its 128 bytes
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    w[q] = *reinterpret_cast<const uint4 *>(mine + sw * kPieceBytes + ((q ^ (row & 7)) << 4));
+            } else {
+                const uint32_t n = at / P.pieces * kRows + row, k = at % P.pieces * kPiece;
+                for (int q = 0; q < 8; ++q)
+                    w[q] = n < P.n && k + 16 * q < P.k ? load16_slow(P.b + n * P.ldb + k + 16 * q, P.k - k - 16 * q)
+                                                       : make_uint4(0, 0, 0, 0);
+            }
+            const uint32_t st = i % kRing, use = i / kRing;
+            if (use > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(empty_a(st), (use - 1) & 1u, limit_ns))) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t dst = tmem + ((quarter * 32) << 16) + st * (kPiece / 2);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                uint32_t f[16];
+                const uint32_t u[8] = {w[2 * h].x, w[2 * h].y, w[2 * h].z, w[2 * h].w,
+                                       w[2 * h + 1].x, w[2 * h + 1].y, w[2 * h + 1].z, w[2 * h + 1].w};
+#pragma unroll
+                for (int q = 0; q < 8; ++q) widen4(u[q], f[2 * q], f[2 * q + 1]);
+                tmem_st16(dst + 16 * h, f);
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(full_a(st));
+                if (P.b_vec) mbar_arrive(empty_w(i % F.w_ring));
+            }
+        }
+    }
+    // ------------------------------------------------------------ cleanup
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    }
 }
 
 // ------------------------------------------------------------------ host
 
 std::mutex g_few_mu;
 int g_few_sms[kMaxDevices];
-
-template <int NB>
-cudaError_t opt_in()
-{
-    return cudaFuncSetAttribute(few_rows_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NB>());
-}
 
 asr_status setup(int *sms)
 {
@@ -292,12 +631,10 @@ asr_status setup(int *sms)
     if (!g_few_sms[dev]) {
         int n = 0;
         e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        if (e == cudaSuccess) e = opt_in<1>();
-        if (e == cudaSuccess) e = opt_in<2>();
-        if (e == cudaSuccess) e = opt_in<3>();
-        if (e == cudaSuccess) e = opt_in<4>();
-        if (e == cudaSuccess) e = opt_in<5>();
-        if (e == cudaSuccess) e = opt_in<6>();
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(few_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+        cudaFuncAttributes fa;                  // loads the kernel, so that its first launch may be captured
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, few_dots_kernel);
         if (e != cudaSuccess) return cuda_fail(e);
         g_few_sms[dev] = n;
     }
@@ -305,45 +642,64 @@ asr_status setup(int *sms)
     return ASR_OK;
 }
 
-uint32_t groups(uint64_t m) { return static_cast<uint32_t>((m + kMaxTokens - 1) / kMaxTokens); }
-
-template <int NB>
-asr_status launch_few(Params &P, int sms, cudaStream_t stream)
+// A row-major matrix of bytes in boxes of 128 x 128.
+asr_status make_map_int8(CUtensorMap *map, const int8_t *ptr, uint64_t rows, uint64_t cols, uint64_t ld)
 {
-    const uint32_t count = (P.m + 8 * NB - 1) / (8 * NB), total = P.tiles * P.slabs;
+    PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    const asr_status st = gemm::encoder(&enc);
+    if (st != ASR_OK) return st;
+    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld};
+    const cuuint32_t box[2] = {kPiece, kRows}, estr[2] = {1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(ptr), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? ASR_OK : ASR_ERR_INVALID_VALUE;
+}
+
+bool dots(uint64_t m) { return m <= kDotTokens; }       // the tokens are given as integers then
+
+uint32_t passes(uint64_t m) { return static_cast<uint32_t>((m + kMaxTokens - 1) / kMaxTokens); }
+
+// P.m tokens in passes of equal size, at most kMaxTokens each.
+asr_status run(Params &P, cudaStream_t stream)
+{
+    int sms = 0;
+    asr_status st = setup(&sms);
+    if (st != ASR_OK) return st;
+    const uint32_t wide = dots(P.m) ? kSlab : kPiece;
+    P.tiles = (P.n + kRows - 1) / kRows;
+    P.pieces = (P.k + wide - 1) / wide;
+    const uint64_t total = static_cast<uint64_t>(P.tiles) * P.pieces;
+    if (total >= (1ull << 31)) return ASR_ERR_INVALID_VALUE;
+    const uint32_t grid = static_cast<uint32_t>(total < static_cast<uint64_t>(sms) ? total : sms);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(total < static_cast<uint32_t>(sms) ? total : static_cast<uint32_t>(sms), count, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem_bytes<NB>();
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, few_rows_kernel<NB>, P);
+    cfg.gridDim = dim3(grid, 1, 1);
+    const uint64_t limit = kWaitLimitNs;
+    cudaError_t e;
+    if (dots(P.m)) {
+        cfg.blockDim = dim3(kThreads, 1, 1);
+        e = cudaLaunchKernelEx(&cfg, few_dots_kernel, P, limit);
+    } else {
+        const uint32_t p = passes(P.m);
+        P.each = ((P.m + p - 1) / p + 15) / 16 * 16;
+        CUtensorMap map, map_w;
+        st = prod::make_map_2d(&map, P.a, P.m, P.k, P.lda, P.each);
+        if (st == ASR_OK && P.b_vec) st = make_map_int8(&map_w, P.b, P.n, P.k, P.ldb);
+        if (st != ASR_OK) return st;
+        if (!P.b_vec) map_w = map;                  // not read
+        cfg.gridDim.y = (P.m + P.each - 1) / P.each;
+        cfg.blockDim = dim3(kFewThreads, 1, 1);
+        cfg.dynamicSmemBytes = few_shape(P.each).bytes;
+        e = cudaLaunchKernelEx(&cfg, few_rows_kernel, map, map_w, P, limit);
+    }
     if (e != cudaSuccess) return cuda_fail(e);
     return launched(ASR_KERNEL_INT8_FEW_ROWS);
-}
-
-// P.m tokens in groups of equal size, at most kMaxTokens each.
-asr_status run(Params &P, cudaStream_t stream)
-{
-    int sms = 0;
-    const asr_status st = setup(&sms);
-    if (st != ASR_OK) return st;
-    P.tiles = (P.n + kRows - 1) / kRows;
-    P.slabs = (P.k + kSlab - 1) / kSlab;
-    if (static_cast<uint64_t>(P.tiles) * P.slabs >= (1ull << 31)) return ASR_ERR_INVALID_VALUE;
-    const uint32_t g = groups(P.m), each = (P.m + g - 1) / g, nb = (each + 7) / 8;
-    switch (nb) {
-    case 1: return launch_few<1>(P, sms, stream);
-    case 2: return launch_few<2>(P, sms, stream);
-    case 3: return launch_few<3>(P, sms, stream);
-    case 4: return launch_few<4>(P, sms, stream);
-    case 5: return launch_few<5>(P, sms, stream);
-    default: return launch_few<6>(P, sms, stream);
-    }
 }
 
 }  // namespace int8few

@@ -698,6 +698,20 @@ asr_status make_map(CUtensorMap *map, const void *ptr, uint64_t rows, uint64_t c
     return r == CUDA_SUCCESS ? ASR_OK : ASR_ERR_INVALID_VALUE;
 }
 
+// One row-major f16 matrix, in boxes of box_rows x 64.
+asr_status make_map_2d(CUtensorMap *map, const void *ptr, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    asr_status st = gemm::encoder(&enc);
+    if (st != ASR_OK) return st;
+    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld * 2};
+    const cuuint32_t box[2] = {64, box_rows}, estr[2] = {1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? ASR_OK : ASR_ERR_INVALID_VALUE;
+}
+
 // One stored stack of matrices: f16, rows a multiple of 32 bytes apart.
 struct Stored {
     __half *ptr;
