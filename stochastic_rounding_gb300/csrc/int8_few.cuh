@@ -303,7 +303,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_dots_kernel(const __grid_cons
 // instruction, left the memory at 4.2 TB/s, and at less with more loads in
 // flight: a line's four sectors came in four requests.)
 constexpr int kPiece = 128;
-constexpr int kSets = 2;                        // of four widening warps
+#ifndef ASR_FEW_SETS
+#define ASR_FEW_SETS 2
+#endif
+constexpr int kSets = ASR_FEW_SETS;                        // of four widening warps
 constexpr int kWidener = 6;                     // first widening warp
 constexpr int kFewThreads = 32 * (kWidener + 4 * kSets + 1);
 constexpr uint32_t kRing = 4;                   // pieces in tensor memory
@@ -397,7 +400,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
     auto acc_empty = [&](uint32_t i) { return bars + 8u * (4 * kMaxRing + 2 * kRing + 2 + i); };
     const uint32_t added = bars + 8u * (kBars - 3), counted = added + 8u, drained = added + 16u, tmem_slot = drained + 8u;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = prod::warp_index(), lane = threadIdx.x & 31;
     const uint32_t token0 = blockIdx.y * each, tokens = min(each, P.m - token0);
     const uint32_t total = P.tiles * P.pieces;
     const uint32_t first = static_cast<uint32_t>(static_cast<uint64_t>(total) * blockIdx.x / gridDim.x);
@@ -431,35 +434,41 @@ few_rows_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
     }
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    const uint32_t tmem = *reinterpret_cast<const uint32_t *>(smem_raw + (tmem_slot - raw));
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *reinterpret_cast<const uint32_t *>(smem_raw + (tmem_slot - raw)), 0);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // ------------------------------------------------------- tokens
         asm volatile("griddepcontrol.wait;" ::: "memory");
         uint32_t s = first % P.pieces, i = 0;
         for (uint32_t at = first; at < end; ++at, ++i) {
             const uint32_t st = i % F.x_ring, use = i / F.x_ring;
-            if (use > 0 && !mbar_wait(empty_x(st), (use - 1) & 1u, limit_ns)) break;
-            mbar_arrive_expect_tx(full_x(st), F.x_bytes);
+            if (use > 0 && !prod::warp_wait(empty_x(st), (use - 1) & 1u, limit_ns)) break;
             const uint32_t dst = xs + st * F.x_bytes;
-            gemm::tma_load_2d(dst, &map_x, static_cast<int32_t>(s * kPiece), static_cast<int32_t>(token0), full_x(st));
-            gemm::tma_load_2d(dst + box, &map_x, static_cast<int32_t>(s * kPiece + 64), static_cast<int32_t>(token0),
-                              full_x(st));
+            if (prod::elect_one()) {
+                mbar_arrive_expect_tx(full_x(st), F.x_bytes);
+                gemm::tma_load_2d(dst, &map_x, static_cast<int32_t>(s * kPiece), static_cast<int32_t>(token0), full_x(st));
+                gemm::tma_load_2d(dst + box, &map_x, static_cast<int32_t>(s * kPiece + 64), static_cast<int32_t>(token0),
+                                  full_x(st));
+            }
+            __syncwarp();
             s = s + 1 == P.pieces ? 0 : s + 1;
         }
         for (uint32_t q = 0; q < F.x_ring && q < i; ++q) mbar_wait(full_x(q), ((i - 1 - q) / F.x_ring) & 1u, limit_ns);
     } else if (warp == kWidener + 4 * kSets) {
         // ------------------------------------------------------- weight
         // older than the previous kernel on the stream, so nothing to wait for
-        if (lane == 0 && P.b_vec) {
+        if (P.b_vec) {
             uint32_t tile = first / P.pieces, s = first % P.pieces, i = 0;
             for (uint32_t at = first; at < end; ++at, ++i) {
                 const uint32_t st = i % F.w_ring, use = i / F.w_ring;
-                if (use > 0 && !mbar_wait(empty_w(st), (use - 1) & 1u, limit_ns)) break;
-                mbar_arrive_expect_tx(full_w(st), kPieceBytes);
-                gemm::tma_load_2d(ws + st * kPieceBytes, &map_w, static_cast<int32_t>(s * kPiece),
-                                  static_cast<int32_t>(tile * kRows), full_w(st));
+                if (use > 0 && !prod::warp_wait(empty_w(st), (use - 1) & 1u, limit_ns)) break;
+                if (prod::elect_one()) {
+                    mbar_arrive_expect_tx(full_w(st), kPieceBytes);
+                    gemm::tma_load_2d(ws + st * kPieceBytes, &map_w, static_cast<int32_t>(s * kPiece),
+                                      static_cast<int32_t>(tile * kRows), full_w(st));
+                }
+                __syncwarp();
                 if (++s == P.pieces) {
                     s = 0;
                     ++tile;
@@ -468,7 +477,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             for (uint32_t q = 0; q < F.w_ring && q < i; ++q)
                 mbar_wait(full_w(q), ((i - 1 - q) / F.w_ring) & 1u, limit_ns);
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         // ------------------------------------------------------- products
         const uint32_t idesc = (1u << 4) | ((each >> 3) << 17) | ((128u >> 4) << 24);
         Place pl(first, P.pieces);
@@ -476,26 +485,29 @@ few_rows_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         bool ok = true;
         for (uint32_t at = first; ok && at < end; ++at, ++i) {
             const uint32_t st = i % kRing, sx = i % F.x_ring, b = r & 1u;
-            if (pl.run == 0 && r >= 2) ok = mbar_wait(acc_empty(b), ((r >> 1) - 1) & 1u, limit_ns);
-            ok = ok && mbar_wait(full_x(sx), (i / F.x_ring) & 1u, limit_ns) &&
-                 mbar_wait(full_a(st), (i / kRing) & 1u, limit_ns);
+            if (pl.run == 0 && r >= 2) ok = prod::warp_wait(acc_empty(b), ((r >> 1) - 1) & 1u, limit_ns);
+            ok = ok && prod::warp_wait(full_x(sx), (i / F.x_ring) & 1u, limit_ns) &&
+                 prod::warp_wait(full_a(st), (i / kRing) & 1u, limit_ns);
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t d = tmem + kAccAt + b * kMaxTokens, a = tmem + st * (kPiece / 2);
             const uint64_t x = gemm::smem_desc(xs + sx * F.x_bytes), x2 = gemm::smem_desc(xs + sx * F.x_bytes + box);
+            const bool ends = pl.ends_run(at, end, P.pieces);
+            if (prod::elect_one()) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                mma_from_tmem(d, a + q * 8, (q < 4 ? x : x2) + (q & 3) * 2, idesc, pl.run != 0 || q != 0);
-            gemm::mma_commit(empty_a(st));
-            gemm::mma_commit(empty_x(sx));
-            if (pl.ends_run(at, end, P.pieces)) {
-                gemm::mma_commit(acc_full(b));
-                ++r;
+                for (int q = 0; q < 8; ++q)
+                    mma_from_tmem(d, a + q * 8, (q < 4 ? x : x2) + (q & 3) * 2, idesc, pl.run != 0 || q != 0);
+                gemm::mma_commit(empty_a(st));
+                gemm::mma_commit(empty_x(sx));
+                if (ends) gemm::mma_commit(acc_full(b));
             }
+            __syncwarp();
+            if (ends) ++r;
             pl.next(at, end, P.pieces);
         }
-        gemm::mma_commit(drained);
-        mbar_wait(drained, 0, limit_ns);
+        if (prod::elect_one()) gemm::mma_commit(drained);
+        __syncwarp();
+        prod::warp_wait(drained, 0, limit_ns);
     } else if (warp >= 2 && warp < 6) {
         // ------------------------------------------------------- sums
         asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -142,6 +142,25 @@ __device__ __forceinline__ void triangle_coords(uint32_t w, uint32_t &mt, uint32
     mt = w - c * (c + 1) / 2;
 }
 
+// One lane of the warp, the same each time.  The producer and the MMA warp run
+// their loops with all lanes and let one issue: their addresses and descriptors
+// then stay in uniform registers.  Issued by a lone lane, each tcgen05.mma cost
+// about 90 cycles (measured at M = 128, where one with N = 48 takes 25).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0); }
+
+// A wait by all lanes of a warp, which go on, or give up, together.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns)
+{
+    return __all_sync(0xFFFFFFFFu, pair_wait(bar, parity, limit_ns));
+}
+
 struct Item {
     uint32_t z, m0, n0, width;
     bool mirror;
@@ -390,7 +409,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     const uint32_t tmem_slot = drained + 8u;
     const uint32_t *tmem_slot_ptr = reinterpret_cast<const uint32_t *>(smem_raw + (tmem_slot - raw));
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const bool leader = rank == 0;
     const uint32_t cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
@@ -419,12 +438,12 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     }
     cluster_sync();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    const uint32_t tmem = *tmem_slot_ptr;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot_ptr, 0);
     // the operands may be the previous kernel's output
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // ------------------------------------------------------- producer
         uint32_t g = 0, s = 0, phase = 0;
         bool wrapped = false, ok = true;
@@ -444,10 +463,11 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 const uint32_t dst = base + s * kStageBytes;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    if (wrapped && !pair_wait(empty(s, j), phase ^ 1u, limit_ns)) {
+                    if (wrapped && !warp_wait(empty(s, j), phase ^ 1u, limit_ns)) {
                         ok = false;
                         break;
                     }
+                    if (!elect_one()) continue;
                     if (j == 0 && leader) mbar_arrive_expect_tx(full(s), bytes);
                     const int32_t k0 = static_cast<int32_t>(kb * kBK + j * 64);
                     const uint32_t da = dst + j * kHalfBytes, db = dst + (2 + j) * kHalfBytes;
@@ -475,9 +495,9 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         }
         for (uint32_t q = 0; q < static_cast<uint32_t>(kStages) && q < g; ++q) {
             const uint32_t last_use = (g - 1 - q) / kStages;
-            for (int j = 0; j < 2; ++j) pair_wait(empty(static_cast<int>(q), j), last_use & 1u, limit_ns);
+            for (int j = 0; j < 2; ++j) warp_wait(empty(static_cast<int>(q), j), last_use & 1u, limit_ns);
         }
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1 && leader) {
         // ------------------------------------------------------ MMA issuer
         uint32_t s = 0, phase = 0, i = 0;
         bool ok = true;
@@ -490,7 +510,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             for (uint32_t kc = 0; ok && kc < kblocks; kc += P.chunk, ++i) {
                 const int b = static_cast<int>(i % kAccBufs);
                 const uint32_t ub = i / kAccBufs;
-                if (ub > 0 && !mbar_wait_cluster(acc_empty(b), (ub - 1) & 1u, limit_ns)) {
+                if (ub > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(acc_empty(b), (ub - 1) & 1u, limit_ns))) {
                     ok = false;
                     break;
                 }
@@ -498,32 +518,38 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 const uint32_t d = tmem + static_cast<uint32_t>(b * kTile);
                 const uint32_t kend = kblocks - kc < P.chunk ? kblocks : kc + P.chunk;
                 for (uint32_t kb = kc; kb < kend; ++kb) {
-                    if (!pair_wait(full(s), phase, limit_ns)) {
+                    if (!warp_wait(full(s), phase, limit_ns)) {
                         ok = false;
                         break;
                     }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const uint64_t ad = desc_a0 + s * kDescStage, bd = desc_b0 + s * kDescStage;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint64_t aj = ad + j * kDescHalf, bj = bd + j * kDescHalf;
-                        mma_bf16_pair(d, aj, bj, idesc, (kb != kc || j != 0) ? 1u : 0u);
-                        mma_bf16_pair(d, aj + kStepA, bj + kStepB, idesc, 1u);
-                        mma_bf16_pair(d, aj + 2 * kStepA, bj + 2 * kStepB, idesc, 1u);
-                        mma_bf16_pair(d, aj + 3 * kStepA, bj + 3 * kStepB, idesc, 1u);
-                        mma_commit_pair(empty(s, j));
+                        for (int j = 0; j < 2; ++j) {
+                            const uint64_t aj = ad + j * kDescHalf, bj = bd + j * kDescHalf;
+                            mma_bf16_pair(d, aj, bj, idesc, (kb != kc || j != 0) ? 1u : 0u);
+                            mma_bf16_pair(d, aj + kStepA, bj + kStepB, idesc, 1u);
+                            mma_bf16_pair(d, aj + 2 * kStepA, bj + 2 * kStepB, idesc, 1u);
+                            mma_bf16_pair(d, aj + 3 * kStepA, bj + 3 * kStepB, idesc, 1u);
+                            mma_commit_pair(empty(s, j));
+                        }
                     }
+                    __syncwarp();
                     if (++s == kStages) {
                         s = 0;
                         phase ^= 1u;
                     }
                 }
-                mma_commit_pair(acc_full(b));
+                if (elect_one()) mma_commit_pair(acc_full(b));
+                __syncwarp();
             }
         }
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(drained)
-                     : "memory");
-        pair_wait(drained, 0, limit_ns);
+        if (elect_one())
+            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(drained)
+                         : "memory");
+        __syncwarp();
+        warp_wait(drained, 0, limit_ns);
     } else if (warp >= 2) {
         // ------------------------------------------------------- epilogue
         const int quarter = warp & 3;
