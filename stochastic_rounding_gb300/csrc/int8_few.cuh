@@ -73,39 +73,43 @@ __device__ __noinline__ uint4 load16_slow(const int8_t *p, uint32_t count)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The outputs of one column and COUNT tokens (`live` of them) from their integer
-// sums.  Loads first: with a load before each store a row block took one trip to
-// L2 a token.
-template <int COUNT>
-__device__ __forceinline__ void store_outputs(const Params &P, uint32_t token, uint32_t col, const int32_t sum[COUNT],
-                                              uint32_t live)
+// Stochastic rounding of the output of element e: out of line, so that the code
+// around it, which runs once or twice a CTA and mostly rounds to nearest, stays
+// short (inlined for 16 tokens, fetching it cost 2 us).
+__device__ __noinline__ uint32_t round_stochastic(float y, uint64_t e, uint32_t step, const RoundKeys &K)
 {
-    const float cs = __ldg(P.col_scale + col);
+    uint32_t r[4];
+    philox_q(e >> 2, step, K, r);
+    const uint32_t sel = static_cast<uint32_t>(e & 3u);
+    return round_sr(y, sel == 0 ? r[0] : sel == 1 ? r[1] : sel == 2 ? r[2] : r[3]);
+}
+
+// The outputs of one column (of scale cs) and COUNT tokens (`live` of them, of
+// scales rs) from their integer sums.
+template <int COUNT>
+__device__ __forceinline__ void store_outputs(const Params &P, uint32_t token, uint32_t col, float cs, const float *rs,
+                                              const int32_t sum[COUNT], uint32_t live)
+{
     float y[COUNT];
 #pragma unroll
-    for (int q = 0; q < COUNT; ++q)
-        y[q] = static_cast<uint32_t>(q) < live ? __ldg(P.row_scale + token + q) : 0.0f;
+    for (int q = 0; q < COUNT; ++q) y[q] = __fmul_rn(__fmul_rn(__int2float_rn(sum[q]), rs[q]), cs);
+    const uint64_t dst = token * P.ldc + col;
+    if (P.c_dtype == ASR_F32) {
 #pragma unroll
-    for (int q = 0; q < COUNT; ++q) y[q] = __fmul_rn(__fmul_rn(__int2float_rn(sum[q]), y[q]), cs);
+        for (int q = 0; q < COUNT; ++q)
+            if (static_cast<uint32_t>(q) < live) static_cast<float *>(P.c)[dst + q * P.ldc] = y[q];
+    } else if (P.rounding == ASR_ROUND_SR) {
+        const uint64_t e = static_cast<uint64_t>(token) * P.n + col;
 #pragma unroll
-    for (int q = 0; q < COUNT; ++q) {
-        if (static_cast<uint32_t>(q) >= live) continue;
-        const uint64_t dst = (token + q) * P.ldc + col;
-        if (P.c_dtype == ASR_F32) {
-            static_cast<float *>(P.c)[dst] = y[q];
-            continue;
-        }
-        uint32_t h;
-        if (P.rounding == ASR_ROUND_SR) {
-            const uint64_t e = static_cast<uint64_t>(token + q) * P.n + col;
-            uint32_t r[4];
-            philox_q(e >> 2, P.step, P.keys, r);
-            const uint32_t sel = static_cast<uint32_t>(e & 3u);
-            h = round_sr(y[q], sel == 0 ? r[0] : sel == 1 ? r[1] : sel == 2 ? r[2] : r[3]);
-        } else {
-            h = round_rne(y[q]);
-        }
-        static_cast<uint16_t *>(P.c)[dst] = static_cast<uint16_t>(h);
+        for (int q = 0; q < COUNT; ++q)
+            if (static_cast<uint32_t>(q) < live)
+                static_cast<uint16_t *>(P.c)[dst + q * P.ldc] =
+                    static_cast<uint16_t>(round_stochastic(y[q], e + static_cast<uint64_t>(q) * P.n, P.step, P.keys));
+    } else {
+#pragma unroll
+        for (int q = 0; q < COUNT; ++q)
+            if (static_cast<uint32_t>(q) < live)
+                static_cast<uint16_t *>(P.c)[dst + q * P.ldc] = static_cast<uint16_t>(round_rne(y[q]));
     }
 }
 
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_dots_kernel(const __grid_cons
                 const int32_t sum = sums[token * kSumPitch + row];
                 sums[token * kSumPitch + row] = 0;
                 if (!whole) atomicAdd(mine, sum);
-                else if (col < P.n) store_outputs<1>(P, token, col, &sum, 1);
+                else if (col < P.n) store_outputs<1>(P, token, col, P.col_scale[col], P.row_scale + token, &sum, 1);
             }
             if (!whole) {
                 __threadfence();
@@ -271,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_dots_kernel(const __grid_cons
                     __threadfence();
                     if (token < P.m && col < P.n) {
                         const int32_t sum = __ldcg(mine);
-                        store_outputs<1>(P, token, col, &sum, 1);
+                        store_outputs<1>(P, token, col, P.col_scale[col], P.row_scale + token, &sum, 1);
                     }
                 }
             }
@@ -320,7 +324,7 @@ constexpr int kBars = 4 * kMaxRing + 2 * kRing + 4 + 3;
 // Shared memory for a pass of `each` tokens: rings of the tokens and of the
 // weight's bytes, and the sums of a part longer than 1,024 of K.
 struct FewShape {
-    uint32_t x_ring, w_ring, x_bytes, sums_at, w_at, bars_at, bytes;
+    uint32_t x_ring, w_ring, x_bytes, sums_at, w_at, scales_at, bars_at, bytes;
 };
 
 __host__ __device__ constexpr FewShape few_shape(uint32_t each)
@@ -329,10 +333,11 @@ __host__ __device__ constexpr FewShape few_shape(uint32_t each)
     f.x_bytes = each * kPiece * 2;
     f.x_ring = each <= 64 ? 4 : 2;
     f.w_at = f.x_ring * f.x_bytes;              // 1,024-byte multiples: each is a multiple of 16
-    const uint32_t left = kFewSmem - 16 - 1024 - f.w_at - each * kRows * 4 - kBars * 8;
+    const uint32_t left = kFewSmem - 16 - 1024 - f.w_at - each * (kRows + 4) * 4 - kBars * 8;
     f.w_ring = left / kPieceBytes < kMaxRing ? left / kPieceBytes : kMaxRing;
     f.sums_at = f.w_at + f.w_ring * kPieceBytes;
-    f.bars_at = f.sums_at + each * kRows * 4;
+    f.scales_at = f.sums_at + each * kRows * 4;
+    f.bars_at = f.scales_at + each * 4 * 4;
     f.bytes = 1024 + f.bars_at + kBars * 8 + 16;
     return f;
 }
@@ -512,16 +517,21 @@ few_rows_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         // ------------------------------------------------------- sums
         asm volatile("griddepcontrol.wait;" ::: "memory");
         const uint32_t quarter = warp & 3u, row = quarter * 32 + lane;
+        // the tokens' scales at hand (each warp writes and reads its own copy), zero past the last
+        float *rs = reinterpret_cast<float *>(smem_raw + (xs - raw) + F.scales_at) + quarter * each;
+        for (uint32_t q = lane; q < each; q += 32) rs[q] = q < tokens ? P.row_scale[token0 + q] : 0.0f;
+        __syncwarp();
         Place pl(first, P.pieces);
         uint32_t r = 0, shares = 0;
         bool held = false;                              // sums of this part in shared memory already
         for (uint32_t at = first; at < end; ++at) {
             if (pl.ends_run(at, end, P.pieces)) {
-                const uint32_t b = r & 1u;
+                const uint32_t b = r & 1u, out = pl.tile * kRows + row;
+                const float cs = out < P.n ? __ldg(P.col_scale + out) : 0.0f;
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_full(b), (r >> 1) & 1u, limit_ns))) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const bool last = pl.ends_part(at, end, P.pieces), whole = last && pl.part + 1 == P.pieces;
-                const uint32_t tq = tmem + ((quarter * 32) << 16) + kAccAt + b * kMaxTokens, col = pl.tile * kRows + row;
+                const uint32_t tq = tmem + ((quarter * 32) << 16) + kAccAt + b * kMaxTokens, col = out;
                 int32_t *shared = P.sums + (static_cast<uint64_t>(pl.tile) * P.m + token0) * kRows + row;
 #pragma unroll 1
                 for (uint32_t c = 0; c < tokens; c += 16) {
@@ -541,7 +551,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                         for (int q = 0; q < 16; ++q)
                             if (c + q < tokens) atomicAdd(shared + (c + q) * kRows, sum[q]);
                     } else if (col < P.n) {
-                        store_outputs<16>(P, token0 + c, col, sum, tokens - c);
+                        store_outputs<16>(P, token0 + c, col, cs, rs + c, sum, tokens - c);
                     }
                 }
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -563,12 +573,22 @@ few_rows_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                     ++shares;
                     if (done == P.pieces) {
                         __threadfence();
+                        // 64 tokens' loads at a time in flight
 #pragma unroll 1
-                        for (uint32_t c = 0; c < tokens && col < P.n; c += 16) {
-                            int32_t sum[16];
+                        for (uint32_t c = 0; c < tokens && col < P.n; c += 64) {
+                            int32_t sum[64];
 #pragma unroll
-                            for (int q = 0; q < 16; ++q) sum[q] = c + q < tokens ? __ldcg(shared + (c + q) * kRows) : 0;
-                            store_outputs<16>(P, token0 + c, col, sum, tokens - c);
+                            for (int h = 0; h < 4; ++h)
+                                if (c + 16 * h < tokens) {
+#pragma unroll
+                                    for (int q = 0; q < 16; ++q)
+                                        sum[16 * h + q] = __ldcg(shared + min(c + 16 * h + q, tokens - 1) * kRows);
+                                }
+#pragma unroll
+                            for (int h = 0; h < 4; ++h)
+                                if (c + 16 * h < tokens)
+                                    store_outputs<16>(P, token0 + c + 16 * h, col, cs, rs + c + 16 * h, sum + 16 * h,
+                                                      tokens - c - 16 * h);
                         }
                     }
                 }
