@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import struct
 from typing import Optional, Sequence
@@ -246,9 +247,15 @@ def make_hparams(lr, beta1, beta2, eps, weight_decay, step, seed, rounding="sr")
 
 # ------------------------------------------------------------ tensor helpers
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dev_ptr(t, name, dtypes, numel=None, device=None):
@@ -557,8 +564,7 @@ _ADJUST = {None: ASR_MUON_ADJUST_NONE, "none": ASR_MUON_ADJUST_NONE, "original":
 def _strided_ptr(t, name, dtypes, device=None):
     """As ``_dev_ptr`` for a 2-D or 3-D tensor whose last dimension is
     contiguous: (pointer, count, rows, cols, row pitch, matrix pitch)."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
@@ -566,13 +572,17 @@ def _strided_ptr(t, name, dtypes, device=None):
         raise ValueError(f"{name} is on cuda:{t.get_device()}; the call's other tensors are on cuda:{device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}; expected one of {dtypes}")
-    if t.dim() not in (2, 3):
-        raise ValueError(f"{name} must be a matrix or a stack of matrices (2-D or 3-D), not {t.dim()}-D")
-    rows, cols = t.shape[-2], t.shape[-1]
-    count = t.shape[0] if t.dim() == 3 else 1
-    ld = t.stride(-2) if rows > 1 else cols
-    stride = t.stride(0) if t.dim() == 3 and count > 1 else 0
-    if (cols > 1 and t.stride(-1) != 1) or ld < cols:
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 2:
+        count, stride = 1, 0
+    elif len(shape) == 3:
+        count = shape[0]
+        stride = strides[0] if count > 1 else 0
+    else:
+        raise ValueError(f"{name} must be a matrix or a stack of matrices (2-D or 3-D), not {len(shape)}-D")
+    rows, cols = shape[-2], shape[-1]
+    ld = strides[-2] if rows > 1 else cols
+    if (cols > 1 and strides[-1] != 1) or ld < cols:
         raise ValueError(f"{name}'s rows must be contiguous and must not overlap")
     return t.data_ptr(), count, rows, cols, ld, stride
 
@@ -582,6 +592,9 @@ def _workspace(workspace, need, device, stream):
     memory of the call's stream, given back to torch's allocator after the
     call (which hands it out again only to later work of that stream)."""
     torch = _torch()
+    if workspace is None and stream is None:
+        buf = torch.empty(need, dtype=torch.uint8, device=device)
+        return buf, buf.data_ptr(), need
     if workspace is not None:
         if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
             raise TypeError("workspace must be a contiguous CUDA tensor")
@@ -591,12 +604,9 @@ def _workspace(workspace, need, device, stream):
         if size < need:
             raise ValueError(f"workspace has {size} bytes; the call needs {need}")
         return workspace, workspace.data_ptr(), size
-    if stream is None:
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(s):
         buf = torch.empty(need, dtype=torch.uint8, device=device)
-    else:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
-        with torch.cuda.stream(s):
-            buf = torch.empty(need, dtype=torch.uint8, device=device)
     return buf, buf.data_ptr(), need
 
 
@@ -720,7 +730,7 @@ _AXIS = {"rows": ASR_ROWS, "columns": ASR_COLUMNS}
 
 def _matrix_ptr(t, name, dtypes, device=None):
     p, count, rows, cols, ld, _ = _strided_ptr(t, name, dtypes, device)
-    if t.dim() != 2:
+    if len(t.shape) != 2:
         raise ValueError(f"{name} must be 2-D")
     return p, rows, cols, ld
 
@@ -758,6 +768,7 @@ def asr_quantize_int8(x, q, scale, *, axis="rows", rounding="rne", base_index: i
     return q, scale
 
 
+@functools.lru_cache(maxsize=1024)
 def asr_gemm_int8_workspace(m: int, n: int, k: int) -> int:
     """Bytes of workspace that ``asr_gemm_int8_sr`` needs at these sizes."""
     need = ctypes.c_uint64(0)
@@ -791,6 +802,7 @@ def asr_gemm_int8_sr(a, b, a_scale, b_scale, c, *, rounding="sr", step: int = 0,
     return c
 
 
+@functools.lru_cache(maxsize=1024)
 def asr_linear_int8_workspace(m: int, n: int, k: int) -> int:
     """Bytes of workspace that ``asr_linear_int8`` needs at these sizes."""
     need = ctypes.c_uint64(0)
@@ -804,10 +816,11 @@ def asr_linear_int8(x, weight, weight_scale, y, *, rounding="rne", step: int = 0
     inside the call; ``weight`` (n, k) int8 with ``weight_scale`` (n) float32;
     ``y`` (tokens, n) bfloat16 or float32."""
     torch = _torch()
-    px, m, k, x_ld = _matrix_ptr(x, "x", (torch.bfloat16, torch.float32))
+    types = (torch.bfloat16, torch.float32)
+    px, m, k, x_ld = _matrix_ptr(x, "x", types)
     d = x.get_device()
     pw, n, kw, ldw = _matrix_ptr(weight, "weight", (torch.int8,), d)
-    py, my, ny, ldy = _matrix_ptr(y, "y", (torch.bfloat16, torch.float32), d)
+    py, my, ny, ldy = _matrix_ptr(y, "y", types, d)
     if kw != k or my != m or ny != n:
         raise ValueError(f"shapes do not chain: x {tuple(x.shape)}, weight {tuple(weight.shape)}, y {tuple(y.shape)}")
     ps = _dev_ptr(weight_scale, "weight_scale", (torch.float32,), n, d)
@@ -824,6 +837,7 @@ def asr_linear_int8(x, weight, weight_scale, y, *, rounding="rne", step: int = 0
     return y
 
 
+@functools.lru_cache(maxsize=1024)
 def asr_linear_int8_grads_workspace(tokens: int, n: int, k: int) -> int:
     """Bytes of workspace that ``asr_linear_int8_grads`` needs at these sizes."""
     need = ctypes.c_uint64(0)
