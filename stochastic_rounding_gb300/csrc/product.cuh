@@ -43,7 +43,7 @@ using gemm::tile_coords;
 constexpr int kTile = 256;                      // tile rows and columns of a CTA pair
 constexpr int kBK = 128;                        // K per stage, two halves of 64
 constexpr int kStages = 3;
-constexpr int kEpi = 8;                         // epilogue warps: two per TMEM lane quarter
+constexpr int kEpi = 16;                        // epilogue warps: four per TMEM lane quarter
 constexpr int kThreads = 64 + 32 * kEpi;
 constexpr int kSpan = kTile / (kEpi / 4);       // columns per epilogue warp
 constexpr uint32_t kHalfBytes = 128 * 64 * 2;   // a K-half of one operand in one CTA
@@ -51,10 +51,9 @@ constexpr uint32_t kStageBytes = 4 * kHalfBytes;
 constexpr int kAccBufs = 2;
 constexpr uint32_t kTmemCols = kTile * kAccBufs;
 constexpr int kBars = kStages * 3 + 2 * kAccBufs + 1;
-// Per epilogue warp, 32 rows x 32 columns of binary32 on their way out, rows 33
-// words apart so that neither rows nor columns collide in a bank.
-constexpr int kPitch = 33;
-constexpr uint32_t kWarpStage = 32 * kPitch * 4;
+constexpr int kBlock = 16;                      // columns an epilogue warp finishes at a time
+// Per epilogue warp, 32 rows x 16 columns of binary32 on their way out.
+constexpr uint32_t kWarpStage = 32 * kBlock * 4;
 constexpr int kBarBytes = (kBars * 8 + 16 + 127) / 128 * 128;
 constexpr int kSmem = 1024 + kStages * kStageBytes + kBarBytes + kEpi * kWarpStage;
 constexpr int kGroupM = 8;
@@ -119,6 +118,10 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
         ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(cluster_bar)
         : "memory");
 }
+
+// Word of row r, column c of a staging area: columns change places by row, so
+// that neither 32 rows of a column nor two whole rows collide in a bank.
+__device__ __forceinline__ uint32_t staged(uint32_t r, uint32_t c) { return r * kBlock + (c ^ ((r >> 1) & 15u)); }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 {
@@ -195,197 +198,161 @@ __device__ __forceinline__ void ld_global_v8(const void *p, uint32_t w[8])
                  : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t v[32])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
-          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
-// 32 sums of this lane's row `row`, columns col .. col+31, to a stored matrix.
+// 16 sums of this lane's row `row`, columns col .. col+15, to a stored matrix.
 // Rows past m are not written; columns are, up to the row's padding (their
-// sums are zero: operands read as zeros there).  Where the tile has a mirror
-// image, the block goes out a second time, turned in the warp's staging area.
+// sums are zero: operands read as zeros there).  `prior`: the stored S there
+// (kPoly).  Where the tile has a mirror image, the block goes out a second time,
+// turned in the warp's staging area: lane l takes rows 16 (l / 16) on of column l % 16.
 template <int OP>
-__device__ __forceinline__ void store_stored(const Params &P, const Item &it, uint32_t row, uint32_t col, float x[32],
-                                             float *stage, int lane)
+__device__ __forceinline__ void store_stored(const Params &P, const Item &it, uint32_t row, uint32_t col,
+                                             const uint32_t v[16], const uint32_t prior[8], float *stage, int lane)
 {
     __half *mat = P.out + it.z * P.stride;
-    const uint64_t at = static_cast<uint64_t>(row) * P.ld + col;
-    const bool in = row < P.m;
+    float x[16];
     if constexpr (OP == kPoly) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t s[8] = {};
-            if (in && col + 16 * h < P.n) ld_global_v8(P.aux + it.z * P.stride + at + 16 * h, s);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const float2 v = unpack_f16(s[q]);
-                x[16 * h + 2 * q] = fmaf(P.alpha, x[16 * h + 2 * q], P.beta * v.x);
-                x[16 * h + 2 * q + 1] = fmaf(P.alpha, x[16 * h + 2 * q + 1], P.beta * v.y);
-            }
+        for (int q = 0; q < 8; ++q) {
+            const float2 s = unpack_f16(prior[q]);
+            x[2 * q] = fmaf(P.alpha, __uint_as_float(v[2 * q]), P.beta * s.x);
+            x[2 * q + 1] = fmaf(P.alpha, __uint_as_float(v[2 * q + 1]), P.beta * s.y);
         }
         if (!it.mirror) {
             const uint32_t d = row - col;
 #pragma unroll
-            for (int q = 0; q < 32; ++q)
+            for (int q = 0; q < 16; ++q)
                 if (d == static_cast<uint32_t>(q)) x[q] += P.diag;
         }
     } else {
 #pragma unroll
-        for (int q = 0; q < 32; ++q) x[q] *= P.alpha;
+        for (int q = 0; q < 16; ++q) x[q] = P.alpha * __uint_as_float(v[q]);
     }
-    if (in) {
+    if (row < P.m) {
+        uint32_t w[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t w[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) w[q] = pack_f16(x[16 * h + 2 * q], x[16 * h + 2 * q + 1]);
-            if (col + 16 * h < P.n) st_global_v8(mat + at + 16 * h, w);
-        }
+        for (int q = 0; q < 8; ++q) w[q] = pack_f16(x[2 * q], x[2 * q + 1]);
+        st_global_v8(mat + static_cast<uint64_t>(row) * P.ld + col, w);
     }
     if (OP != kNext && it.mirror) {
         __syncwarp();
 #pragma unroll
-        for (int q = 0; q < 32; ++q) stage[lane * kPitch + q] = x[q];
+        for (int q = 0; q < 16; ++q) stage[staged(lane, q)] = x[q];
         __syncwarp();
-        if (col + lane < P.n) {
-            const uint32_t row0 = row - lane;        // row col + lane of the image, its columns row0 .. row0+31
-            __half *dst = mat + static_cast<uint64_t>(col + lane) * P.ld + row0;
+        const uint32_t c = lane & 15, r = lane & 16, row0 = row - lane + r;
+        uint32_t w[8];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t w[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    w[q] = pack_f16(stage[(16 * h + 2 * q) * kPitch + lane], stage[(16 * h + 2 * q + 1) * kPitch + lane]);
-                if (row0 + 16 * h < P.m) st_global_v8(dst + 16 * h, w);
-            }
-        }
+        for (int q = 0; q < 8; ++q) w[q] = pack_f16(stage[staged(r + 2 * q, c)], stage[staged(r + 2 * q + 1, c)]);
+        if (col + c < P.n && row0 < P.m) st_global_v8(mat + static_cast<uint64_t>(col + c) * P.ld + row0, w);
     }
 }
 
-// A 32 x 32 block of sums in the warp's staging area (lane r wrote row r), first
-// row row0 and column col, to the caller's matrix.  Each lane finishes its own
-// row, eight columns at a time; full blocks of aligned matrices are stored from
-// there (and parameters read), others pass through the staging area once more,
-// so that the lanes lie along a row in memory whatever the row pitch.
-template <int OP>
-__device__ __forceinline__ void finish_block(const Params &P, uint32_t z, uint32_t row0, uint32_t col, float *stage)
+// The raw words of 16 parameters (bf16: eight, f32: sixteen) at `at`.
+__device__ __forceinline__ void load_params(const Params &P, const void *ptr, uint64_t at, uint32_t p[16])
 {
-    const int lane = threadIdx.x & 31;
-    const uint32_t row = row0 + lane;
-    const uint32_t live = P.n - col < 32 ? P.n - col : 32, rows = P.m - row0 < 32 ? P.m - row0 : 32;
-    const bool direct = P.vec && live == 32, bf16 = P.out_dtype == ASR_BF16;
+    if (P.out_dtype == ASR_BF16) {
+        ld_global_v8(static_cast<const uint16_t *>(ptr) + at, p);
+    } else {
+        ld_global_v8(static_cast<const float *>(ptr) + at, p);
+        ld_global_v8(static_cast<const float *>(ptr) + at + 8, p + 8);
+    }
+}
+
+__device__ __forceinline__ float param_value(const Params &P, const uint32_t p[16], int q)
+{
+    return P.out_dtype == ASR_BF16 ? (q & 1 ? bf16_hi(p[q >> 1]) : bf16_lo(p[q >> 1])) : __uint_as_float(p[q]);
+}
+
+// 16 finished values of one row to bf16 words; random bits of elements e on.
+__device__ __forceinline__ void round16(const Params &P, const float x[16], uint64_t e, uint32_t w[8])
+{
+    if (P.rounding == ASR_ROUND_SR) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            uint32_t r[8];
+            if ((e & 3u) == 0) unit_words<true>(e, 8 * u, P.step, P.keys, r);
+            else unit_words<false>(e, 8 * u, P.step, P.keys, r);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                w[4 * u + q] = sr_pack2<true>(x[8 * u + 2 * q], x[8 * u + 2 * q + 1], r[2 * q], r[2 * q + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) w[q] = pack_bf16(round_rne(x[2 * q]), round_rne(x[2 * q + 1]));
+    }
+}
+
+// 16 sums x of row `row`, columns col .. col+15, to the caller's matrix.  Each
+// lane finishes its own row; full blocks of aligned matrices are stored from
+// there (`params`: what load_params gave), others pass through the staging area,
+// in which the lanes lie along two rows at a time, whatever the row pitch: a
+// lane that stores (and loads) its own row alone touches a sector an element.
+template <int OP>
+__device__ __forceinline__ void finish_block(const Params &P, uint32_t z, uint32_t row, uint32_t col, float x[16],
+                                             const uint32_t params[16], const float *col_scale, float *stage, int lane)
+{
+    const uint32_t row0 = row - lane, live = P.n - col < 16 ? P.n - col : 16;
+    const bool direct = P.vec && live == 16, bf16 = P.out_dtype == ASR_BF16, in = row < P.m;
     const Slot S = P.slot[z];
     uint16_t *out16 = static_cast<uint16_t *>(S.ptr);
     float *out32 = static_cast<float *>(S.ptr);
-    const uint64_t at0 = static_cast<uint64_t>(row0) * P.out_ld + col;
-    float *own = stage + lane * kPitch;
-    float p[32];
+    const uint64_t at = static_cast<uint64_t>(row) * P.out_ld + col;
+    const uint32_t c = lane & 15, r0 = lane >> 4;
     if constexpr (OP == kParam) {
-        // the parameters, into this lane's registers
         if (direct) {
-            if (row < P.m) {
-                const uint64_t at = at0 + lane * P.out_ld;
-                if (bf16) {
-                    uint32_t w[16];
-                    ld_global_v8(out16 + at, w);
-                    ld_global_v8(out16 + at + 16, w + 8);
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) p[2 * q] = bf16_lo(w[q]), p[2 * q + 1] = bf16_hi(w[q]);
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t w[8];
-                        ld_global_v8(out32 + at + 8 * h, w);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) p[8 * h + q] = __uint_as_float(w[q]);
-                    }
-                }
-            }
+            for (int q = 0; q < 16; ++q)
+                x[q] = __fsub_rn(__fmul_rn(param_value(P, params, q), P.beta), __fmul_rn(P.alpha, x[q]));
         } else {
-            float sum[32];
-#pragma unroll
-            for (int q = 0; q < 32; ++q) sum[q] = own[q];
             __syncwarp();
 #pragma unroll 8
-            for (uint32_t r = 0; r < 32; ++r) {
-                const uint64_t at = at0 + r * P.out_ld + lane;
-                if (r < rows && lane < live) stage[r * kPitch + lane] = bf16 ? bf16_lo(out16[at]) : out32[at];
+            for (uint32_t r = r0; r < 32; r += 2) {
+                const uint64_t a = static_cast<uint64_t>(row0 + r) * P.out_ld + col + c;
+                if (row0 + r < P.m && c < live) stage[staged(r, c)] = bf16 ? bf16_lo(out16[a]) : out32[a];
             }
             __syncwarp();
 #pragma unroll
-            for (int q = 0; q < 32; ++q) {
-                p[q] = own[q];
-                own[q] = sum[q];
-            }
+            for (int q = 0; q < 16; ++q)
+                x[q] = __fsub_rn(__fmul_rn(stage[staged(lane, q)], P.beta), __fmul_rn(P.alpha, x[q]));
         }
-#pragma unroll
-        for (int q = 0; q < 32; ++q) own[q] = __fsub_rn(__fmul_rn(p[q], P.beta), __fmul_rn(P.alpha, own[q]));
     }
-    const float rs = OP == kInt8 && row < P.m ? P.row_scale[row] : 0.0f;
-    const uint64_t e = S.base + static_cast<uint64_t>(row) * P.n + col;
-    uint32_t w[4];
-#pragma unroll 1
-    for (int u = 0; u < 4; ++u) {
-        float x[8];
+    if constexpr (OP == kInt8) {
+        const float rs = in ? __ldg(P.row_scale + row) : 0.0f;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            x[q] = own[8 * u + q];
-            if constexpr (OP == kInt8)
-                x[q] = __fmul_rn(__fmul_rn(x[q], rs), 8 * u + q < live ? __ldg(P.col_scale + col + 8 * u + q) : 0.0f);
-            if constexpr (OP == kOut) x[q] *= P.alpha;
-        }
+        for (int q = 0; q < 16; ++q) x[q] = __fmul_rn(__fmul_rn(x[q], rs), col_scale[q]);
+    }
+    if constexpr (OP == kOut) {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) x[q] *= P.alpha;
+    }
+    uint32_t w[8];
+    if (bf16) round16(P, x, S.base + static_cast<uint64_t>(row) * P.n + col, w);
+    if (direct) {
+        if (!in) return;
         if (bf16) {
-            uint32_t h[8];
-            if (P.rounding == ASR_ROUND_SR) {
-                uint32_t r[8];
-                if ((e & 3u) == 0) unit_words<true>(e, 8 * u, P.step, P.keys, r);
-                else unit_words<false>(e, 8 * u, P.step, P.keys, r);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) h[q] = round_sr(x[q], r[q]);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 8; ++q) h[q] = round_rne(x[q]);
-            }
-            if (direct) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) w[q] = pack_bf16(h[2 * q], h[2 * q + 1]);
-                if (row < P.m)
-                    *reinterpret_cast<uint4 *>(out16 + at0 + lane * P.out_ld + 8 * u) = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 8; ++q) own[8 * u + q] = __uint_as_float(h[q]);
-            }
-        } else if (direct) {
-            uint32_t v[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = __float_as_uint(x[q]);
-            if (row < P.m) st_global_v8(out32 + at0 + lane * P.out_ld + 8 * u, v);
+            st_global_v8(out16 + at, w);
         } else {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) own[8 * u + q] = x[q];
+            for (int h = 0; h < 2; ++h) {
+                uint32_t v[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] = __float_as_uint(x[8 * h + q]);
+                st_global_v8(out32 + at + 8 * h, v);
+            }
         }
+        return;
     }
     __syncwarp();
-    if (!direct) {
+#pragma unroll
+    for (int q = 0; q < 16; ++q)
+        stage[staged(lane, q)] = bf16 ? __uint_as_float(w[q >> 1] >> ((q & 1) * 16)) : x[q];
+    __syncwarp();
 #pragma unroll 8
-        for (uint32_t r = 0; r < 32; ++r) {
-            const uint64_t at = at0 + r * P.out_ld + lane;
-            if (r < rows && lane < live) {
-                const float v = stage[r * kPitch + lane];
-                if (bf16) out16[at] = static_cast<uint16_t>(__float_as_uint(v));
-                else out32[at] = v;
-            }
+    for (uint32_t r = r0; r < 32; r += 2) {
+        const uint64_t a = static_cast<uint64_t>(row0 + r) * P.out_ld + col + c;
+        if (row0 + r < P.m && c < live) {
+            const float v = stage[staged(r, c)];
+            if (bf16) out16[a] = static_cast<uint16_t>(__float_as_uint(v));
+            else out32[a] = v;
         }
-        __syncwarp();
     }
 }
 
@@ -563,7 +530,23 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             const uint32_t ncols = it.n0 >= P.n ? 0 : P.n - it.n0 < it.width ? P.n - it.n0 : it.width;
             const uint32_t c_hi = ncols < c_lo + kSpan ? ncols : c_lo + kSpan;
             constexpr bool kStored = OP == kGram || OP == kPoly || OP == kNext;
+            const bool rows_in = row - lane < P.m;          // the same for the whole warp
+            const uint32_t col0 = it.n0 + c_lo, cols = c_hi > c_lo && rows_in ? c_hi - c_lo : 0;
             int32_t acc[OP == kInt8 ? kSpan : 1];
+            uint32_t prior[OP == kPoly ? kSpan / 2 : 1];
+            float scale[OP == kInt8 ? kSpan / 32 : 1];
+            // what the epilogue reads from memory, before it waits for the sums
+            if constexpr (OP == kPoly) {
+#pragma unroll
+                for (int c = 0; c < kSpan; c += kBlock)
+                    if (static_cast<uint32_t>(c) < cols && row < P.m)
+                        ld_global_v8(P.aux + it.z * P.stride + static_cast<uint64_t>(row) * P.ld + col0 + c, prior + c / 2);
+            }
+            if constexpr (OP == kInt8) {
+#pragma unroll
+                for (int h = 0; h < kSpan / 32; ++h)
+                    scale[h] = 32u * h + lane < cols ? __ldg(P.col_scale + col0 + 32 * h + lane) : 0.0f;
+            }
             for (uint32_t kc = 0; kc < kblocks; kc += P.chunk, ++i) {
                 const int b = static_cast<int>(i % kAccBufs);
                 if (!__all_sync(0xFFFFFFFFu, pair_wait(acc_full(b), (i / kAccBufs) & 1u, limit_ns))) {
@@ -581,52 +564,54 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 };
                 if constexpr (OP == kInt8) {
 #pragma unroll
-                    for (int c = 0; c < kSpan; c += 32) {
-                        uint32_t v[32];
-                        tmem_ld32(tq + c, v);
+                    for (int c = 0; c < kSpan; c += kBlock) {
+                        uint32_t v[16];
+                        gemm::tmem_ld16(tq + c, v);
 #pragma unroll
-                        for (int q = 0; q < 32; ++q) {
+                        for (int q = 0; q < 16; ++q) {
                             const int32_t a = __float2int_rn(__uint_as_float(v[q]));
                             acc[c + q] = kc == 0 ? a : acc[c + q] + a;
                         }
                     }
                     release();
                 } else {
-#pragma unroll (kStored ? kSpan / 32 : 1)
-                    for (int c = 0; c < kSpan; c += 32) {
-                        uint32_t v[32];
-                        const bool have = c_lo + c < c_hi;      // the same for the whole warp
-                        if (have) tmem_ld32(tq + c, v);
-                        if (c + 32 == kSpan) release();
+#pragma unroll (kStored ? kSpan / kBlock : 1)
+                    for (int c = 0; c < kSpan; c += kBlock) {
+                        uint32_t v[16], p[16];
+                        const bool have = static_cast<uint32_t>(c) < cols;
+                        if constexpr (OP == kParam)
+                            if (P.vec && have && row < P.m)
+                                load_params(P, P.slot[it.z].ptr, static_cast<uint64_t>(row) * P.out_ld + col0 + c, p);
+                        if (have) gemm::tmem_ld16(tq + c, v);
+                        if (c + kBlock == kSpan) release();
                         if (!have) continue;
-                        float x[32];
-#pragma unroll
-                        for (int q = 0; q < 32; ++q) x[q] = __uint_as_float(v[q]);
                         if constexpr (kStored) {
-                            store_stored<OP>(P, it, row, it.n0 + c_lo + c, x, stage, lane);
-                        } else if (row - lane < P.m) {
+                            store_stored<OP>(P, it, row, col0 + c, v, prior + (OP == kPoly ? c / 2 : 0), stage, lane);
+                        } else {
+                            float x[16];
 #pragma unroll
-                            for (int q = 0; q < 32; ++q) stage[lane * kPitch + q] = x[q];
-                            __syncwarp();
-                            finish_block<OP>(P, it.z, row - lane, it.n0 + c_lo + c, stage);
+                            for (int q = 0; q < 16; ++q) x[q] = __uint_as_float(v[q]);
+                            finish_block<OP>(P, it.z, row, col0 + c, x, p, nullptr, stage, lane);
                         }
                     }
                 }
             }
             if constexpr (OP == kInt8) {
-                if (ok && row - lane < P.m) {
-                    // one copy of the finishing code for the four blocks
+                if (ok) {
+                    // one copy of the finishing code for the warp's blocks
 #pragma unroll 1
-                    for (int c = 0; c < kSpan; c += 32) {
-                        if (c_lo + c >= c_hi) break;
+                    for (int c = 0; static_cast<uint32_t>(c) < cols; c += kBlock) {
+                        float x[16], cs[16];
 #pragma unroll
-                        for (int d = 0; d < kSpan; d += 32) {
+                        for (int d = 0; d < kSpan; d += kBlock) {
                             if (c != d) continue;
 #pragma unroll
-                            for (int q = 0; q < 32; ++q) stage[lane * kPitch + q] = __int2float_rn(acc[d + q]);
+                            for (int q = 0; q < 16; ++q) {
+                                x[q] = __int2float_rn(acc[d + q]);
+                                cs[q] = __shfl_sync(0xFFFFFFFFu, scale[d / 32], (d & 31) + q);
+                            }
                         }
-                        __syncwarp();
-                        finish_block<OP>(P, it.z, row - lane, it.n0 + c_lo + c, stage);
+                        finish_block<OP>(P, 0, row, col0 + c, x, nullptr, cs, stage, lane);
                     }
                 }
             }
