@@ -62,33 +62,26 @@ __global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__
     widen_block(P, blockIdx.x, gridDim.x);
 }
 
-__device__ __forceinline__ uint4 pack8(const float x[8])
+__device__ __forceinline__ void store_int8(int8_t *dst, const int q[8], int live)
 {
-    return make_uint4(prod::pack_f16(x[0], x[1]), prod::pack_f16(x[2], x[3]), prod::pack_f16(x[4], x[5]),
-                      prod::pack_f16(x[6], x[7]));
-}
-
-__device__ __forceinline__ void store_int8(int8_t *dst, const float x[8], int live)
-{
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-        w[q >> 2] |= static_cast<uint32_t>(__float2int_rn(x[q]) & 0xFF) << (8 * (q & 3));
+    const uint32_t w[2] = {__byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410),
+                           __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410)};
     if (live == 8 && (reinterpret_cast<uintptr_t>(dst) & 7u) == 0) {
         *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
     } else {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            if (q < live) dst[q] = static_cast<int8_t>(w[q >> 2] >> (8 * (q & 3)));
+        for (int i = 0; i < 8; ++i)
+            if (i < live) dst[i] = static_cast<int8_t>(w[i >> 2] >> (8 * (i & 3)));
     }
 }
 
 // How a row's values become integers: y = (x * pre) * inv.  A row whose largest
 // value is so small that 127 / max would overflow is raised by 2^64 first (exact);
 // a row that holds an infinity or a NaN gives zeros, and its scale, not finite,
-// marks every product of the row.
+// marks every product of the row.  Both are rare, and `odd` sets them apart.
 struct Levels {
     float pre, inv;
+    bool odd;
 };
 
 __device__ __forceinline__ Levels levels_of(float top)
@@ -96,23 +89,54 @@ __device__ __forceinline__ Levels levels_of(float top)
     Levels L;
     L.pre = top < 0x1p-64f ? 0x1p64f : 1.0f;
     L.inv = top > 0.0f && top <= 3.402823466e38f ? __fdiv_rn(127.0f, __fmul_rn(top, L.pre)) : 0.0f;
+    L.odd = L.inv == 0.0f || L.pre != 1.0f;
     return L;
 }
 
-// The integer of x, as a float.
-template <bool SR>
-__device__ __forceinline__ float quantise(float x, const Levels &L, uint32_t r)
+__device__ __forceinline__ float regular(float x, const Levels &L) { return L.inv == 0.0f ? 0.0f : __fmul_rn(x, L.pre); }
+
+// The integer of x (made regular).  |y| <= 127 (1 + 2^-23), so that the nearest
+// is at most 127, and the sum with 1.5 * 2^23 has it in its low bits.
+__device__ __forceinline__ int to_nearest(float x, const Levels &L)
 {
-    const float y = __fmul_rn(__fmul_rn(x, L.pre), L.inv);
-    float q;
-    if (!SR) {
-        q = rintf(y);                           // |y| <= 127 (1 + 2^-23): rounds to at most 127
-    } else {
-        const float low = floorf(y);
-        q = low + (__fmul_rn(__fsub_rn(y, low), 65536.0f) > static_cast<float>(r & 0xFFFFu) ? 1.0f : 0.0f);
-        q = fmaxf(-127.0f, fminf(127.0f, q));
+    return __float_as_int(__fadd_rn(__fmul_rn(x, L.inv), 12582912.0f)) - 0x4B400000;
+}
+
+// floor(y) + [65536 (y - floor(y)) > r] for whole r in [0, 65535] is
+// floor((ceil(65536 y) + 65535 - r) / 65536), and scaling by 65536 is exact.
+// not_r: its low 16 bits are 65535 - r.
+__device__ __forceinline__ int to_random(float x, const Levels &L, uint32_t not_r)
+{
+    const int up = __float2int_ru(__fmul_rn(x, __fmul_rn(L.inv, 65536.0f)));
+    return max(-127, min(127, (up + static_cast<int>(not_r & 0xFFFFu)) >> 16));
+}
+
+// Two integers as f16: 1,024 + (q + 128) in the bits, less 1,152.
+__device__ __forceinline__ uint32_t half2_of(int lo, int hi)
+{
+    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    const uint32_t a = __byte_perm(static_cast<uint32_t>(lo + 0x6480), static_cast<uint32_t>(hi + 0x6480), 0x5410);
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), bias);
+    return *reinterpret_cast<const uint32_t *>(&x);
+}
+
+__device__ __forceinline__ uint4 halves_of(const int q[8])
+{
+    return make_uint4(half2_of(q[0], q[1]), half2_of(q[2], q[3]), half2_of(q[4], q[5]), half2_of(q[6], q[7]));
+}
+
+template <bool SR>
+__device__ __forceinline__ void quantise8(const float x[8], const Levels &L, const uint32_t not_r[8], int q[8])
+{
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = x[i];
+    if (L.odd) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = regular(x[i], L);
     }
-    return L.inv == 0.0f ? 0.0f : q;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = SR ? to_random(v[i], L, not_r[i]) : to_nearest(v[i], L);
 }
 
 __device__ __forceinline__ uint32_t absbits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
@@ -127,10 +151,13 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *part)
     return v;
 }
 
+// The complements of the random words of elements e .. e+7.
 __device__ __forceinline__ void words8(uint64_t base, uint64_t e, uint32_t step, const RoundKeys &K, uint32_t r[8])
 {
     if (((base + e) & 3u) == 0) unit_words<true>(base, e, step, K, r);
     else unit_words<false>(base, e, step, K, r);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) r[q] = ~r[q];
 }
 
 struct RowParams {
@@ -174,13 +201,10 @@ __global__ void __launch_bounds__(kThreads) quantise_rows_kernel(const __grid_co
             muon::load8(P.x, P.dtype, row * P.x_ld + col, live, P.vec, x);
             uint32_t r[8];
             if (SR) words8(P.base, row * P.cols + col, P.step, P.keys, r);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) x[q] = quantise<SR>(x[q], L, SR ? r[q] : 0u);
-            if (WIDE) {
-                *reinterpret_cast<uint4 *>(static_cast<__half *>(P.q) + row * P.q_ld + col) = pack8(x);
-            } else {
-                store_int8(static_cast<int8_t *>(P.q) + row * P.q_ld + col, x, live);
-            }
+            int v[8];
+            quantise8<SR>(x, L, r, v);
+            if (WIDE) *reinterpret_cast<uint4 *>(static_cast<__half *>(P.q) + row * P.q_ld + col) = halves_of(v);
+            else store_int8(static_cast<int8_t *>(P.q) + row * P.q_ld + col, v, live);
         }
         __syncthreads();
     }
@@ -203,10 +227,10 @@ struct FewPrepParams {
 };
 
 template <bool DOTS>
-__device__ __forceinline__ void store_few(void *row, uint64_t col, const float x[8])
+__device__ __forceinline__ void store_few(void *row, uint64_t col, const int q[8])
 {
-    if (DOTS) store_int8(static_cast<int8_t *>(row) + col, x, 8);
-    else *reinterpret_cast<uint4 *>(static_cast<__half *>(row) + col) = pack8(x);
+    if (DOTS) store_int8(static_cast<int8_t *>(row) + col, q, 8);
+    else *reinterpret_cast<uint4 *>(static_cast<__half *>(row) + col) = halves_of(q);
 }
 
 template <bool DOTS>
@@ -224,9 +248,9 @@ __global__ void __launch_bounds__(kPrepThreads) few_prep_kernel(const __grid_con
     if (!P.scale) {
         const int8_t *src = static_cast<const int8_t *>(P.x) + row * P.x_ld;
         for (uint64_t col = threadIdx.x * 8ull; col < P.out_ld; col += kPrepThreads * 8ull) {
-            float x[8];
+            int x[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) x[q] = col + q < P.cols ? static_cast<float>(src[col + q]) : 0.0f;
+            for (int q = 0; q < 8; ++q) x[q] = col + q < P.cols ? src[col + q] : 0;
             store_few<DOTS>(out, col, x);
         }
         return;
@@ -259,24 +283,24 @@ __global__ void __launch_bounds__(kPrepThreads) few_prep_kernel(const __grid_con
 #pragma unroll
     for (int u = 0; u < kFewUnits; ++u) {
         const uint64_t col = (u * kPrepThreads + threadIdx.x) * 8ull;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) x[u][q] = quantise<false>(x[u][q], L, 0u);
-        if (col < P.out_ld) store_few<DOTS>(out, col, x[u]);
+        int q[8];
+        quantise8<false>(x[u], L, nullptr, q);
+        if (col < P.out_ld) store_few<DOTS>(out, col, q);
     }
     for (uint64_t col = (kFewUnits * kPrepThreads + threadIdx.x) * 8ull; col < P.out_ld; col += kPrepThreads * 8ull) {
         float v[8];
         fetch(col, v);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = quantise<false>(v[q], L, 0u);
-        store_few<DOTS>(out, col, v);
+        int q[8];
+        quantise8<false>(v, L, nullptr, q);
+        store_few<DOTS>(out, col, q);
     }
 }
 
 // Maxima along columns, or along both, of up to three matrices in one launch:
-// blocks of kTileRows x 256, a warp every eighth row, eight columns a lane.
-// `row_max` and `col_max` hold bits of non-negative floats, zero at the start;
-// integer maxima are the same whatever their order.
-constexpr int kTileRows = 64;
+// blocks of 8 * `deep` rows x 256 columns, a warp `deep` rows, eight columns a
+// lane.  `row_max` and `col_max` hold bits of non-negative floats, zero at the
+// start; integer maxima are the same whatever their order.
+constexpr int kDeep = 32;                       // rows a warp, at most, eight loads ahead
 
 struct Side {
     const void *x;
@@ -292,7 +316,7 @@ struct Side {
 
 struct SideParams {
     Side s[3];
-    uint32_t count, blocks;
+    uint32_t count, blocks, deep;
     uint32_t step;
     RoundKeys keys;
 };
@@ -304,40 +328,69 @@ __device__ __forceinline__ const Side &side_of(const SideParams &P, uint32_t blo
 
 __global__ void __launch_bounds__(kThreads) max_kernel(const __grid_constant__ SideParams P)
 {
-    __shared__ uint32_t part[8][256];
+    __shared__ uint32_t part[8][8 * 33];
     const Side &S = side_of(P, blockIdx.x);
     const uint32_t tile = blockIdx.x - S.first, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint64_t r0 = static_cast<uint64_t>(tile / S.tiles_x) * kTileRows;
+    const uint64_t r0 = (static_cast<uint64_t>(tile / S.tiles_x) * 8 + warp) * P.deep;
     const uint64_t c0 = static_cast<uint64_t>(tile % S.tiles_x) * 256, col = c0 + lane * 8;
     const int live = col >= S.cols ? 0 : S.cols - col < 8 ? static_cast<int>(S.cols - col) : 8;
+    const uint32_t rows = r0 >= S.rows ? 0 : S.rows - r0 < P.deep ? static_cast<uint32_t>(S.rows - r0) : P.deep;
     uint32_t top[8] = {};
-#pragma unroll 4
-    for (int i = 0; i < kTileRows / 8; ++i) {
-        const uint64_t row = r0 + i * 8 + warp;
-        if (row >= S.rows) break;
-        uint32_t most = 0;
-        if (live) {
-            float x[8];
-            muon::load8(S.x, S.dtype, row * S.x_ld + col, live, S.vec, x);
+    const bool packed = S.dtype == ASR_BF16 && S.vec && live == 8;      // the first lanes of a warp, or none
+    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, packed);
+    if (packed) {
+        // two values a word: sixteen-bit maxima of the bits without signs
+        const uint16_t *p = static_cast<const uint16_t *>(S.x) + r0 * S.x_ld + col;
+        uint32_t t[4] = {};
+        for (uint32_t i0 = 0; i0 < rows; i0 += 8) {
+            uint4 w[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const uint32_t b = absbits(x[q]);
-                top[q] = max(top[q], b);
-                most = max(most, b);
+            for (uint32_t i = 0; i < 8; ++i)
+                w[i] = i0 + i < rows ? *reinterpret_cast<const uint4 *>(p + (i0 + i) * S.x_ld) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) {
+                const uint32_t a[4] = {w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu, w[i].z & 0x7FFF7FFFu,
+                                       w[i].w & 0x7FFF7FFFu};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) t[q] = __vmaxu2(t[q], a[q]);
+                if (S.row_max && i0 + i < rows) {
+                    uint32_t most = __vmaxu2(__vmaxu2(a[0], a[1]), __vmaxu2(a[2], a[3]));
+                    most = max(most << 16, most & 0xFFFF0000u);
+                    most = __reduce_max_sync(mask, most);
+                    if (lane == 0) atomicMax(S.row_max + r0 + i0 + i, most);
+                }
             }
         }
-        if (S.row_max) {
-            most = __reduce_max_sync(0xFFFFFFFFu, most);
-            if (lane == 0) atomicMax(S.row_max + row, most);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) top[2 * q] = t[q] << 16, top[2 * q + 1] = t[q] & 0xFFFF0000u;
+    } else {
+        for (uint32_t i = 0; i < rows; ++i) {
+            uint32_t most = 0;
+            if (live) {
+                float x[8];
+                muon::load8(S.x, S.dtype, (r0 + i) * S.x_ld + col, live, S.vec, x);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const uint32_t b = absbits(x[q]);
+                    top[q] = max(top[q], b);
+                    most = max(most, b);
+                }
+            }
+            if (S.row_max) {
+                most = __reduce_max_sync(~mask, most);
+                if (lane == static_cast<uint32_t>(__ffs(~mask) - 1)) atomicMax(S.row_max + r0 + i, most);
+            }
         }
     }
+    __syncwarp();
 #pragma unroll
-    for (int q = 0; q < 8; ++q) part[warp][q * 32 + lane] = top[q];     // column lane * 8 + q
+    for (int q = 0; q < 8; ++q) part[warp][q * 33 + lane] = top[q];     // column lane * 8 + q
     __syncthreads();
-    uint32_t v = part[0][threadIdx.x];
+    const uint32_t at = (threadIdx.x & 7) * 33 + (threadIdx.x >> 3);
+    uint32_t v = part[0][at];
 #pragma unroll
-    for (int w = 1; w < 8; ++w) v = max(v, part[w][threadIdx.x]);
-    const uint64_t c = c0 + (threadIdx.x & 31) * 8 + (threadIdx.x >> 5);
+    for (int w = 1; w < 8; ++w) v = max(v, part[w][at]);
+    const uint64_t c = c0 + threadIdx.x;
     if (c < S.cols) atomicMax(S.col_max + c, v);
 }
 
@@ -345,44 +398,74 @@ __global__ void __launch_bounds__(kThreads) max_kernel(const __grid_constant__ S
 // products read them across): side 0 (dy) stochastically, by its rows' and by
 // its columns' maxima with the same random bits; the others to nearest, by
 // columns.  The first tiles write the scales.
-__global__ void __launch_bounds__(kThreads) wide_kernel(const __grid_constant__ SideParams P)
+__global__ void __launch_bounds__(kThreads, 4) wide_kernel(const __grid_constant__ SideParams P)
 {
     const Side &S = side_of(P, blockIdx.x);
     const uint32_t tile = blockIdx.x - S.first, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint64_t r0 = static_cast<uint64_t>(tile / S.tiles_x) * kTileRows;
+    const uint64_t t0 = static_cast<uint64_t>(tile / S.tiles_x) * 8 * P.deep, r0 = t0 + warp * P.deep;
     const uint64_t c0 = static_cast<uint64_t>(tile % S.tiles_x) * 256, col = c0 + lane * 8;
     const int live = col >= S.cols ? 0 : S.cols - col < 8 ? static_cast<int>(S.cols - col) : 8;
-    if (r0 == 0 && c0 + threadIdx.x < S.cols)
+    if (t0 == 0 && c0 + threadIdx.x < S.cols)
         S.col_scale[c0 + threadIdx.x] = __fdiv_rn(__uint_as_float(S.col_max[c0 + threadIdx.x]), 127.0f);
-    if (S.row_max && c0 == 0 && threadIdx.x < kTileRows && r0 + threadIdx.x < S.rows)
-        S.row_scale[r0 + threadIdx.x] = __fdiv_rn(__uint_as_float(S.row_max[r0 + threadIdx.x]), 127.0f);
+    if (S.row_max && c0 == 0 && threadIdx.x < 8 * P.deep && t0 + threadIdx.x < S.rows)
+        S.row_scale[t0 + threadIdx.x] = __fdiv_rn(__uint_as_float(S.row_max[t0 + threadIdx.x]), 127.0f);
     if (!live) return;
     Levels L[8];
+    bool odd = false;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) L[q] = levels_of(q < live ? __uint_as_float(S.col_max[col + q]) : 0.0f);
-    for (int i = 0; i < kTileRows / 8; ++i) {
-        const uint64_t row = r0 + i * 8 + warp;
-        if (row >= S.rows) break;
-        float x[8], y[8];
-        muon::load8(S.x, S.dtype, row * S.x_ld + col, live, S.vec, x);
+    for (int q = 0; q < 8; ++q) {
+        L[q] = levels_of(q < live ? __uint_as_float(S.col_max[col + q]) : 0.0f);
+        odd |= L[q].odd && q < live;
+    }
+    const uint64_t end = r0 + P.deep < S.rows ? r0 + P.deep : S.rows;
+    auto one = [&](uint64_t row, const float x0[8]) {
+        float x[8];
+        int v[8];
+        uint32_t r[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[q] = x0[q];
         if (S.row_max) {
-            uint32_t r[8];
             words8(0, row * S.cols + col, P.step, P.keys, r);
-            const Levels R = levels_of(__uint_as_float(S.row_max[row]));
             if (S.by_row) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q) y[q] = quantise<true>(x[q], R, r[q]);
-                *reinterpret_cast<uint4 *>(S.by_row + row * S.q_ld + col) = pack8(y);
+                quantise8<true>(x, levels_of(__uint_as_float(S.row_max[row])), r, v);
+                *reinterpret_cast<uint4 *>(S.by_row + row * S.q_ld + col) = halves_of(v);
             }
-            if (S.by_col) {
+        }
+        if (!S.by_col) return;
+        if (odd) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) y[q] = quantise<true>(x[q], L[q], r[q]);
-                *reinterpret_cast<uint4 *>(S.by_col + row * S.q_ld + col) = pack8(y);
-            }
+            for (int q = 0; q < 8; ++q) x[q] = regular(x[q], L[q]);
+        }
+        if (S.row_max) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = to_random(x[q], L[q], r[q]);
         } else {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) y[q] = quantise<false>(x[q], L[q], 0u);
-            *reinterpret_cast<uint4 *>(S.by_col + row * S.q_ld + col) = pack8(y);
+            for (int q = 0; q < 8; ++q) v[q] = to_nearest(x[q], L[q]);
+        }
+        // past the last column: zeros (their loads gave zeros)
+        *reinterpret_cast<uint4 *>(S.by_col + row * S.q_ld + col) = halves_of(v);
+    };
+    if (S.dtype == ASR_BF16 && S.vec && live == 8) {
+        const uint16_t *p = static_cast<const uint16_t *>(S.x) + col;
+        for (uint64_t row = r0; row < end; row += 4) {
+            uint4 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = row + i < end ? *reinterpret_cast<const uint4 *>(p + (row + i) * S.x_ld) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (row + i >= end) break;
+                const float x[8] = {bf16_lo(w[i].x), bf16_hi(w[i].x), bf16_lo(w[i].y), bf16_hi(w[i].y),
+                                    bf16_lo(w[i].z), bf16_hi(w[i].z), bf16_lo(w[i].w), bf16_hi(w[i].w)};
+                one(row + i, x);
+            }
+        }
+    } else {
+        for (uint64_t row = r0; row < end; ++row) {
+            float x[8];
+            muon::load8(S.x, S.dtype, row * S.x_ld + col, live, S.vec, x);
+            one(row, x);
         }
     }
 }
@@ -418,8 +501,10 @@ __global__ void __launch_bounds__(kThreads) quantise_columns_kernel(const __grid
         uint32_t r[8];
         if (SR) words8(P.base, row * P.cols + col, P.step, P.keys, r);
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            tile[(threadIdx.x & 7) * 8 + q][tr] = static_cast<int8_t>(__float2int_rn(quantise<SR>(x[q], L[q], SR ? r[q] : 0u)));
+        for (int q = 0; q < 8; ++q) {
+            const float v = regular(x[q], L[q]);
+            tile[(threadIdx.x & 7) * 8 + q][tr] = static_cast<int8_t>(SR ? to_random(v, L[q], r[q]) : to_nearest(v, L[q]));
+        }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < 64 * 64; i += kThreads) {
@@ -448,10 +533,10 @@ bool pitch_ok(uint64_t ld, uint64_t least) { return ld >= least && ld <= (1ull <
 bool quantisable(uint64_t rows, uint64_t cols)
 {
     return rows <= (1u << 30) && cols <= (1u << 30) &&
-           ((rows + kTileRows - 1) / kTileRows) * ((cols + 255) / 256) < (1ull << 28);
+           ((rows + 7) / 8) * ((cols + 255) / 256) < (1ull << 28);
 }
 
-Side side(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t first)
+Side side(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, uint64_t ld)
 {
     Side S;
     std::memset(&S, 0, sizeof(S));
@@ -462,13 +547,22 @@ Side side(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, uint64_t l
     S.vec = muon::units_aligned(x, ld, 0);
     S.dtype = static_cast<uint32_t>(dtype);
     S.tiles_x = static_cast<uint32_t>((cols + 255) / 256);
-    S.first = first;
     return S;
 }
 
-uint32_t side_blocks(const Side &S)
+// Lays the sides' blocks end to end: as many rows a warp as leave the GPU full
+// (four blocks an SM).
+void lay_out(SideParams &M)
 {
-    return static_cast<uint32_t>((S.rows + kTileRows - 1) / kTileRows) * S.tiles_x;
+    for (M.deep = kDeep;; M.deep /= 2) {
+        M.blocks = 0;
+        for (uint32_t i = 0; i < M.count; ++i) {
+            Side &S = M.s[i];
+            S.first = M.blocks;
+            M.blocks += static_cast<uint32_t>((S.rows + 8 * M.deep - 1) / (8 * M.deep)) * S.tiles_x;
+        }
+        if (M.blocks >= 608 || M.deep == 1) return;
+    }
 }
 
 asr_status quantize(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, uint64_t x_ld, int32_t axis, int8_t *q,
@@ -510,10 +604,11 @@ asr_status quantize(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, 
     if (e != cudaSuccess) return cuda_fail(e);
     SideParams M;
     std::memset(&M, 0, sizeof(M));
-    M.s[0] = side(x, dtype, rows, cols, x_ld, 0);
+    M.s[0] = side(x, dtype, rows, cols, x_ld);
     M.s[0].col_max = reinterpret_cast<uint32_t *>(scale);
     M.count = 1;
-    max_kernel<<<side_blocks(M.s[0]), kThreads, 0, stream>>>(M);
+    lay_out(M);
+    max_kernel<<<M.blocks, kThreads, 0, stream>>>(M);
     asr_status st = launched(ASR_KERNEL_QUANTIZE);
     if (st != ASR_OK) return st;
     ColumnParams P;
@@ -832,7 +927,7 @@ asr_status grads(const GradSource &dy, const GradSource &x, const GradSource &w,
     M.step = step;
     M.keys = make_keys(seed);
     Side &D = M.s[M.count++];
-    D = side(dy.p, dy.dtype, t, n, dy.ld, 0);
+    D = side(dy.p, dy.dtype, t, n, dy.ld);
     D.row_max = words(L.max_row);
     D.col_max = words(L.max_dy);
     D.row_scale = floats(L.row);
@@ -840,25 +935,23 @@ asr_status grads(const GradSource &dy, const GradSource &x, const GradSource &w,
     D.by_row = dx ? halves(L.dy_row) : nullptr;
     D.by_col = dw ? halves(L.dy_col) : nullptr;
     D.q_ld = L.ldn;
-    M.blocks = side_blocks(D);
     if (dx) {
         Side &W = M.s[M.count++];
-        W = side(w.p, w.dtype, n, k, w.ld, M.blocks);
+        W = side(w.p, w.dtype, n, k, w.ld);
         W.col_max = words(L.max_w);
         W.col_scale = floats(L.col_w);
         W.by_col = halves(L.w);
         W.q_ld = L.ldk;
-        M.blocks += side_blocks(W);
     }
     if (dw) {
         Side &X = M.s[M.count++];
-        X = side(x.p, x.dtype, t, k, x.ld, M.blocks);
+        X = side(x.p, x.dtype, t, k, x.ld);
         X.col_max = words(L.max_x);
         X.col_scale = floats(L.col_x);
         X.by_col = halves(L.x);
         X.q_ld = L.ldk;
-        M.blocks += side_blocks(X);
     }
+    lay_out(M);
     max_kernel<<<M.blocks, kThreads, 0, stream>>>(M);
     st = launched(ASR_KERNEL_QUANTIZE);
     if (st != ASR_OK) return st;
