@@ -16,3 +16,4 @@ from ._lib import (  # noqa: F401
 )
 from .int8 import Int8Linear, int8_linear, int8_linear_grads  # noqa: F401,E402
 from .optim import AdamWSR, DeviceError  # noqa: F401,E402
+from .muon import MuonSR  # noqa: F401,E402

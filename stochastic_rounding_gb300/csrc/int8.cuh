@@ -62,19 +62,6 @@ __global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__
     widen_block(P, blockIdx.x, gridDim.x);
 }
 
-__device__ __forceinline__ void store_int8(int8_t *dst, const int q[8], int live)
-{
-    const uint32_t w[2] = {__byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410),
-                           __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410)};
-    if (live == 8 && (reinterpret_cast<uintptr_t>(dst) & 7u) == 0) {
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < live) dst[i] = static_cast<int8_t>(w[i >> 2] >> (8 * (i & 3)));
-    }
-}
-
 // How a row's values become integers: y = (x * pre) * inv.  A row whose largest
 // value is so small that 127 / max would overflow is raised by 2^64 first (exact);
 // a row that holds an infinity or a NaN gives zeros, and its scale, not finite,
@@ -95,38 +82,61 @@ __device__ __forceinline__ Levels levels_of(float top)
 
 __device__ __forceinline__ float regular(float x, const Levels &L) { return L.inv == 0.0f ? 0.0f : __fmul_rn(x, L.pre); }
 
-// The integer of x (made regular).  |y| <= 127 (1 + 2^-23), so that the nearest
-// is at most 127, and the sum with 1.5 * 2^23 has it in its low bits.
-__device__ __forceinline__ int to_nearest(float x, const Levels &L)
+// Integers come in pairs, as 0x6480 + q in each half of a word: as f16 that is
+// 1,152 + q.
+//
+// To nearest: |y| <= 127 (1 + 2^-23), so that the nearest is at most 127, and
+// the sum with 1.5 * 2^23 + 0x6480 has it in its low half.
+__device__ __forceinline__ uint32_t nearest2(float x, float y, float inv_x, float inv_y)
 {
-    return __float_as_int(__fadd_rn(__fmul_rn(x, L.inv), 12582912.0f)) - 0x4B400000;
+    constexpr float kMagic = 12582912.0f + 25728.0f;
+    return __byte_perm(__float_as_uint(__fadd_rn(__fmul_rn(x, inv_x), kMagic)),
+                       __float_as_uint(__fadd_rn(__fmul_rn(y, inv_y), kMagic)), 0x5410);
 }
 
-// floor(y) + [65536 (y - floor(y)) > r] for whole r in [0, 65535] is
-// floor((ceil(65536 y) + 65535 - r) / 65536), and scaling by 65536 is exact.
-// not_r: its low 16 bits are 65535 - r.
-__device__ __forceinline__ int to_random(float x, const Levels &L, uint32_t not_r)
+// Stochastically: floor(y) + [65536 (y - floor(y)) > r] for whole r in [0, 65535]
+// is floor((ceil(65536 y) + 65535 - r) / 65536), the sum's high half.  The scales
+// come times 65536 (exact); not_r is 65535 - r.  |q| may come to 128.
+__device__ __forceinline__ uint32_t random2(float x, float y, float inv_x, float inv_y, uint32_t not_r, uint32_t not_s)
 {
-    const int up = __float2int_ru(__fmul_rn(x, __fmul_rn(L.inv, 65536.0f)));
-    return max(-127, min(127, (up + static_cast<int>(not_r & 0xFFFFu)) >> 16));
+    const uint32_t a = static_cast<uint32_t>(__float2int_ru(__fmul_rn(x, inv_x))) + not_r + 0x64800000u;
+    const uint32_t b = static_cast<uint32_t>(__float2int_ru(__fmul_rn(y, inv_y))) + not_s + 0x64800000u;
+    return __vmaxu2(__vminu2(__byte_perm(a, b, 0x7632), 0x64FF64FFu), 0x64016401u);
 }
 
-// Two integers as f16: 1,024 + (q + 128) in the bits, less 1,152.
-__device__ __forceinline__ uint32_t half2_of(int lo, int hi)
+// Eight of them as f16, or as bytes.
+__device__ __forceinline__ uint4 halves_of(const uint32_t e[4])
 {
     const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-    const uint32_t a = __byte_perm(static_cast<uint32_t>(lo + 0x6480), static_cast<uint32_t>(hi + 0x6480), 0x5410);
-    const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), bias);
-    return *reinterpret_cast<const uint32_t *>(&x);
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&e[i]), bias);
+        h[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
-__device__ __forceinline__ uint4 halves_of(const int q[8])
+__device__ __forceinline__ uint2 bytes_of(const uint32_t e[4])
 {
-    return make_uint4(half2_of(q[0], q[1]), half2_of(q[2], q[3]), half2_of(q[4], q[5]), half2_of(q[6], q[7]));
+    return make_uint2(__byte_perm(e[0], e[1], 0x6420) ^ 0x80808080u, __byte_perm(e[2], e[3], 0x6420) ^ 0x80808080u);
 }
 
+__device__ __forceinline__ void store_int8(int8_t *dst, const uint32_t e[4], int live)
+{
+    const uint2 w = bytes_of(e);
+    if (live == 8 && (reinterpret_cast<uintptr_t>(dst) & 7u) == 0) {
+        *reinterpret_cast<uint2 *>(dst) = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < live) dst[i] = static_cast<int8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+    }
+}
+
+// Eight values of one scale.
 template <bool SR>
-__device__ __forceinline__ void quantise8(const float x[8], const Levels &L, const uint32_t not_r[8], int q[8])
+__device__ __forceinline__ void quantise8(const float x[8], const Levels &L, const uint32_t not_r[8], uint32_t e[4])
 {
     float v[8];
 #pragma unroll
@@ -135,8 +145,11 @@ __device__ __forceinline__ void quantise8(const float x[8], const Levels &L, con
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = regular(x[i], L);
     }
+    const float inv = SR ? __fmul_rn(L.inv, 65536.0f) : L.inv;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = SR ? to_random(v[i], L, not_r[i]) : to_nearest(v[i], L);
+    for (int i = 0; i < 4; ++i)
+        e[i] = SR ? random2(v[2 * i], v[2 * i + 1], inv, inv, not_r[2 * i], not_r[2 * i + 1])
+                  : nearest2(v[2 * i], v[2 * i + 1], inv, inv);
 }
 
 __device__ __forceinline__ uint32_t absbits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
@@ -151,13 +164,13 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *part)
     return v;
 }
 
-// The complements of the random words of elements e .. e+7.
+// 65535 less the random words (their low halves) of elements e .. e+7.
 __device__ __forceinline__ void words8(uint64_t base, uint64_t e, uint32_t step, const RoundKeys &K, uint32_t r[8])
 {
     if (((base + e) & 3u) == 0) unit_words<true>(base, e, step, K, r);
     else unit_words<false>(base, e, step, K, r);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) r[q] = ~r[q];
+    for (int q = 0; q < 8; ++q) r[q] = ~r[q] & 0xFFFFu;
 }
 
 struct RowParams {
@@ -201,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) quantise_rows_kernel(const __grid_co
             muon::load8(P.x, P.dtype, row * P.x_ld + col, live, P.vec, x);
             uint32_t r[8];
             if (SR) words8(P.base, row * P.cols + col, P.step, P.keys, r);
-            int v[8];
+            uint32_t v[4];
             quantise8<SR>(x, L, r, v);
             if (WIDE) *reinterpret_cast<uint4 *>(static_cast<__half *>(P.q) + row * P.q_ld + col) = halves_of(v);
             else store_int8(static_cast<int8_t *>(P.q) + row * P.q_ld + col, v, live);
@@ -227,7 +240,7 @@ struct FewPrepParams {
 };
 
 template <bool DOTS>
-__device__ __forceinline__ void store_few(void *row, uint64_t col, const int q[8])
+__device__ __forceinline__ void store_few(void *row, uint64_t col, const uint32_t q[4])
 {
     if (DOTS) store_int8(static_cast<int8_t *>(row) + col, q, 8);
     else *reinterpret_cast<uint4 *>(static_cast<__half *>(row) + col) = halves_of(q);
@@ -248,10 +261,13 @@ __global__ void __launch_bounds__(kPrepThreads) few_prep_kernel(const __grid_con
     if (!P.scale) {
         const int8_t *src = static_cast<const int8_t *>(P.x) + row * P.x_ld;
         for (uint64_t col = threadIdx.x * 8ull; col < P.out_ld; col += kPrepThreads * 8ull) {
-            int x[8];
+            uint32_t e[4];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) x[q] = col + q < P.cols ? src[col + q] : 0;
-            store_few<DOTS>(out, col, x);
+            for (int q = 0; q < 4; ++q) {
+                const int lo = col + 2 * q < P.cols ? src[col + 2 * q] : 0, hi = col + 2 * q + 1 < P.cols ? src[col + 2 * q + 1] : 0;
+                e[q] = __byte_perm(static_cast<uint32_t>(lo + 0x6480), static_cast<uint32_t>(hi + 0x6480), 0x5410);
+            }
+            store_few<DOTS>(out, col, e);
         }
         return;
     }
@@ -283,14 +299,14 @@ __global__ void __launch_bounds__(kPrepThreads) few_prep_kernel(const __grid_con
 #pragma unroll
     for (int u = 0; u < kFewUnits; ++u) {
         const uint64_t col = (u * kPrepThreads + threadIdx.x) * 8ull;
-        int q[8];
+        uint32_t q[4];
         quantise8<false>(x[u], L, nullptr, q);
         if (col < P.out_ld) store_few<DOTS>(out, col, q);
     }
     for (uint64_t col = (kFewUnits * kPrepThreads + threadIdx.x) * 8ull; col < P.out_ld; col += kPrepThreads * 8ull) {
         float v[8];
         fetch(col, v);
-        int q[8];
+        uint32_t q[4];
         quantise8<false>(v, L, nullptr, q);
         store_few<DOTS>(out, col, q);
     }
@@ -409,40 +425,43 @@ __global__ void __launch_bounds__(kThreads, 4) wide_kernel(const __grid_constant
         S.col_scale[c0 + threadIdx.x] = __fdiv_rn(__uint_as_float(S.col_max[c0 + threadIdx.x]), 127.0f);
     if (S.row_max && c0 == 0 && threadIdx.x < 8 * P.deep && t0 + threadIdx.x < S.rows)
         S.row_scale[t0 + threadIdx.x] = __fdiv_rn(__uint_as_float(S.row_max[t0 + threadIdx.x]), 127.0f);
+    // the block's rows' levels, once
+    __shared__ Levels by_row[8 * kDeep];
+    if (S.row_max && threadIdx.x < 8 * P.deep && t0 + threadIdx.x < S.rows)
+        by_row[threadIdx.x] = levels_of(__uint_as_float(S.row_max[t0 + threadIdx.x]));
+    __syncthreads();
     if (!live) return;
-    Levels L[8];
+    float inv[8];
     bool odd = false;
+    auto column = [&](int q) { return levels_of(q < live ? __uint_as_float(S.col_max[col + q]) : 0.0f); };
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-        L[q] = levels_of(q < live ? __uint_as_float(S.col_max[col + q]) : 0.0f);
-        odd |= L[q].odd && q < live;
+        const Levels L = column(q);
+        inv[q] = S.row_max ? __fmul_rn(L.inv, 65536.0f) : L.inv;
+        odd |= L.odd && q < live;
     }
     const uint64_t end = r0 + P.deep < S.rows ? r0 + P.deep : S.rows;
     auto one = [&](uint64_t row, const float x0[8]) {
         float x[8];
-        int v[8];
-        uint32_t r[8];
+        uint32_t v[4], r[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) x[q] = x0[q];
         if (S.row_max) {
             words8(0, row * S.cols + col, P.step, P.keys, r);
             if (S.by_row) {
-                quantise8<true>(x, levels_of(__uint_as_float(S.row_max[row])), r, v);
+                quantise8<true>(x, by_row[row - t0], r, v);
                 *reinterpret_cast<uint4 *>(S.by_row + row * S.q_ld + col) = halves_of(v);
             }
         }
         if (!S.by_col) return;
         if (odd) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) x[q] = regular(x[q], L[q]);
+            for (int q = 0; q < 8; ++q) x[q] = regular(x[q], column(q));
         }
-        if (S.row_max) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = to_random(x[q], L[q], r[q]);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = to_nearest(x[q], L[q]);
-        }
+        for (int q = 0; q < 4; ++q)
+            v[q] = S.row_max ? random2(x[2 * q], x[2 * q + 1], inv[2 * q], inv[2 * q + 1], r[2 * q], r[2 * q + 1])
+                             : nearest2(x[2 * q], x[2 * q + 1], inv[2 * q], inv[2 * q + 1]);
         // past the last column: zeros (their loads gave zeros)
         *reinterpret_cast<uint4 *>(S.by_col + row * S.q_ld + col) = halves_of(v);
     };
@@ -500,11 +519,18 @@ __global__ void __launch_bounds__(kThreads) quantise_columns_kernel(const __grid
         muon::load8(P.x, P.dtype, row * P.x_ld + col, live, P.vec, x);
         uint32_t r[8];
         if (SR) words8(P.base, row * P.cols + col, P.step, P.keys, r);
+        uint32_t e[4];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const float v = regular(x[q], L[q]);
-            tile[(threadIdx.x & 7) * 8 + q][tr] = static_cast<int8_t>(SR ? to_random(v, L[q], r[q]) : to_nearest(v, L[q]));
-        }
+        for (int q = 0; q < 8; ++q) x[q] = regular(x[q], L[q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            e[q] = SR ? random2(x[2 * q], x[2 * q + 1], __fmul_rn(L[2 * q].inv, 65536.0f),
+                                __fmul_rn(L[2 * q + 1].inv, 65536.0f), r[2 * q], r[2 * q + 1])
+                      : nearest2(x[2 * q], x[2 * q + 1], L[2 * q].inv, L[2 * q + 1].inv);
+        const uint2 w = bytes_of(e);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            tile[(threadIdx.x & 7) * 8 + q][tr] = static_cast<int8_t>((q < 4 ? w.x : w.y) >> (8 * (q & 3)));
     }
     __syncthreads();
     for (int i = threadIdx.x; i < 64 * 64; i += kThreads) {

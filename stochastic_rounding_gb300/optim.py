@@ -47,55 +47,16 @@ class DeviceError(RuntimeError):
     and moments are partly updated and should be restored from a checkpoint."""
 
 
-class AdamWSR(torch.optim.Optimizer):
-    """AdamW with stochastic rounding of bf16 parameters.
+class _PlacedOptimizer(torch.optim.Optimizer):
+    """What the optimizers here share: the global positions of their parameters
+    and the reads of the device error bit (see the module notes)."""
 
-    Arguments follow ``torch.optim.AdamW`` (``lr``, ``betas``, ``eps``,
-    ``weight_decay``) plus ``seed`` (64-bit key of the rounding stream) and
-    ``rounding`` (``"sr"``, or ``"rne"`` for round-to-nearest-even, the
-    biased baseline), ``base_offset`` (global position of the first
-    parameter's element 0) and ``check_errors`` (when to read the device
-    error bit: ``True``, ``"deferred"`` or ``False``; see the module notes).
-    Parameters must be contiguous CUDA tensors of float32 or bfloat16;
-    gradients dense float32 or bfloat16.
-
-    ``torch.optim.AdamW``'s other keywords are taken so that code written for
-    it runs unchanged: ``foreach``, ``fused`` and ``capturable`` are accepted
-    and have no effect (every step is one fused launch per group);
-    ``amsgrad``, ``maximize`` and ``differentiable`` are accepted when False
-    and refused otherwise (the fused step implements neither variant).
-    """
-
-    def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
-                 weight_decay: float = 1e-2, amsgrad: bool = False, *, maximize: bool = False,
-                 foreach=None, capturable: bool = False, differentiable: bool = False, fused=None,
-                 seed: int = 0, rounding: str = "sr", base_offset: int = 0, check_errors=True):
-        for name, value in (("amsgrad", amsgrad), ("maximize", maximize), ("differentiable", differentiable)):
-            if value:
-                raise ValueError(f"AdamWSR does not support {name}=True")
-        if not 0.0 <= lr:
-            raise ValueError(f"Invalid learning rate: {lr}")
-        if not 0.0 <= eps:
-            raise ValueError(f"Invalid epsilon value: {eps}")
-        if not 0.0 <= betas[0] < 1.0:
-            raise ValueError(f"Invalid beta parameter at index 0: {betas[0]}")
-        if not 0.0 <= betas[1] < 1.0:
-            raise ValueError(f"Invalid beta parameter at index 1: {betas[1]}")
-        if not 0.0 <= weight_decay:
-            raise ValueError(f"Invalid weight_decay value: {weight_decay}")
-        if rounding not in ("sr", "rne"):
-            raise ValueError(f"rounding must be 'sr' or 'rne', not {rounding!r}")
-        if not 0 <= int(seed) < 2**64:
-            raise ValueError("seed must fit in 64 bits")
+    def _place(self, base_offset, check_errors):
         if not 0 <= int(base_offset) < 2**64:
             raise ValueError("base_offset must fit in 64 bits")
         self.base_offset = int(base_offset)
         self.check_errors = self._error_mode(check_errors)
         self._pending: Dict[torch.device, List[tuple]] = {}
-        defaults = dict(lr=lr, betas=tuple(betas), eps=eps, weight_decay=weight_decay,
-                        seed=int(seed), rounding=rounding, base_index=None)
-        super().__init__(params, defaults)
-        self._assign_positions()
 
     def _assign_positions(self):
         pos = self.base_offset
@@ -141,7 +102,7 @@ class AdamWSR(torch.optim.Optimizer):
                     bad.append((device, int(word.item())))
         if bad:
             device, bits = bad[0]
-            raise DeviceError(f"AdamWSR: device error bits {bits:#x} on {device} from an earlier step "
+            raise DeviceError(f"{type(self).__name__}: device error bits {bits:#x} on {device} from an earlier step "
                               "(a pipeline wait gave up; that step is incomplete)")
 
     def _queue_error_read(self, device):
@@ -158,6 +119,65 @@ class AdamWSR(torch.optim.Optimizer):
     def base_index(self, p: torch.Tensor) -> int:
         """Global parameter position of element 0 of ``p``."""
         return self._base[id(p)]
+
+    def _finish_step(self, devices, mode):
+        """The error reads of a step that has launched on these devices."""
+        if mode == "deferred":
+            for device in devices:
+                self._queue_error_read(device)
+        elif mode:
+            for device in devices:
+                bits = _lib.asr_take_device_error(device=device)
+                if bits:
+                    raise DeviceError(f"{type(self).__name__}.step: device error bits {bits:#x} on {device} "
+                                      "(a pipeline wait gave up; the step is incomplete)")
+
+
+class AdamWSR(_PlacedOptimizer):
+    """AdamW with stochastic rounding of bf16 parameters.
+
+    Arguments follow ``torch.optim.AdamW`` (``lr``, ``betas``, ``eps``,
+    ``weight_decay``) plus ``seed`` (64-bit key of the rounding stream) and
+    ``rounding`` (``"sr"``, or ``"rne"`` for round-to-nearest-even, the
+    biased baseline), ``base_offset`` (global position of the first
+    parameter's element 0) and ``check_errors`` (when to read the device
+    error bit: ``True``, ``"deferred"`` or ``False``; see the module notes).
+    Parameters must be contiguous CUDA tensors of float32 or bfloat16;
+    gradients dense float32 or bfloat16.
+
+    ``torch.optim.AdamW``'s other keywords are taken so that code written for
+    it runs unchanged: ``foreach``, ``fused`` and ``capturable`` are accepted
+    and have no effect (every step is one fused launch per group);
+    ``amsgrad``, ``maximize`` and ``differentiable`` are accepted when False
+    and refused otherwise (the fused step implements neither variant).
+    """
+
+    def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay: float = 1e-2, amsgrad: bool = False, *, maximize: bool = False,
+                 foreach=None, capturable: bool = False, differentiable: bool = False, fused=None,
+                 seed: int = 0, rounding: str = "sr", base_offset: int = 0, check_errors=True):
+        for name, value in (("amsgrad", amsgrad), ("maximize", maximize), ("differentiable", differentiable)):
+            if value:
+                raise ValueError(f"AdamWSR does not support {name}=True")
+        if not 0.0 <= lr:
+            raise ValueError(f"Invalid learning rate: {lr}")
+        if not 0.0 <= eps:
+            raise ValueError(f"Invalid epsilon value: {eps}")
+        if not 0.0 <= betas[0] < 1.0:
+            raise ValueError(f"Invalid beta parameter at index 0: {betas[0]}")
+        if not 0.0 <= betas[1] < 1.0:
+            raise ValueError(f"Invalid beta parameter at index 1: {betas[1]}")
+        if not 0.0 <= weight_decay:
+            raise ValueError(f"Invalid weight_decay value: {weight_decay}")
+        if rounding not in ("sr", "rne"):
+            raise ValueError(f"rounding must be 'sr' or 'rne', not {rounding!r}")
+        if not 0 <= int(seed) < 2**64:
+            raise ValueError("seed must fit in 64 bits")
+        self._place(base_offset, check_errors)
+        defaults = dict(lr=lr, betas=tuple(betas), eps=eps, weight_decay=weight_decay,
+                        seed=int(seed), rounding=rounding, base_index=None)
+        super().__init__(params, defaults)
+        self._assign_positions()
 
     _DTYPES = frozenset((torch.float32, torch.bfloat16))
 
@@ -220,15 +240,7 @@ class AdamWSR(torch.optim.Optimizer):
                     weight_decay=group["weight_decay"], step=step, seed=group["seed"],
                     rounding=group["rounding"], device=device)
                 devices.add(device)
-        if mode == "deferred":
-            for device in devices:
-                self._queue_error_read(device)
-        elif mode:
-            for device in devices:
-                bits = _lib.asr_take_device_error(device=device)
-                if bits:
-                    raise DeviceError(f"AdamWSR.step: device error bits {bits:#x} on {device} "
-                                      "(a pipeline wait gave up; the step is incomplete)")
+        self._finish_step(devices, mode)
         return loss
 
     def load_state_dict(self, state_dict):
