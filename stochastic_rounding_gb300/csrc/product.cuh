@@ -78,7 +78,8 @@ struct Slot {                       // one matrix of the stack: the caller's
 struct Params {
     uint32_t m, n, k, batch;
     uint32_t tiles_m, tiles_n, per_matrix;
-    uint32_t wide, narrow;          // work items: whole tiles, then halves of the last ones
+    uint32_t wide, narrow;          // work items: whole tiles, then parts of the last ones
+    uint32_t parts;                 // 1, 2 or 4: a narrow item is 256 / parts columns
     uint32_t chunk;                 // K slices per accumulation
     float alpha, beta, diag;
     uint32_t ld;                    // stored output (and S): elements between rows
@@ -173,19 +174,19 @@ template <bool SYM>
 __device__ __forceinline__ Item work_item(const Params &P, uint32_t t)
 {
     Item it;
-    uint32_t whole = t, half = 0;
+    uint32_t whole = t, part = 0;
     it.width = kTile;
     if (t >= P.wide) {
-        whole = P.wide + (t - P.wide) / 2;
-        half = (t - P.wide) & 1u;
-        it.width = kTile / 2;
+        whole = P.wide + (t - P.wide) / P.parts;
+        part = (t - P.wide) & (P.parts - 1);
+        it.width = kTile / P.parts;
     }
     it.z = whole / P.per_matrix;
     uint32_t mt, nt;
     if (SYM) triangle_coords(whole % P.per_matrix, mt, nt);
     else tile_coords(whole % P.per_matrix, P.tiles_m, P.tiles_n, mt, nt, kGroupM);
     it.m0 = mt * kTile;
-    it.n0 = nt * kTile + half * (kTile / 2);
+    it.n0 = nt * kTile + part * it.width;
     it.mirror = SYM && mt != nt;
     return it;
 }
@@ -361,7 +362,7 @@ __device__ __forceinline__ void finish_block(const Params &P, uint32_t z, uint32
 template <bool A_MN, bool B_MN, int OP>
 __global__ void __launch_bounds__(kThreads, 1)
 product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-               const __grid_constant__ CUtensorMap map_b_half, const __grid_constant__ Params P, uint64_t limit_ns)
+               const __grid_constant__ CUtensorMap map_b_part, const __grid_constant__ Params P, uint64_t limit_ns)
 {
     constexpr bool kSym = OP == kGram || OP == kPoly;
     extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -417,13 +418,15 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         const uint32_t full0 = peer_addr(full(0), 0);
         for (uint32_t t = cluster; ok && t < items; t += clusters) {
             const Item it = work_item<kSym>(P, t);
-            const bool half = it.width != kTile;
+            const bool narrow = it.width != kTile;
             uint32_t ra = it.m0 + rank * 128, rb = it.n0 + rank * (it.width / 2);
             // rows wholly past the matrix: any rows do, their sums are not stored
             const bool a2 = ra + 64 < P.m, b2 = rb + 64 < P.n;
             if (ra >= P.m) ra = 0;
             if (rb >= P.n) rb = 0;
-            const uint32_t bytes = 4 * (kHalfBytes + (half ? kHalfBytes / 2 : kHalfBytes));
+            // B in this CTA: half of the item's columns, or (stored across) blocks of 64 of them
+            const uint32_t bytes_b = !narrow ? kHalfBytes : B_MN ? kHalfBytes / 2 : kHalfBytes / P.parts;
+            const uint32_t bytes = 4 * (kHalfBytes + bytes_b);
             const int32_t z = static_cast<int32_t>(it.z);
             for (uint32_t kb = 0; kb < kblocks; ++kb, ++g) {
                 const uint32_t bar = full0 + 8u * s;
@@ -446,10 +449,10 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     }
                     if (B_MN) {
                         tma_load_3d_pair(db, &map_b, static_cast<int32_t>(rb), k0, z, bar);
-                        if (!half)
+                        if (!narrow)
                             tma_load_3d_pair(db + 8192, &map_b, static_cast<int32_t>(b2 ? rb + 64 : rb), k0, z, bar);
                     } else {
-                        tma_load_3d_pair(db, half ? &map_b_half : &map_b, k0, static_cast<int32_t>(rb), z, bar);
+                        tma_load_3d_pair(db, narrow ? &map_b_part : &map_b, k0, static_cast<int32_t>(rb), z, bar);
                     }
                 }
                 if (!ok) break;
@@ -468,12 +471,13 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         // ------------------------------------------------------ MMA issuer
         uint32_t s = 0, phase = 0, i = 0;
         bool ok = true;
-        constexpr uint32_t kDescWide = instr_desc(kTile, A_MN, B_MN), kDescNarrow = instr_desc(kTile / 2, A_MN, B_MN);
+        constexpr uint32_t kDescWide = instr_desc(kTile, A_MN, B_MN);
+        const uint32_t desc_narrow = instr_desc(kTile / P.parts, A_MN, B_MN);
         const uint64_t desc_a0 = operand_desc<A_MN>(base), desc_b0 = operand_desc<B_MN>(base + 2 * kHalfBytes);
         constexpr uint64_t kDescStage = kStageBytes >> 4, kDescHalf = kHalfBytes >> 4;
         constexpr uint64_t kStepA = A_MN ? 2048 >> 4 : 32 >> 4, kStepB = B_MN ? 2048 >> 4 : 32 >> 4;
         for (uint32_t t = cluster; ok && t < items; t += clusters) {
-            const uint32_t idesc = t < P.wide ? kDescWide : kDescNarrow;
+            const uint32_t idesc = t < P.wide ? kDescWide : desc_narrow;
             for (uint32_t kc = 0; ok && kc < kblocks; kc += P.chunk, ++i) {
                 const int b = static_cast<int>(i % kAccBufs);
                 const uint32_t ub = i / kAccBufs;
@@ -520,7 +524,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     } else if (warp >= 2) {
         // ------------------------------------------------------- epilogue
         const int quarter = warp & 3;
-        const uint32_t c_lo = static_cast<uint32_t>((warp - 2) / 4) * kSpan;
+        const uint32_t group = static_cast<uint32_t>((warp - 2) / 4);
         float *stage = reinterpret_cast<float *>(smem_raw + (bars + kBarBytes - raw) + (warp - 2) * kWarpStage);
         uint32_t i = 0;
         bool ok = true;
@@ -528,7 +532,8 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             const Item it = work_item<kSym>(P, t);
             const uint32_t row = it.m0 + rank * 128 + quarter * 32 + lane;
             const uint32_t ncols = it.n0 >= P.n ? 0 : P.n - it.n0 < it.width ? P.n - it.n0 : it.width;
-            const uint32_t c_hi = ncols < c_lo + kSpan ? ncols : c_lo + kSpan;
+            const uint32_t span = it.width / (kEpi / 4), c_lo = group * span;      // this warp's columns
+            const uint32_t c_hi = ncols < c_lo + span ? ncols : c_lo + span;
             constexpr bool kStored = OP == kGram || OP == kPoly || OP == kNext;
             const bool rows_in = row - lane < P.m;          // the same for the whole warp
             const uint32_t col0 = it.n0 + c_lo, cols = c_hi > c_lo && rows_in ? c_hi - c_lo : 0;
@@ -565,6 +570,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 if constexpr (OP == kInt8) {
 #pragma unroll
                     for (int c = 0; c < kSpan; c += kBlock) {
+                        if (static_cast<uint32_t>(c) >= span) continue;
                         uint32_t v[16];
                         gemm::tmem_ld16(tq + c, v);
 #pragma unroll
@@ -748,17 +754,18 @@ asr_status launch(const Stored &a, const Stored &b, Params &P, int kind, cudaStr
     const uint64_t tiles = per * P.batch;
     if (tiles >= (1ull << 30)) return ASR_ERR_INVALID_VALUE;
     P.per_matrix = static_cast<uint32_t>(per);
-    // as in gemm_sr.cuh: the tiles of a last round that is at most half full go as halves
-    uint64_t rest = tiles % static_cast<uint64_t>(pairs);
-    if (2 * rest > static_cast<uint64_t>(pairs)) rest = 0;
-    P.wide = static_cast<uint32_t>(tiles - rest);
-    P.narrow = static_cast<uint32_t>(2 * rest);
+    // as in gemm_sr.cuh: the tiles of a last round that is at most half full go
+    // as halves, of one at most a quarter full as quarters
+    const uint64_t rest = tiles % static_cast<uint64_t>(pairs);
+    P.parts = 4 * rest <= static_cast<uint64_t>(pairs) ? 4 : 2 * rest <= static_cast<uint64_t>(pairs) ? 2 : 1;
+    P.narrow = static_cast<uint32_t>(P.parts > 1 ? P.parts * rest : 0);
+    P.wide = static_cast<uint32_t>(tiles - (P.narrow ? rest : 0));
     const uint64_t items = P.wide + static_cast<uint64_t>(P.narrow);
     const unsigned clusters = static_cast<unsigned>(items < static_cast<uint64_t>(pairs) ? items : pairs);
     CUtensorMap ma, mb, mbh;
     st = make_map(&ma, a.ptr, a.rows, a.cols, a.ld, a.stride, P.batch, A_MN ? 64 : 128);
     if (st == ASR_OK) st = make_map(&mb, b.ptr, b.rows, b.cols, b.ld, b.stride, P.batch, B_MN ? 64 : 128);
-    if (st == ASR_OK) st = make_map(&mbh, b.ptr, b.rows, b.cols, b.ld, b.stride, P.batch, 64);
+    if (st == ASR_OK) st = make_map(&mbh, b.ptr, b.rows, b.cols, b.ld, b.stride, P.batch, B_MN ? 64 : 128 / P.parts);
     if (st != ASR_OK) return st;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
