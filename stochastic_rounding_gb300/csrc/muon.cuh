@@ -196,6 +196,8 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
     }
 }
 
+#include "skinny.cuh"
+
 // ------------------------------------------------------------------ host
 
 uint64_t up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
@@ -259,7 +261,11 @@ struct Layout {                             // a group's part of the workspace
 
 Layout layout(uint64_t rows, uint64_t cols, uint64_t batch)
 {
-    Layout L;
+    Layout L{};
+    if (skinny_fits(rows, cols)) {              // everything in shared memory
+        L.bytes = 256;
+        return L;
+    }
     L.m = rows < cols ? rows : cols;
     L.ldx = up(cols, 16);
     L.lds = up(L.m, 16);
@@ -282,37 +288,104 @@ uint32_t batch_limit(uint64_t rows, uint64_t cols)
     return static_cast<uint32_t>(fit < 1 ? 1 : fit < prod::kMaxBatch ? fit : prod::kMaxBatch);
 }
 
+void prep_params(PrepParams &P, const Group &G, const NsParams &ns, float mu, bool nesterov)
+{
+    P.rows = G.rows;
+    P.cols = G.cols;
+    P.src_ld = G.src_ld;
+    P.src_dtype = G.src_dtype;
+    P.vec = G.vec_in;
+    P.nesterov = nesterov;
+    P.mu = mu;
+    P.omu = static_cast<float>(1.0 - static_cast<double>(mu));
+    P.eps = static_cast<float>(ns.eps);
+    std::memcpy(P.m, G.m, sizeof(Matrix) * G.batch);
+}
+
 template <bool MUON>
 asr_status prep(const Group &G, const NsParams &ns, const Layout &L, char *ws, float mu, bool nesterov,
                 cudaStream_t stream)
 {
     PrepParams P;
     std::memset(&P, 0, sizeof(P));
-    P.rows = G.rows;
-    P.cols = G.cols;
-    P.src_ld = G.src_ld;
-    P.src_dtype = G.src_dtype;
-    P.vec = G.vec_in;
+    prep_params(P, G, ns, mu, nesterov);
     // eight spans a block at least, and no more blocks than fill the GPU (152
     // SMs, eight a SM) or make enough partial sums
     const uint64_t want = (G.rows * ((G.cols + kSpan - 1) / kSpan) + 7) / 8;
     const uint64_t fill = std::max<uint64_t>(16, std::min<uint64_t>(kPartBlocks, 1216 / G.batch));
     P.blocks = static_cast<uint32_t>(want < fill ? want : fill);
-    P.nesterov = nesterov;
-    P.mu = mu;
-    P.omu = static_cast<float>(1.0 - static_cast<double>(mu));
-    P.eps = static_cast<float>(ns.eps);
     P.partial = reinterpret_cast<float *>(ws + L.partial);
     P.out = reinterpret_cast<__half *>(ws + L.x0);
     P.out_ld = L.ldx;
     P.out_stride = up(G.rows * L.ldx * 2, 256) / 2;
-    std::memcpy(P.m, G.m, sizeof(Matrix) * G.batch);
     const dim3 grid(P.blocks, G.batch, 1);
     square_sum_kernel<MUON><<<grid, kThreads, 0, stream>>>(P);
     asr_status st = launched(ASR_KERNEL_MATRIX_PREP);
     if (st != ASR_OK) return st;
     scale_kernel<MUON><<<grid, kThreads, 0, stream>>>(P);
     return launched(ASR_KERNEL_MATRIX_PREP);
+}
+
+// A group whose matrices' smaller side is at most 128: one launch.
+std::mutex g_skinny_mu;
+bool g_skinny_ready[kMaxDevices];
+
+asr_status skinny_setup()
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (dev < 0 || dev >= kMaxDevices) return ASR_ERR_INVALID_VALUE;
+    std::lock_guard<std::mutex> lk(g_skinny_mu);
+    if (!g_skinny_ready[dev]) {
+        e = cudaFuncSetAttribute(skinny_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSkinnySmem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(skinny_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSkinnySmem);
+        if (e != cudaSuccess) return cuda_fail(e);
+        g_skinny_ready[dev] = true;
+    }
+    return ASR_OK;
+}
+
+template <bool MUON>
+asr_status skinny(const Group &G, const NsParams &ns, const prod::Params &last, float mu, bool nesterov,
+                  cudaStream_t stream)
+{
+    asr_status st = skinny_setup();
+    if (st != ASR_OK) return st;
+    SkinnyParams P;
+    std::memset(&P, 0, sizeof(P));
+    prep_params(P.in, G, ns, mu, nesterov);
+    P.out = last;
+    P.out.m = static_cast<uint32_t>(G.rows);
+    P.out.n = static_cast<uint32_t>(G.cols);
+    P.out.alpha = last.alpha / kStore / kStore;
+    P.tall = G.rows > G.cols;
+    P.m = static_cast<uint32_t>(P.tall ? G.cols : G.rows);
+    P.n = static_cast<uint32_t>(P.tall ? G.rows : G.cols);
+    P.steps = ns.steps;
+    P.a = static_cast<float>(ns.a);
+    P.b = static_cast<float>(ns.b);
+    P.c = static_cast<float>(ns.c);
+    uint32_t ctas = 1;
+    while (ctas * kSkinnyCols < P.n) ctas *= 2;
+    P.share = (P.n + 64 * ctas - 1) / (64 * ctas) * 64;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(G.batch * ctas, 1, 1);
+    cfg.blockDim = dim3(kSkinnyThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSkinnySmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const uint64_t limit = kWaitLimitNs;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, skinny_kernel<MUON>, P, limit);
+    if (e != cudaSuccess) return cuda_fail(e);
+    return launched(ASR_KERNEL_PRODUCT);
 }
 
 // The products of a group.  `last` holds the fields of the last product's
@@ -571,10 +644,11 @@ asr_status newton_schulz(const asr_matrix_desc *table, int32_t n, const asr_ns_p
     return for_groups(flat, [&](const Group &G) {
         const Layout L = layout(G.rows, G.cols, G.batch);
         char *w = static_cast<char *>(ws);
-        asr_status s = prep<false>(G, ns, L, w, 0.0f, false, stream);
-        if (s != ASR_OK) return s;
         prod::Params last = last_params(G);
         last.alpha = 1.0f;
+        if (skinny_fits(G.rows, G.cols)) return skinny<false>(G, ns, last, 0.0f, false, stream);
+        asr_status s = prep<false>(G, ns, L, w, 0.0f, false, stream);
+        if (s != ASR_OK) return s;
         return iterate<prod::kOut>(G, ns, L, w, last, stream);
     });
 }
@@ -606,8 +680,6 @@ asr_status step(const asr_muon_desc *table, int32_t n, const asr_muon_hparams *h
     return for_groups(flat, [&](const Group &G) {
         const Layout L = layout(G.rows, G.cols, G.batch);
         char *w = static_cast<char *>(ws);
-        asr_status s = prep<true>(G, ns, L, w, static_cast<float>(hp->momentum), hp->nesterov != 0, stream);
-        if (s != ASR_OK) return s;
         const double r = static_cast<double>(G.rows), c = static_cast<double>(G.cols);
         const double adjust = hp->adjust == ASR_MUON_ADJUST_RMS ? 0.2 * std::sqrt(std::max(r, c))
                               : hp->adjust == ASR_MUON_ADJUST_SPECTRAL ? std::sqrt(std::max(1.0, r / c)) : 1.0;
@@ -617,6 +689,10 @@ asr_status step(const asr_muon_desc *table, int32_t n, const asr_muon_hparams *h
         last.rounding = hp->rounding;
         last.step = hp->step;
         last.keys = make_keys(hp->seed);
+        if (skinny_fits(G.rows, G.cols))
+            return skinny<true>(G, ns, last, static_cast<float>(hp->momentum), hp->nesterov != 0, stream);
+        asr_status s = prep<true>(G, ns, L, w, static_cast<float>(hp->momentum), hp->nesterov != 0, stream);
+        if (s != ASR_OK) return s;
         return iterate<prod::kParam>(G, ns, L, w, last, stream);
     });
 }

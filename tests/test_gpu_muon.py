@@ -51,7 +51,10 @@ def _far(got, want):
 
 SHAPES = [(1, 1), (1, 17), (17, 1), (2, 3), (8, 8), (16, 64), (65, 31), (96, 160), (127, 129), (128, 128), (129, 400),
           (256, 256), (257, 255), (300, 513), (515, 1365), (1365, 515), (640, 640), (1024, 256), (512, 2048),
-          (2048, 520)]
+          (2048, 520),
+          # a smaller side of at most 128: one to eight CTAs a matrix, just below and above their limits
+          (128, 512), (128, 513), (100, 1500), (1025, 77), (128, 4096), (4096, 128), (3, 4000), (4000, 1), (128, 4097),
+          (4097, 128)]
 
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
@@ -140,6 +143,36 @@ def test_orthogonalise_stacks_and_strides(asr):
         assert (buf[..., :2] == 7).all() and (buf[..., -3:] == 7).all()
 
 
+def test_orthogonalise_strided_larger(asr):
+    """The same on matrices that go through memory: strided views, odd starts."""
+    import torch
+    torch.manual_seed(16)
+    store = torch.randn(3, 210, 333, device="cuda")
+    x = store[:, 1:201, 3:320]
+    buf = torch.full((3, 200, 325), 7.0, device="cuda", dtype=torch.bfloat16)
+    out = buf[..., 2:319]
+    asr.asr_newton_schulz([(x, out)])
+    for z in range(3):
+        alone = torch.empty(200, 317, device="cuda", dtype=torch.bfloat16)
+        asr.asr_newton_schulz([(x[z].contiguous(), alone)])
+        assert_same_bits(host(out[z].contiguous()), host(alone))
+        assert _far(out[z], _exact(x[z])) <= _bound(5)
+    assert (buf[..., :2] == 7).all() and (buf[..., 319:] == 7).all()
+
+
+@pytest.mark.parametrize("shape", [(128, 700), (700, 128), (150, 200)])
+def test_orthogonalise_zero_and_not_finite_each_path(asr, shape):
+    import torch
+    g = torch.randn(4, *shape, device="cuda")
+    g[0] = 0
+    g[1, 5, 7] = float("-inf")
+    g[2, -1, -1] = float("nan")
+    out = torch.empty(4, *shape, device="cuda", dtype=torch.bfloat16)
+    asr.asr_newton_schulz([(g, out)])
+    assert (out[0] == 0).all() and out[1].isnan().all() and out[2].isnan().all()
+    assert _far(out[3], _exact(g[3])) <= _bound(5)
+
+
 def _momentum(m, g, mu, nesterov):
     """binary32, every operation rounded."""
     f = np.float32
@@ -149,7 +182,8 @@ def _momentum(m, g, mu, nesterov):
     return m, u
 
 
-@pytest.mark.parametrize("shape", [(40, 64), (65, 33), (2, 100, 256), (3, 515, 130), (1, 300, 300)])
+@pytest.mark.parametrize("shape", [(40, 64), (65, 33), (2, 100, 256), (3, 515, 130), (1, 300, 300), (2, 2000, 50),
+                                   (60, 1103), (1103, 61), (128, 640)])
 @pytest.mark.parametrize("gdt", ["float32", "bfloat16"])
 @pytest.mark.parametrize("nesterov", [True, False])
 @pytest.mark.parametrize("adjust", ["original", "match_rms_adamw", None])
