@@ -62,98 +62,6 @@ __global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__
     widen_block(P, blockIdx.x, gridDim.x);
 }
 
-// How a row's values become integers: y = (x * pre) * inv.  A row whose largest
-// value is so small that 127 / max would overflow is raised by 2^64 first (exact);
-// a row that holds an infinity or a NaN gives zeros, and its scale, not finite,
-// marks every product of the row.  Both are rare, and `odd` sets them apart.
-struct Levels {
-    float pre, inv;
-    bool odd;
-};
-
-__device__ __forceinline__ Levels levels_of(float top)
-{
-    Levels L;
-    L.pre = top < 0x1p-64f ? 0x1p64f : 1.0f;
-    L.inv = top > 0.0f && top <= 3.402823466e38f ? __fdiv_rn(127.0f, __fmul_rn(top, L.pre)) : 0.0f;
-    L.odd = L.inv == 0.0f || L.pre != 1.0f;
-    return L;
-}
-
-__device__ __forceinline__ float regular(float x, const Levels &L) { return L.inv == 0.0f ? 0.0f : __fmul_rn(x, L.pre); }
-
-// Integers come in pairs, as 0x6480 + q in each half of a word: as f16 that is
-// 1,152 + q.
-//
-// To nearest: |y| <= 127 (1 + 2^-23), so that the nearest is at most 127, and
-// the sum with 1.5 * 2^23 + 0x6480 has it in its low half.
-__device__ __forceinline__ uint32_t nearest2(float x, float y, float inv_x, float inv_y)
-{
-    constexpr float kMagic = 12582912.0f + 25728.0f;
-    return __byte_perm(__float_as_uint(__fadd_rn(__fmul_rn(x, inv_x), kMagic)),
-                       __float_as_uint(__fadd_rn(__fmul_rn(y, inv_y), kMagic)), 0x5410);
-}
-
-// Stochastically: floor(y) + [65536 (y - floor(y)) > r] for whole r in [0, 65535]
-// is floor((ceil(65536 y) + 65535 - r) / 65536), the sum's high half.  The scales
-// come times 65536 (exact); not_r is 65535 - r.  |q| may come to 128.
-__device__ __forceinline__ uint32_t random2(float x, float y, float inv_x, float inv_y, uint32_t not_r, uint32_t not_s)
-{
-    const uint32_t a = static_cast<uint32_t>(__float2int_ru(__fmul_rn(x, inv_x))) + not_r + 0x64800000u;
-    const uint32_t b = static_cast<uint32_t>(__float2int_ru(__fmul_rn(y, inv_y))) + not_s + 0x64800000u;
-    return __vmaxu2(__vminu2(__byte_perm(a, b, 0x7632), 0x64FF64FFu), 0x64016401u);
-}
-
-// Eight of them as f16, or as bytes.
-__device__ __forceinline__ uint4 halves_of(const uint32_t e[4])
-{
-    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-    uint32_t h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&e[i]), bias);
-        h[i] = *reinterpret_cast<const uint32_t *>(&v);
-    }
-    return make_uint4(h[0], h[1], h[2], h[3]);
-}
-
-__device__ __forceinline__ uint2 bytes_of(const uint32_t e[4])
-{
-    return make_uint2(__byte_perm(e[0], e[1], 0x6420) ^ 0x80808080u, __byte_perm(e[2], e[3], 0x6420) ^ 0x80808080u);
-}
-
-__device__ __forceinline__ void store_int8(int8_t *dst, const uint32_t e[4], int live)
-{
-    const uint2 w = bytes_of(e);
-    if (live == 8 && (reinterpret_cast<uintptr_t>(dst) & 7u) == 0) {
-        *reinterpret_cast<uint2 *>(dst) = w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < live) dst[i] = static_cast<int8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
-    }
-}
-
-// Eight values of one scale.
-template <bool SR>
-__device__ __forceinline__ void quantise8(const float x[8], const Levels &L, const uint32_t not_r[8], uint32_t e[4])
-{
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = x[i];
-    if (L.odd) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = regular(x[i], L);
-    }
-    const float inv = SR ? __fmul_rn(L.inv, 65536.0f) : L.inv;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        e[i] = SR ? random2(v[2 * i], v[2 * i + 1], inv, inv, not_r[2 * i], not_r[2 * i + 1])
-                  : nearest2(v[2 * i], v[2 * i + 1], inv, inv);
-}
-
-__device__ __forceinline__ uint32_t absbits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-
 __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *part)
 {
     v = __reduce_max_sync(0xFFFFFFFFu, v);
@@ -232,21 +140,13 @@ constexpr int kFewUnits = 4;                    // rows of up to 4 * 8 * 1,024 v
 
 struct FewPrepParams {
     const void *x;
-    void *out;                                  // f16, or int8 (DOTS)
+    __half *out;
     float *scale;                               // null: x is int8
     uint4 *zero;
     uint64_t rows, cols, x_ld, out_ld, zero_units;
     uint32_t dtype, vec;
 };
 
-template <bool DOTS>
-__device__ __forceinline__ void store_few(void *row, uint64_t col, const uint32_t q[4])
-{
-    if (DOTS) store_int8(static_cast<int8_t *>(row) + col, q, 8);
-    else *reinterpret_cast<uint4 *>(static_cast<__half *>(row) + col) = halves_of(q);
-}
-
-template <bool DOTS>
 __global__ void __launch_bounds__(kPrepThreads) few_prep_kernel(const __grid_constant__ FewPrepParams P)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -257,7 +157,7 @@ __global__ void __launch_bounds__(kPrepThreads) few_prep_kernel(const __grid_con
         return;
     }
     const uint64_t row = blockIdx.x;
-    void *out = static_cast<char *>(P.out) + row * P.out_ld * (DOTS ? 1 : 2);
+    __half *out = P.out + row * P.out_ld;
     if (!P.scale) {
         const int8_t *src = static_cast<const int8_t *>(P.x) + row * P.x_ld;
         for (uint64_t col = threadIdx.x * 8ull; col < P.out_ld; col += kPrepThreads * 8ull) {
@@ -267,7 +167,7 @@ __global__ void __launch_bounds__(kPrepThreads) few_prep_kernel(const __grid_con
                 const int lo = col + 2 * q < P.cols ? src[col + 2 * q] : 0, hi = col + 2 * q + 1 < P.cols ? src[col + 2 * q + 1] : 0;
                 e[q] = __byte_perm(static_cast<uint32_t>(lo + 0x6480), static_cast<uint32_t>(hi + 0x6480), 0x5410);
             }
-            store_few<DOTS>(out, col, e);
+            *reinterpret_cast<uint4 *>(out + col) = halves_of(e);
         }
         return;
     }
@@ -301,14 +201,14 @@ __global__ void __launch_bounds__(kPrepThreads) few_prep_kernel(const __grid_con
         const uint64_t col = (u * kPrepThreads + threadIdx.x) * 8ull;
         uint32_t q[4];
         quantise8<false>(x[u], L, nullptr, q);
-        if (col < P.out_ld) store_few<DOTS>(out, col, q);
+        if (col < P.out_ld) *reinterpret_cast<uint4 *>(out + col) = halves_of(q);
     }
     for (uint64_t col = (kFewUnits * kPrepThreads + threadIdx.x) * 8ull; col < P.out_ld; col += kPrepThreads * 8ull) {
         float v[8];
         fetch(col, v);
         uint32_t q[4];
         quantise8<false>(v, L, nullptr, q);
-        store_few<DOTS>(out, col, q);
+        *reinterpret_cast<uint4 *>(out + col) = halves_of(q);
     }
 }
 
@@ -677,8 +577,9 @@ struct Layout {
 
 Layout layout(uint64_t m, uint64_t n, uint64_t k)
 {
-    Layout L;
+    Layout L{};
     L.ld = muon::up(k, 16);
+    if (few(m) && int8few::dots(m, n, k)) return L;     // none
     L.scale = 0;
     L.zero = muon::up(m * sizeof(float), 256);
     L.zero_bytes = 0;
@@ -754,10 +655,33 @@ asr_status few_rows(const void *x, int32_t x_dtype, uint64_t x_ld, const float *
                     const float *sb, const Output &o, uint64_t m, uint64_t n, uint64_t k, char *ws, const Layout &L,
                     cudaStream_t stream)
 {
+    if (int8few::dots(m, n, k)) {
+        int8few::DotParams D;
+        std::memset(&D, 0, sizeof(D));
+        D.a = x;
+        D.b = b;
+        D.row_scale = sa;
+        D.col_scale = sb;
+        D.c = o.c;
+        D.lda = x_ld;
+        D.ldb = ldb;
+        D.ldc = o.ld;
+        D.m = static_cast<uint32_t>(m);
+        D.n = static_cast<uint32_t>(n);
+        D.k = static_cast<uint32_t>(k);
+        D.a_dtype = static_cast<uint32_t>(x_dtype);
+        D.a_vec = !sa && muon::units_aligned(x, x_ld, 0);
+        D.b_vec = aligned16(b) && ldb % 16 == 0;
+        D.c_dtype = static_cast<uint32_t>(o.dtype);
+        D.rounding = o.rounding;
+        D.step = o.step;
+        D.keys = make_keys(o.seed);
+        return int8few::run_dots(D, !sa, stream);
+    }
     FewPrepParams F;
     std::memset(&F, 0, sizeof(F));
     F.x = x;
-    F.out = ws + L.a;
+    F.out = reinterpret_cast<__half *>(ws + L.a);
     F.scale = sa ? nullptr : reinterpret_cast<float *>(ws + L.scale);
     F.zero = reinterpret_cast<uint4 *>(ws + L.zero);
     F.rows = m;
@@ -768,8 +692,7 @@ asr_status few_rows(const void *x, int32_t x_dtype, uint64_t x_ld, const float *
     F.dtype = static_cast<uint32_t>(x_dtype);
     F.vec = !sa && muon::units_aligned(x, x_ld, 0);
     const unsigned blocks = static_cast<unsigned>(m) + blocks_for(F.zero_units, 4 * kPrepThreads, 64);
-    if (int8few::dots(m)) few_prep_kernel<true><<<blocks, kPrepThreads, 0, stream>>>(F);
-    else few_prep_kernel<false><<<blocks, kPrepThreads, 0, stream>>>(F);
+    few_prep_kernel<<<blocks, kPrepThreads, 0, stream>>>(F);
     asr_status st = launched(ASR_KERNEL_QUANTIZE);
     if (st != ASR_OK) return st;
     int8few::Params P;
@@ -806,7 +729,7 @@ asr_status gemm(const int8_t *a, uint64_t lda, const int8_t *b, uint64_t ldb, co
         !muon::element_aligned(sa, ASR_F32) || !muon::element_aligned(sb, ASR_F32))
         return ASR_ERR_INVALID_VALUE;
     const Layout L = layout(m, n, k);
-    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < L.bytes) return ASR_ERR_INVALID_VALUE;
+    if (L.bytes && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < L.bytes)) return ASR_ERR_INVALID_VALUE;
     st = setup();
     if (st != ASR_OK) return st;
     char *w = static_cast<char *>(ws);
@@ -846,7 +769,7 @@ asr_status linear(const void *x, int32_t x_dtype, uint64_t x_ld, const int8_t *q
         !muon::element_aligned(x, x_dtype) || !muon::element_aligned(sw, ASR_F32))
         return ASR_ERR_INVALID_VALUE;
     const Layout L = layout(m, n, k);
-    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < L.bytes) return ASR_ERR_INVALID_VALUE;
+    if (L.bytes && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < L.bytes)) return ASR_ERR_INVALID_VALUE;
     st = setup();
     if (st != ASR_OK) return st;
     char *w = static_cast<char *>(ws);

@@ -11,7 +11,7 @@
 // anybody.  A warp streams its rows of the weight from global memory straight
 // into registers, several pieces ahead.
 //
-// Two kernels:
+// Two kernels; the first is for so few tokens that no tensor core is needed:
 //   few_dots_kernel    up to 4 tokens: dot products of four bytes (dp4a), 16
 //                      instructions for a lane's four rows of 16 bytes;
 //   few_rows_kernel    up to 128 tokens a pass: tcgen05.mma with the weight as
@@ -24,6 +24,7 @@
 //                      (measured: 1.05 ns), so beyond 16 tokens it falls behind
 //                      the memory: 40 us against 58.7 MB and 33 tokens.
 // At most 1,024 products are added in binary32, which is exact; int32 then.
+// (What follows of pieces and shared sums is the second kernel's.)
 
 namespace int8few {
 
@@ -32,8 +33,7 @@ constexpr int kDotTokens = 4;               // up to this many, dot products
 constexpr int kMaxTokens = 128;             // of a pass over B
 
 struct Params {
-    const void *a;                          // tokens, m x k: widened, rows a multiple of 16 values apart and zero
-                                            // past k (dot products: integers, likewise)
+    const __half *a;                        // tokens, m x k: widened, rows a multiple of 16 values apart and zero past k
     const int8_t *b;                        // weight, n x k
     const float *row_scale, *col_scale;
     void *c;
@@ -86,8 +86,8 @@ __device__ __noinline__ uint32_t round_stochastic(float y, uint64_t e, uint32_t 
 
 // The outputs of one column (of scale cs) and COUNT tokens (`live` of them, of
 // scales rs) from their integer sums.
-template <int COUNT>
-__device__ __forceinline__ void store_outputs(const Params &P, uint32_t token, uint32_t col, float cs, const float *rs,
+template <int COUNT, typename P_>
+__device__ __forceinline__ void store_outputs(const P_ &P, uint32_t token, uint32_t col, float cs, const float *rs,
                                               const int32_t sum[COUNT], uint32_t live)
 {
     float y[COUNT];
@@ -115,123 +115,144 @@ __device__ __forceinline__ void store_outputs(const Params &P, uint32_t token, u
 
 // ------------------------------------------------------------ dot products
 //
-// Sixteen warps: four blocks of 32 rows, four quarters of a piece's 512 of K.
-// The tokens come into a ring in shared memory by bulk copies.
+// A cluster of up to eight CTAs takes 64 rows of the weight, each CTA a share of
+// K; a CTA has eight warps, two blocks of 32 rows and four quarters of every 512
+// of K.  A lane holds 16 bytes of four rows at a time, a 512 ahead.  The tokens
+// lie in shared memory as integers, quantised by every CTA for itself (the
+// scale needs the whole row, a few KB out of L2) while its first weights are on
+// their way; so there is one launch and no workspace.  With the quantiser in a
+// launch of its own and the sums of shared row blocks through memory one token of
+// 14,336 x 4,096 took 17.3 us, of which 8.6 us are the weight's bytes.
+constexpr int kDotThreads = 256;
+constexpr uint32_t kDotRows = 64;
+constexpr uint32_t kSlab = 512;                 // K a round, a quarter of it a warp
+constexpr uint32_t kDotSmem = 96 * 1024;        // room for the tokens
+constexpr uint32_t kDotSplit = 8;
 
-constexpr int kThreads = 512;
-constexpr int kSlab = 512;                  // K a piece, a quarter of it a warp
-constexpr int kTokenPitch = kSlab + 16;
-constexpr int kSumPitch = kRows + 4;        // words between tokens' sums
-constexpr int kStages = 8;                  // pieces of tokens in shared memory
-constexpr int kAhead = kStages / 2;
+struct DotParams {
+    const void *a;                              // tokens: f32, bf16, or (with row_scale) int8
+    const int8_t *b;
+    const float *row_scale, *col_scale;
+    void *c;
+    uint64_t lda, ldb, ldc;
+    uint32_t m, n, k, share;                    // share: K of a CTA, a multiple of kSlab
+    uint32_t a_dtype, a_vec, b_vec;
+    uint32_t c_dtype, rounding, step;
+    RoundKeys keys;
+};
 
-__global__ void __launch_bounds__(kThreads, 1) few_dots_kernel(const __grid_constant__ Params P, uint64_t limit_ns)
+__device__ __forceinline__ int32_t ld_cluster_s32(uint32_t addr)
 {
-    __shared__ __align__(16) unsigned char ring[kStages * kDotTokens * kTokenPitch];
-    __shared__ int32_t sums[kDotTokens * kSumPitch];
-    __shared__ __align__(8) uint64_t bar[2 * kStages];
-    __shared__ uint32_t done;
-    const uint32_t xs = smem_addr(ring), bars = smem_addr(bar);
-    auto full = [&](uint32_t i) { return bars + 8u * i; };
-    auto empty = [&](uint32_t i) { return bars + 8u * (kStages + i); };
+    int32_t v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <bool QUANTISE>
+__global__ void __launch_bounds__(kDotThreads, 2) few_dots_kernel(const __grid_constant__ DotParams P)
+{
+    extern __shared__ __align__(16) int8_t xs[];                            // [token][share]
+    __shared__ int32_t sums[kDotTokens * kDotRows];
+    __shared__ uint32_t part[kDotTokens][kDotThreads / 32];
+    __shared__ float scales[kDotTokens];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = lane >> 2, t = lane & 3, quarter = warp & 3, wr = warp >> 2;
-    const uint32_t total = P.tiles * P.pieces;
-    const uint32_t first = static_cast<uint32_t>(static_cast<uint64_t>(total) * blockIdx.x / gridDim.x);
-    const uint32_t end = static_cast<uint32_t>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / gridDim.x);
+    const uint32_t g = lane >> 2, t = lane & 3, quarter = warp & 3, block = warp >> 2;
+    const uint32_t rank = gemm::cluster_rank();
+    uint32_t split;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
+    const uint32_t n0 = blockIdx.x / split * kDotRows, k0 = rank * P.share;
+    const uint32_t k1 = min(P.k, k0 + P.share);                             // at or below k0: nothing to add
 
-    // the weight of piece (tile, s): rows g, g + 8, g + 16, g + 24 of the warp's 32, two 64-wide parts
-    uint4 w[2][4];
+    // the weight's rows g, g + 8, g + 16, g + 24 of the warp's 32, two 64-wide pieces a round
+    const uint32_t row = n0 + block * 32 + g;
+    const int8_t *src = P.b + row * P.ldb;
     const uint64_t ldb8 = 8 * P.ldb;
-    auto weight = [&](uint32_t tile, uint32_t s, int i) {
-        const uint32_t row = tile * kRows + wr * 32 + g, k = s * kSlab + quarter * (kSlab / 4) + i * 64 + t * 16;
-        const int8_t *p = P.b + row * P.ldb + k;
-        if (P.b_vec && (tile + 1) * kRows <= P.n && (s + 1) * kSlab <= P.k) {     // the same for the whole CTA
+    uint4 w[2][4];
+    auto weight = [&](uint32_t k, int i) {
+        const uint32_t at = k + quarter * (kSlab / 4) + i * 64 + t * 16;
+        if (P.b_vec && n0 + kDotRows <= P.n && k + kSlab <= k1) {           // the same for the whole CTA
 #pragma unroll
-            for (int r = 0; r < 4; ++r) w[i][r] = __ldcs(reinterpret_cast<const uint4 *>(p + r * ldb8));
+            for (int r = 0; r < 4; ++r) w[i][r] = __ldcs(reinterpret_cast<const uint4 *>(src + r * ldb8 + at));
         } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 w[i][r] = make_uint4(0, 0, 0, 0);
-                if (row + 8 * r < P.n && k < P.k) {
-                    if (P.b_vec && k + 16 <= P.k) w[i][r] = __ldcs(reinterpret_cast<const uint4 *>(p + r * ldb8));
-                    else w[i][r] = load16_slow(p + r * ldb8, P.k - k);
+                if (row + 8 * r < P.n && at < k1) {
+                    if (P.b_vec && at + 16 <= k1) w[i][r] = __ldcs(reinterpret_cast<const uint4 *>(src + r * ldb8 + at));
+                    else w[i][r] = load16_slow(src + r * ldb8 + at, k1 - at);
                 }
             }
         }
     };
-    // the tokens of a piece (warp 0, a token a lane); what a short last piece leaves in its stage meets weights
-    // that are zero there
-    auto fetch = [&](uint32_t s, uint32_t stage) {
-        const uint64_t k = static_cast<uint64_t>(s) * kSlab;
-        const uint32_t bytes = P.lda - k < kSlab ? static_cast<uint32_t>(P.lda - k) : kSlab;
-        if (lane == 0) mbar_arrive_expect_tx(full(stage), bytes * P.m);
-        __syncwarp();
-        if (lane < static_cast<int>(P.m)) {
-            const int8_t *src = static_cast<const int8_t *>(P.a) + lane * P.lda + k;
-            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                             xs + (stage * kDotTokens + lane) * kTokenPitch),
-                         "l"(src), "r"(bytes), "r"(full(stage))
-                         : "memory");
-        }
-    };
-
-    uint32_t tile = first / P.pieces, s = first % P.pieces;
-    if (first < end) {
-        weight(tile, s, 0);
-        weight(tile, s, 1);
+    if (k0 < k1) {
+        weight(k0, 0);
+        weight(k0, 1);
     }
-    for (int i = threadIdx.x; i < kDotTokens * kSumPitch; i += kThreads) sums[i] = 0;
-    if (threadIdx.x == 0) {
-        for (uint32_t i = 0; i < kStages; ++i) {
-            mbar_init(full(i), 1);
-            mbar_init(empty(i), kThreads / 32);
+    for (uint32_t i = threadIdx.x; i < kDotTokens * kDotRows; i += kDotThreads) sums[i] = 0;
+
+    // ---- the tokens
+    if (QUANTISE) {
+        uint32_t top[kDotTokens] = {};
+        for (uint32_t c = threadIdx.x * 8; c < P.k; c += kDotThreads * 8) {
+            const int live = P.k - c < 8 ? static_cast<int>(P.k - c) : 8;
+#pragma unroll
+            for (int q = 0; q < kDotTokens; ++q) {
+                if (q >= static_cast<int>(P.m)) break;
+                float x[8];
+                muon::load8(P.a, P.a_dtype, q * P.lda + c, live, P.a_vec, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top[q] = max(top[q], int8::absbits(x[e]));
+            }
         }
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+#pragma unroll
+        for (int q = 0; q < kDotTokens; ++q) {
+            top[q] = __reduce_max_sync(0xFFFFFFFFu, top[q]);
+            if (lane == 0) part[q][warp] = top[q];
+        }
+        __syncthreads();
+        for (uint32_t q = 0; q < P.m; ++q) {
+            uint32_t most = part[q][0];
+#pragma unroll
+            for (int e = 1; e < kDotThreads / 32; ++e) most = max(most, part[q][e]);
+            const float amax = __uint_as_float(most);
+            const int8::Levels L = int8::levels_of(amax);
+            if (threadIdx.x == 0) scales[q] = __fdiv_rn(amax, 127.0f);
+            for (uint32_t c = threadIdx.x * 8; c < P.share; c += kDotThreads * 8) {
+                const int live = k0 + c >= P.k ? 0 : P.k - k0 - c < 8 ? static_cast<int>(P.k - k0 - c) : 8;
+                float x[8];
+                uint32_t e[4];
+                muon::load8(P.a, P.a_dtype, q * P.lda + k0 + c, live, P.a_vec, x);
+                int8::quantise8<false>(x, L, nullptr, e);
+                *reinterpret_cast<uint2 *>(xs + q * P.share + c) = int8::bytes_of(e);
+            }
+        }
+    } else {
+        for (uint32_t q = 0; q < P.m; ++q) {
+            const int8_t *a = static_cast<const int8_t *>(P.a) + q * P.lda + k0;
+            for (uint32_t c = threadIdx.x; c < P.share; c += kDotThreads) xs[q * P.share + c] = k0 + c < P.k ? a[c] : 0;
+            if (threadIdx.x == 0) scales[q] = P.row_scale[q];
+        }
     }
     __syncthreads();
-    // the weight is older than the previous kernel on the stream; the tokens and the sums are its output
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    uint32_t fs = s, fetched = first, ahead = 0;
-    if (warp == 0) {
-        for (int i = 0; i < kAhead && fetched < end; ++i, ++fetched) {
-            fetch(fs, ahead++);
-            fs = fs + 1 == P.pieces ? 0 : fs + 1;
-        }
-    }
 
     int32_t dot[4][kDotTokens];                 // rows g + 8 r, this lane's part of K
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int q = 0; q < kDotTokens; ++q) dot[r][q] = 0;
-
-    uint32_t run = 0, stage = 0, phase = 0;
-    for (uint32_t at = first; at < end; ++at) {
-        if (warp == 0 && fetched < end) {
-            // the stage's last use was piece fetched - kStages of this CTA's
-            const uint32_t use = (fetched - first) / kStages;
-            if (use > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(empty(ahead), (use - 1) & 1u, limit_ns))) break;
-            fetch(fs, ahead);
-            ++fetched;
-            fs = fs + 1 == P.pieces ? 0 : fs + 1;
-            ahead = ahead + 1 == kStages ? 0 : ahead + 1;
-        }
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(full(stage), phase, limit_ns))) break;
-        const uint32_t ns = s + 1 == P.pieces ? 0 : s + 1, nt = s + 1 == P.pieces ? tile + 1 : tile;
-        const unsigned char *x = ring + stage * kDotTokens * kTokenPitch + quarter * (kSlab / 4) + t * 16;
+    for (uint32_t k = k0; k < k1; k += kSlab) {
+        const int8_t *x = xs + (k - k0) + quarter * (kSlab / 4) + t * 16;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             uint32_t v[4][4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r][0] = w[i][r].x, v[r][1] = w[i][r].y, v[r][2] = w[i][r].z, v[r][3] = w[i][r].w;
-            if (at + 1 < end) weight(nt, ns, i);
+            if (k + kSlab < k1) weight(k + kSlab, i);
 #pragma unroll
             for (int q = 0; q < kDotTokens; ++q) {
                 if (q > 0 && q >= static_cast<int>(P.m)) break;
-                const int4 b = *reinterpret_cast<const int4 *>(x + q * kTokenPitch + i * 64);
+                const int4 b = *reinterpret_cast<const int4 *>(x + q * P.share + i * 64);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     dot[r][q] = __dp4a(static_cast<int>(v[r][0]), b.x, dot[r][q]);
@@ -241,58 +262,28 @@ __global__ void __launch_bounds__(kThreads, 1) few_dots_kernel(const __grid_cons
                 }
             }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty(stage));
-        ++run;
-        if (at + 1 == end || s + 1 == P.pieces) {
-            // add the warps' sums up
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int q = 0; q < kDotTokens; ++q) {
-                    int32_t v = dot[r][q];
-                    v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
-                    v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
-                    if (t == q) atomicAdd(sums + q * kSumPitch + wr * 32 + r * 8 + g, v);
-                    dot[r][q] = 0;
-                }
-            __syncthreads();
-            const bool whole = run == P.pieces;     // the block's only part
-            const uint32_t row = threadIdx.x % kRows, col = tile * kRows + row, token = threadIdx.x / kRows;
-            int32_t *mine = P.sums + (static_cast<uint64_t>(tile) * P.m + token) * kRows + row;
-            if (token < P.m) {
-                const int32_t sum = sums[token * kSumPitch + row];
-                sums[token * kSumPitch + row] = 0;
-                if (!whole) atomicAdd(mine, sum);
-                else if (col < P.n) store_outputs<1>(P, token, col, P.col_scale[col], P.row_scale + token, &sum, 1);
-            }
-            if (!whole) {
-                __threadfence();
-                __syncthreads();
-                if (threadIdx.x == 0) done = atomicAdd(P.counts + tile, run) + run;
-                __syncthreads();
-                if (done == P.pieces) {
-                    __threadfence();
-                    if (token < P.m && col < P.n) {
-                        const int32_t sum = __ldcg(mine);
-                        store_outputs<1>(P, token, col, P.col_scale[col], P.row_scale + token, &sum, 1);
-                    }
-                }
-            }
-            run = 0;
-            __syncthreads();                        // the sums are zero again before any warp adds to them
-        }
-        s = ns;
-        tile = nt;
-        if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-        }
     }
-    // after a wait that gave up: the copies issued here have landed before the CTA leaves
-    if (warp == 0)
-        for (uint32_t i = 0; i < kStages && i < fetched - first; ++i)
-            mbar_wait(full(i), ((fetched - first - 1 - i) / kStages) & 1u, limit_ns);
+    // the warps' sums, then the cluster's
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int q = 0; q < kDotTokens; ++q) {
+            int32_t v = dot[r][q];
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+            if (t == static_cast<uint32_t>(q)) atomicAdd(sums + q * kDotRows + block * 32 + r * 8 + g, v);
+        }
+    gemm::cluster_sync();
+    // each CTA finishes its share of the outputs: rows of the weight by rank
+    const uint32_t each = kDotRows / split;
+    for (uint32_t o = threadIdx.x; o < each * P.m; o += kDotThreads) {
+        const uint32_t token = o / each, r = rank * each + o % each, col = n0 + r;
+        int32_t sum = 0;
+        for (uint32_t p = 0; p < split; ++p)
+            sum += ld_cluster_s32(gemm::peer_addr(smem_addr(sums + token * kDotRows + r), p));
+        if (col < P.n) store_outputs<1>(P, token, col, __ldg(P.col_scale + col), scales + token, &sum, 1);
+    }
+    gemm::cluster_sync();                       // no CTA leaves while another reads its sums
 }
 
 // ------------------------------------------------------------------ tcgen05
@@ -307,10 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_dots_kernel(const __grid_cons
 // instruction, left the memory at 4.2 TB/s, and at less with more loads in
 // flight: a line's four sectors came in four requests.)
 constexpr int kPiece = 128;
-#ifndef ASR_FEW_SETS
-#define ASR_FEW_SETS 2
-#endif
-constexpr int kSets = ASR_FEW_SETS;                        // of four widening warps
+constexpr int kSets = 2;                        // of four widening warps
 constexpr int kWidener = 6;                     // first widening warp
 constexpr int kFewThreads = 32 * (kWidener + 4 * kSets + 1);
 constexpr uint32_t kRing = 4;                   // pieces in tensor memory
@@ -665,8 +653,10 @@ asr_status setup(int *sms)
         e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(few_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
-        cudaFuncAttributes fa;                  // loads the kernel, so that its first launch may be captured
-        if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, few_dots_kernel);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(few_dots_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDotSmem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(few_dots_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDotSmem);
         if (e != cudaSuccess) return cuda_fail(e);
         g_few_sms[dev] = n;
     }
@@ -688,7 +678,49 @@ asr_status make_map_int8(CUtensorMap *map, const int8_t *ptr, uint64_t rows, uin
     return r == CUDA_SUCCESS ? ASR_OK : ASR_ERR_INVALID_VALUE;
 }
 
-bool dots(uint64_t m) { return m <= kDotTokens; }       // the tokens are given as integers then
+// CTAs that share a row block's K: enough to give every SM one, none of them
+// less than a round.
+uint32_t dot_split(uint64_t n, uint64_t k)
+{
+    const uint64_t tiles = (n + kDotRows - 1) / kDotRows, rounds = (k + kSlab - 1) / kSlab;
+    uint32_t split = 1;
+    while (split < kDotSplit && 2 * split <= rounds && tiles * split < 152) split *= 2;
+    return split;
+}
+
+uint64_t dot_share(uint64_t n, uint64_t k)
+{
+    const uint32_t split = dot_split(n, k);
+    return ((k + kSlab - 1) / kSlab + split - 1) / split * kSlab;
+}
+
+// Whether the dot products' kernel takes m tokens: their shares have to fit its shared memory.
+bool dots(uint64_t m, uint64_t n, uint64_t k) { return m <= kDotTokens && m * dot_share(n, k) <= kDotSmem; }
+
+asr_status run_dots(DotParams &P, bool quantise, cudaStream_t stream)
+{
+    int sms = 0;
+    const asr_status st = setup(&sms);
+    if (st != ASR_OK) return st;
+    const uint32_t split = dot_split(P.n, P.k);
+    P.share = static_cast<uint32_t>(dot_share(P.n, P.k));
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((P.n + kDotRows - 1) / kDotRows * split, 1, 1);
+    cfg.blockDim = dim3(kDotThreads, 1, 1);
+    cfg.dynamicSmemBytes = P.m * P.share;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = quantise ? cudaLaunchKernelEx(&cfg, few_dots_kernel<true>, P)
+                                   : cudaLaunchKernelEx(&cfg, few_dots_kernel<false>, P);
+    if (e != cudaSuccess) return cuda_fail(e);
+    return launched(ASR_KERNEL_INT8_FEW_ROWS);
+}
 
 uint32_t passes(uint64_t m) { return static_cast<uint32_t>((m + kMaxTokens - 1) / kMaxTokens); }
 
@@ -698,38 +730,30 @@ asr_status run(Params &P, cudaStream_t stream)
     int sms = 0;
     asr_status st = setup(&sms);
     if (st != ASR_OK) return st;
-    const uint32_t wide = dots(P.m) ? kSlab : kPiece;
     P.tiles = (P.n + kRows - 1) / kRows;
-    P.pieces = (P.k + wide - 1) / wide;
+    P.pieces = (P.k + kPiece - 1) / kPiece;
     const uint64_t total = static_cast<uint64_t>(P.tiles) * P.pieces;
     if (total >= (1ull << 31)) return ASR_ERR_INVALID_VALUE;
-    const uint32_t grid = static_cast<uint32_t>(total < static_cast<uint64_t>(sms) ? total : sms);
+    const uint32_t p = passes(P.m);
+    P.each = ((P.m + p - 1) / p + 15) / 16 * 16;
+    CUtensorMap map, map_w;
+    st = prod::make_map_2d(&map, P.a, P.m, P.k, P.lda, P.each);
+    if (st == ASR_OK && P.b_vec) st = make_map_int8(&map_w, P.b, P.n, P.k, P.ldb);
+    if (st != ASR_OK) return st;
+    if (!P.b_vec) map_w = map;                  // not read
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(total < static_cast<uint64_t>(sms) ? static_cast<uint32_t>(total) : static_cast<uint32_t>(sms),
+                       (P.m + P.each - 1) / P.each, 1);
+    cfg.blockDim = dim3(kFewThreads, 1, 1);
+    cfg.dynamicSmemBytes = few_shape(P.each).bytes;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3(grid, 1, 1);
     const uint64_t limit = kWaitLimitNs;
-    cudaError_t e;
-    if (dots(P.m)) {
-        cfg.blockDim = dim3(kThreads, 1, 1);
-        e = cudaLaunchKernelEx(&cfg, few_dots_kernel, P, limit);
-    } else {
-        const uint32_t p = passes(P.m);
-        P.each = ((P.m + p - 1) / p + 15) / 16 * 16;
-        CUtensorMap map, map_w;
-        st = prod::make_map_2d(&map, P.a, P.m, P.k, P.lda, P.each);
-        if (st == ASR_OK && P.b_vec) st = make_map_int8(&map_w, P.b, P.n, P.k, P.ldb);
-        if (st != ASR_OK) return st;
-        if (!P.b_vec) map_w = map;                  // not read
-        cfg.gridDim.y = (P.m + P.each - 1) / P.each;
-        cfg.blockDim = dim3(kFewThreads, 1, 1);
-        cfg.dynamicSmemBytes = few_shape(P.each).bytes;
-        e = cudaLaunchKernelEx(&cfg, few_rows_kernel, map, map_w, P, limit);
-    }
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, few_rows_kernel, map, map_w, P, limit);
     if (e != cudaSuccess) return cuda_fail(e);
     return launched(ASR_KERNEL_INT8_FEW_ROWS);
 }

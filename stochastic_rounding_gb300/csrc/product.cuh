@@ -56,7 +56,7 @@ constexpr int kBlock = 16;                      // columns an epilogue warp fini
 constexpr uint32_t kWarpStage = 32 * kBlock * 4;
 constexpr int kBarBytes = (kBars * 8 + 16 + 127) / 128 * 128;
 constexpr int kSmem = 1024 + kStages * kStageBytes + kBarBytes + kEpi * kWarpStage;
-constexpr int kGroupM = 8;
+constexpr int kGroupM = 16;                     // tile order: rows of tiles walked across together (8: 1 % slower)
 constexpr int kMaxBatch = 64;                   // matrices per launch
 
 // What the epilogue makes of a sum.  "Stored" values are f16 at 2^12 times the

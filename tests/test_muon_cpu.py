@@ -107,7 +107,7 @@ def test_int8_checks(L):
     assert q(P, 1, 8, 8, 8, 0, P, 8, P, 1, 2**64 - 3, 1, 0, None) == bad
     assert q(None, 1, 0, 8, 8, 0, None, 8, None, 1, 0, 1, 0, None) == ok
     g = L.asr_gemm_int8_sr
-    args = dict(a=P, lda=32, b=P, ldb=32, sa=P, sb=P, c=P, ldc=8, cdt=1, m=4, n=8, k=32, r=1, step=0, seed=0, ws=P,
+    args = dict(a=P, lda=32, b=P, ldb=32, sa=P, sb=P, c=P, ldc=8, cdt=1, m=40, n=8, k=32, r=1, step=0, seed=0, ws=P,
                 size=1 << 30, stream=None)
     for kw in (dict(a=None), dict(sb=None), dict(lda=31), dict(ldc=7), dict(k=0), dict(k=131072), dict(m=2**25),
                dict(ws=None), dict(size=0), dict(c=ctypes.c_void_p(4097))):
@@ -115,7 +115,7 @@ def test_int8_checks(L):
     assert g(*{**args, "cdt": 7}.values()) == dt and g(*{**args, "r": 7}.values()) == dt
     assert g(*{**args, "m": 0}.values()) == ok
     lin = L.asr_linear_int8
-    args = dict(x=P, xdt=1, x_ld=32, w=P, ldw=32, sw=P, y=P, ldy=8, ydt=1, m=4, n=8, k=32, r=1, step=0, seed=0, ws=P,
+    args = dict(x=P, xdt=1, x_ld=32, w=P, ldw=32, sw=P, y=P, ldy=8, ydt=1, m=40, n=8, k=32, r=1, step=0, seed=0, ws=P,
                 size=1 << 30, stream=None)
     for kw in (dict(x=None), dict(sw=None), dict(x_ld=31), dict(ldy=7), dict(k=0), dict(ws=None), dict(size=0)):
         assert lin(*{**args, **kw}.values()) == bad, kw
