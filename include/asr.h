@@ -54,8 +54,10 @@
  *     asr_adamw_sr_multi_tensor_static keeps its table in one shared device
  *     array, so its calls must not overlap one another on the GPU.
  *   - CUDA graphs: asr_philox4x32, asr_stochastic_round_bf16,
- *     asr_adamw_sr_step, asr_adamw_sr_multi_tensor and asr_gemm_bf16_sr may
- *     be captured into a graph (stream capture) once a call of the same
+ *     asr_adamw_sr_step, asr_adamw_sr_multi_tensor, asr_gemm_bf16_sr,
+ *     asr_newton_schulz, asr_muon_sr_multi_tensor, asr_quantize_int8,
+ *     asr_gemm_int8_sr, asr_linear_int8 and asr_linear_int8_grads may be
+ *     captured into a graph (stream capture) once a call of the same
  *     entry point with work to do has run on the device outside any capture
  *     -- that first call sets up the launch shapes of every kernel the entry
  *     point may pick on that device (for the two AdamW entry points, of
@@ -350,7 +352,7 @@ asr_status asr_muon_workspace(const asr_muon_desc *table, int32_t n, uint64_t *b
  * that holds an infinity or a NaN gives zeros and a scale that is not finite,
  * so that its products are NaN.
  * ASR_ROWS: q is rows x cols, q_ld >= cols bytes between rows, scale has `rows`
- * entries.  ASR_COLUMNS: q is stored transposed, cols x rows, q_ld >= rows, and
+ * entries.  ASR_COLUMNS (rows at most 4,194,240): q is stored transposed, cols x rows, q_ld >= rows, and
  * scale has `cols` entries.  Bytes between a row's end and the next row are
  * not written. */
 typedef enum { ASR_ROWS = 0, ASR_COLUMNS = 1 } asr_axis;

@@ -592,6 +592,8 @@ def _workspace(workspace, need, device, stream):
     memory of the call's stream, given back to torch's allocator after the
     call (which hands it out again only to later work of that stream)."""
     torch = _torch()
+    if need == 0 and workspace is None:
+        return None, None, 0
     if workspace is None and stream is None:
         buf = torch.empty(need, dtype=torch.uint8, device=device)
         return buf, buf.data_ptr(), need

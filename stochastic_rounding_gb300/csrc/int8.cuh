@@ -13,7 +13,18 @@
 // integer kind; an 8-bit integer is exact in f16, a product of two in binary32,
 // and so is any sum of 1,024 of them (1,024 * 128^2 = 2^24).  So the operands
 // are widened to f16 in the workspace, product.cuh sums chunks of 1,024 in
-// tensor memory at the f16 rate, and its epilogue adds the chunks in int32.
+// tensor memory at the f16 rate, and its epilogue adds the chunks in int32.  With
+// few rows of A the weight is read as it is (int8_few.cuh).
+//
+// Widening costs three bytes' traffic an element, once: 52 us of 610 for tokens
+// 8,192 x 4,096 and a weight 14,336 x 4,096 (310 MB, 6.0 TB/s).  Widening inside
+// the product instead would cost shared memory two bytes written and one read an
+// element and tile next to the 64 bytes a cycle that the products read, more than
+// its 128.  The gradients' operands are quantised where they lie and read across,
+// in two streams: maxima (4,096 tokens, 8,192 x 2,048: 117 MB, 24 us), then the
+// integers, dy's by rows and by columns from one read and one set of random bits
+// (301 MB, 77 us; bound by instructions: 15 an element for Philox, 5 for each
+// rounding).
 
 namespace int8 {
 
@@ -491,6 +502,32 @@ void lay_out(SideParams &M)
     }
 }
 
+// Every kernel of this file and of the products ready on the device, whichever a call takes.
+asr_status setup()
+{
+    static std::atomic<uint64_t> ready{0};
+    int pairs = 0, sms = 0, dev = 0;
+    asr_status st = prod::setup(&pairs);
+    if (st == ASR_OK) st = int8few::setup(&sms);
+    if (st != ASR_OK) return st;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (e == cudaSuccess && (ready.load(std::memory_order_acquire) & bit)) return ASR_OK;
+    if (e == cudaSuccess) e = prod::load_kernel(few_prep_kernel);
+    if (e == cudaSuccess) e = prod::load_kernel(quantise_rows_kernel<false, false>);
+    if (e == cudaSuccess) e = prod::load_kernel(quantise_rows_kernel<true, false>);
+    if (e == cudaSuccess) e = prod::load_kernel(quantise_rows_kernel<false, true>);
+    if (e == cudaSuccess) e = prod::load_kernel(quantise_columns_kernel<false>);
+    if (e == cudaSuccess) e = prod::load_kernel(quantise_columns_kernel<true>);
+    if (e == cudaSuccess) e = prod::load_kernel(column_scale_kernel);
+    if (e == cudaSuccess) e = prod::load_kernel(widen_kernel);
+    if (e == cudaSuccess) e = prod::load_kernel(max_kernel);
+    if (e == cudaSuccess) e = prod::load_kernel(wide_kernel);
+    if (e != cudaSuccess) return cuda_fail(e);
+    ready.fetch_or(bit, std::memory_order_release);
+    return ASR_OK;
+}
+
 asr_status quantize(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, uint64_t x_ld, int32_t axis, int8_t *q,
                     uint64_t q_ld, float *scale, uint32_t rounding, uint64_t base, uint32_t step, uint64_t seed,
                     cudaStream_t stream)
@@ -502,8 +539,10 @@ asr_status quantize(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, 
     if (!x || !q || !scale || !muon::element_aligned(x, dtype) || !muon::element_aligned(scale, ASR_F32))
         return ASR_ERR_INVALID_VALUE;
     if (!quantisable(rows, cols) || !pitch_ok(x_ld, cols) || !pitch_ok(q_ld, axis == ASR_ROWS ? cols : rows) ||
-        base > UINT64_MAX - rows * cols)
+        base > UINT64_MAX - rows * cols || (axis == ASR_COLUMNS && (rows + 63) / 64 > 65535))
         return ASR_ERR_INVALID_VALUE;
+    asr_status st = setup();
+    if (st != ASR_OK) return st;
     const bool sr = rounding == ASR_ROUND_SR;
     if (axis == ASR_ROWS) {
         RowParams P;
@@ -525,7 +564,6 @@ asr_status quantize(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, 
         else quantise_rows_kernel<false, false><<<grid, kThreads, 0, stream>>>(P, grid);
         return launched(ASR_KERNEL_QUANTIZE);
     }
-    if ((rows + 63) / 64 > 65535) return ASR_ERR_INVALID_VALUE;
     const cudaError_t e = cudaMemsetAsync(scale, 0, cols * sizeof(float), stream);
     if (e != cudaSuccess) return cuda_fail(e);
     SideParams M;
@@ -535,7 +573,7 @@ asr_status quantize(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, 
     M.count = 1;
     lay_out(M);
     max_kernel<<<M.blocks, kThreads, 0, stream>>>(M);
-    asr_status st = launched(ASR_KERNEL_QUANTIZE);
+    st = launched(ASR_KERNEL_QUANTIZE);
     if (st != ASR_OK) return st;
     ColumnParams P;
     P.x = x;
@@ -593,14 +631,6 @@ Layout layout(uint64_t m, uint64_t n, uint64_t k)
     L.b = L.a + muon::up(m * L.ld * 2, 256);
     L.bytes = few(m) ? L.b : L.b + muon::up(n * L.ld * 2, 256);
     return L;
-}
-
-// Every kernel of the products ready on this device, whichever a call takes.
-asr_status setup()
-{
-    int pairs = 0, sms = 0;
-    const asr_status st = prod::setup(&pairs);
-    return st == ASR_OK ? int8few::setup(&sms) : st;
 }
 
 struct Output {

@@ -2,16 +2,7 @@
 // bounds it is reading B (the weight) once.  Included into asr.cu (inside its
 // anonymous namespace), before int8.cuh.
 //
-// The work is cut into pieces, 128 rows of B by a stretch of K, and every CTA
-// (one on each SM) takes the same number of consecutive ones, across row blocks
-// where they end: all SMs read the same share of the weight, whatever its shape.
-// The int32 sums of a row block that several CTAs share are added up in the
-// workspace, and the CTA that completes the block's count of pieces writes its
-// outputs.  Integer sums are the same in every order, and nobody waits for
-// anybody.  A warp streams its rows of the weight from global memory straight
-// into registers, several pieces ahead.
-//
-// Two kernels; the first is for so few tokens that no tensor core is needed:
+// Two kernels:
 //   few_dots_kernel    up to 4 tokens: dot products of four bytes (dp4a), 16
 //                      instructions for a lane's four rows of 16 bytes;
 //   few_rows_kernel    up to 128 tokens a pass: tcgen05.mma with the weight as
@@ -22,9 +13,13 @@
 //                      arrive.  The tokens are the B operand, from shared memory.
 //                      mma.sync takes 2 cycles an SM for 256 bytes and 8 tokens
 //                      (measured: 1.05 ns), so beyond 16 tokens it falls behind
-//                      the memory: 40 us against 58.7 MB and 33 tokens.
+//                      the memory: 40 us for 58.7 MB and 33 tokens.
 // At most 1,024 products are added in binary32, which is exact; int32 then.
-// (What follows of pieces and shared sums is the second kernel's.)
+//
+// Measured on a weight of 14,336 x 4,096 (58.7 MB, 8.6 us at the copy rate), with
+// the launch: 1 token 14.4 us, 4 17.5, 16 20.5, 33 23.8, 64 26, 128 39; on one
+// eight times as large 1 token 87 us (5.4 TB/s), 33 tokens 92.  What is left at
+// the small end is latency: launch, first weights, quantiser, last sums.
 
 namespace int8few {
 
@@ -288,7 +283,15 @@ __global__ void __launch_bounds__(kDotThreads, 2) few_dots_kernel(const __grid_c
 
 // ------------------------------------------------------------------ tcgen05
 //
-// A piece is 128 rows by 128 of K.  Warp 0 brings the tokens (two boxes of 64
+// The work is cut into pieces, 128 rows of B by 128 of K, and every CTA (one on
+// each SM) takes the same number of consecutive ones, across row blocks where
+// they end: all SMs read the same share of the weight, whatever its shape.  The
+// int32 sums of a row block that several CTAs share are added up in the
+// workspace, and the CTA that completes the block's count of pieces writes its
+// outputs.  Integer sums are the same in every order, and nobody waits for
+// anybody.
+//
+// Warp 0 brings the tokens (two boxes of 64
 // of K, 128-byte swizzle), warp 14 the weight's bytes (one box of 128 x 128,
 // likewise), warp 1 issues the products, warps 2 to 5 read the sums (after 1,024
 // of K or at the end of a row block) and finish them, warps 6 to 13 widen the

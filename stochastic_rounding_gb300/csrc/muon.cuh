@@ -6,11 +6,13 @@
 //   S   = X X^T (rows <= cols) or X^T X
 //   X'  = a X + (b S + c S S) X, or X (..) on the other side;   `steps` times
 //
-// The step's two outer stages stream the matrix once each: sums of squares (and
-// the momentum, for Muon) in one kernel, the scaled f16 copy in the next; the
-// products are product.cuh's, and the last one's epilogue writes the caller's
-// matrix -- the bf16 result, or the parameter itself, decayed, stepped and
-// rounded with its own random bits.  With P = a I + b S + c S S formed by the
+// Matrices whose smaller side is at most 128 (the larger at most 4,096) take one
+// launch (skinny.cuh).  The others are streamed once each by two kernels: sums of
+// squares (and the momentum, for Muon), then the scaled f16 copy (8 x 2,048^2,
+// Muon: 54 and 49 us for 335 and 268 MB, 6.2 and 5.5 TB/s); the products are
+// product.cuh's, all matrices of one shape in each launch, and the last one's
+// epilogue writes the caller's matrix -- the bf16 result, or the parameter
+// itself, decayed, stepped and rounded with its own random bits.  With P = a I + b S + c S S formed by the
 // epilogue of S S, a step is three products: S and S S (symmetric: half the
 // tiles), and P X.  m = min(rows, cols), n = max: 3 m^2 n + m^3 multiplications
 // and additions a step.
@@ -18,7 +20,7 @@
 // Number format.  Every matrix between the products is f16 at 2^12 times its
 // value.  Singular values start at or below 1 and the polynomial keeps them
 // small (checked on the host for the coefficients of the call), an entry is
-// never larger than the largest singular value, so 2^12 leaves a factor of 8
+// never larger than the largest singular value, so 2^12 leaves a factor of 16
 // to f16's largest number and puts its smallest normal number at 1.5e-8 --
 // below the entries of S (about n^-1.5) that a matrix of any practical size
 // has.  f16 keeps three more bits than bf16 at the same tensor rate, which the
@@ -330,8 +332,12 @@ asr_status prep(const Group &G, const NsParams &ns, const Layout &L, char *ws, f
 std::mutex g_skinny_mu;
 bool g_skinny_ready[kMaxDevices];
 
-asr_status skinny_setup()
+// Every kernel of this file and of the products ready on the device.
+asr_status setup()
 {
+    int pairs = 0;
+    const asr_status st = prod::setup(&pairs);
+    if (st != ASR_OK) return st;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
@@ -341,6 +347,10 @@ asr_status skinny_setup()
         e = cudaFuncSetAttribute(skinny_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSkinnySmem);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(skinny_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSkinnySmem);
+        if (e == cudaSuccess) e = prod::load_kernel(square_sum_kernel<false>);
+        if (e == cudaSuccess) e = prod::load_kernel(square_sum_kernel<true>);
+        if (e == cudaSuccess) e = prod::load_kernel(scale_kernel<false>);
+        if (e == cudaSuccess) e = prod::load_kernel(scale_kernel<true>);
         if (e != cudaSuccess) return cuda_fail(e);
         g_skinny_ready[dev] = true;
     }
@@ -351,8 +361,6 @@ template <bool MUON>
 asr_status skinny(const Group &G, const NsParams &ns, const prod::Params &last, float mu, bool nesterov,
                   cudaStream_t stream)
 {
-    asr_status st = skinny_setup();
-    if (st != ASR_OK) return st;
     SkinnyParams P;
     std::memset(&P, 0, sizeof(P));
     prep_params(P.in, G, ns, mu, nesterov);
@@ -638,8 +646,7 @@ asr_status newton_schulz(const asr_matrix_desc *table, int32_t n, const asr_ns_p
     asr_status st = flatten(table, n, flat);
     if (st != ASR_OK || flat.empty()) return st;
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < workspace(flat)) return ASR_ERR_INVALID_VALUE;
-    int pairs = 0;
-    st = prod::setup(&pairs);
+    st = setup();
     if (st != ASR_OK) return st;
     return for_groups(flat, [&](const Group &G) {
         const Layout L = layout(G.rows, G.cols, G.batch);
@@ -674,8 +681,7 @@ asr_status step(const asr_muon_desc *table, int32_t n, const asr_muon_hparams *h
     st = flatten(table, n, flat);
     if (st != ASR_OK || flat.empty()) return st;
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < workspace(flat)) return ASR_ERR_INVALID_VALUE;
-    int pairs = 0;
-    st = prod::setup(&pairs);
+    st = setup();
     if (st != ASR_OK) return st;
     return for_groups(flat, [&](const Group &G) {
         const Layout L = layout(G.rows, G.cols, G.batch);

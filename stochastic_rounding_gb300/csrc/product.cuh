@@ -18,7 +18,17 @@
 //     diagonal and writes each of the others as a mirror image: half the work;
 //   - the sum over K may be cut into chunks, each accumulated on its own and
 //     added up by the epilogue in int32 (8-bit integers, whose chunk sums are
-//     exact in binary32).
+//     exact in binary32);
+//   - sixteen epilogue warps: a tile's epilogue is exposed at a launch's end (last
+//     products of ortho and Muon steps 31 and 87 us, with eight warps that took 32
+//     columns at a time 49 and 111 us);
+//   - the tiles of a last round that would leave most pairs idle go in halves or
+//     quarters of their columns.
+// What bounds it: large products run at the tensor cores' sustained rate under
+// the power limit (8,192 x 14,336 x 4,096 integers: 520 us alone, 1,850 TFLOP/s);
+// short ones at the L2's (a 256 x 256 tile moves 64 bytes a cycle and SM), or,
+// below about 10 us, at the chain of launch (1.4 us after the last kernel's end),
+// first copies (1.6 us), epilogue and exit (2 us).
 //
 // A K-half of a stage (64 of K, 16 KB an operand and CTA) in shared memory:
 //   K-major    128 rows of 128 bytes, 128-byte swizzle; a K=16 step is 32 bytes;
@@ -642,6 +652,14 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 std::mutex g_prod_mu;
 bool g_prod_ready[kMaxDevices];
 int g_prod_pairs[kMaxDevices];
+
+// Loads a kernel, so that its first launch may be in a stream capture.
+template <typename K>
+cudaError_t load_kernel(K kernel)
+{
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, kernel);
+}
 
 template <bool A_MN, bool B_MN, int OP>
 cudaError_t setup_one(int sms, int *pairs)

@@ -270,6 +270,36 @@ def test_linear_from_either_type_strided(asr, dtype, size):
     assert none is None and torch.equal(only, dw)
 
 
+@pytest.mark.parametrize("tokens", [2, 30, 200])
+def test_captured_into_a_graph(asr, tokens):
+    """A replay gives the direct calls' bits, on inputs that changed since the capture."""
+    import torch
+    torch.manual_seed(tokens)
+    n, k = 300, 1030
+    w = torch.randn(n, k, device="cuda", dtype=torch.bfloat16)
+    x = torch.randn(tokens, k, device="cuda", dtype=torch.bfloat16)
+    dy = torch.randn(tokens, n, device="cuda", dtype=torch.bfloat16)
+    qw, sw = asr.int8_empty(n, k), torch.empty(n, device="cuda")
+    y, dx, dw = (torch.empty(*s, device="cuda", dtype=torch.bfloat16) for s in ((tokens, n), (tokens, k), (n, k)))
+
+    def call():
+        asr.asr_quantize_int8(w, qw, sw)
+        asr.int8_linear(x, qw, sw, out=y, rounding="sr", step=1)
+        asr.asr_linear_int8_grads(dy, x, w, dx, dw, step=2)
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for t in (w, x, dy):
+        t.copy_(torch.randn_like(t))
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [host(t) for t in (y, dx, dw, sw)]
+    call()
+    for a, b in zip(got, (y, dx, dw, sw)):
+        assert_same_bits(a, host(b))
+
+
 def test_linear_module_gradients_against_differences(asr):
     """Int8Linear's gradients along a direction against differences of the
     unquantised layer.  One entry of an operand is off by at most half a step

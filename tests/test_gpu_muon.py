@@ -267,6 +267,27 @@ def test_streams_graph_and_workspace(asr):
         asr.asr_newton_schulz([(g, out)], workspace=ws[:-256])
 
 
+def test_muon_step_captured_into_a_graph(asr):
+    import torch
+    torch.manual_seed(3)
+    sets = [(torch.randn(s, device="cuda").bfloat16(), torch.randn(s, device="cuda"), torch.zeros(s, device="cuda"), 4)
+            for s in ((2, 90, 300), (200, 260), (260, 200))]
+    again = [tuple(t.clone() for t in s[:3]) + s[3:] for s in sets]
+    kw = dict(lr=0.02, step=9, seed=1)
+    asr.asr_muon_sr_multi_tensor([tuple(t.clone() for t in s[:3]) + s[3:] for s in sets], **kw)
+    ws = torch.empty(asr.asr_muon_workspace(sets), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        asr.asr_muon_sr_multi_tensor(sets, workspace=ws, **kw)
+    for _ in range(2):
+        graph.replay()
+        asr.asr_muon_sr_multi_tensor(again, **kw)
+    torch.cuda.synchronize()
+    for a, b in zip(sets, again):
+        assert_same_bits(host(a[0]), host(b[0]))
+        assert_same_bits(host(a[2]), host(b[2]))
+
+
 def test_refusals(asr):
     import torch
     g = torch.randn(8, 16, device="cuda")
