@@ -16,8 +16,8 @@ HDR = os.path.join(ROOT, "include", "asr.h")
 # textually included by asr.cu (one translation unit)
 INCLUDED = [os.path.join(HERE, "csrc", f) for f in (
     "common.cuh", "pipeline.cuh", "adamw_kernels.cuh", "rounding_kernels.cuh", "static_table.cuh",
-    "host_pipeline.cuh", "gemm_sr.cuh", "product.cuh", "muon.cuh", "skinny.cuh", "int8_levels.cuh", "int8_few.cuh",
-    "int8.cuh")]
+    "host_pipeline.cuh", "gemm_sr.cuh", "product.cuh", "muon.cuh", "skinny.cuh", "int8_product.cuh",
+    "int8_levels.cuh", "int8_few.cuh", "int8.cuh")]
 LIB = os.path.join(HERE, "libasr.so")
 
 NVCC_FLAGS = [

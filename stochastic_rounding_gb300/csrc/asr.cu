@@ -582,6 +582,7 @@ std::atomic<uint64_t> g_philox_ready{0}, g_round_ready{0};
 #include "gemm_sr.cuh"
 #include "product.cuh"
 #include "muon.cuh"
+#include "int8_product.cuh"
 #include "int8_levels.cuh"
 #include "int8_few.cuh"
 #include "int8.cuh"

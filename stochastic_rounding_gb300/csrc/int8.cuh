@@ -507,7 +507,7 @@ asr_status setup()
 {
     static std::atomic<uint64_t> ready{0};
     int pairs = 0, sms = 0, dev = 0;
-    asr_status st = prod::setup(&pairs);
+    asr_status st = prod::int8_setup(&pairs);
     if (st == ASR_OK) st = int8few::setup(&sms);
     if (st != ASR_OK) return st;
     cudaError_t e = cudaGetDevice(&dev);
@@ -653,15 +653,11 @@ asr_status output_kind(const Output &o)
     return ASR_OK;
 }
 
-// The product of widened operands.
-template <bool A_MN, bool B_MN>
-asr_status product(const prod::Stored &a, const prod::Stored &b, const float *sa, const float *sb, const Output &o,
-                   cudaStream_t stream)
+// The output's fields of a product of widened operands.
+prod::Params product_params(const float *sa, const float *sb, const Output &o)
 {
     prod::Params P;
     std::memset(&P, 0, sizeof(P));
-    P.batch = 1;
-    P.chunk = kChunk;
     P.out_ld = o.ld;
     P.out_dtype = static_cast<uint32_t>(o.dtype);
     P.rounding = o.rounding;
@@ -671,7 +667,17 @@ asr_status product(const prod::Stored &a, const prod::Stored &b, const float *sa
     P.col_scale = sb;
     P.keys = make_keys(o.seed);
     P.slot[0].ptr = o.c;
-    return prod::launch<A_MN, B_MN, prod::kInt8>(a, b, P, ASR_KERNEL_PRODUCT, stream);
+    return P;
+}
+
+asr_status product(const prod::Stored &a, const prod::Stored &b, const float *sa, const float *sb, const Output &o,
+                   cudaStream_t stream)
+{
+    prod::Int8Products L;
+    prod::Stored operands[4];
+    std::memset(&L, 0, sizeof(L));
+    prod::int8_add(L, operands, a, false, b, false, product_params(sa, sb, o));
+    return prod::int8_launch(L, operands, kChunk, stream);
 }
 
 prod::Stored stored(__half *p, uint64_t rows, uint64_t cols, uint64_t ld)
@@ -781,7 +787,7 @@ asr_status gemm(const int8_t *a, uint64_t lda, const int8_t *b, uint64_t ldb, co
     widen_kernel<<<blocks_for((m + n) * ((k + 511) / 512), 8, 1216), kThreads, 0, stream>>>(W);
     st = launched(ASR_KERNEL_QUANTIZE);
     if (st != ASR_OK) return st;
-    return product<false, false>(stored(W.dst[0], m, k, L.ld), stored(W.dst[1], n, k, L.ld), sa, sb, o, stream);
+    return product(stored(W.dst[0], m, k, L.ld), stored(W.dst[1], n, k, L.ld), sa, sb, o, stream);
 }
 
 // ---- the linear layer's calls
@@ -827,7 +833,7 @@ asr_status linear(const void *x, int32_t x_dtype, uint64_t x_ld, const int8_t *q
     quantise_rows_kernel<false, true><<<row_blocks + more, kThreads, 0, stream>>>(P, row_blocks);
     st = launched(ASR_KERNEL_QUANTIZE);
     if (st != ASR_OK) return st;
-    return product<false, false>(stored(static_cast<__half *>(P.q), m, k, L.ld), stored(P.w.dst[0], n, k, L.ld),
+    return product(stored(static_cast<__half *>(P.q), m, k, L.ld), stored(P.w.dst[0], n, k, L.ld),
                                  P.scale, sw, o, stream);
 }
 
@@ -936,13 +942,17 @@ asr_status grads(const GradSource &dy, const GradSource &x, const GradSource &w,
     if (st != ASR_OK) return st;
     wide_kernel<<<M.blocks, kThreads, 0, stream>>>(M);
     st = launched(ASR_KERNEL_QUANTIZE);
-    if (st == ASR_OK && dx)
-        st = product<false, true>(stored(halves(L.dy_row), t, n, L.ldn), stored(halves(L.w), n, k, L.ldk),
-                                  floats(L.row), floats(L.col_w), ox, stream);
-    if (st == ASR_OK && dw)
-        st = product<true, true>(stored(halves(L.dy_col), t, n, L.ldn), stored(halves(L.x), t, k, L.ldk),
-                                 floats(L.col_dy), floats(L.col_x), ow, stream);
-    return st;
+    if (st != ASR_OK) return st;
+    prod::Int8Products P;
+    prod::Stored operands[4];
+    std::memset(&P, 0, sizeof(P));
+    if (dx)
+        prod::int8_add(P, operands, stored(halves(L.dy_row), t, n, L.ldn), false, stored(halves(L.w), n, k, L.ldk), true,
+                       product_params(floats(L.row), floats(L.col_w), ox));
+    if (dw)
+        prod::int8_add(P, operands, stored(halves(L.dy_col), t, n, L.ldn), true, stored(halves(L.x), t, k, L.ldk), true,
+                       product_params(floats(L.col_dy), floats(L.col_x), ow));
+    return prod::int8_launch(P, operands, kChunk, stream);
 }
 
 }  // namespace int8

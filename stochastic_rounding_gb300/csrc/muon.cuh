@@ -414,34 +414,33 @@ asr_status iterate(const Group &G, const NsParams &ns, const Layout &L, char *ws
     for (uint32_t i = 0; st == ASR_OK && i < ns.steps; ++i) {
         prod::Params P = last;
         P.batch = G.batch;
-        P.chunk = 1u << 30;
         P.alpha = down;
         P.ld = static_cast<uint32_t>(S.ld);
         P.stride = S.stride;
         P.out = S.ptr;
-        st = tall ? prod::launch<true, true, prod::kGram>(x, x, P, ASR_KERNEL_PRODUCT, stream)
-                  : prod::launch<false, false, prod::kGram>(x, x, P, ASR_KERNEL_PRODUCT, stream);
+        st = tall ? prod::launch<true, true, prod::kGram>(x, x, P, stream)
+                  : prod::launch<false, false, prod::kGram>(x, x, P, stream);
         if (st != ASR_OK) break;
         P.alpha = static_cast<float>(ns.c) * down;
         P.beta = static_cast<float>(ns.b);
         P.diag = static_cast<float>(ns.a) * kStore;
         P.aux = S.ptr;
         P.out = Q.ptr;
-        st = prod::launch<false, false, prod::kPoly>(S, S, P, ASR_KERNEL_PRODUCT, stream);
+        st = prod::launch<false, false, prod::kPoly>(S, S, P, stream);
         if (st != ASR_OK) break;
         if (i + 1 < ns.steps) {
             P.alpha = down;
             P.ld = static_cast<uint32_t>(y.ld);
             P.stride = y.stride;
             P.out = y.ptr;
-            st = tall ? prod::launch<false, false, prod::kNext>(x, Q, P, ASR_KERNEL_PRODUCT, stream)
-                      : prod::launch<false, true, prod::kNext>(Q, x, P, ASR_KERNEL_PRODUCT, stream);
+            st = tall ? prod::launch<false, false, prod::kNext>(x, Q, P, stream)
+                      : prod::launch<false, true, prod::kNext>(Q, x, P, stream);
             std::swap(x, y);
         } else {
             P.alpha = last.alpha * down * down;
             P.beta = last.beta;
-            st = tall ? prod::launch<false, false, LAST>(x, Q, P, ASR_KERNEL_PRODUCT, stream)
-                      : prod::launch<false, true, LAST>(Q, x, P, ASR_KERNEL_PRODUCT, stream);
+            st = tall ? prod::launch<false, false, LAST>(x, Q, P, stream)
+                      : prod::launch<false, true, LAST>(Q, x, P, stream);
         }
     }
     return st;

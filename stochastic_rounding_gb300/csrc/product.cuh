@@ -1,7 +1,7 @@
 // product.cuh -- batched matrix products with f16 operands on the
-// 5th-generation tensor cores, the core of the Newton-Schulz orthogonalisation
-// (muon.cuh) and of the 8-bit integer product (int8.cuh).  Included into
-// asr.cu (inside its anonymous namespace), after gemm_sr.cuh, whose cluster,
+// 5th-generation tensor cores: the kernel of the Newton-Schulz orthogonalisation
+// (muon.cuh), and what the 8-bit integer product's (int8_product.cuh) shares with
+// it.  Included into asr.cu (inside its anonymous namespace), after gemm_sr.cuh, whose cluster,
 // barrier and tensor-map helpers it uses.
 //
 // out_z = epilogue(A_z . B_z^T) for the matrices z of a stack, with binary32
@@ -16,9 +16,6 @@
 //     the one row-major X, and nothing is ever transposed in memory;
 //   - a product whose result is symmetric computes the tiles on and above the
 //     diagonal and writes each of the others as a mirror image: half the work;
-//   - the sum over K may be cut into chunks, each accumulated on its own and
-//     added up by the epilogue in int32 (8-bit integers, whose chunk sums are
-//     exact in binary32);
 //   - sixteen epilogue warps: a tile's epilogue is exposed at a launch's end (last
 //     products of ortho and Muon steps 31 and 87 us, with eight warps that took 32
 //     columns at a time 49 and 111 us);
@@ -77,7 +74,7 @@ enum Op {
     kNext,      // stored X' = alpha * sum
     kOut,       // caller's bf16 matrix = alpha * sum, to nearest
     kParam,     // caller's parameter p = p * beta - alpha * sum, f32 or rounded to bf16
-    kInt8       // caller's matrix = sum * row scale * column scale
+    kScaled     // caller's matrix = sum * row scale * column scale (int8_product.cuh)
 };
 
 struct Slot {                       // one matrix of the stack: the caller's
@@ -90,7 +87,6 @@ struct Params {
     uint32_t tiles_m, tiles_n, per_matrix;
     uint32_t wide, narrow;          // work items: whole tiles, then parts of the last ones
     uint32_t parts;                 // 1, 2 or 4: a narrow item is 256 / parts columns
-    uint32_t chunk;                 // K slices per accumulation
     float alpha, beta, diag;
     uint32_t ld;                    // stored output (and S): elements between rows
     uint64_t stride;                // and between matrices
@@ -325,7 +321,7 @@ __device__ __forceinline__ void finish_block(const Params &P, uint32_t z, uint32
                 x[q] = __fsub_rn(__fmul_rn(stage[staged(lane, q)], P.beta), __fmul_rn(P.alpha, x[q]));
         }
     }
-    if constexpr (OP == kInt8) {
+    if constexpr (OP == kScaled) {
         const float rs = in ? __ldg(P.row_scale + row) : 0.0f;
 #pragma unroll
         for (int q = 0; q < 16; ++q) x[q] = __fmul_rn(__fmul_rn(x[q], rs), col_scale[q]);
@@ -488,43 +484,37 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         constexpr uint64_t kStepA = A_MN ? 2048 >> 4 : 32 >> 4, kStepB = B_MN ? 2048 >> 4 : 32 >> 4;
         for (uint32_t t = cluster; ok && t < items; t += clusters) {
             const uint32_t idesc = t < P.wide ? kDescWide : desc_narrow;
-            for (uint32_t kc = 0; ok && kc < kblocks; kc += P.chunk, ++i) {
-                const int b = static_cast<int>(i % kAccBufs);
-                const uint32_t ub = i / kAccBufs;
-                if (ub > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(acc_empty(b), (ub - 1) & 1u, limit_ns))) {
+            const int b = static_cast<int>(i % kAccBufs);
+            const uint32_t ub = i++ / kAccBufs;
+            if (ub > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(acc_empty(b), (ub - 1) & 1u, limit_ns))) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t d = tmem + static_cast<uint32_t>(b * kTile);
+            for (uint32_t kb = 0; kb < kblocks; ++kb) {
+                if (!warp_wait(full(s), phase, limit_ns)) {
                     ok = false;
                     break;
                 }
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t d = tmem + static_cast<uint32_t>(b * kTile);
-                const uint32_t kend = kblocks - kc < P.chunk ? kblocks : kc + P.chunk;
-                for (uint32_t kb = kc; kb < kend; ++kb) {
-                    if (!warp_wait(full(s), phase, limit_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint64_t ad = desc_a0 + s * kDescStage, bd = desc_b0 + s * kDescStage;
-                    if (elect_one()) {
+                const uint64_t ad = desc_a0 + s * kDescStage, bd = desc_b0 + s * kDescStage;
+                if (elect_one()) {
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const uint64_t aj = ad + j * kDescHalf, bj = bd + j * kDescHalf;
-                            mma_bf16_pair(d, aj, bj, idesc, (kb != kc || j != 0) ? 1u : 0u);
-                            mma_bf16_pair(d, aj + kStepA, bj + kStepB, idesc, 1u);
-                            mma_bf16_pair(d, aj + 2 * kStepA, bj + 2 * kStepB, idesc, 1u);
-                            mma_bf16_pair(d, aj + 3 * kStepA, bj + 3 * kStepB, idesc, 1u);
-                            mma_commit_pair(empty(s, j));
-                        }
-                    }
-                    __syncwarp();
-                    if (++s == kStages) {
-                        s = 0;
-                        phase ^= 1u;
+                    for (int j = 0; j < 2; ++j) {
+                        const uint64_t aj = ad + j * kDescHalf, bj = bd + j * kDescHalf;
+                        mma_bf16_pair(d, aj, bj, idesc, (kb | j) != 0 ? 1u : 0u);
+                        mma_bf16_pair(d, aj + kStepA, bj + kStepB, idesc, 1u);
+                        mma_bf16_pair(d, aj + 2 * kStepA, bj + 2 * kStepB, idesc, 1u);
+                        mma_bf16_pair(d, aj + 3 * kStepA, bj + 3 * kStepB, idesc, 1u);
+                        mma_commit_pair(empty(s, j));
                     }
                 }
-                if (elect_one()) mma_commit_pair(acc_full(b));
                 __syncwarp();
+                if (++s == kStages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
             }
+            if (elect_one()) mma_commit_pair(acc_full(b));
+            __syncwarp();
         }
         if (elect_one())
             asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(drained)
@@ -537,8 +527,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         const uint32_t group = static_cast<uint32_t>((warp - 2) / 4);
         float *stage = reinterpret_cast<float *>(smem_raw + (bars + kBarBytes - raw) + (warp - 2) * kWarpStage);
         uint32_t i = 0;
-        bool ok = true;
-        for (uint32_t t = cluster; ok && t < items; t += clusters) {
+        for (uint32_t t = cluster; t < items; t += clusters) {
             const Item it = work_item<kSym>(P, t);
             const uint32_t row = it.m0 + rank * 128 + quarter * 32 + lane;
             const uint32_t ncols = it.n0 >= P.n ? 0 : P.n - it.n0 < it.width ? P.n - it.n0 : it.width;
@@ -547,9 +536,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             constexpr bool kStored = OP == kGram || OP == kPoly || OP == kNext;
             const bool rows_in = row - lane < P.m;          // the same for the whole warp
             const uint32_t col0 = it.n0 + c_lo, cols = c_hi > c_lo && rows_in ? c_hi - c_lo : 0;
-            int32_t acc[OP == kInt8 ? kSpan : 1];
             uint32_t prior[OP == kPoly ? kSpan / 2 : 1];
-            float scale[OP == kInt8 ? kSpan / 32 : 1];
             // what the epilogue reads from memory, before it waits for the sums
             if constexpr (OP == kPoly) {
 #pragma unroll
@@ -557,78 +544,33 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     if (static_cast<uint32_t>(c) < cols && row < P.m)
                         ld_global_v8(P.aux + it.z * P.stride + static_cast<uint64_t>(row) * P.ld + col0 + c, prior + c / 2);
             }
-            if constexpr (OP == kInt8) {
-#pragma unroll
-                for (int h = 0; h < kSpan / 32; ++h)
-                    scale[h] = 32u * h + lane < cols ? __ldg(P.col_scale + col0 + 32 * h + lane) : 0.0f;
-            }
-            for (uint32_t kc = 0; kc < kblocks; kc += P.chunk, ++i) {
-                const int b = static_cast<int>(i % kAccBufs);
-                if (!__all_sync(0xFFFFFFFFu, pair_wait(acc_full(b), (i / kAccBufs) & 1u, limit_ns))) {
-                    ok = false;
-                    break;
-                }
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t tq =
-                    tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(b * kTile) + c_lo;
-                // this warp has read its part of accumulator b
-                auto release = [&]() {
+            const int b = static_cast<int>(i % kAccBufs);
+            if (!__all_sync(0xFFFFFFFFu, pair_wait(acc_full(b), (i++ / kAccBufs) & 1u, limit_ns))) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t tq =
+                tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(b * kTile) + c_lo;
+#pragma unroll (kStored ? kSpan / kBlock : 1)
+            for (int c = 0; c < kSpan; c += kBlock) {
+                uint32_t v[16], p[16];
+                const bool have = static_cast<uint32_t>(c) < cols;
+                if constexpr (OP == kParam)
+                    if (P.vec && have && row < P.m)
+                        load_params(P, P.slot[it.z].ptr, static_cast<uint64_t>(row) * P.out_ld + col0 + c, p);
+                if (have) gemm::tmem_ld16(tq + c, v);
+                if (c + kBlock == kSpan) {
+                    // this warp has read its part of accumulator b
                     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote(peer_addr(acc_empty(b), 0));
-                };
-                if constexpr (OP == kInt8) {
-#pragma unroll
-                    for (int c = 0; c < kSpan; c += kBlock) {
-                        if (static_cast<uint32_t>(c) >= span) continue;
-                        uint32_t v[16];
-                        gemm::tmem_ld16(tq + c, v);
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) {
-                            const int32_t a = __float2int_rn(__uint_as_float(v[q]));
-                            acc[c + q] = kc == 0 ? a : acc[c + q] + a;
-                        }
-                    }
-                    release();
-                } else {
-#pragma unroll (kStored ? kSpan / kBlock : 1)
-                    for (int c = 0; c < kSpan; c += kBlock) {
-                        uint32_t v[16], p[16];
-                        const bool have = static_cast<uint32_t>(c) < cols;
-                        if constexpr (OP == kParam)
-                            if (P.vec && have && row < P.m)
-                                load_params(P, P.slot[it.z].ptr, static_cast<uint64_t>(row) * P.out_ld + col0 + c, p);
-                        if (have) gemm::tmem_ld16(tq + c, v);
-                        if (c + kBlock == kSpan) release();
-                        if (!have) continue;
-                        if constexpr (kStored) {
-                            store_stored<OP>(P, it, row, col0 + c, v, prior + (OP == kPoly ? c / 2 : 0), stage, lane);
-                        } else {
-                            float x[16];
-#pragma unroll
-                            for (int q = 0; q < 16; ++q) x[q] = __uint_as_float(v[q]);
-                            finish_block<OP>(P, it.z, row, col0 + c, x, p, nullptr, stage, lane);
-                        }
-                    }
                 }
-            }
-            if constexpr (OP == kInt8) {
-                if (ok) {
-                    // one copy of the finishing code for the warp's blocks
-#pragma unroll 1
-                    for (int c = 0; static_cast<uint32_t>(c) < cols; c += kBlock) {
-                        float x[16], cs[16];
+                if (!have) continue;
+                if constexpr (kStored) {
+                    store_stored<OP>(P, it, row, col0 + c, v, prior + (OP == kPoly ? c / 2 : 0), stage, lane);
+                } else {
+                    float x[16];
 #pragma unroll
-                        for (int d = 0; d < kSpan; d += kBlock) {
-                            if (c != d) continue;
-#pragma unroll
-                            for (int q = 0; q < 16; ++q) {
-                                x[q] = __int2float_rn(acc[d + q]);
-                                cs[q] = __shfl_sync(0xFFFFFFFFu, scale[d / 32], (d & 31) + q);
-                            }
-                        }
-                        finish_block<OP>(P, 0, row, col0 + c, x, nullptr, cs, stage, lane);
-                    }
+                    for (int q = 0; q < 16; ++q) x[q] = __uint_as_float(v[q]);
+                    finish_block<OP>(P, it.z, row, col0 + c, x, p, nullptr, stage, lane);
                 }
             }
         }
@@ -661,11 +603,15 @@ cudaError_t load_kernel(K kernel)
     return cudaFuncGetAttributes(&a, kernel);
 }
 
-template <bool A_MN, bool B_MN, int OP>
-cudaError_t setup_one(int sms, int *pairs)
+// Opts a kernel of this shape in to its shared memory; *pairs: how many pairs of
+// CTAs of it and of those before can be resident at once.
+template <typename K>
+cudaError_t setup_one(K kernel, int *pairs)
 {
-    cudaError_t e = cudaFuncSetAttribute(product_kernel<A_MN, B_MN, OP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSmem);
+    int dev = 0, sms = 0, n = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -678,8 +624,7 @@ cudaError_t setup_one(int sms, int *pairs)
     cfg.dynamicSmemBytes = kSmem;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, product_kernel<A_MN, B_MN, OP>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
     if (e == cudaSuccess && (*pairs == 0 || n < *pairs)) *pairs = n;
     return e;
 }
@@ -692,20 +637,16 @@ asr_status setup(int *pairs)
     if (dev < 0 || dev >= kMaxDevices) return ASR_ERR_INVALID_VALUE;
     std::lock_guard<std::mutex> lk(g_prod_mu);
     if (!g_prod_ready[dev]) {
-        int sms = 0, n = 0;
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e == cudaSuccess) e = setup_one<false, false, kGram>(sms, &n);
-        if (e == cudaSuccess) e = setup_one<true, true, kGram>(sms, &n);
-        if (e == cudaSuccess) e = setup_one<false, false, kPoly>(sms, &n);
-        if (e == cudaSuccess) e = setup_one<false, true, kNext>(sms, &n);
-        if (e == cudaSuccess) e = setup_one<false, false, kNext>(sms, &n);
-        if (e == cudaSuccess) e = setup_one<false, true, kOut>(sms, &n);
-        if (e == cudaSuccess) e = setup_one<false, false, kOut>(sms, &n);
-        if (e == cudaSuccess) e = setup_one<false, true, kParam>(sms, &n);
-        if (e == cudaSuccess) e = setup_one<false, false, kParam>(sms, &n);
-        if (e == cudaSuccess) e = setup_one<false, false, kInt8>(sms, &n);
-        if (e == cudaSuccess) e = setup_one<false, true, kInt8>(sms, &n);
-        if (e == cudaSuccess) e = setup_one<true, true, kInt8>(sms, &n);
+        int n = 0;
+        e = setup_one(product_kernel<false, false, kGram>, &n);
+        if (e == cudaSuccess) e = setup_one(product_kernel<true, true, kGram>, &n);
+        if (e == cudaSuccess) e = setup_one(product_kernel<false, false, kPoly>, &n);
+        if (e == cudaSuccess) e = setup_one(product_kernel<false, true, kNext>, &n);
+        if (e == cudaSuccess) e = setup_one(product_kernel<false, false, kNext>, &n);
+        if (e == cudaSuccess) e = setup_one(product_kernel<false, true, kOut>, &n);
+        if (e == cudaSuccess) e = setup_one(product_kernel<false, false, kOut>, &n);
+        if (e == cudaSuccess) e = setup_one(product_kernel<false, true, kParam>, &n);
+        if (e == cudaSuccess) e = setup_one(product_kernel<false, false, kParam>, &n);
         if (e != cudaSuccess) return cuda_fail(e);
         if (n < 1) return cuda_fail(cudaErrorNotSupported);
         g_prod_pairs[dev] = n;
@@ -756,7 +697,7 @@ struct Stored {
 // Launches the product of a (m x k, or k x m where A_MN) and b (n x k, or
 // k x n where B_MN); P's sizes and schedule are filled in here.
 template <bool A_MN, bool B_MN, int OP>
-asr_status launch(const Stored &a, const Stored &b, Params &P, int kind, cudaStream_t stream)
+asr_status launch(const Stored &a, const Stored &b, Params &P, cudaStream_t stream)
 {
     int pairs = 0;
     asr_status st = setup(&pairs);
@@ -802,7 +743,7 @@ asr_status launch(const Stored &a, const Stored &b, Params &P, int kind, cudaStr
     const uint64_t limit = kWaitLimitNs;
     cudaError_t e = cudaLaunchKernelEx(&cfg, product_kernel<A_MN, B_MN, OP>, ma, mb, mbh, P, limit);
     if (e != cudaSuccess) return cuda_fail(e);
-    return launched(kind);
+    return launched(ASR_KERNEL_PRODUCT);
 }
 
 }  // namespace prod
