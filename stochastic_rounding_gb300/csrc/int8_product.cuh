@@ -288,7 +288,7 @@ int8_product_kernel(const __grid_constant__ Int8Products L, uint64_t limit_ns)
                             cs[q] = __shfl_sync(0xFFFFFFFFu, scale[d / 32], (d & 31) + q);
                         }
                     }
-                    finish_block<kScaled>(P, 0, row, col0 + c, x, nullptr, cs, stage, lane);
+                    finish_block<kScaled>(P, 0, row, col0 + c, x, nullptr, cs, stage, lane, []() {});
                 }
             }
         }

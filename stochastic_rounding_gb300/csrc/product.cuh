@@ -252,15 +252,33 @@ __device__ __forceinline__ void store_stored(const Params &P, const Item &it, ui
     }
 }
 
-// The raw words of 16 parameters (bf16: eight, f32: sixteen) at `at`.
-__device__ __forceinline__ void load_params(const Params &P, const void *ptr, uint64_t at, uint32_t p[16])
+// The raw words of a block's parameters.  Full blocks of aligned matrices: the 16
+// of the lane's own row (bf16: eight words).  Others: one of every second row,
+// in a word each, the lanes along two rows (see finish_block).
+__device__ __forceinline__ void load_params(const Params &P, const void *ptr, uint32_t row, uint32_t col, int lane,
+                                            uint32_t p[16])
 {
-    if (P.out_dtype == ASR_BF16) {
-        ld_global_v8(static_cast<const uint16_t *>(ptr) + at, p);
-    } else {
-        ld_global_v8(static_cast<const float *>(ptr) + at, p);
-        ld_global_v8(static_cast<const float *>(ptr) + at + 8, p + 8);
+    const uint16_t *in16 = static_cast<const uint16_t *>(ptr);
+    const float *in32 = static_cast<const float *>(ptr);
+    const bool bf16 = P.out_dtype == ASR_BF16;
+    const uint64_t at = static_cast<uint64_t>(row) * P.out_ld + col;
+    if (P.vec && P.n - col >= kBlock) {
+        if (row >= P.m) return;
+        if (bf16) {
+            ld_global_v8(in16 + at, p);
+        } else {
+            ld_global_v8(in32 + at, p);
+            ld_global_v8(in32 + at + 8, p + 8);
+        }
+        return;
     }
+    const uint32_t c = lane & 15, first = row - lane + (lane >> 4);
+    const uint64_t a = static_cast<uint64_t>(first) * P.out_ld + col + c;
+#pragma unroll
+    for (int q = 0; q < 16; ++q)
+        p[q] = col + c >= P.n || first + 2 * q >= P.m ? 0u
+               : bf16                                 ? in16[a + 2 * q * P.out_ld]
+                                                      : __float_as_uint(in32[a + 2 * q * P.out_ld]);
 }
 
 __device__ __forceinline__ float param_value(const Params &P, const uint32_t p[16], int q)
@@ -289,12 +307,14 @@ __device__ __forceinline__ void round16(const Params &P, const float x[16], uint
 
 // 16 sums x of row `row`, columns col .. col+15, to the caller's matrix.  Each
 // lane finishes its own row; full blocks of aligned matrices are stored from
-// there (`params`: what load_params gave), others pass through the staging area,
+// there (`params`: what load_params gave; `next` is called when they are used up,
+// and may load others), others pass through the staging area,
 // in which the lanes lie along two rows at a time, whatever the row pitch: a
 // lane that stores (and loads) its own row alone touches a sector an element.
-template <int OP>
+template <int OP, typename Next>
 __device__ __forceinline__ void finish_block(const Params &P, uint32_t z, uint32_t row, uint32_t col, float x[16],
-                                             const uint32_t params[16], const float *col_scale, float *stage, int lane)
+                                             const uint32_t *params, const float *col_scale, float *stage, int lane,
+                                             Next next)
 {
     const uint32_t row0 = row - lane, live = P.n - col < 16 ? P.n - col : 16;
     const bool direct = P.vec && live == 16, bf16 = P.out_dtype == ASR_BF16, in = row < P.m;
@@ -310,17 +330,16 @@ __device__ __forceinline__ void finish_block(const Params &P, uint32_t z, uint32
                 x[q] = __fsub_rn(__fmul_rn(param_value(P, params, q), P.beta), __fmul_rn(P.alpha, x[q]));
         } else {
             __syncwarp();
-#pragma unroll 8
-            for (uint32_t r = r0; r < 32; r += 2) {
-                const uint64_t a = static_cast<uint64_t>(row0 + r) * P.out_ld + col + c;
-                if (row0 + r < P.m && c < live) stage[staged(r, c)] = bf16 ? bf16_lo(out16[a]) : out32[a];
-            }
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                stage[staged(r0 + 2 * q, c)] = bf16 ? bf16_lo(params[q]) : __uint_as_float(params[q]);
             __syncwarp();
 #pragma unroll
             for (int q = 0; q < 16; ++q)
                 x[q] = __fsub_rn(__fmul_rn(stage[staged(lane, q)], P.beta), __fmul_rn(P.alpha, x[q]));
         }
     }
+    next();
     if constexpr (OP == kScaled) {
         const float rs = in ? __ldg(P.row_scale + row) : 0.0f;
 #pragma unroll
@@ -544,6 +563,9 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     if (static_cast<uint32_t>(c) < cols && row < P.m)
                         ld_global_v8(P.aux + it.z * P.stride + static_cast<uint64_t>(row) * P.ld + col0 + c, prior + c / 2);
             }
+            uint32_t p[OP == kParam ? 16 : 1];
+            if constexpr (OP == kParam)
+                if (cols) load_params(P, P.slot[it.z].ptr, row, col0, lane, p);
             const int b = static_cast<int>(i % kAccBufs);
             if (!__all_sync(0xFFFFFFFFu, pair_wait(acc_full(b), (i++ / kAccBufs) & 1u, limit_ns))) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -551,11 +573,8 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(b * kTile) + c_lo;
 #pragma unroll (kStored ? kSpan / kBlock : 1)
             for (int c = 0; c < kSpan; c += kBlock) {
-                uint32_t v[16], p[16];
+                uint32_t v[16];
                 const bool have = static_cast<uint32_t>(c) < cols;
-                if constexpr (OP == kParam)
-                    if (P.vec && have && row < P.m)
-                        load_params(P, P.slot[it.z].ptr, static_cast<uint64_t>(row) * P.out_ld + col0 + c, p);
                 if (have) gemm::tmem_ld16(tq + c, v);
                 if (c + kBlock == kSpan) {
                     // this warp has read its part of accumulator b
@@ -570,7 +589,11 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     float x[16];
 #pragma unroll
                     for (int q = 0; q < 16; ++q) x[q] = __uint_as_float(v[q]);
-                    finish_block<OP>(P, it.z, row, col0 + c, x, p, nullptr, stage, lane);
+                    finish_block<OP>(P, it.z, row, col0 + c, x, p, nullptr, stage, lane, [&]() {
+                        if constexpr (OP == kParam)
+                            if (static_cast<uint32_t>(c + kBlock) < cols)
+                                load_params(P, P.slot[it.z].ptr, row, col0 + c + kBlock, lane, p);
+                    });
                 }
             }
         }

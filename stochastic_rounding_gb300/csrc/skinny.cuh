@@ -342,9 +342,10 @@ skinny_kernel(const __grid_constant__ SkinnyParams P, uint64_t limit_ns)
 #pragma unroll
         for (int q = 0; q < 16; ++q) x[q] = __uint_as_float(v[q]);
         if (!P.tall) {
-            if (MUON && P.out.vec && row < P.m)
-                prod::load_params(P.out, P.out.slot[z].ptr, static_cast<uint64_t>(row) * P.out.out_ld + col0 + c, p);
-            if (row - lane < P.m) prod::finish_block<OP>(P.out, z, row, col0 + c, x, p, nullptr, stage, lane);
+            if (row - lane < P.m) {
+                if (MUON) prod::load_params(P.out, P.out.slot[z].ptr, row, col0 + c, lane, p);
+                prod::finish_block<OP>(P.out, z, row, col0 + c, x, p, nullptr, stage, lane, []() {});
+            }
         } else if (row < P.m) {
             // column `row` of the caller's matrix, a warp 32 of them: rows c .. c+15 of this CTA's
             const prod::Slot S = P.out.slot[z];
