@@ -12,7 +12,7 @@
 // integers is exact.  sm_103a's tensor memory instructions have no 8-bit
 // integer kind; an 8-bit integer is exact in f16, a product of two in binary32,
 // and so is any sum of 1,024 of them (1,024 * 128^2 = 2^24).  So the operands
-// are widened to f16 in the workspace, product.cuh sums chunks of 1,024 in
+// are widened to f16 in the workspace, int8_product.cuh sums chunks of 1,024 in
 // tensor memory at the f16 rate, and its epilogue adds the chunks in int32.  With
 // few rows of A the weight is read as it is (int8_few.cuh).
 //
@@ -602,10 +602,20 @@ bool sizes_ok(uint64_t m, uint64_t n, uint64_t k)
     return m <= (1u << 24) && n <= (1u << 24) && k <= kMaxK;
 }
 
-#ifndef ASR_FEW_TOKENS
-#define ASR_FEW_TOKENS 128
-#endif
-bool few(uint64_t m) { return m <= ASR_FEW_TOKENS; }
+// Whether the weight is read as it is (int8_few.cuh) or widened first.  Reading it
+// costs more with every token (int32 sums of n x tokens through memory: 0.1 to 0.3
+// us a token), widening 0.84 us a million values of the weight, and the product
+// that follows does not share out K (2.2 us a thousand), so the choice goes by
+// tokens against K.  Measured, us, weight as it is / widened: 1,024 x 1,024: 16
+// tokens 8.8 / 9.8, 32 9.9 / 9.4; 2,048 x 2,048: 48 12.1 / 13.5, 64 14.0 / 13.7, 128
+// 20.2 / 13.9; 4,096 x 4,096: 64 19.7 / 23.5, 128 30.7 / 24.1; 14,336 x 4,096: 128
+// 39.5 / 62.7, 160 58.9 / 62.8, 256 75 / 64; 4,096 x 14,336: 256 71 / 84, 384 99 / 97;
+// 28,672 x 8,192: 256 163 / 224; 8,192 x 512: 16 11.2 / 13.2, 32 14.4 / 13.0.
+bool few(uint64_t m, uint64_t n, uint64_t k)
+{
+    const uint64_t most = k / 32 < 16 ? 16 : k / 32 < 256 ? k / 32 : 256;
+    return m <= most || int8few::dots(m, n, k);
+}
 
 // Workspace: with few rows of A the widened rows, their scales and the sums;
 // otherwise the scales and both operands, widened.
@@ -617,19 +627,20 @@ Layout layout(uint64_t m, uint64_t n, uint64_t k)
 {
     Layout L{};
     L.ld = muon::up(k, 16);
-    if (few(m) && int8few::dots(m, n, k)) return L;     // none
+    if (int8few::dots(m, n, k)) return L;     // none
     L.scale = 0;
     L.zero = muon::up(m * sizeof(float), 256);
     L.zero_bytes = 0;
     L.counts = L.zero;
-    if (few(m)) {
+    const bool narrow = few(m, n, k);
+    if (narrow) {
         const uint64_t tiles = (n + int8few::kRows - 1) / int8few::kRows;
         L.counts = L.zero + tiles * m * int8few::kRows * sizeof(int32_t);
         L.zero_bytes = muon::up(L.counts - L.zero + tiles * int8few::passes(m) * sizeof(uint32_t), 256);
     }
     L.a = L.zero + L.zero_bytes;
     L.b = L.a + muon::up(m * L.ld * 2, 256);
-    L.bytes = few(m) ? L.b : L.b + muon::up(n * L.ld * 2, 256);
+    L.bytes = narrow ? L.b : L.b + muon::up(n * L.ld * 2, 256);
     return L;
 }
 
@@ -769,7 +780,7 @@ asr_status gemm(const int8_t *a, uint64_t lda, const int8_t *b, uint64_t ldb, co
     st = setup();
     if (st != ASR_OK) return st;
     char *w = static_cast<char *>(ws);
-    if (few(m)) return few_rows(a, 0, lda, sa, b, ldb, sb, o, m, n, k, w, L, stream);
+    if (few(m, n, k)) return few_rows(a, 0, lda, sa, b, ldb, sb, o, m, n, k, w, L, stream);
     WidenParams W;
     std::memset(&W, 0, sizeof(W));
     W.src[0] = a;
@@ -809,7 +820,7 @@ asr_status linear(const void *x, int32_t x_dtype, uint64_t x_ld, const int8_t *q
     st = setup();
     if (st != ASR_OK) return st;
     char *w = static_cast<char *>(ws);
-    if (few(m)) return few_rows(x, x_dtype, x_ld, nullptr, qw, ldw, sw, o, m, n, k, w, L, stream);
+    if (few(m, n, k)) return few_rows(x, x_dtype, x_ld, nullptr, qw, ldw, sw, o, m, n, k, w, L, stream);
     RowParams P;
     std::memset(&P, 0, sizeof(P));
     P.x = x;

@@ -6,11 +6,15 @@
 // tensor memory -- exact in binary32 -- and added up by the epilogue warps in
 // int32 registers; the next chunk's products go into the other accumulator
 // meanwhile.  The two products of a backward pass (dx and dw) go as one list of
-// tiles, the one of the longer sum first: alone each leaves its last round of
-// tiles part empty (4,096 tokens, 8,192 x 2,048: 1.68 rounds of long tiles, then
-// 3.37 of half as long ones; 295 us the call with two launches, 273 with one), and small
-// ones cost a launch each.  How an operand is stored is a field of the product
-// here, the same for all lanes.
+// tiles, those of the longer sum first: in a launch each, both leave their last
+// round of tiles part empty, and small ones pay for two launches (4,096 tokens,
+// 8,192 x 2,048: the call 295 us with two, 273 with one; 1,111 tokens, 515 x 1,365:
+// 49.3 and 46.6).  How an operand is stored is a field of its product here, the
+// same for all lanes.
+//
+// What bounds it: the tensor cores, at 1,660 TFLOP/s for the first of these (166
+// us) and 1,850 for 8,192 x 14,336 x 4,096, where the power limit holds them; small
+// ones the chain of copies, sums and epilogue (20 us for 777 x 1,001 x 2,049).
 
 namespace prod {
 

@@ -1,8 +1,8 @@
 // product.cuh -- batched matrix products with f16 operands on the
 // 5th-generation tensor cores: the kernel of the Newton-Schulz orthogonalisation
 // (muon.cuh), and what the 8-bit integer product's (int8_product.cuh) shares with
-// it.  Included into asr.cu (inside its anonymous namespace), after gemm_sr.cuh, whose cluster,
-// barrier and tensor-map helpers it uses.
+// it.  Included into asr.cu (inside its anonymous namespace), after gemm_sr.cuh,
+// whose cluster, barrier and tensor-map helpers it uses.
 //
 // out_z = epilogue(A_z . B_z^T) for the matrices z of a stack, with binary32
 // sums.  The shape is gemm_sr.cuh's two-SM kernel: 256 x 256 tiles on clusters
@@ -18,7 +18,9 @@
 //     diagonal and writes each of the others as a mirror image: half the work;
 //   - sixteen epilogue warps: a tile's epilogue is exposed at a launch's end (last
 //     products of ortho and Muon steps 31 and 87 us, with eight warps that took 32
-//     columns at a time 49 and 111 us);
+//     columns at a time 49 and 111 us); what they read for a block is on its way
+//     while they finish the one before (3 stacked 515 x 1,365: 161 us, 165 with
+//     the loads where they are used);
 //   - the tiles of a last round that would leave most pairs idle go in halves or
 //     quarters of their columns.
 // What bounds it: large products run at the tensor cores' sustained rate under

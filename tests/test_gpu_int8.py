@@ -192,6 +192,22 @@ def test_product_strided_unaligned(asr, m, dtype):
     assert (rest == 7.0).all()
 
 
+@pytest.mark.parametrize("shift", [0, 1, 2, 3])
+@pytest.mark.parametrize("m,n,k", [(2, 70, 2049), (16, 64, 130), (17, 64, 130), (33, 129, 2051), (64, 130, 2048),
+                                   (65, 130, 2048), (150, 133, 5001), (256, 40, 8200), (257, 40, 8200)])
+def test_product_weight_at_any_address(asr, m, n, k, shift):
+    """A weight whose rows follow one another without a gap, from any byte on to
+    the end of its memory, on both sides of the choice between the kernels."""
+    import torch
+    a, b, sa, sb = _operands(m, n, k, m + k)
+    room = torch.empty(shift + n * k, device="cuda", dtype=torch.int8)
+    w = room[shift:].view(n, k)
+    w.copy_(b)
+    c = torch.empty(m, n, device="cuda")
+    asr.asr_gemm_int8_sr(a, w, sa, sb, c)
+    assert_same_bits(host(c), host(_want_product(a, b, sa, sb)))
+
+
 @pytest.mark.parametrize("m", [1, 12, 140])
 def test_product_scales_that_are_not_finite(asr, m):
     import torch
