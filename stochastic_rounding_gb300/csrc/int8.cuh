@@ -255,6 +255,7 @@ __device__ __forceinline__ const Side &side_of(const SideParams &P, uint32_t blo
 
 __global__ void __launch_bounds__(kThreads) max_kernel(const __grid_constant__ SideParams P)
 {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ uint32_t part[8][8 * 33];
     const Side &S = side_of(P, blockIdx.x);
     const uint32_t tile = blockIdx.x - S.first, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -327,6 +328,8 @@ __global__ void __launch_bounds__(kThreads) max_kernel(const __grid_constant__ S
 // columns.  The first tiles write the scales.
 __global__ void __launch_bounds__(kThreads, 4) wide_kernel(const __grid_constant__ SideParams P)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Side &S = side_of(P, blockIdx.x);
     const uint32_t tile = blockIdx.x - S.first, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t t0 = static_cast<uint64_t>(tile / S.tiles_x) * 8 * P.deep, r0 = t0 + warp * P.deep;
@@ -952,8 +955,7 @@ asr_status grads(const GradSource &dy, const GradSource &x, const GradSource &w,
     max_kernel<<<M.blocks, kThreads, 0, stream>>>(M);
     st = launched(ASR_KERNEL_QUANTIZE);
     if (st != ASR_OK) return st;
-    wide_kernel<<<M.blocks, kThreads, 0, stream>>>(M);
-    st = launched(ASR_KERNEL_QUANTIZE);
+    st = prod::launch_early(ASR_KERNEL_QUANTIZE, wide_kernel, dim3(M.blocks), kThreads, M, stream);
     if (st != ASR_OK) return st;
     prod::Int8Products P;
     prod::Stored operands[4];

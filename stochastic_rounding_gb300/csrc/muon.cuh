@@ -118,6 +118,7 @@ struct Walk {
 template <bool MUON>
 __global__ void __launch_bounds__(kThreads) square_sum_kernel(const __grid_constant__ PrepParams P)
 {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Matrix M = P.m[blockIdx.y];
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float sum = 0.0f;
@@ -165,6 +166,8 @@ __global__ void __launch_bounds__(kThreads) square_sum_kernel(const __grid_const
 template <bool MUON>
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ PrepParams P)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Matrix M = P.m[blockIdx.y];
     __shared__ float part[kThreads / 32];
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -322,10 +325,9 @@ asr_status prep(const Group &G, const NsParams &ns, const Layout &L, char *ws, f
     P.out_stride = up(G.rows * L.ldx * 2, 256) / 2;
     const dim3 grid(P.blocks, G.batch, 1);
     square_sum_kernel<MUON><<<grid, kThreads, 0, stream>>>(P);
-    asr_status st = launched(ASR_KERNEL_MATRIX_PREP);
+    const asr_status st = launched(ASR_KERNEL_MATRIX_PREP);
     if (st != ASR_OK) return st;
-    scale_kernel<MUON><<<grid, kThreads, 0, stream>>>(P);
-    return launched(ASR_KERNEL_MATRIX_PREP);
+    return prod::launch_early(ASR_KERNEL_MATRIX_PREP, scale_kernel<MUON>, grid, kThreads, P, stream);
 }
 
 // A group whose matrices' smaller side is at most 128: one launch.

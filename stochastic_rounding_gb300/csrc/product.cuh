@@ -628,6 +628,25 @@ cudaError_t load_kernel(K kernel)
     return cudaFuncGetAttributes(&a, kernel);
 }
 
+// Launches a kernel that may start before the one ahead of it on the stream has
+// ended; it waits for that itself (griddepcontrol.wait).
+template <typename P>
+asr_status launch_early(int kind, void (*kernel)(P), dim3 grid, unsigned threads, const P &params, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, params);
+    if (e != cudaSuccess) return cuda_fail(e);
+    return launched(kind);
+}
+
 // Opts a kernel of this shape in to its shared memory; *pairs: how many pairs of
 // CTAs of it and of those before can be resident at once.
 template <typename K>
