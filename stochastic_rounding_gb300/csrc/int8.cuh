@@ -223,6 +223,13 @@ __global__ void __launch_bounds__(kPrepThreads) few_prep_kernel(const __grid_con
     }
 }
 
+__global__ void __launch_bounds__(kThreads) zero_kernel(uint32_t *p, uint64_t n)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint64_t i = blockIdx.x * static_cast<uint64_t>(kThreads) + threadIdx.x;
+    if (i < n) p[i] = 0;
+}
+
 // Maxima along columns, or along both, of up to three matrices in one launch:
 // blocks of 8 * `deep` rows x 256 columns, a warp `deep` rows, eight columns a
 // lane.  `row_max` and `col_max` hold bits of non-negative floats, zero at the
@@ -255,6 +262,7 @@ __device__ __forceinline__ const Side &side_of(const SideParams &P, uint32_t blo
 
 __global__ void __launch_bounds__(kThreads) max_kernel(const __grid_constant__ SideParams P)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ uint32_t part[8][8 * 33];
     const Side &S = side_of(P, blockIdx.x);
@@ -505,6 +513,16 @@ void lay_out(SideParams &M)
     }
 }
 
+// The sides' maxima, which lie in the `words` words from `zero` on.
+asr_status maxima(SideParams &M, uint32_t *zero, uint64_t words, cudaStream_t stream)
+{
+    lay_out(M);
+    zero_kernel<<<static_cast<unsigned>((words + kThreads - 1) / kThreads), kThreads, 0, stream>>>(zero, words);
+    const asr_status st = launched(ASR_KERNEL_QUANTIZE);
+    if (st != ASR_OK) return st;
+    return prod::launch_early(ASR_KERNEL_QUANTIZE, max_kernel, dim3(M.blocks), kThreads, M, stream);
+}
+
 // Every kernel of this file and of the products ready on the device, whichever a call takes.
 asr_status setup()
 {
@@ -516,6 +534,7 @@ asr_status setup()
     cudaError_t e = cudaGetDevice(&dev);
     const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
     if (e == cudaSuccess && (ready.load(std::memory_order_acquire) & bit)) return ASR_OK;
+    if (e == cudaSuccess) e = prod::load_kernel(zero_kernel);
     if (e == cudaSuccess) e = prod::load_kernel(few_prep_kernel);
     if (e == cudaSuccess) e = prod::load_kernel(quantise_rows_kernel<false, false>);
     if (e == cudaSuccess) e = prod::load_kernel(quantise_rows_kernel<true, false>);
@@ -567,16 +586,12 @@ asr_status quantize(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, 
         else quantise_rows_kernel<false, false><<<grid, kThreads, 0, stream>>>(P, grid);
         return launched(ASR_KERNEL_QUANTIZE);
     }
-    const cudaError_t e = cudaMemsetAsync(scale, 0, cols * sizeof(float), stream);
-    if (e != cudaSuccess) return cuda_fail(e);
     SideParams M;
     std::memset(&M, 0, sizeof(M));
     M.s[0] = side(x, dtype, rows, cols, x_ld);
     M.s[0].col_max = reinterpret_cast<uint32_t *>(scale);
     M.count = 1;
-    lay_out(M);
-    max_kernel<<<M.blocks, kThreads, 0, stream>>>(M);
-    st = launched(ASR_KERNEL_QUANTIZE);
+    st = maxima(M, M.s[0].col_max, cols, stream);
     if (st != ASR_OK) return st;
     ColumnParams P;
     P.x = x;
@@ -920,8 +935,6 @@ asr_status grads(const GradSource &dy, const GradSource &x, const GradSource &w,
     auto words = [&](uint64_t at) { return reinterpret_cast<uint32_t *>(b + at); };
     auto floats = [&](uint64_t at) { return reinterpret_cast<float *>(b + at); };
     auto halves = [&](uint64_t at) { return reinterpret_cast<__half *>(b + at); };
-    const cudaError_t e = cudaMemsetAsync(ws, 0, L.zeroed, stream);
-    if (e != cudaSuccess) return cuda_fail(e);
     SideParams M;
     std::memset(&M, 0, sizeof(M));
     M.step = step;
@@ -951,9 +964,7 @@ asr_status grads(const GradSource &dy, const GradSource &x, const GradSource &w,
         X.by_col = halves(L.x);
         X.q_ld = L.ldk;
     }
-    lay_out(M);
-    max_kernel<<<M.blocks, kThreads, 0, stream>>>(M);
-    st = launched(ASR_KERNEL_QUANTIZE);
+    st = maxima(M, words(0), L.zeroed / sizeof(uint32_t), stream);
     if (st != ASR_OK) return st;
     st = prod::launch_early(ASR_KERNEL_QUANTIZE, wide_kernel, dim3(M.blocks), kThreads, M, stream);
     if (st != ASR_OK) return st;
