@@ -23,7 +23,7 @@
 // its 128.  The gradients' operands are quantised where they lie and read across,
 // in two streams: maxima (4,096 tokens, 8,192 x 2,048: 117 MB, 24 us), then the
 // integers, dy's by rows and by columns from one read and one set of random bits
-// (301 MB, 77 us; bound by instructions: 15 an element for Philox, 5 for each
+// (301 MB, 73 us; bound by instructions: 15 an element for Philox, 5 for each
 // rounding).
 
 namespace int8 {
@@ -389,13 +389,14 @@ __global__ void __launch_bounds__(kThreads, 4) wide_kernel(const __grid_constant
     };
     if (S.dtype == ASR_BF16 && S.vec && live == 8) {
         const uint16_t *p = static_cast<const uint16_t *>(S.x) + col;
-        for (uint64_t row = r0; row < end; row += 4) {
-            uint4 w[4];
+        // two rows' loads ahead: four do not fit the registers (gradients of the size above 265 us, 270 with four)
+        for (uint64_t row = r0; row < end; row += 2) {
+            uint4 w[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
                 w[i] = row + i < end ? *reinterpret_cast<const uint4 *>(p + (row + i) * S.x_ld) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 if (row + i >= end) break;
                 const float x[8] = {bf16_lo(w[i].x), bf16_hi(w[i].x), bf16_lo(w[i].y), bf16_hi(w[i].y),
                                     bf16_lo(w[i].z), bf16_hi(w[i].z), bf16_lo(w[i].w), bf16_hi(w[i].w)};
