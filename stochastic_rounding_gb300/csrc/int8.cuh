@@ -330,6 +330,83 @@ __global__ void __launch_bounds__(kThreads) max_kernel(const __grid_constant__ S
     if (c < S.cols) atomicMax(S.col_max + c, v);
 }
 
+// Rows r0 on of a lane's eight columns (`live` of them), for wide_kernel.
+// inv_rows: the rows' scales times 65536.
+template <bool RANDOM>
+__device__ __forceinline__ void wide_rows(const SideParams &P, const Side &S, uint64_t r0, uint32_t rows, uint64_t col,
+                                          int live, const float *inv_rows)
+{
+    float inv[8];
+    bool odd = false;
+    auto column = [&](int q) { return levels_of(q < live ? __uint_as_float(S.col_max[col + q]) : 0.0f); };
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const Levels L = column(q);
+        inv[q] = RANDOM ? __fmul_rn(L.inv, 65536.0f) : L.inv;
+        odd |= L.odd && q < live;
+    }
+    __half *by_row = RANDOM && S.by_row ? S.by_row + r0 * S.q_ld + col : nullptr;
+    __half *by_col = S.by_col ? S.by_col + r0 * S.q_ld + col : nullptr;
+    uint64_t e = r0 * S.cols + col;
+    auto one = [&](uint32_t i, float x[8]) {
+        uint32_t v[4], r[8];
+        if (RANDOM) {
+            words8(0, e, P.step, P.keys, r);
+            e += S.cols;
+            if (by_row) {
+                float f = inv_rows[i], z[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) z[q] = x[q];
+                if (f < 0.0f) {
+                    const Levels L = levels_of(__uint_as_float(S.row_max[r0 + i]));
+                    f = __fmul_rn(L.inv, 65536.0f);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) z[q] = regular(x[q], L);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] = random2(z[2 * q], z[2 * q + 1], f, f, r[2 * q], r[2 * q + 1]);
+                *reinterpret_cast<uint4 *>(by_row) = halves_of(v);
+                by_row += S.q_ld;
+            }
+        }
+        if (!by_col) return;
+        if (odd) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) x[q] = regular(x[q], column(q));
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            v[q] = RANDOM ? random2(x[2 * q], x[2 * q + 1], inv[2 * q], inv[2 * q + 1], r[2 * q], r[2 * q + 1])
+                          : nearest2(x[2 * q], x[2 * q + 1], inv[2 * q], inv[2 * q + 1]);
+        // past the last column: zeros (their loads gave zeros)
+        *reinterpret_cast<uint4 *>(by_col) = halves_of(v);
+        by_col += S.q_ld;
+    };
+    if (S.dtype == ASR_BF16 && S.vec && live == 8) {
+        const uint16_t *p = static_cast<const uint16_t *>(S.x) + r0 * S.x_ld + col;
+        // two rows' loads ahead: four do not fit the registers (gradients of the size above 265 us, 270 with four)
+        for (uint32_t i = 0; i < rows; i += 2) {
+            uint4 w[2];
+            w[0] = *reinterpret_cast<const uint4 *>(p);
+            w[1] = i + 1 < rows ? *reinterpret_cast<const uint4 *>(p + S.x_ld) : make_uint4(0, 0, 0, 0);
+            p += 2 * S.x_ld;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (i + j >= rows) break;
+                float x[8] = {bf16_lo(w[j].x), bf16_hi(w[j].x), bf16_lo(w[j].y), bf16_hi(w[j].y),
+                              bf16_lo(w[j].z), bf16_hi(w[j].z), bf16_lo(w[j].w), bf16_hi(w[j].w)};
+                one(i + j, x);
+            }
+        }
+    } else {
+        for (uint32_t i = 0; i < rows; ++i) {
+            float x[8];
+            muon::load8(S.x, S.dtype, (r0 + i) * S.x_ld + col, live, S.vec, x);
+            one(i, x);
+        }
+    }
+}
+
 // The integers of every matrix of the call, as f16, where they lie (the
 // products read them across): side 0 (dy) stochastically, by its rows' and by
 // its columns' maxima with the same random bits; the others to nearest, by
@@ -347,69 +424,17 @@ __global__ void __launch_bounds__(kThreads, 4) wide_kernel(const __grid_constant
         S.col_scale[c0 + threadIdx.x] = __fdiv_rn(__uint_as_float(S.col_max[c0 + threadIdx.x]), 127.0f);
     if (S.row_max && c0 == 0 && threadIdx.x < 8 * P.deep && t0 + threadIdx.x < S.rows)
         S.row_scale[t0 + threadIdx.x] = __fdiv_rn(__uint_as_float(S.row_max[t0 + threadIdx.x]), 127.0f);
-    // the block's rows' levels, once
-    __shared__ Levels by_row[8 * kDeep];
-    if (S.row_max && threadIdx.x < 8 * P.deep && t0 + threadIdx.x < S.rows)
-        by_row[threadIdx.x] = levels_of(__uint_as_float(S.row_max[t0 + threadIdx.x]));
+    // the block's rows' scales, once; -1 for an odd row
+    __shared__ float by_row[8 * kDeep];
+    if (S.row_max && threadIdx.x < 8 * P.deep && t0 + threadIdx.x < S.rows) {
+        const Levels L = levels_of(__uint_as_float(S.row_max[t0 + threadIdx.x]));
+        by_row[threadIdx.x] = L.odd ? -1.0f : __fmul_rn(L.inv, 65536.0f);
+    }
     __syncthreads();
-    if (!live) return;
-    float inv[8];
-    bool odd = false;
-    auto column = [&](int q) { return levels_of(q < live ? __uint_as_float(S.col_max[col + q]) : 0.0f); };
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        const Levels L = column(q);
-        inv[q] = S.row_max ? __fmul_rn(L.inv, 65536.0f) : L.inv;
-        odd |= L.odd && q < live;
-    }
-    const uint64_t end = r0 + P.deep < S.rows ? r0 + P.deep : S.rows;
-    auto one = [&](uint64_t row, const float x0[8]) {
-        float x[8];
-        uint32_t v[4], r[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) x[q] = x0[q];
-        if (S.row_max) {
-            words8(0, row * S.cols + col, P.step, P.keys, r);
-            if (S.by_row) {
-                quantise8<true>(x, by_row[row - t0], r, v);
-                *reinterpret_cast<uint4 *>(S.by_row + row * S.q_ld + col) = halves_of(v);
-            }
-        }
-        if (!S.by_col) return;
-        if (odd) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) x[q] = regular(x[q], column(q));
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            v[q] = S.row_max ? random2(x[2 * q], x[2 * q + 1], inv[2 * q], inv[2 * q + 1], r[2 * q], r[2 * q + 1])
-                             : nearest2(x[2 * q], x[2 * q + 1], inv[2 * q], inv[2 * q + 1]);
-        // past the last column: zeros (their loads gave zeros)
-        *reinterpret_cast<uint4 *>(S.by_col + row * S.q_ld + col) = halves_of(v);
-    };
-    if (S.dtype == ASR_BF16 && S.vec && live == 8) {
-        const uint16_t *p = static_cast<const uint16_t *>(S.x) + col;
-        // two rows' loads ahead: four do not fit the registers (gradients of the size above 265 us, 270 with four)
-        for (uint64_t row = r0; row < end; row += 2) {
-            uint4 w[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                w[i] = row + i < end ? *reinterpret_cast<const uint4 *>(p + (row + i) * S.x_ld) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (row + i >= end) break;
-                const float x[8] = {bf16_lo(w[i].x), bf16_hi(w[i].x), bf16_lo(w[i].y), bf16_hi(w[i].y),
-                                    bf16_lo(w[i].z), bf16_hi(w[i].z), bf16_lo(w[i].w), bf16_hi(w[i].w)};
-                one(row + i, x);
-            }
-        }
-    } else {
-        for (uint64_t row = r0; row < end; ++row) {
-            float x[8];
-            muon::load8(S.x, S.dtype, row * S.x_ld + col, live, S.vec, x);
-            one(row, x);
-        }
-    }
+    if (!live || r0 >= S.rows) return;
+    const uint32_t rows = S.rows - r0 < P.deep ? static_cast<uint32_t>(S.rows - r0) : P.deep;
+    if (S.row_max) wide_rows<true>(P, S, r0, rows, col, live, by_row + warp * P.deep);
+    else wide_rows<false>(P, S, r0, rows, col, live, nullptr);
 }
 
 struct ColumnParams {

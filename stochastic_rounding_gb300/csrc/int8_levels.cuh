@@ -38,12 +38,18 @@ __device__ __forceinline__ uint32_t nearest2(float x, float y, float inv_x, floa
 
 // Stochastically: floor(y) + [65536 (y - floor(y)) > r] for whole r in [0, 65535]
 // is floor((ceil(65536 y) + 65535 - r) / 65536), the sum's high half.  The scales
-// come times 65536 (exact); not_r is 65535 - r.  |q| may come to 128.
+// come times 65536 (exact); not_r is 65535 - r.  |65536 y| <= 127 * 65536 (1 + 2^-24)
+// before its rounding, in steps of 1/2, so at most 127 * 65536 + 1/2: the sum can
+// come to 128 but not below -127.  The minimum is taken as of f16 numbers, whose
+// order is that of these patterns.
 __device__ __forceinline__ uint32_t random2(float x, float y, float inv_x, float inv_y, uint32_t not_r, uint32_t not_s)
 {
     const uint32_t a = static_cast<uint32_t>(__float2int_ru(__fmul_rn(x, inv_x))) + not_r + 0x64800000u;
     const uint32_t b = static_cast<uint32_t>(__float2int_ru(__fmul_rn(y, inv_y))) + not_s + 0x64800000u;
-    return __vmaxu2(__vminu2(__byte_perm(a, b, 0x7632), 0x64FF64FFu), 0x64016401u);
+    const uint32_t v = __byte_perm(a, b, 0x7632);
+    const __half2 most = __halves2half2(__ushort_as_half(0x64FF), __ushort_as_half(0x64FF));
+    const __half2 m = __hmin2(*reinterpret_cast<const __half2 *>(&v), most);
+    return *reinterpret_cast<const uint32_t *>(&m);
 }
 
 // Eight of them as f16, or as bytes.
