@@ -23,7 +23,7 @@
 // its 128.  The gradients' operands are quantised where they lie and read across,
 // in two streams: maxima (4,096 tokens, 8,192 x 2,048: 117 MB, 24 us), then the
 // integers, dy's by rows and by columns from one read and one set of random bits
-// (301 MB, 73 us; bound by instructions: 15 an element for Philox, 5 for each
+// (301 MB, 66 us; bound by instructions: 15 an element for Philox, 5 for each
 // rounding).
 
 namespace int8 {
@@ -384,7 +384,7 @@ __device__ __forceinline__ void wide_rows(const SideParams &P, const Side &S, ui
     };
     if (S.dtype == ASR_BF16 && S.vec && live == 8) {
         const uint16_t *p = static_cast<const uint16_t *>(S.x) + r0 * S.x_ld + col;
-        // two rows' loads ahead: four do not fit the registers (gradients of the size above 265 us, 270 with four)
+        // two rows at a time: four do not fit the registers (gradients of the size above 258 us; one 262)
         for (uint32_t i = 0; i < rows; i += 2) {
             uint4 w[2];
             w[0] = *reinterpret_cast<const uint4 *>(p);
