@@ -647,17 +647,17 @@ bool sizes_ok(uint64_t m, uint64_t n, uint64_t k)
 }
 
 // Whether the weight is read as it is (int8_few.cuh) or widened first.  Reading it
-// costs more with every token (sums of n x tokens through memory: 0.06 to 0.2 us a
-// token), widening 0.84 us a million values of the weight, and the product that
-// follows does not share out K (2.2 us a thousand), so the choice goes by tokens
-// against K.  Measured, us, weight as it is / widened: 1,024 x 1,024: 32 tokens
-// 9.4 / 9.4, 64 11.3 / 9.5; 2,048 x 2,048: 64 12.2 / 13.7, 96 14.2 / 13.8; 4,096 x
-// 4,096: 96 20.6 / 23.9, 128 24.3 / 24.1, 160 34 / 24; 14,336 x 4,096: 128 33 / 63, 256
-// 62 / 64; 4,096 x 14,336: 384 83 / 97; 28,672 x 8,192: 256 142 / 224; 8,192 x 512: 16
-// 11.3 / 13.2, 32 14.2 / 13.0.
+// costs more with every token (int32 sums of n x tokens through memory: 0.1 to 0.3
+// us a token), widening 0.84 us a million values of the weight, and the product
+// that follows does not share out K (2.2 us a thousand), so the choice goes by
+// tokens against K.  Measured, us, weight as it is / widened: 1,024 x 1,024: 16
+// tokens 8.8 / 9.8, 32 9.9 / 9.4; 2,048 x 2,048: 48 12.1 / 13.5, 64 14.0 / 13.7, 128
+// 20.2 / 13.9; 4,096 x 4,096: 64 19.7 / 23.5, 128 30.7 / 24.1; 14,336 x 4,096: 128
+// 39.5 / 62.7, 160 58.9 / 62.8, 256 75 / 64; 4,096 x 14,336: 256 71 / 84, 384 99 / 97;
+// 28,672 x 8,192: 256 163 / 224; 8,192 x 512: 16 11.2 / 13.2, 32 14.4 / 13.0.
 bool few(uint64_t m, uint64_t n, uint64_t k)
 {
-    const uint64_t most = k / 32 < 16 ? 16 : k / 32 < 384 ? k / 32 : 384;
+    const uint64_t most = k / 32 < 16 ? 16 : k / 32 < 256 ? k / 32 : 256;
     return m <= most || int8few::dots(m, n, k);
 }
 
@@ -802,7 +802,6 @@ asr_status few_rows(const void *x, int32_t x_dtype, uint64_t x_ld, const float *
     P.n = static_cast<uint32_t>(n);
     P.k = static_cast<uint32_t>(k);
     P.b_vec = aligned16(b) && ldb % 16 == 0;
-    P.c_vec = o.ld % 4 == 0 && reinterpret_cast<uintptr_t>(o.c) % (o.dtype == ASR_F32 ? 16 : 8) == 0;
     P.c_dtype = static_cast<uint32_t>(o.dtype);
     P.rounding = o.rounding;
     P.step = o.step;

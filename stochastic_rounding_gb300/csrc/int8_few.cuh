@@ -17,11 +17,9 @@
 // At most 1,024 products are added in binary32, which is exact; int32 then.
 //
 // Measured on a weight of 14,336 x 4,096 (58.7 MB, 8.6 us at the copy rate), with
-// the launch: 1 token 14.4 us, 4 17.5, 16 21, 32 23.2, 64 25, 128 32.7; on one
+// the launch: 1 token 14.4 us, 4 17.5, 16 20.5, 33 23.8, 64 26, 128 39; on one
 // eight times as large 1 token 87 us (5.4 TB/s), 33 tokens 92.  What is left at
-// the small end is latency: launch, first weights, quantiser, and at a CTA's end
-// its sums to memory (1.3 us), the count (0.8), and for the last one the sums
-// back (1.0) and the outputs (0.5 to 2 for 128 tokens).
+// the small end is latency: launch, first weights, quantiser, last sums.
 
 namespace int8few {
 
@@ -40,7 +38,6 @@ struct Params {
     uint32_t m, n, k, tiles, pieces;        // row blocks, pieces of each
     uint32_t each;                          // tokens a pass, a multiple of 16 (tcgen05)
     uint32_t b_vec;                         // rows of B in 16-byte aligned units
-    uint32_t c_vec;                         // four outputs of a row are stored at once
     uint32_t c_dtype, rounding, step;
     RoundKeys keys;
 };
@@ -93,6 +90,35 @@ __device__ __noinline__ uint32_t round_stochastic(float y, uint64_t e, uint32_t 
     return round_sr(y, sel == 0 ? r[0] : sel == 1 ? r[1] : sel == 2 ? r[2] : r[3]);
 }
 
+// The outputs of one column (of scale cs) and COUNT tokens (`live` of them, of
+// scales rs) from their integer sums.
+template <int COUNT, typename P_>
+__device__ __forceinline__ void store_outputs(const P_ &P, uint32_t token, uint32_t col, float cs, const float *rs,
+                                              const int32_t sum[COUNT], uint32_t live)
+{
+    float y[COUNT];
+#pragma unroll
+    for (int q = 0; q < COUNT; ++q) y[q] = __fmul_rn(__fmul_rn(__int2float_rn(sum[q]), rs[q]), cs);
+    const uint64_t dst = token * P.ldc + col;
+    if (P.c_dtype == ASR_F32) {
+#pragma unroll
+        for (int q = 0; q < COUNT; ++q)
+            if (static_cast<uint32_t>(q) < live) static_cast<float *>(P.c)[dst + q * P.ldc] = y[q];
+    } else if (P.rounding == ASR_ROUND_SR) {
+        const uint64_t e = static_cast<uint64_t>(token) * P.n + col;
+#pragma unroll
+        for (int q = 0; q < COUNT; ++q)
+            if (static_cast<uint32_t>(q) < live)
+                static_cast<uint16_t *>(P.c)[dst + q * P.ldc] =
+                    static_cast<uint16_t>(round_stochastic(y[q], e + static_cast<uint64_t>(q) * P.n, P.step, P.keys));
+    } else {
+#pragma unroll
+        for (int q = 0; q < COUNT; ++q)
+            if (static_cast<uint32_t>(q) < live)
+                static_cast<uint16_t *>(P.c)[dst + q * P.ldc] = static_cast<uint16_t>(round_rne(y[q]));
+    }
+}
+
 // ------------------------------------------------------------ dot products
 //
 // A cluster of up to eight CTAs takes 64 rows of the weight, each CTA a share of
@@ -120,21 +146,6 @@ struct DotParams {
     uint32_t c_dtype, rounding, step;
     RoundKeys keys;
 };
-
-// The output of one token and column from its integer sum and the scales.
-__device__ __forceinline__ void store_output(const DotParams &P, uint32_t token, uint32_t col, float rs, float cs,
-                                             int32_t sum)
-{
-    const float y = __fmul_rn(__fmul_rn(__int2float_rn(sum), rs), cs);
-    const uint64_t dst = token * P.ldc + col;
-    if (P.c_dtype == ASR_F32)
-        static_cast<float *>(P.c)[dst] = y;
-    else
-        static_cast<uint16_t *>(P.c)[dst] = static_cast<uint16_t>(
-            P.rounding == ASR_ROUND_SR
-                ? round_stochastic(y, static_cast<uint64_t>(token) * P.n + col, P.step, P.keys)
-                : round_rne(y));
-}
 
 __device__ __forceinline__ int32_t ld_cluster_s32(uint32_t addr)
 {
@@ -276,7 +287,7 @@ __global__ void __launch_bounds__(kDotThreads, 2) few_dots_kernel(const __grid_c
         int32_t sum = 0;
         for (uint32_t p = 0; p < split; ++p)
             sum += ld_cluster_s32(gemm::peer_addr(smem_addr(sums + token * kDotRows + r), p));
-        if (col < P.n) store_output(P, token, col, scales[token], __ldg(P.col_scale + col), sum);
+        if (col < P.n) store_outputs<1>(P, token, col, __ldg(P.col_scale + col), scales + token, &sum, 1);
     }
     gemm::cluster_sync();                       // no CTA leaves while another reads its sums
 }
@@ -289,17 +300,15 @@ __global__ void __launch_bounds__(kDotThreads, 2) few_dots_kernel(const __grid_c
 // int32 sums of a row block that several CTAs share are added up in the
 // workspace, and the CTA that completes the block's count of pieces writes its
 // outputs.  Integer sums are the same in every order, and nobody waits for
-// anybody.  Sums leave and come back as one bulk copy: a reduction instruction for
-// every 32 of them takes the SM 18 cycles, and loads back as many at a time as
-// registers hold are waits for the L2 (14,336 x 4,096: 64 tokens 25.0 us, 26.7 with
-// both, 128 tokens 32.7 and 39.5; 16 tokens 21.1 and 20.4).
+// anybody.
 //
-// Warp 0 brings the tokens (two boxes of 64 of K, 128-byte swizzle), warp 14 the
-// weight's bytes (one box of 128 x 128, likewise), warp 1 issues the products, warps
-// 2 to 5 read the sums (after 1,024 of K or at the end of a row block) and finish
-// them, warps 6 to 13 widen the weight: four of them, one for each quarter of the
-// tensor memory's lanes, take every other piece.  A lane is a row: 128 bytes of it a
-// piece, which become 64 columns.  (Loading a lane's row straight into its registers, 32 rows a load
+// Warp 0 brings the tokens (two boxes of 64
+// of K, 128-byte swizzle), warp 14 the weight's bytes (one box of 128 x 128,
+// likewise), warp 1 issues the products, warps 2 to 5 read the sums (after 1,024
+// of K or at the end of a row block) and finish them, warps 6 to 13 widen the
+// weight: four of them, one for each quarter of the tensor memory's lanes, take
+// every other piece.  A lane is a row: 128 bytes of it a piece, which become 64
+// columns.  (Loading a lane's row straight into its registers, 32 rows a load
 // instruction, left the memory at 4.2 TB/s, and at less with more loads in
 // flight: a line's four sectors came in four requests.)
 constexpr int kPiece = 128;
@@ -312,10 +321,10 @@ constexpr uint32_t kAccAt = kRing * kPiece / 2; // columns: the weight, then two
 constexpr uint32_t kFewSmem = 226 * 1024;      // of the 227 KB, some static
 constexpr uint32_t kMaxRing = 8;                // stages of a ring in shared memory
 constexpr uint32_t kPieceBytes = kRows * kPiece;
-constexpr int kBars = 4 * kMaxRing + 2 * kRing + 4 + 4;
+constexpr int kBars = 4 * kMaxRing + 2 * kRing + 4 + 3;
 
 // Shared memory for a pass of `each` tokens: rings of the tokens and of the
-// weight's bytes, and the sums of a part.
+// weight's bytes, and the sums of a part longer than 1,024 of K.
 struct FewShape {
     uint32_t x_ring, w_ring, x_bytes, sums_at, w_at, scales_at, bars_at, bytes;
 };
@@ -377,101 +386,6 @@ struct Place {
     }
 };
 
-// Adds `bytes` of int32 in shared memory to memory, and waits until that is done.
-__device__ __forceinline__ void bulk_add(int32_t *dst, uint32_t src, uint32_t bytes)
-{
-    asm volatile("cp.reduce.async.bulk.global.shared::cta.bulk_group.add.s32 [%0], [%1], %2;" ::"l"(dst), "r"(src),
-                 "r"(bytes)
-                 : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    asm volatile("fence.proxy.async;" ::: "memory");
-}
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const int32_t *src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
-
-// Random words of elements e .. e+3; out of line, as above.
-__device__ __noinline__ uint4 words4(uint64_t e, uint32_t step, const RoundKeys &K)
-{
-    uint32_t r[8];
-    philox_q(e >> 2, step, K, r);
-    const uint32_t sel = static_cast<uint32_t>(e & 3u);
-    if (sel == 0) return make_uint4(r[0], r[1], r[2], r[3]);
-    philox_q((e >> 2) + 1, step, K, r + 4);
-    return sel == 1   ? make_uint4(r[1], r[2], r[3], r[4])
-           : sel == 2 ? make_uint4(r[2], r[3], r[4], r[5])
-                      : make_uint4(r[3], r[4], r[5], r[6]);
-}
-
-// The outputs of a row block (columns col0 on) from its sums, [token][128] in
-// shared memory: each of the four warps every fourth token, four columns a lane.
-// rs: the tokens' scales.
-__device__ __forceinline__ void finish(const Params &P, const int32_t *sums, uint32_t col0, uint32_t token0,
-                                       uint32_t tokens, uint32_t warp, int lane, const float *rs)
-{
-    const uint32_t col = col0 + 4 * lane;
-    if (col >= P.n) return;
-    const uint32_t live = min(P.n - col, 4u);
-    const bool vec = P.c_vec && live == 4, bf16 = P.c_dtype != ASR_F32, sr = P.rounding == ASR_ROUND_SR;
-    float cs[4];
-#pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) cs[i] = i < live ? __ldg(P.col_scale + col + i) : 0.0f;
-#pragma unroll 1
-    for (uint32_t t0 = warp; t0 < tokens; t0 += 8) {
-        float y[2][4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {               // the second may be past the last token: read, not stored
-            const uint32_t t = min(t0 + 4 * u, tokens - 1);
-            const int4 v = *reinterpret_cast<const int4 *>(sums + t * kRows + 4 * lane);
-            const float s = rs[t];
-            y[u][0] = __fmul_rn(__fmul_rn(__int2float_rn(v.x), s), cs[0]);
-            y[u][1] = __fmul_rn(__fmul_rn(__int2float_rn(v.y), s), cs[1]);
-            y[u][2] = __fmul_rn(__fmul_rn(__int2float_rn(v.z), s), cs[2]);
-            y[u][3] = __fmul_rn(__fmul_rn(__int2float_rn(v.w), s), cs[3]);
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const uint32_t t = t0 + 4 * u;
-            if (t >= tokens) break;
-            const uint64_t dst = (token0 + t) * P.ldc + col;
-            if (!bf16) {
-                float *c = static_cast<float *>(P.c) + dst;
-                if (vec) {
-                    *reinterpret_cast<float4 *>(c) = make_float4(y[u][0], y[u][1], y[u][2], y[u][3]);
-                } else {
-#pragma unroll
-                    for (uint32_t i = 0; i < 4; ++i)
-                        if (i < live) c[i] = y[u][i];
-                }
-                continue;
-            }
-            uint32_t h[4];
-            if (sr) {
-                const uint4 r = words4(static_cast<uint64_t>(token0 + t) * P.n + col, P.step, P.keys);
-                const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) h[i] = round_sr(y[u][i], w[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) h[i] = round_rne(y[u][i]);
-            }
-            uint16_t *c = static_cast<uint16_t *>(P.c) + dst;
-            if (vec) {
-                *reinterpret_cast<uint2 *>(c) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-            } else {
-#pragma unroll
-                for (uint32_t i = 0; i < 4; ++i)
-                    if (i < live) c[i] = static_cast<uint16_t>(h[i]);
-            }
-        }
-    }
-}
-
 __global__ void __launch_bounds__(kFewThreads, 1)
 few_rows_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                 const __grid_constant__ Params P, uint64_t limit_ns)
@@ -491,7 +405,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
     auto empty_a = [&](uint32_t i) { return bars + 8u * (4 * kMaxRing + kRing + i); };
     auto acc_full = [&](uint32_t i) { return bars + 8u * (4 * kMaxRing + 2 * kRing + i); };
     auto acc_empty = [&](uint32_t i) { return bars + 8u * (4 * kMaxRing + 2 * kRing + 2 + i); };
-    const uint32_t fetched = bars + 8u * (kBars - 4), added = bars + 8u * (kBars - 3), counted = added + 8u, drained = added + 16u, tmem_slot = drained + 8u;
+    const uint32_t added = bars + 8u * (kBars - 3), counted = added + 8u, drained = added + 16u, tmem_slot = drained + 8u;
 
     const int warp = prod::warp_index(), lane = threadIdx.x & 31;
     const uint32_t token0 = blockIdx.y * each, tokens = min(each, P.m - token0);
@@ -516,7 +430,6 @@ few_rows_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         }
         mbar_init(added, 4);
         mbar_init(counted, 1);
-        mbar_init(fetched, 1);
         mbar_init(drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -611,72 +524,80 @@ few_rows_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         for (uint32_t q = lane; q < each; q += 32) rs[q] = q < tokens ? P.row_scale[token0 + q] : 0.0f;
         __syncwarp();
         Place pl(first, P.pieces);
-        uint32_t r = 0, shares = 0, met = 0, fetches = 0, asked = 0;
-        // the four warps' writes to shared memory and reads of it so far are done
-        auto meet = [&]() {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(added);
-            return __all_sync(0xFFFFFFFFu, mbar_wait(added, met++ & 1u, limit_ns)) != 0;
-        };
+        uint32_t r = 0, shares = 0;
         bool held = false;                              // sums of this part in shared memory already
         for (uint32_t at = first; at < end; ++at) {
             if (pl.ends_run(at, end, P.pieces)) {
-                const uint32_t b = r & 1u;
+                const uint32_t b = r & 1u, out = pl.tile * kRows + row;
+                const float cs = out < P.n ? __ldg(P.col_scale + out) : 0.0f;
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_full(b), (r >> 1) & 1u, limit_ns))) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const bool last = pl.ends_part(at, end, P.pieces), whole = last && pl.part + 1 == P.pieces;
-                const uint32_t tq = tmem + ((quarter * 32) << 16) + kAccAt + b * kMaxTokens;
+                const uint32_t tq = tmem + ((quarter * 32) << 16) + kAccAt + b * kMaxTokens, col = out;
+                int32_t *shared = P.sums + (static_cast<uint64_t>(pl.tile) * P.m + token0) * kRows + row;
 #pragma unroll 1
                 for (uint32_t c = 0; c < tokens; c += 16) {
                     uint32_t v[16];
+                    int32_t sum[16];
                     gemm::tmem_ld16(tq + c, v);
-                    int32_t *to = sums + c * kRows + row;
 #pragma unroll
                     for (int q = 0; q < 16; ++q) {
-                        const int32_t sum = __float2int_rn(__uint_as_float(v[q]));
-                        to[q * kRows] = held ? to[q * kRows] + sum : sum;
+                        sum[q] = __float2int_rn(__uint_as_float(v[q]));
+                        if (held) sum[q] += sums[(c + q) * kRows + row];
+                    }
+                    if (!last) {
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) sums[(c + q) * kRows + row] = sum[q];
+                    } else if (!whole) {
+#pragma unroll
+                        for (int q = 0; q < 16; ++q)
+                            if (c + q < tokens) atomicAdd(shared + (c + q) * kRows, sum[q]);
+                    } else if (col < P.n) {
+                        store_outputs<16>(P, token0 + c, col, cs, rs + c, sum, tokens - c);
                     }
                 }
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(acc_empty(b));
                 held = !last;
-                if (last) {
-                    int32_t *shared = P.sums + (static_cast<uint64_t>(pl.tile) * P.m + token0) * kRows;
-                    bool mine = whole;
-                    asm volatile("fence.proxy.async;" ::: "memory");
-                    if (!meet()) break;
-                    if (!whole) {
-                        // the last CTA to add its part finishes the row block, on a copy of the sums
-                        if (threadIdx.x == 64) {
-                            const uint32_t run = pl.part + 1, bytes = tokens * kRows * 4;
-                            bulk_add(shared, smem_addr(sums), bytes);
-                            __threadfence();
-                            done = atomicAdd(P.counts + blockIdx.y * P.tiles + pl.tile, run) + run;
-                            if (done == P.pieces) {
-                                __threadfence();
-                                asm volatile("fence.proxy.async;" ::: "memory");
-                                ++asked;
-                                mbar_arrive_expect_tx(fetched, bytes);
-                                bulk_load(smem_addr(sums), shared, bytes, fetched);
-                            }
-                            mbar_arrive(counted);
-                        }
-                        if (!__all_sync(0xFFFFFFFFu, mbar_wait(counted, shares & 1u, limit_ns))) break;
-                        ++shares;
-                        mine = done == P.pieces;
-                        if (mine && !__all_sync(0xFFFFFFFFu, mbar_wait(fetched, fetches++ & 1u, limit_ns))) break;
+                if (last && !whole) {
+                    // the last CTA to add its part finishes the row block
+                    __threadfence();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(added);
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(added, shares & 1u, limit_ns))) break;
+                    if (threadIdx.x == 64) {
+                        const uint32_t run = pl.part + 1;
+                        done = atomicAdd(P.counts + blockIdx.y * P.tiles + pl.tile, run) + run;
+                        mbar_arrive(counted);
                     }
-                    if (mine) {
-                        finish(P, sums, pl.tile * kRows, token0, tokens, quarter, lane, rs);
-                        if (!meet()) break;
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(counted, shares & 1u, limit_ns))) break;
+                    ++shares;
+                    if (done == P.pieces) {
+                        __threadfence();
+                        // 64 tokens' loads at a time in flight
+#pragma unroll 1
+                        for (uint32_t c = 0; c < tokens && col < P.n; c += 64) {
+                            int32_t sum[64];
+#pragma unroll
+                            for (int h = 0; h < 4; ++h)
+                                if (c + 16 * h < tokens) {
+#pragma unroll
+                                    for (int q = 0; q < 16; ++q)
+                                        sum[16 * h + q] = __ldcg(shared + min(c + 16 * h + q, tokens - 1) * kRows);
+                                }
+#pragma unroll
+                            for (int h = 0; h < 4; ++h)
+                                if (c + 16 * h < tokens)
+                                    store_outputs<16>(P, token0 + c + 16 * h, col, cs, rs + c + 16 * h, sum + 16 * h,
+                                                      tokens - c - 16 * h);
+                        }
                     }
                 }
                 ++r;
             }
             pl.next(at, end, P.pieces);
         }
-        if (asked > fetches) mbar_wait(fetched, fetches & 1u, limit_ns);    // after a wait that ran out
     } else if (warp >= kWidener && warp < kWidener + 4 * kSets) {
         // ------------------------------------------------------- widening
         const uint32_t quarter = warp & 3u, row = quarter * 32 + lane;
