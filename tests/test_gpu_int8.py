@@ -160,7 +160,8 @@ def test_product_exact_at_the_ends_of_the_range(asr, size):
     assert_same_bits(host(c), host(_want_product(a, b, sa, sb)))
 
 
-@pytest.mark.parametrize("size", [(1, 515, 300), (6, 77, 100), (40, 130, 257), (300, 271, 513)])
+@pytest.mark.parametrize("size", [(1, 515, 300), (6, 77, 100), (40, 130, 257), (300, 271, 513),
+                                  (33, 130, 1500), (40, 260, 5000)])
 def test_product_stochastic_rounding(asr, orc, size):
     import torch
     m, n, k = size
@@ -194,7 +195,7 @@ def test_product_strided_unaligned(asr, m, dtype):
 
 @pytest.mark.parametrize("shift", [0, 1, 2, 3])
 @pytest.mark.parametrize("m,n,k", [(2, 70, 2049), (16, 64, 130), (17, 64, 130), (33, 129, 2051), (64, 130, 2048),
-                                   (65, 130, 2048), (150, 133, 5001), (256, 40, 8200), (257, 40, 8200)])
+                                   (65, 130, 2048), (150, 133, 5001), (256, 40, 8200), (257, 40, 8200), (300, 70, 12400)])
 def test_product_weight_at_any_address(asr, m, n, k, shift):
     """A weight whose rows follow one another without a gap, from any byte on to
     the end of its memory, on both sides of the choice between the kernels."""
