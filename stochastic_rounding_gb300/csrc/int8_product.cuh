@@ -248,11 +248,12 @@ int8_product_kernel(const __grid_constant__ Int8Products L, uint64_t limit_ns)
             const uint32_t c_hi = ncols < c_lo + span ? ncols : c_lo + span;
             const uint32_t col0 = it.n0 + c_lo, cols = c_hi > c_lo && row - lane < P.m ? c_hi - c_lo : 0;
             int32_t acc[kSpan];
-            // the scales, before the wait for the sums
+            // the scales, before the wait for the sums; ordinary loads, as the kernel
+            // that wrote them may have been running when this one started
             float scale[kSpan / 32];
 #pragma unroll
             for (int h = 0; h < kSpan / 32; ++h)
-                scale[h] = 32u * h + lane < cols ? __ldg(P.col_scale + col0 + 32 * h + lane) : 0.0f;
+                scale[h] = 32u * h + lane < cols ? P.col_scale[col0 + 32 * h + lane] : 0.0f;
             for (uint32_t kc = 0; kc < kblocks; kc += L.chunk, ++i) {
                 const int b = static_cast<int>(i % kAccBufs);
                 if (!__all_sync(0xFFFFFFFFu, pair_wait(acc_full(b), (i / kAccBufs) & 1u, limit_ns))) {

@@ -343,7 +343,9 @@ __device__ __forceinline__ void finish_block(const Params &P, uint32_t z, uint32
     }
     next();
     if constexpr (OP == kScaled) {
-        const float rs = in ? __ldg(P.row_scale + row) : 0.0f;
+        // written by a kernel that may have been running when this one started: an
+        // ordinary load (the read-only path is for what nobody writes meanwhile)
+        const float rs = in ? P.row_scale[row] : 0.0f;
 #pragma unroll
         for (int q = 0; q < 16; ++q) x[q] = __fmul_rn(__fmul_rn(x[q], rs), col_scale[q]);
     }

@@ -1,0 +1,61 @@
+"""The linear layer's 8-bit calls and the module on them, beyond single
+products: calls one after another, gradients on their own, the module's inputs
+and state."""
+import numpy as np
+import pytest
+
+from gpu_util import assert_same_bits, host, torch_cuda
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def asr():
+    torch_cuda()
+    from stochastic_rounding_gb300 import build
+    build.build()
+    import stochastic_rounding_gb300 as m
+    yield m
+    assert m.asr_take_device_error() == 0
+
+
+def _want_product(a, b, sa, sb):
+    """Of int8 matrices, as the product is defined: the exact sum, then binary32."""
+    s = a.double() @ b.double().t()              # whole numbers below 2^53: exact in any order
+    return (s.float() * sa[:, None]) * sb[None]
+
+
+def _quantised(asr, v, axis="rows", **kw):
+    import torch
+    q = asr.int8_empty(*(v.shape if axis == "rows" else v.shape[::-1]))
+    return asr.asr_quantize_int8(v, q, torch.empty(q.shape[0], device="cuda"), axis=axis, **kw)
+
+
+def test_scales_of_one_call_after_another(asr):
+    """Calls in a row through one workspace, of operands whose scales differ by
+    powers of two: each has the scales of its own operands, not those that the
+    same memory held for the call before."""
+    import torch
+    torch.manual_seed(1)
+    t, n, k = 300, 400, 260
+    x, w, dy = (torch.randn(*s, device="cuda").to(torch.bfloat16) for s in ((t, k), (n, k), (t, n)))
+    qw, sw = _quantised(asr, w)
+    size = max(asr.asr_linear_int8_workspace(t, n, k), asr.asr_linear_int8_grads_workspace(t, n, k))
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    y1 = asr.asr_linear_int8(x, qw, sw, torch.empty(t, n, device="cuda"), workspace=ws)
+    dx1, dw1 = asr.int8_linear_grads(dy, x, w, step=1)
+    xs, dys, ys, dxs, dws = [], [], [], [], []
+    scales = [2.0 ** (i % 7 - 3) for i in range(40)]
+    for f in scales:
+        xs.append(x * f)
+        dys.append(dy * f)
+        ys.append(torch.empty(t, n, device="cuda"))
+        dxs.append(torch.empty(t, k, device="cuda", dtype=torch.bfloat16))
+        dws.append(torch.empty(n, k, device="cuda", dtype=torch.bfloat16))
+    for a, d, y, gx, gw in zip(xs, dys, ys, dxs, dws):
+        asr.asr_linear_int8(a, qw, sw, y, workspace=ws)
+        asr.asr_linear_int8_grads(d, a, w, gx, gw, step=1, workspace=ws)
+    for f, y, gx, gw in zip(scales, ys, dxs, dws):
+        assert torch.equal(y, y1 * f)
+        assert torch.equal(gx, dx1 * f)
+        assert torch.equal(gw, dw1 * (f * f))
