@@ -12,6 +12,7 @@ package updates.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from ._lib import asr_linear_int8, asr_linear_int8_grads, asr_quantize_int8, int8_empty
 
@@ -45,6 +46,7 @@ class _Int8LinearFunction(torch.autograd.Function):
         return int8_linear(x, q, scale)
 
     @staticmethod
+    @once_differentiable                    # the calls record nothing: a second derivative through them is an error
     def backward(ctx, dy):
         x, weight = ctx.saved_tensors
         step, seed = ctx.key
