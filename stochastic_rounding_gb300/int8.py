@@ -35,9 +35,17 @@ def int8_linear_grads(dy, x, weight, *, step: int = 0, seed: int = 0, need_dx=Tr
     return dx, dw
 
 
+def _by_rows(t):
+    """``t``, or a copy of it where its rows are not contiguous or overlap."""
+    rows, cols = t.shape
+    ok = (cols <= 1 or t.stride(1) == 1) and (rows <= 1 or t.stride(0) >= cols)
+    return t if ok else t.contiguous()
+
+
 class _Int8LinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, step, seed):
+        x, weight = _by_rows(x), _by_rows(weight)
         ctx.save_for_backward(x, weight)
         ctx.key = (step, seed)
         q = int8_empty(*weight.shape, weight.device)

@@ -59,3 +59,24 @@ def test_scales_of_one_call_after_another(asr):
         assert torch.equal(y, y1 * f)
         assert torch.equal(gx, dx1 * f)
         assert torch.equal(gw, dw1 * (f * f))
+
+
+def test_module_inputs_of_any_layout(asr):
+    """Transposed and broadcast inputs, and a transposed weight, give what their
+    contiguous copies give."""
+    import torch
+    torch.manual_seed(2)
+    base = torch.randn(72, 40, device="cuda", dtype=torch.bfloat16)
+    inputs = [torch.randn(1, 72, 50, device="cuda", dtype=torch.bfloat16).transpose(1, 2),
+              torch.randn(1, 72, device="cuda", dtype=torch.bfloat16).expand(50, 72)]
+    for x in inputs:
+        got = []
+        for copy in (False, True):
+            layer = asr.Int8Linear(72, 40, seed=3, device="cuda")
+            layer.weight = torch.nn.Parameter(base.t().contiguous() if copy else base.t())
+            v = (x.contiguous() if copy else x).detach().requires_grad_()
+            y = layer(v)
+            y.float().square().sum().backward()
+            got.append([host(t.detach().contiguous()) for t in (y, v.grad, layer.weight.grad)])
+        for a, b in zip(*got):
+            assert_same_bits(a, b)
