@@ -68,8 +68,11 @@ class Int8Linear(torch.nn.Module):
     """``torch.nn.Linear`` without a bias on the 8-bit products: a bf16 (or
     float32) weight of shape (out_features, in_features), quantised in every
     forward pass.  ``seed`` keys the stochastic rounding of the gradients; it
-    is drawn anew for every forward pass of the layer (the pass's number is the
-    Philox step), so a run repeats bit for bit."""
+    is drawn anew for every forward pass that records gradients (``calls``, the
+    number of such passes, is the Philox step).  ``calls`` is part of the state
+    dict (``_extra_state``), so a run repeats bit for bit, resumed from a checkpoint or
+    not; a state dict without it, such as ``torch.nn.Linear``'s, loads too and
+    leaves it as it is."""
 
     def __init__(self, in_features: int, out_features: int, *, seed: int = 0, device=None, dtype=torch.bfloat16):
         super().__init__()
@@ -78,10 +81,24 @@ class Int8Linear(torch.nn.Module):
         torch.nn.init.normal_(self.weight, std=in_features ** -0.5)
 
     def forward(self, x):
-        self.calls += 1
+        if torch.is_grad_enabled() and (x.requires_grad or self.weight.requires_grad):
+            self.calls += 1
         flat = x.reshape(-1, self.in_features)
         y = _Int8LinearFunction.apply(flat, self.weight, self.calls, self.seed)
         return y.reshape(*x.shape[:-1], self.out_features)
+
+    def get_extra_state(self):
+        return torch.tensor(self.calls, device="cpu")
+
+    def set_extra_state(self, state):
+        self.calls = int(state)
+
+    def _load_from_state_dict(self, state_dict, prefix, local_metadata, strict, missing_keys, unexpected_keys,
+                              error_msgs):
+        super()._load_from_state_dict(state_dict, prefix, local_metadata, strict, missing_keys, unexpected_keys,
+                                      error_msgs)
+        if prefix + "_extra_state" in missing_keys:
+            missing_keys.remove(prefix + "_extra_state")
 
     def extra_repr(self):
         return f"in_features={self.in_features}, out_features={self.out_features}, seed={self.seed}"

@@ -80,3 +80,41 @@ def test_module_inputs_of_any_layout(asr):
             got.append([host(t.detach().contiguous()) for t in (y, v.grad, layer.weight.grad)])
         for a, b in zip(*got):
             assert_same_bits(a, b)
+
+
+def test_a_run_resumed_from_a_checkpoint_repeats(asr):
+    """Six steps in one go, and three, a checkpoint (saved and loaded), evaluation
+    and three more: the same weights and momentum, bit for bit."""
+    import io
+    import torch
+    rows = [torch.randn(48, 64, device="cuda", generator=torch.Generator("cuda").manual_seed(i)).bfloat16()
+            for i in range(6)]
+
+    def make():
+        torch.manual_seed(4)
+        net = torch.nn.Sequential(asr.Int8Linear(64, 96, seed=11, device="cuda"), torch.nn.ReLU(),
+                                  asr.Int8Linear(96, 64, seed=12, device="cuda"))
+        return net, asr.MuonSR(net.parameters(), lr=0.02, seed=13)
+
+    def steps(net, opt, batches):
+        for x in batches:
+            opt.zero_grad()
+            (net(x).float() - x.float()).square().mean().backward()
+            opt.step()
+    net, opt = make()
+    steps(net, opt, rows)
+    half, half_opt = make()
+    steps(half, half_opt, rows[:3])
+    with torch.no_grad():
+        half(rows[0])
+    file = io.BytesIO()
+    torch.save({"net": half.state_dict(), "opt": half_opt.state_dict()}, file)
+    file.seek(0)
+    saved = torch.load(file, weights_only=True)
+    rest, rest_opt = make()
+    rest.load_state_dict(saved["net"])
+    rest_opt.load_state_dict(saved["opt"])
+    steps(rest, rest_opt, rows[3:])
+    for p, q in zip(net.parameters(), rest.parameters()):
+        assert_same_bits(host(p), host(q))
+        assert_same_bits(host(opt.state[p]["momentum_buffer"]), host(rest_opt.state[q]["momentum_buffer"]))

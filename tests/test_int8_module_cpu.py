@@ -104,3 +104,49 @@ def test_weight_of_any_layout(calls):
     x = torch.randn(5, 8)
     layer(x).float().sum().backward()
     assert torch.allclose(layer.weight.grad, x.sum(0).expand(6, 8), rtol=2.0 ** -7, atol=2.0 ** -7 * 5)
+
+
+def _train(layer, passes, calls, evaluate=0):
+    for _ in range(passes):
+        for _ in range(evaluate):
+            with torch.no_grad():
+                layer(torch.ones(2, 8))
+        layer(torch.ones(2, 8)).float().sum().backward()
+    return calls.steps
+
+
+def test_a_resumed_layer_goes_on_with_its_random_numbers(calls):
+    """The count of passes is part of the state, so passes after a checkpoint draw
+    what they draw without one."""
+    whole = _train(int8.Int8Linear(8, 6), 5, calls)[:]
+    calls.steps.clear()
+    first = int8.Int8Linear(8, 6)
+    _train(first, 2, calls)
+    second = int8.Int8Linear(8, 6)
+    second.load_state_dict(first.state_dict())
+    assert _train(second, 3, calls) == whole == [1, 2, 3, 4, 5]
+
+
+def test_passes_without_gradients_draw_nothing(calls):
+    """A run that is evaluated in between draws the numbers of one that is not."""
+    assert _train(int8.Int8Linear(8, 6), 3, calls, evaluate=2) == [1, 2, 3]
+    frozen = int8.Int8Linear(8, 6)
+    frozen.weight.requires_grad_(False)
+    frozen(torch.ones(2, 8))
+    assert frozen.calls == 0
+    frozen(torch.ones(2, 8, requires_grad=True))
+    assert frozen.calls == 1
+
+
+def test_state_of_other_modules_and_of_older_checkpoints(calls):
+    """A dictionary with the weight alone loads, and leaves the count as it is."""
+    layer = int8.Int8Linear(8, 6)
+    _train(layer, 2, calls)
+    plain = torch.nn.Linear(8, 6, bias=False)
+    assert not layer.load_state_dict(plain.state_dict()).missing_keys and layer.calls == 2
+    net = torch.nn.Sequential(int8.Int8Linear(8, 6), int8.Int8Linear(6, 8))
+    net.load_state_dict({k: v for k, v in net.state_dict().items() if k.endswith("weight")})
+    with pytest.raises(RuntimeError):
+        layer.load_state_dict({})
+    with pytest.raises(RuntimeError):
+        layer.load_state_dict({**plain.state_dict(), "bias": torch.zeros(6)})
