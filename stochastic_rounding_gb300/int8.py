@@ -72,7 +72,13 @@ class Int8Linear(torch.nn.Module):
     number of such passes, is the Philox step).  ``calls`` is part of the state
     dict (``_extra_state``), so a run repeats bit for bit, resumed from a checkpoint or
     not; a state dict without it, such as ``torch.nn.Linear``'s, loads too and
-    leaves it as it is."""
+    leaves it as it is.
+
+    The random bits of an output gradient's element are those of its index in
+    (tokens, out_features), from position 0 on, under (seed, pass).  Layers that share a
+    seed share them, as do data-parallel ranks, and an optimizer of that seed
+    uses them for its first parameters: give each layer and rank a seed of its
+    own where the errors are to be independent."""
 
     def __init__(self, in_features: int, out_features: int, *, seed: int = 0, device=None, dtype=torch.bfloat16):
         super().__init__()

@@ -6,7 +6,9 @@ bfloat16 parameters are decayed, stepped and rounded stochastically in place.
 The rounding bits are keyed by (seed, step) and indexed by each element's global
 parameter position, as ``AdamWSR``'s are (``stochastic_rounding_gb300.optim``
 says how positions are given, and when the device error bit is read), so a
-model's matrices can go to ``MuonSR`` and its other parameters to ``AdamWSR``.
+model's matrices can go to ``MuonSR`` and its other parameters to ``AdamWSR``:
+with one seed, at positions of their own (``base_offset`` of the second: the
+number of elements of the first), or the two would round with the same bits.
 An update depends on the whole matrix: unlike AdamW's, a step of a matrix cannot
 be cut into shards.
 
