@@ -394,7 +394,9 @@ asr_status asr_linear_int8_workspace(uint64_t m, uint64_t n, uint64_t k, uint64_
  *   dw = dy^T . x   dy's columns rounded stochastically, x's columns to nearest
  * both bf16, to nearest; bitwise what the quantiser and the product give.
  * dx or dw may be NULL where it is not needed (then w, or x, may be NULL).
- * tokens, n and k between 1 and 131071. */
+ * The sums over n and over tokens are exact at any length.  tokens, n and k
+ * at least 1, tokens and n at most 2^24, k at most 131071, as in the forward
+ * call; each of the three matrices has fewer than 5 * 10^11 elements. */
 asr_status asr_linear_int8_grads(const void *dy, int32_t dy_dtype, uint64_t dy_ld, const void *x, int32_t x_dtype,
                                  uint64_t x_ld, const void *w, int32_t w_dtype, uint64_t w_ld, uint16_t *dx,
                                  uint64_t dx_ld, uint16_t *dw, uint64_t dw_ld, uint64_t tokens, uint64_t n,

@@ -29,7 +29,7 @@
 namespace int8 {
 
 constexpr int kThreads = 256;
-constexpr uint64_t kMaxK = 131071;              // 128^2 K < 2^31
+constexpr uint64_t kMaxK = prod::kMaxIntSum;
 constexpr uint32_t kChunk = 1024 / prod::kBK;
 
 struct WidenParams {
@@ -929,7 +929,7 @@ GradLayout grad_layout(uint64_t t, uint64_t n, uint64_t k, bool dx, bool dw)
 
 bool grad_sizes_ok(uint64_t t, uint64_t n, uint64_t k)
 {
-    return sizes_ok(t, n, k) && n <= kMaxK && t <= kMaxK && k <= kMaxK;
+    return sizes_ok(t, n, k) && quantisable(t, n) && quantisable(n, k) && quantisable(t, k);
 }
 
 struct GradSource {

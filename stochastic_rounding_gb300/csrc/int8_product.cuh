@@ -5,7 +5,10 @@
 // The sum over K is cut into chunks of 1,024, each accumulated on its own in
 // tensor memory -- exact in binary32 -- and added up by the epilogue warps in
 // int32 registers; the next chunk's products go into the other accumulator
-// meanwhile.  The two products of a backward pass (dx and dw) go as one list of
+// meanwhile.  Sums of more than 131,071 products (gradients over as many tokens
+// or outputs), which int32 need not hold, are added up in int64 by a form of the
+// kernel of its own (LONG), whose running sums do not fit the registers (dw of
+// 1,024 x 2,048 over 131,071 tokens 962 us, over 131,072 974 us).  The two products of a backward pass (dx and dw) go as one list of
 // tiles, those of the longer sum first: in a launch each, both leave their last
 // round of tiles part empty, and small ones pay for two launches (4,096 tokens,
 // 8,192 x 2,048: the call 295 us with two, 273 with one; 1,111 tokens, 515 x 1,365:
@@ -17,6 +20,8 @@
 // ones the chain of copies, sums and epilogue (20 us for 777 x 1,001 x 2,049).
 
 namespace prod {
+
+constexpr uint32_t kMaxIntSum = 131071;         // 128^2 of each product: below 2^31
 
 struct Int8Product {
     Params P;                       // sizes, output, scales; parts of its tiles in the last round
@@ -65,6 +70,7 @@ __device__ __forceinline__ Int8Item int8_item(const Int8Products &L, uint32_t t,
 }
 
 // Persistent over work items: cluster c takes items c, c + clusters, ...
+template <bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
 int8_product_kernel(const __grid_constant__ Int8Products L, uint64_t limit_ns)
 {
@@ -247,7 +253,7 @@ int8_product_kernel(const __grid_constant__ Int8Products L, uint64_t limit_ns)
             const uint32_t span = it.width / (kEpi / 4), c_lo = group * span;      // this warp's columns
             const uint32_t c_hi = ncols < c_lo + span ? ncols : c_lo + span;
             const uint32_t col0 = it.n0 + c_lo, cols = c_hi > c_lo && row - lane < P.m ? c_hi - c_lo : 0;
-            int32_t acc[kSpan];
+            std::conditional_t<LONG, int64_t, int32_t> acc[kSpan];
             // the scales, before the wait for the sums; ordinary loads, as the kernel
             // that wrote them may have been running when this one started
             float scale[kSpan / 32];
@@ -289,7 +295,7 @@ int8_product_kernel(const __grid_constant__ Int8Products L, uint64_t limit_ns)
                         if (c != d) continue;
 #pragma unroll
                         for (int q = 0; q < 16; ++q) {
-                            x[q] = __int2float_rn(acc[d + q]);
+                            x[q] = LONG ? __ll2float_rn(acc[d + q]) : __int2float_rn(static_cast<int32_t>(acc[d + q]));
                             cs[q] = __shfl_sync(0xFFFFFFFFu, scale[d / 32], (d & 31) + q);
                         }
                     }
@@ -324,7 +330,8 @@ asr_status int8_setup(int *pairs)
     std::lock_guard<std::mutex> lk(g_prod_mu);
     if (!g_int8_ready[dev]) {
         int n = 0;
-        e = setup_one(int8_product_kernel, &n);
+        e = setup_one(int8_product_kernel<false>, &n);
+        if (e == cudaSuccess) e = setup_one(int8_product_kernel<true>, &n);
         if (e != cudaSuccess) return cuda_fail(e);
         if (n < 1) return cuda_fail(cudaErrorNotSupported);
         g_int8_pairs[dev] = n;
@@ -412,7 +419,9 @@ asr_status int8_launch(Int8Products &L, Stored operands[4], uint32_t chunk, cuda
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     const uint64_t limit = kWaitLimitNs;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, int8_product_kernel, L, limit);
+    const bool wide_sums = L.p[0].P.k > kMaxIntSum || L.p[1].P.k > kMaxIntSum;
+    const cudaError_t e = wide_sums ? cudaLaunchKernelEx(&cfg, int8_product_kernel<true>, L, limit)
+                                    : cudaLaunchKernelEx(&cfg, int8_product_kernel<false>, L, limit);
     if (e != cudaSuccess) return cuda_fail(e);
     return launched(ASR_KERNEL_PRODUCT);
 }

@@ -118,3 +118,26 @@ def test_a_run_resumed_from_a_checkpoint_repeats(asr):
     for p, q in zip(net.parameters(), rest.parameters()):
         assert_same_bits(host(p), host(q))
         assert_same_bits(host(opt.state[p]["momentum_buffer"]), host(rest_opt.state[q]["momentum_buffer"]))
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("size", [(131072, 40, 72), (150001, 72, 40), (24, 151936, 200), (300, 131073, 272)])
+def test_gradients_of_long_sums(asr, size, dtype):
+    """More tokens, or outputs (a vocabulary), than int32 sums can hold: exact, of
+    random operands and of constant ones (whose sums pass 2^31)."""
+    import torch
+    t, n, k = size
+    torch.manual_seed(n)
+    for constant in (False, True):
+        mk = lambda *s: (torch.full(s, 0.75, device="cuda") if constant else torch.randn(s, device="cuda")  # noqa: E731
+                         ).to(getattr(torch, dtype))
+        dy, x, w = mk(t, n), mk(t, k), mk(n, k)
+        dx, dw = asr.int8_linear_grads(dy, x, w, step=2, seed=5)
+        sr = dict(rounding="sr", step=2, seed=5)
+        a, sa = _quantised(asr, dy, **sr)
+        b, sb = _quantised(asr, w, axis="columns")
+        assert_same_bits(host(dx), host(_want_product(a, b, sa, sb).bfloat16()))
+        a, sa = _quantised(asr, dy, axis="columns", **sr)
+        b, sb = _quantised(asr, x, axis="columns")
+        assert_same_bits(host(dw), host(_want_product(a, b, sa, sb).bfloat16()))
+        assert not constant or (a == 127).all() and (b == 127).all()
