@@ -261,7 +261,8 @@ asr_status asr_gemm_bf16_sr(const uint16_t *a, const uint16_t *b, uint16_t *c, f
  * a + b x^2 + c x^4, must stay within 8 over all steps, otherwise
  * ASR_ERR_INVALID_VALUE (the usual 3.4445, -4.7750, 2.0315 stay below 3.5).
  * A zero matrix gives zeros; one that holds an infinity or a NaN, or whose sum
- * of squares overflows binary32, gives NaN throughout.  1 <= steps <= 100,
+ * of squares overflows binary32, gives NaN throughout.  The norm holds down to
+ * the smallest eps: small squares are not lost.  1 <= steps <= 100,
  * 1e-30 <= eps <= 1e30, rows and cols at most 2^20. */
 typedef struct {
     double a, b, c;

@@ -49,7 +49,7 @@ struct PrepParams {
     uint32_t nesterov;
     float mu, omu;                          // momentum, 1 - momentum
     float eps;
-    float *partial;                         // [batch][blocks]
+    float2 *partial;                        // [batch][blocks]
     __half *out;                            // [batch][rows][ld], 2^12 X
     uint64_t out_ld, out_stride;
     Matrix m[prod::kMaxBatch];
@@ -86,6 +86,44 @@ __device__ __forceinline__ float update_of(const PrepParams &P, float g, float m
     return P.nesterov ? __fadd_rn(g, __fmul_rn(P.mu, __fsub_rn(m, g))) : m;
 }
 
+// A sum of squares of x, and of 2^64 x.  The first is used unless it is below
+// 2^-60; squares below 2^-126, which binary32 loses, do not matter in one that is
+// not.  If it is, every x is below 2^-30 and the second does not overflow.
+// (Squares alone: entries of 1e-23 come out as zeros, and 2^12 x / eps past f16.)
+struct Squares {
+    float plain, raised;
+};
+
+__device__ __forceinline__ void add_square(Squares &s, float x)
+{
+    s.plain = fmaf(x, x, s.plain);
+    const float y = __fmul_rn(x, 0x1p64f);
+    s.raised = fmaf(y, y, s.raised);
+}
+
+__device__ __forceinline__ void add_squares(Squares &s, float plain, float raised)
+{
+    s.plain += plain;
+    s.raised += raised;
+}
+
+// Over a warp, in every lane.
+__device__ __forceinline__ void add_warp(Squares &s)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        add_squares(s, __shfl_xor_sync(0xFFFFFFFFu, s.plain, o), __shfl_xor_sync(0xFFFFFFFFu, s.raised, o));
+}
+
+// What X_0 = G / max(norm, eps) is multiplied with to be stored.  A norm that is
+// not finite makes every entry NaN, so that a gradient holding an infinity or a
+// NaN shows in the whole result.
+__device__ __forceinline__ float factor_of(const Squares &s, float eps)
+{
+    const float norm = s.plain < 0x1p-60f ? __fmul_rn(__fsqrt_rn(s.raised), 0x1p-64f) : __fsqrt_rn(s.plain);
+    return norm <= 3.402823466e38f ? __fdiv_rn(kStore, fmaxf(norm, eps)) : __int_as_float(0x7FC00000);
+}
+
 // A warp's way through a matrix in spans of kSpan columns: span `at` counted
 // along the rows, then every `stride`-th.  One division at the start instead of
 // one an element.
@@ -114,14 +152,14 @@ struct Walk {
     }
 };
 
-// First pass: m <- m + (1 - mu)(g - m) (MUON), and each block's sum of squares.
+// First pass: m <- m + (1 - mu)(g - m) (MUON), and each block's sums of squares.
 template <bool MUON>
 __global__ void __launch_bounds__(kThreads) square_sum_kernel(const __grid_constant__ PrepParams P)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Matrix M = P.m[blockIdx.y];
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float sum = 0.0f;
+    Squares sum = {0.0f, 0.0f};
     for (Walk k(P.rows, P.cols, blockIdx.x * 8ull + warp, P.blocks * 8ull); k.more(); k.next()) {
         const uint64_t row = k.row, col = k.span * static_cast<uint64_t>(kSpan) + lane * 8;
         if (col >= P.cols) continue;
@@ -147,40 +185,39 @@ __global__ void __launch_bounds__(kThreads) square_sum_kernel(const __grid_const
             }
         }
 #pragma unroll
-        for (int q = 0; q < 8; ++q) sum = fmaf(x[q], x[q], sum);
+        for (int q = 0; q < 8; ++q) add_square(sum, x[q]);
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    __shared__ float part[kThreads / 32];
+    add_warp(sum);
+    __shared__ Squares part[kThreads / 32];
     if (lane == 0) part[warp] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 1; w < kThreads / 32; ++w) sum += part[w];
-        P.partial[blockIdx.y * P.blocks + blockIdx.x] = sum;
+        for (int w = 1; w < kThreads / 32; ++w) add_squares(sum, part[w].plain, part[w].raised);
+        P.partial[blockIdx.y * P.blocks + blockIdx.x] = make_float2(sum.plain, sum.raised);
     }
 }
 
 // Second pass: X_0 in f16.  Each block adds the matrix's partial sums again, in
-// one order.  A norm that is not finite makes every entry NaN, so that a
-// gradient holding an infinity or a NaN shows in the whole result.
+// one order.
 template <bool MUON>
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ PrepParams P)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Matrix M = P.m[blockIdx.y];
-    __shared__ float part[kThreads / 32];
+    __shared__ Squares part[kThreads / 32];
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float sum = 0.0f;
-    for (uint32_t i = threadIdx.x; i < P.blocks; i += kThreads) sum += P.partial[blockIdx.y * P.blocks + i];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    Squares sum = {0.0f, 0.0f};
+    for (uint32_t i = threadIdx.x; i < P.blocks; i += kThreads) {
+        const float2 v = P.partial[blockIdx.y * P.blocks + i];
+        add_squares(sum, v.x, v.y);
+    }
+    add_warp(sum);
     if (lane == 0) part[warp] = sum;
     __syncthreads();
-    sum = 0.0f;
-    for (int w = 0; w < kThreads / 32; ++w) sum += part[w];
-    const float norm = __fsqrt_rn(sum);
-    const float f = norm <= 3.402823466e38f ? __fdiv_rn(kStore, fmaxf(norm, P.eps)) : __int_as_float(0x7FC00000);
+    sum = {0.0f, 0.0f};
+    for (int w = 0; w < kThreads / 32; ++w) add_squares(sum, part[w].plain, part[w].raised);
+    const float f = factor_of(sum, P.eps);
     __half *out = P.out + blockIdx.y * P.out_stride;
     for (Walk k(P.rows, P.cols, blockIdx.x * 8ull + warp, gridDim.x * 8ull); k.more(); k.next()) {
         const uint64_t row = k.row, col = k.span * static_cast<uint64_t>(kSpan) + lane * 8;
@@ -276,7 +313,7 @@ Layout layout(uint64_t rows, uint64_t cols, uint64_t batch)
     L.lds = up(L.m, 16);
     const uint64_t x = up(rows * L.ldx * 2, 256) * batch, s = up(L.m * L.lds * 2, 256) * batch;
     L.partial = 0;
-    L.x0 = up(batch * kPartBlocks * sizeof(float), 256);
+    L.x0 = up(batch * kPartBlocks * sizeof(float2), 256);
     L.x1 = L.x0 + x;
     L.s = L.x1 + x;
     L.p = L.s + s;
@@ -319,7 +356,7 @@ asr_status prep(const Group &G, const NsParams &ns, const Layout &L, char *ws, f
     const uint64_t want = (G.rows * ((G.cols + kSpan - 1) / kSpan) + 7) / 8;
     const uint64_t fill = std::max<uint64_t>(16, std::min<uint64_t>(kPartBlocks, 1216 / G.batch));
     P.blocks = static_cast<uint32_t>(want < fill ? want : fill);
-    P.partial = reinterpret_cast<float *>(ws + L.partial);
+    P.partial = reinterpret_cast<float2 *>(ws + L.partial);
     P.out = reinterpret_cast<__half *>(ws + L.x0);
     P.out_ld = L.ldx;
     P.out_stride = up(G.rows * L.ldx * 2, 256) / 2;

@@ -92,7 +92,7 @@ skinny_kernel(const __grid_constant__ SkinnyParams P, uint64_t limit_ns)
     extern __shared__ __align__(128) unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t bar_mem;
     __shared__ uint32_t tmem_slot;
-    __shared__ float squares[8], total;
+    __shared__ Squares squares[8], total;
     const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
     unsigned char *xs = smem_raw + (base - raw), *ss = xs + kSkinnyX, *ps = ss + kSkinnyS;
     float *part = reinterpret_cast<float *>(ps);
@@ -134,7 +134,7 @@ skinny_kernel(const __grid_constant__ SkinnyParams P, uint64_t limit_ns)
             f(line, c, live, row * P.in.cols + col, x);
         }
     };
-    float sum = 0.0f;
+    Squares sum = {0.0f, 0.0f};
     visit([&](uint32_t, uint32_t, int live, uint64_t at, float x[8]) {
         if (MUON) {
             float m[8];
@@ -154,27 +154,27 @@ skinny_kernel(const __grid_constant__ SkinnyParams P, uint64_t limit_ns)
             }
         }
 #pragma unroll
-        for (int q = 0; q < 8; ++q) sum = fmaf(x[q], x[q], sum);
+        for (int q = 0; q < 8; ++q) add_square(sum, x[q]);
     });
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    add_warp(sum);
     if (lane == 0) squares[warp] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 1; w < 8; ++w) sum += squares[w];
+        for (int w = 1; w < 8; ++w) add_squares(sum, squares[w].plain, squares[w].raised);
         total = sum;
     }
     gemm::cluster_sync();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_slot, 0);
-    sum = 0.0f;
+    sum = {0.0f, 0.0f};
     for (uint32_t r = 0; r < ctas; ++r) {
-        float v;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(gemm::peer_addr(smem_addr(&total), r)) : "memory");
-        sum += v;
+        float v, w;
+        const uint32_t at = gemm::peer_addr(smem_addr(&total), r);
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(w) : "r"(at + 4) : "memory");
+        add_squares(sum, v, w);
     }
-    const float norm = __fsqrt_rn(sum);
-    const float f = norm <= 3.402823466e38f ? __fdiv_rn(kStore, fmaxf(norm, P.in.eps)) : __int_as_float(0x7FC00000);
+    const float f = factor_of(sum, P.in.eps);
     visit([&](uint32_t line, uint32_t c, int live, uint64_t at, float x[8]) {
         if (MUON) {
             float m[8];

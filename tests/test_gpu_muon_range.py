@@ -1,0 +1,81 @@
+"""Newton-Schulz and the Muon step past the sizes and values of the ordinary
+tests: gradients whose squares binary32 loses, and products of more tiles than
+the GPU takes at once.  The bound is derived in test_gpu_muon.py."""
+import pytest
+
+from gpu_util import torch_cuda
+
+pytestmark = pytest.mark.gpu
+ABC = (3.4445, -4.7750, 2.0315)
+
+
+@pytest.fixture(scope="module")
+def asr():
+    torch_cuda()
+    from stochastic_rounding_gb300 import build
+    build.build()
+    import stochastic_rounding_gb300 as m
+    yield m
+    assert m.asr_take_device_error() == 0
+
+
+def _exact(g, eps=1e-7):
+    x = g.double()
+    x = x / max(float(x.norm()), eps)
+    if x.shape[0] > x.shape[1]:
+        x = x.t()
+    a, b, c = ABC
+    for _ in range(5):
+        s = x @ x.t()
+        x = a * x + (b * s + c * (s @ s)) @ x
+    return x.t() if g.shape[0] > g.shape[1] else x
+
+
+BOUND = 3 * 5 * 2.0 ** -11 + 2.0 ** -9
+
+
+def _far(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+# one CTA a matrix, clusters, products in memory; wide and tall
+@pytest.mark.parametrize("shape", [(96, 160), (700, 128), (100, 4000), (256, 256), (515, 300)])
+@pytest.mark.parametrize("size", [1e-12, 1e-18, 1e-20, 1e-23, 3e-26, 1e-29])
+def test_gradients_whose_squares_underflow(asr, shape, size):
+    import torch
+    torch.manual_seed(7)
+    g = torch.randn(shape, device="cuda") * size
+    out = torch.empty(shape, device="cuda", dtype=torch.bfloat16)
+    asr.asr_newton_schulz([(g, out)], eps=1e-30)
+    assert _far(out, _exact(g, 1e-30)) <= BOUND
+    p, m = torch.zeros(shape, device="cuda"), torch.zeros(shape, device="cuda")
+    asr.asr_muon_sr_multi_tensor([(p, g, m, 0)], lr=1.0, momentum=0.5, weight_decay=0.0, nesterov=False, adjust=None,
+                                 step=1, eps=1e-30)
+    assert _far(-p, _exact(m, 1e-30)) <= BOUND
+
+
+@pytest.mark.parametrize("shape", [(96, 160), (256, 256)])
+def test_gradients_below_eps(asr, shape):
+    """A norm below eps: G / eps, not G / |G|."""
+    import torch
+    torch.manual_seed(8)
+    g = torch.randn(shape, device="cuda")
+    g *= 0.25e-20 / float(g.norm())
+    out = torch.empty(shape, device="cuda", dtype=torch.bfloat16)
+    asr.asr_newton_schulz([(g, out)], eps=1e-20)
+    assert _far(out, _exact(g, 1e-20)) <= BOUND
+
+
+@pytest.mark.parametrize("shape", [(96, 160), (256, 256)])
+def test_small_entries_beside_large_ones(asr, shape):
+    """Squares that underflow next to ones that do not, on both sides of where
+    the sums change over (a sum of squares of 2^-60)."""
+    import torch
+    torch.manual_seed(9)
+    for top in (1e-8, 2.0 ** -30, 1e-10):
+        g = torch.randn(shape, device="cuda") * 1e-22
+        g[::7] = torch.randn_like(g[::7]) * (top / 16)
+        out = torch.empty(shape, device="cuda", dtype=torch.bfloat16)
+        asr.asr_newton_schulz([(g, out)], eps=1e-30)
+        got, want = out[::7], _exact(g, 1e-30)[::7]
+        assert _far(got, want) <= BOUND
