@@ -630,7 +630,10 @@ def _matrix_table(pairs):
         po, *shape, out_ld, out_stride = _strided_ptr(out, f"out[{i}]", (torch.bfloat16,), dev)
         if tuple(x.shape) != tuple(out.shape):
             raise ValueError(f"out[{i}] has shape {tuple(out.shape)}; x[{i}] has {tuple(x.shape)}")
-        if count > 1 and rows * cols and abs(out_stride) < (rows - 1) * out_ld + cols:
+        # one matrix after another, or one row of each after another
+        apart = out_stride >= (rows - 1) * out_ld + cols or (out_stride >= cols and
+                                                             out_ld >= (count - 1) * out_stride + cols)
+        if count > 1 and rows * cols and not apart:
             raise ValueError(f"out[{i}]'s matrices must not overlap")
         if stride < 0 or out_stride < 0:
             raise ValueError("negative strides are not supported")

@@ -79,3 +79,32 @@ def test_small_entries_beside_large_ones(asr, shape):
         asr.asr_newton_schulz([(g, out)], eps=1e-30)
         got, want = out[::7], _exact(g, 1e-30)[::7]
         assert _far(got, want) <= BOUND
+
+
+@pytest.mark.parametrize("shape", [(60, 96), (1, 96), (96, 1), (200, 150)])
+def test_stacks_whose_rows_alternate(asr, shape):
+    """A stack along the middle of a tensor (the heads of a projection), as input
+    and as output: what each matrix gives on its own."""
+    import torch
+    torch.manual_seed(10)
+    rows, cols = shape
+    g = torch.randn(rows, 5, cols, device="cuda").bfloat16().transpose(0, 1)
+    buf = torch.full((rows, 7, cols), 9.0, device="cuda", dtype=torch.bfloat16)
+    out = buf[:, 1:6].transpose(0, 1)
+    asr.asr_newton_schulz([(g, out)])
+    for z in range(5):
+        alone = torch.empty(rows, cols, device="cuda", dtype=torch.bfloat16)
+        asr.asr_newton_schulz([(g[z].contiguous(), alone)])
+        assert torch.equal(out[z], alone)
+    assert (buf[:, 0] == 9).all() and (buf[:, 6] == 9).all()
+
+
+def test_overlapping_outputs_are_refused(asr):
+    import torch
+    g = torch.randn(3, 4, 8, device="cuda")
+    buf = torch.empty(200, device="cuda", dtype=torch.bfloat16)
+    for strides in ((31, 8, 1), (0, 8, 1), (7, 24, 1), (8, 23, 1), (8, 8, 1)):
+        with pytest.raises(ValueError, match="overlap"):
+            asr.asr_newton_schulz([(g, buf.as_strided((3, 4, 8), strides))])
+    for strides in ((32, 8, 1), (8, 24, 1), (40, 9, 1), (9, 30, 1)):
+        asr.asr_newton_schulz([(g, buf.as_strided((3, 4, 8), strides))])
