@@ -63,11 +63,22 @@ class MuonSR(_PlacedOptimizer):
                         ns_coefficients=tuple(ns_coefficients), eps=eps, ns_steps=ns_steps,
                         adjust_lr_fn=adjust_lr_fn or "original", seed=int(seed), rounding=rounding, base_index=None)
         super().__init__(params, defaults)
-        for group in self.param_groups:
-            for p in group["params"]:
-                if p.dim() not in (2, 3):
-                    raise ValueError(f"MuonSR takes matrices (2-D) and stacks of them (3-D), not {p.dim()}-D parameters")
         self._assign_positions()
+
+    def add_param_group(self, param_group):
+        super().add_param_group(param_group)
+        for p in self.param_groups[-1]["params"]:
+            if p.dim() not in (2, 3):
+                self.param_groups.pop()
+                if hasattr(self, "_base"):
+                    self._assign_positions()
+                raise ValueError(f"MuonSR takes matrices (2-D) and stacks of them (3-D), not {p.dim()}-D parameters")
+
+    @staticmethod
+    def _settings(group):
+        return dict(lr=group["lr"], momentum=group["momentum"], weight_decay=group["weight_decay"],
+                    nesterov=group["nesterov"], steps=group["ns_steps"], coefficients=group["ns_coefficients"],
+                    eps=group["eps"], adjust=group["adjust_lr_fn"], seed=group["seed"], rounding=group["rounding"])
 
     @staticmethod
     def _check(p: torch.Tensor):
@@ -96,11 +107,14 @@ class MuonSR(_PlacedOptimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
-        # every parameter is checked before anything is launched or counted
+        # every parameter, and every group's settings (by a step over no matrices), are
+        # checked before anything is launched or counted
         for group in self.param_groups:
-            for p in group["params"]:
-                if p.grad is not None:
-                    self._check(p)
+            live = [p for p in group["params"] if p.grad is not None]
+            for p in live:
+                self._check(p)
+            if live:
+                _lib.asr_muon_sr_multi_tensor([], step=1, **self._settings(group))
         devices = set()
         for group in self.param_groups:
             batches: Dict[tuple, List[tuple]] = {}
@@ -116,11 +130,7 @@ class MuonSR(_PlacedOptimizer):
                 batches.setdefault((p.device, state["step"]), []).append(
                     (p, p.grad, state["momentum_buffer"], self._base[id(p)]))
             for (device, step), entries in batches.items():
-                _lib.asr_muon_sr_multi_tensor(
-                    entries, lr=group["lr"], momentum=group["momentum"], weight_decay=group["weight_decay"],
-                    nesterov=group["nesterov"], steps=group["ns_steps"], coefficients=group["ns_coefficients"],
-                    eps=group["eps"], adjust=group["adjust_lr_fn"], step=step, seed=group["seed"],
-                    rounding=group["rounding"])
+                _lib.asr_muon_sr_multi_tensor(entries, step=step, **self._settings(group))
                 devices.add(device)
         self._finish_step(devices, mode)
         return loss
