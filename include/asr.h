@@ -349,9 +349,9 @@ asr_status asr_muon_workspace(const asr_muon_desc *table, int32_t n, uint64_t *b
  *   q = floor(y) + (65536 (y - floor(y)) > r)          ASR_ROUND_SR
  * in binary32 (rows with top < 2^-64 are raised by 2^64 first), |q| <= 127;
  * r is the low 16 bits of the Philox word of global index base_index +
- * i * cols + j at (seed, step).  A row of zeros gives scale 0 and zeros; one
- * that holds an infinity or a NaN gives zeros and a scale that is not finite,
- * so that its products are NaN.
+ * i * cols + j at (seed, step).  A row of zeros, or of no elements, gives
+ * scale 0 and zeros; one that holds an infinity or a NaN gives zeros and a
+ * scale that is not finite, so that its products are NaN.
  * ASR_ROWS: q is rows x cols, q_ld >= cols bytes between rows, scale has `rows`
  * entries.  ASR_COLUMNS (rows at most 4,194,240): q is stored transposed, cols x rows, q_ld >= rows, and
  * scale has `cols` entries.  Bytes between a row's end and the next row are

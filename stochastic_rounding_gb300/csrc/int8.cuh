@@ -583,7 +583,16 @@ asr_status quantize(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, 
     if (dtype != ASR_F32 && dtype != ASR_BF16) return ASR_ERR_UNSUPPORTED_DTYPE;
     if (rounding != ASR_ROUND_SR && rounding != ASR_ROUND_RNE) return ASR_ERR_UNSUPPORTED_DTYPE;
     if (axis != ASR_ROWS && axis != ASR_COLUMNS) return ASR_ERR_INVALID_VALUE;
-    if (rows == 0 || cols == 0) return ASR_OK;
+    const uint64_t scales = axis == ASR_ROWS ? rows : cols;
+    if (scales == 0) return ASR_OK;
+    if (rows == 0 || cols == 0) {                   // rows of no elements: scales of zero
+        if (!scale || !muon::element_aligned(scale, ASR_F32) || scales > (1u << 30)) return ASR_ERR_INVALID_VALUE;
+        const asr_status st = setup();
+        if (st != ASR_OK) return st;
+        zero_kernel<<<static_cast<unsigned>((scales + kThreads - 1) / kThreads), kThreads, 0, stream>>>(
+            reinterpret_cast<uint32_t *>(scale), scales);
+        return launched(ASR_KERNEL_QUANTIZE);
+    }
     if (!x || !q || !scale || !muon::element_aligned(x, dtype) || !muon::element_aligned(scale, ASR_F32))
         return ASR_ERR_INVALID_VALUE;
     if (!quantisable(rows, cols) || !pitch_ok(x_ld, cols) || !pitch_ok(q_ld, axis == ASR_ROWS ? cols : rows) ||

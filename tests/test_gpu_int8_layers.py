@@ -141,3 +141,16 @@ def test_gradients_of_long_sums(asr, size, dtype):
         b, sb = _quantised(asr, x, axis="columns")
         assert_same_bits(host(dw), host(_want_product(a, b, sa, sb).bfloat16()))
         assert not constant or (a == 127).all() and (b == 127).all()
+
+
+@pytest.mark.parametrize("axis", ["rows", "columns"])
+def test_quantise_rows_of_no_elements(asr, axis):
+    """Their scales are those of zeros, not what the memory held."""
+    import torch
+    x = torch.empty((300, 0) if axis == "rows" else (0, 300), device="cuda")
+    scale = torch.full((300,), 3.0, device="cuda")
+    asr.asr_quantize_int8(x, asr.int8_empty(300, 0), scale, axis=axis)
+    assert (scale == 0).all()
+    none = torch.empty((0, 5) if axis == "rows" else (5, 0), device="cuda")
+    asr.asr_quantize_int8(none, asr.int8_empty(0, 5), scale[:0], axis=axis)
+    assert (scale == 0).all()
