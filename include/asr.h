@@ -347,9 +347,11 @@ asr_status asr_muon_workspace(const asr_muon_desc *table, int32_t n, uint64_t *b
  * between rows: top = max |x|, scale = top / 127, y = x (127 / top), and
  *   q = rint(y)                                        ASR_ROUND_RNE
  *   q = floor(y) + (65536 (y - floor(y)) > r)          ASR_ROUND_SR
- * in binary32 (rows with top < 2^-64 are raised by 2^64 first), |q| <= 127;
- * r is the low 16 bits of the Philox word of global index base_index +
- * i * cols + j at (seed, step).  A row of zeros, or of no elements, gives
+ * with top, scale and y in binary32 (rows with top < 2^-64 are raised by 2^64
+ * first), the comparison exact, |q| <= 127; r is the low 16 bits of the Philox word of global index base_index +
+ * i * cols + j at (seed, step).  Of the 65,536 values of r, ceil(65536 (y -
+ * floor(y))) round up, so that a stochastic q is y on average to within 2^-16
+ * (above it, by half of that on average).  A row of zeros, or of no elements, gives
  * scale 0 and zeros; one that holds an infinity or a NaN gives zeros and a
  * scale that is not finite, so that its products are NaN.
  * ASR_ROWS: q is rows x cols, q_ld >= cols bytes between rows, scale has `rows`

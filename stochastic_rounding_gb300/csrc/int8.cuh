@@ -8,8 +8,8 @@
 //   C_ij    = (sum_k a_ik b_jk) * sa_i * sb_j
 //
 // r_ij: the low 16 bits of the Philox word of x_ij's index, i * cols + j from
-// the call's base index, whichever way the matrix is stored.  The sum of
-// integers is exact.  sm_103a's tensor memory instructions have no 8-bit
+// the call's base index, whichever way the matrix is stored; y in binary32, the
+// comparison exact.  The sum of integers is exact.  sm_103a's tensor memory instructions have no 8-bit
 // integer kind; an 8-bit integer is exact in f16, a product of two in binary32,
 // and so is any sum of 1,024 of them (1,024 * 128^2 = 2^24).  So the operands
 // are widened to f16 in the workspace, int8_product.cuh sums chunks of 1,024 in

@@ -5,7 +5,9 @@
     dw = dy^T x      dy's columns and x's columns
 
 The gradient operand is rounded stochastically, so that what it contributes is
-unbiased; the others to nearest.  Sums of integers are exact; outputs are bf16.
+right on average (to within 2^-16 of a step, from 16 random bits); the others to
+nearest.  Sums of integers are exact.  Outputs and gradients are bf16, whatever
+the inputs' types: the operands hold 8 bits, and what those lose is larger.
 The weight itself stays bf16 (or float32) and is what an optimizer of this
 package updates.
 """

@@ -154,3 +154,26 @@ def test_quantise_rows_of_no_elements(asr, axis):
     none = torch.empty((0, 5) if axis == "rows" else (5, 0), device="cuda")
     asr.asr_quantize_int8(none, asr.int8_empty(0, 5), scale[:0], axis=axis)
     assert (scale == 0).all()
+
+
+@pytest.mark.parametrize("axis", ["rows", "columns"])
+def test_stochastic_comparison_is_exact(asr, orc, axis):
+    """Fractions just above a random number, of values below zero: y - floor(y)
+    rounded to binary32 would come out equal to it, and the integer one too low."""
+    import torch
+    rows, cols, step, seed = 64, 512, 3, 21
+    words = (orc.philox_fill(rows * cols // 4, 0, step, 0, seed).reshape(rows, cols) & 0xFFFF).astype(np.float64)
+    near = words >= 49152                                   # 24 bits hold 65536 - r - 2^-10
+    rng = np.random.default_rng(0)
+    x = np.where(near, -(65536 - words - 2.0 ** -10) / 65536, rng.normal(size=words.shape).astype(np.float32))
+    line = (slice(None), 0) if axis == "rows" else (0, slice(None))
+    x[line], near[line] = 127.0, False                      # scale 1, so that y = x
+    x = x.astype(np.float32)
+    y = x.astype(np.float64)
+    low = np.floor(y)
+    want = low + (65536 * (y - low) > words)
+    rounded = np.floor(x) + ((x - np.floor(x)) * np.float32(65536) > words.astype(np.float32))
+    assert near.sum() > 5000 and (want[near] == 0).all() and (rounded[near] == -1).all()
+    q, scale = _quantised(asr, torch.from_numpy(x).cuda(), axis, rounding="sr", step=step, seed=seed)
+    assert (scale == 1).all()
+    assert np.array_equal(q.cpu().numpy() if axis == "rows" else q.t().cpu().numpy(), want.astype(np.int8))
