@@ -177,3 +177,80 @@ def test_stochastic_comparison_is_exact(asr, orc, axis):
     q, scale = _quantised(asr, torch.from_numpy(x).cuda(), axis, rounding="sr", step=step, seed=seed)
     assert (scale == 1).all()
     assert np.array_equal(q.cpu().numpy() if axis == "rows" else q.t().cpu().numpy(), want.astype(np.int8))
+
+
+# Tiles of 256 x 256 on 76 pairs of SMs, whole rounds of them and what is left: 0 and
+# 50 (whole tiles), 1 and 14 (in quarters), 1 and 24 (in halves), 2 and 68, 4 and 37.
+@pytest.mark.parametrize("size", [(1277, 2500, 1100), (2300, 2560, 130), (2300, 2700, 2049), (2309, 5500, 1025),
+                                  (2600, 7800, 515)])
+def test_products_of_several_rounds_of_tiles(asr, orc, size):
+    import torch
+    m, n, k = size
+    g = torch.Generator(device="cuda").manual_seed(m)
+    a, b = asr.int8_empty(m, k), asr.int8_empty(n, k)
+    for v in (a, b):
+        v.copy_(torch.randint(-128, 128, v.shape, device="cuda", generator=g, dtype=torch.int8))
+    sa, sb = (torch.rand(s, device="cuda", generator=g) + 0.5 for s in (m, n))
+    want = _want_product(a, b, sa, sb)
+    c = torch.empty(m, n, device="cuda")
+    asr.asr_gemm_int8_sr(a, b, sa, sb, c)
+    assert_same_bits(host(c), host(want))
+    pitched = torch.full((m, n + 3), 7.0, device="cuda", dtype=torch.bfloat16)
+    asr.asr_gemm_int8_sr(a, b, sa, sb, pitched[:, :n], rounding="sr", step=3, seed=8)
+    assert_same_bits(host(pitched[:, :n].contiguous()).reshape(-1), orc.sr_fill(host(want).reshape(-1), 0, 3, 8))
+    assert (pitched[:, n:] == 7.0).all()
+
+
+# Weights of more rows than the tests of single products have: dot products of one CTA a
+# row block, stretches of pieces over several row blocks, passes over the weight.
+@pytest.mark.parametrize("size", [(1, 14336, 4096), (3, 20001, 1030), (4, 9700, 2050), (7, 30000, 515), (33, 14336, 4096),
+                                  (128, 9001, 4096), (200, 5000, 8192), (16, 40003, 130)])
+def test_few_rows_with_large_weights(asr, size):
+    import torch
+    m, n, k = size
+    torch.manual_seed(n)
+    x = torch.randn(m, k, device="cuda").bfloat16()
+    (a, sa), (b, sb) = _quantised(asr, x), _quantised(asr, torch.randn(n, k, device="cuda"))
+    want = _want_product(a, b, sa, sb)
+    c, y = torch.empty(m, n, device="cuda"), torch.empty(m, n, device="cuda")
+    asr.asr_gemm_int8_sr(a, b, sa, sb, c)
+    assert_same_bits(host(c), host(want))
+    asr.int8_linear(x, b, sb, out=y)
+    assert_same_bits(host(y), host(want))
+
+
+# The same of two products in a launch, either first; 1, 2, 4, 8, 16 and 32 rows a warp of
+# the quantiser, the last of them part empty.
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("size", [(517, 901, 515), (701, 1301, 901), (1285, 2563, 1285), (2051, 1031, 2053),
+                                  (2051, 4104, 2064), (2051, 4102, 2060), (4102, 2051, 2064), (8201, 1030, 1029), (4101, 8203, 2056)])
+def test_gradients_of_several_rounds_of_tiles(asr, size, dtype):
+    import torch
+    t, n, k = size
+    torch.manual_seed(t)
+    dy, x, w = (torch.randn(*s, device="cuda").to(getattr(torch, dtype)) for s in ((t, n), (t, k), (n, k)))
+    dx, dw = asr.int8_linear_grads(dy, x, w, step=4, seed=6)
+    sr = dict(rounding="sr", step=4, seed=6)
+    (a, sa), (b, sb) = _quantised(asr, dy, **sr), _quantised(asr, w, "columns")
+    assert_same_bits(host(dx), host(_want_product(a, b, sa, sb).bfloat16()))
+    (a, sa), (b, sb) = _quantised(asr, dy, "columns", **sr), _quantised(asr, x, "columns")
+    assert_same_bits(host(dw), host(_want_product(a, b, sa, sb).bfloat16()))
+    assert torch.equal(asr.int8_linear_grads(dy, x, w, step=4, seed=6, need_dw=False)[0], dx)
+    assert torch.equal(asr.int8_linear_grads(dy, x, w, step=4, seed=6, need_dx=False)[1], dw)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("size", [(1, 300, 515), (40, 64, 1000), (200, 130, 77), (513, 1001, 257), (1285, 515, 1365)])
+def test_both_gradients_of_strided_operands(asr, dtype, size):
+    """Views at odd starts and pitches: each gradient from the quantiser's integers."""
+    import torch
+    torch.manual_seed(size[1])
+    t, n, k = size
+    mk = lambda r, c: torch.randn(r + 1, c + 5, device="cuda").to(getattr(torch, dtype))[1:, 2:c + 2]  # noqa: E731
+    x, w, dy = mk(t, k), mk(n, k), mk(t, n)
+    dx, dw = asr.int8_linear_grads(dy, x, w, step=1, seed=2)
+    sr = dict(rounding="sr", step=1, seed=2)
+    (a, sa), (b, sb) = _quantised(asr, dy, **sr), _quantised(asr, w, "columns")
+    assert_same_bits(host(dx), host(_want_product(a, b, sa, sb).bfloat16()))
+    (a, sa), (b, sb) = _quantised(asr, dy, "columns", **sr), _quantised(asr, x, "columns")
+    assert_same_bits(host(dw), host(_want_product(a, b, sa, sb).bfloat16()))

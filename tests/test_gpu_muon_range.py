@@ -108,3 +108,61 @@ def test_overlapping_outputs_are_refused(asr):
             asr.asr_newton_schulz([(g, buf.as_strided((3, 4, 8), strides))])
     for strides in ((32, 8, 1), (8, 24, 1), (40, 9, 1), (9, 30, 1)):
         asr.asr_newton_schulz([(g, buf.as_strided((3, 4, 8), strides))])
+
+
+# Stacks whose products take more tiles (of 256 x 256, on 76 pairs of SMs) than half the
+# pairs, and several rounds of them.  Of S and P, and of X', whole rounds and what is
+# left: 1 + 24 and 2 + 48; 0 + 54 and 2 + 10; 0 + 48 and 1 + 20; 0 + 45 and 1 + 23.
+STACKS = [(10, 1024, 1100), (10, 1100, 1024), (9, 600, 1300), (9, 1300, 600), (16, 500, 700), (16, 700, 500),
+          (1, 2300, 2600), (1, 2600, 2300)]
+
+
+@pytest.mark.parametrize("shape", STACKS)
+def test_products_of_several_rounds_of_tiles(asr, shape):
+    import torch
+    torch.manual_seed(shape[1])
+    g = (torch.randn(shape, device="cuda") * 1e-3).bfloat16()
+    want = [_exact(v) for v in g]
+    out = torch.full(shape, 9.0, device="cuda", dtype=torch.bfloat16)
+    asr.asr_newton_schulz([(g, out)])
+    for got, w in zip(out, want):
+        assert _far(got, w) <= BOUND
+    # the same rounded from parameters of zero: f32, and bf16 by its random bits
+    kw = dict(lr=1.0, momentum=0.5, weight_decay=0.0, nesterov=False, adjust=None, step=3, seed=5)
+    p, m = torch.zeros(shape, device="cuda"), torch.zeros(shape, device="cuda")
+    asr.asr_muon_sr_multi_tensor([(p, g, m, 8)], **kw)
+    for got, w in zip(p, want):
+        assert _far(-got, w) <= BOUND
+    pb, m = torch.zeros(shape, device="cuda", dtype=torch.bfloat16), torch.zeros(shape, device="cuda")
+    asr.asr_muon_sr_multi_tensor([(pb, g, m, 8)], **kw)
+    rounded = torch.empty_like(pb)
+    asr.asr_stochastic_round_bf16(p, rounded, base_index=8, step=3, seed=5)
+    assert torch.equal(pb, rounded)
+
+
+@pytest.mark.parametrize("shape", [(5, 700, 1001), (5, 1001, 700)])
+def test_parameters_off_every_alignment(asr, shape):
+    """Rows of odd length, bf16 parameters and gradients that start at odd
+    elements, with decay and momentum from before."""
+    import torch
+    torch.manual_seed(11)
+    size = shape[0] * shape[1] * shape[2]
+    base = torch.randn(size, device="cuda") * 0.02
+    g = torch.randn(size + 3, device="cuda").bfloat16()[3:].view(shape)
+    m = torch.randn(size + 1, device="cuda")[1:].view(shape)
+    kw = dict(lr=0.1, momentum=0.9, weight_decay=0.3, adjust="match_rms_adamw", step=2, seed=9)
+    pb = torch.empty(size + 1, device="cuda", dtype=torch.bfloat16)[1:].view(shape)
+    pb.copy_(base.view(shape))
+    pf, m2 = pb.float(), m.clone()
+    before = pf.double()
+    asr.asr_muon_sr_multi_tensor([(pb, g, m, 7)], **kw)
+    asr.asr_muon_sr_multi_tensor([(pf, g, m2, 7)], **kw)
+    assert torch.equal(m, m2)
+    rounded = torch.empty(shape, device="cuda", dtype=torch.bfloat16)
+    asr.asr_stochastic_round_bf16(pf, rounded, base_index=7, step=2, seed=9)
+    assert torch.equal(pb, rounded)
+    u = g.float() + 0.9 * (m2 - g.float())
+    for z in range(shape[0]):
+        step = 0.1 * 0.2 * max(shape[1:]) ** 0.5 * _exact(u[z])
+        err = pf[z].double() - (before[z] * (1 - 0.1 * 0.3) - step)
+        assert float(err.norm()) <= BOUND * float(step.norm()) + 3 * 2.0 ** -24 * float(before[z].norm())
