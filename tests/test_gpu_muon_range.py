@@ -166,3 +166,30 @@ def test_parameters_off_every_alignment(asr, shape):
         step = 0.1 * 0.2 * max(shape[1:]) ** 0.5 * _exact(u[z])
         err = pf[z].double() - (before[z] * (1 - 0.1 * 0.3) - step)
         assert float(err.norm()) <= BOUND * float(step.norm()) + 3 * 2.0 ** -24 * float(before[z].norm())
+
+
+@pytest.mark.parametrize("small", [1e-2, 1e-3, 1e-4])
+@pytest.mark.parametrize("shape", [(96, 160), (256, 256), (512, 2048), (300, 200)])
+def test_small_directions_beside_eight_large_ones(asr, shape, small):
+    """Rounding X_0 and X' to f16 puts errors of entries' size 2^-11 / sqrt(12)
+    at most into every direction, as a random matrix whose largest singular
+    value is that times (sqrt m + sqrt n) / sqrt(m n), and the iteration raises
+    the small directions, true or not, by at most a^5 = 485: four such sizes and the
+    bf16 rounding of the result, as in the test of a matrix of rank 3.  The small
+    directions, raised to 485 times their share, are there to the same bound each."""
+    import torch
+    torch.manual_seed(12)
+    m, n = shape
+    r = min(shape)
+    u = torch.linalg.qr(torch.randn(m, r, device="cuda", dtype=torch.float64))[0]
+    v = torch.linalg.qr(torch.randn(n, r, device="cuda", dtype=torch.float64))[0]
+    s = torch.full((r,), small, device="cuda", dtype=torch.float64)
+    s[:8] = 1.0
+    g = ((u * s) @ v.t()).float()
+    out = torch.empty(shape, device="cuda", dtype=torch.bfloat16)
+    asr.asr_newton_schulz([(g, out)])
+    want = _exact(g)
+    bound = 4 * 485 * 2.0 ** -11 / 12 ** 0.5 * (m ** 0.5 + n ** 0.5) / (m * n) ** 0.5 + 2.0 ** -8
+    assert float(torch.linalg.matrix_norm(out.double() - want, 2)) <= bound
+    got, there = ((u.t() @ o @ v).diagonal()[8:] for o in (out.double(), want))
+    assert float((got - there).abs().max()) <= bound
