@@ -27,6 +27,16 @@
 // iteration needs: it raises small singular values by a^steps (485 for the
 // usual coefficients), and the rounding of X's entries with them.  Sums, norms
 // and momentum are binary32 or wider.
+//
+// Diagonals.  Where singular values bunch (a short and wide matrix), S and P are
+// nearly multiples of I, and the rounding of their diagonals is the same for
+// all rows: not noise but a factor, up to 2^-11 a step and matrix.  So S's
+// diagonal is kept in binary32 as well and P's made from it, and each row of P X is
+// multiplied by P's diagonal over its rounded value (the rest of the row takes
+// the same factor, within its own rounding).  Error of the bf16 result against
+// 64 bits, without and with: 137 x 7,674 0.0028 and 0.0018, 16 x 300 0.0027 and
+// 0.0022, 512 x 2,048 0.0019 and 0.0018; of the exact result rounded to bf16
+// 0.0017.  It costs 1.5 us of 27 for 96 x 160 and nothing that shows above that.
 
 namespace muon {
 
@@ -297,7 +307,7 @@ struct Group {                              // a launch's stack: up to kMaxBatch
 };
 
 struct Layout {                             // a group's part of the workspace
-    uint64_t partial, x0, x1, s, p, bytes;
+    uint64_t partial, diag, gain, x0, x1, s, p, bytes;
     uint64_t ldx, lds, m;
 };
 
@@ -313,7 +323,9 @@ Layout layout(uint64_t rows, uint64_t cols, uint64_t batch)
     L.lds = up(L.m, 16);
     const uint64_t x = up(rows * L.ldx * 2, 256) * batch, s = up(L.m * L.lds * 2, 256) * batch;
     L.partial = 0;
-    L.x0 = up(batch * kPartBlocks * sizeof(float2), 256);
+    L.diag = up(batch * kPartBlocks * sizeof(float2), 256);
+    L.gain = L.diag + up(batch * L.lds * sizeof(float), 256);
+    L.x0 = L.gain + up(batch * L.lds * sizeof(float), 256);
     L.x1 = L.x0 + x;
     L.s = L.x1 + x;
     L.p = L.s + s;
@@ -457,12 +469,15 @@ asr_status iterate(const Group &G, const NsParams &ns, const Layout &L, char *ws
         P.ld = static_cast<uint32_t>(S.ld);
         P.stride = S.stride;
         P.out = S.ptr;
+        P.diag = reinterpret_cast<float *>(ws + L.diag);
+        P.gain = reinterpret_cast<float *>(ws + L.gain);
+        P.side = static_cast<uint32_t>(L.lds);
         st = tall ? prod::launch<true, true, prod::kGram>(x, x, P, stream)
                   : prod::launch<false, false, prod::kGram>(x, x, P, stream);
         if (st != ASR_OK) break;
         P.alpha = static_cast<float>(ns.c) * down;
         P.beta = static_cast<float>(ns.b);
-        P.diag = static_cast<float>(ns.a) * kStore;
+        P.shift = static_cast<float>(ns.a) * kStore;
         P.aux = S.ptr;
         P.out = Q.ptr;
         st = prod::launch<false, false, prod::kPoly>(S, S, P, stream);

@@ -55,6 +55,7 @@ constexpr int kStages = 3;
 constexpr int kEpi = 16;                        // epilogue warps: four per TMEM lane quarter
 constexpr int kThreads = 64 + 32 * kEpi;
 constexpr int kSpan = kTile / (kEpi / 4);       // columns per epilogue warp
+static_assert(kSpan == 64, "two words a lane hold a warp's column gains");
 constexpr uint32_t kHalfBytes = 128 * 64 * 2;   // a K-half of one operand in one CTA
 constexpr uint32_t kStageBytes = 4 * kHalfBytes;
 constexpr int kAccBufs = 2;
@@ -69,11 +70,11 @@ constexpr int kGroupM = 16;                     // tile order: rows of tiles wal
 constexpr int kMaxBatch = 64;                   // matrices per launch
 
 // What the epilogue makes of a sum.  "Stored" values are f16 at 2^12 times the
-// matrix (see muon.cuh).
+// matrix, S and P with their diagonals' rounding kept besides (see muon.cuh).
 enum Op {
-    kGram,      // stored S = alpha * sum, symmetric
-    kPoly,      // stored P = alpha * sum + beta * (stored S) + diag on the diagonal, symmetric
-    kNext,      // stored X' = alpha * sum
+    kGram,      // stored S = alpha * sum, symmetric; its diagonal
+    kPoly,      // stored P = alpha * sum + beta * (stored S) + shift on the diagonal, symmetric; its rows' gains
+    kNext,      // stored X' = alpha * gain * sum
     kOut,       // caller's bf16 matrix = alpha * sum, to nearest
     kParam,     // caller's parameter p = p * beta - alpha * sum, f32 or rounded to bf16
     kScaled     // caller's matrix = sum * row scale * column scale (int8_product.cuh)
@@ -89,11 +90,13 @@ struct Params {
     uint32_t tiles_m, tiles_n, per_matrix;
     uint32_t wide, narrow;          // work items: whole tiles, then parts of the last ones
     uint32_t parts;                 // 1, 2 or 4: a narrow item is 256 / parts columns
-    float alpha, beta, diag;
+    float alpha, beta, shift;
     uint32_t ld;                    // stored output (and S): elements between rows
     uint64_t stride;                // and between matrices
     __half *out;
     const __half *aux;
+    float *diag, *gain;             // of S, before its rounding; of P's rows.  `side` between matrices
+    uint32_t side;
     // the caller's output
     uint64_t out_ld;
     uint32_t out_dtype;             // asr_dtype
@@ -207,16 +210,47 @@ __device__ __forceinline__ void ld_global_v8(const void *p, uint32_t w[8])
                  : "memory");
 }
 
+// An element of P's diagonal from S's before its rounding to s: what the rounding
+// took away enters b S whole and c S S to first order.
+__device__ __forceinline__ float with_diagonal(float x, float s, float diagonal, float alpha, float beta)
+{
+    return fmaf(diagonal - s, fmaf(2.0f * alpha, s, beta), x);
+}
+
+// What P's row is multiplied with after its product, so that its rounded diagonal
+// counts as x.  (Below 1, 2^-12 of P, f16 is not exact to 2^-11.)
+__device__ __forceinline__ float gain_of(float x)
+{
+    const float h = __half2float(__float2half_rn(x));
+    return fabsf(h) >= 1.0f ? 1.0f + __fdividef(x - h, h) : 1.0f;
+}
+
+// Element i of sixteen, without an address.
+__device__ __forceinline__ float pick(const float x[16], uint32_t i)
+{
+    float v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = i & 8u ? x[q + 8] : x[q];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = i & 4u ? v[q + 4] : v[q];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) v[q] = i & 2u ? v[q + 2] : v[q];
+    return i & 1u ? v[1] : v[0];
+}
+
 // 16 sums of this lane's row `row`, columns col .. col+15, to a stored matrix.
 // Rows past m are not written; columns are, up to the row's padding (their
-// sums are zero: operands read as zeros there).  `prior`: the stored S there
-// (kPoly).  Where the tile has a mirror image, the block goes out a second time,
+// sums are zero: operands read as zeros there).  `prior`: the stored S there,
+// `diagonal`: its diagonal in this row (kPoly).  Where the tile has a mirror image, the block goes out a second time,
 // turned in the warp's staging area: lane l takes rows 16 (l / 16) on of column l % 16.
 template <int OP>
 __device__ __forceinline__ void store_stored(const Params &P, const Item &it, uint32_t row, uint32_t col,
-                                             const uint32_t v[16], const uint32_t prior[8], float *stage, int lane)
+                                             const uint32_t v[16], const uint32_t prior[8], float diagonal,
+                                             float *stage, int lane)
 {
     __half *mat = P.out + it.z * P.stride;
+    const uint32_t d = row - col;
+    const bool crosses = d < 16u && row < P.m;          // the diagonal passes through
     float x[16];
     if constexpr (OP == kPoly) {
 #pragma unroll
@@ -225,15 +259,19 @@ __device__ __forceinline__ void store_stored(const Params &P, const Item &it, ui
             x[2 * q] = fmaf(P.alpha, __uint_as_float(v[2 * q]), P.beta * s.x);
             x[2 * q + 1] = fmaf(P.alpha, __uint_as_float(v[2 * q + 1]), P.beta * s.y);
         }
-        if (!it.mirror) {
-            const uint32_t d = row - col;
+        if (crosses) {
+            float t[16];
 #pragma unroll
-            for (int q = 0; q < 16; ++q)
-                if (d == static_cast<uint32_t>(q)) x[q] += P.diag;
+            for (int q = 0; q < 8; ++q) t[2 * q] = unpack_f16(prior[q]).x, t[2 * q + 1] = unpack_f16(prior[q]).y;
+            const float y = with_diagonal(pick(x, d) + P.shift, pick(t, d), diagonal, P.alpha, P.beta);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) x[q] = d == static_cast<uint32_t>(q) ? y : x[q];
+            P.gain[it.z * P.side + row] = gain_of(y);
         }
     } else {
 #pragma unroll
         for (int q = 0; q < 16; ++q) x[q] = P.alpha * __uint_as_float(v[q]);
+        if (OP == kGram && crosses) P.diag[it.z * P.side + row] = pick(x, d);
     }
     if (row < P.m) {
         uint32_t w[8];
@@ -557,15 +595,27 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             const uint32_t span = it.width / (kEpi / 4), c_lo = group * span;      // this warp's columns
             const uint32_t c_hi = ncols < c_lo + span ? ncols : c_lo + span;
             constexpr bool kStored = OP == kGram || OP == kPoly || OP == kNext;
+            constexpr bool kGains = OP == kNext || OP == kOut || OP == kParam;
             const bool rows_in = row - lane < P.m;          // the same for the whole warp
             const uint32_t col0 = it.n0 + c_lo, cols = c_hi > c_lo && rows_in ? c_hi - c_lo : 0;
             uint32_t prior[OP == kPoly ? kSpan / 2 : 1];
+            float diagonal = 0.0f, gain[kSpan / 32];
             // what the epilogue reads from memory, before it waits for the sums
             if constexpr (OP == kPoly) {
 #pragma unroll
                 for (int c = 0; c < kSpan; c += kBlock)
                     if (static_cast<uint32_t>(c) < cols && row < P.m)
                         ld_global_v8(P.aux + it.z * P.stride + static_cast<uint64_t>(row) * P.ld + col0 + c, prior + c / 2);
+                if (!it.mirror && row < P.m) diagonal = P.diag[it.z * P.side + row];
+            }
+            // P's rows' gains: it is operand A where B is stored across (its rows are the
+            // output's), else B (the output's columns)
+            if constexpr (kGains) {
+#pragma unroll
+                for (int h = 0; h < kSpan / 32; ++h) {
+                    if (B_MN) gain[h] = row < P.m ? P.gain[it.z * P.side + row] : 0.0f;
+                    else gain[h] = 32u * h + lane < cols ? P.gain[it.z * P.side + col0 + 32 * h + lane] : 0.0f;
+                }
             }
             uint32_t p[OP == kParam ? 16 : 1];
             if constexpr (OP == kParam)
@@ -587,8 +637,15 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     if (lane == 0) mbar_arrive_remote(peer_addr(acc_empty(b), 0));
                 }
                 if (!have) continue;
+                if constexpr (kGains) {
+                    const float g = c < 32 ? gain[0] : gain[1];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        v[q] = __float_as_uint(__uint_as_float(v[q]) *
+                                               (B_MN ? g : __shfl_sync(0xFFFFFFFFu, g, (c & 31) + q)));
+                }
                 if constexpr (kStored) {
-                    store_stored<OP>(P, it, row, col0 + c, v, prior + (OP == kPoly ? c / 2 : 0), stage, lane);
+                    store_stored<OP>(P, it, row, col0 + c, v, prior + (OP == kPoly ? c / 2 : 0), diagonal, stage, lane);
                 } else {
                     float x[16];
 #pragma unroll

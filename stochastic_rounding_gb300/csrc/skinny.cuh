@@ -15,7 +15,7 @@
 //   - X' = P X over X.
 // Number format, formulas and order of the epilogue's operations are those of
 // the products in memory (muon.cuh).  Those take three launches a step of 4.5 us
-// each however small the matrix is: 70 us for 96 x 160, against 27 us here (both
+// each however small the matrix is: 70 us for 96 x 160, against 28 us here (both
 // with the host's part).
 // What bounds it is latency: a chain of MMA, tensor memory read and shared memory
 // write three times a step.
@@ -68,6 +68,11 @@ __device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_
     asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
 __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile(
@@ -76,6 +81,14 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t adesc, uint64_t bde
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
         ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+__device__ __forceinline__ float pick_word(const uint32_t v[16], uint32_t i)
+{
+    float x[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) x[q] = __uint_as_float(v[q]);
+    return prod::pick(x, i);
 }
 
 // Descriptor of 64-column blocks read across (their rows are the contraction).
@@ -93,6 +106,7 @@ skinny_kernel(const __grid_constant__ SkinnyParams P, uint64_t limit_ns)
     __shared__ __align__(8) uint64_t bar_mem;
     __shared__ uint32_t tmem_slot;
     __shared__ Squares squares[8], total;
+    __shared__ float diagonal[kSkinnyRows], gain[kSkinnyRows];      // S's before its rounding; of P's rows
     const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
     unsigned char *xs = smem_raw + (base - raw), *ss = xs + kSkinnyX, *ps = ss + kSkinnyS;
     float *part = reinterpret_cast<float *>(ps);
@@ -241,6 +255,7 @@ skinny_kernel(const __grid_constant__ SkinnyParams P, uint64_t limit_ns)
                     w[q] = prod::pack_f16(kDown * __uint_as_float(v[2 * q]), kDown * __uint_as_float(v[2 * q + 1]));
                 *reinterpret_cast<uint4 *>(ss + tile_at(row, c)) = make_uint4(w[0], w[1], w[2], w[3]);
                 *reinterpret_cast<uint4 *>(ss + tile_at(row, c + 8)) = make_uint4(w[4], w[5], w[6], w[7]);
+                if (row - c < 16u) diagonal[row] = kDown * pick_word(v, row - c);
             } else {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -260,6 +275,10 @@ skinny_kernel(const __grid_constant__ SkinnyParams P, uint64_t limit_ns)
                 }
                 const uint32_t lo = prod::pack_f16(kDown * s.x, kDown * s.y), hi = prod::pack_f16(kDown * s.z, kDown * s.w);
                 for (uint32_t p = 0; p < ctas; ++p) st_cluster_v2(gemm::peer_addr(sa + tile_at(r, 4 * q), p), lo, hi);
+                if (r / 4 == q) {
+                    const float d = kDown * ((r & 3) == 0 ? s.x : (r & 3) == 1 ? s.y : (r & 3) == 2 ? s.z : s.w);
+                    for (uint32_t p = 0; p < ctas; ++p) st_cluster_f32(gemm::peer_addr(smem_addr(diagonal + r), p), d);
+                }
             }
             settle(true);
         } else {
@@ -277,6 +296,9 @@ skinny_kernel(const __grid_constant__ SkinnyParams P, uint64_t limit_ns)
             }
             __syncwarp();
         }
+        // P's diagonal but for c S S
+        const float t = __half2float(*reinterpret_cast<const __half *>(ss + tile_at(row, row)));
+        const float rest = prod::with_diagonal(fmaf(P.b, t, P.a * kStore), t, diagonal[row], P.c * kDown, P.b);
         done();
 #pragma unroll 1
         for (uint32_t c = half * 64; c < half * 64 + 64; c += 16) {
@@ -285,20 +307,23 @@ skinny_kernel(const __grid_constant__ SkinnyParams P, uint64_t limit_ns)
             const uint4 lo = *reinterpret_cast<const uint4 *>(ss + tile_at(row, c));
             const uint4 hi = *reinterpret_cast<const uint4 *>(ss + tile_at(row, c + 8));
             const uint32_t s[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-            const uint32_t d = row - c;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 const float2 t = prod::unpack_f16(s[q]);
-                float x = fmaf(P.c * kDown, __uint_as_float(v[2 * q]), P.b * t.x);
-                float y = fmaf(P.c * kDown, __uint_as_float(v[2 * q + 1]), P.b * t.y);
-                if (d == static_cast<uint32_t>(2 * q)) x += P.a * kStore;
-                if (d == static_cast<uint32_t>(2 * q + 1)) y += P.a * kStore;
+                const float x = fmaf(P.c * kDown, __uint_as_float(v[2 * q]), P.b * t.x);
+                const float y = fmaf(P.c * kDown, __uint_as_float(v[2 * q + 1]), P.b * t.y);
                 w[q] = prod::pack_f16(x, y);
             }
             *reinterpret_cast<uint4 *>(ps + tile_at(row, c)) = make_uint4(w[0], w[1], w[2], w[3]);
             *reinterpret_cast<uint4 *>(ps + tile_at(row, c + 8)) = make_uint4(w[4], w[5], w[6], w[7]);
+            if (row - c < 16u) {
+                const float x = fmaf(P.c * kDown, pick_word(v, row - c), rest);
+                *reinterpret_cast<__half *>(ps + tile_at(row, row)) = __float2half_rn(x);
+                gain[row] = prod::gain_of(x);
+            }
         }
         settle(false);
+        const float down = kDown * gain[row];
         // P X, 256 columns an instruction
         if (warp == 0) {
             if (prod::elect_one()) {
@@ -323,7 +348,7 @@ skinny_kernel(const __grid_constant__ SkinnyParams P, uint64_t limit_ns)
                 gemm::tmem_ld16(tq + c, v);
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
-                    w[q] = prod::pack_f16(kDown * __uint_as_float(v[2 * q]), kDown * __uint_as_float(v[2 * q + 1]));
+                    w[q] = prod::pack_f16(down * __uint_as_float(v[2 * q]), down * __uint_as_float(v[2 * q + 1]));
                 *reinterpret_cast<uint4 *>(xs + tile_at(row, c)) = make_uint4(w[0], w[1], w[2], w[3]);
                 *reinterpret_cast<uint4 *>(xs + tile_at(row, c + 8)) = make_uint4(w[4], w[5], w[6], w[7]);
             }
@@ -340,7 +365,7 @@ skinny_kernel(const __grid_constant__ SkinnyParams P, uint64_t limit_ns)
         float x[16];
         gemm::tmem_ld16(tq + c, v);
 #pragma unroll
-        for (int q = 0; q < 16; ++q) x[q] = __uint_as_float(v[q]);
+        for (int q = 0; q < 16; ++q) x[q] = __uint_as_float(v[q]) * gain[row];
         if (!P.tall) {
             if (row - lane < P.m) {
                 if (MUON) prod::load_params(P.out, P.out.slot[z].ptr, row, col0 + c, lane, p);

@@ -193,3 +193,30 @@ def test_small_directions_beside_eight_large_ones(asr, shape, small):
     assert float(torch.linalg.matrix_norm(out.double() - want, 2)) <= bound
     got, there = ((u.t() @ o @ v).diagonal()[8:] for o in (out.double(), want))
     assert float((got - there).abs().max()) <= bound
+
+
+@pytest.mark.parametrize("shape", [(1, 137, 7674), (2, 128, 4000), (4, 16, 300), (1, 196, 9939), (3, 2107, 8),
+                                   (2, 300, 16), (1, 7674, 137), (2, 30, 6000), (1, 96, 160), (2, 512, 2048)])
+def test_as_near_as_independent_roundings_leave_it(asr, shape):
+    """Gradients of noise and eight directions at two thirds of the norm.  A
+    rounding to f16 is off by at most 2^-11 of an entry, evenly spread: 2^-11 /
+    sqrt(3) of it in the mean square; sqrt(3) times that of what the eight
+    directions leave.  Fifteen of them (X, S and P of five steps), if they are
+    independent, leave sqrt(15) 2^-11; what is the same for a whole diagonal would
+    add up faster and is kept out.  The result's own rounding is that of the exact one."""
+    import torch
+    torch.manual_seed(13)
+    count, rows, cols = shape
+    rank = min(8, rows, cols)
+    g = torch.randn(shape, device="cuda")
+    g += 0.5 * torch.randn(count, rows, rank, device="cuda") @ torch.randn(count, rank, cols, device="cuda")
+    g *= 1e-3
+    out = torch.empty(shape, device="cuda", dtype=torch.bfloat16)
+    asr.asr_newton_schulz([(g, out)])
+    p, m = torch.zeros(shape, device="cuda"), torch.zeros(shape, device="cuda")
+    asr.asr_muon_sr_multi_tensor([(p, g, m, 0)], lr=1.0, momentum=0.5, weight_decay=0.0, nesterov=False, adjust=None,
+                                 step=1)
+    want = torch.stack([_exact(v) for v in g])
+    own = _far(want.bfloat16(), want)
+    assert _far(-p, want) <= 15 ** 0.5 * 2.0 ** -11
+    assert _far(out, want) <= (own ** 2 + 15 * 2.0 ** -22) ** 0.5
