@@ -606,7 +606,11 @@ def _workspace(workspace, need, device, stream):
         if size < need:
             raise ValueError(f"workspace has {size} bytes; the call needs {need}")
         return workspace, workspace.data_ptr(), size
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
+    raw = _stream_handle(device, stream).value
+    if isinstance(stream, torch.cuda.Stream):
+        s = stream
+    else:                                           # ExternalStream(0) would be one of torch's pool
+        s = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
     with torch.cuda.stream(s):
         buf = torch.empty(need, dtype=torch.uint8, device=device)
     return buf, buf.data_ptr(), need
