@@ -348,16 +348,17 @@ asr_status asr_muon_workspace(const asr_muon_desc *table, int32_t n, uint64_t *b
  *   q = rint(y)                                        ASR_ROUND_RNE
  *   q = floor(y) + (65536 (y - floor(y)) > r)          ASR_ROUND_SR
  * with top, scale and y in binary32 (rows with top < 2^-64 are raised by 2^64
- * first), the comparison exact, |q| <= 127; r is the low 16 bits of the Philox word of global index base_index +
- * i * cols + j at (seed, step).  Of the 65,536 values of r, ceil(65536 (y -
- * floor(y))) round up, so that a stochastic q is y on average to within 2^-16
- * (above it, by half of that on average).  A row of zeros, or of no elements, gives
- * scale 0 and zeros; one that holds an infinity or a NaN gives zeros and a
- * scale that is not finite, so that its products are NaN.
+ * first), the comparison exact, |q| <= 127; r is the low 16 bits of the
+ * Philox word of global index base_index + i * cols + j at (seed, step).  Of
+ * the 65,536 values of r, ceil(65536 (y - floor(y))) round up, so that a
+ * stochastic q is y on average to within 2^-16 (above it, by half of that on
+ * average).  A row of zeros, or of no elements, gives scale 0 and zeros; one
+ * that holds an infinity or a NaN gives zeros and a scale that is not finite,
+ * so that its products are NaN.
  * ASR_ROWS: q is rows x cols, q_ld >= cols bytes between rows, scale has `rows`
- * entries.  ASR_COLUMNS (rows at most 4,194,240): q is stored transposed, cols x rows, q_ld >= rows, and
- * scale has `cols` entries.  Bytes between a row's end and the next row are
- * not written. */
+ * entries.  ASR_COLUMNS (rows at most 4,194,240): q is stored transposed, cols
+ * x rows, q_ld >= rows, and scale has `cols` entries.  Bytes between a row's
+ * end and the next row are not written. */
 typedef enum { ASR_ROWS = 0, ASR_COLUMNS = 1 } asr_axis;
 
 asr_status asr_quantize_int8(const void *x, int32_t x_dtype, uint64_t rows, uint64_t cols, uint64_t x_ld,

@@ -8,16 +8,20 @@
 // meanwhile.  Sums of more than 131,071 products (gradients over as many tokens
 // or outputs), which int32 need not hold, are added up in int64 by a form of the
 // kernel of its own (LONG), whose running sums do not fit the registers (dw of
-// 1,024 x 2,048 over 131,071 tokens 962 us, over 131,072 974 us).  The two products of a backward pass (dx and dw) go as one list of
-// tiles, those of the longer sum first: in a launch each, both leave their last
-// round of tiles part empty, and small ones pay for two launches (4,096 tokens,
-// 8,192 x 2,048: the call 295 us with two, 273 with one; 1,111 tokens, 515 x 1,365:
-// 49.3 and 46.6).  How an operand is stored is a field of its product here, the
-// same for all lanes.
+// 1,024 x 2,048 over 131,071 tokens 962 us, over 131,072 974 us).
 //
-// What bounds it: the tensor cores, at 1,660 TFLOP/s for the first of these (166
-// us) and 1,850 for 8,192 x 14,336 x 4,096, where the power limit holds them; small
-// ones the chain of copies, sums and epilogue (20 us for 777 x 1,001 x 2,049).
+// The two products of a backward pass (dx and dw) go as one list of tiles, those
+// of the longer sum first: in a launch each, both leave their last round of tiles
+// part empty, and small ones pay for two launches (4,096 tokens, 8,192 x 2,048: the
+// call 295 us with two, 273 with one; 1,111 tokens, 515 x 1,365: 49.3 and 46.6).  How
+// an operand is stored is a field of its product here, the same for all lanes.
+//
+// What bounds it: the tensor cores, at 1,590 to 1,660 TFLOP/s for the first of
+// these (166 to 173 us) and 1,820 for 8,192 x 14,336 x 4,096 alone (528 us), less
+// where calls follow one another and the power limit lowers the clock; small ones
+// the chain of copies, sums and epilogue (20 us for 777 x 1,001 x 2,049).  The
+// running sums take 64 of an epilogue thread's 96 registers: 248 bytes of a
+// thread's other values are spilled, once a tile.
 
 namespace prod {
 

@@ -9,7 +9,7 @@
 // Matrices whose smaller side is at most 128 (the larger at most 4,096) take one
 // launch (skinny.cuh).  The others are streamed once each by two kernels: sums of
 // squares (and the momentum, for Muon), then the scaled f16 copy (8 x 2,048^2,
-// Muon: 54 and 49 us for 335 and 268 MB, 6.2 and 5.5 TB/s); the products are
+// Muon: 55 and 50 us for 335 and 268 MB, 6.0 and 5.4 TB/s); the products are
 // product.cuh's, all matrices of one shape in each launch, and the last one's
 // epilogue writes the caller's matrix -- the bf16 result, or the parameter
 // itself, decayed, stepped and rounded with its own random bits.  With P = a I + b S + c S S formed by the

@@ -24,7 +24,7 @@
 //   - the tiles of a last round that would leave most pairs idle go in halves or
 //     quarters of their columns.
 // What bounds it: large products run at the tensor cores' sustained rate under
-// the power limit (8,192 x 14,336 x 4,096 integers: 520 us alone, 1,850 TFLOP/s);
+// the power limit (8,192 x 14,336 x 4,096 integers: 528 us alone, 1,820 TFLOP/s);
 // short ones at the L2's (a 256 x 256 tile moves 64 bytes a cycle and SM), or,
 // below about 10 us, at the chain of launch (1.4 us after the last kernel's end),
 // first copies (1.6 us), epilogue and exit (2 us).

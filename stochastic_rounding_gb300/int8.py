@@ -74,7 +74,8 @@ class Int8Linear(torch.nn.Module):
     number of such passes, is the Philox step).  ``calls`` is part of the state
     dict (``_extra_state``), so a run repeats bit for bit, resumed from a checkpoint or
     not; a state dict without it, such as ``torch.nn.Linear``'s, loads too and
-    leaves it as it is.
+    leaves it as it is (the other way, ``torch.nn.Linear`` takes the weight with
+    ``strict=False``).
 
     The random bits of an output gradient's element are those of its index in
     (tokens, out_features), from position 0 on, under (seed, pass).  Layers that share a
