@@ -410,6 +410,114 @@ asr_status asr_linear_int8_grads(const void *dy, int32_t dy_dtype, uint64_t dy_l
 /* Workspace of that call for both gradients. */
 asr_status asr_linear_int8_grads_workspace(uint64_t tokens, uint64_t n, uint64_t k, uint64_t *bytes);
 
+/* ------------------------------ activations kept in 8 bits for the backward pass
+ *
+ * A checkpoint of a matrix, rows x cols: 32 values of a row share a power of two
+ * 2^e, the least (at least 2^-127) with max |x| <= 127 2^e.  With y = x 2^-e, which
+ * is exact,
+ *   q = rint(y)                                        ASR_ROUND_RNE
+ *   q = floor(y) + (65536 (y - floor(y)) > r)          ASR_ROUND_SR
+ * and what is read back is q 2^e, exact in f32 and in bf16 (down to their smallest
+ * numbers; values within 2^-8 of f32's largest may round to 2^128, an infinity, as they do
+ * in bf16).  A group that holds an infinity or a NaN is read back as NaN.  The random
+ * bits are not the optimizers', whatever the seed: value i, counted in rows of whole
+ * groups (row * 32 * ceil(cols / 32) + column) from base_index, a multiple of 32, has
+ * the counter ((i >> 3) lo32, (i >> 3) hi32, step, 1) and r = the low (i even) or high
+ * (i odd) half of its word (i >> 1) & 3. */
+typedef struct {
+    int8_t *q;              /* rows x cols codes, q_ld >= cols bytes between rows          */
+    uint8_t *power;         /* e + 127 of each group, 255 for NaN: rows x ceil(cols / 32),
+                               power_ld bytes between rows                                 */
+    uint64_t q_ld, power_ld;
+    uint64_t base_index;    /* the rest is read where a checkpoint is made                 */
+    uint64_t seed;
+    uint32_t step;
+    uint32_t rounding;      /* asr_rounding */
+} asr_checkpoint;
+
+/* Makes the checkpoint of x (x_ld elements between rows); bytes between a row's end
+ * and the next are not written.  rows at most 2^30, cols at most 2^24. */
+asr_status asr_checkpoint_int8(const void *x, int32_t x_dtype, uint64_t rows, uint64_t cols, uint64_t x_ld,
+                               const asr_checkpoint *to, asr_stream_t stream);
+
+/* The values that a checkpoint stands for. */
+asr_status asr_restore_int8(const asr_checkpoint *from, uint64_t rows, uint64_t cols, void *out, int32_t out_dtype,
+                            uint64_t out_ld, asr_stream_t stream);
+
+/* A layer's activation: f(a) = a s(u), s(u) = 1 / (1 + e^-u), with u = a (ASR_SILU) or
+ * u = sqrt(8/pi) (a + 0.044715 a^3) (ASR_GELU, its tanh form).  gated == 0: x is rows x
+ * cols and y = f(x).  gated == 1: x is rows x 2 cols, [a | b], and y = f(a) b.
+ * x and y of one dtype.  keep, if not NULL, receives x's checkpoint (of all its columns). */
+typedef enum { ASR_SILU = 0, ASR_GELU = 1 } asr_function;
+
+asr_status asr_activation(const void *x, uint64_t x_ld, void *y, uint64_t y_ld, int32_t dtype, uint64_t rows,
+                          uint64_t cols, uint32_t function, uint32_t gated, const asr_checkpoint *keep,
+                          asr_stream_t stream);
+
+/* Its backward pass: dx (x's shape) from dy (rows x cols), at x itself or at the values
+ * of its checkpoint (one of the two, the other NULL): dx = dy f'(x), or [dy f'(a) b | dy f(a)]. */
+asr_status asr_activation_grads(const void *dy, uint64_t dy_ld, const void *x, uint64_t x_ld,
+                                const asr_checkpoint *kept, void *dx, uint64_t dx_ld, int32_t dtype, uint64_t rows,
+                                uint64_t cols, uint32_t function, uint32_t gated, asr_stream_t stream);
+
+/* ------------------------------------------------------------- layer norm
+ *
+ * For each row of x: mean = sum x / cols (centred) or 0, rstd = 1 / sqrt(sum (x -
+ * mean)^2 / cols + eps), h = (x - mean) rstd, y = h weight + bias; centred == 0 is the
+ * norm by the root mean square.  x, y, dy and dx are of `dtype`; weight (cols) and bias
+ * (cols) of their own, or NULL (ones, zeros).  Sums are binary32, the squares about the
+ * mean; a row whose squares overflow has rstd 0.  y may be x. */
+typedef struct {
+    uint64_t rows, cols;
+    const void *weight, *bias;
+    double eps;             /* finite, >= 0 */
+    int32_t dtype, weight_dtype, bias_dtype;
+    uint32_t centred;       /* 0 or 1 */
+    uint64_t reserved;      /* 0 */
+} asr_norm_params;
+
+/* mean and rstd (rows each, binary32) are what the backward pass reads; either may be
+ * NULL (mean without rstd may not).  keep, if not NULL, receives x's checkpoint. */
+asr_status asr_layer_norm(const asr_norm_params *params, const void *x, uint64_t x_ld, void *y, uint64_t y_ld,
+                          float *mean, float *rstd, const asr_checkpoint *keep, asr_stream_t stream);
+
+/* Backward, at x or at the values of its checkpoint (the other NULL), with the forward
+ * pass's mean (not read if not centred) and rstd:
+ *   g = dy weight;  dx = rstd (g - [mean of g, centred] - h (mean of g h))
+ *   dweight = sum over rows of dy h;  dbias = sum over rows of dy
+ * any of the three may be NULL where it is not needed; dweight and dbias without rows
+ * are zeros.  workspace (for dweight and dbias): device, 256-byte aligned, at least
+ * asr_layer_norm_grads_workspace's bytes. */
+asr_status asr_layer_norm_grads(const asr_norm_params *params, const void *dy, uint64_t dy_ld, const void *x,
+                                uint64_t x_ld, const asr_checkpoint *kept, const float *mean, const float *rstd,
+                                void *dx, uint64_t dx_ld, void *dweight, int32_t dweight_dtype, void *dbias,
+                                int32_t dbias_dtype, void *workspace, uint64_t workspace_bytes, asr_stream_t stream);
+
+asr_status asr_layer_norm_grads_workspace(uint64_t rows, uint64_t cols, uint64_t *bytes);
+
+/* -------------------------------------------------------------- embedding
+ *
+ * y[t] = scale * table[ids[t]] for `tokens` ids (32- or 64-bit); table is vocab x dim,
+ * y tokens x dim, of one dtype.  An id outside [0, vocab) has no row: y[t] is NaN.
+ * tokens and vocab at most 2^28, dim at most 2^24. */
+typedef enum { ASR_I32 = 0, ASR_I64 = 1 } asr_index;
+
+asr_status asr_embedding(const void *ids, int32_t index, uint64_t tokens, const void *table, uint64_t table_ld,
+                         uint64_t vocab, uint64_t dim, double scale, void *y, uint64_t y_ld, int32_t dtype,
+                         asr_stream_t stream);
+
+/* The table's gradient, all of it (vocab x dim, contiguous): dtable[v] = scale * sum of
+ * dy[t] over the tokens with ids[t] == v, zeros where there are none.  Tokens of
+ * padding_idx (negative: none) and of ids outside the table add nothing.  Sums are
+ * binary32 in one order, so the result repeats bit for bit.  workspace: device, 256-byte
+ * aligned, at least asr_embedding_grads_workspace's bytes. */
+asr_status asr_embedding_grads(const void *ids, int32_t index, uint64_t tokens, const void *dy, uint64_t dy_ld,
+                               int32_t dy_dtype, uint64_t vocab, uint64_t dim, double scale, int64_t padding_idx,
+                               void *dtable, int32_t dtable_dtype, void *workspace, uint64_t workspace_bytes,
+                               asr_stream_t stream);
+
+asr_status asr_embedding_grads_workspace(uint64_t tokens, uint64_t dim, uint64_t *bytes);
+
 /* Static description of a status code. */
 const char *asr_status_string(asr_status status);
 
@@ -499,7 +607,11 @@ typedef enum {
     ASR_KERNEL_PRODUCT = 9,                  /* f16-operand products of Newton-Schulz, Muon and the 8-bit GEMM */
     ASR_KERNEL_QUANTIZE = 10,                /* 8-bit quantiser, and the 8-bit GEMM's widening of its operands */
     ASR_KERNEL_INT8_FEW_ROWS = 11,           /* the 8-bit GEMM with few rows */
-    ASR_KERNEL_KINDS = 12
+    ASR_KERNEL_CHECKPOINT = 12,              /* asr_checkpoint_int8, asr_restore_int8 */
+    ASR_KERNEL_ACTIVATION = 13,              /* asr_activation and its gradients */
+    ASR_KERNEL_NORM = 14,                    /* asr_layer_norm and its gradients */
+    ASR_KERNEL_EMBEDDING = 15,               /* asr_embedding and its gradient */
+    ASR_KERNEL_KINDS = 16
 } asr_kernel_kind;
 
 /* Diagnostic (no counterpart on the pages): copies into counts[k], for

@@ -12,8 +12,13 @@ from ._lib import (  # noqa: F401
     asr_kernel_launches, asr_adamw_sr_multi_tensor_host, lib, make_host_table, make_table,
     asr_gemm_int8_sr, asr_gemm_int8_workspace, asr_muon_sr_multi_tensor, asr_muon_workspace, asr_newton_schulz,
     asr_newton_schulz_workspace, asr_quantize_int8, int8_empty, asr_linear_int8, asr_linear_int8_workspace,
-    asr_linear_int8_grads, asr_linear_int8_grads_workspace,
+    asr_linear_int8_grads, asr_linear_int8_grads_workspace, asr_checkpoint_int8, asr_restore_int8, asr_activation,
+    asr_activation_grads, asr_layer_norm, asr_layer_norm_grads, asr_layer_norm_grads_workspace, asr_embedding,
+    asr_embedding_grads, asr_embedding_grads_workspace,
 )
-from .int8 import Int8Linear, int8_linear, int8_linear_grads  # noqa: F401,E402
+from .int8 import (Int8Checkpoint, Int8Linear, checkpoint_int8, int8_linear, int8_linear_grads,  # noqa: F401,E402
+                   restore_int8)
+from .layers import (Activation, Embedding, LayerNorm, NormSaved, activation, activation_grads,  # noqa: F401,E402
+                     embedding, embedding_grads, layer_norm, layer_norm_grads)
 from .optim import AdamWSR, DeviceError  # noqa: F401,E402
 from .muon import MuonSR  # noqa: F401,E402

@@ -30,12 +30,18 @@ EXPORTS = ("asr_philox4x32", "asr_stochastic_round_bf16", "asr_adamw_prepare",
            "asr_kernel_launches", "asr_adamw_sr_multi_tensor_host",
            "asr_newton_schulz", "asr_newton_schulz_workspace", "asr_muon_sr_multi_tensor", "asr_muon_workspace",
            "asr_quantize_int8", "asr_gemm_int8_sr", "asr_gemm_int8_workspace", "asr_linear_int8",
-           "asr_linear_int8_workspace", "asr_linear_int8_grads", "asr_linear_int8_grads_workspace")
+           "asr_linear_int8_workspace", "asr_linear_int8_grads", "asr_linear_int8_grads_workspace",
+           "asr_checkpoint_int8", "asr_restore_int8", "asr_activation", "asr_activation_grads", "asr_layer_norm",
+           "asr_layer_norm_grads", "asr_layer_norm_grads_workspace", "asr_embedding", "asr_embedding_grads",
+           "asr_embedding_grads_workspace")
 # asr_kernel_kind, in order
 KERNEL_KINDS = ("adamw_scalar", "adamw_vector", "adamw_pipelined", "adamw_pipelined_any_base", "adamw_static",
-                "round", "philox", "gemm", "matrix_prep", "product", "quantize", "int8_few_rows")
+                "round", "philox", "gemm", "matrix_prep", "product", "quantize", "int8_few_rows", "checkpoint", "activation",
+                "norm", "embedding")
 ASR_MUON_ADJUST_NONE, ASR_MUON_ADJUST_SPECTRAL, ASR_MUON_ADJUST_RMS = 0, 1, 2
 ASR_ROWS, ASR_COLUMNS = 0, 1
+ASR_SILU, ASR_GELU = 0, 1
+ASR_I32, ASR_I64 = 0, 1
 ASR_STATIC_TABLE_MAX = 4096
 
 
@@ -84,6 +90,19 @@ class MuonDesc(ctypes.Structure):
     _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("momentum", ctypes.c_void_p),
                 ("count", ctypes.c_uint64), ("rows", ctypes.c_uint64), ("cols", ctypes.c_uint64),
                 ("base_index", ctypes.c_uint64), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+
+
+class Checkpoint(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("power", ctypes.c_void_p), ("q_ld", ctypes.c_uint64),
+                ("power_ld", ctypes.c_uint64), ("base_index", ctypes.c_uint64), ("seed", ctypes.c_uint64),
+                ("step", ctypes.c_uint32), ("rounding", ctypes.c_uint32)]
+
+
+class NormParams(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_uint64), ("cols", ctypes.c_uint64), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("eps", ctypes.c_double), ("dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("bias_dtype", ctypes.c_int32), ("centred", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint64)]
 
 
 class AsrError(RuntimeError):
@@ -135,6 +154,22 @@ def lib() -> ctypes.CDLL:
         L.asr_linear_int8_grads.argtypes = [vp, i32, u64, vp, i32, u64, vp, i32, u64, vp, u64, vp, u64, u64, u64, u64,
                                             u32, u64, vp, u64, vp]
         L.asr_linear_int8_grads_workspace.argtypes = [u64, u64, u64, pu64]
+        i64, pck, pnp = ctypes.c_int64, ctypes.POINTER(Checkpoint), ctypes.POINTER(NormParams)
+        L.asr_checkpoint_int8.argtypes = [vp, i32, u64, u64, u64, pck, vp]
+        L.asr_restore_int8.argtypes = [pck, u64, u64, vp, i32, u64, vp]
+        L.asr_activation.argtypes = [vp, u64, vp, u64, i32, u64, u64, u32, u32, pck, vp]
+        L.asr_activation_grads.argtypes = [vp, u64, vp, u64, pck, vp, u64, i32, u64, u64, u32, u32, vp]
+        L.asr_layer_norm.argtypes = [pnp, vp, u64, vp, u64, vp, vp, pck, vp]
+        L.asr_layer_norm_grads.argtypes = [pnp, vp, u64, vp, u64, pck, vp, vp, vp, u64, vp, i32, vp, i32, vp, u64, vp]
+        L.asr_layer_norm_grads_workspace.argtypes = [u64, u64, pu64]
+        L.asr_embedding.argtypes = [vp, i32, u64, vp, u64, u64, u64, ctypes.c_double, vp, u64, i32, vp]
+        L.asr_embedding_grads.argtypes = [vp, i32, u64, vp, u64, i32, u64, u64, ctypes.c_double, i64, vp, i32, vp, u64,
+                                          vp]
+        L.asr_embedding_grads_workspace.argtypes = [u64, u64, pu64]
+        for f in ("asr_checkpoint_int8", "asr_restore_int8", "asr_activation", "asr_activation_grads",
+                  "asr_layer_norm", "asr_layer_norm_grads", "asr_layer_norm_grads_workspace", "asr_embedding",
+                  "asr_embedding_grads", "asr_embedding_grads_workspace"):
+            getattr(L, f).restype = ctypes.c_int
         for f in ("asr_newton_schulz", "asr_newton_schulz_workspace", "asr_muon_sr_multi_tensor",
                   "asr_muon_workspace", "asr_quantize_int8", "asr_gemm_int8_sr", "asr_gemm_int8_workspace",
                   "asr_linear_int8", "asr_linear_int8_workspace", "asr_linear_int8_grads",
@@ -898,3 +933,254 @@ def asr_linear_int8_grads(dy, x, w, dx, dw, *, step: int = 0, seed: int = 0, wor
         _check(lib().asr_linear_int8_grads(pg, _dt(dy), g_ld, *args, t, n, k, int(step) & 0xFFFFFFFF,
                                            int(seed) & (2**64 - 1), pws, size, _stream_handle(device, stream)),
                "asr_linear_int8_grads")
+
+
+# ------------------------------- activations kept in 8 bits, norm, embedding
+
+_FUNCTION = {"silu": ASR_SILU, "gelu": ASR_GELU}
+CHECKPOINT_GROUP = 32           # values of a row that share a power of two
+
+
+def _checkpoint(kept, rows, cols, device, rounding="rne", base_index=0, step=0, seed=0):
+    """The C struct of a checkpoint (q, power) of a rows x cols matrix."""
+    torch = _torch()
+    q, power = kept[0], kept[1]
+    pq, qr, qc, q_ld = _matrix_ptr(q, "q", (torch.int8,), device)
+    pp, pr, pc, p_ld = _matrix_ptr(power, "power", (torch.uint8,), device)
+    groups = (cols + CHECKPOINT_GROUP - 1) // CHECKPOINT_GROUP
+    if qr != rows or qc != cols or pr != rows or pc != groups:
+        raise ValueError(f"a checkpoint of {(rows, cols)} has q of that shape and power of {(rows, groups)}, not "
+                         f"{(qr, qc)} and {(pr, pc)}")
+    r = _ROUNDING.get(rounding)
+    if r is None:
+        raise ValueError(f"rounding must be 'sr' or 'rne', not {rounding!r}")
+    return Checkpoint(pq, pp, q_ld, p_ld, int(base_index) & (2**64 - 1), int(seed) & (2**64 - 1), int(step) & 0xFFFFFFFF,
+                      r)
+
+
+def asr_checkpoint_int8(x, q, power, *, rounding="rne", base_index: int = 0, step: int = 0, seed: int = 0, stream=None):
+    """The 8-bit checkpoint of ``x`` (float32 or bfloat16, 2-D): codes into ``q``
+    (int8, x's shape), the power of two of each 32 of a row's values into
+    ``power`` (uint8, x's rows by ceil(columns / 32)).  ``rounding="sr"`` rounds
+    stochastically."""
+    torch = _torch()
+    px, rows, cols, ld = _matrix_ptr(x, "x", (torch.bfloat16, torch.float32))
+    c = _checkpoint((q, power), rows, cols, x.get_device(), rounding, base_index, step, seed)
+    with _on_device(x.device):
+        _check(lib().asr_checkpoint_int8(px, _dt(x), rows, cols, ld, ctypes.byref(c), _stream_handle(x.device, stream)),
+               "asr_checkpoint_int8")
+    return q, power
+
+
+def asr_restore_int8(q, power, out, *, stream=None):
+    """The values that a checkpoint stands for, into ``out`` (float32 or bfloat16)."""
+    torch = _torch()
+    po, rows, cols, ld = _matrix_ptr(out, "out", (torch.bfloat16, torch.float32))
+    c = _checkpoint((q, power), rows, cols, out.get_device())
+    with _on_device(out.device):
+        _check(lib().asr_restore_int8(ctypes.byref(c), rows, cols, po, _dt(out), ld, _stream_handle(out.device, stream)),
+               "asr_restore_int8")
+    return out
+
+
+def _function(function):
+    code = _FUNCTION.get(function)
+    if code is None:
+        raise ValueError(f"function must be 'silu' or 'gelu', not {function!r}")
+    return code
+
+
+def asr_activation(x, y, function="silu", *, gated=False, keep=None, rounding="rne", base_index: int = 0, step: int = 0,
+                   seed: int = 0, stream=None):
+    """``y`` = f(x), or, ``gated``, f of x's first half of columns times its second
+    half; x and y 2-D of one dtype, float32 or bfloat16.  ``keep``: (q, power) that
+    receive x's checkpoint."""
+    torch = _torch()
+    code = _function(function)
+    py, rows, cols, y_ld = _matrix_ptr(y, "y", (torch.bfloat16, torch.float32))
+    d = y.get_device()
+    px, xr, xc, x_ld = _matrix_ptr(x, "x", (y.dtype,), d)
+    width = 2 * cols if gated else cols
+    if xr != rows or xc != width:
+        raise ValueError(f"x has shape {(xr, xc)}; expected {(rows, width)}")
+    c = None
+    if keep is not None:
+        c = ctypes.byref(_checkpoint(keep, rows, width, d, rounding, base_index, step, seed))
+    with _on_device(y.device):
+        _check(lib().asr_activation(px, x_ld, py, y_ld, _dt(y), rows, cols, code, 1 if gated else 0, c,
+                                    _stream_handle(y.device, stream)), "asr_activation")
+    return y
+
+
+def asr_activation_grads(dy, x, dx, function="silu", *, gated=False, kept=None, stream=None):
+    """``dx`` from ``dy`` at ``x``, or, x None, at the values of the checkpoint
+    ``kept`` (q, power); dy, x and dx 2-D of one dtype."""
+    torch = _torch()
+    code = _function(function)
+    pg, rows, cols, g_ld = _matrix_ptr(dy, "dy", (torch.bfloat16, torch.float32))
+    d = dy.get_device()
+    pd, dr, dc, d_ld = _matrix_ptr(dx, "dx", (dy.dtype,), d)
+    width = 2 * cols if gated else cols
+    if dr != rows or dc != width:
+        raise ValueError(f"dx has shape {(dr, dc)}; expected {(rows, width)}")
+    if (x is None) == (kept is None):
+        raise ValueError("give x or its checkpoint, one of the two")
+    px, x_ld, c = None, width, None
+    if x is not None:
+        px, xr, xc, x_ld = _matrix_ptr(x, "x", (dy.dtype,), d)
+        if xr != rows or xc != width:
+            raise ValueError(f"x has shape {(xr, xc)}; expected {(rows, width)}")
+    else:
+        c = ctypes.byref(_checkpoint(kept, rows, width, d))
+    with _on_device(dy.device):
+        _check(lib().asr_activation_grads(pg, g_ld, px, x_ld, c, pd, d_ld, _dt(dy), rows, cols, code, 1 if gated else 0,
+                                          _stream_handle(dy.device, stream)), "asr_activation_grads")
+    return dx
+
+
+def _norm_params(rows, cols, x, weight, bias, eps, centred, device) -> NormParams:
+    torch = _torch()
+    types = (torch.bfloat16, torch.float32)
+    pw = None if weight is None else _dev_ptr(weight, "weight", types, cols, device)
+    pb = None if bias is None else _dev_ptr(bias, "bias", types, cols, device)
+    return NormParams(rows, cols, pw, pb, float(eps), _dt(x), ASR_F32 if weight is None else _dt(weight),
+                      ASR_F32 if bias is None else _dt(bias), 1 if centred else 0, 0)
+
+
+def asr_layer_norm(x, weight, bias, y, mean=None, rstd=None, *, eps=1e-5, centred=True, keep=None, rounding="rne",
+                   base_index: int = 0, step: int = 0, seed: int = 0, stream=None):
+    """``y`` = (x - mean) rstd weight + bias for each row of ``x`` (2-D, float32 or
+    bfloat16; y likewise, y may be x); ``centred=False`` leaves the mean out (the norm
+    by the root mean square).  ``weight`` and ``bias`` may be None.  ``mean`` and
+    ``rstd`` (float32, a value a row) and ``keep`` (q, power) receive what the
+    backward pass reads."""
+    torch = _torch()
+    px, rows, cols, x_ld = _matrix_ptr(x, "x", (torch.bfloat16, torch.float32))
+    d = x.get_device()
+    py, yr, yc, y_ld = _matrix_ptr(y, "y", (x.dtype,), d)
+    if yr != rows or yc != cols:
+        raise ValueError(f"y has shape {(yr, yc)}; expected {(rows, cols)}")
+    p = _norm_params(rows, cols, x, weight, bias, eps, centred, d)
+    f32 = (torch.float32,)
+    pm = None if mean is None else _dev_ptr(mean, "mean", f32, rows, d)
+    pr = None if rstd is None else _dev_ptr(rstd, "rstd", f32, rows, d)
+    c = None
+    if keep is not None:
+        c = ctypes.byref(_checkpoint(keep, rows, cols, d, rounding, base_index, step, seed))
+    with _on_device(x.device):
+        _check(lib().asr_layer_norm(ctypes.byref(p), px, x_ld, py, y_ld, pm, pr, c, _stream_handle(x.device, stream)),
+               "asr_layer_norm")
+    return y
+
+
+@functools.lru_cache(maxsize=1024)
+def asr_layer_norm_grads_workspace(rows: int, cols: int) -> int:
+    """Bytes of workspace that ``asr_layer_norm_grads`` needs for a weight's or a bias's gradient."""
+    need = ctypes.c_uint64(0)
+    _check(lib().asr_layer_norm_grads_workspace(int(rows), int(cols), ctypes.byref(need)),
+           "asr_layer_norm_grads_workspace")
+    return int(need.value)
+
+
+def asr_layer_norm_grads(dy, x, weight, mean, rstd, dx, dweight, dbias, *, centred=True, kept=None, workspace=None,
+                         stream=None):
+    """Gradients of ``asr_layer_norm`` from ``dy``, at ``x``, or, x None, at the
+    values of the checkpoint ``kept`` (q, power), with the forward pass's ``mean``
+    (None if not centred) and ``rstd``.  ``dx`` (dy's dtype), ``dweight`` and
+    ``dbias`` (float32 or bfloat16): any may be None where it is not needed."""
+    torch = _torch()
+    types = (torch.bfloat16, torch.float32)
+    pg, rows, cols, g_ld = _matrix_ptr(dy, "dy", types)
+    d = dy.get_device()
+    if (x is None) == (kept is None):
+        raise ValueError("give x or its checkpoint, one of the two")
+    px, x_ld, c = None, cols, None
+    if x is not None:
+        px, xr, xc, x_ld = _matrix_ptr(x, "x", (dy.dtype,), d)
+        if xr != rows or xc != cols:
+            raise ValueError(f"x has shape {(xr, xc)}; expected {(rows, cols)}")
+    else:
+        c = ctypes.byref(_checkpoint(kept, rows, cols, d))
+    p = _norm_params(rows, cols, dy, weight, None, 0.0, centred, d)
+    f32 = (torch.float32,)
+    if rstd is None or (centred and mean is None):
+        raise ValueError("the backward pass needs the forward pass's rstd, and its mean if centred")
+    pm = _dev_ptr(mean, "mean", f32, rows, d) if centred else None
+    pr = _dev_ptr(rstd, "rstd", f32, rows, d)
+    pd, d_ld = None, cols
+    if dx is not None:
+        pd, dr, dc, d_ld = _matrix_ptr(dx, "dx", (dy.dtype,), d)
+        if dr != rows or dc != cols:
+            raise ValueError(f"dx has shape {(dr, dc)}; expected {(rows, cols)}")
+    pw = None if dweight is None else _dev_ptr(dweight, "dweight", types, cols, d)
+    pb = None if dbias is None else _dev_ptr(dbias, "dbias", types, cols, d)
+    sums = dweight is not None or dbias is not None
+    need = asr_layer_norm_grads_workspace(rows, cols) if sums else 0
+    device = dy.device
+    with _on_device(device):
+        buf, pws, size = _workspace(workspace, need, device, stream)
+        _check(lib().asr_layer_norm_grads(ctypes.byref(p), pg, g_ld, px, x_ld, c, pm, pr, pd, d_ld, pw,
+                                          ASR_F32 if dweight is None else _dt(dweight), pb,
+                                          ASR_F32 if dbias is None else _dt(dbias), pws, size,
+                                          _stream_handle(device, stream)), "asr_layer_norm_grads")
+
+
+def _ids(ids, device):
+    torch = _torch()
+    p = _dev_ptr(ids, "ids", (torch.int64, torch.int32), None, device)
+    if ids.dim() != 1:
+        raise ValueError("ids must be 1-D")
+    return p, ASR_I64 if ids.dtype == torch.int64 else ASR_I32, ids.numel()
+
+
+def asr_embedding(ids, table, y, *, scale=1.0, stream=None):
+    """``y[t] = scale * table[ids[t]]``: ``ids`` 1-D, int64 or int32; ``table``
+    (vocab, dim) and ``y`` (tokens, dim) of one dtype, float32 or bfloat16.  An id
+    outside the table gives a row of NaN."""
+    torch = _torch()
+    pt, vocab, dim, t_ld = _matrix_ptr(table, "table", (torch.bfloat16, torch.float32))
+    d = table.get_device()
+    pi, index, tokens = _ids(ids, d)
+    py, yr, yc, y_ld = _matrix_ptr(y, "y", (table.dtype,), d)
+    if yr != tokens or yc != dim:
+        raise ValueError(f"y has shape {(yr, yc)}; expected {(tokens, dim)}")
+    with _on_device(table.device):
+        _check(lib().asr_embedding(pi, index, tokens, pt, t_ld, vocab, dim, float(scale), py, y_ld, _dt(y),
+                                   _stream_handle(table.device, stream)), "asr_embedding")
+    return y
+
+
+@functools.lru_cache(maxsize=1024)
+def asr_embedding_grads_workspace(tokens: int, dim: int) -> int:
+    """Bytes of workspace that ``asr_embedding_grads`` needs at these sizes."""
+    need = ctypes.c_uint64(0)
+    _check(lib().asr_embedding_grads_workspace(int(tokens), int(dim), ctypes.byref(need)),
+           "asr_embedding_grads_workspace")
+    return int(need.value)
+
+
+def asr_embedding_grads(ids, dy, dtable, *, scale=1.0, padding_idx=None, workspace=None, stream=None):
+    """The gradient of ``asr_embedding``'s table, all of it, into ``dtable``
+    (contiguous, (vocab, dim), float32 or bfloat16) from ``dy`` (tokens, dim).
+    Tokens of ``padding_idx`` and of ids outside the table add nothing."""
+    torch = _torch()
+    types = (torch.bfloat16, torch.float32)
+    pd = _dev_ptr(dtable, "dtable", types)
+    if dtable.dim() != 2:
+        raise ValueError("dtable must be 2-D")
+    vocab, dim = dtable.shape
+    d = dtable.get_device()
+    pi, index, tokens = _ids(ids, d)
+    pg, gr, gc, g_ld = _matrix_ptr(dy, "dy", types, d)
+    if gr != tokens or gc != dim:
+        raise ValueError(f"dy has shape {(gr, gc)}; expected {(tokens, dim)}")
+    if padding_idx is not None and not 0 <= int(padding_idx) < vocab:
+        raise ValueError(f"padding_idx must be a row of the table (0 to {vocab - 1}), not {padding_idx}")
+    need = asr_embedding_grads_workspace(tokens, dim)
+    device = dtable.device
+    with _on_device(device):
+        buf, pws, size = _workspace(workspace, need, device, stream)
+        _check(lib().asr_embedding_grads(pi, index, tokens, pg, g_ld, _dt(dy), vocab, dim, float(scale),
+                                         -1 if padding_idx is None else int(padding_idx), pd, _dt(dtable), pws, size,
+                                         _stream_handle(device, stream)), "asr_embedding_grads")
+    return dtable

@@ -13,10 +13,42 @@ package updates.
 """
 from __future__ import annotations
 
+from typing import NamedTuple
+
 import torch
 from torch.autograd.function import once_differentiable
 
-from ._lib import asr_linear_int8, asr_linear_int8_grads, asr_quantize_int8, int8_empty
+from ._lib import (CHECKPOINT_GROUP, asr_checkpoint_int8, asr_linear_int8, asr_linear_int8_grads, asr_quantize_int8,
+                   asr_restore_int8, int8_empty)
+
+
+class Int8Checkpoint(NamedTuple):
+    """A matrix kept in 8 bits: codes, the power of two (plus 127) of each 32 of a
+    row's values, and the dtype of what it was made from."""
+    q: torch.Tensor
+    power: torch.Tensor
+    dtype: torch.dtype
+
+
+def empty_checkpoint(rows: int, cols: int, device, dtype) -> Int8Checkpoint:
+    """An uninitialised checkpoint of a rows x cols matrix."""
+    power = torch.empty(rows, (cols + CHECKPOINT_GROUP - 1) // CHECKPOINT_GROUP, dtype=torch.uint8, device=device)
+    return Int8Checkpoint(int8_empty(rows, cols, device), power, dtype)
+
+
+def checkpoint_int8(x, *, rounding="rne", base_index: int = 0, step: int = 0, seed: int = 0) -> Int8Checkpoint:
+    """``x`` (2-D, float32 or bfloat16) kept in 8 bits for a backward pass: 32 values
+    of a row share a power of two.  ``rounding="sr"`` rounds stochastically, so that
+    what is read back is x on average (to within 2^-16 of a step)."""
+    c = empty_checkpoint(*x.shape, x.device, x.dtype)
+    asr_checkpoint_int8(x, c.q, c.power, rounding=rounding, base_index=base_index, step=step, seed=seed)
+    return c
+
+
+def restore_int8(checkpoint: Int8Checkpoint, dtype=None):
+    """The values that a checkpoint stands for, in ``dtype`` (the original's unless given); exact in either."""
+    out = torch.empty(checkpoint.q.shape, dtype=dtype or checkpoint.dtype, device=checkpoint.q.device)
+    return asr_restore_int8(checkpoint.q, checkpoint.power, out)
 
 
 def int8_linear(x, qweight, weight_scale, *, rounding="rne", step: int = 0, seed: int = 0, out=None):
@@ -46,10 +78,16 @@ def _by_rows(t):
 
 class _Int8LinearFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, step, seed):
+    def forward(ctx, x, weight, step, seed, save):
         x, weight = _by_rows(x), _by_rows(weight)
-        ctx.save_for_backward(x, weight)
-        ctx.key = (step, seed)
+        ctx.key, ctx.x_dtype = (step, seed), x.dtype
+        if save == "int8" and ctx.needs_input_grad[1]:
+            kept = checkpoint_int8(x, rounding="sr", step=step, seed=seed)
+            ctx.save_for_backward(weight, kept.q, kept.power)
+        elif save == "int8":                # dx does not read x
+            ctx.save_for_backward(weight)
+        else:
+            ctx.save_for_backward(weight, x)
         q = int8_empty(*weight.shape, weight.device)
         scale = torch.empty(weight.shape[0], dtype=torch.float32, device=weight.device)
         asr_quantize_int8(weight, q, scale)
@@ -58,43 +96,36 @@ class _Int8LinearFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable                    # the calls record nothing: a second derivative through them is an error
     def backward(ctx, dy):
-        x, weight = ctx.saved_tensors
+        weight, *x = ctx.saved_tensors
         step, seed = ctx.key
-        dx, dw = int8_linear_grads(dy.contiguous(), x, weight, step=step, seed=seed, need_dx=ctx.needs_input_grad[0],
-                                   need_dw=ctx.needs_input_grad[1])
-        return (dx.to(x.dtype) if dx is not None else None, dw.to(weight.dtype) if dw is not None else None, None,
-                None)
+        dy = dy.contiguous()
+        need_dx, need_dw = ctx.needs_input_grad[:2]
+        if len(x) == 2:                     # what 8 bits stand for is exact in bf16
+            x = restore_int8(Int8Checkpoint(*x, torch.bfloat16))
+        elif x:
+            x = x[0]
+        else:
+            x = dy.new_empty(dy.shape[0], weight.shape[1])
+        dx, dw = int8_linear_grads(dy, x, weight, step=step, seed=seed, need_dx=need_dx, need_dw=need_dw)
+        return (dx.to(ctx.x_dtype) if dx is not None else None, dw.to(weight.dtype) if dw is not None else None, None,
+                None, None)
 
 
-class Int8Linear(torch.nn.Module):
-    """``torch.nn.Linear`` without a bias on the 8-bit products: a bf16 (or
-    float32) weight of shape (out_features, in_features), quantised in every
-    forward pass.  ``seed`` keys the stochastic rounding of the gradients; it
-    is drawn anew for every forward pass that records gradients (``calls``, the
-    number of such passes, is the Philox step).  ``calls`` is part of the state
-    dict (``_extra_state``), so a run repeats bit for bit, resumed from a checkpoint or
-    not; a state dict without it, such as ``torch.nn.Linear``'s, loads too and
-    leaves it as it is (the other way, ``torch.nn.Linear`` takes the weight with
-    ``strict=False``).
+class _CountedModule(torch.nn.Module):
+    """A module whose passes that record gradients are counted: ``calls`` is the
+    Philox step of what a pass rounds stochastically, and part of the state dict
+    (``_extra_state``), so that a run repeats bit for bit, resumed from a checkpoint or
+    not.  A state dict without it loads too and leaves the count as it is."""
 
-    The random bits of an output gradient's element are those of its index in
-    (tokens, out_features), from position 0 on, under (seed, pass).  Layers that share a
-    seed share them, as do data-parallel ranks, and an optimizer of that seed
-    uses them for its first parameters: give each layer and rank a seed of its
-    own where the errors are to be independent."""
-
-    def __init__(self, in_features: int, out_features: int, *, seed: int = 0, device=None, dtype=torch.bfloat16):
+    def __init__(self, seed: int):
         super().__init__()
-        self.in_features, self.out_features, self.seed, self.calls = in_features, out_features, int(seed), 0
-        self.weight = torch.nn.Parameter(torch.empty(out_features, in_features, device=device, dtype=dtype))
-        torch.nn.init.normal_(self.weight, std=in_features ** -0.5)
+        self.seed, self.calls = int(seed), 0
 
-    def forward(self, x):
-        if torch.is_grad_enabled() and (x.requires_grad or self.weight.requires_grad):
+    def _count(self, *tensors):
+        if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
             self.calls += 1
-        flat = x.reshape(-1, self.in_features)
-        y = _Int8LinearFunction.apply(flat, self.weight, self.calls, self.seed)
-        return y.reshape(*x.shape[:-1], self.out_features)
+            return True
+        return False
 
     def get_extra_state(self):
         return torch.tensor(self.calls, device="cpu")
@@ -109,5 +140,44 @@ class Int8Linear(torch.nn.Module):
         if prefix + "_extra_state" in missing_keys:
             missing_keys.remove(prefix + "_extra_state")
 
+
+class Int8Linear(_CountedModule):
+    """``torch.nn.Linear`` without a bias on the 8-bit products: a bf16 (or
+    float32) weight of shape (out_features, in_features), quantised in every
+    forward pass.  ``seed`` keys the stochastic rounding of the gradients; it
+    is drawn anew for every forward pass that records gradients (``calls``, the
+    number of such passes, is the Philox step).  ``calls`` is part of the state
+    dict (``_extra_state``), so a run repeats bit for bit, resumed from a checkpoint or
+    not; a state dict without it, such as ``torch.nn.Linear``'s, loads too and
+    leaves it as it is (the other way, ``torch.nn.Linear`` takes the weight with
+    ``strict=False``).
+
+    ``save="int8"`` keeps the input in 8 bits for the backward pass, rounded
+    stochastically, in place of the input itself: a little over half of a bf16
+    input's memory, and a weight's gradient that is right on average.
+
+    The random bits of an output gradient's element are those of its index in
+    (tokens, out_features), from position 0 on, under (seed, pass).  Layers that share a
+    seed share them, as do data-parallel ranks, and an optimizer of that seed
+    uses them for its first parameters: give each layer and rank a seed of its
+    own where the errors are to be independent.  (The kept input's are others, but
+    also shared by layers of one seed.)"""
+
+    def __init__(self, in_features: int, out_features: int, *, seed: int = 0, device=None, dtype=torch.bfloat16,
+                 save: str = "input"):
+        if save not in ("input", "int8"):
+            raise ValueError(f"save must be 'input' or 'int8', not {save!r}")
+        super().__init__(seed)
+        self.in_features, self.out_features, self.save = in_features, out_features, save
+        self.weight = torch.nn.Parameter(torch.empty(out_features, in_features, device=device, dtype=dtype))
+        torch.nn.init.normal_(self.weight, std=in_features ** -0.5)
+
+    def forward(self, x):
+        self._count(x, self.weight)
+        flat = x.reshape(-1, self.in_features)
+        y = _Int8LinearFunction.apply(flat, self.weight, self.calls, self.seed, self.save)
+        return y.reshape(*x.shape[:-1], self.out_features)
+
     def extra_repr(self):
-        return f"in_features={self.in_features}, out_features={self.out_features}, seed={self.seed}"
+        return (f"in_features={self.in_features}, out_features={self.out_features}, seed={self.seed}" +
+                ("" if self.save == "input" else f", save={self.save!r}"))
