@@ -7,10 +7,9 @@
 //   f'(a) = s(u) (1 + a u' s(-u))
 //   y = f(a), or gated, x = [a | b]:  y = f(a) b,  da = dy f'(a) b,  db = dy f(a)
 //
-// s from t = e^-|u|, as 1 / (1 + t) or t / (1 + t): no cancellation on either side,
-// and no overflow.  bf16 results take the hardware's exponential and division,
-// whose error (below 2^-16 where e^-|u| is a normal number) their rounding hides;
-// f32 results take the library's.
+// bf16 results take the hardware's exponential and reciprocal, whose errors (a few
+// 2^-24, and |u| 2^-24 from the exponent's rounding) are far below their rounding;
+// f32 results take the library's.  Below u = -87, where e^-u leaves binary32, s is 0.
 //
 // Bound by bytes: an element of x and y each once, the kept form on the way.
 
@@ -31,25 +30,24 @@ struct Params {
 
 constexpr float kSlope = 1.5957691216057308f;   // sqrt(8 / pi)
 constexpr float kCube = 0.044715f;
+constexpr float kLog2e = 1.4426950408889634f;
 
-struct Sigmoid {
-    float plus, minus;                          // s(u), s(-u)
-};
-
+// s(u), and s(-u) from e^-u.
 template <int DT>
-__device__ __forceinline__ Sigmoid sigmoid(float u)
+__device__ __forceinline__ float sigmoid(float u, float &minus)
 {
-    float t, big, small;
+    float s;
     if (DT == ASR_BF16) {
-        t = __expf(-fabsf(u));
-        big = __fdividef(1.0f, __fadd_rn(1.0f, t));
-        small = __fmul_rn(t, big);
+        float e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(u, -kLog2e)));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(__fadd_rn(1.0f, e)));
+        minus = __fsub_rn(1.0f, s);             // what is lost near u = 25 is added to 1
     } else {
-        t = expf(-fabsf(u));
-        big = __fdiv_rn(1.0f, __fadd_rn(1.0f, t));
-        small = __fdiv_rn(t, __fadd_rn(1.0f, t));
+        const float e = expf(-u);
+        s = __frcp_rn(__fadd_rn(1.0f, e));
+        minus = e <= 3.402823466e38f ? __fmul_rn(e, s) : 1.0f;
     }
-    return u >= 0.0f ? Sigmoid{big, small} : u < 0.0f ? Sigmoid{small, big} : Sigmoid{u + big, u + big};
+    return s;
 }
 
 __device__ __forceinline__ float argument(float a, bool gelu)
@@ -57,56 +55,80 @@ __device__ __forceinline__ float argument(float a, bool gelu)
     return gelu ? __fmul_rn(kSlope, __fmaf_rn(__fmul_rn(__fmul_rn(a, a), a), kCube, a)) : a;
 }
 
-// f(a), and f'(a).  Where s(-u) is zero, so is what it multiplies, whatever the size.
 template <int DT>
 __device__ __forceinline__ float value(float a, bool gelu)
 {
-    return __fmul_rn(a, sigmoid<DT>(argument(a, gelu)).plus);
+    float minus;
+    return __fmul_rn(a, sigmoid<DT>(argument(a, gelu), minus));
 }
 
 template <int DT>
 __device__ __forceinline__ void value_and_slope(float a, bool gelu, float &f, float &df)
 {
-    const Sigmoid s = sigmoid<DT>(argument(a, gelu));
-    float r = a;                                // a u'
-    if (gelu) r = __fmul_rn(__fmul_rn(a, kSlope), __fmaf_rn(__fmul_rn(a, a), 3.0f * kCube, 1.0f));
-    f = __fmul_rn(a, s.plus);
-    df = s.minus == 0.0f ? s.plus : __fmul_rn(s.plus, __fmaf_rn(r, s.minus, 1.0f));
+    float minus;
+    const float s = sigmoid<DT>(argument(a, gelu), minus);
+    f = __fmul_rn(a, s);
+    // a u', finite: from |a| = 128 on s s(-u) is 0, as the product is whatever a
+    float r = fminf(fmaxf(a, -128.0f), 128.0f);
+    if (gelu) r = __fmul_rn(__fmul_rn(r, kSlope), __fmaf_rn(__fmul_rn(r, r), 3.0f * kCube, 1.0f));
+    df = __fmaf_rn(__fmul_rn(s, minus), r, s);
 }
 
-// KEEP: 0 nothing, 1 to nearest, 2 stochastically.  A warp a span of 256 columns
-// of y, gated, or 512, two units of eight values of x a lane either way.
+// The units of a lane and span: of x's two halves at one column, gated, or at two
+// columns 256 apart.
+template <bool GATED>
+struct Place {
+    uint64_t row, col[2];                       // of x
+    int live;                                   // of the first; gated, of both
+    int live1;
+    __device__ Place(const kept::Walk &k, uint64_t cols)
+    {
+        const uint64_t at = k.span * (GATED ? 256ull : 512ull) + (threadIdx.x & 31) * 8;
+        row = k.row;
+        col[0] = at;
+        col[1] = at + (GATED ? cols : 256);
+        live = k.more() ? live_of(cols, at) : 0;
+        live1 = GATED ? live : k.more() ? live_of(cols, at + 256) : 0;
+    }
+    __device__ int of(int u) const { return u ? live1 : live; }
+};
+
+// KEEP: 0 nothing, 1 to nearest, 2 stochastically.  The next span's values are
+// fetched before the current one's are worked on.
 template <int DT, bool GATED, int KEEP>
-__global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant__ Params P)
+__global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant__ Params P, uint32_t spans)
 {
-    constexpr int kUnits = GATED ? 1 : 2;
-    const uint32_t lane = threadIdx.x & 31;
-    const bool gelu = P.gelu;
-    muon::Walk k(P.rows, (P.cols + kUnits - 1) / kUnits, blockIdx.x * 8ull + (threadIdx.x >> 5), gridDim.x * 8ull);
-    for (; k.more(); k.next()) {
+    const bool gelu = P.gelu, vec1 = P.x.vec && (!GATED || P.cols % 8 == 0);
+    kept::Raw<DT> raw[2];
+    auto load = [&](const Place<GATED> &at) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            raw[u] = kept::fetch<DT>(P.x.p, at.row * P.x.ld + at.col[u], at.of(u), u ? vec1 : P.x.vec);
+    };
+    kept::Walk k(P.rows, spans);
+    Place<GATED> at(k, P.cols);
+    load(at);
+    while (k.more()) {
         float x[2][8];
-        uint64_t col[2];                        // of x
-        int live[2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const uint64_t c = k.span * (256ull * kUnits) + (GATED ? 0 : u * 256) + lane * 8;
-            live[u] = live_of(P.cols, c);
-            col[u] = GATED && u ? P.cols + c : c;
-            muon::load8(P.x.p, DT, k.row * P.x.ld + col[u], live[u], P.x.vec && (!GATED || !u || P.cols % 8 == 0), x[u]);
-        }
-        float y[2][8];
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                y[u][i] = value<DT>(x[u][i], gelu);
-                if (GATED) y[u][i] = __fmul_rn(y[u][i], x[1][i]);
-            }
-            kept::store8<DT>(P.y.p, k.row * P.y.ld + col[u], live[u], P.y.vec, y[u]);
-        }
+        for (int u = 0; u < 2; ++u) kept::values(raw[u], x[u]);
+        const Place<GATED> now = at;
+        k.next();
+        at = Place<GATED>(k, P.cols);
+        load(at);
         if (KEEP) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) kept::keep8<KEEP == 2>(P.to, k.row, col[u], live[u], x[u]);
+            for (int u = 0; u < 2; ++u) kept::keep8<KEEP == 2>(P.to, now.row, now.col[u], now.of(u), x[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < (GATED ? 1 : 2); ++u) {
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                y[i] = value<DT>(x[u][i], gelu);
+                if (GATED) y[i] = __fmul_rn(y[i], x[1][i]);
+            }
+            kept::store8<DT>(P.y.p, now.row * P.y.ld + now.col[u], now.of(u), P.y.vec, y);
         }
     }
 }
@@ -114,53 +136,58 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
 // KEPT: 0 from x, 1 from its codes, 2 from codes whose groups do not begin anew with
 // the gating half (cols not a multiple of 32).
 template <int DT, bool GATED, int KEPT>
-__global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constant__ Params P)
+__global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constant__ Params P, uint32_t spans)
 {
-    constexpr int kUnits = GATED ? 1 : 2;
-    const uint32_t lane = threadIdx.x & 31;
-    const bool gelu = P.gelu;
-    muon::Walk k(P.rows, (P.cols + kUnits - 1) / kUnits, blockIdx.x * 8ull + (threadIdx.x >> 5), gridDim.x * 8ull);
-    for (; k.more(); k.next()) {
-        float x[2][8], g[kUnits][8];
-        Codes c[2];
-        uint64_t col[2];
-        int live[2];
+    constexpr int kGrads = GATED ? 1 : 2;
+    const bool gelu = P.gelu, vec1 = P.x.vec && (!GATED || P.cols % 8 == 0);
+    kept::Raw<DT> raw[2], grad[kGrads];
+    Codes codes[2];
+    auto load = [&](const Place<GATED> &at) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const uint64_t at = k.span * (256ull * kUnits) + (GATED ? 0 : u * 256) + lane * 8;
-            live[u] = live_of(P.cols, at);
-            col[u] = GATED && u ? P.cols + at : at;
-            if (KEPT == 2 && u == 1) kept::values_across(P.from, k.row, col[u], live[u], x[u]);
-            else if (KEPT) c[u] = kept::fetch8(P.from, k.row, col[u], live[u]);
-            else muon::load8(P.x.p, DT, k.row * P.x.ld + col[u], live[u], P.x.vec && (!GATED || !u || P.cols % 8 == 0), x[u]);
-            if (u < kUnits) muon::load8(P.dy.p, DT, k.row * P.dy.ld + col[u], live[u], P.dy.vec, g[u]);
+            if (!KEPT) raw[u] = kept::fetch<DT>(P.x.p, at.row * P.x.ld + at.col[u], at.of(u), u ? vec1 : P.x.vec);
+            else if (KEPT == 1 || u == 0) codes[u] = kept::fetch_codes(P.from, at.row, at.col[u], at.of(u));
+            if (u < kGrads) grad[u] = kept::fetch<DT>(P.dy.p, at.row * P.dy.ld + at.col[u], at.of(u), P.dy.vec);
         }
-        if (KEPT) {
+    };
+    kept::Walk k(P.rows, spans);
+    Place<GATED> at(k, P.cols);
+    load(at);
+    while (k.more()) {
+        float x[2][8], g[kGrads][8];
+        const Place<GATED> now = at;
 #pragma unroll
-            for (int u = 0; u < (KEPT == 2 ? 1 : 2); ++u) kept::values8(c[u], x[u]);
+        for (int u = 0; u < 2; ++u) {
+            if (!KEPT) kept::values(raw[u], x[u]);
+            else if (KEPT == 1 || u == 0) kept::values(codes[u], x[u]);
+            else kept::values_across(P.from, now.row, now.col[u], now.of(u), x[u]);
+            if (u < kGrads) kept::values(grad[u], g[u]);
         }
+        k.next();
+        at = Place<GATED>(k, P.cols);
+        load(at);
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-            float da[8], db[8];
+        for (int u = 0; u < kGrads; ++u) {
+            float db[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float f, df;
                 value_and_slope<DT>(x[u][i], gelu, f, df);
-                da[i] = __fmul_rn(g[u][i], df);
                 if (GATED) {
-                    da[i] = __fmul_rn(da[i], x[1][i]);
                     db[i] = __fmul_rn(g[u][i], f);
+                    df = __fmul_rn(df, x[1][i]);
                 }
+                g[u][i] = __fmul_rn(g[u][i], df);
             }
-            kept::store8<DT>(P.dx.p, k.row * P.dx.ld + col[u], live[u], P.dx.vec, da);
-            if (GATED) kept::store8<DT>(P.dx.p, k.row * P.dx.ld + col[1], live[1], P.dx.vec && P.cols % 8 == 0, db);
+            kept::store8<DT>(P.dx.p, now.row * P.dx.ld + now.col[u], now.of(u), P.dx.vec, g[u]);
+            if (GATED) kept::store8<DT>(P.dx.p, now.row * P.dx.ld + now.col[1], now.of(1), P.dx.vec && P.cols % 8 == 0, db);
         }
     }
 }
 
 // ------------------------------------------------------------------ host
 
-using Kernel = void (*)(const Params);
+using Kernel = void (*)(const Params, uint32_t);
 
 template <int DT, bool GATED>
 Kernel forward_of(int keep)
@@ -211,10 +238,9 @@ asr_status kind_ok(int32_t dtype, uint32_t function)
     return kept::dtype_ok(dtype) && (function == ASR_SILU || function == ASR_GELU) ? ASR_OK : ASR_ERR_UNSUPPORTED_DTYPE;
 }
 
-unsigned blocks(uint64_t rows, uint64_t cols, bool gated)
+asr_status launch(Kernel kernel, const Params &P, uint32_t gated, cudaStream_t stream)
 {
-    const uint64_t span = gated ? 256 : 512;
-    return int8::blocks_for(rows * ((cols + span - 1) / span), 8, 1u << 20);
+    return kept::walk(ASR_KERNEL_ACTIVATION, kernel, P, P.rows, P.cols, gated ? 256 : 512, stream);
 }
 
 asr_status forward(const void *x, uint64_t x_ld, void *y, uint64_t y_ld, int32_t dtype, uint64_t rows, uint64_t cols,
@@ -245,8 +271,7 @@ asr_status forward(const void *x, uint64_t x_ld, void *y, uint64_t y_ld, int32_t
         P.to = kept::store(*to, width);
         keep = to->rounding == ASR_ROUND_SR ? 2 : 1;
     }
-    forward_of(dtype, gated != 0, keep)<<<blocks(rows, cols, gated != 0), kThreads, 0, stream>>>(P);
-    st = launched(ASR_KERNEL_ACTIVATION);
+    st = launch(forward_of(dtype, gated != 0, keep), P, gated, stream);
     if (st == ASR_OK && apart) st = kept::pack(x, dtype, rows, width, x_ld, to, stream);
     return st;
 }
@@ -275,8 +300,7 @@ asr_status backward(const void *dy, uint64_t dy_ld, const void *x, uint64_t x_ld
     P.cols = cols;
     P.gelu = function == ASR_GELU;
     const int codes = !from ? 0 : gated && cols % kept::kGroup != 0 ? 2 : 1;
-    backward_of(dtype, gated != 0, codes)<<<blocks(rows, cols, gated != 0), kThreads, 0, stream>>>(P);
-    return launched(ASR_KERNEL_ACTIVATION);
+    return launch(backward_of(dtype, gated != 0, codes), P, gated, stream);
 }
 
 }  // namespace act

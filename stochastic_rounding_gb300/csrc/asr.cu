@@ -888,33 +888,43 @@ asr_status asr_linear_int8_grads_workspace(uint64_t tokens, uint64_t n, uint64_t
 asr_status asr_checkpoint_int8(const void *x, int32_t x_dtype, uint64_t rows, uint64_t cols, uint64_t x_ld,
                                const asr_checkpoint *to, asr_stream_t stream)
 {
-    return kept::pack(x, x_dtype, rows, cols, x_ld, to, reinterpret_cast<cudaStream_t>(stream));
+    return guarded([&] {
+        return kept::pack(x, x_dtype, rows, cols, x_ld, to, reinterpret_cast<cudaStream_t>(stream));
+    });
 }
 
 asr_status asr_restore_int8(const asr_checkpoint *from, uint64_t rows, uint64_t cols, void *out, int32_t out_dtype,
                             uint64_t out_ld, asr_stream_t stream)
 {
-    return kept::unpack(from, rows, cols, out, out_dtype, out_ld, reinterpret_cast<cudaStream_t>(stream));
+    return guarded([&] {
+        return kept::unpack(from, rows, cols, out, out_dtype, out_ld, reinterpret_cast<cudaStream_t>(stream));
+    });
 }
 
 asr_status asr_activation(const void *x, uint64_t x_ld, void *y, uint64_t y_ld, int32_t dtype, uint64_t rows, uint64_t cols,
                           uint32_t function, uint32_t gated, const asr_checkpoint *keep, asr_stream_t stream)
 {
-    return act::forward(x, x_ld, y, y_ld, dtype, rows, cols, function, gated, keep, reinterpret_cast<cudaStream_t>(stream));
+    return guarded([&] {
+        return act::forward(x, x_ld, y, y_ld, dtype, rows, cols, function, gated, keep, reinterpret_cast<cudaStream_t>(stream));
+    });
 }
 
 asr_status asr_activation_grads(const void *dy, uint64_t dy_ld, const void *x, uint64_t x_ld, const asr_checkpoint *kept,
                                 void *dx, uint64_t dx_ld, int32_t dtype, uint64_t rows, uint64_t cols, uint32_t function,
                                 uint32_t gated, asr_stream_t stream)
 {
-    return act::backward(dy, dy_ld, x, x_ld, kept, dx, dx_ld, dtype, rows, cols, function, gated,
+    return guarded([&] {
+        return act::backward(dy, dy_ld, x, x_ld, kept, dx, dx_ld, dtype, rows, cols, function, gated,
                          reinterpret_cast<cudaStream_t>(stream));
+    });
 }
 
 asr_status asr_layer_norm(const asr_norm_params *params, const void *x, uint64_t x_ld, void *y, uint64_t y_ld, float *mean,
                           float *rstd, const asr_checkpoint *keep, asr_stream_t stream)
 {
-    return norm::forward(params, x, x_ld, y, y_ld, mean, rstd, keep, reinterpret_cast<cudaStream_t>(stream));
+    return guarded([&] {
+        return norm::forward(params, x, x_ld, y, y_ld, mean, rstd, keep, reinterpret_cast<cudaStream_t>(stream));
+    });
 }
 
 asr_status asr_layer_norm_grads(const asr_norm_params *params, const void *dy, uint64_t dy_ld, const void *x, uint64_t x_ld,
@@ -922,8 +932,10 @@ asr_status asr_layer_norm_grads(const asr_norm_params *params, const void *dy, u
                                 void *dweight, int32_t dweight_dtype, void *dbias, int32_t dbias_dtype, void *workspace,
                                 uint64_t workspace_bytes, asr_stream_t stream)
 {
-    return norm::backward(params, dy, dy_ld, x, x_ld, kept, mean, rstd, dx, dx_ld, dweight, dweight_dtype, dbias, dbias_dtype,
+    return guarded([&] {
+        return norm::backward(params, dy, dy_ld, x, x_ld, kept, mean, rstd, dx, dx_ld, dweight, dweight_dtype, dbias, dbias_dtype,
                           workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+    });
 }
 
 asr_status asr_layer_norm_grads_workspace(uint64_t rows, uint64_t cols, uint64_t *bytes)
@@ -937,8 +949,10 @@ asr_status asr_embedding(const void *ids, int32_t index, uint64_t tokens, const 
                          uint64_t vocab, uint64_t dim, double scale, void *y, uint64_t y_ld, int32_t dtype,
                          asr_stream_t stream)
 {
-    return embed::lookup(ids, index, tokens, table, table_ld, vocab, dim, scale, y, y_ld, dtype,
+    return guarded([&] {
+        return embed::lookup(ids, index, tokens, table, table_ld, vocab, dim, scale, y, y_ld, dtype,
                          reinterpret_cast<cudaStream_t>(stream));
+    });
 }
 
 asr_status asr_embedding_grads(const void *ids, int32_t index, uint64_t tokens, const void *dy, uint64_t dy_ld,

@@ -46,6 +46,99 @@ __device__ __forceinline__ int live_of(uint64_t cols, uint64_t col)
     return col >= cols ? 0 : cols - col < 8 ? static_cast<int>(cols - col) : 8;
 }
 
+// A matrix of f32 or bf16 values, rows `ld` apart.
+struct Matrix {
+    const void *p;
+    uint64_t ld;
+    uint32_t vec;                               // units of eight are 16-byte aligned
+};
+
+struct Out {
+    void *p;
+    uint64_t ld;
+    uint32_t vec;
+};
+
+// Eight values as they lie in memory, so that they can be fetched ahead of their use
+// in as few registers as they take there.
+template <int DT>
+struct Raw {
+    uint32_t w[DT == ASR_BF16 ? 4 : 8];
+};
+
+template <int DT>
+__device__ __forceinline__ Raw<DT> fetch(const void *src, uint64_t at, int live, bool vec)
+{
+    Raw<DT> r;
+    if (vec && live == 8) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(src) + at * (DT == ASR_BF16 ? 2 : 4));
+        const uint4 a = p[0];
+        r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+        if (DT == ASR_F32) {
+            const uint4 b = p[1];
+            r.w[DT == ASR_F32 ? 4 : 0] = b.x, r.w[DT == ASR_F32 ? 5 : 0] = b.y;
+            r.w[DT == ASR_F32 ? 6 : 0] = b.z, r.w[DT == ASR_F32 ? 7 : 0] = b.w;
+        }
+    } else if (DT == ASR_BF16) {
+        const uint16_t *p = static_cast<const uint16_t *>(src) + at;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r.w[i] = (2 * i < live ? p[2 * i] : 0u) | (2 * i + 1 < live ? static_cast<uint32_t>(p[2 * i + 1]) << 16 : 0u);
+    } else {
+        const uint32_t *p = static_cast<const uint32_t *>(src) + at;
+#pragma unroll
+        for (int i = 0; i < (DT == ASR_F32 ? 8 : 0); ++i) r.w[i] = i < live ? p[i] : 0u;
+    }
+    return r;
+}
+
+template <int DT>
+__device__ __forceinline__ void values(const Raw<DT> &r, float x[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        x[i] = DT == ASR_F32 ? __uint_as_float(r.w[DT == ASR_F32 ? i : 0])
+                             : (i & 1) ? bf16_hi(r.w[DT == ASR_F32 ? 0 : i >> 1]) : bf16_lo(r.w[DT == ASR_F32 ? 0 : i >> 1]);
+}
+
+// A warp's way through a matrix in spans of kSpan columns: span `at` counted along
+// the rows, then every `stride`-th.  Both are counts of a launch's warps.
+constexpr int kUnits = 2;                       // of eight values, a lane and span
+constexpr int kSpan = 256 * kUnits;
+
+struct Walk {
+    uint64_t row, rows;
+    uint32_t span, spans, drow, dspan;
+    __device__ Walk(uint64_t rows_, uint32_t spans_)
+    {
+        const uint32_t at = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), stride = gridDim.x * (kThreads / 32);
+        rows = rows_;
+        spans = spans_;
+        row = at / spans;
+        span = at % spans;
+        drow = stride / spans;
+        dspan = stride % spans;
+    }
+    __device__ bool more() const { return row < rows; }
+    __device__ void next()
+    {
+        row += drow;
+        span += dspan;
+        if (span >= spans) {
+            span -= spans;
+            ++row;
+        }
+    }
+};
+
+// The larger magnitude, NaN where one of them is.
+__device__ __forceinline__ float most(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return d;
+}
+
 // e + 127 for the bits of a largest value, 127 being 1.984375 * 2^6.
 __device__ __forceinline__ uint32_t power_of(uint32_t top)
 {
@@ -60,15 +153,19 @@ __device__ __forceinline__ float scale_of(uint32_t b)
 
 // Eight values of a row from `col` on, a multiple of 8, of which `live` are the
 // row's.  All lanes of a warp call this together; four in a row hold a group.
+//
+// To nearest: x 2^-e + 1.5 * 2^23, rounded once, has q in its low byte.
+// Stochastically: q = ceil(y - r / 65536), which is floor(y), or one more where the
+// fraction is above r / 65536.  128 + r / 65536 is a binary32 number with r for its
+// low bits; taken from y and rounded up, the difference keeps its ceiling, -128 away
+// (whole numbers are representable), and 1.5 * 2^23 + 128 more, rounded up, is it.
 template <bool SR>
 __device__ __forceinline__ void keep8(const Store &S, uint64_t row, uint64_t col, int live, const float x[8])
 {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-    const uint32_t b = power_of(top);
+    float m = most(most(most(x[0], x[1]), most(x[2], x[3])), most(most(x[4], x[5]), most(x[6], x[7])));
+    m = most(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = most(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    const uint32_t b = power_of(__float_as_uint(m));
     const float up = __uint_as_float((254u - b) << 23);
     uint32_t c[8], w[4];
     if (SR) {
@@ -77,18 +174,15 @@ __device__ __forceinline__ void keep8(const Store &S, uint64_t row, uint64_t col
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float y = __fmul_rn(x[i], up);
         if (SR) {
-            // the high half of ceil(65536 y) + 65535 - r; |y| <= 127, so the sum stays below 128 * 65536
-            const uint32_t not_r = (i & 1) ? ~w[i >> 1] >> 16 : ~w[i >> 1] & 0xFFFFu;
-            c[i] = static_cast<uint32_t>(__float2int_ru(__fmul_rn(y, 65536.0f))) + not_r;
+            const float r = __uint_as_float(__byte_perm(w[i >> 1], 0x43000000u, (i & 1) ? 0x7632 : 0x7610));
+            c[i] = __float_as_uint(__fadd_ru(__fmaf_ru(x[i], up, -r), 12583040.0f));
         } else {
-            c[i] = __float_as_uint(__fadd_rn(y, 12582912.0f));      // its low byte
+            c[i] = __float_as_uint(__fmaf_rn(x[i], up, 12582912.0f));
         }
     }
-    constexpr uint32_t kPick = SR ? 0x0062 : 0x0040;
-    uint2 v = make_uint2(__byte_perm(__byte_perm(c[0], c[1], kPick), __byte_perm(c[2], c[3], kPick), 0x5410),
-                         __byte_perm(__byte_perm(c[4], c[5], kPick), __byte_perm(c[6], c[7], kPick), 0x5410));
+    uint2 v = make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
+                         __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
     if (b == 255u) v = make_uint2(0, 0);
     int8_t *q = S.q + row * S.q_ld + col;
     if (live == 8 && S.vec) {
@@ -101,13 +195,13 @@ __device__ __forceinline__ void keep8(const Store &S, uint64_t row, uint64_t col
     if (live > 0 && (threadIdx.x & 3) == 0) S.power[row * S.power_ld + (col >> 5)] = static_cast<uint8_t>(b);
 }
 
-// Codes and scale of eight values, to be loaded ahead of their use.
+// Codes and power of eight values, to be fetched ahead of their use.
 struct Codes {
     uint2 v;
     uint32_t b;
 };
 
-__device__ __forceinline__ Codes fetch8(const Source &S, uint64_t row, uint64_t col, int live)
+__device__ __forceinline__ Codes fetch_codes(const Source &S, uint64_t row, uint64_t col, int live)
 {
     Codes c{make_uint2(0, 0), 0};
     if (live <= 0) return c;
@@ -123,14 +217,22 @@ __device__ __forceinline__ Codes fetch8(const Source &S, uint64_t row, uint64_t 
     return c;
 }
 
-__device__ __forceinline__ void values8(const Codes &c, float x[8])
+// 2^7 + (128 + q) 2^-16 has a code for its low byte: times 2^16 2^e, less a constant
+// times that, it is q 2^e, exactly.  The constant's product leaves binary32 above
+// e = 104, where values are that large a number of times 2^7.
+__device__ __forceinline__ void values(const Codes &c, float x[8])
 {
-    const float scale = scale_of(c.b);
     const uint32_t lo = c.v.x ^ 0x80808080u, hi = c.v.y ^ 0x80808080u;
+    const float scale = scale_of(c.b);
+    const bool large = c.b > 220u && c.b < 255u;
+    const float by = large ? 65536.0f : __fmul_rn(scale, 65536.0f), less = __fmul_rn(-128.001953125f, by);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)     // 2^23 + 128 + q
-        x[i] = __fmul_rn(__fsub_rn(__uint_as_float(__byte_perm(i < 4 ? lo : hi, 0x4B000000u, 0x7440 + (i & 3))),
-                                   8388736.0f), scale);
+    for (int i = 0; i < 8; ++i)
+        x[i] = __fmaf_rn(__uint_as_float(__byte_perm(i < 4 ? lo : hi, 0x43000000u, 0x7650 + (i & 3))), by, less);
+    if (large) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(x[i], scale);
+    }
 }
 
 // Eight values from any column on, whose group may end among them.
@@ -174,43 +276,39 @@ __device__ __forceinline__ void store8(void *dst, uint64_t at, int live, bool ve
     }
 }
 
-// A matrix of f32 or bf16 values, rows `ld` apart.
-struct Matrix {
-    const void *p;
-    uint64_t ld;
-    uint32_t vec;                               // units of eight are 16-byte aligned
-};
-
-struct Out {
-    void *p;
-    uint64_t ld;
-    uint32_t vec;
-};
-
 struct PackParams {
     Matrix x;
     uint64_t rows, cols;
     Store to;
 };
 
-// A warp a span of 512 columns, two units of eight a lane.
+// The next span's values are fetched before the current one's are worked on.
 template <bool SR, int DT>
-__global__ void __launch_bounds__(kThreads) pack_kernel(const __grid_constant__ PackParams P)
+__global__ void __launch_bounds__(kThreads) pack_kernel(const __grid_constant__ PackParams P, uint32_t spans)
 {
     const uint32_t lane = threadIdx.x & 31;
-    muon::Walk k(P.rows, (P.cols + 1) / 2, blockIdx.x * 8ull + (threadIdx.x >> 5), gridDim.x * 8ull);
-    for (; k.more(); k.next()) {
-        float x[2][8];
-        int live[2];
-        uint64_t col[2];
+    Raw<DT> x[kUnits];
+    auto load = [&](const Walk &k) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            col[u] = k.span * 512ull + u * 256 + lane * 8;
-            live[u] = live_of(P.cols, col[u]);
-            muon::load8(P.x.p, DT, k.row * P.x.ld + col[u], live[u], P.x.vec, x[u]);
+        for (int u = 0; u < kUnits; ++u) {
+            const uint64_t col = k.span * static_cast<uint64_t>(kSpan) + u * 256 + lane * 8;
+            x[u] = fetch<DT>(P.x.p, k.row * P.x.ld + col, k.more() ? live_of(P.cols, col) : 0, P.x.vec);
         }
+    };
+    Walk k(P.rows, spans);
+    load(k);
+    while (k.more()) {
+        float v[kUnits][8];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) keep8<SR>(P.to, k.row, col[u], live[u], x[u]);
+        for (int u = 0; u < kUnits; ++u) values(x[u], v[u]);
+        const Walk now = k;
+        k.next();
+        load(k);
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            const uint64_t col = now.span * static_cast<uint64_t>(kSpan) + u * 256 + lane * 8;
+            keep8<SR>(P.to, now.row, col, live_of(P.cols, col), v[u]);
+        }
     }
 }
 
@@ -221,25 +319,30 @@ struct UnpackParams {
 };
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads) unpack_kernel(const __grid_constant__ UnpackParams P)
+__global__ void __launch_bounds__(kThreads) unpack_kernel(const __grid_constant__ UnpackParams P, uint32_t spans)
 {
     const uint32_t lane = threadIdx.x & 31;
-    muon::Walk k(P.rows, (P.cols + 1) / 2, blockIdx.x * 8ull + (threadIdx.x >> 5), gridDim.x * 8ull);
-    for (; k.more(); k.next()) {
-        Codes c[2];
-        int live[2];
-        uint64_t col[2];
+    Codes c[kUnits];
+    auto load = [&](const Walk &k) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            col[u] = k.span * 512ull + u * 256 + lane * 8;
-            live[u] = live_of(P.cols, col[u]);
-            c[u] = fetch8(P.from, k.row, col[u], live[u]);
+        for (int u = 0; u < kUnits; ++u) {
+            const uint64_t col = k.span * static_cast<uint64_t>(kSpan) + u * 256 + lane * 8;
+            c[u] = fetch_codes(P.from, k.row, col, k.more() ? live_of(P.cols, col) : 0);
         }
+    };
+    Walk k(P.rows, spans);
+    load(k);
+    while (k.more()) {
+        float v[kUnits][8];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            float v[8];
-            values8(c[u], v);
-            store8<DT>(P.out.p, k.row * P.out.ld + col[u], live[u], P.out.vec, v);
+        for (int u = 0; u < kUnits; ++u) values(c[u], v[u]);
+        const Walk now = k;
+        k.next();
+        load(k);
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            const uint64_t col = now.span * static_cast<uint64_t>(kSpan) + u * 256 + lane * 8;
+            store8<DT>(P.out.p, now.row * P.out.ld + col, live_of(P.cols, col), P.out.vec, v[u]);
         }
     }
 }
@@ -315,10 +418,40 @@ asr_status load_once(std::atomic<uint64_t> &ready, K... kernels)
     return ASR_OK;
 }
 
-// Blocks of eight warps for spans of 512 columns.
-unsigned span_blocks(uint64_t rows, uint64_t cols)
+// How many blocks of a kernel the current device holds at once.
+template <typename K>
+asr_status resident(K kernel, int threads, size_t smem, int *blocks)
 {
-    return int8::blocks_for(rows * ((cols + 511) / 512), 8, 1u << 20);
+    int dev = 0, sms = 0, per_sm = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    const uint64_t key = (static_cast<uint64_t>(dev) << 48) ^ reinterpret_cast<uintptr_t>(kernel) ^
+                         (static_cast<uint64_t>(threads / 32) << 54);
+    std::lock_guard<std::mutex> lk(g_grid_mu);
+    auto it = g_grid_cache.find(key);
+    if (it != g_grid_cache.end()) {
+        *blocks = it->second;
+        return ASR_OK;
+    }
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
+    if (e != cudaSuccess) return cuda_fail(e);
+    *blocks = sms * (per_sm < 1 ? 1 : per_sm);
+    g_grid_cache[key] = *blocks;
+    return ASR_OK;
+}
+
+// A launch of blocks of eight warps that walk over `count` spans.
+template <typename K, typename P>
+asr_status walk(int kind, K kernel, const P &params, uint64_t rows, uint64_t cols, uint64_t span, cudaStream_t stream)
+{
+    int most = 0;
+    const asr_status st = resident(kernel, kThreads, 0, &most);
+    if (st != ASR_OK) return st;
+    const uint64_t spans = (cols + span - 1) / span;
+    kernel<<<int8::blocks_for(rows * spans, kThreads / 32, static_cast<uint64_t>(most)), kThreads, 0, stream>>>(
+        params, static_cast<uint32_t>(spans));
+    return launched(kind);
 }
 
 asr_status setup()
@@ -347,8 +480,7 @@ asr_status pack(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, uint
     const bool sr = to->rounding == ASR_ROUND_SR, bf = dtype == ASR_BF16;
     auto kernel = sr ? (bf ? pack_kernel<true, ASR_BF16> : pack_kernel<true, ASR_F32>)
                      : (bf ? pack_kernel<false, ASR_BF16> : pack_kernel<false, ASR_F32>);
-    kernel<<<span_blocks(rows, cols), kThreads, 0, stream>>>(P);
-    return launched(ASR_KERNEL_CHECKPOINT);
+    return walk(ASR_KERNEL_CHECKPOINT, kernel, P, rows, cols, kSpan, stream);
 }
 
 asr_status unpack(const asr_checkpoint *from, uint64_t rows, uint64_t cols, void *dst, int32_t dtype, uint64_t ld,
@@ -367,8 +499,7 @@ asr_status unpack(const asr_checkpoint *from, uint64_t rows, uint64_t cols, void
     P.rows = rows;
     P.cols = cols;
     auto kernel = dtype == ASR_BF16 ? unpack_kernel<ASR_BF16> : unpack_kernel<ASR_F32>;
-    kernel<<<span_blocks(rows, cols), kThreads, 0, stream>>>(P);
-    return launched(ASR_KERNEL_CHECKPOINT);
+    return walk(ASR_KERNEL_CHECKPOINT, kernel, P, rows, cols, kSpan, stream);
 }
 
 }  // namespace kept

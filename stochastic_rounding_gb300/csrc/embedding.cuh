@@ -62,29 +62,27 @@ struct LookupParams {
     float scale;
 };
 
-// A warp a span of 512 columns of a token's row.
 template <int DT>
-__global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant__ LookupParams P)
+__global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant__ LookupParams P, uint32_t spans)
 {
     const uint32_t lane = threadIdx.x & 31;
-    muon::Walk k(P.ids.n, (P.dim + 1) / 2, blockIdx.x * 8ull + (threadIdx.x >> 5), gridDim.x * 8ull);
-    for (; k.more(); k.next()) {
+    for (kept::Walk k(P.ids.n, spans); k.more(); k.next()) {
         const uint32_t id = key_of(P.ids, k.row);
-        float v[2][8];
-        uint64_t col[2];
-        int live[2];
+        kept::Raw<DT> raw[kept::kUnits];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            col[u] = k.span * 512ull + u * 256 + lane * 8;
-            live[u] = live_of(P.dim, col[u]);
-            muon::load8(P.table.p, DT, id * P.table.ld + col[u], id < P.ids.vocab ? live[u] : 0, P.table.vec, v[u]);
+        for (int u = 0; u < kept::kUnits; ++u) {
+            const uint64_t col = k.span * static_cast<uint64_t>(kept::kSpan) + u * 256 + lane * 8;
+            raw[u] = kept::fetch<DT>(P.table.p, id * P.table.ld + col, id < P.ids.vocab ? live_of(P.dim, col) : 0, P.table.vec);
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < kept::kUnits; ++u) {
+            const uint64_t col = k.span * static_cast<uint64_t>(kept::kSpan) + u * 256 + lane * 8;
+            float v[8];
+            kept::values(raw[u], v);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                v[u][i] = id < P.ids.vocab ? __fmul_rn(v[u][i], P.scale) : __uint_as_float(0x7FC00000u);
-            kept::store8<DT>(P.y.p, k.row * P.y.ld + col[u], live[u], P.y.vec, v[u]);
+                v[i] = id < P.ids.vocab ? __fmul_rn(v[i], P.scale) : __uint_as_float(0x7FC00000u);
+            kept::store8<DT>(P.y.p, k.row * P.y.ld + col, live_of(P.dim, col), P.y.vec, v);
         }
     }
 }
@@ -525,8 +523,7 @@ asr_status lookup(const void *ids, int32_t index, uint64_t tokens, const void *t
     P.dim = dim;
     P.scale = static_cast<float>(scale);
     auto kernel = dtype == ASR_BF16 ? lookup_kernel<ASR_BF16> : lookup_kernel<ASR_F32>;
-    kernel<<<kept::span_blocks(tokens, dim), kThreads, 0, stream>>>(P);
-    return launched(ASR_KERNEL_EMBEDDING);
+    return kept::walk(ASR_KERNEL_EMBEDDING, kernel, P, tokens, dim, kept::kSpan, stream);
 }
 
 // Chunks of eight tokens, longer where there would be more than 4,096 of them: what

@@ -7,12 +7,18 @@
 //   g = dy w;   dx = rstd (g - [sum g / n] - h sum (g h) / n)
 //   dw = sum over rows of dy h;   db = sum over rows of dy
 //
-// A row is held in registers, 16 values a thread, by a warp or by a block, so it is
-// read once.  Its sums: each warp's own mean and its squares about that, then the
-// warps' joined (the squares of a warp's mean about the row's added), so nothing
-// cancels.  The backward kernel's blocks walk over rows and keep their columns'
-// sums for dw and db in registers; a second kernel adds the blocks' sums up, in one
-// order.  Rows that do not fit a block of 1,024 threads are read anew for each sum.
+// A row is held in registers, 16 values a thread, so it is read once: by 4 to 32
+// lanes where it has up to 512 values, else by a block.  Its sums: each warp's own
+// mean and its squares about that, then the warps' joined (the squares of a warp's
+// mean about the row's added), so nothing cancels.  Blocks walk over rows, the next
+// row's values fetched before the current one's are worked on.
+//
+// The backward kernel keeps its columns' sums for dw and db in registers (up to 608
+// blocks leave theirs, and a second kernel adds them up, in one order), which leaves
+// too few warps to hide memory behind: each thread copies its own values of the next
+// rows into shared memory, asynchronously, and reads them back itself, so the ring
+// needs no barrier.  Rows that do not fit a block of 1,024 threads are read anew for
+// each sum.
 
 namespace norm {
 
@@ -21,7 +27,7 @@ using kept::live_of;
 constexpr int kUnits = 2;                       // of eight values, a thread
 constexpr uint64_t kWarpCols = 32 * 8 * kUnits; // a warp's row at most
 constexpr uint64_t kBlockCols = 1024 * 8 * kUnits;
-constexpr int kWarpThreads = 256;               // eight rows a block where a warp has one
+constexpr int kWarpThreads = 256;               // where lanes have rows
 
 struct Params {
     kept::Matrix x, dy;
@@ -33,16 +39,25 @@ struct Params {
     uint32_t w_dtype, b_dtype, w_vec, b_vec;
     uint32_t centred;
     uint32_t sr;
+    uint32_t lanes;                             // of a row, where lanes have rows
     kept::Store to;
     kept::Source from;
-    float *partial;                             // backward: [groups of threads][2][cols]
-    uint32_t sums;                              // whether it is wanted
+    float *partial;                             // backward: [blocks][dw, db][pitch]
+    uint64_t pitch;                             // cols up to a multiple of eight
+    uint32_t dw, db;                            // which are wanted
 };
 
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
     for (int d = 16; d; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+    return v;
+}
+
+// Over `lanes` neighbours, a power of two.
+__device__ __forceinline__ float lane_sum(float v, uint32_t lanes)
+{
+    for (uint32_t d = lanes / 2; d; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
     return v;
 }
 
@@ -58,129 +73,149 @@ __device__ __forceinline__ void params8(const void *p, uint32_t dtype, uint64_t 
     }
 }
 
-// A row's place: a warp's, or a block's.
+// Which rows a thread works on, and which values of them.  All threads of a warp make
+// the same number of steps; `row` may lie past the last row.
 template <bool WARP>
 struct Place {
-    uint64_t first, stride, group;              // rows; which group of threads this is
-    uint32_t at, threads;                       // within the group
-    __device__ Place()
+    uint64_t base, stride, col[kUnits];
+    uint32_t sub, at;                           // row of a step; place in the row's threads
+    int live[kUnits];
+    __device__ explicit Place(const Params &P)
     {
+        uint32_t threads;
         if (WARP) {
-            group = blockIdx.x * static_cast<uint64_t>(kWarpThreads / 32) + (threadIdx.x >> 5);
-            stride = gridDim.x * static_cast<uint64_t>(kWarpThreads / 32);
-            at = threadIdx.x & 31;
-            threads = 32;
+            const uint32_t lane = threadIdx.x & 31, rows = 32 / P.lanes;
+            base = (blockIdx.x * static_cast<uint64_t>(kWarpThreads / 32) + (threadIdx.x >> 5)) * rows;
+            stride = gridDim.x * static_cast<uint64_t>(kWarpThreads / 32) * rows;
+            sub = lane / P.lanes;
+            at = lane % P.lanes;
+            threads = P.lanes;
         } else {
-            group = blockIdx.x;
+            base = blockIdx.x;
             stride = gridDim.x;
+            sub = 0;
             at = threadIdx.x;
             threads = blockDim.x;
         }
-        first = group;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            col[u] = (static_cast<uint64_t>(u) * threads + at) * 8;
+            live[u] = live_of(P.cols, col[u]);
+        }
     }
+    __device__ uint64_t row() const { return base + sub; }
+    __device__ int of(int u, uint64_t row, uint64_t rows) const { return row < rows ? live[u] : 0; }
 };
 
-// The values' places in a row, for one thread.
-struct Unit {
-    uint64_t col[kUnits];
-    int live[kUnits];
+// Sums of a block's warps: `part` holds theirs, `turn` says which half of it this row
+// uses, so that one barrier a row is enough.
+struct Parts {
+    float2 v[2][32];
 };
 
-__device__ __forceinline__ Unit units_of(uint32_t at, uint32_t threads, uint64_t cols)
+__device__ __forceinline__ float2 exchange(Parts &parts, uint32_t turn, float2 mine)
 {
-    Unit U;
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-        U.col[u] = (static_cast<uint64_t>(u) * threads + at) * 8;
-        U.live[u] = live_of(cols, U.col[u]);
-    }
-    return U;
-}
-
-// How many of a row's values the caller's warp holds.
-__device__ __forceinline__ float warp_count(const Unit &U)
-{
-    int n = 0;
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) n += U.live[u];
-    return static_cast<float>(__reduce_add_sync(0xFFFFFFFFu, n));
-}
-
-// The row's mean and sum of squares about it from each warp's; `part` is used by
-// turns, so that one barrier a row is enough.
-template <bool WARP>
-__device__ __forceinline__ void join_moments(float sum, float squares, float count, const Params &P, float3 *part,
-                                             float &mean, float &total)
-{
-    // `sum`, `squares`: of the warp; the squares about its own mean (centred), or about zero
-    if (WARP) {
-        mean = P.centred ? __fmul_rn(sum, P.over_n) : 0.0f;
-        total = squares;
-        return;
-    }
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    if (lane == 0) part[warp] = make_float3(sum, squares, count);
+    const uint32_t lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (lane == 0) parts.v[turn][threadIdx.x >> 5] = mine;
     __syncthreads();
-    const float3 p = lane < warps ? part[lane] : make_float3(0.0f, 0.0f, 0.0f);
-    mean = P.centred ? __fmul_rn(warp_sum(p.x), P.over_n) : 0.0f;
-    float q = p.y;
-    if (P.centred && p.z > 0.0f) {
-        const float d = __fsub_rn(__fdiv_rn(p.x, p.z), mean);
-        q = __fmaf_rn(__fmul_rn(d, d), p.z, q);
-    }
-    total = warp_sum(q);
+    return lane < warps ? parts.v[turn][lane] : make_float2(0.0f, 0.0f);
+}
+
+// How many of a row's values warp `lane` of the block holds.
+__device__ __forceinline__ float count_of(uint64_t cols)
+{
+    const uint64_t first = (threadIdx.x & 31) * 256ull;
+    float n = 0.0f;
+    if ((threadIdx.x & 31) < blockDim.x >> 5)
+        for (int u = 0; u < kUnits; ++u) {
+            const uint64_t col = first + u * blockDim.x * 8ull;
+            n += col >= cols ? 0.0f : static_cast<float>(cols - col < 256 ? cols - col : 256);
+        }
+    return n;
 }
 
 template <int DT, bool WARP, bool KEEP>
 __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) forward_kernel(const __grid_constant__ Params P)
 {
-    __shared__ float3 part[2][32];
-    const Place<WARP> at;
-    const Unit U = units_of(at.at, at.threads, P.cols);
-    const float count = warp_count(U);
-    uint32_t turn = 0;
-    for (uint64_t row = at.first; row < P.rows; row += at.stride, turn ^= 1) {
-        float x[kUnits][8], sum = 0.0f, squares = 0.0f;
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-            muon::load8(P.x.p, DT, row * P.x.ld + U.col[u], U.live[u], P.x.vec, x[u]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum = __fadd_rn(sum, x[u][i]);
-        }
-        float middle = 0.0f;
-        if (P.centred) {
-            sum = warp_sum(sum);
-            middle = count > 0.0f ? __fdiv_rn(sum, count) : 0.0f;
-        }
+    __shared__ Parts parts;
+    Place<WARP> at(P);
+    float counts = 0.0f, own = 0.0f;            // of warp `lane`, of the caller's
+    if (!WARP) {
+        counts = count_of(P.cols);
+        own = __shfl_sync(0xFFFFFFFFu, counts, threadIdx.x >> 5);
+    }
+    const float over_own = own > 0.0f ? __frcp_rn(own) : 0.0f;
+    kept::Raw<DT> raw[kUnits];
+    auto load = [&]() {
 #pragma unroll
         for (int u = 0; u < kUnits; ++u)
+            raw[u] = kept::fetch<DT>(P.x.p, at.row() * P.x.ld + at.col[u], at.of(u, at.row(), P.rows), P.x.vec);
+    };
+    load();
+    for (uint32_t turn = 0; at.base < P.rows; turn ^= 1) {
+        const uint64_t row = at.row();
+        float x[kUnits][8], sum = 0.0f, squares = 0.0f, mean = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float d = i < U.live[u] ? __fsub_rn(x[u][i], middle) : 0.0f;
-                squares = __fmaf_rn(d, d, squares);
+        for (int u = 0; u < kUnits; ++u) kept::values(raw[u], x[u]);
+        at.base += at.stride;
+        load();
+        if (P.centred) {
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum = __fadd_rn(sum, x[u][i]);
+            sum = WARP ? lane_sum(sum, P.lanes) : warp_sum(sum);
+            mean = __fmul_rn(sum, WARP ? P.over_n : over_own);
+        }
+        if (P.centred) {
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float d = i < at.live[u] ? __fsub_rn(x[u][i], mean) : 0.0f;
+                    squares = __fmaf_rn(d, d, squares);
+                }
+        } else {
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) squares = __fmaf_rn(x[u][i], x[u][i], squares);
+        }
+        squares = WARP ? lane_sum(squares, P.lanes) : warp_sum(squares);
+        if (!WARP) {
+            const float2 p = exchange(parts, turn, make_float2(sum, squares));
+            squares = p.y;
+            if (P.centred) {
+                mean = __fmul_rn(warp_sum(p.x), P.over_n);
+                const float d = counts > 0.0f ? __fsub_rn(__fdiv_rn(p.x, counts), mean) : 0.0f;
+                squares = __fmaf_rn(__fmul_rn(d, d), counts, squares);
             }
-        squares = warp_sum(squares);
-        float mean, total;
-        join_moments<WARP>(sum, squares, count, P, part[turn], mean, total);
-        const float rstd = __frsqrt_rn(__fmaf_rn(total, P.over_n, P.eps));
-        if (at.at == 0 && P.rstd) {
+            squares = warp_sum(squares);
+        }
+        const float rstd = __frsqrt_rn(__fmaf_rn(squares, P.over_n, P.eps));
+        if (at.at == 0 && P.rstd && row < P.rows) {
             P.rstd[row] = rstd;
             if (P.mean) P.mean[row] = mean;
         }
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
+            const int live = at.of(u, row, P.rows);
             if (KEEP) {
-                if (P.sr) kept::keep8<true>(P.to, row, U.col[u], U.live[u], x[u]);
-                else kept::keep8<false>(P.to, row, U.col[u], U.live[u], x[u]);
+                if (P.sr) kept::keep8<true>(P.to, row, at.col[u], live, x[u]);
+                else kept::keep8<false>(P.to, row, at.col[u], live, x[u]);
             }
-            if (U.live[u] == 0) continue;
+            if (live == 0) continue;
             float w[8], b[8];
-            params8(P.w, P.w_dtype, U.col[u], U.live[u], P.w_vec, 1.0f, w);
-            params8(P.b, P.b_dtype, U.col[u], U.live[u], P.b_vec, 0.0f, b);
+            params8(P.w, P.w_dtype, at.col[u], live, P.w_vec, 1.0f, w);
+            if (P.b) {
+                muon::load8(P.b, P.b_dtype, at.col[u], live, P.b_vec, b);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                x[u][i] = __fmaf_rn(__fmul_rn(__fsub_rn(x[u][i], mean), rstd), w[i], b[i]);
-            kept::store8<DT>(P.y.p, row * P.y.ld + U.col[u], U.live[u], P.y.vec, x[u]);
+                for (int i = 0; i < 8; ++i) x[u][i] = __fmaf_rn(__fmul_rn(__fsub_rn(x[u][i], mean), rstd), w[i], b[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[u][i] = __fmul_rn(__fmul_rn(__fsub_rn(x[u][i], mean), rstd), w[i]);
+            }
+            kept::store8<DT>(P.y.p, row * P.y.ld + at.col[u], live, P.y.vec, x[u]);
         }
     }
 }
@@ -250,71 +285,223 @@ __global__ void __launch_bounds__(kLongThreads) forward_long_kernel(const __grid
 template <int DT, bool KEPT>
 __device__ __forceinline__ void input8(const Params &P, uint64_t row, uint64_t col, int live, float x[8])
 {
-    if (KEPT) kept::values8(kept::fetch8(P.from, row, col, live), x);
+    if (KEPT) kept::values(kept::fetch_codes(P.from, row, col, live), x);
     else muon::load8(P.x.p, DT, row * P.x.ld + col, live, P.x.vec, x);
 }
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *to, const void *from)
+{
+    if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(to)), "l"(from), "n"(BYTES) : "memory");
+}
+
+// Eight values of a matrix, from memory to a thread's place in shared memory (words
+// `step` apart for 16 bytes each): asynchronously, in 16 bytes or, off alignment, f32
+// by one; bf16 off alignment at once.
+template <int DT>
+__device__ __forceinline__ void bring(uint4 *to, uint32_t step, const kept::Matrix &M, uint64_t at, int live)
+{
+    constexpr int kWords = DT == ASR_BF16 ? 1 : 2;
+    const char *from = static_cast<const char *>(M.p) + at * (DT == ASR_BF16 ? 2 : 4);
+    if (M.vec && live == 8) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) copy_async<16>(to + i * step, from + 16 * i);
+    } else if (DT == ASR_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t *w = reinterpret_cast<uint32_t *>(to + (i >> 2) * step) + (i & 3);
+            if (i < live) copy_async<4>(w, from + 4 * i);
+            else *w = 0;
+        }
+    } else {
+        const kept::Raw<DT> r = kept::fetch<DT>(M.p, at, live, false);
+        to[0] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void taken(const uint4 *from, uint32_t step, float x[8])
+{
+    kept::Raw<DT> r;
+#pragma unroll
+    for (int i = 0; i < (DT == ASR_BF16 ? 1 : 2); ++i) {
+        const uint4 v = from[i * step];
+        r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
+    }
+    kept::values(r, x);
+}
+
+// A thread's share of a stage, in words of 16 bytes: dy, then x or its codes.
+template <int DT, bool KEPT>
+struct Stage {
+    static constexpr int kDy = (DT == ASR_BF16 ? 1 : 2) * kUnits;
+    static constexpr int kX = KEPT ? 1 : kDy;               // codes: 8 bytes a unit
+    static constexpr int kWords = kDy + kX;
+};
+static_assert(kUnits == 2, "codes of two units fill a word");
+
+// Stages of the ring: four, fewer where a block's values and weight would not leave
+// room (227 KB) for them, or for a second block of up to 256 threads.
+template <int DT, bool KEPT, int THREADS>
+struct Ring {
+    static constexpr int kRoom = (THREADS <= 256 ? 110 : 220) * 1024 - THREADS * 64;
+    static constexpr int kFit = kRoom / (THREADS * Stage<DT, KEPT>::kWords * 16);
+    static constexpr int kStages = kFit < 1 ? 1 : kFit > 4 ? 4 : kFit;
+    static size_t bytes(unsigned threads) { return (static_cast<size_t>(kStages) * Stage<DT, KEPT>::kWords + 4) * 16 * threads; }
+};
 
 template <int DT, bool WARP, bool KEPT, int THREADS>
 __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant__ Params P)
 {
-    __shared__ float2 part[2][32];
-    const Place<WARP> at;
-    const Unit U = units_of(at.at, at.threads, P.cols);
-    float dw[kUnits][8] = {}, db[kUnits][8] = {};
-    uint32_t turn = 0;
-    for (uint64_t row = at.first; row < P.rows; row += at.stride, turn ^= 1) {
-        float h[kUnits][8], g[kUnits][8], along = 0.0f, sum = 0.0f;
-        const float mean = P.centred ? P.mean[row] : 0.0f, rstd = P.rstd[row];
+    using S = Stage<DT, KEPT>;
+    constexpr int kStages = Ring<DT, KEPT, THREADS>::kStages;
+    extern __shared__ __align__(16) uint4 ring[];           // [weight: 4][stage][word][thread]
+    __shared__ Parts parts;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    Place<WARP> at(P);
+    const uint32_t step = blockDim.x;
+    uint4 *const mine = ring + threadIdx.x;
+    auto bring_row = [&](uint64_t row, uint32_t slot) {
+        uint4 *to = mine + (4 + slot * S::kWords) * step;
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
-            muon::load8(P.dy.p, DT, row * P.dy.ld + U.col[u], U.live[u], P.dy.vec, g[u]);
-            input8<DT, KEPT>(P, row, U.col[u], U.live[u], h[u]);
+            const int live = at.of(u, row, P.rows);
+            if (live == 0) continue;
+            bring<DT>(to + u * (S::kDy / kUnits) * step, step, P.dy, row * P.dy.ld + at.col[u], live);
+            if (!KEPT) {
+                bring<DT>(to + (S::kDy + u * (S::kDy / kUnits)) * step, step, P.x, row * P.x.ld + at.col[u], live);
+            } else {
+                uint2 *q = reinterpret_cast<uint2 *>(to + S::kDy * step) + u;
+                if (P.from.vec && live == 8) copy_async<8>(q, P.from.q + row * P.from.q_ld + at.col[u]);
+                else *q = kept::fetch_codes(P.from, row, at.col[u], live).v;
+            }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // what is too little for the ring is fetched a row ahead
+    float mean = 0.0f, rstd = 0.0f;
+    uint32_t power[kUnits] = {};
+    auto fetch_rest = [&](uint64_t row) {
+        if (row >= P.rows) return;
+        rstd = P.rstd[row];
+        if (P.centred) mean = P.mean[row];
+        if (KEPT)
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u)
+                if (at.live[u]) power[u] = P.from.power[row * P.from.power_ld + (at.col[u] >> 5)];
+    };
+    if constexpr (kStages > 1) {
+#pragma unroll
+        for (int s = 0; s < kStages - 1; ++s) bring_row(at.row() + s * at.stride, s);
+    }
+    fetch_rest(at.row());
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+        float w[8];
+        params8(P.w, P.w_dtype, at.col[u], at.live[u], P.w_vec, 1.0f, w);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<float4 *>(mine + (2 * u + i) * step) = make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    float dw[kUnits][8] = {}, db[kUnits][8] = {};
+    uint32_t slot = 0;
+    for (uint32_t turn = 0; at.base < P.rows; turn ^= 1) {
+        const uint64_t row = at.row();
+        bring_row(row + (kStages - 1) * at.stride, slot ? slot - 1 : kStages - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        const uint4 *from = mine + (4 + slot * S::kWords) * step;
+        slot = slot + 1 == kStages ? 0 : slot + 1;
+        const float m = mean, r = rstd;
+        const uint32_t b[kUnits] = {power[0], power[1]};
+        at.base += at.stride;
+        fetch_rest(at.row());
+        float h[kUnits][8], g[kUnits][8], along = 0.0f, sum = 0.0f;
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
-            float w[8];
-            params8(P.w, P.w_dtype, U.col[u], U.live[u], P.w_vec, 1.0f, w);
+            if (at.of(u, row, P.rows) == 0) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[u][i] = g[u][i] = 0.0f;
+                continue;
+            }
+            taken<DT>(from + u * (S::kDy / kUnits) * step, step, g[u]);
+            if (KEPT) kept::values(kept::Codes{*(reinterpret_cast<const uint2 *>(from + S::kDy * step) + u), b[u]}, h[u]);
+            else taken<DT>(from + (S::kDy + u * (S::kDy / kUnits)) * step, step, h[u]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                h[u][i] = __fmul_rn(__fsub_rn(h[u][i], mean), rstd);
+                const float4 w = *reinterpret_cast<const float4 *>(mine + (2 * u + (i >> 2)) * step);
+                h[u][i] = __fmul_rn(P.centred ? __fsub_rn(h[u][i], m) : h[u][i], r);
                 dw[u][i] = __fmaf_rn(g[u][i], h[u][i], dw[u][i]);
-                db[u][i] = __fadd_rn(db[u][i], g[u][i]);
-                g[u][i] = __fmul_rn(g[u][i], w[i]);
-                sum = __fadd_rn(sum, g[u][i]);
+                if (P.db) db[u][i] = __fadd_rn(db[u][i], g[u][i]);
+                g[u][i] = __fmul_rn(g[u][i], (i & 3) == 0 ? w.x : (i & 3) == 1 ? w.y : (i & 3) == 2 ? w.z : w.w);
+                if (P.centred) sum = __fadd_rn(sum, g[u][i]);
                 along = __fmaf_rn(g[u][i], h[u][i], along);
             }
         }
         if (!P.dx.p) continue;
-        if (P.centred) sum = warp_sum(sum);
-        along = warp_sum(along);
+        if (P.centred) sum = WARP ? lane_sum(sum, P.lanes) : warp_sum(sum);
+        along = WARP ? lane_sum(along, P.lanes) : warp_sum(along);
         if (!WARP) {
-            const uint32_t lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-            if (lane == 0) part[turn][threadIdx.x >> 5] = make_float2(sum, along);
-            __syncthreads();
-            const float2 p = lane < warps ? part[turn][lane] : make_float2(0.0f, 0.0f);
+            const float2 p = exchange(parts, turn, make_float2(sum, along));
             if (P.centred) sum = warp_sum(p.x);
             along = warp_sum(p.y);
         }
-        sum = P.centred ? __fmul_rn(sum, P.over_n) : 0.0f;
+        sum = __fmul_rn(sum, P.over_n);
         along = __fmul_rn(along, P.over_n);
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
+            const int live = at.of(u, row, P.rows);
+            if (live == 0) continue;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                g[u][i] = __fmul_rn(__fmaf_rn(-h[u][i], along, __fsub_rn(g[u][i], sum)), rstd);
-            kept::store8<DT>(P.dx.p, row * P.dx.ld + U.col[u], U.live[u], P.dx.vec, g[u]);
+                g[u][i] = __fmul_rn(__fmaf_rn(-h[u][i], along, __fsub_rn(g[u][i], sum)), r);
+            kept::store8<DT>(P.dx.p, row * P.dx.ld + at.col[u], live, P.dx.vec, g[u]);
         }
     }
-    if (!P.sums) return;
-    float *to = P.partial + at.group * 2 * P.cols;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!P.dw && !P.db) return;
+    float *to = P.partial + blockIdx.x * 2 * P.pitch;
+    if constexpr (WARP) {
+        // a row's lanes, then the warps, one after another, in the first rows of the ring
+        float *const sums = reinterpret_cast<float *>(ring);
+        const uint32_t lane = threadIdx.x & 31;
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u)
+        for (int u = 0; u < kUnits; ++u)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < U.live[u]) {
-                to[U.col[u] + i] = dw[u][i];
-                to[P.cols + U.col[u] + i] = db[u][i];
+            for (int i = 0; i < 8; ++i)
+                for (uint32_t d = P.lanes; d < 32; d <<= 1) {
+                    dw[u][i] = __fadd_rn(dw[u][i], __shfl_xor_sync(0xFFFFFFFFu, dw[u][i], d));
+                    if (P.db) db[u][i] = __fadd_rn(db[u][i], __shfl_xor_sync(0xFFFFFFFFu, db[u][i], d));
+                }
+        for (uint32_t w = 0; w < kWarpThreads / 32; ++w) {
+            __syncthreads();
+            if (threadIdx.x >> 5 == w && lane < P.lanes)
+#pragma unroll
+                for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float *p = sums + at.col[u] + i;
+                        p[0] = w ? __fadd_rn(p[0], dw[u][i]) : dw[u][i];
+                        p[kWarpCols] = w ? __fadd_rn(p[kWarpCols], db[u][i]) : db[u][i];
+                    }
+        }
+        __syncthreads();
+        for (uint64_t c = threadIdx.x; c < P.cols; c += kWarpThreads) {
+            to[c] = sums[c];
+            if (P.db) to[P.pitch + c] = sums[kWarpCols + c];
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            if (at.live[u] == 0) continue;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float4 *p = reinterpret_cast<float4 *>(to + at.col[u]) + i;
+                *p = make_float4(dw[u][4 * i], dw[u][4 * i + 1], dw[u][4 * i + 2], dw[u][4 * i + 3]);
+                if (P.db) p[P.pitch / 4] = make_float4(db[u][4 * i], db[u][4 * i + 1], db[u][4 * i + 2], db[u][4 * i + 3]);
             }
+        }
+    }
 }
 
 // Rows that do not fit: dx, a block a row, read twice.
@@ -370,36 +557,39 @@ __global__ void __launch_bounds__(256) columns_kernel(const __grid_constant__ Pa
             db[i] = __fadd_rn(db[i], g[i]);
         }
     }
-    float *to = P.partial + blockIdx.y * 2 * P.cols;
+    float *to = P.partial + blockIdx.y * 2 * P.pitch;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (i < live) {
             to[col + i] = dw[i];
-            to[P.cols + col + i] = db[i];
+            to[P.pitch + col + i] = db[i];
         }
 }
 
 struct SumParams {
     const float *partial;
-    uint64_t cols, groups;
+    uint64_t cols, pitch;
+    uint32_t groups;
     void *out[2];                               // dw, db; null where not wanted
     uint32_t dtype[2];
 };
 
-// Adds the groups' sums of a column up in one order: a block 32 columns, of dw or of
-// db, every sixteenth group a warp.
+// Adds the blocks' sums of a column up in one order: a block 32 columns, of dw or of
+// db, every sixteenth sum a warp.
 constexpr int kSumWarps = 16;
 
 __global__ void __launch_bounds__(kSumWarps * 32) sum_kernel(const __grid_constant__ SumParams P)
 {
     __shared__ float part[kSumWarps][32];
-    const int which = blockIdx.y;
-    if (!P.out[which]) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int which = P.out[blockIdx.y] ? blockIdx.y : 1;       // db alone comes in the grid's only row
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint64_t col = blockIdx.x * 32ull + lane;
     float sum = 0.0f;
     if (col < P.cols)
-        for (uint64_t g = warp; g < P.groups; g += kSumWarps) sum = __fadd_rn(sum, P.partial[(g * 2 + which) * P.cols + col]);
+#pragma unroll 8
+        for (uint32_t g = warp; g < P.groups; g += kSumWarps)
+            sum = __fadd_rn(sum, P.partial[(g * 2ull + which) * P.pitch + col]);
     part[warp][lane] = sum;
     __syncthreads();
     if (warp || col >= P.cols) return;
@@ -418,6 +608,20 @@ int shape_of(uint64_t cols) { return cols <= kWarpCols ? kWarp : cols <= kBlockC
 
 unsigned block_threads(uint64_t cols) { return static_cast<unsigned>((cols + kWarpCols - 1) / kWarpCols * 32); }
 
+unsigned threads_of(uint64_t cols)
+{
+    const int shape = shape_of(cols);
+    return shape == kWarp ? kWarpThreads : shape == kBlock ? block_threads(cols) : kLongThreads;
+}
+
+// Lanes of a row of up to 512 values, 16 each.
+uint32_t lanes_of(uint64_t cols)
+{
+    uint32_t n = 4;
+    while (n * 8 * kUnits < cols && n < 32) n *= 2;
+    return n;
+}
+
 template <int DT, bool KEEP>
 Kernel forward_of(int shape)
 {
@@ -431,17 +635,29 @@ Kernel forward_of(int32_t dtype, int shape, bool keep)
     return keep ? forward_of<ASR_F32, true>(shape) : forward_of<ASR_F32, false>(shape);
 }
 
-// Threads that a block's registers are budgeted for: more a thread in smaller blocks.
-template <int DT, bool KEPT>
-Kernel backward_of(int shape, unsigned threads)
+// A backward kernel and its shared memory, the registers of its blocks budgeted for
+// their size: fewer a thread in larger ones.
+struct Backward {
+    Kernel kernel;
+    size_t smem;
+};
+
+template <int DT, bool KEPT, bool WARP, int THREADS>
+Backward backward_at(unsigned threads)
 {
-    if (shape == kWarp) return backward_kernel<DT, true, KEPT, kWarpThreads>;
-    if (shape == kLong) return backward_long_kernel<DT, KEPT>;
-    return threads <= 256 ? backward_kernel<DT, false, KEPT, 256> : threads <= 512 ? backward_kernel<DT, false, KEPT, 512>
-                                                                                   : backward_kernel<DT, false, KEPT, 1024>;
+    return Backward{backward_kernel<DT, WARP, KEPT, THREADS>, Ring<DT, KEPT, THREADS>::bytes(threads)};
 }
 
-Kernel backward_of(int32_t dtype, bool codes, int shape, unsigned threads)
+template <int DT, bool KEPT>
+Backward backward_of(int shape, unsigned threads)
+{
+    if (shape == kWarp) return backward_at<DT, KEPT, true, kWarpThreads>(threads);
+    if (shape == kLong) return Backward{backward_long_kernel<DT, KEPT>, 0};
+    return threads <= 256 ? backward_at<DT, KEPT, false, 256>(threads) : threads <= 512 ? backward_at<DT, KEPT, false, 512>(threads)
+                                                                     : backward_at<DT, KEPT, false, 1024>(threads);
+}
+
+Backward backward_of(int32_t dtype, bool codes, int shape, unsigned threads)
 {
     if (dtype == ASR_BF16)
         return codes ? backward_of<ASR_BF16, true>(shape, threads) : backward_of<ASR_BF16, false>(shape, threads);
@@ -472,8 +688,13 @@ asr_status setup()
             if (e == cudaSuccess) e = prod::load_kernel(columns_of(dtype, kept != 0));
             for (int shape : {kWarp, kBlock, kLong}) {
                 if (e == cudaSuccess) e = prod::load_kernel(forward_of(dtype, shape, kept != 0));
-                for (unsigned threads : {256u, 512u, 1024u})
-                    if (e == cudaSuccess) e = prod::load_kernel(backward_of(dtype, kept != 0, shape, threads));
+                for (unsigned threads : {256u, 512u, 1024u}) {
+                    const Backward k = backward_of(dtype, kept != 0, shape, threads);
+                    if (e == cudaSuccess && k.smem)
+                        e = cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem));
+                    if (e == cudaSuccess) e = prod::load_kernel(k.kernel);
+                    if (shape == kWarp) break;
+                }
             }
         }
     if (e != cudaSuccess) return cuda_fail(e);
@@ -512,6 +733,8 @@ Params common(const asr_norm_params *p)
     P.w_vec = aligned16(p->weight);
     P.b_vec = aligned16(p->bias);
     P.centred = p->centred;
+    P.lanes = lanes_of(p->cols);
+    P.pitch = muon::up(p->cols, 8);
     return P;
 }
 
@@ -538,25 +761,30 @@ asr_status forward(const asr_norm_params *p, const void *x, uint64_t x_ld, void 
         P.sr = to->rounding == ASR_ROUND_SR;
     }
     const int shape = shape_of(p->cols);
-    const unsigned threads = shape == kWarp ? kWarpThreads : shape == kBlock ? block_threads(p->cols) : kLongThreads;
-    const unsigned grid = int8::blocks_for(p->rows, shape == kWarp ? kWarpThreads / 32 : 1, 1u << 20);
-    forward_of(p->dtype, shape, to != nullptr)<<<grid, threads, 0, stream>>>(P);
+    const unsigned threads = threads_of(p->cols);
+    auto kernel = forward_of(p->dtype, shape, to != nullptr);
+    int most = 0;
+    st = kept::resident(kernel, threads, 0, &most);
+    if (st != ASR_OK) return st;
+    const unsigned grid = int8::blocks_for(p->rows, shape == kWarp ? kWarpThreads / P.lanes : 1, static_cast<uint64_t>(most));
+    kernel<<<grid, threads, 0, stream>>>(P);
     return launched(ASR_KERNEL_NORM);
 }
 
-// Groups of threads that walk over the rows of a backward pass: enough to fill the
-// GPU, and eight rows each where there are fewer, since each leaves 2 x cols sums.
+// Blocks that leave sums of a backward pass at most: enough to fill the GPU, and four
+// steps' rows each where there are fewer, since each leaves 2 x cols of them.  Of rows
+// that do not fit, 64, with 32 rows each.
 constexpr uint64_t kMostGroups = 152 * 4;
 
 uint64_t groups_of(uint64_t rows, uint64_t cols)
 {
-    const uint64_t most = shape_of(cols) == kWarp ? kMostGroups * (kWarpThreads / 32) : kMostGroups;
-    const uint64_t want = shape_of(cols) == kLong ? (rows + 31) / 32 : (rows + 7) / 8;
-    const uint64_t g = want < most ? want : most;
-    return shape_of(cols) == kWarp ? (g + 7) / 8 * 8 : shape_of(cols) == kLong && g > 64 ? 64 : g;
+    const int shape = shape_of(cols);
+    const uint64_t each = shape == kLong ? 32 : 4 * (shape == kWarp ? kWarpThreads / lanes_of(cols) : 1);
+    const uint64_t want = (rows + each - 1) / each, most = shape == kLong ? 64 : kMostGroups;
+    return want < most ? want : most;
 }
 
-uint64_t workspace_of(uint64_t rows, uint64_t cols) { return groups_of(rows, cols) * 2 * cols * sizeof(float); }
+uint64_t workspace_of(uint64_t rows, uint64_t cols) { return groups_of(rows, cols) * 2 * muon::up(cols, 8) * sizeof(float); }
 
 asr_status backward(const asr_norm_params *p, const void *dy, uint64_t dy_ld, const void *x, uint64_t x_ld,
                     const asr_checkpoint *from, const float *mean, const float *rstd, void *dx, uint64_t dx_ld, void *dweight,
@@ -571,7 +799,7 @@ asr_status backward(const asr_norm_params *p, const void *dy, uint64_t dy_ld, co
     if ((dweight && !muon::element_aligned(dweight, dweight_dtype)) || (dbias && !muon::element_aligned(dbias, dbias_dtype)) ||
         !kept::sizes_ok(p->rows, p->cols))
         return ASR_ERR_INVALID_VALUE;
-    const uint64_t groups = groups_of(p->rows, p->cols);
+    uint64_t groups = groups_of(p->rows, p->cols);
     if (p->rows) {
         if (!kept::matrix_ok(dy, p->dtype, dy_ld, p->cols) || (dx && !kept::matrix_ok(dx, p->dtype, dx_ld, p->cols)) ||
             !params_ok(p) || !rstd || (p->centred && !mean) || !muon::element_aligned(mean, ASR_F32) ||
@@ -594,13 +822,18 @@ asr_status backward(const asr_norm_params *p, const void *dy, uint64_t dy_ld, co
         P.mean = const_cast<float *>(mean);
         P.rstd = const_cast<float *>(rstd);
         P.partial = static_cast<float *>(ws);
-        P.sums = sums;
+        P.dw = dweight != nullptr;
+        P.db = dbias != nullptr;
         const int shape = shape_of(p->cols);
-        const unsigned threads = shape == kWarp ? kWarpThreads : shape == kBlock ? block_threads(p->cols) : kLongThreads;
+        const unsigned threads = threads_of(p->cols);
+        const Backward k = backward_of(p->dtype, from != nullptr, shape, threads);
+        int most = 0;
+        st = kept::resident(k.kernel, static_cast<int>(threads), k.smem, &most);
+        if (st != ASR_OK) return st;
+        if (shape != kLong && groups > static_cast<uint64_t>(most)) groups = static_cast<uint64_t>(most);
         if (shape != kLong || dx) {
-            const unsigned grid = shape == kWarp ? static_cast<unsigned>(groups / 8) :
-                                  shape == kBlock ? static_cast<unsigned>(groups) : int8::blocks_for(p->rows, 1, 1u << 20);
-            backward_of(p->dtype, from != nullptr, shape, threads)<<<grid, threads, 0, stream>>>(P);
+            const unsigned grid = shape == kLong ? int8::blocks_for(p->rows, 1, static_cast<uint64_t>(most)) : static_cast<unsigned>(groups);
+            k.kernel<<<grid, threads, k.smem, stream>>>(P);
             st = launched(ASR_KERNEL_NORM);
         }
         if (st == ASR_OK && shape == kLong && sums) {
@@ -614,14 +847,14 @@ asr_status backward(const asr_norm_params *p, const void *dy, uint64_t dy_ld, co
     SumParams S;
     S.partial = static_cast<const float *>(ws);
     S.cols = p->cols;
-    S.groups = p->rows ? groups : 0;
+    S.pitch = muon::up(p->cols, 8);
+    S.groups = p->rows ? static_cast<uint32_t>(groups) : 0;
     S.out[0] = dweight;
     S.out[1] = dbias;
     S.dtype[0] = static_cast<uint32_t>(dweight_dtype);
     S.dtype[1] = static_cast<uint32_t>(dbias_dtype);
-    const dim3 grid(static_cast<unsigned>((p->cols + 31) / 32), dbias ? 2 : 1);
-    sum_kernel<<<grid, kSumWarps * 32, 0, stream>>>(S);
-    return launched(ASR_KERNEL_NORM);
+    const dim3 grid(static_cast<unsigned>((p->cols + 31) / 32), dweight && dbias ? 2 : 1);
+    return prod::launch_early(ASR_KERNEL_NORM, sum_kernel, grid, kSumWarps * 32, S, stream);
 }
 
 }  // namespace norm
