@@ -105,6 +105,12 @@ class NormParams(ctypes.Structure):
                 ("reserved", ctypes.c_uint64)]
 
 
+# both packed in one call (their fields in order, native alignment)
+_CHECKPOINT_PACK = struct.Struct("=6Q2I")
+_NORM_PACK = struct.Struct("=4Qd3iIQ")
+assert _CHECKPOINT_PACK.size == ctypes.sizeof(Checkpoint) and _NORM_PACK.size == ctypes.sizeof(NormParams)
+
+
 class AsrError(RuntimeError):
     def __init__(self, status: int, what: str):
         msg = f"{what}: {status_string(status)}"
@@ -324,9 +330,21 @@ def _on_device(device):
     torch = _torch()
     if not isinstance(device, torch.device):
         device = torch.device(device)
-    if device.index is None or device.index == torch.cuda.current_device():
+    if device.index is None or device.index == _current_device():
         return _NULL_CONTEXT
     return torch.cuda.device(device)
+
+
+def _current_device() -> int:
+    torch = _torch()
+    get = getattr(torch._C, "_cuda_getDevice", None)        # a third of current_device()'s time, with CUDA up
+    return get() if get is not None and torch.cuda.is_initialized() else torch.cuda.current_device()
+
+
+def _raw_stream(index: int) -> int:
+    """The current stream of CUDA device ``index``, as a number."""
+    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else _torch().cuda.current_stream(index).cuda_stream
 
 
 def _stream_handle(device, stream):
@@ -941,21 +959,28 @@ _FUNCTION = {"silu": ASR_SILU, "gelu": ASR_GELU}
 CHECKPOINT_GROUP = 32           # values of a row that share a power of two
 
 
+def _pack_checkpoint(pq, pp, q_ld, power_ld, rounding="rne", base_index=0, step=0, seed=0):
+    """The C struct of a checkpoint whose pointers and pitches have been checked."""
+    r = _ROUNDING.get(rounding)
+    if r is None:
+        raise ValueError(f"rounding must be 'sr' or 'rne', not {rounding!r}")
+    c = Checkpoint()
+    _CHECKPOINT_PACK.pack_into(c, 0, pq, pp, q_ld, power_ld, int(base_index) & (2**64 - 1), int(seed) & (2**64 - 1),
+                               int(step) & 0xFFFFFFFF, r)
+    return ctypes.byref(c)
+
+
 def _checkpoint(kept, rows, cols, device, rounding="rne", base_index=0, step=0, seed=0):
-    """The C struct of a checkpoint (q, power) of a rows x cols matrix."""
+    """The C struct of a checkpoint of a rows x cols matrix: (q, power), or an ``Int8Checkpoint``."""
     torch = _torch()
-    q, power = kept[0], kept[1]
+    q, power = kept if type(kept) is tuple or isinstance(kept, list) else (kept.q, kept.power)
     pq, qr, qc, q_ld = _matrix_ptr(q, "q", (torch.int8,), device)
     pp, pr, pc, p_ld = _matrix_ptr(power, "power", (torch.uint8,), device)
     groups = (cols + CHECKPOINT_GROUP - 1) // CHECKPOINT_GROUP
     if qr != rows or qc != cols or pr != rows or pc != groups:
         raise ValueError(f"a checkpoint of {(rows, cols)} has q of that shape and power of {(rows, groups)}, not "
                          f"{(qr, qc)} and {(pr, pc)}")
-    r = _ROUNDING.get(rounding)
-    if r is None:
-        raise ValueError(f"rounding must be 'sr' or 'rne', not {rounding!r}")
-    return Checkpoint(pq, pp, q_ld, p_ld, int(base_index) & (2**64 - 1), int(seed) & (2**64 - 1), int(step) & 0xFFFFFFFF,
-                      r)
+    return _pack_checkpoint(pq, pp, q_ld, p_ld, rounding, base_index, step, seed)
 
 
 def asr_checkpoint_int8(x, q, power, *, rounding="rne", base_index: int = 0, step: int = 0, seed: int = 0, stream=None):
@@ -967,7 +992,7 @@ def asr_checkpoint_int8(x, q, power, *, rounding="rne", base_index: int = 0, ste
     px, rows, cols, ld = _matrix_ptr(x, "x", (torch.bfloat16, torch.float32))
     c = _checkpoint((q, power), rows, cols, x.get_device(), rounding, base_index, step, seed)
     with _on_device(x.device):
-        _check(lib().asr_checkpoint_int8(px, _dt(x), rows, cols, ld, ctypes.byref(c), _stream_handle(x.device, stream)),
+        _check(lib().asr_checkpoint_int8(px, _dt(x), rows, cols, ld, c, _stream_handle(x.device, stream)),
                "asr_checkpoint_int8")
     return q, power
 
@@ -978,7 +1003,7 @@ def asr_restore_int8(q, power, out, *, stream=None):
     po, rows, cols, ld = _matrix_ptr(out, "out", (torch.bfloat16, torch.float32))
     c = _checkpoint((q, power), rows, cols, out.get_device())
     with _on_device(out.device):
-        _check(lib().asr_restore_int8(ctypes.byref(c), rows, cols, po, _dt(out), ld, _stream_handle(out.device, stream)),
+        _check(lib().asr_restore_int8(c, rows, cols, po, _dt(out), ld, _stream_handle(out.device, stream)),
                "asr_restore_int8")
     return out
 
@@ -993,8 +1018,8 @@ def _function(function):
 def asr_activation(x, y, function="silu", *, gated=False, keep=None, rounding="rne", base_index: int = 0, step: int = 0,
                    seed: int = 0, stream=None):
     """``y`` = f(x), or, ``gated``, f of x's first half of columns times its second
-    half; x and y 2-D of one dtype, float32 or bfloat16.  ``keep``: (q, power) that
-    receive x's checkpoint."""
+    half; x and y 2-D of one dtype, float32 or bfloat16.  ``keep``: (q, power), or
+    an ``Int8Checkpoint``, that receives x's checkpoint."""
     torch = _torch()
     code = _function(function)
     py, rows, cols, y_ld = _matrix_ptr(y, "y", (torch.bfloat16, torch.float32))
@@ -1005,7 +1030,7 @@ def asr_activation(x, y, function="silu", *, gated=False, keep=None, rounding="r
         raise ValueError(f"x has shape {(xr, xc)}; expected {(rows, width)}")
     c = None
     if keep is not None:
-        c = ctypes.byref(_checkpoint(keep, rows, width, d, rounding, base_index, step, seed))
+        c = _checkpoint(keep, rows, width, d, rounding, base_index, step, seed)
     with _on_device(y.device):
         _check(lib().asr_activation(px, x_ld, py, y_ld, _dt(y), rows, cols, code, 1 if gated else 0, c,
                                     _stream_handle(y.device, stream)), "asr_activation")
@@ -1031,20 +1056,22 @@ def asr_activation_grads(dy, x, dx, function="silu", *, gated=False, kept=None, 
         if xr != rows or xc != width:
             raise ValueError(f"x has shape {(xr, xc)}; expected {(rows, width)}")
     else:
-        c = ctypes.byref(_checkpoint(kept, rows, width, d))
+        c = _checkpoint(kept, rows, width, d)
     with _on_device(dy.device):
         _check(lib().asr_activation_grads(pg, g_ld, px, x_ld, c, pd, d_ld, _dt(dy), rows, cols, code, 1 if gated else 0,
                                           _stream_handle(dy.device, stream)), "asr_activation_grads")
     return dx
 
 
-def _norm_params(rows, cols, x, weight, bias, eps, centred, device) -> NormParams:
+def _norm_params(rows, cols, dtype, weight, bias, eps, centred, device):
     torch = _torch()
     types = (torch.bfloat16, torch.float32)
-    pw = None if weight is None else _dev_ptr(weight, "weight", types, cols, device)
-    pb = None if bias is None else _dev_ptr(bias, "bias", types, cols, device)
-    return NormParams(rows, cols, pw, pb, float(eps), _dt(x), ASR_F32 if weight is None else _dt(weight),
-                      ASR_F32 if bias is None else _dt(bias), 1 if centred else 0, 0)
+    p = NormParams()
+    _NORM_PACK.pack_into(p, 0, rows, cols, 0 if weight is None else _dev_ptr(weight, "weight", types, cols, device),
+                         0 if bias is None else _dev_ptr(bias, "bias", types, cols, device), eps, dtype,
+                         ASR_F32 if weight is None else _dt(weight), ASR_F32 if bias is None else _dt(bias),
+                         1 if centred else 0, 0)
+    return ctypes.byref(p)
 
 
 def asr_layer_norm(x, weight, bias, y, mean=None, rstd=None, *, eps=1e-5, centred=True, keep=None, rounding="rne",
@@ -1060,15 +1087,15 @@ def asr_layer_norm(x, weight, bias, y, mean=None, rstd=None, *, eps=1e-5, centre
     py, yr, yc, y_ld = _matrix_ptr(y, "y", (x.dtype,), d)
     if yr != rows or yc != cols:
         raise ValueError(f"y has shape {(yr, yc)}; expected {(rows, cols)}")
-    p = _norm_params(rows, cols, x, weight, bias, eps, centred, d)
+    p = _norm_params(rows, cols, _dt(x), weight, bias, eps, centred, d)
     f32 = (torch.float32,)
     pm = None if mean is None else _dev_ptr(mean, "mean", f32, rows, d)
     pr = None if rstd is None else _dev_ptr(rstd, "rstd", f32, rows, d)
     c = None
     if keep is not None:
-        c = ctypes.byref(_checkpoint(keep, rows, cols, d, rounding, base_index, step, seed))
+        c = _checkpoint(keep, rows, cols, d, rounding, base_index, step, seed)
     with _on_device(x.device):
-        _check(lib().asr_layer_norm(ctypes.byref(p), px, x_ld, py, y_ld, pm, pr, c, _stream_handle(x.device, stream)),
+        _check(lib().asr_layer_norm(p, px, x_ld, py, y_ld, pm, pr, c, _stream_handle(x.device, stream)),
                "asr_layer_norm")
     return y
 
@@ -1100,8 +1127,8 @@ def asr_layer_norm_grads(dy, x, weight, mean, rstd, dx, dweight, dbias, *, centr
         if xr != rows or xc != cols:
             raise ValueError(f"x has shape {(xr, xc)}; expected {(rows, cols)}")
     else:
-        c = ctypes.byref(_checkpoint(kept, rows, cols, d))
-    p = _norm_params(rows, cols, dy, weight, None, 0.0, centred, d)
+        c = _checkpoint(kept, rows, cols, d)
+    p = _norm_params(rows, cols, _dt(dy), weight, None, 0.0, centred, d)
     f32 = (torch.float32,)
     if rstd is None or (centred and mean is None):
         raise ValueError("the backward pass needs the forward pass's rstd, and its mean if centred")
@@ -1119,7 +1146,7 @@ def asr_layer_norm_grads(dy, x, weight, mean, rstd, dx, dweight, dbias, *, centr
     device = dy.device
     with _on_device(device):
         buf, pws, size = _workspace(workspace, need, device, stream)
-        _check(lib().asr_layer_norm_grads(ctypes.byref(p), pg, g_ld, px, x_ld, c, pm, pr, pd, d_ld, pw,
+        _check(lib().asr_layer_norm_grads(p, pg, g_ld, px, x_ld, c, pm, pr, pd, d_ld, pw,
                                           ASR_F32 if dweight is None else _dt(dweight), pb,
                                           ASR_F32 if dbias is None else _dt(dbias), pws, size,
                                           _stream_handle(device, stream)), "asr_layer_norm_grads")

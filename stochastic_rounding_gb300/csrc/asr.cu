@@ -960,8 +960,10 @@ asr_status asr_embedding_grads(const void *ids, int32_t index, uint64_t tokens, 
                                void *dtable, int32_t dtable_dtype, void *workspace, uint64_t workspace_bytes,
                                asr_stream_t stream)
 {
-    return embed::grads(ids, index, tokens, dy, dy_ld, dy_dtype, vocab, dim, scale, padding_idx, dtable, dtable_dtype,
+    return guarded([&] {
+        return embed::grads(ids, index, tokens, dy, dy_ld, dy_dtype, vocab, dim, scale, padding_idx, dtable, dtable_dtype,
                         workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+    });
 }
 
 asr_status asr_embedding_grads_workspace(uint64_t tokens, uint64_t dim, uint64_t *bytes)

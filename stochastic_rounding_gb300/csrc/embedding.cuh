@@ -5,30 +5,39 @@
 //
 // The gradient is the whole table's, and most of its bytes are zeros.  Tokens are
 // sorted by id, stably, so that every row's tokens lie together and in order; the
-// sorted list is cut into chunks of one length, a block each, whatever the ids --
-// a token that makes up half of a batch is as even a share of the work as any.  A
-// block adds its tokens' rows up in registers: a row that begins and ends within
-// the chunk is written at once, one that reaches over an end leaves a binary32 sum
-// in the workspace, and a last kernel adds those up, in order.  Rows without
-// tokens are zeroed by the blocks that do not sort.
+// sorted list is cut into chunks of one length, a block each (and a slice of the
+// columns), whatever the ids -- a token that makes up half of a batch is as even a
+// share of the work as any.  A block adds its tokens' rows up in registers: a row that
+// begins and ends within the chunk is written at once, one that reaches over an end
+// leaves a binary32 sum in the workspace, and the last of its blocks to finish adds
+// those up, in order.
+// Rows without tokens are zeroed beside the sort, as many as it takes the time of, and
+// beside the sums.
 //
-// The sort is by digits of up to nine bits, from the lowest, each by counts and
+// The sort is by digits of up to ten bits, from the lowest, each by counts and
 // ranks: a warp ranks 32 keys at a time (lanes of one digit find one another), the
-// warps' counts are added up by digit.  Up to 8,192 tokens are one block's, in
-// shared memory; more are cut into tiles of 8,192, with a launch each for their
-// counts, the tiles' places, and the moves.
+// warps' counts are added up by digit.  Up to 16,384 tokens are a cluster's of eight
+// blocks, which read one another's counts and hand the keys to one another's shared
+// memory (by one block alone 8,192 tokens took 20 us: its instructions); more are cut
+// into tiles of 4,096, with a launch each for their counts, the tiles' places, and the
+// moves.
 
 namespace embed {
 
 using kept::live_of;
 
-constexpr int kSortThreads = 1024;
-constexpr int kTile = 8192;                     // keys a block sorts, eight a thread
-constexpr int kRounds = kTile / kSortThreads;
-constexpr int kDigitBits = 9;
+constexpr int kCluster = 8;
+constexpr int kSortThreads = 256;
+constexpr int kSortRounds = 8;                  // of 32 keys, a warp at most
+constexpr int kSort = kCluster * kSortThreads * kSortRounds;        // keys a cluster sorts
+constexpr int kTileThreads = 512;
+constexpr int kTileRounds = 8;
+constexpr int kTile = kTileThreads * kTileRounds;       // keys of one block of many
+constexpr int kDigitBits = 10;
 constexpr int kBins = 1 << kDigitBits;
 constexpr int kThreads = 256;
-constexpr int kZeroRows = 64;                   // of the table, a block at a time
+constexpr int kZeroRows = 64;                   // of the table, a block at most
+constexpr uint64_t kZeroBytes = 256 << 10;      // of zeros, a block beside the sort
 
 struct Ids {
     const void *p;
@@ -89,19 +98,22 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant_
 
 // ---- sort
 
-// Ranks of a block's keys by one digit.  Warp w holds keys w * 256 .. + 255 of the
-// tile, 32 a round.  Afterwards `counts` holds, for each warp and digit, how many
-// keys of the digit the warps before have; totals[d] is the tile's.
-__device__ __forceinline__ void rank_digits(const uint32_t key[kRounds], uint32_t live, uint32_t shift,
-                                            uint16_t (*counts)[kBins], uint32_t *totals, uint16_t rank[kRounds])
+// Ranks of a block's keys by one digit.  Warp w holds keys w * rounds * 32 on, 32 a
+// round.  Afterwards `counts` holds, for each warp and digit, how many keys of the
+// digit the warps before have; totals[d] is the block's.
+template <int ROUNDS, int WARPS>
+__device__ __forceinline__ void rank_digits(const uint32_t key[ROUNDS], uint32_t live, uint32_t rounds, uint32_t shift,
+                                            uint32_t bins, uint16_t (*counts)[kBins], uint32_t *totals,
+                                            uint16_t rank[ROUNDS])
 {
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (uint32_t i = threadIdx.x; i < 32 * kBins / 2; i += kSortThreads) reinterpret_cast<uint32_t *>(counts)[i] = 0;
-    __syncthreads();
+    for (uint32_t i = lane; i < bins / 2; i += 32) reinterpret_cast<uint32_t *>(counts[warp])[i] = 0;
+    __syncwarp();
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
+    for (int r = 0; r < ROUNDS; ++r) {
+        if (r >= rounds) break;
         const bool in = (live >> r) & 1;
-        const uint32_t d = in ? (key[r] >> shift) & (kBins - 1) : kBins;
+        const uint32_t d = in ? (key[r] >> shift) & (bins - 1) : bins;
         const uint32_t peers = __match_any_sync(0xFFFFFFFFu, d);
         const uint32_t before = peers & ((1u << lane) - 1);
         if (in) rank[r] = static_cast<uint16_t>(counts[warp][d] + __popc(before));
@@ -110,48 +122,18 @@ __device__ __forceinline__ void rank_digits(const uint32_t key[kRounds], uint32_
         __syncwarp();
     }
     __syncthreads();
-    if (threadIdx.x < kBins) {
-        uint32_t sum = 0;
-#pragma unroll 8
-        for (int w = 0; w < 32; ++w) {
-            const uint32_t c = counts[w][threadIdx.x];
-            counts[w][threadIdx.x] = static_cast<uint16_t>(sum);
-            sum += c;
-        }
-        totals[threadIdx.x] = sum;
-    }
-    __syncthreads();
-}
-
-// totals[d] becomes the sum of those before it.
-__device__ __forceinline__ void scan_bins(uint32_t *totals, uint32_t *part)
-{
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t own = 0, v = 0;
-    if (threadIdx.x < kBins) {
-        own = v = totals[threadIdx.x];
+    for (uint32_t d = threadIdx.x; d < bins; d += WARPS * 32) {
+        uint32_t c[WARPS], sum = 0;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, v, d);
-            if (lane >= static_cast<uint32_t>(d)) v += o;
+        for (int w = 0; w < WARPS; ++w) c[w] = counts[w][d];
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            counts[w][d] = static_cast<uint16_t>(sum);
+            sum += c[w];
         }
-        if (lane == 31) part[warp] = v;
+        totals[d] = sum;
     }
-    __syncthreads();
-    if (threadIdx.x < kBins) {
-        for (uint32_t w = 0; w < warp; ++w) v += part[w];
-        totals[threadIdx.x] = v - own;
-    }
-    __syncthreads();
 }
-
-struct SortShared {
-    uint32_t key[kTile];
-    uint16_t order[kTile];
-    uint16_t counts[32][kBins];
-    uint32_t totals[kBins];
-    uint32_t part[32];
-};
 
 struct ZeroParams {
     void *p;                                    // vocab x dim
@@ -159,19 +141,12 @@ struct ZeroParams {
     uint32_t dtype, vec;
 };
 
-struct SortParams {
-    Ids ids;
-    uint32_t *key, *order;
-    uint32_t bits;                              // of a key, vocab among them
-    ZeroParams zero;
-};
-
-// Zeroes rows v0 .. v0 + kZeroRows - 1 of the table but those set in `taken`.
-__device__ __forceinline__ void zero_rows(const ZeroParams &Z, uint32_t vocab, uint64_t v0, const uint32_t *taken)
+// Zeroes rows v0 .. v0 + rows - 1 of the table but those set in `taken`.
+__device__ __forceinline__ void zero_rows(const ZeroParams &Z, uint64_t v0, uint32_t rows, const uint32_t *taken)
 {
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const uint64_t size = Z.dtype == ASR_BF16 ? 2 : 4, bytes = Z.dim * size;
-    for (uint32_t r = warp; r < kZeroRows && v0 + r < vocab; r += warps) {
+    for (uint32_t r = warp; r < rows; r += warps) {
         if ((taken[r >> 5] >> (r & 31)) & 1) continue;
         char *p = static_cast<char *>(Z.p) + (v0 + r) * bytes;
         if (Z.vec) {
@@ -184,59 +159,130 @@ __device__ __forceinline__ void zero_rows(const ZeroParams &Z, uint32_t vocab, u
     }
 }
 
-// Up to kTile tokens: block 0 sorts, the others zero the rows that no token has.
-__global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constant__ SortParams P)
+struct SortParams {
+    Ids ids;
+    uint32_t *key, *order;
+    uint32_t passes, width;                     // digits of a key (vocab among them) and their bits
+    uint32_t log_rounds;                        // of 32 keys a warp
+    uint32_t rows;                              // a block zeroes
+    uint32_t *arrived, counters;                // zeroed for the sums
+    ZeroParams zero;
+};
+
+struct __align__(16) SortShared {
+    uint64_t item[kSortThreads * kSortRounds];  // keys and where they came from
+    uint16_t counts[kSortThreads / 32][kBins];
+    uint32_t totals[kBins], base[kBins];        // of this block; places of its keys of each digit
+    uint32_t part[kSortThreads / 32];
+    uint32_t taken[kZeroRows / 32];
+};
+
+__device__ __forceinline__ uint4 remote_words(uint32_t addr)
 {
-    extern __shared__ __align__(16) unsigned char raw[];
-    if (blockIdx.x > 0) {
-        uint32_t *taken = reinterpret_cast<uint32_t *>(raw);
-        const uint64_t v0 = (blockIdx.x - 1) * static_cast<uint64_t>(kZeroRows);
-        if (threadIdx.x < kZeroRows / 32) taken[threadIdx.x] = 0;
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// Up to kSort tokens: the first cluster sorts, the other blocks zero rows that no token
+// has.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
+    sort_kernel(const __grid_constant__ SortParams P)
+{
+    __shared__ SortShared S;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x >= kCluster) {
+        const uint64_t v0 = (blockIdx.x - kCluster) * static_cast<uint64_t>(P.rows);
+        if (v0 >= P.ids.vocab) return;
+        const uint32_t rows = P.ids.vocab - v0 < P.rows ? static_cast<uint32_t>(P.ids.vocab - v0) : P.rows;
+        if (threadIdx.x < kZeroRows / 32) S.taken[threadIdx.x] = 0;
         __syncthreads();
+#pragma unroll 4
         for (uint64_t t = threadIdx.x; t < P.ids.n; t += kSortThreads) {
             const uint64_t d = key_of(P.ids, t) - v0;
-            if (d < kZeroRows) atomicOr(taken + (d >> 5), 1u << (d & 31));
+            if (d < rows) atomicOr(S.taken + (d >> 5), 1u << (d & 31));
         }
         __syncthreads();
-        zero_rows(P.zero, P.ids.vocab, v0, taken);
+        zero_rows(P.zero, v0, rows, S.taken);
         return;
     }
-    SortShared &S = *reinterpret_cast<SortShared *>(raw);
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = static_cast<uint32_t>(P.ids.n);
-    uint32_t key[kRounds], live = 0;
-    uint16_t from[kRounds], rank[kRounds];
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = blockIdx.x;
+    const uint32_t n = static_cast<uint32_t>(P.ids.n), rounds = 1u << P.log_rounds, log_share = 8 + P.log_rounds;
+    const uint32_t at = warp * rounds * 32 + lane, bins = 1u << P.width;       // place in the block's share
+    static_assert(kSortThreads == 1 << 8, "a block's share is 2^log_share keys");
+    for (uint32_t i = block * kSortThreads + threadIdx.x; i < P.counters; i += kCluster * kSortThreads) P.arrived[i] = 0;
+    uint32_t key[kSortRounds], live = 0;
+    uint16_t from[kSortRounds], rank[kSortRounds];
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-        const uint32_t t = warp * 256 + r * 32 + lane;
+    for (int r = 0; r < kSortRounds; ++r) {
+        const uint32_t t = (block << log_share) + at + r * 32;
         key[r] = 0;
         from[r] = static_cast<uint16_t>(t);
-        if (t < n) live |= 1u << r, key[r] = key_of(P.ids, t);
+        if (r < rounds && t < n) live |= 1u << r, key[r] = key_of(P.ids, t);
     }
-    for (uint32_t shift = 0; shift < P.bits; shift += kDigitBits) {
-        rank_digits(key, live, shift, S.counts, S.totals, rank);
-        scan_bins(S.totals, S.part);
+    for (uint32_t pass = 0, shift = 0; pass < P.passes; ++pass, shift += P.width) {
+        rank_digits<kSortRounds, kSortThreads / 32>(key, live, rounds, shift, bins, S.counts, S.totals, rank);
+        gemm::cluster_sync();
+        // four digits a thread: all blocks' keys of them, those of the blocks before, and the digits before
+        uint32_t all[4] = {}, before[4] = {};
+        if (threadIdx.x * 4 < bins) {
+            uint4 c[kCluster];
 #pragma unroll
-        for (int r = 0; r < kRounds; ++r)
-            if ((live >> r) & 1) {
-                const uint32_t d = (key[r] >> shift) & (kBins - 1), to = S.totals[d] + S.counts[warp][d] + rank[r];
-                S.key[to] = key[r];
-                S.order[to] = from[r];
+            for (int b = 0; b < kCluster; ++b) c[b] = remote_words(gemm::peer_addr(smem_addr(S.totals + threadIdx.x * 4), b));
+#pragma unroll
+            for (int b = 0; b < kCluster; ++b) {
+                const uint32_t w[4] = {c[b].x, c[b].y, c[b].z, c[b].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t k = threadIdx.x * 4 + i < bins ? w[i] : 0;
+                    all[i] += k;
+                    before[i] += b < block ? k : 0;
+                }
             }
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < kRounds; ++r)
-            if ((live >> r) & 1) {
-                key[r] = S.key[warp * 256 + r * 32 + lane];
-                from[r] = S.order[warp * 256 + r * 32 + lane];
-            }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r)
-        if ((live >> r) & 1) {
-            P.key[warp * 256 + r * 32 + lane] = key[r];
-            P.order[warp * 256 + r * 32 + lane] = from[r];
         }
+        const uint32_t own = all[0] + all[1] + all[2] + all[3];
+        uint32_t v = own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+            if (lane >= static_cast<uint32_t>(d)) v += o;
+        }
+        if (lane == 31) S.part[warp] = v;
+        __syncthreads();
+        v -= own;
+        for (uint32_t w = 0; w < warp; ++w) v += S.part[w];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            S.base[threadIdx.x * 4 + i] = v + before[i];
+            v += all[i];
+        }
+        __syncthreads();
+        const bool last = pass + 1 == P.passes;
+#pragma unroll
+        for (int r = 0; r < kSortRounds; ++r)
+            if ((live >> r) & 1) {
+                const uint32_t d = (key[r] >> shift) & (bins - 1), to = S.base[d] + S.counts[warp][d] + rank[r];
+                if (last) {
+                    P.key[to] = key[r];
+                    P.order[to] = from[r];
+                } else {
+                    const uint32_t p = gemm::peer_addr(smem_addr(S.item + (to & ((1u << log_share) - 1))), to >> log_share);
+                    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(p),
+                                 "l"(static_cast<uint64_t>(key[r]) << 32 | from[r]) : "memory");
+                }
+            }
+        // what the others read of this block has been read, and what they hand it is there
+        gemm::cluster_sync();
+        if (last) break;
+#pragma unroll
+        for (int r = 0; r < kSortRounds; ++r)
+            if ((live >> r) & 1) {
+                const uint64_t v = S.item[at + r * 32];
+                key[r] = static_cast<uint32_t>(v >> 32);
+                from[r] = static_cast<uint16_t>(v);
+            }
+    }
 }
 
 // More tokens: one digit's counts of each tile, their places, and the moves.
@@ -245,34 +291,41 @@ struct TileParams {
     const uint32_t *key, *order;                // later ones
     uint32_t *key_out, *order_out;
     uint32_t *counts;                           // [bin][tile]
-    uint32_t tiles, shift, first;
+    uint32_t tiles, shift, bins, first;
+    uint32_t *arrived, counters;                // zeroed for the sums, with the first digit
 };
 
-__global__ void __launch_bounds__(kSortThreads) tile_count_kernel(const __grid_constant__ TileParams P)
+__global__ void __launch_bounds__(kTileThreads) tile_count_kernel(const __grid_constant__ TileParams P)
 {
     __shared__ uint32_t bins[kBins];
-    for (uint32_t i = threadIdx.x; i < kBins; i += kSortThreads) bins[i] = 0;
+    for (uint32_t i = threadIdx.x; i < P.bins; i += kTileThreads) bins[i] = 0;
     __syncthreads();
-    for (int r = 0; r < kRounds; ++r) {
-        const uint64_t t = blockIdx.x * static_cast<uint64_t>(kTile) + r * kSortThreads + threadIdx.x;
-        if (t < P.ids.n) atomicAdd(bins + (((P.first ? key_of(P.ids, t) : P.key[t]) >> P.shift) & (kBins - 1)), 1u);
+    if (P.first)
+        for (uint32_t i = blockIdx.x * kTileThreads + threadIdx.x; i < P.counters; i += gridDim.x * kTileThreads) P.arrived[i] = 0;
+    for (int r = 0; r < kTileRounds; ++r) {
+        const uint64_t t = blockIdx.x * static_cast<uint64_t>(kTile) + r * kTileThreads + threadIdx.x;
+        if (t < P.ids.n) atomicAdd(bins + (((P.first ? key_of(P.ids, t) : P.key[t]) >> P.shift) & (P.bins - 1)), 1u);
     }
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < kBins; i += kSortThreads) P.counts[i * static_cast<uint64_t>(P.tiles) + blockIdx.x] = bins[i];
+    for (uint32_t i = threadIdx.x; i < P.bins; i += kTileThreads) P.counts[i * static_cast<uint64_t>(P.tiles) + blockIdx.x] = bins[i];
 }
 
 // Every count becomes the sum of those before it: one block.
-__global__ void __launch_bounds__(kSortThreads) tile_scan_kernel(const __grid_constant__ TileParams P)
+constexpr int kScanThreads = 1024;
+
+__global__ void __launch_bounds__(kScanThreads) tile_scan_kernel(const __grid_constant__ TileParams P)
 {
     __shared__ uint32_t part[32];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint64_t n = static_cast<uint64_t>(kBins) * P.tiles;
+    const uint64_t n = static_cast<uint64_t>(P.bins) * P.tiles;
     uint32_t carry = 0;
-    for (uint64_t at = 0; at < n; at += kSortThreads * 4) {
-        const uint64_t i = at + threadIdx.x * 4;            // n is a multiple of 4
-        uint4 c = make_uint4(0, 0, 0, 0);
-        if (i < n) c = *reinterpret_cast<const uint4 *>(P.counts + i);
-        const uint32_t own = c.x + c.y + c.z + c.w;
+    for (uint64_t at = 0; at < n; at += kScanThreads * 4) {
+        const uint64_t i = at + threadIdx.x * 4;            // n is a multiple of 4 or less than it
+        uint32_t c[4] = {};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i + k < n) c[k] = P.counts[i + k];
+        const uint32_t own = c[0] + c[1] + c[2] + c[3];
         uint32_t v = own;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -282,31 +335,37 @@ __global__ void __launch_bounds__(kSortThreads) tile_scan_kernel(const __grid_co
         __syncthreads();
         if (lane == 31) part[warp] = v;
         __syncthreads();
-        uint32_t before = 0, total = 0;
-        for (uint32_t w = 0; w < 32; ++w) {
-            before += w < warp ? part[w] : 0;
-            total += part[w];
+        uint32_t mine = part[lane], before = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, before, d);
+            if (lane >= static_cast<uint32_t>(d)) before += o;
         }
-        v += carry + before - own;
+        const uint32_t total = __shfl_sync(0xFFFFFFFFu, before, 31);
+        v += carry + __shfl_sync(0xFFFFFFFFu, before - mine, warp) - own;
         carry += total;
-        if (i < n) *reinterpret_cast<uint4 *>(P.counts + i) = make_uint4(v, v + c.x, v + c.x + c.y, v + c.x + c.y + c.z);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (i + k < n) P.counts[i + k] = v;
+            v += c[k];
+        }
     }
 }
 
 struct TileShared {
-    uint16_t counts[32][kBins];
+    uint16_t counts[kTileThreads / 32][kBins];
     uint32_t totals[kBins];
 };
 
-__global__ void __launch_bounds__(kSortThreads) tile_move_kernel(const __grid_constant__ TileParams P)
+__global__ void __launch_bounds__(kTileThreads) tile_move_kernel(const __grid_constant__ TileParams P)
 {
     __shared__ TileShared S;
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint64_t t0 = blockIdx.x * static_cast<uint64_t>(kTile) + warp * 256 + lane;
-    uint32_t key[kRounds], from[kRounds], live = 0;
-    uint16_t rank[kRounds];
+    const uint32_t warp = threadIdx.x >> 5;
+    const uint64_t t0 = blockIdx.x * static_cast<uint64_t>(kTile) + warp * (kTileRounds * 32) + (threadIdx.x & 31);
+    uint32_t key[kTileRounds], from[kTileRounds], live = 0;
+    uint16_t rank[kTileRounds];
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
+    for (int r = 0; r < kTileRounds; ++r) {
         const uint64_t t = t0 + r * 32;
         key[r] = from[r] = 0;
         if (t < P.ids.n) {
@@ -315,11 +374,12 @@ __global__ void __launch_bounds__(kSortThreads) tile_move_kernel(const __grid_co
             from[r] = P.first ? static_cast<uint32_t>(t) : P.order[t];
         }
     }
-    rank_digits(key, live, P.shift, S.counts, S.totals, rank);
+    rank_digits<kTileRounds, kTileThreads / 32>(key, live, kTileRounds, P.shift, P.bins, S.counts, S.totals, rank);
+    __syncthreads();
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r)
+    for (int r = 0; r < kTileRounds; ++r)
         if ((live >> r) & 1) {
-            const uint32_t d = (key[r] >> P.shift) & (kBins - 1);
+            const uint32_t d = (key[r] >> P.shift) & (P.bins - 1);
             const uint64_t to = static_cast<uint64_t>(P.counts[d * static_cast<uint64_t>(P.tiles) + blockIdx.x]) +
                                 S.counts[warp][d] + rank[r];
             P.key_out[to] = key[r];
@@ -327,39 +387,20 @@ __global__ void __launch_bounds__(kSortThreads) tile_move_kernel(const __grid_co
         }
 }
 
-// The first place in the sorted keys that holds `key` or more.
+// The first place in the sorted keys that holds `key` or more: 33 parts a step, by a warp.
 __device__ __forceinline__ uint64_t lower_bound(const uint32_t *keys, uint64_t n, uint64_t key)
 {
-    uint64_t lo = 0, hi = n;
+    const uint32_t lane = threadIdx.x & 31;
+    uint64_t lo = 0, hi = n;                    // keys before lo are less, from hi on not
     while (lo < hi) {
-        const uint64_t mid = (lo + hi) / 2;
-        if (keys[mid] < key) lo = mid + 1;
-        else hi = mid;
+        const uint64_t part = (hi - lo + 32) / 33, at = lo + (lane + 1) * part - 1;
+        const bool less = at < hi && keys[at] < key;
+        const uint32_t below = __popc(__ballot_sync(0xFFFFFFFFu, less));
+        const uint64_t end = lo + (below + 1) * part - 1;
+        lo += below * part;
+        hi = below < 32 && end < hi ? end : hi;
     }
     return lo;
-}
-
-struct SparseZeroParams {
-    const uint32_t *key;
-    uint64_t n;
-    uint32_t vocab;
-    ZeroParams zero;
-};
-
-// Zeroes the rows without tokens once the keys are sorted.
-__global__ void __launch_bounds__(kThreads) zero_kernel(const __grid_constant__ SparseZeroParams P)
-{
-    __shared__ uint32_t taken[kZeroRows / 32];
-    const uint64_t v0 = blockIdx.x * static_cast<uint64_t>(kZeroRows);
-    if (threadIdx.x < kZeroRows / 32) taken[threadIdx.x] = 0;
-    __syncthreads();
-    const uint64_t lo = lower_bound(P.key, P.n, v0), hi = lower_bound(P.key, P.n, v0 + kZeroRows);
-    for (uint64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
-        const uint32_t d = P.key[i] - static_cast<uint32_t>(v0);
-        atomicOr(taken + (d >> 5), 1u << (d & 31));
-    }
-    __syncthreads();
-    zero_rows(P.zero, P.vocab, v0, taken);
 }
 
 // ---- sums
@@ -367,29 +408,16 @@ __global__ void __launch_bounds__(kThreads) zero_kernel(const __grid_constant__ 
 struct SumParams {
     const uint32_t *key, *order;
     uint64_t n;                                 // tokens
-    uint32_t chunk, chunks, vocab;
-    uint64_t dim;
+    uint32_t chunk, chunks, slices, vocab;
+    uint64_t dim, pitch;                        // of a row of sums
     kept::Matrix dy;
     kept::Out out;
-    float *head, *tail;                         // [chunk][dim]: sums of a row that began before, that goes on after
+    float *head, *tail;                         // [chunk][pitch]: sums of a row that began before, that goes on after
+    uint32_t *arrived;                          // [chunk][slice]: blocks that have left theirs of the row that goes on there
     float scale;
+    uint32_t zero_from;                         // rows before are zeroed already
+    ZeroParams zero;
 };
-
-// What is known of a chunk's ends.
-struct Ends {
-    uint64_t begin, end;
-    bool open, on;                              // its first key began before; its last goes on after
-};
-
-__device__ __forceinline__ Ends ends_of(const SumParams &P, uint64_t c)
-{
-    Ends E;
-    E.begin = c * P.chunk;
-    E.end = E.begin + P.chunk < P.n ? E.begin + P.chunk : P.n;
-    E.open = c > 0 && P.key[E.begin - 1] == P.key[E.begin];
-    E.on = E.end < P.n && P.key[E.end] == P.key[E.end - 1];
-    return E;
-}
 
 template <int OT>
 __device__ __forceinline__ void store_row(const SumParams &P, uint32_t row, uint64_t col, int live, float v[8])
@@ -399,76 +427,150 @@ __device__ __forceinline__ void store_row(const SumParams &P, uint32_t row, uint
     kept::store8<OT>(P.out.p, row * P.out.ld + col, live, P.out.vec, v);
 }
 
-__device__ __forceinline__ void store_sum(float *p, uint64_t dim, uint64_t c, uint64_t col, int live, const float v[8])
+__device__ __forceinline__ void store_sum(float *p, const float v[8])
 {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < live) p[c * dim + col + i] = v[i];
+    __stcg(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
+    __stcg(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
 }
 
-// A block a chunk and 8 columns a thread.
-constexpr int kAhead = 4;                       // rows loaded before they are added up
+__device__ __forceinline__ void add_sum(float acc[8], const float *p)
+{
+    const float4 a = __ldcg(reinterpret_cast<const float4 *>(p)), b = __ldcg(reinterpret_cast<const float4 *>(p) + 1);
+    acc[0] = __fadd_rn(acc[0], a.x), acc[1] = __fadd_rn(acc[1], a.y), acc[2] = __fadd_rn(acc[2], a.z);
+    acc[3] = __fadd_rn(acc[3], a.w), acc[4] = __fadd_rn(acc[4], b.x), acc[5] = __fadd_rn(acc[5], b.y);
+    acc[6] = __fadd_rn(acc[6], b.z), acc[7] = __fadd_rn(acc[7], b.w);
+}
+
+// Block c has left its sum of `row`, which reaches over chunks' ends (`began`: from
+// before this one).  The last one to do so adds them all up: of the chunk where the row
+// begins its tail, of the others their heads, in order.  All threads of the block come
+// here together.
+template <int OT>
+__device__ __forceinline__ void join(const SumParams &P, uint32_t c, uint32_t row, bool began, uint32_t slice, uint64_t col,
+                                     int live)
+{
+    __shared__ uint32_t ends[2], before;
+    __threadfence();                            // what this thread has left, before its block is counted
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        // the chunks that begin with the row follow one another: 32 a look
+        uint32_t first = c, last = c;
+        for (uint32_t up = 32, down = began ? 32 : 0; up == 32 || down == 32;) {
+            const uint64_t d = static_cast<uint64_t>(last) + 1 + threadIdx.x;
+            const uint32_t e = first - threadIdx.x;
+            const bool after = up == 32 && d < P.chunks && P.key[d * P.chunk] == row;
+            const bool before = down == 32 && threadIdx.x < first && P.key[static_cast<uint64_t>(e) * P.chunk - 1] == row;
+            up = __popc(__ballot_sync(0xFFFFFFFFu, after));
+            down = __popc(__ballot_sync(0xFFFFFFFFu, before));
+            last += up;
+            first -= down;
+        }
+        if (threadIdx.x == 0) {
+            ends[0] = first;
+            ends[1] = last;
+            before = atomicAdd(P.arrived + static_cast<uint64_t>(first) * P.slices + slice, 1u);
+            __threadfence();
+        }
+    }
+    __syncthreads();
+    const uint32_t first = ends[0], last = ends[1];
+    if (before != last - first || live == 0) return;
+    float acc[8] = {};
+    add_sum(acc, P.tail + first * P.pitch + col);
+#pragma unroll 8
+    for (uint32_t d = first + 1; d <= last; ++d) add_sum(acc, P.head + d * P.pitch + col);
+    store_row<OT>(P, row, col, live, acc);
+}
+
+// A block a chunk and a slice of the columns, eight a thread; the blocks behind those
+// zero rows without tokens.
+constexpr int kSumThreads = 128;                // at most
+constexpr int kPiece = 64;                      // tokens whose keys are at hand
 
 template <int DT, int OT>
-__global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ SumParams P)
+__global__ void __launch_bounds__(kSumThreads, 6) sum_kernel(const __grid_constant__ SumParams P)
 {
-    const uint64_t c = blockIdx.x, col = (blockIdx.y * static_cast<uint64_t>(blockDim.x) + threadIdx.x) * 8;
+    constexpr int kAhead = DT == ASR_BF16 ? 8 : 4;          // rows fetched before they are added up
+    __shared__ uint32_t key[kPiece + 2], order[kPiece];     // keys from the one before on
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint32_t sums = P.chunks * P.slices;
+    if (blockIdx.x >= sums) {
+        const uint64_t v0 = P.zero_from + (blockIdx.x - sums) * static_cast<uint64_t>(kZeroRows);
+        const uint32_t rows = P.vocab - v0 < kZeroRows ? static_cast<uint32_t>(P.vocab - v0) : kZeroRows;
+        uint32_t *taken = key;
+        if (threadIdx.x < kZeroRows / 32) taken[threadIdx.x] = 0;
+        __syncthreads();
+        const uint64_t lo = lower_bound(P.key, P.n, v0), hi = lower_bound(P.key, P.n, v0 + rows);
+        // a row's tokens may be many: each is looked for on its own
+        for (uint32_t d = threadIdx.x; d < rows; d += blockDim.x) {
+            uint64_t a = lo, b = hi;
+            while (a < b) {
+                const uint64_t mid = (a + b) / 2;
+                if (P.key[mid] < v0 + d) a = mid + 1;
+                else b = mid;
+            }
+            if (a < hi && P.key[a] == v0 + d) atomicOr(taken + (d >> 5), 1u << (d & 31));
+        }
+        __syncthreads();
+        zero_rows(P.zero, v0, rows, taken);
+        return;
+    }
+    const uint32_t c = blockIdx.x / P.slices, slice = blockIdx.x % P.slices;
+    const uint64_t col = (slice * static_cast<uint64_t>(blockDim.x) + threadIdx.x) * 8;
     const int live = live_of(P.dim, col);
-    const Ends E = ends_of(P, c);
+    const uint64_t begin = static_cast<uint64_t>(c) * P.chunk, end = begin + P.chunk < P.n ? begin + P.chunk : P.n;
     float acc[8] = {};
     bool first = true;                          // still in the chunk's first row
-    for (uint64_t i0 = E.begin; i0 < E.end; i0 += kAhead) {
-        uint32_t key[kAhead + 1];
-        float v[kAhead][8];
-#pragma unroll
-        for (int a = 0; a <= kAhead; ++a) key[a] = i0 + a < P.n ? P.key[i0 + a] : P.vocab;
-#pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-            const bool in = i0 + a < E.end && key[a] < P.vocab;
-            muon::load8(P.dy.p, DT, in ? P.order[i0 + a] * P.dy.ld + col : 0, in ? live : 0, P.dy.vec, v[a]);
+    bool began = false, goes_on = false;        // that one before the chunk; the last one after it
+    uint32_t front = 0, back = 0;
+    for (uint64_t i0 = begin; i0 < end; i0 += kPiece) {
+        const uint32_t n = end - i0 < kPiece ? static_cast<uint32_t>(end - i0) : kPiece;
+        __syncthreads();
+        for (uint32_t j = threadIdx.x; j < kPiece + 2; j += blockDim.x) {
+            const uint64_t i = i0 + j;          // of the key before place i0 + j - 1's
+            key[j] = j <= n + 1 && i > 0 && i <= P.n ? P.key[i - 1] : P.vocab;
+            if (j < kPiece) order[j] = j < n ? P.order[i0 + j] : 0;
         }
+        __syncthreads();
+        const uint32_t *const at = key + 1;
+        if (i0 == begin) {
+            front = at[0];
+            began = begin > 0 && key[0] == front;
+        }
+        back = at[n - 1];
+        goes_on = i0 + n < P.n && at[n] == back;
+        for (uint32_t a0 = 0; a0 < n && at[a0] < P.vocab; a0 += kAhead) {
+            kept::Raw<DT> raw[kAhead];
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-            if (i0 + a >= E.end || key[a] >= P.vocab) break;
+            for (int a = 0; a < kAhead; ++a) {
+                const bool in = a0 + a < n && at[a0 + a] < P.vocab;
+                raw[a] = kept::fetch<DT>(P.dy.p, in ? order[a0 + a] * P.dy.ld + col : 0, in ? live : 0, P.dy.vec);
+            }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], v[a][i]);
-            const bool last = i0 + a + 1 == E.end;
-            if (!last && key[a + 1] == key[a]) continue;
-            if (first && E.open) store_sum(P.head, P.dim, c, col, live, acc);
-            else if (last && E.on) store_sum(P.tail, P.dim, c, col, live, acc);
-            else store_row<OT>(P, key[a], col, live, acc);
-            first = false;
+            for (int a = 0; a < kAhead; ++a) {
+                if (a0 + a >= n || at[a0 + a] >= P.vocab) break;
+                float v[8];
+                kept::values(raw[a], v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+                for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], v[i]);
+                const bool last = i0 + a0 + a + 1 == end;
+                if (!last && at[a0 + a + 1] == at[a0 + a]) continue;
+                if (first && began) {
+                    if (live) store_sum(P.head + c * P.pitch + col, acc);
+                } else if (last && goes_on) {
+                    if (live) store_sum(P.tail + c * P.pitch + col, acc);
+                } else {
+                    store_row<OT>(P, at[a0 + a], col, live, acc);
+                }
+                first = false;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+            }
         }
     }
-}
-
-// Rows that reach over chunks' ends, by the chunk where they begin: the sum there
-// and those of the chunks that go on with it, in order.
-template <int OT>
-__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ SumParams P)
-{
-    const uint64_t c = blockIdx.x, col = (blockIdx.y * static_cast<uint64_t>(blockDim.x) + threadIdx.x) * 8;
-    const int live = live_of(P.dim, col);
-    const Ends E = ends_of(P, c);
-    const uint32_t key = P.key[E.end - 1];
-    if (!E.on || key >= P.vocab || (E.open && P.key[E.begin] == key)) return;
-    // how many chunks go on with it: they follow one another
-    uint64_t last = c + 1;
-    for (int more = static_cast<int>(blockDim.x); more == static_cast<int>(blockDim.x); last += more) {
-        const uint64_t d = last + threadIdx.x;
-        more = __syncthreads_count(d < P.chunks && P.key[d * P.chunk] == key);
-    }
-    float acc[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = i < live ? P.tail[c * P.dim + col + i] : 0.0f;
-#pragma unroll 4
-    for (uint64_t d = c + 1; d < last; ++d)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < live) acc[i] = __fadd_rn(acc[i], P.head[d * P.dim + col + i]);
-    store_row<OT>(P, key, col, live, acc);
+    // the chunk's first row, if it began before, and its last, if that goes on and is not the same
+    if (began && front < P.vocab) join<OT>(P, c, front, true, slice, col, live);
+    if (goes_on && back < P.vocab && !(began && front == back)) join<OT>(P, c, back, false, slice, col, live);
 }
 
 // ------------------------------------------------------------------ host
@@ -490,19 +592,10 @@ Ids ids_of(const void *ids, int32_t index, uint64_t tokens, uint64_t vocab, int6
 
 asr_status setup()
 {
-    static std::atomic<uint64_t> ready{0}, opted{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
-    if (e == cudaSuccess && !(opted.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SortShared));
-        if (e == cudaSuccess) opted.fetch_or(bit, std::memory_order_release);
-    }
-    if (e != cudaSuccess) return cuda_fail(e);
+    static std::atomic<uint64_t> ready{0};
     return kept::load_once(ready, lookup_kernel<ASR_F32>, lookup_kernel<ASR_BF16>, sort_kernel, tile_count_kernel,
-                           tile_scan_kernel, tile_move_kernel, zero_kernel, sum_kernel<ASR_F32, ASR_F32>,
-                           sum_kernel<ASR_F32, ASR_BF16>, sum_kernel<ASR_BF16, ASR_F32>, sum_kernel<ASR_BF16, ASR_BF16>,
-                           join_kernel<ASR_F32>, join_kernel<ASR_BF16>);
+                           tile_scan_kernel, tile_move_kernel, sum_kernel<ASR_F32, ASR_F32>,
+                           sum_kernel<ASR_F32, ASR_BF16>, sum_kernel<ASR_BF16, ASR_F32>, sum_kernel<ASR_BF16, ASR_BF16>);
 }
 
 asr_status lookup(const void *ids, int32_t index, uint64_t tokens, const void *table, uint64_t table_ld, uint64_t vocab,
@@ -526,17 +619,27 @@ asr_status lookup(const void *ids, int32_t index, uint64_t tokens, const void *t
     return kept::walk(ASR_KERNEL_EMBEDDING, kernel, P, tokens, dim, kept::kSpan, stream);
 }
 
-// Chunks of eight tokens, longer where there would be more than 4,096 of them: what
-// reaches over their ends takes 2 dim sums of workspace each.
-uint32_t chunk_of(uint64_t tokens)
+// Columns go to blocks of up to 128 threads, and tokens to chunks that make 1,216
+// blocks (eight an SM) or more, of 8 to 64 tokens: shorter ones leave more sums in the
+// workspace, longer ones are too few.  Never more than 8,192 chunks, each of which
+// takes two rows of sums.
+unsigned threads_of(uint64_t dim)
 {
-    const uint64_t c = (tokens + 4095) / 4096;
-    return static_cast<uint32_t>(c < 8 ? 8 : (c + kAhead - 1) / kAhead * kAhead);
+    return dim >= kSumThreads * 8 ? kSumThreads : static_cast<unsigned>((dim + 255) / 256 * 32);
+}
+
+uint64_t slices_of(uint64_t dim) { return (dim + threads_of(dim) * 8 - 1) / (threads_of(dim) * 8); }
+
+uint32_t chunk_of(uint64_t tokens, uint64_t dim)
+{
+    const uint64_t even = (tokens * slices_of(dim) / 1216 + 7) / 8 * 8, least = (tokens + 8191) / 8192;
+    const uint64_t c = even < 8 ? 8 : even > 64 ? 64 : even;
+    return static_cast<uint32_t>(c < least ? least : c);
 }
 
 struct Layout {
-    uint64_t key[2], order[2], counts, head, tail, bytes;
-    uint32_t tiles;
+    uint64_t key[2], order[2], counts, arrived, head, tail, bytes;
+    uint32_t tiles, counters;                   // no tiles: one cluster sorts
 };
 
 Layout layout(uint64_t tokens, uint64_t dim)
@@ -548,16 +651,18 @@ Layout layout(uint64_t tokens, uint64_t dim)
         at += muon::up(bytes, 256);
         return was;
     };
-    L.tiles = static_cast<uint32_t>((tokens + kTile - 1) / kTile);
-    const uint64_t chunks = (tokens + chunk_of(tokens) - 1) / chunk_of(tokens);
+    L.tiles = tokens <= kSort ? 0 : static_cast<uint32_t>((tokens + kTile - 1) / kTile);
+    const uint64_t chunk = chunk_of(tokens, dim), chunks = (tokens + chunk - 1) / chunk;
     for (int i = 0; i < 2; ++i) {
-        const bool used = i == 0 || L.tiles > 1;
+        const bool used = i == 0 || L.tiles;
         L.key[i] = take(used ? tokens * 4 : 0);
         L.order[i] = take(used ? tokens * 4 : 0);
     }
-    L.counts = take(L.tiles > 1 ? static_cast<uint64_t>(kBins) * L.tiles * 4 : 0);
-    L.head = take(chunks * dim * 4);
-    L.tail = take(chunks * dim * 4);
+    L.counts = take(static_cast<uint64_t>(kBins) * L.tiles * 4);
+    L.counters = static_cast<uint32_t>(chunks * slices_of(dim));
+    L.arrived = take(L.counters * 4ull);
+    L.head = take(chunks * muon::up(dim, 8) * 4);
+    L.tail = take(chunks * muon::up(dim, 8) * 4);
     L.bytes = at;
     return L;
 }
@@ -590,66 +695,84 @@ asr_status grads(const void *ids, int32_t index, uint64_t tokens, const void *dy
                        aligned16(dtable) && dim % (dtable_dtype == ASR_BF16 ? 8 : 4) == 0 ? 1u : 0u};
     uint32_t bits = 1;
     while ((vocab >> bits) != 0) ++bits;
-    const unsigned zero_blocks = static_cast<unsigned>((vocab + kZeroRows - 1) / kZeroRows);
+    const uint32_t passes = (bits + kDigitBits - 1) / kDigitBits, width = (bits + passes - 1) / passes;
     int now = 0;
-    if (L.tiles <= 1) {
+    uint64_t zeroed = 0;
+    if (L.tiles == 0) {
+        // as many zeros beside the sort as the GPU writes meanwhile: a block an SM
+        int dev = 0, sms = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return cuda_fail(e);
+        const uint64_t row = dim * (dtable_dtype == ASR_BF16 ? 2 : 4), fit = kZeroBytes / row;
         SortParams P;
         P.ids = I;
         P.key = words(L.key[0]);
         P.order = words(L.order[0]);
-        P.bits = bits;
+        P.passes = passes;
+        P.width = width;
+        P.log_rounds = 0;
+        while ((static_cast<uint64_t>(kCluster * kSortThreads) << P.log_rounds) < tokens) ++P.log_rounds;
+        P.rows = static_cast<uint32_t>(fit < 1 ? 1 : fit > kZeroRows ? kZeroRows : fit);
+        P.arrived = words(L.arrived);
+        P.counters = tokens ? L.counters : 0;
         P.zero = Z;
-        sort_kernel<<<zero_blocks + 1, kSortThreads, sizeof(SortShared), stream>>>(P);
+        const uint64_t all = (vocab + P.rows - 1) / P.rows, beside = tokens ? static_cast<uint64_t>(sms) : all;
+        const unsigned blocks = static_cast<unsigned>(all < beside ? all : beside);
+        zeroed = static_cast<uint64_t>(blocks) * P.rows;
+        sort_kernel<<<(kCluster + blocks + kCluster - 1) / kCluster * kCluster, kSortThreads, 0, stream>>>(P);
         st = launched(ASR_KERNEL_EMBEDDING);
     } else {
         TileParams P;
         P.ids = I;
         P.counts = words(L.counts);
         P.tiles = L.tiles;
-        for (uint32_t shift = 0; shift < bits && st == ASR_OK; shift += kDigitBits) {
-            P.shift = shift;
-            P.first = shift == 0;
+        P.bins = 1u << width;
+        P.arrived = words(L.arrived);
+        P.counters = L.counters;
+        for (uint32_t pass = 0; pass < passes; ++pass) {
+            P.shift = pass * width;
+            P.first = pass == 0;
             P.key = words(L.key[now]);
             P.order = words(L.order[now]);
             now ^= 1;
             P.key_out = words(L.key[now]);
             P.order_out = words(L.order[now]);
-            tile_count_kernel<<<L.tiles, kSortThreads, 0, stream>>>(P);
+            tile_count_kernel<<<L.tiles, kTileThreads, 0, stream>>>(P);
             st = launched(ASR_KERNEL_EMBEDDING);
             if (st != ASR_OK) return st;
-            tile_scan_kernel<<<1, kSortThreads, 0, stream>>>(P);
+            tile_scan_kernel<<<1, kScanThreads, 0, stream>>>(P);
             st = launched(ASR_KERNEL_EMBEDDING);
             if (st != ASR_OK) return st;
-            tile_move_kernel<<<L.tiles, kSortThreads, 0, stream>>>(P);
+            tile_move_kernel<<<L.tiles, kTileThreads, 0, stream>>>(P);
             st = launched(ASR_KERNEL_EMBEDDING);
+            if (st != ASR_OK) return st;
         }
-        if (st != ASR_OK) return st;
-        const SparseZeroParams P0{words(L.key[now]), tokens, static_cast<uint32_t>(vocab), Z};
-        zero_kernel<<<zero_blocks, kThreads, 0, stream>>>(P0);
-        st = launched(ASR_KERNEL_EMBEDDING);
     }
     if (st != ASR_OK || tokens == 0) return st;
     SumParams P;
     P.key = words(L.key[now]);
     P.order = words(L.order[now]);
     P.n = tokens;
-    P.chunk = chunk_of(tokens);
+    P.chunk = chunk_of(tokens, dim);
     P.chunks = static_cast<uint32_t>((tokens + P.chunk - 1) / P.chunk);
+    P.slices = static_cast<uint32_t>(slices_of(dim));
     P.vocab = static_cast<uint32_t>(vocab);
     P.dim = dim;
+    P.pitch = muon::up(dim, 8);
     P.dy = kept::matrix(dy, dy_ld);
     P.out = kept::out(dtable, dim);
     P.head = reinterpret_cast<float *>(w + L.head);
     P.tail = reinterpret_cast<float *>(w + L.tail);
+    P.arrived = words(L.arrived);
     P.scale = static_cast<float>(scale);
-    const unsigned threads = dim >= kThreads * 8 ? kThreads : static_cast<unsigned>((dim + 255) / 256 * 32);
-    const dim3 grid(P.chunks, static_cast<unsigned>((dim + threads * 8 - 1) / (threads * 8)));
+    P.zero_from = static_cast<uint32_t>(zeroed < vocab ? zeroed : vocab);
+    P.zero = Z;
+    const unsigned threads = threads_of(dim), sums = P.chunks * P.slices;
+    const unsigned zeros = static_cast<unsigned>((vocab - P.zero_from + kZeroRows - 1) / kZeroRows);
     const bool bf = dtable_dtype == ASR_BF16;
-    (dy_dtype == ASR_BF16 ? sums_of<ASR_BF16>(bf) : sums_of<ASR_F32>(bf))<<<grid, threads, 0, stream>>>(P);
-    st = launched(ASR_KERNEL_EMBEDDING);
-    if (st != ASR_OK) return st;
-    (bf ? join_kernel<ASR_BF16> : join_kernel<ASR_F32>)<<<grid, threads, 0, stream>>>(P);
-    return launched(ASR_KERNEL_EMBEDDING);
+    return prod::launch_early(ASR_KERNEL_EMBEDDING, dy_dtype == ASR_BF16 ? sums_of<ASR_BF16>(bf) : sums_of<ASR_F32>(bf),
+                              dim3(sums + zeros), threads, P, stream);
 }
 
 }  // namespace embed

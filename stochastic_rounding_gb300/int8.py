@@ -18,37 +18,87 @@ from typing import NamedTuple
 import torch
 from torch.autograd.function import once_differentiable
 
-from ._lib import (CHECKPOINT_GROUP, asr_checkpoint_int8, asr_linear_int8, asr_linear_int8_grads, asr_quantize_int8,
-                   asr_restore_int8, int8_empty)
+from . import _lib
+from ._lib import asr_linear_int8, asr_linear_int8_grads, asr_quantize_int8, int8_empty
 
 
 class Int8Checkpoint(NamedTuple):
-    """A matrix kept in 8 bits: codes, the power of two (plus 127) of each 32 of a
-    row's values, and the dtype of what it was made from."""
-    q: torch.Tensor
-    power: torch.Tensor
-    dtype: torch.dtype
+    """A matrix kept in 8 bits.  A row of ``data`` (uint8) holds its codes, up to a
+    multiple of 16 bytes, and behind them the power of two (plus 127) of each 32 of its
+    values."""
+    data: torch.Tensor
+    cols: int
+    dtype: torch.dtype                      # of what it was made from
+
+    @property
+    def q(self):
+        """The codes: int8, the matrix's shape."""
+        return self.data.view(torch.int8)[:, :self.cols]
+
+    @property
+    def power(self):
+        at = (self.cols + 15) // 16 * 16
+        return self.data[:, at:at + (self.cols + _lib.CHECKPOINT_GROUP - 1) // _lib.CHECKPOINT_GROUP]
+
+    def _struct(self, *key):
+        """For the library, with the key of its rounding where it is made."""
+        p, ld = self.data.data_ptr(), self.data.shape[1]
+        return _lib._pack_checkpoint(p, p + (self.cols + 15) // 16 * 16, ld, ld, *key)
 
 
 def empty_checkpoint(rows: int, cols: int, device, dtype) -> Int8Checkpoint:
     """An uninitialised checkpoint of a rows x cols matrix."""
-    power = torch.empty(rows, (cols + CHECKPOINT_GROUP - 1) // CHECKPOINT_GROUP, dtype=torch.uint8, device=device)
-    return Int8Checkpoint(int8_empty(rows, cols, device), power, dtype)
+    groups = (cols + _lib.CHECKPOINT_GROUP - 1) // _lib.CHECKPOINT_GROUP
+    width = (cols + 15) // 16 * 16 + (groups + 15) // 16 * 16
+    return Int8Checkpoint(torch.empty((rows, width), dtype=torch.uint8, device=device), cols, dtype)
+
+
+# The functions that return new tensors check what they are given and call the library
+# themselves: going through the calls that fill a caller's tensors would check the new
+# ones too, and cost as much again as the launch.
+
+_FLOATS = (torch.bfloat16, torch.float32)
 
 
 def checkpoint_int8(x, *, rounding="rne", base_index: int = 0, step: int = 0, seed: int = 0) -> Int8Checkpoint:
     """``x`` (2-D, float32 or bfloat16) kept in 8 bits for a backward pass: 32 values
     of a row share a power of two.  ``rounding="sr"`` rounds stochastically, so that
     what is read back is x on average (to within 2^-16 of a step)."""
-    c = empty_checkpoint(*x.shape, x.device, x.dtype)
-    asr_checkpoint_int8(x, c.q, c.power, rounding=rounding, base_index=base_index, step=step, seed=seed)
+    px, rows, cols, ld = _lib._matrix_ptr(x, "x", _FLOATS)
+    with _lib._on_device(x.device):
+        c = empty_checkpoint(rows, cols, x.device, x.dtype)
+        _lib._check(_lib.lib().asr_checkpoint_int8(px, _lib._dt(x), rows, cols, ld, c._struct(rounding, base_index, step, seed),
+                                                   _lib._raw_stream(x.get_device())), "asr_checkpoint_int8")
     return c
+
+
+def _checked(c: Int8Checkpoint, rows, cols, device):
+    """The C struct of a checkpoint that a caller gives."""
+    if not isinstance(c, Int8Checkpoint):
+        raise TypeError("an Int8Checkpoint is wanted")
+    t = c.data
+    if not t.is_cuda or t.dtype != torch.uint8 or t.dim() != 2 or not t.is_contiguous():
+        raise ValueError("a checkpoint's data must be a contiguous 2-D uint8 CUDA tensor")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"the checkpoint is on {t.device}; the call's other tensors are on cuda:{device}")
+    want = (cols + 15) // 16 * 16 + ((cols + 31) // 32 + 15) // 16 * 16
+    if c.cols != cols or t.shape[0] != rows or t.shape[1] != want:
+        raise ValueError(f"a checkpoint of {(rows, cols)} is wanted, not of {(t.shape[0], c.cols)} in {tuple(t.shape)}")
+    return c._struct()
 
 
 def restore_int8(checkpoint: Int8Checkpoint, dtype=None):
     """The values that a checkpoint stands for, in ``dtype`` (the original's unless given); exact in either."""
-    out = torch.empty(checkpoint.q.shape, dtype=dtype or checkpoint.dtype, device=checkpoint.q.device)
-    return asr_restore_int8(checkpoint.q, checkpoint.power, out)
+    dtype = dtype or checkpoint.dtype
+    if dtype not in _FLOATS:
+        raise TypeError(f"values come as float32 or bfloat16, not {dtype}")
+    t, cols = checkpoint.data, checkpoint.cols
+    s = _checked(checkpoint, t.shape[0], cols, None)
+    with _lib._on_device(t.device):
+        out = torch.empty((t.shape[0], cols), dtype=dtype, device=t.device)
+        _lib._check(_lib.lib().asr_restore_int8(s, t.shape[0], cols, out.data_ptr(), _lib._dt(out), cols,
+                                                _lib._raw_stream(t.get_device())), "asr_restore_int8")
+    return out
 
 
 def int8_linear(x, qweight, weight_scale, *, rounding="rne", step: int = 0, seed: int = 0, out=None):
@@ -83,11 +133,12 @@ class _Int8LinearFunction(torch.autograd.Function):
         ctx.key, ctx.x_dtype = (step, seed), x.dtype
         if save == "int8" and ctx.needs_input_grad[1]:
             kept = checkpoint_int8(x, rounding="sr", step=step, seed=seed)
-            ctx.save_for_backward(weight, kept.q, kept.power)
+            ctx.save_for_backward(weight, kept.data)
         elif save == "int8":                # dx does not read x
             ctx.save_for_backward(weight)
         else:
             ctx.save_for_backward(weight, x)
+        ctx.save = save
         q = int8_empty(*weight.shape, weight.device)
         scale = torch.empty(weight.shape[0], dtype=torch.float32, device=weight.device)
         asr_quantize_int8(weight, q, scale)
@@ -100,12 +151,12 @@ class _Int8LinearFunction(torch.autograd.Function):
         step, seed = ctx.key
         dy = dy.contiguous()
         need_dx, need_dw = ctx.needs_input_grad[:2]
-        if len(x) == 2:                     # what 8 bits stand for is exact in bf16
-            x = restore_int8(Int8Checkpoint(*x, torch.bfloat16))
-        elif x:
-            x = x[0]
-        else:
+        if not x:
             x = dy.new_empty(dy.shape[0], weight.shape[1])
+        elif ctx.save == "int8":            # what 8 bits stand for is exact in bf16
+            x = restore_int8(Int8Checkpoint(x[0], weight.shape[1], torch.bfloat16))
+        else:
+            x = x[0]
         dx, dw = int8_linear_grads(dy, x, weight, step=step, seed=seed, need_dx=need_dx, need_dw=need_dw)
         return (dx.to(ctx.x_dtype) if dx is not None else None, dw.to(weight.dtype) if dw is not None else None, None,
                 None, None)

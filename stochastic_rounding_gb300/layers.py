@@ -18,9 +18,8 @@ from typing import NamedTuple, Optional, Union
 import torch
 from torch.autograd.function import once_differentiable
 
-from ._lib import (asr_activation, asr_activation_grads, asr_embedding, asr_embedding_grads, asr_layer_norm,
-                   asr_layer_norm_grads)
-from .int8 import Int8Checkpoint, _by_rows, _CountedModule, empty_checkpoint
+from . import _lib
+from .int8 import _FLOATS, Int8Checkpoint, _by_rows, _checked, _CountedModule, empty_checkpoint
 
 _SAVE = (None, "input", "int8")
 
@@ -39,40 +38,63 @@ def activation(x, function="silu", *, gated=False, save=None, rounding="rne", st
     ``save`` returns (y, saved) for ``activation_grads``: "input" saves x itself,
     "int8" its 8-bit checkpoint, made in the same pass."""
     _check_save(save)
-    rows, width = x.shape
+    code = _lib._function(function)
+    px, rows, width, ld = _lib._matrix_ptr(x, "x", _FLOATS)
     if gated and width % 2:
         raise ValueError(f"a gated activation takes an even number of columns, not {width}")
-    y = torch.empty(rows, width // 2 if gated else width, dtype=x.dtype, device=x.device)
-    kept = empty_checkpoint(rows, width, x.device, x.dtype) if save == "int8" else None
-    asr_activation(x, y, function, gated=gated, keep=kept, rounding=rounding, step=step, seed=seed)
+    cols = width // 2 if gated else width
+    with _lib._on_device(x.device):
+        y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+        kept = empty_checkpoint(rows, width, x.device, x.dtype) if save == "int8" else None
+        _lib._check(_lib.lib().asr_activation(px, ld, y.data_ptr(), cols, _lib._dt(x), rows, cols, code, 1 if gated else 0,
+                                              None if kept is None else kept._struct(rounding, 0, step, seed),
+                                              _lib._raw_stream(x.get_device())), "asr_activation")
     return y if save is None else (y, x if kept is None else kept)
 
 
 def activation_grads(dy, saved: Union[torch.Tensor, Int8Checkpoint], function="silu", *, gated=False):
     """dx from ``dy`` and what ``activation`` saved."""
-    kept = saved if isinstance(saved, Int8Checkpoint) else None
-    dx = torch.empty(dy.shape[0], dy.shape[1] * (2 if gated else 1), dtype=dy.dtype, device=dy.device)
-    return asr_activation_grads(dy, saved if kept is None else None, dx, function, gated=gated, kept=kept)
+    code = _lib._function(function)
+    pg, rows, cols, g_ld = _lib._matrix_ptr(dy, "dy", _FLOATS)
+    width = 2 * cols if gated else cols
+    px, x_ld, kept = _saved_input(saved, rows, width, dy)
+    with _lib._on_device(dy.device):
+        dx = torch.empty((rows, width), dtype=dy.dtype, device=dy.device)
+        _lib._check(_lib.lib().asr_activation_grads(pg, g_ld, px, x_ld, kept, dx.data_ptr(), width, _lib._dt(dy), rows, cols,
+                                                    code, 1 if gated else 0, _lib._raw_stream(dy.get_device())),
+                    "asr_activation_grads")
+    return dx
+
+
+def _saved_input(saved, rows, cols, dy):
+    """(pointer, pitch, checkpoint) of what a forward pass saved, the pointer or the checkpoint None."""
+    if isinstance(saved, Int8Checkpoint):
+        return None, cols, _checked(saved, rows, cols, dy.get_device())
+    px, xr, xc, ld = _lib._matrix_ptr(saved, "the saved input", (dy.dtype,), dy.get_device())
+    if xr != rows or xc != cols:
+        raise ValueError(f"the saved input has shape {(xr, xc)}; expected {(rows, cols)}")
+    return px, ld, None
 
 
 class _ActivationFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, function, gated, save, rounding, step, seed):
         x = _by_rows(x)
-        ctx.kind = (function, gated)
-        ctx.x_dtype = x.dtype
+        ctx.kind = (function, gated, x.shape[1], x.dtype)
         if not ctx.needs_input_grad[0]:
             return activation(x, function, gated=gated)
         y, saved = activation(x, function, gated=gated, save=save, rounding=rounding, step=step, seed=seed)
-        ctx.save_for_backward(*(saved[:2] if save == "int8" else (saved,)))
+        ctx.kept = save == "int8"
+        ctx.save_for_backward(saved.data if ctx.kept else saved)
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        function, gated = ctx.kind
-        saved = ctx.saved_tensors
-        saved = Int8Checkpoint(*saved, ctx.x_dtype) if len(saved) == 2 else saved[0]
+        function, gated, width, dtype = ctx.kind
+        (saved,) = ctx.saved_tensors
+        if ctx.kept:
+            saved = Int8Checkpoint(saved, width, dtype)
         return activation_grads(_by_rows(dy), saved, function, gated=gated), None, None, None, None, None, None
 
 
@@ -107,8 +129,15 @@ class Activation(_CountedModule):
 class NormSaved(NamedTuple):
     """What a norm's backward pass reads."""
     input: Union[torch.Tensor, Int8Checkpoint]
-    mean: Optional[torch.Tensor]            # None if not centred
-    rstd: torch.Tensor
+    stats: torch.Tensor                     # float32, (1 or 2, rows): rstd, and, centred, the mean
+
+    @property
+    def rstd(self):
+        return self.stats[0]
+
+    @property
+    def mean(self):
+        return self.stats[1] if self.stats.shape[0] == 2 else None
 
 
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, centred=True, save=None, rounding="rne", step: int = 0,
@@ -118,16 +147,22 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, centred=True, sa
     ``layer_norm_grads``: "input" saves x itself, "int8" its 8-bit checkpoint, made in
     the same pass."""
     _check_save(save)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if save is None:
-        return asr_layer_norm(x, weight, bias, y, eps=eps, centred=centred)
-    rows = x.shape[0]
-    rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
-    mean = torch.empty(rows, dtype=torch.float32, device=x.device) if centred else None
-    kept = empty_checkpoint(*x.shape, x.device, x.dtype) if save == "int8" else None
-    asr_layer_norm(x, weight, bias, y, mean, rstd, eps=eps, centred=centred, keep=kept, rounding=rounding, step=step,
-                   seed=seed)
-    return y, NormSaved(x if kept is None else kept, mean, rstd)
+    px, rows, cols, ld = _lib._matrix_ptr(x, "x", _FLOATS)
+    d = x.get_device()
+    p = _lib._norm_params(rows, cols, _lib._dt(x), weight, bias, float(eps), centred, d)
+    with _lib._on_device(x.device):
+        y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+        rstd = mean = kept = stats = None
+        if save is not None:
+            stats = torch.empty((2 if centred else 1, rows), dtype=torch.float32, device=x.device)
+            rstd = stats.data_ptr()
+            mean = rstd + 4 * rows if centred else None
+            if save == "int8":
+                kept = empty_checkpoint(rows, cols, x.device, x.dtype)
+        _lib._check(_lib.lib().asr_layer_norm(p, px, ld, y.data_ptr(), cols, mean, rstd,
+                                              None if kept is None else kept._struct(rounding, 0, step, seed),
+                                              _lib._raw_stream(d)), "asr_layer_norm")
+    return y if save is None else (y, NormSaved(x if kept is None else kept, stats))
 
 
 def layer_norm_grads(dy, saved: NormSaved, weight=None, *, need_dx=True, need_dweight=True, need_dbias=True,
@@ -135,14 +170,26 @@ def layer_norm_grads(dy, saved: NormSaved, weight=None, *, need_dx=True, need_dw
     """(dx, dweight, dbias) from ``dy`` and what ``layer_norm`` saved, each None where it
     is not needed; dx of dy's dtype, dweight of the weight's (dy's, if the norm has none),
     dbias of ``dbias_dtype`` (dweight's unless given)."""
-    cols = dy.shape[1]
-    kept = saved.input if isinstance(saved.input, Int8Checkpoint) else None
-    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device) if need_dx else None
+    pg, rows, cols, g_ld = _lib._matrix_ptr(dy, "dy", _FLOATS)
+    d, device = dy.get_device(), dy.device
+    px, x_ld, kept = _saved_input(saved.input, rows, cols, dy)
+    centred = saved.stats.shape[0] == 2
+    rstd = _lib._dev_ptr(saved.stats, "stats", (torch.float32,), (2 if centred else 1) * rows, d)
+    p = _lib._norm_params(rows, cols, _lib._dt(dy), weight, None, 0.0, centred, d)
     dtype = dy.dtype if weight is None else weight.dtype
-    dweight = torch.empty(cols, dtype=dtype, device=dy.device) if need_dweight else None
-    dbias = torch.empty(cols, dtype=dbias_dtype or dtype, device=dy.device) if need_dbias else None
-    asr_layer_norm_grads(dy, saved.input if kept is None else None, weight, saved.mean, saved.rstd, dx, dweight, dbias,
-                         centred=saved.mean is not None, kept=kept)
+    if dbias_dtype is not None and dbias_dtype not in _FLOATS:
+        raise TypeError(f"a gradient comes as float32 or bfloat16, not {dbias_dtype}")
+    with _lib._on_device(device):
+        dx = torch.empty((rows, cols), dtype=dy.dtype, device=device) if need_dx else None
+        dweight = torch.empty(cols, dtype=dtype, device=device) if need_dweight else None
+        dbias = torch.empty(cols, dtype=dbias_dtype or dtype, device=device) if need_dbias else None
+        need = _lib.asr_layer_norm_grads_workspace(rows, cols) if need_dweight or need_dbias else 0
+        buf = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        _lib._check(_lib.lib().asr_layer_norm_grads(
+            p, pg, g_ld, px, x_ld, kept, rstd + 4 * rows if centred else None, rstd, None if dx is None else dx.data_ptr(), cols,
+            None if dweight is None else dweight.data_ptr(), 0 if dweight is None else _lib._dt(dweight),
+            None if dbias is None else dbias.data_ptr(), 0 if dbias is None else _lib._dt(dbias),
+            None if buf is None else buf.data_ptr(), need, _lib._raw_stream(d)), "asr_layer_norm_grads")
     return dx, dweight, dbias
 
 
@@ -152,19 +199,20 @@ class _LayerNormFunction(torch.autograd.Function):
         x = _by_rows(x)
         if not any(ctx.needs_input_grad):
             return layer_norm(x, weight, bias, eps=eps, centred=centred)
-        ctx.x_dtype, ctx.bias_dtype = x.dtype, None if bias is None else bias.dtype
+        ctx.kept, ctx.kind = save == "int8", (x.dtype, None if bias is None else bias.dtype)
         y, saved = layer_norm(x, weight, bias, eps=eps, centred=centred, save=save, rounding=rounding, step=step, seed=seed)
-        ctx.save_for_backward(weight, saved.mean, saved.rstd, *(saved.input[:2] if save == "int8" else (saved.input,)))
+        ctx.save_for_backward(weight, saved.stats, saved.input.data if ctx.kept else saved.input)
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        weight, mean, rstd, *x = ctx.saved_tensors
-        saved = NormSaved(Int8Checkpoint(*x, ctx.x_dtype) if len(x) == 2 else x[0], mean, rstd)
+        weight, stats, x = ctx.saved_tensors
+        x_dtype, bias_dtype = ctx.kind
+        saved = NormSaved(Int8Checkpoint(x, dy.shape[1], x_dtype) if ctx.kept else x, stats)
         need = ctx.needs_input_grad
         dx, dw, db = layer_norm_grads(_by_rows(dy), saved, weight, need_dx=need[0], need_dweight=need[1], need_dbias=need[2],
-                                      dbias_dtype=ctx.bias_dtype)
+                                      dbias_dtype=bias_dtype)
         return dx, dw, db, None, None, None, None, None, None
 
 
@@ -204,15 +252,37 @@ class LayerNorm(_CountedModule):
 def embedding(ids, table, *, scale: float = 1.0):
     """``scale * table[ids]`` for ``ids`` (1-D, int64 or int32): (tokens, dim).  An id
     outside the table gives a row of NaN."""
-    y = torch.empty(ids.shape[0], table.shape[1], dtype=table.dtype, device=table.device)
-    return asr_embedding(ids, table, y, scale=scale)
+    pt, vocab, dim, ld = _lib._matrix_ptr(table, "table", _FLOATS)
+    d = table.get_device()
+    pi, index, tokens = _lib._ids(ids, d)
+    with _lib._on_device(table.device):
+        y = torch.empty((tokens, dim), dtype=table.dtype, device=table.device)
+        _lib._check(_lib.lib().asr_embedding(pi, index, tokens, pt, ld, vocab, dim, scale, y.data_ptr(), dim, _lib._dt(y),
+                                             _lib._raw_stream(d)), "asr_embedding")
+    return y
 
 
 def embedding_grads(ids, dy, vocab: int, *, scale: float = 1.0, padding_idx: Optional[int] = None, dtype=None):
     """The whole table's gradient, (vocab, dim) in ``dtype`` (dy's unless given): for each
     row, scale times the sum of ``dy`` over its tokens, in their order."""
-    dtable = torch.empty(int(vocab), dy.shape[1], dtype=dtype or dy.dtype, device=dy.device)
-    return asr_embedding_grads(ids, dy, dtable, scale=scale, padding_idx=padding_idx)
+    pg, rows, dim, ld = _lib._matrix_ptr(dy, "dy", _FLOATS)
+    d, device = dy.get_device(), dy.device
+    pi, index, tokens = _lib._ids(ids, d)
+    if rows != tokens:
+        raise ValueError(f"dy has {rows} rows; expected {tokens}")
+    if padding_idx is not None and not 0 <= padding_idx < vocab:
+        raise ValueError(f"padding_idx must be a row of the table (0 to {vocab - 1}), not {padding_idx}")
+    if dtype is not None and dtype not in _FLOATS:
+        raise TypeError(f"a gradient comes as float32 or bfloat16, not {dtype}")
+    need = _lib.asr_embedding_grads_workspace(tokens, dim)
+    with _lib._on_device(device):
+        out = torch.empty((vocab, dim), dtype=dtype or dy.dtype, device=device)
+        buf = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        _lib._check(_lib.lib().asr_embedding_grads(pi, index, tokens, pg, ld, _lib._dt(dy), vocab, dim, scale,
+                                                   -1 if padding_idx is None else padding_idx, out.data_ptr(), _lib._dt(out),
+                                                   None if buf is None else buf.data_ptr(), need, _lib._raw_stream(d)),
+                    "asr_embedding_grads")
+    return out
 
 
 class _EmbeddingFunction(torch.autograd.Function):
