@@ -22,7 +22,7 @@ constexpr int kThreads = kept::kThreads;
 struct Params {
     kept::Matrix x, dy;
     kept::Out y, dx;
-    uint64_t rows, cols;                        // of y
+    uint32_t rows, cols;                        // of y
     uint32_t gelu;
     kept::Store to;                             // forward
     kept::Source from;                          // backward
@@ -76,96 +76,98 @@ __device__ __forceinline__ void value_and_slope(float a, bool gelu, float &f, fl
 
 // The units of a lane and span: of x's two halves at one column, gated, or at two
 // columns 256 apart.
-template <bool GATED>
+template <bool GATED, bool FULL>
 struct Place {
-    uint64_t row, col[2];                       // of x
-    int live;                                   // of the first; gated, of both
-    int live1;
-    __device__ Place(const kept::Walk &k, uint64_t cols)
+    uint32_t row, col;                          // of the first unit
+    uint32_t apart;                             // columns of x between the two
+    int live[2];
+    __device__ Place(const kept::Walk &k, uint32_t cols)
     {
-        const uint64_t at = k.span * (GATED ? 256ull : 512ull) + (threadIdx.x & 31) * 8;
         row = k.row;
-        col[0] = at;
-        col[1] = at + (GATED ? cols : 256);
-        live = k.more() ? live_of(cols, at) : 0;
-        live1 = GATED ? live : k.more() ? live_of(cols, at + 256) : 0;
+        col = k.span * (GATED ? 256u : 512u) + (threadIdx.x & 31) * 8;
+        apart = GATED ? cols : 256;
+        live[0] = FULL ? 8 : live_of(cols, col);
+        live[1] = FULL ? 8 : GATED ? live[0] : live_of(cols, col + 256);
     }
-    __device__ int of(int u) const { return u ? live1 : live; }
+    __device__ uint32_t of(int u) const { return u ? col + apart : col; }
 };
 
 // KEEP: 0 nothing, 1 to nearest, 2 stochastically.  The next span's values are
 // fetched before the current one's are worked on.
-template <int DT, bool GATED, int KEEP>
-__global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant__ Params P, uint32_t spans)
+template <int DT, bool GATED, int KEEP, bool FULL>
+__global__ void __launch_bounds__(kThreads, DT == ASR_BF16 ? 4 : 3) forward_kernel(const __grid_constant__ Params P, uint32_t spans)
 {
+    using At = Place<GATED, FULL>;
     const bool gelu = P.gelu, vec1 = P.x.vec && (!GATED || P.cols % 8 == 0);
-    kept::Raw<DT> raw[2];
-    auto load = [&](const Place<GATED> &at) {
+    kept::Raw<DT> next[2];
+    auto load = [&](const kept::Walk &k) {
+        if (!k.more()) return;
+        const At at(k, P.cols);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-            raw[u] = kept::fetch<DT>(P.x.p, at.row * P.x.ld + at.col[u], at.of(u), u ? vec1 : P.x.vec);
+        for (int u = 0; u < 2; ++u) next[u] = kept::fetch<DT, FULL>(P.x, at.row, at.of(u), at.live[u], u ? vec1 : P.x.vec);
     };
     kept::Walk k(P.rows, spans);
-    Place<GATED> at(k, P.cols);
-    load(at);
+    load(k);
     while (k.more()) {
-        float x[2][8];
+        kept::Raw<DT> raw[2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) kept::values(raw[u], x[u]);
-        const Place<GATED> now = at;
+        for (int u = 0; u < 2; ++u) raw[u] = next[u];
+        const At now(k, P.cols);
         k.next();
-        at = Place<GATED>(k, P.cols);
-        load(at);
+        load(k);
         if (KEEP) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) kept::keep8<KEEP == 2>(P.to, now.row, now.col[u], now.of(u), x[u]);
+            for (int u = 0; u < 2; ++u) kept::keep8<KEEP == 2, DT, FULL>(P.to, now.row, now.of(u), now.live[u], raw[u]);
         }
 #pragma unroll
         for (int u = 0; u < (GATED ? 1 : 2); ++u) {
-            float y[8];
+            float y[8], b[8];
+            kept::values(raw[u], y);
+            if (GATED) kept::values(raw[1], b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                y[i] = value<DT>(x[u][i], gelu);
-                if (GATED) y[i] = __fmul_rn(y[i], x[1][i]);
+                y[i] = value<DT>(y[i], gelu);
+                if (GATED) y[i] = __fmul_rn(y[i], b[i]);
             }
-            kept::store8<DT>(P.y.p, now.row * P.y.ld + now.col[u], now.of(u), P.y.vec, y);
+            kept::store8<DT, FULL>(P.y, now.row, now.of(u), now.live[u], P.y.vec, y);
         }
     }
 }
 
 // KEPT: 0 from x, 1 from its codes, 2 from codes whose groups do not begin anew with
 // the gating half (cols not a multiple of 32).
-template <int DT, bool GATED, int KEPT>
+template <int DT, bool GATED, int KEPT, bool FULL>
 __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constant__ Params P, uint32_t spans)
 {
+    using At = Place<GATED, FULL>;
     constexpr int kGrads = GATED ? 1 : 2;
     const bool gelu = P.gelu, vec1 = P.x.vec && (!GATED || P.cols % 8 == 0);
     kept::Raw<DT> raw[2], grad[kGrads];
     Codes codes[2];
-    auto load = [&](const Place<GATED> &at) {
+    auto load = [&](const kept::Walk &k) {
+        if (!k.more()) return;
+        const At at(k, P.cols);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            if (!KEPT) raw[u] = kept::fetch<DT>(P.x.p, at.row * P.x.ld + at.col[u], at.of(u), u ? vec1 : P.x.vec);
-            else if (KEPT == 1 || u == 0) codes[u] = kept::fetch_codes(P.from, at.row, at.col[u], at.of(u));
-            if (u < kGrads) grad[u] = kept::fetch<DT>(P.dy.p, at.row * P.dy.ld + at.col[u], at.of(u), P.dy.vec);
+            if (!KEPT) raw[u] = kept::fetch<DT, FULL>(P.x, at.row, at.of(u), at.live[u], u ? vec1 : P.x.vec);
+            else if (KEPT == 1 || u == 0) codes[u] = kept::fetch_codes<FULL>(P.from, at.row, at.of(u), at.live[u]);
+            if (u < kGrads) grad[u] = kept::fetch<DT, FULL>(P.dy, at.row, at.of(u), at.live[u], P.dy.vec);
         }
     };
     kept::Walk k(P.rows, spans);
-    Place<GATED> at(k, P.cols);
-    load(at);
+    load(k);
     while (k.more()) {
         float x[2][8], g[kGrads][8];
-        const Place<GATED> now = at;
+        const At now(k, P.cols);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             if (!KEPT) kept::values(raw[u], x[u]);
             else if (KEPT == 1 || u == 0) kept::values(codes[u], x[u]);
-            else kept::values_across(P.from, now.row, now.col[u], now.of(u), x[u]);
+            else kept::values_across(P.from, now.row, now.of(u), now.live[u], x[u]);
             if (u < kGrads) kept::values(grad[u], g[u]);
         }
         k.next();
-        at = Place<GATED>(k, P.cols);
-        load(at);
+        load(k);
 #pragma unroll
         for (int u = 0; u < kGrads; ++u) {
             float db[8];
@@ -179,8 +181,8 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
                 }
                 g[u][i] = __fmul_rn(g[u][i], df);
             }
-            kept::store8<DT>(P.dx.p, now.row * P.dx.ld + now.col[u], now.of(u), P.dx.vec, g[u]);
-            if (GATED) kept::store8<DT>(P.dx.p, now.row * P.dx.ld + now.col[1], now.of(1), P.dx.vec && P.cols % 8 == 0, db);
+            kept::store8<DT, FULL>(P.dx, now.row, now.of(u), now.live[u], P.dx.vec, g[u]);
+            if (GATED) kept::store8<DT, FULL>(P.dx, now.row, now.of(1), now.live[1], P.dx.vec && P.cols % 8 == 0, db);
         }
     }
 }
@@ -189,29 +191,32 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
 
 using Kernel = void (*)(const Params, uint32_t);
 
-template <int DT, bool GATED>
+template <int DT, bool GATED, bool FULL>
 Kernel forward_of(int keep)
 {
-    return keep == 2 ? forward_kernel<DT, GATED, 2> : keep ? forward_kernel<DT, GATED, 1> : forward_kernel<DT, GATED, 0>;
+    return keep == 2 ? forward_kernel<DT, GATED, 2, FULL> : keep ? forward_kernel<DT, GATED, 1, FULL>
+                                                                 : forward_kernel<DT, GATED, 0, FULL>;
 }
 
-Kernel forward_of(int32_t dtype, bool gated, int keep)
+Kernel forward_of(int32_t dtype, bool gated, int keep, bool full)
 {
-    if (dtype == ASR_BF16) return gated ? forward_of<ASR_BF16, true>(keep) : forward_of<ASR_BF16, false>(keep);
-    return gated ? forward_of<ASR_F32, true>(keep) : forward_of<ASR_F32, false>(keep);
+    if (dtype != ASR_BF16) return gated ? forward_of<ASR_F32, true, false>(keep) : forward_of<ASR_F32, false, false>(keep);
+    if (full) return gated ? forward_of<ASR_BF16, true, true>(keep) : forward_of<ASR_BF16, false, true>(keep);
+    return gated ? forward_of<ASR_BF16, true, false>(keep) : forward_of<ASR_BF16, false, false>(keep);
 }
 
-template <int DT>
+template <int DT, bool FULL>
 Kernel backward_of(bool gated, int codes)
 {
-    if (gated)
-        return codes == 2 ? backward_kernel<DT, true, 2> : codes ? backward_kernel<DT, true, 1> : backward_kernel<DT, true, 0>;
-    return codes ? backward_kernel<DT, false, 1> : backward_kernel<DT, false, 0>;
+    if (!gated) return codes ? backward_kernel<DT, false, 1, FULL> : backward_kernel<DT, false, 0, FULL>;
+    if (codes == 2) return backward_kernel<DT, true, 2, false>;
+    return codes ? backward_kernel<DT, true, 1, FULL> : backward_kernel<DT, true, 0, FULL>;
 }
 
-Kernel backward_of(int32_t dtype, bool gated, int codes)
+Kernel backward_of(int32_t dtype, bool gated, int codes, bool full)
 {
-    return dtype == ASR_BF16 ? backward_of<ASR_BF16>(gated, codes) : backward_of<ASR_F32>(gated, codes);
+    if (dtype != ASR_BF16) return backward_of<ASR_F32, false>(gated, codes);
+    return full ? backward_of<ASR_BF16, true>(gated, codes) : backward_of<ASR_BF16, false>(gated, codes);
 }
 
 asr_status setup()
@@ -222,12 +227,12 @@ asr_status setup()
     const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
     if (e == cudaSuccess && (ready.load(std::memory_order_acquire) & bit)) return ASR_OK;
     for (int32_t dtype : {ASR_F32, ASR_BF16})
-        for (int gated = 0; gated < 2; ++gated) {
-            for (int keep = 0; keep < 3; ++keep)
-                if (e == cudaSuccess) e = prod::load_kernel(forward_of(dtype, gated != 0, keep));
-            for (int codes = 0; codes < 3; ++codes)
-                if (e == cudaSuccess) e = prod::load_kernel(backward_of(dtype, gated != 0, codes));
-        }
+        for (int full = 0; full < 2; ++full)
+            for (int gated = 0; gated < 2; ++gated)
+                for (int form = 0; form < 3; ++form) {
+                    if (e == cudaSuccess) e = prod::load_kernel(forward_of(dtype, gated != 0, form, full != 0));
+                    if (e == cudaSuccess) e = prod::load_kernel(backward_of(dtype, gated != 0, form, full != 0));
+                }
     if (e != cudaSuccess) return cuda_fail(e);
     ready.fetch_or(bit, std::memory_order_release);
     return ASR_OK;
@@ -238,9 +243,11 @@ asr_status kind_ok(int32_t dtype, uint32_t function)
     return kept::dtype_ok(dtype) && (function == ASR_SILU || function == ASR_GELU) ? ASR_OK : ASR_ERR_UNSUPPORTED_DTYPE;
 }
 
+uint32_t span_of(uint32_t gated) { return gated ? 256 : 512; }
+
 asr_status launch(Kernel kernel, const Params &P, uint32_t gated, cudaStream_t stream)
 {
-    return kept::walk(ASR_KERNEL_ACTIVATION, kernel, P, P.rows, P.cols, gated ? 256 : 512, stream);
+    return kept::walk(ASR_KERNEL_ACTIVATION, kernel, P, P.rows, P.cols, span_of(gated), stream);
 }
 
 asr_status forward(const void *x, uint64_t x_ld, void *y, uint64_t y_ld, int32_t dtype, uint64_t rows, uint64_t cols,
@@ -261,8 +268,8 @@ asr_status forward(const void *x, uint64_t x_ld, void *y, uint64_t y_ld, int32_t
     std::memset(&P, 0, sizeof(P));
     P.x = kept::matrix(x, x_ld);
     P.y = kept::out(y, y_ld);
-    P.rows = rows;
-    P.cols = cols;
+    P.rows = static_cast<uint32_t>(rows);
+    P.cols = static_cast<uint32_t>(cols);
     P.gelu = function == ASR_GELU;
     // the kernel's lanes hold whole groups of both halves where they begin with the halves
     const bool apart = to && gated && cols % kept::kGroup != 0;
@@ -271,7 +278,8 @@ asr_status forward(const void *x, uint64_t x_ld, void *y, uint64_t y_ld, int32_t
         P.to = kept::store(*to, width);
         keep = to->rounding == ASR_ROUND_SR ? 2 : 1;
     }
-    st = launch(forward_of(dtype, gated != 0, keep), P, gated, stream);
+    const bool full = cols % span_of(gated) == 0 && P.x.vec && P.y.vec && (!keep || P.to.vec);
+    st = launch(forward_of(dtype, gated != 0, keep, full), P, gated, stream);
     if (st == ASR_OK && apart) st = kept::pack(x, dtype, rows, width, x_ld, to, stream);
     return st;
 }
@@ -296,11 +304,12 @@ asr_status backward(const void *dy, uint64_t dy_ld, const void *x, uint64_t x_ld
     P.dx = kept::out(dx, dx_ld);
     if (from) P.from = kept::source(*from);
     else P.x = kept::matrix(x, x_ld);
-    P.rows = rows;
-    P.cols = cols;
+    P.rows = static_cast<uint32_t>(rows);
+    P.cols = static_cast<uint32_t>(cols);
     P.gelu = function == ASR_GELU;
     const int codes = !from ? 0 : gated && cols % kept::kGroup != 0 ? 2 : 1;
-    return launch(backward_of(dtype, gated != 0, codes), P, gated, stream);
+    const bool full = cols % span_of(gated) == 0 && P.dy.vec && P.dx.vec && (from ? P.from.vec : P.x.vec);
+    return launch(backward_of(dtype, gated != 0, codes, full), P, gated, stream);
 }
 
 }  // namespace act

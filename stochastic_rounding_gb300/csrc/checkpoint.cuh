@@ -27,8 +27,9 @@ constexpr uint32_t kStream = 1;                 // last counter word
 struct Store {                                  // where it goes
     int8_t *q;
     uint8_t *power;                             // e + 127; 255: the group holds an infinity or a NaN
-    uint64_t q_ld, power_ld;
-    uint64_t base, across;                      // first counter; counters a row
+    uint32_t q_ld, power_ld;
+    uint64_t base;                              // first counter
+    uint32_t across;                            // counters a row
     uint32_t vec;                               // eight codes are 8-byte aligned
     uint32_t step;
     RoundKeys keys;
@@ -37,11 +38,16 @@ struct Store {                                  // where it goes
 struct Source {
     const int8_t *q;
     const uint8_t *power;
-    uint64_t q_ld, power_ld;
+    uint32_t q_ld, power_ld;
     uint32_t vec;
 };
 
-__device__ __forceinline__ int live_of(uint64_t cols, uint64_t col)
+// Whether kernels look at a unit's bounds: FULL is for matrices of whole spans whose
+// units are all aligned, as the widths of layers are, and leaves out the tests and the
+// element by element accesses.  Only for bf16, whose kernels are bound by their
+// instructions (8,192 x 14,336: pack 67 -> 59 us, unpack 68 -> 57 us, the gated
+// activation's backward pass from codes 197 -> 168 us); f32's are bound by bytes.
+__device__ __forceinline__ int live_of(uint32_t cols, uint32_t col)
 {
     return col >= cols ? 0 : cols - col < 8 ? static_cast<int>(cols - col) : 8;
 }
@@ -49,15 +55,20 @@ __device__ __forceinline__ int live_of(uint64_t cols, uint64_t col)
 // A matrix of f32 or bf16 values, rows `ld` apart.
 struct Matrix {
     const void *p;
-    uint64_t ld;
+    uint32_t ld;
     uint32_t vec;                               // units of eight are 16-byte aligned
 };
 
 struct Out {
     void *p;
-    uint64_t ld;
+    uint32_t ld;
     uint32_t vec;
 };
+
+__device__ __forceinline__ uint64_t place(uint32_t row, uint32_t ld, uint32_t col)
+{
+    return static_cast<uint64_t>(row) * ld + col;
+}
 
 // Eight values as they lie in memory, so that they can be fetched ahead of their use
 // in as few registers as they take there.
@@ -66,12 +77,13 @@ struct Raw {
     uint32_t w[DT == ASR_BF16 ? 4 : 8];
 };
 
-template <int DT>
-__device__ __forceinline__ Raw<DT> fetch(const void *src, uint64_t at, int live, bool vec)
+template <int DT, bool FULL = false>
+__device__ __forceinline__ Raw<DT> fetch(const Matrix &M, uint32_t row, uint32_t col, int live, bool vec)
 {
     Raw<DT> r;
-    if (vec && live == 8) {
-        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(src) + at * (DT == ASR_BF16 ? 2 : 4));
+    const char *src = static_cast<const char *>(M.p) + place(row, M.ld, col) * (DT == ASR_BF16 ? 2 : 4);
+    if (FULL || (vec && live == 8)) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(src);
         const uint4 a = p[0];
         r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
         if (DT == ASR_F32) {
@@ -80,12 +92,12 @@ __device__ __forceinline__ Raw<DT> fetch(const void *src, uint64_t at, int live,
             r.w[DT == ASR_F32 ? 6 : 0] = b.z, r.w[DT == ASR_F32 ? 7 : 0] = b.w;
         }
     } else if (DT == ASR_BF16) {
-        const uint16_t *p = static_cast<const uint16_t *>(src) + at;
+        const uint16_t *p = reinterpret_cast<const uint16_t *>(src);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             r.w[i] = (2 * i < live ? p[2 * i] : 0u) | (2 * i + 1 < live ? static_cast<uint32_t>(p[2 * i + 1]) << 16 : 0u);
     } else {
-        const uint32_t *p = static_cast<const uint32_t *>(src) + at;
+        const uint32_t *p = reinterpret_cast<const uint32_t *>(src);
 #pragma unroll
         for (int i = 0; i < (DT == ASR_F32 ? 8 : 0); ++i) r.w[i] = i < live ? p[i] : 0u;
     }
@@ -104,12 +116,11 @@ __device__ __forceinline__ void values(const Raw<DT> &r, float x[8])
 // A warp's way through a matrix in spans of kSpan columns: span `at` counted along
 // the rows, then every `stride`-th.  Both are counts of a launch's warps.
 constexpr int kUnits = 2;                       // of eight values, a lane and span
-constexpr int kSpan = 256 * kUnits;
+constexpr uint32_t kSpan = 256 * kUnits;
 
 struct Walk {
-    uint64_t row, rows;
-    uint32_t span, spans, drow, dspan;
-    __device__ Walk(uint64_t rows_, uint32_t spans_)
+    uint32_t row, rows, span, spans, drow, dspan;
+    __device__ Walk(uint32_t rows_, uint32_t spans_)
     {
         const uint32_t at = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), stride = gridDim.x * (kThreads / 32);
         rows = rows_;
@@ -139,6 +150,31 @@ __device__ __forceinline__ float most(float a, float b)
     return d;
 }
 
+// Of pairs of bf16; their signs are left to be taken off.
+__device__ __forceinline__ uint32_t most2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// The bits of a group's largest magnitude, from the unit of each of its four lanes.
+template <int DT>
+__device__ __forceinline__ uint32_t group_most(const Raw<DT> &r)
+{
+    if (DT == ASR_BF16) {
+        uint32_t m = most2(most2(r.w[0], r.w[1]), most2(r.w[2], r.w[3]));
+        m = most2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = most2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2)) & 0x7FFF7FFFu;
+        return max(m << 16, m & 0xFFFF0000u);               // as numbers: a NaN's bits are the largest
+    }
+    float x[8];
+    values(r, x);
+    float m = most(most(most(x[0], x[1]), most(x[2], x[3])), most(most(x[4], x[5]), most(x[6], x[7])));
+    m = most(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    return __float_as_uint(most(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2)));
+}
+
 // e + 127 for the bits of a largest value, 127 being 1.984375 * 2^6.
 __device__ __forceinline__ uint32_t power_of(uint32_t top)
 {
@@ -159,17 +195,16 @@ __device__ __forceinline__ float scale_of(uint32_t b)
 // fraction is above r / 65536.  128 + r / 65536 is a binary32 number with r for its
 // low bits; taken from y and rounded up, the difference keeps its ceiling, -128 away
 // (whole numbers are representable), and 1.5 * 2^23 + 128 more, rounded up, is it.
-template <bool SR>
-__device__ __forceinline__ void keep8(const Store &S, uint64_t row, uint64_t col, int live, const float x[8])
+template <bool SR, int DT, bool FULL>
+__device__ __forceinline__ void keep8(const Store &S, uint32_t row, uint32_t col, int live, const Raw<DT> &raw)
 {
-    float m = most(most(most(x[0], x[1]), most(x[2], x[3])), most(most(x[4], x[5]), most(x[6], x[7])));
-    m = most(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = most(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    const uint32_t b = power_of(__float_as_uint(m));
+    const uint32_t b = power_of(group_most(raw));
     const float up = __uint_as_float((254u - b) << 23);
+    float x[8];
+    values(raw, x);
     uint32_t c[8], w[4];
     if (SR) {
-        const uint64_t at = S.base + row * S.across + (col >> 3);
+        const uint64_t at = S.base + place(row, S.across, col >> 3);
         philox4x32_10(static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32), S.step, kStream, S.keys, w);
     }
 #pragma unroll
@@ -184,15 +219,15 @@ __device__ __forceinline__ void keep8(const Store &S, uint64_t row, uint64_t col
     uint2 v = make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
                          __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
     if (b == 255u) v = make_uint2(0, 0);
-    int8_t *q = S.q + row * S.q_ld + col;
-    if (live == 8 && S.vec) {
+    int8_t *q = S.q + place(row, S.q_ld, col);
+    if (FULL || (live == 8 && S.vec)) {
         *reinterpret_cast<uint2 *>(q) = v;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i < live) q[i] = static_cast<int8_t>((i < 4 ? v.x : v.y) >> (8 * (i & 3)));
     }
-    if (live > 0 && (threadIdx.x & 3) == 0) S.power[row * S.power_ld + (col >> 5)] = static_cast<uint8_t>(b);
+    if ((FULL || live > 0) && (threadIdx.x & 3) == 0) S.power[place(row, S.power_ld, col >> 5)] = static_cast<uint8_t>(b);
 }
 
 // Codes and power of eight values, to be fetched ahead of their use.
@@ -201,19 +236,20 @@ struct Codes {
     uint32_t b;
 };
 
-__device__ __forceinline__ Codes fetch_codes(const Source &S, uint64_t row, uint64_t col, int live)
+template <bool FULL = false>
+__device__ __forceinline__ Codes fetch_codes(const Source &S, uint32_t row, uint32_t col, int live)
 {
     Codes c{make_uint2(0, 0), 0};
-    if (live <= 0) return c;
-    const int8_t *q = S.q + row * S.q_ld + col;
-    if (live == 8 && S.vec) {
+    if (!FULL && live <= 0) return c;
+    const int8_t *q = S.q + place(row, S.q_ld, col);
+    if (FULL || (live == 8 && S.vec)) {
         c.v = *reinterpret_cast<const uint2 *>(q);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i < live) (i < 4 ? c.v.x : c.v.y) |= static_cast<uint32_t>(static_cast<uint8_t>(q[i])) << (8 * (i & 3));
     }
-    c.b = S.power[row * S.power_ld + (col >> 5)];
+    c.b = S.power[place(row, S.power_ld, col >> 5)];
     return c;
 }
 
@@ -236,27 +272,28 @@ __device__ __forceinline__ void values(const Codes &c, float x[8])
 }
 
 // Eight values from any column on, whose group may end among them.
-__device__ __forceinline__ void values_across(const Source &S, uint64_t row, uint64_t col, int live, float x[8])
+__device__ __forceinline__ void values_across(const Source &S, uint32_t row, uint32_t col, int live, float x[8])
 {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        x[i] = i < live ? __fmul_rn(static_cast<float>(S.q[row * S.q_ld + col + i]),
-                                    scale_of(S.power[row * S.power_ld + ((col + i) >> 5)])) : 0.0f;
+        x[i] = i < live ? __fmul_rn(static_cast<float>(S.q[place(row, S.q_ld, col + i)]),
+                                    scale_of(S.power[place(row, S.power_ld, (col + i) >> 5)])) : 0.0f;
 }
 
 // Eight values out, `live` of them, to nearest where they are bf16.
-template <int DT>
-__device__ __forceinline__ void store8(void *dst, uint64_t at, int live, bool vec, const float v[8])
+template <int DT, bool FULL = false>
+__device__ __forceinline__ void store8(const Out &O, uint32_t row, uint32_t col, int live, bool vec, const float v[8])
 {
+    char *dst = static_cast<char *>(O.p) + place(row, O.ld, col) * (DT == ASR_BF16 ? 2 : 4);
     if (DT == ASR_BF16) {
-        uint16_t *p = static_cast<uint16_t *>(dst) + at;
+        uint16_t *p = reinterpret_cast<uint16_t *>(dst);
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
             w[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        if (vec && live == 8) {
+        if (FULL || (vec && live == 8)) {
             *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
 #pragma unroll
@@ -264,8 +301,8 @@ __device__ __forceinline__ void store8(void *dst, uint64_t at, int live, bool ve
                 if (i < live) p[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
         }
     } else {
-        float *p = static_cast<float *>(dst) + at;
-        if (vec && live == 8) {
+        float *p = reinterpret_cast<float *>(dst);
+        if (FULL || (vec && live == 8)) {
             reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
             reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
         } else {
@@ -278,71 +315,72 @@ __device__ __forceinline__ void store8(void *dst, uint64_t at, int live, bool ve
 
 struct PackParams {
     Matrix x;
-    uint64_t rows, cols;
+    uint32_t rows, cols;
     Store to;
 };
 
 // The next span's values are fetched before the current one's are worked on.
-template <bool SR, int DT>
+template <bool SR, int DT, bool FULL>
 __global__ void __launch_bounds__(kThreads) pack_kernel(const __grid_constant__ PackParams P, uint32_t spans)
 {
-    const uint32_t lane = threadIdx.x & 31;
-    Raw<DT> x[kUnits];
+    const uint32_t at = (threadIdx.x & 31) * 8;
+    Raw<DT> next[kUnits];
     auto load = [&](const Walk &k) {
+        if (!k.more()) return;
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
-            const uint64_t col = k.span * static_cast<uint64_t>(kSpan) + u * 256 + lane * 8;
-            x[u] = fetch<DT>(P.x.p, k.row * P.x.ld + col, k.more() ? live_of(P.cols, col) : 0, P.x.vec);
+            const uint32_t col = k.span * kSpan + u * 256 + at;
+            next[u] = fetch<DT, FULL>(P.x, k.row, col, FULL ? 8 : live_of(P.cols, col), P.x.vec);
         }
     };
     Walk k(P.rows, spans);
     load(k);
     while (k.more()) {
-        float v[kUnits][8];
+        Raw<DT> x[kUnits];
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) values(x[u], v[u]);
-        const Walk now = k;
+        for (int u = 0; u < kUnits; ++u) x[u] = next[u];
+        const uint32_t row = k.row, first = k.span * kSpan + at;
         k.next();
         load(k);
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-            const uint64_t col = now.span * static_cast<uint64_t>(kSpan) + u * 256 + lane * 8;
-            keep8<SR>(P.to, now.row, col, live_of(P.cols, col), v[u]);
-        }
+        for (int u = 0; u < kUnits; ++u)
+            keep8<SR, DT, FULL>(P.to, row, first + u * 256, FULL ? 8 : live_of(P.cols, first + u * 256), x[u]);
     }
 }
 
 struct UnpackParams {
     Source from;
     Out out;
-    uint64_t rows, cols;
+    uint32_t rows, cols;
 };
 
-template <int DT>
+template <int DT, bool FULL>
 __global__ void __launch_bounds__(kThreads) unpack_kernel(const __grid_constant__ UnpackParams P, uint32_t spans)
 {
-    const uint32_t lane = threadIdx.x & 31;
-    Codes c[kUnits];
+    const uint32_t at = (threadIdx.x & 31) * 8;
+    Codes next[kUnits];
     auto load = [&](const Walk &k) {
+        if (!k.more()) return;
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
-            const uint64_t col = k.span * static_cast<uint64_t>(kSpan) + u * 256 + lane * 8;
-            c[u] = fetch_codes(P.from, k.row, col, k.more() ? live_of(P.cols, col) : 0);
+            const uint32_t col = k.span * kSpan + u * 256 + at;
+            next[u] = fetch_codes<FULL>(P.from, k.row, col, FULL ? 8 : live_of(P.cols, col));
         }
     };
     Walk k(P.rows, spans);
     load(k);
     while (k.more()) {
-        float v[kUnits][8];
+        Codes c[kUnits];
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) values(c[u], v[u]);
-        const Walk now = k;
+        for (int u = 0; u < kUnits; ++u) c[u] = next[u];
+        const uint32_t row = k.row, first = k.span * kSpan + at;
         k.next();
         load(k);
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
-            const uint64_t col = now.span * static_cast<uint64_t>(kSpan) + u * 256 + lane * 8;
-            store8<DT>(P.out.p, now.row * P.out.ld + col, live_of(P.cols, col), P.out.vec, v[u]);
+            float v[8];
+            values(c[u], v);
+            store8<DT, FULL>(P.out, row, first + u * 256, FULL ? 8 : live_of(P.cols, first + u * 256), P.out.vec, v);
         }
     }
 }
@@ -355,14 +393,19 @@ bool sizes_ok(uint64_t rows, uint64_t cols) { return rows <= kMaxRows && cols <=
 
 bool dtype_ok(int32_t dtype) { return dtype == ASR_F32 || dtype == ASR_BF16; }
 
+bool pitch_ok(uint64_t ld, uint64_t least) { return ld >= least && ld < (1ull << 32); }
+
 bool matrix_ok(const void *p, int32_t dtype, uint64_t ld, uint64_t cols)
 {
-    return p && muon::element_aligned(p, dtype) && int8::pitch_ok(ld, cols);
+    return p && muon::element_aligned(p, dtype) && pitch_ok(ld, cols);
 }
 
-Matrix matrix(const void *p, uint64_t ld) { return Matrix{p, ld, muon::units_aligned(p, ld, 0) ? 1u : 0u}; }
+Matrix matrix(const void *p, uint64_t ld)
+{
+    return Matrix{p, static_cast<uint32_t>(ld), muon::units_aligned(p, ld, 0) ? 1u : 0u};
+}
 
-Out out(void *p, uint64_t ld) { return Out{p, ld, muon::units_aligned(p, ld, 0) ? 1u : 0u}; }
+Out out(void *p, uint64_t ld) { return Out{p, static_cast<uint32_t>(ld), muon::units_aligned(p, ld, 0) ? 1u : 0u}; }
 
 bool aligned8(const void *p, uint64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0 && ld % 8 == 0; }
 
@@ -371,7 +414,7 @@ uint64_t groups(uint64_t cols) { return (cols + kGroup - 1) / kGroup; }
 // Whether a checkpoint of rows x cols can be read.
 asr_status readable(const asr_checkpoint &c, uint64_t cols)
 {
-    return c.q && c.power && int8::pitch_ok(c.q_ld, cols) && int8::pitch_ok(c.power_ld, groups(cols))
+    return c.q && c.power && pitch_ok(c.q_ld, cols) && pitch_ok(c.power_ld, groups(cols))
                ? ASR_OK : ASR_ERR_INVALID_VALUE;
 }
 
@@ -385,7 +428,8 @@ asr_status writable(const asr_checkpoint &c, uint64_t rows, uint64_t cols)
 
 Source source(const asr_checkpoint &c)
 {
-    return Source{c.q, c.power, c.q_ld, c.power_ld, aligned8(c.q, c.q_ld) ? 1u : 0u};
+    return Source{c.q, c.power, static_cast<uint32_t>(c.q_ld), static_cast<uint32_t>(c.power_ld),
+                  aligned8(c.q, c.q_ld) ? 1u : 0u};
 }
 
 Store store(const asr_checkpoint &c, uint64_t cols)
@@ -393,10 +437,10 @@ Store store(const asr_checkpoint &c, uint64_t cols)
     Store S;
     S.q = c.q;
     S.power = c.power;
-    S.q_ld = c.q_ld;
-    S.power_ld = c.power_ld;
+    S.q_ld = static_cast<uint32_t>(c.q_ld);
+    S.power_ld = static_cast<uint32_t>(c.power_ld);
     S.base = c.base_index / 8;
-    S.across = groups(cols) * (kGroup / 8);
+    S.across = static_cast<uint32_t>(groups(cols) * (kGroup / 8));
     S.vec = aligned8(c.q, c.q_ld);
     S.step = c.step;
     S.keys = make_keys(c.seed);
@@ -457,8 +501,10 @@ asr_status walk(int kind, K kernel, const P &params, uint64_t rows, uint64_t col
 asr_status setup()
 {
     static std::atomic<uint64_t> ready{0};
-    return load_once(ready, pack_kernel<false, ASR_F32>, pack_kernel<false, ASR_BF16>, pack_kernel<true, ASR_F32>,
-                     pack_kernel<true, ASR_BF16>, unpack_kernel<ASR_F32>, unpack_kernel<ASR_BF16>);
+    return load_once(ready, pack_kernel<false, ASR_F32, false>, pack_kernel<false, ASR_BF16, false>,
+                     pack_kernel<false, ASR_BF16, true>, pack_kernel<true, ASR_F32, false>,
+                     pack_kernel<true, ASR_BF16, false>, pack_kernel<true, ASR_BF16, true>, unpack_kernel<ASR_F32, false>,
+                     unpack_kernel<ASR_BF16, false>, unpack_kernel<ASR_BF16, true>);
 }
 
 asr_status pack(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, uint64_t x_ld, const asr_checkpoint *to,
@@ -474,12 +520,14 @@ asr_status pack(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, uint
     if (st != ASR_OK) return st;
     PackParams P;
     P.x = matrix(x, x_ld);
-    P.rows = rows;
-    P.cols = cols;
+    P.rows = static_cast<uint32_t>(rows);
+    P.cols = static_cast<uint32_t>(cols);
     P.to = store(*to, cols);
-    const bool sr = to->rounding == ASR_ROUND_SR, bf = dtype == ASR_BF16;
-    auto kernel = sr ? (bf ? pack_kernel<true, ASR_BF16> : pack_kernel<true, ASR_F32>)
-                     : (bf ? pack_kernel<false, ASR_BF16> : pack_kernel<false, ASR_F32>);
+    const bool sr = to->rounding == ASR_ROUND_SR, full = cols % kSpan == 0 && P.x.vec && P.to.vec;
+    auto kernel = sr ? pack_kernel<true, ASR_F32, false> : pack_kernel<false, ASR_F32, false>;
+    if (dtype == ASR_BF16)
+        kernel = full ? (sr ? pack_kernel<true, ASR_BF16, true> : pack_kernel<false, ASR_BF16, true>)
+                      : (sr ? pack_kernel<true, ASR_BF16, false> : pack_kernel<false, ASR_BF16, false>);
     return walk(ASR_KERNEL_CHECKPOINT, kernel, P, rows, cols, kSpan, stream);
 }
 
@@ -496,9 +544,11 @@ asr_status unpack(const asr_checkpoint *from, uint64_t rows, uint64_t cols, void
     UnpackParams P;
     P.from = source(*from);
     P.out = out(dst, ld);
-    P.rows = rows;
-    P.cols = cols;
-    auto kernel = dtype == ASR_BF16 ? unpack_kernel<ASR_BF16> : unpack_kernel<ASR_F32>;
+    P.rows = static_cast<uint32_t>(rows);
+    P.cols = static_cast<uint32_t>(cols);
+    const bool full = cols % kSpan == 0 && P.from.vec && P.out.vec;
+    auto kernel = dtype != ASR_BF16 ? unpack_kernel<ASR_F32, false> : full ? unpack_kernel<ASR_BF16, true>
+                                                                           : unpack_kernel<ASR_BF16, false>;
     return walk(ASR_KERNEL_CHECKPOINT, kernel, P, rows, cols, kSpan, stream);
 }
 

@@ -67,7 +67,7 @@ struct LookupParams {
     Ids ids;
     kept::Matrix table;
     kept::Out y;
-    uint64_t dim;
+    uint32_t dim;
     float scale;
 };
 
@@ -75,23 +75,23 @@ template <int DT>
 __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant__ LookupParams P, uint32_t spans)
 {
     const uint32_t lane = threadIdx.x & 31;
-    for (kept::Walk k(P.ids.n, spans); k.more(); k.next()) {
+    for (kept::Walk k(static_cast<uint32_t>(P.ids.n), spans); k.more(); k.next()) {
         const uint32_t id = key_of(P.ids, k.row);
         kept::Raw<DT> raw[kept::kUnits];
 #pragma unroll
         for (int u = 0; u < kept::kUnits; ++u) {
-            const uint64_t col = k.span * static_cast<uint64_t>(kept::kSpan) + u * 256 + lane * 8;
-            raw[u] = kept::fetch<DT>(P.table.p, id * P.table.ld + col, id < P.ids.vocab ? live_of(P.dim, col) : 0, P.table.vec);
+            const uint32_t col = k.span * kept::kSpan + u * 256 + lane * 8;
+            raw[u] = kept::fetch<DT>(P.table, id, col, id < P.ids.vocab ? live_of(P.dim, col) : 0, P.table.vec);
         }
 #pragma unroll
         for (int u = 0; u < kept::kUnits; ++u) {
-            const uint64_t col = k.span * static_cast<uint64_t>(kept::kSpan) + u * 256 + lane * 8;
+            const uint32_t col = k.span * kept::kSpan + u * 256 + lane * 8;
             float v[8];
             kept::values(raw[u], v);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v[i] = id < P.ids.vocab ? __fmul_rn(v[i], P.scale) : __uint_as_float(0x7FC00000u);
-            kept::store8<DT>(P.y.p, k.row * P.y.ld + col, live_of(P.dim, col), P.y.vec, v);
+            kept::store8<DT>(P.y, k.row, col, live_of(P.dim, col), P.y.vec, v);
         }
     }
 }
@@ -420,11 +420,11 @@ struct SumParams {
 };
 
 template <int OT>
-__device__ __forceinline__ void store_row(const SumParams &P, uint32_t row, uint64_t col, int live, float v[8])
+__device__ __forceinline__ void store_row(const SumParams &P, uint32_t row, uint32_t col, int live, float v[8])
 {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], P.scale);
-    kept::store8<OT>(P.out.p, row * P.out.ld + col, live, P.out.vec, v);
+    kept::store8<OT>(P.out, row, col, live, P.out.vec, v);
 }
 
 __device__ __forceinline__ void store_sum(float *p, const float v[8])
@@ -446,7 +446,7 @@ __device__ __forceinline__ void add_sum(float acc[8], const float *p)
 // begins its tail, of the others their heads, in order.  All threads of the block come
 // here together.
 template <int OT>
-__device__ __forceinline__ void join(const SumParams &P, uint32_t c, uint32_t row, bool began, uint32_t slice, uint64_t col,
+__device__ __forceinline__ void join(const SumParams &P, uint32_t c, uint32_t row, bool began, uint32_t slice, uint32_t col,
                                      int live)
 {
     __shared__ uint32_t ends[2], before;
@@ -516,8 +516,8 @@ __global__ void __launch_bounds__(kSumThreads, 6) sum_kernel(const __grid_consta
         return;
     }
     const uint32_t c = blockIdx.x / P.slices, slice = blockIdx.x % P.slices;
-    const uint64_t col = (slice * static_cast<uint64_t>(blockDim.x) + threadIdx.x) * 8;
-    const int live = live_of(P.dim, col);
+    const uint32_t col = (slice * blockDim.x + threadIdx.x) * 8;
+    const int live = live_of(static_cast<uint32_t>(P.dim), col);
     const uint64_t begin = static_cast<uint64_t>(c) * P.chunk, end = begin + P.chunk < P.n ? begin + P.chunk : P.n;
     float acc[8] = {};
     bool first = true;                          // still in the chunk's first row
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kSumThreads, 6) sum_kernel(const __grid_consta
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
                 const bool in = a0 + a < n && at[a0 + a] < P.vocab;
-                raw[a] = kept::fetch<DT>(P.dy.p, in ? order[a0 + a] * P.dy.ld + col : 0, in ? live : 0, P.dy.vec);
+                raw[a] = kept::fetch<DT>(P.dy, in ? order[a0 + a] : 0, col, in ? live : 0, P.dy.vec);
             }
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
@@ -613,7 +613,7 @@ asr_status lookup(const void *ids, int32_t index, uint64_t tokens, const void *t
     P.ids = ids_of(ids, index, tokens, vocab, -1);
     P.table = kept::matrix(table, table_ld);
     P.y = kept::out(y, y_ld);
-    P.dim = dim;
+    P.dim = static_cast<uint32_t>(dim);
     P.scale = static_cast<float>(scale);
     auto kernel = dtype == ASR_BF16 ? lookup_kernel<ASR_BF16> : lookup_kernel<ASR_F32>;
     return kept::walk(ASR_KERNEL_EMBEDDING, kernel, P, tokens, dim, kept::kSpan, stream);

@@ -34,7 +34,7 @@ struct Params {
     kept::Out y, dx;
     const void *w, *b;                          // may be null
     float *mean, *rstd;                         // forward: may be null
-    uint64_t rows, cols;
+    uint32_t rows, cols;
     float eps, over_n;                          // 1 / n
     uint32_t w_dtype, b_dtype, w_vec, b_vec;
     uint32_t centred;
@@ -75,9 +75,9 @@ __device__ __forceinline__ void params8(const void *p, uint32_t dtype, uint64_t 
 
 // Which rows a thread works on, and which values of them.  All threads of a warp make
 // the same number of steps; `row` may lie past the last row.
-template <bool WARP>
+template <bool WARP, bool FULL>
 struct Place {
-    uint64_t base, stride, col[kUnits];
+    uint32_t base, stride, col[kUnits];
     uint32_t sub, at;                           // row of a step; place in the row's threads
     int live[kUnits];
     __device__ explicit Place(const Params &P)
@@ -85,8 +85,8 @@ struct Place {
         uint32_t threads;
         if (WARP) {
             const uint32_t lane = threadIdx.x & 31, rows = 32 / P.lanes;
-            base = (blockIdx.x * static_cast<uint64_t>(kWarpThreads / 32) + (threadIdx.x >> 5)) * rows;
-            stride = gridDim.x * static_cast<uint64_t>(kWarpThreads / 32) * rows;
+            base = (blockIdx.x * (kWarpThreads / 32) + (threadIdx.x >> 5)) * rows;
+            stride = gridDim.x * (kWarpThreads / 32) * rows;
             sub = lane / P.lanes;
             at = lane % P.lanes;
             threads = P.lanes;
@@ -99,12 +99,15 @@ struct Place {
         }
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
-            col[u] = (static_cast<uint64_t>(u) * threads + at) * 8;
-            live[u] = live_of(P.cols, col[u]);
+            col[u] = (u * threads + at) * 8;
+            live[u] = FULL ? 8 : live_of(P.cols, col[u]);
         }
     }
-    __device__ uint64_t row() const { return base + sub; }
-    __device__ int of(int u, uint64_t row, uint64_t rows) const { return row < rows ? live[u] : 0; }
+    __device__ uint32_t row() const { return base + sub; }
+    __device__ int of(int u, uint32_t row, uint32_t rows) const
+    {
+        return FULL && !WARP ? 8 : row < rows ? live[u] : 0;
+    }
 };
 
 // Sums of a block's warps: `part` holds theirs, `turn` says which half of it this row
@@ -122,41 +125,48 @@ __device__ __forceinline__ float2 exchange(Parts &parts, uint32_t turn, float2 m
 }
 
 // How many of a row's values warp `lane` of the block holds.
-__device__ __forceinline__ float count_of(uint64_t cols)
+__device__ __forceinline__ float count_of(uint32_t cols)
 {
-    const uint64_t first = (threadIdx.x & 31) * 256ull;
+    const uint32_t first = (threadIdx.x & 31) * 256;
     float n = 0.0f;
     if ((threadIdx.x & 31) < blockDim.x >> 5)
         for (int u = 0; u < kUnits; ++u) {
-            const uint64_t col = first + u * blockDim.x * 8ull;
+            const uint32_t col = first + u * blockDim.x * 8;
             n += col >= cols ? 0.0f : static_cast<float>(cols - col < 256 ? cols - col : 256);
         }
     return n;
 }
 
-template <int DT, bool WARP, bool KEEP>
+template <int DT, bool WARP, bool KEEP, bool FULL>
 __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) forward_kernel(const __grid_constant__ Params P)
 {
     __shared__ Parts parts;
-    Place<WARP> at(P);
+    Place<WARP, FULL> at(P);
     float counts = 0.0f, own = 0.0f;            // of warp `lane`, of the caller's
     if (!WARP) {
         counts = count_of(P.cols);
         own = __shfl_sync(0xFFFFFFFFu, counts, threadIdx.x >> 5);
     }
     const float over_own = own > 0.0f ? __frcp_rn(own) : 0.0f;
-    kept::Raw<DT> raw[kUnits];
+    kept::Raw<DT> next[kUnits];
     auto load = [&]() {
+        if (at.base >= P.rows) return;
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u)
-            raw[u] = kept::fetch<DT>(P.x.p, at.row() * P.x.ld + at.col[u], at.of(u, at.row(), P.rows), P.x.vec);
+        for (int u = 0; u < kUnits; ++u) {
+            const int live = at.of(u, at.row(), P.rows);
+            next[u] = kept::fetch<DT, FULL && !WARP>(P.x, at.row(), at.col[u], live, P.x.vec);
+        }
     };
     load();
     for (uint32_t turn = 0; at.base < P.rows; turn ^= 1) {
-        const uint64_t row = at.row();
+        const uint32_t row = at.row();
+        kept::Raw<DT> raw[kUnits];
         float x[kUnits][8], sum = 0.0f, squares = 0.0f, mean = 0.0f;
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) kept::values(raw[u], x[u]);
+        for (int u = 0; u < kUnits; ++u) {
+            raw[u] = next[u];
+            kept::values(raw[u], x[u]);
+        }
         at.base += at.stride;
         load();
         if (P.centred) {
@@ -172,7 +182,7 @@ __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) forward_kernel(con
             for (int u = 0; u < kUnits; ++u)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float d = i < at.live[u] ? __fsub_rn(x[u][i], mean) : 0.0f;
+                    const float d = FULL || i < at.live[u] ? __fsub_rn(x[u][i], mean) : 0.0f;
                     squares = __fmaf_rn(d, d, squares);
                 }
         } else {
@@ -201,10 +211,10 @@ __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) forward_kernel(con
         for (int u = 0; u < kUnits; ++u) {
             const int live = at.of(u, row, P.rows);
             if (KEEP) {
-                if (P.sr) kept::keep8<true>(P.to, row, at.col[u], live, x[u]);
-                else kept::keep8<false>(P.to, row, at.col[u], live, x[u]);
+                if (P.sr) kept::keep8<true, DT, FULL && !WARP>(P.to, row, at.col[u], live, raw[u]);
+                else kept::keep8<false, DT, FULL && !WARP>(P.to, row, at.col[u], live, raw[u]);
             }
-            if (live == 0) continue;
+            if (!(FULL && !WARP) && live == 0) continue;
             float w[8], b[8];
             params8(P.w, P.w_dtype, at.col[u], live, P.w_vec, 1.0f, w);
             if (P.b) {
@@ -215,7 +225,7 @@ __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) forward_kernel(con
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[u][i] = __fmul_rn(__fmul_rn(__fsub_rn(x[u][i], mean), rstd), w[i]);
             }
-            kept::store8<DT>(P.y.p, row * P.y.ld + at.col[u], live, P.y.vec, x[u]);
+            kept::store8<DT, FULL && !WARP>(P.y, row, at.col[u], live, P.y.vec, x[u]);
         }
     }
 }
@@ -238,19 +248,19 @@ template <int DT, bool KEEP>
 __global__ void __launch_bounds__(kLongThreads) forward_long_kernel(const __grid_constant__ Params P)
 {
     __shared__ float part[32];
-    const uint64_t end = (P.cols + 255) / 256 * 256;        // whole warps take part, for the groups
-    for (uint64_t row = blockIdx.x; row < P.rows; row += gridDim.x) {
+    const uint32_t end = (P.cols + 255) / 256 * 256;        // whole warps take part, for the groups
+    for (uint32_t row = blockIdx.x; row < P.rows; row += gridDim.x) {
         float sum = 0.0f, squares = 0.0f, x[8];
         if (P.centred)
-            for (uint64_t col = threadIdx.x * 8ull; col < P.cols; col += kLongThreads * 8ull) {
-                muon::load8(P.x.p, DT, row * P.x.ld + col, live_of(P.cols, col), P.x.vec, x);
+            for (uint32_t col = threadIdx.x * 8; col < P.cols; col += kLongThreads * 8) {
+                kept::values(kept::fetch<DT>(P.x, row, col, live_of(P.cols, col), P.x.vec), x);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sum = __fadd_rn(sum, x[i]);
             }
         const float mean = P.centred ? __fmul_rn(block_sum(sum, part), P.over_n) : 0.0f;
-        for (uint64_t col = threadIdx.x * 8ull; col < P.cols; col += kLongThreads * 8ull) {
+        for (uint32_t col = threadIdx.x * 8; col < P.cols; col += kLongThreads * 8) {
             const int live = live_of(P.cols, col);
-            muon::load8(P.x.p, DT, row * P.x.ld + col, live, P.x.vec, x);
+            kept::values(kept::fetch<DT>(P.x, row, col, live, P.x.vec), x);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float d = i < live ? __fsub_rn(x[i], mean) : 0.0f;
@@ -262,12 +272,13 @@ __global__ void __launch_bounds__(kLongThreads) forward_long_kernel(const __grid
             P.rstd[row] = rstd;
             if (P.mean) P.mean[row] = mean;
         }
-        for (uint64_t col = threadIdx.x * 8ull; col < end; col += kLongThreads * 8ull) {
+        for (uint32_t col = threadIdx.x * 8; col < end; col += kLongThreads * 8) {
             const int live = live_of(P.cols, col);
-            muon::load8(P.x.p, DT, row * P.x.ld + col, live, P.x.vec, x);
+            const kept::Raw<DT> raw = kept::fetch<DT>(P.x, row, col, live, P.x.vec);
+            kept::values(raw, x);
             if (KEEP) {
-                if (P.sr) kept::keep8<true>(P.to, row, col, live, x);
-                else kept::keep8<false>(P.to, row, col, live, x);
+                if (P.sr) kept::keep8<true, DT, false>(P.to, row, col, live, raw);
+                else kept::keep8<false, DT, false>(P.to, row, col, live, raw);
             }
             if (live == 0) continue;
             float w[8], b[8];
@@ -275,7 +286,7 @@ __global__ void __launch_bounds__(kLongThreads) forward_long_kernel(const __grid
             params8(P.b, P.b_dtype, col, live, P.b_vec, 0.0f, b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = __fmaf_rn(__fmul_rn(__fsub_rn(x[i], mean), rstd), w[i], b[i]);
-            kept::store8<DT>(P.y.p, row * P.y.ld + col, live, P.y.vec, x);
+            kept::store8<DT>(P.y, row, col, live, P.y.vec, x);
         }
     }
 }
@@ -283,10 +294,10 @@ __global__ void __launch_bounds__(kLongThreads) forward_long_kernel(const __grid
 // ---- backward
 
 template <int DT, bool KEPT>
-__device__ __forceinline__ void input8(const Params &P, uint64_t row, uint64_t col, int live, float x[8])
+__device__ __forceinline__ void input8(const Params &P, uint32_t row, uint32_t col, int live, float x[8])
 {
     if (KEPT) kept::values(kept::fetch_codes(P.from, row, col, live), x);
-    else muon::load8(P.x.p, DT, row * P.x.ld + col, live, P.x.vec, x);
+    else kept::values(kept::fetch<DT>(P.x, row, col, live, P.x.vec), x);
 }
 
 template <int BYTES>
@@ -299,12 +310,12 @@ __device__ __forceinline__ void copy_async(void *to, const void *from)
 // Eight values of a matrix, from memory to a thread's place in shared memory (words
 // `step` apart for 16 bytes each): asynchronously, in 16 bytes or, off alignment, f32
 // by one; bf16 off alignment at once.
-template <int DT>
-__device__ __forceinline__ void bring(uint4 *to, uint32_t step, const kept::Matrix &M, uint64_t at, int live)
+template <int DT, bool FULL>
+__device__ __forceinline__ void bring(uint4 *to, uint32_t step, const kept::Matrix &M, uint32_t row, uint32_t col, int live)
 {
     constexpr int kWords = DT == ASR_BF16 ? 1 : 2;
-    const char *from = static_cast<const char *>(M.p) + at * (DT == ASR_BF16 ? 2 : 4);
-    if (M.vec && live == 8) {
+    const char *from = static_cast<const char *>(M.p) + kept::place(row, M.ld, col) * (DT == ASR_BF16 ? 2 : 4);
+    if (FULL || (M.vec && live == 8)) {
 #pragma unroll
         for (int i = 0; i < kWords; ++i) copy_async<16>(to + i * step, from + 16 * i);
     } else if (DT == ASR_F32) {
@@ -315,7 +326,7 @@ __device__ __forceinline__ void bring(uint4 *to, uint32_t step, const kept::Matr
             else *w = 0;
         }
     } else {
-        const kept::Raw<DT> r = kept::fetch<DT>(M.p, at, live, false);
+        const kept::Raw<DT> r = kept::fetch<DT>(M, row, col, live, false);
         to[0] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
     }
 }
@@ -342,16 +353,19 @@ struct Stage {
 static_assert(kUnits == 2, "codes of two units fill a word");
 
 // Stages of the ring: four, fewer where a block's values and weight would not leave
-// room (227 KB) for them, or for a second block of up to 256 threads.
+// room (227 KB) for them.
 template <int DT, bool KEPT, int THREADS>
 struct Ring {
-    static constexpr int kRoom = (THREADS <= 256 ? 110 : 220) * 1024 - THREADS * 64;
+    static constexpr int kRoom = 220 * 1024 - THREADS * 64;
     static constexpr int kFit = kRoom / (THREADS * Stage<DT, KEPT>::kWords * 16);
     static constexpr int kStages = kFit < 1 ? 1 : kFit > 4 ? 4 : kFit;
     static size_t bytes(unsigned threads) { return (static_cast<size_t>(kStages) * Stage<DT, KEPT>::kWords + 4) * 16 * threads; }
 };
 
-template <int DT, bool WARP, bool KEPT, int THREADS>
+// What a norm that is not centred, or has no bias, does not need is computed all the
+// same: a form without it had a quarter fewer instructions and took as long (8,192 x
+// 4,096 from codes 49 us, 46 to 48 as it is).
+template <int DT, bool WARP, bool KEPT, int THREADS, bool FULL>
 __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant__ Params P)
 {
     using S = Stage<DT, KEPT>;
@@ -359,21 +373,22 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
     extern __shared__ __align__(16) uint4 ring[];           // [weight: 4][stage][word][thread]
     __shared__ Parts parts;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    Place<WARP> at(P);
+    Place<WARP, FULL> at(P);
     const uint32_t step = blockDim.x;
     uint4 *const mine = ring + threadIdx.x;
-    auto bring_row = [&](uint64_t row, uint32_t slot) {
+    auto bring_row = [&](uint32_t row, uint32_t slot) {
         uint4 *to = mine + (4 + slot * S::kWords) * step;
+        if (row < P.rows)
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             const int live = at.of(u, row, P.rows);
-            if (live == 0) continue;
-            bring<DT>(to + u * (S::kDy / kUnits) * step, step, P.dy, row * P.dy.ld + at.col[u], live);
+            if (!FULL && live == 0) continue;
+            bring<DT, FULL>(to + u * (S::kDy / kUnits) * step, step, P.dy, row, at.col[u], live);
             if (!KEPT) {
-                bring<DT>(to + (S::kDy + u * (S::kDy / kUnits)) * step, step, P.x, row * P.x.ld + at.col[u], live);
+                bring<DT, FULL>(to + (S::kDy + u * (S::kDy / kUnits)) * step, step, P.x, row, at.col[u], live);
             } else {
                 uint2 *q = reinterpret_cast<uint2 *>(to + S::kDy * step) + u;
-                if (P.from.vec && live == 8) copy_async<8>(q, P.from.q + row * P.from.q_ld + at.col[u]);
+                if (FULL || (P.from.vec && live == 8)) copy_async<8>(q, P.from.q + kept::place(row, P.from.q_ld, at.col[u]));
                 else *q = kept::fetch_codes(P.from, row, at.col[u], live).v;
             }
         }
@@ -382,14 +397,14 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
     // what is too little for the ring is fetched a row ahead
     float mean = 0.0f, rstd = 0.0f;
     uint32_t power[kUnits] = {};
-    auto fetch_rest = [&](uint64_t row) {
+    auto fetch_rest = [&](uint32_t row) {
         if (row >= P.rows) return;
         rstd = P.rstd[row];
         if (P.centred) mean = P.mean[row];
         if (KEPT)
 #pragma unroll
             for (int u = 0; u < kUnits; ++u)
-                if (at.live[u]) power[u] = P.from.power[row * P.from.power_ld + (at.col[u] >> 5)];
+                if (FULL || at.live[u]) power[u] = P.from.power[kept::place(row, P.from.power_ld, at.col[u] >> 5)];
     };
     if constexpr (kStages > 1) {
 #pragma unroll
@@ -407,7 +422,7 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
     float dw[kUnits][8] = {}, db[kUnits][8] = {};
     uint32_t slot = 0;
     for (uint32_t turn = 0; at.base < P.rows; turn ^= 1) {
-        const uint64_t row = at.row();
+        const uint32_t row = at.row();
         bring_row(row + (kStages - 1) * at.stride, slot ? slot - 1 : kStages - 1);
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
         const uint4 *from = mine + (4 + slot * S::kWords) * step;
@@ -429,33 +444,34 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
             else taken<DT>(from + (S::kDy + u * (S::kDy / kUnits)) * step, step, h[u]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float4 w = *reinterpret_cast<const float4 *>(mine + (2 * u + (i >> 2)) * step);
-                h[u][i] = __fmul_rn(P.centred ? __fsub_rn(h[u][i], m) : h[u][i], r);
+                const float4 w4 = *reinterpret_cast<const float4 *>(mine + (2 * u + (i >> 2)) * step);
+                const float w = (i & 3) == 0 ? w4.x : (i & 3) == 1 ? w4.y : (i & 3) == 2 ? w4.z : w4.w;
+                h[u][i] = __fmul_rn(__fsub_rn(h[u][i], m), r);
                 dw[u][i] = __fmaf_rn(g[u][i], h[u][i], dw[u][i]);
-                if (P.db) db[u][i] = __fadd_rn(db[u][i], g[u][i]);
-                g[u][i] = __fmul_rn(g[u][i], (i & 3) == 0 ? w.x : (i & 3) == 1 ? w.y : (i & 3) == 2 ? w.z : w.w);
-                if (P.centred) sum = __fadd_rn(sum, g[u][i]);
+                db[u][i] = __fadd_rn(db[u][i], g[u][i]);
+                g[u][i] = __fmul_rn(g[u][i], w);
+                sum = __fadd_rn(sum, g[u][i]);
                 along = __fmaf_rn(g[u][i], h[u][i], along);
             }
         }
         if (!P.dx.p) continue;
-        if (P.centred) sum = WARP ? lane_sum(sum, P.lanes) : warp_sum(sum);
+        sum = WARP ? lane_sum(sum, P.lanes) : warp_sum(sum);
         along = WARP ? lane_sum(along, P.lanes) : warp_sum(along);
         if (!WARP) {
             const float2 p = exchange(parts, turn, make_float2(sum, along));
-            if (P.centred) sum = warp_sum(p.x);
+            sum = warp_sum(p.x);
             along = warp_sum(p.y);
         }
-        sum = __fmul_rn(sum, P.over_n);
-        along = __fmul_rn(along, P.over_n);
+        sum = !P.centred ? 0.0f : __fmul_rn(__fmul_rn(sum, P.over_n), r);
+        along = __fmul_rn(__fmul_rn(along, P.over_n), r);
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             const int live = at.of(u, row, P.rows);
-            if (live == 0) continue;
+            if (!(FULL && !WARP) && live == 0) continue;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                g[u][i] = __fmul_rn(__fmaf_rn(-h[u][i], along, __fsub_rn(g[u][i], sum)), r);
-            kept::store8<DT>(P.dx.p, row * P.dx.ld + at.col[u], live, P.dx.vec, g[u]);
+                g[u][i] = __fmaf_rn(-h[u][i], along, __fmaf_rn(g[u][i], r, -sum));
+            kept::store8<DT, FULL && !WARP>(P.dx, row, at.col[u], live, P.dx.vec, g[u]);
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -471,7 +487,7 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
             for (int i = 0; i < 8; ++i)
                 for (uint32_t d = P.lanes; d < 32; d <<= 1) {
                     dw[u][i] = __fadd_rn(dw[u][i], __shfl_xor_sync(0xFFFFFFFFu, dw[u][i], d));
-                    if (P.db) db[u][i] = __fadd_rn(db[u][i], __shfl_xor_sync(0xFFFFFFFFu, db[u][i], d));
+                    db[u][i] = __fadd_rn(db[u][i], __shfl_xor_sync(0xFFFFFFFFu, db[u][i], d));
                 }
         for (uint32_t w = 0; w < kWarpThreads / 32; ++w) {
             __syncthreads();
@@ -509,12 +525,12 @@ template <int DT, bool KEPT>
 __global__ void __launch_bounds__(kLongThreads) backward_long_kernel(const __grid_constant__ Params P)
 {
     __shared__ float part[32];
-    for (uint64_t row = blockIdx.x; row < P.rows; row += gridDim.x) {
+    for (uint32_t row = blockIdx.x; row < P.rows; row += gridDim.x) {
         const float mean = P.centred ? P.mean[row] : 0.0f, rstd = P.rstd[row];
         float sum = 0.0f, along = 0.0f, g[8], h[8], w[8];
-        for (uint64_t col = threadIdx.x * 8ull; col < P.cols; col += kLongThreads * 8ull) {
+        for (uint32_t col = threadIdx.x * 8; col < P.cols; col += kLongThreads * 8) {
             const int live = live_of(P.cols, col);
-            muon::load8(P.dy.p, DT, row * P.dy.ld + col, live, P.dy.vec, g);
+            kept::values(kept::fetch<DT>(P.dy, row, col, live, P.dy.vec), g);
             input8<DT, KEPT>(P, row, col, live, h);
             params8(P.w, P.w_dtype, col, live, P.w_vec, 1.0f, w);
 #pragma unroll
@@ -526,16 +542,16 @@ __global__ void __launch_bounds__(kLongThreads) backward_long_kernel(const __gri
         }
         sum = P.centred ? __fmul_rn(block_sum(sum, part), P.over_n) : 0.0f;
         along = __fmul_rn(block_sum(along, part), P.over_n);
-        for (uint64_t col = threadIdx.x * 8ull; col < P.cols; col += kLongThreads * 8ull) {
+        for (uint32_t col = threadIdx.x * 8; col < P.cols; col += kLongThreads * 8) {
             const int live = live_of(P.cols, col);
-            muon::load8(P.dy.p, DT, row * P.dy.ld + col, live, P.dy.vec, g);
+            kept::values(kept::fetch<DT>(P.dy, row, col, live, P.dy.vec), g);
             input8<DT, KEPT>(P, row, col, live, h);
             params8(P.w, P.w_dtype, col, live, P.w_vec, 1.0f, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 g[i] = __fmul_rn(__fmaf_rn(-__fmul_rn(__fsub_rn(h[i], mean), rstd), along,
                                            __fsub_rn(__fmul_rn(g[i], w[i]), sum)), rstd);
-            kept::store8<DT>(P.dx.p, row * P.dx.ld + col, live, P.dx.vec, g);
+            kept::store8<DT>(P.dx, row, col, live, P.dx.vec, g);
         }
     }
 }
@@ -544,12 +560,12 @@ __global__ void __launch_bounds__(kLongThreads) backward_long_kernel(const __gri
 template <int DT, bool KEPT>
 __global__ void __launch_bounds__(256) columns_kernel(const __grid_constant__ Params P)
 {
-    const uint64_t col = (blockIdx.x * 256ull + threadIdx.x) * 8;
+    const uint32_t col = (blockIdx.x * 256 + threadIdx.x) * 8;
     const int live = live_of(P.cols, col);
     float dw[8] = {}, db[8] = {}, g[8], h[8];
-    for (uint64_t row = blockIdx.y; row < P.rows; row += gridDim.y) {
+    for (uint32_t row = blockIdx.y; row < P.rows; row += gridDim.y) {
         const float mean = P.centred ? P.mean[row] : 0.0f, rstd = P.rstd[row];
-        muon::load8(P.dy.p, DT, row * P.dy.ld + col, live, P.dy.vec, g);
+        kept::values(kept::fetch<DT>(P.dy, row, col, live, P.dy.vec), g);
         input8<DT, KEPT>(P, row, col, live, h);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -622,17 +638,25 @@ uint32_t lanes_of(uint64_t cols)
     return n;
 }
 
-template <int DT, bool KEEP>
+template <int DT, bool KEEP, bool FULL>
 Kernel forward_of(int shape)
 {
-    return shape == kWarp ? forward_kernel<DT, true, KEEP> : shape == kBlock ? forward_kernel<DT, false, KEEP>
-                                                                             : forward_long_kernel<DT, KEEP>;
+    return shape == kWarp ? forward_kernel<DT, true, KEEP, FULL> : shape == kBlock ? forward_kernel<DT, false, KEEP, FULL>
+                                                                                   : forward_long_kernel<DT, KEEP>;
 }
 
-Kernel forward_of(int32_t dtype, int shape, bool keep)
+Kernel forward_of(int32_t dtype, int shape, bool keep, bool full)
 {
-    if (dtype == ASR_BF16) return keep ? forward_of<ASR_BF16, true>(shape) : forward_of<ASR_BF16, false>(shape);
-    return keep ? forward_of<ASR_F32, true>(shape) : forward_of<ASR_F32, false>(shape);
+    if (dtype != ASR_BF16) return keep ? forward_of<ASR_F32, true, false>(shape) : forward_of<ASR_F32, false, false>(shape);
+    if (full) return keep ? forward_of<ASR_BF16, true, true>(shape) : forward_of<ASR_BF16, false, true>(shape);
+    return keep ? forward_of<ASR_BF16, true, false>(shape) : forward_of<ASR_BF16, false, false>(shape);
+}
+
+// Whether every thread of a row's has its sixteen values.
+bool whole(uint64_t cols)
+{
+    const int shape = shape_of(cols);
+    return shape == kWarp ? cols == lanes_of(cols) * 8 * kUnits : shape == kBlock && cols % kWarpCols == 0;
 }
 
 // A backward kernel and its shared memory, the registers of its blocks budgeted for
@@ -642,26 +666,30 @@ struct Backward {
     size_t smem;
 };
 
-template <int DT, bool KEPT, bool WARP, int THREADS>
+template <int DT, bool KEPT, bool WARP, int THREADS, bool FULL>
 Backward backward_at(unsigned threads)
 {
-    return Backward{backward_kernel<DT, WARP, KEPT, THREADS>, Ring<DT, KEPT, THREADS>::bytes(threads)};
+    return Backward{backward_kernel<DT, WARP, KEPT, THREADS, FULL>, Ring<DT, KEPT, THREADS>::bytes(threads)};
 }
 
-template <int DT, bool KEPT>
+template <int DT, bool KEPT, bool FULL>
 Backward backward_of(int shape, unsigned threads)
 {
-    if (shape == kWarp) return backward_at<DT, KEPT, true, kWarpThreads>(threads);
+    if (shape == kWarp) return backward_at<DT, KEPT, true, kWarpThreads, FULL>(threads);
     if (shape == kLong) return Backward{backward_long_kernel<DT, KEPT>, 0};
-    return threads <= 256 ? backward_at<DT, KEPT, false, 256>(threads) : threads <= 512 ? backward_at<DT, KEPT, false, 512>(threads)
-                                                                     : backward_at<DT, KEPT, false, 1024>(threads);
+    return threads <= 512 ? backward_at<DT, KEPT, false, 512, FULL>(threads) : backward_at<DT, KEPT, false, 1024, FULL>(threads);
 }
 
-Backward backward_of(int32_t dtype, bool codes, int shape, unsigned threads)
+template <bool KEPT>
+Backward backward_of(int32_t dtype, int shape, unsigned threads, bool full)
 {
-    if (dtype == ASR_BF16)
-        return codes ? backward_of<ASR_BF16, true>(shape, threads) : backward_of<ASR_BF16, false>(shape, threads);
-    return codes ? backward_of<ASR_F32, true>(shape, threads) : backward_of<ASR_F32, false>(shape, threads);
+    if (dtype != ASR_BF16) return backward_of<ASR_F32, KEPT, false>(shape, threads);
+    return full ? backward_of<ASR_BF16, KEPT, true>(shape, threads) : backward_of<ASR_BF16, KEPT, false>(shape, threads);
+}
+
+Backward backward_of(int32_t dtype, bool codes, int shape, unsigned threads, bool full)
+{
+    return codes ? backward_of<true>(dtype, shape, threads, full) : backward_of<false>(dtype, shape, threads, full);
 }
 
 template <int DT>
@@ -686,14 +714,16 @@ asr_status setup()
     for (int32_t dtype : {ASR_F32, ASR_BF16})
         for (int kept = 0; kept < 2; ++kept) {
             if (e == cudaSuccess) e = prod::load_kernel(columns_of(dtype, kept != 0));
-            for (int shape : {kWarp, kBlock, kLong}) {
-                if (e == cudaSuccess) e = prod::load_kernel(forward_of(dtype, shape, kept != 0));
-                for (unsigned threads : {256u, 512u, 1024u}) {
-                    const Backward k = backward_of(dtype, kept != 0, shape, threads);
+            for (int form = 0; form < 6; ++form) {
+                const int shape = form % 3;
+                const bool full = form >= 3;
+                if (e == cudaSuccess) e = prod::load_kernel(forward_of(dtype, shape, kept != 0, full));
+                for (unsigned threads : {512u, 1024u}) {
+                    if (shape == kWarp) threads = kWarpThreads;
+                    const Backward k = backward_of(dtype, kept != 0, shape, threads, full);
                     if (e == cudaSuccess && k.smem)
                         e = cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem));
                     if (e == cudaSuccess) e = prod::load_kernel(k.kernel);
-                    if (shape == kWarp) break;
                 }
             }
         }
@@ -724,8 +754,8 @@ Params common(const asr_norm_params *p)
     std::memset(&P, 0, sizeof(P));
     P.w = p->weight;
     P.b = p->bias;
-    P.rows = p->rows;
-    P.cols = p->cols;
+    P.rows = static_cast<uint32_t>(p->rows);
+    P.cols = static_cast<uint32_t>(p->cols);
     P.eps = static_cast<float>(p->eps);
     P.over_n = static_cast<float>(1.0 / static_cast<double>(p->cols));
     P.w_dtype = static_cast<uint32_t>(p->weight_dtype);
@@ -762,7 +792,8 @@ asr_status forward(const asr_norm_params *p, const void *x, uint64_t x_ld, void 
     }
     const int shape = shape_of(p->cols);
     const unsigned threads = threads_of(p->cols);
-    auto kernel = forward_of(p->dtype, shape, to != nullptr);
+    const bool full = whole(p->cols) && P.x.vec && P.y.vec && (!to || P.to.vec);
+    auto kernel = forward_of(p->dtype, shape, to != nullptr, full);
     int most = 0;
     st = kept::resident(kernel, threads, 0, &most);
     if (st != ASR_OK) return st;
@@ -826,7 +857,8 @@ asr_status backward(const asr_norm_params *p, const void *dy, uint64_t dy_ld, co
         P.db = dbias != nullptr;
         const int shape = shape_of(p->cols);
         const unsigned threads = threads_of(p->cols);
-        const Backward k = backward_of(p->dtype, from != nullptr, shape, threads);
+        const bool full = whole(p->cols) && P.dy.vec && (!dx || P.dx.vec) && (from ? P.from.vec : P.x.vec);
+        const Backward k = backward_of(p->dtype, from != nullptr, shape, threads, full);
         int most = 0;
         st = kept::resident(k.kernel, static_cast<int>(threads), k.smem, &most);
         if (st != ASR_OK) return st;
