@@ -959,6 +959,11 @@ _FUNCTION = {"silu": ASR_SILU, "gelu": ASR_GELU}
 CHECKPOINT_GROUP = 32           # values of a row that share a power of two
 
 
+def _check_rounding(rounding):
+    if rounding not in _ROUNDING:
+        raise ValueError(f"rounding must be 'sr' or 'rne', not {rounding!r}")
+
+
 def _pack_checkpoint(pq, pp, q_ld, power_ld, rounding="rne", base_index=0, step=0, seed=0):
     """The C struct of a checkpoint whose pointers and pitches have been checked."""
     r = _ROUNDING.get(rounding)

@@ -65,6 +65,7 @@ def checkpoint_int8(x, *, rounding="rne", base_index: int = 0, step: int = 0, se
     of a row share a power of two.  ``rounding="sr"`` rounds stochastically, so that
     what is read back is x on average (to within 2^-16 of a step)."""
     px, rows, cols, ld = _lib._matrix_ptr(x, "x", _FLOATS)
+    _lib._check_rounding(rounding)
     with _lib._on_device(x.device):
         c = empty_checkpoint(rows, cols, x.device, x.dtype)
         _lib._check(_lib.lib().asr_checkpoint_int8(px, _lib._dt(x), rows, cols, ld, c._struct(rounding, base_index, step, seed),
@@ -130,15 +131,13 @@ class _Int8LinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, step, seed, save):
         x, weight = _by_rows(x), _by_rows(weight)
-        ctx.key, ctx.x_dtype = (step, seed), x.dtype
+        ctx.key, ctx.x_dtype, ctx.save = (step, seed), x.dtype, save
         if save == "int8" and ctx.needs_input_grad[1]:
-            kept = checkpoint_int8(x, rounding="sr", step=step, seed=seed)
-            ctx.save_for_backward(weight, kept.data)
+            ctx.save_for_backward(weight, checkpoint_int8(x, rounding="sr", step=step, seed=seed).data)
         elif save == "int8":                # dx does not read x
             ctx.save_for_backward(weight)
-        else:
+        elif save:
             ctx.save_for_backward(weight, x)
-        ctx.save = save
         q = int8_empty(*weight.shape, weight.device)
         scale = torch.empty(weight.shape[0], dtype=torch.float32, device=weight.device)
         asr_quantize_int8(weight, q, scale)
@@ -224,9 +223,9 @@ class Int8Linear(_CountedModule):
         torch.nn.init.normal_(self.weight, std=in_features ** -0.5)
 
     def forward(self, x):
-        self._count(x, self.weight)
+        save = self.save if self._count(x, self.weight) else None
         flat = x.reshape(-1, self.in_features)
-        y = _Int8LinearFunction.apply(flat, self.weight, self.calls, self.seed, self.save)
+        y = _Int8LinearFunction.apply(flat, self.weight, self.calls, self.seed, save)
         return y.reshape(*x.shape[:-1], self.out_features)
 
     def extra_repr(self):

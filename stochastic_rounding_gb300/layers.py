@@ -38,6 +38,7 @@ def activation(x, function="silu", *, gated=False, save=None, rounding="rne", st
     ``save`` returns (y, saved) for ``activation_grads``: "input" saves x itself,
     "int8" its 8-bit checkpoint, made in the same pass."""
     _check_save(save)
+    _lib._check_rounding(rounding)
     code = _lib._function(function)
     px, rows, width, ld = _lib._matrix_ptr(x, "x", _FLOATS)
     if gated and width % 2:
@@ -81,7 +82,7 @@ class _ActivationFunction(torch.autograd.Function):
     def forward(ctx, x, function, gated, save, rounding, step, seed):
         x = _by_rows(x)
         ctx.kind = (function, gated, x.shape[1], x.dtype)
-        if not ctx.needs_input_grad[0]:
+        if save is None:
             return activation(x, function, gated=gated)
         y, saved = activation(x, function, gated=gated, save=save, rounding=rounding, step=step, seed=seed)
         ctx.kept = save == "int8"
@@ -114,9 +115,9 @@ class Activation(_CountedModule):
         self.function, self.gated, self.save, self.rounding = function, bool(gated), save, rounding
 
     def forward(self, x):
-        self._count(x)
-        flat = x.reshape(-1, x.shape[-1])
-        y = _ActivationFunction.apply(flat, self.function, self.gated, self.save, self.rounding, self.calls, self.seed)
+        save = self.save if self._count(x) else None
+        flat = x.reshape(x.shape[:-1].numel(), x.shape[-1])
+        y = _ActivationFunction.apply(flat, self.function, self.gated, save, self.rounding, self.calls, self.seed)
         return y.reshape(*x.shape[:-1], y.shape[-1])
 
     def extra_repr(self):
@@ -147,6 +148,7 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, centred=True, sa
     ``layer_norm_grads``: "input" saves x itself, "int8" its 8-bit checkpoint, made in
     the same pass."""
     _check_save(save)
+    _lib._check_rounding(rounding)
     px, rows, cols, ld = _lib._matrix_ptr(x, "x", _FLOATS)
     d = x.get_device()
     p = _lib._norm_params(rows, cols, _lib._dt(x), weight, bias, float(eps), centred, d)
@@ -197,7 +199,7 @@ class _LayerNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps, centred, save, rounding, step, seed):
         x = _by_rows(x)
-        if not any(ctx.needs_input_grad):
+        if save is None:
             return layer_norm(x, weight, bias, eps=eps, centred=centred)
         ctx.kept, ctx.kind = save == "int8", (x.dtype, None if bias is None else bias.dtype)
         y, saved = layer_norm(x, weight, bias, eps=eps, centred=centred, save=save, rounding=rounding, step=step, seed=seed)
@@ -235,10 +237,12 @@ class LayerNorm(_CountedModule):
             self.register_parameter("bias", None)
 
     def forward(self, x):
-        self._count(x, self.weight, self.bias)
-        flat = x.reshape(-1, self.width)
-        y = _LayerNormFunction.apply(flat, self.weight, self.bias, self.eps, self.centred, self.save, self.rounding,
-                                     self.calls, self.seed)
+        if x.shape[-1:] != (self.width,):
+            raise ValueError(f"the last dimension must be {self.width}, not that of {tuple(x.shape)}")
+        save = self.save if self._count(x, self.weight, self.bias) else None
+        flat = x.reshape(x.shape[:-1].numel(), self.width)
+        y = _LayerNormFunction.apply(flat, self.weight, self.bias, self.eps, self.centred, save, self.rounding, self.calls,
+                                     self.seed)
         return y.reshape(x.shape)
 
     def extra_repr(self):
