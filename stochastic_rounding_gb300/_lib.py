@@ -341,12 +341,6 @@ def _current_device() -> int:
     return get() if get is not None and torch.cuda.is_initialized() else torch.cuda.current_device()
 
 
-def _raw_stream(index: int) -> int:
-    """The current stream of CUDA device ``index``, as a number."""
-    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
-    return raw(index) if raw is not None else _torch().cuda.current_stream(index).cuda_stream
-
-
 def _stream_handle(device, stream):
     """The cudaStream_t of ``stream``, or of the device's current stream."""
     torch = _torch()
@@ -788,6 +782,23 @@ def asr_muon_sr_multi_tensor(tensors, *, lr, momentum=0.95, weight_decay=0.1, ne
 # ------------------------------------------------- 8-bit integer products
 
 _AXIS = {"rows": ASR_ROWS, "columns": ASR_COLUMNS}
+
+
+def _rows_of(t, name):
+    """As ``_matrix_ptr`` for float32 or bfloat16, with the dtype's code and the device's index: (pointer, rows, columns,
+    row pitch, dtype, device).  What is not as it should be is left to ``_matrix_ptr`` to say."""
+    torch = _torch()
+    if isinstance(t, torch.Tensor) and t.is_cuda:
+        shape, dtype = t.shape, t.dtype
+        if len(shape) == 2 and (dtype is torch.bfloat16 or dtype is torch.float32):
+            rows, cols = shape
+            ld, one = t.stride()
+            if rows <= 1:
+                ld = cols
+            if ld >= cols and (one == 1 or cols <= 1):
+                return t.data_ptr(), rows, cols, ld, ASR_BF16 if dtype is torch.bfloat16 else ASR_F32, t.get_device()
+    _matrix_ptr(t, name, (torch.bfloat16, torch.float32))
+    raise ValueError(f"{name} must be a matrix whose rows are contiguous")
 
 
 def _matrix_ptr(t, name, dtypes, device=None):

@@ -48,57 +48,77 @@ class Int8Checkpoint(NamedTuple):
 
 def empty_checkpoint(rows: int, cols: int, device, dtype) -> Int8Checkpoint:
     """An uninitialised checkpoint of a rows x cols matrix."""
-    groups = (cols + _lib.CHECKPOINT_GROUP - 1) // _lib.CHECKPOINT_GROUP
-    width = (cols + 15) // 16 * 16 + (groups + 15) // 16 * 16
+    width = (cols + 15) // 16 * 16 + ((cols + 31) // 32 + 15) // 16 * 16
     return Int8Checkpoint(torch.empty((rows, width), dtype=torch.uint8, device=device), cols, dtype)
 
 
 # The functions that return new tensors check what they are given and call the library
 # themselves: going through the calls that fill a caller's tensors would check the new
-# ones too, and cost as much again as the launch.
+# ones too, and cost as much again as the launch.  For small tensors the host's time is
+# the call's: a launch 3 us, an allocation beside it 3 to 5.
 
 _FLOATS = (torch.bfloat16, torch.float32)
+
+
+def _elsewhere(device: int) -> bool:
+    """Whether a CUDA device is not the current one."""
+    return device != _get_device()
+
+
+def _python_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _python_stream
 
 
 def checkpoint_int8(x, *, rounding="rne", base_index: int = 0, step: int = 0, seed: int = 0) -> Int8Checkpoint:
     """``x`` (2-D, float32 or bfloat16) kept in 8 bits for a backward pass: 32 values
     of a row share a power of two.  ``rounding="sr"`` rounds stochastically, so that
     what is read back is x on average (to within 2^-16 of a step)."""
-    px, rows, cols, ld = _lib._matrix_ptr(x, "x", _FLOATS)
+    px, rows, cols, ld, code, d = _lib._rows_of(x, "x")
     _lib._check_rounding(rounding)
-    with _lib._on_device(x.device):
-        c = empty_checkpoint(rows, cols, x.device, x.dtype)
-        _lib._check(_lib.lib().asr_checkpoint_int8(px, _lib._dt(x), rows, cols, ld, c._struct(rounding, base_index, step, seed),
-                                                   _lib._raw_stream(x.get_device())), "asr_checkpoint_int8")
+    if _elsewhere(d):
+        with torch.cuda.device(d):
+            return checkpoint_int8(x, rounding=rounding, base_index=base_index, step=step, seed=seed)
+    c = empty_checkpoint(rows, cols, x.device, x.dtype)
+    _lib._check(_lib.lib().asr_checkpoint_int8(px, code, rows, cols, ld, c._struct(rounding, base_index, step, seed),
+                                               _raw_stream(d)), "asr_checkpoint_int8")
     return c
 
 
 def _checked(c: Int8Checkpoint, rows, cols, device):
     """The C struct of a checkpoint that a caller gives."""
-    if not isinstance(c, Int8Checkpoint):
-        raise TypeError("an Int8Checkpoint is wanted")
-    t = c.data
+    t, n = c.data, c.cols
     if not t.is_cuda or t.dtype != torch.uint8 or t.dim() != 2 or not t.is_contiguous():
         raise ValueError("a checkpoint's data must be a contiguous 2-D uint8 CUDA tensor")
-    if device is not None and t.get_device() != device:
+    if t.get_device() != device:
         raise ValueError(f"the checkpoint is on {t.device}; the call's other tensors are on cuda:{device}")
-    want = (cols + 15) // 16 * 16 + ((cols + 31) // 32 + 15) // 16 * 16
-    if c.cols != cols or t.shape[0] != rows or t.shape[1] != want:
-        raise ValueError(f"a checkpoint of {(rows, cols)} is wanted, not of {(t.shape[0], c.cols)} in {tuple(t.shape)}")
-    return c._struct()
+    have, width = t.shape
+    at = (n + 15) // 16 * 16
+    if n != cols or have != rows or width != at + ((n + 31) // 32 + 15) // 16 * 16:
+        raise ValueError(f"a checkpoint of {(rows, cols)} is wanted, not of {(have, n)} in {tuple(t.shape)}")
+    p = t.data_ptr()
+    return _lib._pack_checkpoint(p, p + at, width, width)
 
 
 def restore_int8(checkpoint: Int8Checkpoint, dtype=None):
     """The values that a checkpoint stands for, in ``dtype`` (the original's unless given); exact in either."""
+    if not isinstance(checkpoint, Int8Checkpoint):
+        raise TypeError(f"an Int8Checkpoint is wanted, not {type(checkpoint).__name__}")
     dtype = dtype or checkpoint.dtype
     if dtype not in _FLOATS:
         raise TypeError(f"values come as float32 or bfloat16, not {dtype}")
     t, cols = checkpoint.data, checkpoint.cols
-    s = _checked(checkpoint, t.shape[0], cols, None)
-    with _lib._on_device(t.device):
-        out = torch.empty((t.shape[0], cols), dtype=dtype, device=t.device)
-        _lib._check(_lib.lib().asr_restore_int8(s, t.shape[0], cols, out.data_ptr(), _lib._dt(out), cols,
-                                                _lib._raw_stream(t.get_device())), "asr_restore_int8")
+    rows, d = t.shape[0], t.get_device()
+    s = _checked(checkpoint, rows, cols, d)
+    if _elsewhere(d):
+        with torch.cuda.device(d):
+            return restore_int8(checkpoint, dtype)
+    out = torch.empty((rows, cols), dtype=dtype, device=t.device)
+    _lib._check(_lib.lib().asr_restore_int8(s, rows, cols, out.data_ptr(), _lib._dt(out), cols, _raw_stream(d)),
+                "asr_restore_int8")
     return out
 
 

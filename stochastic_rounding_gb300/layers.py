@@ -19,7 +19,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from .int8 import _FLOATS, Int8Checkpoint, _by_rows, _checked, _CountedModule, empty_checkpoint
+from .int8 import (_FLOATS, Int8Checkpoint, _by_rows, _checked, _CountedModule, _elsewhere, _raw_stream,
+                   empty_checkpoint)
 
 _SAVE = (None, "input", "int8")
 
@@ -40,40 +41,46 @@ def activation(x, function="silu", *, gated=False, save=None, rounding="rne", st
     _check_save(save)
     _lib._check_rounding(rounding)
     code = _lib._function(function)
-    px, rows, width, ld = _lib._matrix_ptr(x, "x", _FLOATS)
+    px, rows, width, ld, dtype, d = _lib._rows_of(x, "x")
     if gated and width % 2:
         raise ValueError(f"a gated activation takes an even number of columns, not {width}")
+    if _elsewhere(d):
+        with torch.cuda.device(d):
+            return activation(x, function, gated=gated, save=save, rounding=rounding, step=step, seed=seed)
     cols = width // 2 if gated else width
-    with _lib._on_device(x.device):
-        y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-        kept = empty_checkpoint(rows, width, x.device, x.dtype) if save == "int8" else None
-        _lib._check(_lib.lib().asr_activation(px, ld, y.data_ptr(), cols, _lib._dt(x), rows, cols, code, 1 if gated else 0,
-                                              None if kept is None else kept._struct(rounding, 0, step, seed),
-                                              _lib._raw_stream(x.get_device())), "asr_activation")
+    y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    kept = key = None
+    if save == "int8":
+        kept = empty_checkpoint(rows, width, x.device, x.dtype)
+        key = kept._struct(rounding, 0, step, seed)
+    _lib._check(_lib.lib().asr_activation(px, ld, y.data_ptr(), cols, dtype, rows, cols, code, 1 if gated else 0, key,
+                                          _raw_stream(d)), "asr_activation")
     return y if save is None else (y, x if kept is None else kept)
 
 
 def activation_grads(dy, saved: Union[torch.Tensor, Int8Checkpoint], function="silu", *, gated=False):
     """dx from ``dy`` and what ``activation`` saved."""
     code = _lib._function(function)
-    pg, rows, cols, g_ld = _lib._matrix_ptr(dy, "dy", _FLOATS)
+    pg, rows, cols, g_ld, dtype, d = _lib._rows_of(dy, "dy")
     width = 2 * cols if gated else cols
-    px, x_ld, kept = _saved_input(saved, rows, width, dy)
-    with _lib._on_device(dy.device):
-        dx = torch.empty((rows, width), dtype=dy.dtype, device=dy.device)
-        _lib._check(_lib.lib().asr_activation_grads(pg, g_ld, px, x_ld, kept, dx.data_ptr(), width, _lib._dt(dy), rows, cols,
-                                                    code, 1 if gated else 0, _lib._raw_stream(dy.get_device())),
-                    "asr_activation_grads")
+    px, x_ld, kept = _saved_input(saved, rows, width, dtype, d)
+    if _elsewhere(d):
+        with torch.cuda.device(d):
+            return activation_grads(dy, saved, function, gated=gated)
+    dx = torch.empty((rows, width), dtype=dy.dtype, device=dy.device)
+    _lib._check(_lib.lib().asr_activation_grads(pg, g_ld, px, x_ld, kept, dx.data_ptr(), width, dtype, rows, cols, code,
+                                                1 if gated else 0, _raw_stream(d)), "asr_activation_grads")
     return dx
 
 
-def _saved_input(saved, rows, cols, dy):
+def _saved_input(saved, rows, cols, dtype, device):
     """(pointer, pitch, checkpoint) of what a forward pass saved, the pointer or the checkpoint None."""
     if isinstance(saved, Int8Checkpoint):
-        return None, cols, _checked(saved, rows, cols, dy.get_device())
-    px, xr, xc, ld = _lib._matrix_ptr(saved, "the saved input", (dy.dtype,), dy.get_device())
-    if xr != rows or xc != cols:
-        raise ValueError(f"the saved input has shape {(xr, xc)}; expected {(rows, cols)}")
+        return None, cols, _checked(saved, rows, cols, device)
+    px, xr, xc, ld, xt, xd = _lib._rows_of(saved, "the saved input")
+    if xr != rows or xc != cols or xt != dtype or xd != device:
+        raise ValueError(f"the saved input has shape {(xr, xc)} and type {saved.dtype} on cuda:{xd}; it must have {(rows, cols)}, "
+                         f"dy's type and dy's device (cuda:{device})")
     return px, ld, None
 
 
@@ -149,21 +156,21 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, centred=True, sa
     the same pass."""
     _check_save(save)
     _lib._check_rounding(rounding)
-    px, rows, cols, ld = _lib._matrix_ptr(x, "x", _FLOATS)
-    d = x.get_device()
-    p = _lib._norm_params(rows, cols, _lib._dt(x), weight, bias, float(eps), centred, d)
-    with _lib._on_device(x.device):
-        y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-        rstd = mean = kept = stats = None
-        if save is not None:
-            stats = torch.empty((2 if centred else 1, rows), dtype=torch.float32, device=x.device)
-            rstd = stats.data_ptr()
-            mean = rstd + 4 * rows if centred else None
-            if save == "int8":
-                kept = empty_checkpoint(rows, cols, x.device, x.dtype)
-        _lib._check(_lib.lib().asr_layer_norm(p, px, ld, y.data_ptr(), cols, mean, rstd,
-                                              None if kept is None else kept._struct(rounding, 0, step, seed),
-                                              _lib._raw_stream(d)), "asr_layer_norm")
+    px, rows, cols, ld, dtype, d = _lib._rows_of(x, "x")
+    p = _lib._norm_params(rows, cols, dtype, weight, bias, eps, centred, d)
+    if _elsewhere(d):
+        with torch.cuda.device(d):
+            return layer_norm(x, weight, bias, eps=eps, centred=centred, save=save, rounding=rounding, step=step, seed=seed)
+    y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    rstd = mean = kept = key = None
+    if save is not None:
+        stats = torch.empty((2 if centred else 1, rows), dtype=torch.float32, device=x.device)
+        rstd = stats.data_ptr()
+        mean = rstd + 4 * rows if centred else None
+        if save == "int8":
+            kept = empty_checkpoint(rows, cols, x.device, x.dtype)
+            key = kept._struct(rounding, 0, step, seed)
+    _lib._check(_lib.lib().asr_layer_norm(p, px, ld, y.data_ptr(), cols, mean, rstd, key, _raw_stream(d)), "asr_layer_norm")
     return y if save is None else (y, NormSaved(x if kept is None else kept, stats))
 
 
@@ -172,26 +179,38 @@ def layer_norm_grads(dy, saved: NormSaved, weight=None, *, need_dx=True, need_dw
     """(dx, dweight, dbias) from ``dy`` and what ``layer_norm`` saved, each None where it
     is not needed; dx of dy's dtype, dweight of the weight's (dy's, if the norm has none),
     dbias of ``dbias_dtype`` (dweight's unless given)."""
-    pg, rows, cols, g_ld = _lib._matrix_ptr(dy, "dy", _FLOATS)
-    d, device = dy.get_device(), dy.device
-    px, x_ld, kept = _saved_input(saved.input, rows, cols, dy)
-    centred = saved.stats.shape[0] == 2
-    rstd = _lib._dev_ptr(saved.stats, "stats", (torch.float32,), (2 if centred else 1) * rows, d)
-    p = _lib._norm_params(rows, cols, _lib._dt(dy), weight, None, 0.0, centred, d)
+    pg, rows, cols, g_ld, code, d = _lib._rows_of(dy, "dy")
+    px, x_ld, kept = _saved_input(saved.input, rows, cols, code, d)
+    stats = saved.stats
+    centred = stats.shape[0] == 2
+    rstd = _lib._dev_ptr(stats, "stats", (torch.float32,), (2 if centred else 1) * rows, d)
+    p = _lib._norm_params(rows, cols, code, weight, None, 0.0, centred, d)
     dtype = dy.dtype if weight is None else weight.dtype
     if dbias_dtype is not None and dbias_dtype not in _FLOATS:
         raise TypeError(f"a gradient comes as float32 or bfloat16, not {dbias_dtype}")
-    with _lib._on_device(device):
-        dx = torch.empty((rows, cols), dtype=dy.dtype, device=device) if need_dx else None
-        dweight = torch.empty(cols, dtype=dtype, device=device) if need_dweight else None
-        dbias = torch.empty(cols, dtype=dbias_dtype or dtype, device=device) if need_dbias else None
-        need = _lib.asr_layer_norm_grads_workspace(rows, cols) if need_dweight or need_dbias else 0
-        buf = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-        _lib._check(_lib.lib().asr_layer_norm_grads(
-            p, pg, g_ld, px, x_ld, kept, rstd + 4 * rows if centred else None, rstd, None if dx is None else dx.data_ptr(), cols,
-            None if dweight is None else dweight.data_ptr(), 0 if dweight is None else _lib._dt(dweight),
-            None if dbias is None else dbias.data_ptr(), 0 if dbias is None else _lib._dt(dbias),
-            None if buf is None else buf.data_ptr(), need, _lib._raw_stream(d)), "asr_layer_norm_grads")
+    if _elsewhere(d):
+        with torch.cuda.device(d):
+            return layer_norm_grads(dy, saved, weight, need_dx=need_dx, need_dweight=need_dweight, need_dbias=need_dbias,
+                                    dbias_dtype=dbias_dtype)
+    device = dy.device
+    dx = dweight = dbias = buf = None
+    to_x = to_w = to_b = to_ws = None
+    w_type = b_type = need = 0
+    if need_dx:
+        dx = torch.empty((rows, cols), dtype=dy.dtype, device=device)
+        to_x = dx.data_ptr()
+    if need_dweight:
+        dweight = torch.empty(cols, dtype=dtype, device=device)
+        to_w, w_type = dweight.data_ptr(), _lib._dt(dweight)
+    if need_dbias:
+        dbias = torch.empty(cols, dtype=dbias_dtype or dtype, device=device)
+        to_b, b_type = dbias.data_ptr(), _lib._dt(dbias)
+    if need_dweight or need_dbias:
+        need = _lib.asr_layer_norm_grads_workspace(rows, cols)
+        buf = torch.empty(need, dtype=torch.uint8, device=device)
+        to_ws = buf.data_ptr()
+    _lib._check(_lib.lib().asr_layer_norm_grads(p, pg, g_ld, px, x_ld, kept, rstd + 4 * rows if centred else None, rstd, to_x, cols,
+                                                to_w, w_type, to_b, b_type, to_ws, need, _raw_stream(d)), "asr_layer_norm_grads")
     return dx, dweight, dbias
 
 
@@ -256,21 +275,21 @@ class LayerNorm(_CountedModule):
 def embedding(ids, table, *, scale: float = 1.0):
     """``scale * table[ids]`` for ``ids`` (1-D, int64 or int32): (tokens, dim).  An id
     outside the table gives a row of NaN."""
-    pt, vocab, dim, ld = _lib._matrix_ptr(table, "table", _FLOATS)
-    d = table.get_device()
+    pt, vocab, dim, ld, dtype, d = _lib._rows_of(table, "table")
     pi, index, tokens = _lib._ids(ids, d)
-    with _lib._on_device(table.device):
-        y = torch.empty((tokens, dim), dtype=table.dtype, device=table.device)
-        _lib._check(_lib.lib().asr_embedding(pi, index, tokens, pt, ld, vocab, dim, scale, y.data_ptr(), dim, _lib._dt(y),
-                                             _lib._raw_stream(d)), "asr_embedding")
+    if _elsewhere(d):
+        with torch.cuda.device(d):
+            return embedding(ids, table, scale=scale)
+    y = torch.empty((tokens, dim), dtype=table.dtype, device=table.device)
+    _lib._check(_lib.lib().asr_embedding(pi, index, tokens, pt, ld, vocab, dim, scale, y.data_ptr(), dim, dtype, _raw_stream(d)),
+                "asr_embedding")
     return y
 
 
 def embedding_grads(ids, dy, vocab: int, *, scale: float = 1.0, padding_idx: Optional[int] = None, dtype=None):
     """The whole table's gradient, (vocab, dim) in ``dtype`` (dy's unless given): for each
     row, scale times the sum of ``dy`` over its tokens, in their order."""
-    pg, rows, dim, ld = _lib._matrix_ptr(dy, "dy", _FLOATS)
-    d, device = dy.get_device(), dy.device
+    pg, rows, dim, ld, code, d = _lib._rows_of(dy, "dy")
     pi, index, tokens = _lib._ids(ids, d)
     if rows != tokens:
         raise ValueError(f"dy has {rows} rows; expected {tokens}")
@@ -278,14 +297,16 @@ def embedding_grads(ids, dy, vocab: int, *, scale: float = 1.0, padding_idx: Opt
         raise ValueError(f"padding_idx must be a row of the table (0 to {vocab - 1}), not {padding_idx}")
     if dtype is not None and dtype not in _FLOATS:
         raise TypeError(f"a gradient comes as float32 or bfloat16, not {dtype}")
+    if _elsewhere(d):
+        with torch.cuda.device(d):
+            return embedding_grads(ids, dy, vocab, scale=scale, padding_idx=padding_idx, dtype=dtype)
     need = _lib.asr_embedding_grads_workspace(tokens, dim)
-    with _lib._on_device(device):
-        out = torch.empty((vocab, dim), dtype=dtype or dy.dtype, device=device)
-        buf = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-        _lib._check(_lib.lib().asr_embedding_grads(pi, index, tokens, pg, ld, _lib._dt(dy), vocab, dim, scale,
-                                                   -1 if padding_idx is None else padding_idx, out.data_ptr(), _lib._dt(out),
-                                                   None if buf is None else buf.data_ptr(), need, _lib._raw_stream(d)),
-                    "asr_embedding_grads")
+    out = torch.empty((vocab, dim), dtype=dtype or dy.dtype, device=dy.device)
+    buf = torch.empty(need, dtype=torch.uint8, device=dy.device) if need else None
+    _lib._check(_lib.lib().asr_embedding_grads(pi, index, tokens, pg, ld, code, vocab, dim, scale,
+                                               -1 if padding_idx is None else padding_idx, out.data_ptr(), _lib._dt(out),
+                                               None if buf is None else buf.data_ptr(), need, _raw_stream(d)),
+                "asr_embedding_grads")
     return out
 
 

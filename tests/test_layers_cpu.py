@@ -145,7 +145,9 @@ def fake(monkeypatch):
     monkeypatch.setattr(_lib, "_lib", lib)
     monkeypatch.setattr(_lib, "_on_device", lambda d: contextlib.nullcontext())
     monkeypatch.setattr(_lib, "_stream_handle", lambda d, s: ctypes.c_void_p(None))
-    monkeypatch.setattr(_lib, "_raw_stream", lambda i: 0)
+    for module in (int8, layers):
+        monkeypatch.setattr(module, "_raw_stream", lambda i: 0)
+        monkeypatch.setattr(module, "_elsewhere", lambda d: False)
     yield lib
     _lib.asr_layer_norm_grads_workspace.cache_clear()
     _lib.asr_embedding_grads_workspace.cache_clear()
