@@ -98,7 +98,8 @@ template <int DT, bool GATED, int KEEP, bool FULL>
 __global__ void __launch_bounds__(kThreads, DT == ASR_BF16 ? 4 : 3) forward_kernel(const __grid_constant__ Params P, uint32_t spans)
 {
     using At = Place<GATED, FULL>;
-    const bool gelu = P.gelu, vec1 = P.x.vec && (!GATED || P.cols % 8 == 0);
+    const bool gelu = P.gelu;
+    const uint32_t vec1 = !GATED || P.cols % 8 == 0 ? P.x.vec : 0;
     kept::Raw<DT> next[2];
     auto load = [&](const kept::Walk &k) {
         if (!k.more()) return;
@@ -141,7 +142,8 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
 {
     using At = Place<GATED, FULL>;
     constexpr int kGrads = GATED ? 1 : 2;
-    const bool gelu = P.gelu, vec1 = P.x.vec && (!GATED || P.cols % 8 == 0);
+    const bool gelu = P.gelu;
+    const uint32_t vec1 = !GATED || P.cols % 8 == 0 ? P.x.vec : 0;
     kept::Raw<DT> raw[2], grad[kGrads];
     Codes codes[2];
     auto load = [&](const kept::Walk &k) {
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
                 g[u][i] = __fmul_rn(g[u][i], df);
             }
             kept::store8<DT, FULL>(P.dx, now.row, now.of(u), now.live[u], P.dx.vec, g[u]);
-            if (GATED) kept::store8<DT, FULL>(P.dx, now.row, now.of(1), now.live[1], P.dx.vec && P.cols % 8 == 0, db);
+            if (GATED) kept::store8<DT, FULL>(P.dx, now.row, now.of(1), now.live[1], P.cols % 8 == 0 ? P.dx.vec : 0, db);
         }
     }
 }

@@ -326,7 +326,7 @@ __device__ __forceinline__ void bring(uint4 *to, uint32_t step, const kept::Matr
             else *w = 0;
         }
     } else {
-        const kept::Raw<DT> r = kept::fetch<DT>(M, row, col, live, false);
+        const kept::Raw<DT> r = kept::fetch<DT>(M, row, col, live, 0);
         to[0] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
     }
 }
