@@ -74,64 +74,55 @@ __device__ __forceinline__ void value_and_slope(float a, bool gelu, float &f, fl
     df = __fmaf_rn(__fmul_rn(s, minus), r, s);
 }
 
-// The units of a lane and span: of x's two halves at one column, gated, or at two
-// columns 256 apart.
-template <bool GATED, bool FULL>
-struct Place {
-    uint32_t row, col;                          // of the first unit
-    uint32_t apart;                             // columns of x between the two
-    int live[2];
-    __device__ Place(const kept::Walk &k, uint32_t cols)
-    {
-        row = k.row;
-        col = k.span * (GATED ? 256u : 512u) + (threadIdx.x & 31) * 8;
-        apart = GATED ? cols : 256;
-        live[0] = FULL ? 8 : live_of(cols, col);
-        live[1] = FULL ? 8 : GATED ? live[0] : live_of(cols, col + 256);
-    }
-    __device__ uint32_t of(int u) const { return u ? col + apart : col; }
-};
-
-// KEEP: 0 nothing, 1 to nearest, 2 stochastically.  The next span's values are
-// fetched before the current one's are worked on.
-template <int DT, bool GATED, int KEEP, bool FULL>
-__global__ void __launch_bounds__(kThreads, DT == ASR_BF16 ? 4 : 3) forward_kernel(const __grid_constant__ Params P, uint32_t spans)
+// How the gating half's rows begin, `cols` values behind the others.
+__device__ __forceinline__ uint32_t half_vec(uint32_t vec, uint32_t cols)
 {
-    using At = Place<GATED, FULL>;
+    return cols % 16 == 0 ? vec : cols % 8 == 0 && vec ? 1 : 0;
+}
+
+// KEEP: 0 nothing, 1 to nearest, 2 stochastically.  A span is 512 columns of y; the
+// next one's values are fetched before the current one's are worked on.
+template <int DT, bool GATED, int KEEP, bool FULL>
+__global__ void __launch_bounds__(kThreads, DT == ASR_F32 ? 2 : GATED && KEEP == 2 ? 3 : 4) forward_kernel(const __grid_constant__ Params P, uint32_t spans)
+{
+    constexpr int kHalves = GATED ? 2 : 1;      // of x
     const bool gelu = P.gelu;
-    const uint32_t vec1 = !GATED || P.cols % 8 == 0 ? P.x.vec : 0;
-    kept::Raw<DT> next[2];
+    const uint32_t vec1 = half_vec(P.x.vec, P.cols), lane = (threadIdx.x & 31) * 16;
+    kept::Pair<DT> next[kHalves];
     auto load = [&](const kept::Walk &k) {
+        const uint32_t col = k.span * kept::kSpan + lane;
+        const int live = FULL ? 16 : live_of(P.cols, col, 16);
         if (!k.more()) return;
-        const At at(k, P.cols);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) next[u] = kept::fetch<DT, FULL>(P.x, at.row, at.of(u), at.live[u], u ? vec1 : P.x.vec);
+        next[0] = kept::fetch16<DT, FULL>(P.x, k.row, col, live, P.x.vec);
+        if (GATED) next[kHalves - 1] = kept::fetch16<DT, FULL>(P.x, k.row, P.cols + col, live, vec1);
     };
     kept::Walk k(P.rows, spans);
     load(k);
     while (k.more()) {
-        kept::Raw<DT> raw[2];
+        kept::Pair<DT> raw[kHalves];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) raw[u] = next[u];
-        const At now(k, P.cols);
+        for (int u = 0; u < kHalves; ++u) raw[u] = next[u];
+        const uint32_t row = k.row, col = k.span * kept::kSpan + lane;
+        const int live = FULL ? 16 : live_of(P.cols, col, 16);
         k.next();
         load(k);
         if (KEEP) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) kept::keep8<KEEP == 2, DT, FULL>(P.to, now.row, now.of(u), now.live[u], raw[u]);
+            for (int u = 0; u < kHalves; ++u) kept::keep16<KEEP == 2, DT, FULL>(P.to, row, u * P.cols + col, live, raw[u]);
         }
+        float y[2][8];
 #pragma unroll
-        for (int u = 0; u < (GATED ? 1 : 2); ++u) {
-            float y[8], b[8];
-            kept::values(raw[u], y);
-            if (GATED) kept::values(raw[1], b);
+        for (int h = 0; h < 2; ++h) {
+            float b[8];
+            kept::values(raw[0].h[h], y[h]);
+            if (GATED) kept::values(raw[kHalves - 1].h[h], b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                y[i] = value<DT>(y[i], gelu);
-                if (GATED) y[i] = __fmul_rn(y[i], b[i]);
+                y[h][i] = value<DT>(y[h][i], gelu);
+                if (GATED) y[h][i] = __fmul_rn(y[h][i], b[i]);
             }
-            kept::store8<DT, FULL>(P.y, now.row, now.of(u), now.live[u], P.y.vec, y);
         }
+        kept::store16<DT, FULL>(P.y, row, col, live, P.y.vec, y);
     }
 }
 
@@ -140,52 +131,60 @@ __global__ void __launch_bounds__(kThreads, DT == ASR_BF16 ? 4 : 3) forward_kern
 template <int DT, bool GATED, int KEPT, bool FULL>
 __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constant__ Params P, uint32_t spans)
 {
-    using At = Place<GATED, FULL>;
-    constexpr int kGrads = GATED ? 1 : 2;
+    constexpr int kHalves = GATED ? 2 : 1;
     const bool gelu = P.gelu;
-    const uint32_t vec1 = !GATED || P.cols % 8 == 0 ? P.x.vec : 0;
-    kept::Raw<DT> raw[2], grad[kGrads];
-    Codes codes[2];
+    const uint32_t in1 = half_vec(P.x.vec, P.cols), out1 = half_vec(P.dx.vec, P.cols), lane = (threadIdx.x & 31) * 16;
+    kept::Pair<DT> raw[kHalves], grad;
+    kept::Codes16 codes[kHalves];
     auto load = [&](const kept::Walk &k) {
         if (!k.more()) return;
-        const At at(k, P.cols);
+        const uint32_t col = k.span * kept::kSpan + lane;
+        const int live = FULL ? 16 : live_of(P.cols, col, 16);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            if (!KEPT) raw[u] = kept::fetch<DT, FULL>(P.x, at.row, at.of(u), at.live[u], u ? vec1 : P.x.vec);
-            else if (KEPT == 1 || u == 0) codes[u] = kept::fetch_codes<FULL>(P.from, at.row, at.of(u), at.live[u]);
-            if (u < kGrads) grad[u] = kept::fetch<DT, FULL>(P.dy, at.row, at.of(u), at.live[u], P.dy.vec);
+        for (int u = 0; u < kHalves; ++u) {
+            if (!KEPT) raw[u] = kept::fetch16<DT, FULL>(P.x, k.row, u * P.cols + col, live, u ? in1 : P.x.vec);
+            else if (KEPT == 1 || u == 0) codes[u] = kept::fetch_codes16<FULL>(P.from, k.row, u * P.cols + col, live);
         }
+        grad = kept::fetch16<DT, FULL>(P.dy, k.row, col, live, P.dy.vec);
     };
     kept::Walk k(P.rows, spans);
     load(k);
     while (k.more()) {
-        float x[2][8], g[kGrads][8];
-        const At now(k, P.cols);
+        const uint32_t row = k.row, col = k.span * kept::kSpan + lane;
+        const int live = FULL ? 16 : live_of(P.cols, col, 16);
+        kept::Pair<DT> x0[kHalves], g0 = grad;
+        kept::Codes16 c0[kHalves];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            if (!KEPT) kept::values(raw[u], x[u]);
-            else if (KEPT == 1 || u == 0) kept::values(codes[u], x[u]);
-            else kept::values_across(P.from, now.row, now.of(u), now.live[u], x[u]);
-            if (u < kGrads) kept::values(grad[u], g[u]);
+        for (int u = 0; u < kHalves; ++u) {
+            if (!KEPT) x0[u] = raw[u];
+            else c0[u] = codes[u];
         }
         k.next();
         load(k);
+        float da[2][8], db[2][8];
 #pragma unroll
-        for (int u = 0; u < kGrads; ++u) {
-            float db[8];
+        for (int h = 0; h < 2; ++h) {
+            float x[2][8];
+            kept::values(g0.h[h], da[h]);
+#pragma unroll
+            for (int u = 0; u < kHalves; ++u) {
+                if (!KEPT) kept::values(x0[u].h[h], x[u]);
+                else if (KEPT == 1 || u == 0) kept::values(Codes{c0[u].h[h], c0[u].b}, x[u]);
+                else kept::values_across(P.from, row, P.cols + col + 8 * h, kept::half_of(live, h), x[u]);
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float f, df;
-                value_and_slope<DT>(x[u][i], gelu, f, df);
+                value_and_slope<DT>(x[0][i], gelu, f, df);
                 if (GATED) {
-                    db[i] = __fmul_rn(g[u][i], f);
+                    db[h][i] = __fmul_rn(da[h][i], f);
                     df = __fmul_rn(df, x[1][i]);
                 }
-                g[u][i] = __fmul_rn(g[u][i], df);
+                da[h][i] = __fmul_rn(da[h][i], df);
             }
-            kept::store8<DT, FULL>(P.dx, now.row, now.of(u), now.live[u], P.dx.vec, g[u]);
-            if (GATED) kept::store8<DT, FULL>(P.dx, now.row, now.of(1), now.live[1], P.cols % 8 == 0 ? P.dx.vec : 0, db);
         }
+        kept::store16<DT, FULL>(P.dx, row, col, live, P.dx.vec, da);
+        if (GATED) kept::store16<DT, FULL>(P.dx, row, P.cols + col, live, out1, db);
     }
 }
 
@@ -245,13 +244,6 @@ asr_status kind_ok(int32_t dtype, uint32_t function)
     return kept::dtype_ok(dtype) && (function == ASR_SILU || function == ASR_GELU) ? ASR_OK : ASR_ERR_UNSUPPORTED_DTYPE;
 }
 
-uint32_t span_of(uint32_t gated) { return gated ? 256 : 512; }
-
-asr_status launch(Kernel kernel, const Params &P, uint32_t gated, cudaStream_t stream)
-{
-    return kept::walk(ASR_KERNEL_ACTIVATION, kernel, P, P.rows, P.cols, span_of(gated), stream);
-}
-
 asr_status forward(const void *x, uint64_t x_ld, void *y, uint64_t y_ld, int32_t dtype, uint64_t rows, uint64_t cols,
                    uint32_t function, uint32_t gated, const asr_checkpoint *to, cudaStream_t stream)
 {
@@ -268,8 +260,8 @@ asr_status forward(const void *x, uint64_t x_ld, void *y, uint64_t y_ld, int32_t
     if (st != ASR_OK) return st;
     Params P;
     std::memset(&P, 0, sizeof(P));
-    P.x = kept::matrix(x, x_ld);
-    P.y = kept::out(y, y_ld);
+    P.x = kept::matrix(x, x_ld, dtype);
+    P.y = kept::out(y, y_ld, dtype);
     P.rows = static_cast<uint32_t>(rows);
     P.cols = static_cast<uint32_t>(cols);
     P.gelu = function == ASR_GELU;
@@ -280,8 +272,8 @@ asr_status forward(const void *x, uint64_t x_ld, void *y, uint64_t y_ld, int32_t
         P.to = kept::store(*to, width);
         keep = to->rounding == ASR_ROUND_SR ? 2 : 1;
     }
-    const bool full = cols % span_of(gated) == 0 && P.x.vec && P.y.vec && (!keep || P.to.vec);
-    st = launch(forward_of(dtype, gated != 0, keep, full), P, gated, stream);
+    const bool full = cols % kept::kSpan == 0 && P.x.vec == 2 && P.y.vec == 2 && (!keep || P.to.vec == 2);
+    st = kept::walk(ASR_KERNEL_ACTIVATION, forward_of(dtype, gated != 0, keep, full), P, rows, cols, kept::kSpan, stream);
     if (st == ASR_OK && apart) st = kept::pack(x, dtype, rows, width, x_ld, to, stream);
     return st;
 }
@@ -302,16 +294,16 @@ asr_status backward(const void *dy, uint64_t dy_ld, const void *x, uint64_t x_ld
     if (st != ASR_OK) return st;
     Params P;
     std::memset(&P, 0, sizeof(P));
-    P.dy = kept::matrix(dy, dy_ld);
-    P.dx = kept::out(dx, dx_ld);
+    P.dy = kept::matrix(dy, dy_ld, dtype);
+    P.dx = kept::out(dx, dx_ld, dtype);
     if (from) P.from = kept::source(*from);
-    else P.x = kept::matrix(x, x_ld);
+    else P.x = kept::matrix(x, x_ld, dtype);
     P.rows = static_cast<uint32_t>(rows);
     P.cols = static_cast<uint32_t>(cols);
     P.gelu = function == ASR_GELU;
     const int codes = !from ? 0 : gated && cols % kept::kGroup != 0 ? 2 : 1;
-    const bool full = cols % span_of(gated) == 0 && P.dy.vec && P.dx.vec && (from ? P.from.vec : P.x.vec);
-    return launch(backward_of(dtype, gated != 0, codes, full), P, gated, stream);
+    const bool full = cols % kept::kSpan == 0 && P.dy.vec == 2 && P.dx.vec == 2 && (from ? P.from.vec : P.x.vec) == 2;
+    return kept::walk(ASR_KERNEL_ACTIVATION, backward_of(dtype, gated != 0, codes, full), P, rows, cols, kept::kSpan, stream);
 }
 
 }  // namespace act

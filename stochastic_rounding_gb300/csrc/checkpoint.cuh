@@ -30,7 +30,7 @@ struct Store {                                  // where it goes
     uint32_t q_ld, power_ld;
     uint64_t base;                              // first counter
     uint32_t across;                            // counters a row
-    uint32_t vec;                               // eight codes are 8-byte aligned
+    uint32_t vec;                               // codes of 16 values (2) or 8 (1) are aligned to their size
     uint32_t step;
     RoundKeys keys;
 };
@@ -47,16 +47,16 @@ struct Source {
 // element by element accesses.  Only for bf16, whose kernels are bound by their
 // instructions (8,192 x 14,336: pack 67 -> 59 us, unpack 68 -> 57 us, the gated
 // activation's backward pass from codes 197 -> 168 us); f32's are bound by bytes.
-__device__ __forceinline__ int live_of(uint32_t cols, uint32_t col)
+__device__ __forceinline__ int live_of(uint32_t cols, uint32_t col, uint32_t most = 8)
 {
-    return col >= cols ? 0 : cols - col < 8 ? static_cast<int>(cols - col) : 8;
+    return col >= cols ? 0 : static_cast<int>(cols - col < most ? cols - col : most);
 }
 
 // A matrix of f32 or bf16 values, rows `ld` apart.
 struct Matrix {
     const void *p;
     uint32_t ld;
-    uint32_t vec;                               // units of eight are 16-byte aligned (1), 32-byte (2), or not (0)
+    uint32_t vec;                               // rows begin on 16 bytes (1), 32 bytes (2), or not (0)
 };
 
 struct Out {
@@ -128,10 +128,33 @@ __device__ __forceinline__ void values(const Raw<DT> &r, float x[8])
                              : (i & 1) ? bf16_hi(r.w[DT == ASR_F32 ? 0 : i >> 1]) : bf16_lo(r.w[DT == ASR_F32 ? 0 : i >> 1]);
 }
 
+// Sixteen values of a lane: two units side by side.
+template <int DT>
+struct Pair {
+    Raw<DT> h[2];
+};
+
+__device__ __forceinline__ int half_of(int live, int h) { return live - 8 * h < 0 ? 0 : live - 8 * h < 8 ? live - 8 * h : 8; }
+
+template <int DT, bool FULL>
+__device__ __forceinline__ Pair<DT> fetch16(const Matrix &M, uint32_t row, uint32_t col, int live, uint32_t vec)
+{
+    Pair<DT> p;
+    if (DT == ASR_BF16 && (FULL || (vec == 2 && live == 16))) {
+        uint32_t w[8];
+        load32(static_cast<const char *>(M.p) + place(row, M.ld, col) * 2, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p.h[i >> 2].w[i & 3] = w[i];
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) p.h[h] = fetch<DT>(M, row, col + 8 * h, half_of(live, h), vec);
+    }
+    return p;
+}
+
 // A warp's way through a matrix in spans of kSpan columns: span `at` counted along
 // the rows, then every `stride`-th.  Both are counts of a launch's warps.
-constexpr int kUnits = 2;                       // of eight values, a lane and span
-constexpr uint32_t kSpan = 256 * kUnits;
+constexpr uint32_t kSpan = 512;                 // sixteen values a lane
 
 struct Walk {
     uint32_t row, rows, span, spans, drow, dspan;
@@ -173,21 +196,33 @@ __device__ __forceinline__ uint32_t most2(uint32_t a, uint32_t b)
     return d;
 }
 
-// The bits of a group's largest magnitude, from the unit of each of its four lanes.
-template <int DT>
-__device__ __forceinline__ uint32_t group_most(const Raw<DT> &r)
+// The bits of a group's largest magnitude, from COUNT units of each of its 4 / COUNT
+// lanes.
+template <int DT, int COUNT>
+__device__ __forceinline__ uint32_t group_most(const Raw<DT> *r)
 {
     if (DT == ASR_BF16) {
-        uint32_t m = most2(most2(r.w[0], r.w[1]), most2(r.w[2], r.w[3]));
-        m = most2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        m = most2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2)) & 0x7FFF7FFFu;
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < COUNT; ++k) {
+            const uint32_t u = most2(most2(r[k].w[0], r[k].w[1]), most2(r[k].w[2], r[k].w[3]));
+            m = k ? most2(m, u) : u;
+        }
+#pragma unroll
+        for (int d = 1; d < 4 / COUNT; d *= 2) m = most2(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        m &= 0x7FFF7FFFu;
         return max(m << 16, m & 0xFFFF0000u);               // as numbers: a NaN's bits are the largest
     }
-    float x[8];
-    values(r, x);
-    float m = most(most(most(x[0], x[1]), most(x[2], x[3])), most(most(x[4], x[5]), most(x[6], x[7])));
-    m = most(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    return __float_as_uint(most(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2)));
+    float m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < COUNT; ++k) {
+        float x[8];
+        values(r[k], x);
+        m = most(m, most(most(most(x[0], x[1]), most(x[2], x[3])), most(most(x[4], x[5]), most(x[6], x[7]))));
+    }
+#pragma unroll
+    for (int d = 1; d < 4 / COUNT; d *= 2) m = most(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    return __float_as_uint(m);
 }
 
 // e + 127 for the bits of a largest value, 127 being 1.984375 * 2^6.
@@ -202,26 +237,21 @@ __device__ __forceinline__ float scale_of(uint32_t b)
     return __uint_as_float(b == 255u ? 0x7FC00000u : b ? b << 23 : 0x00400000u);
 }
 
-// Eight values of a row from `col` on, a multiple of 8, of which `live` are the
-// row's.  All lanes of a warp call this together; four in a row hold a group.
+// Codes of a unit, the first value's in the lowest byte.  `up` is 2^-e; `at` the unit's
+// counter.
 //
 // To nearest: x 2^-e + 1.5 * 2^23, rounded once, has q in its low byte.
 // Stochastically: q = ceil(y - r / 65536), which is floor(y), or one more where the
 // fraction is above r / 65536.  128 + r / 65536 is a binary32 number with r for its
 // low bits; taken from y and rounded up, the difference keeps its ceiling, -128 away
 // (whole numbers are representable), and 1.5 * 2^23 + 128 more, rounded up, is it.
-template <bool SR, int DT, bool FULL>
-__device__ __forceinline__ void keep8(const Store &S, uint32_t row, uint32_t col, int live, const Raw<DT> &raw)
+template <bool SR, int DT>
+__device__ __forceinline__ uint2 codes8(const Store &S, uint64_t at, float up, const Raw<DT> &raw)
 {
-    const uint32_t b = power_of(group_most(raw));
-    const float up = __uint_as_float((254u - b) << 23);
     float x[8];
     values(raw, x);
     uint32_t c[8], w[4];
-    if (SR) {
-        const uint64_t at = S.base + place(row, S.across, col >> 3);
-        philox4x32_10(static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32), S.step, kStream, S.keys, w);
-    }
+    if (SR) philox4x32_10(static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32), S.step, kStream, S.keys, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         if (SR) {
@@ -231,10 +261,13 @@ __device__ __forceinline__ void keep8(const Store &S, uint32_t row, uint32_t col
             c[i] = __float_as_uint(__fmaf_rn(x[i], up, 12582912.0f));
         }
     }
-    uint2 v = make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
-                         __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
-    if (b == 255u) v = make_uint2(0, 0);
-    int8_t *q = S.q + place(row, S.q_ld, col);
+    return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
+                      __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
+}
+
+template <bool FULL>
+__device__ __forceinline__ void store_codes(const Store &S, int8_t *q, int live, uint2 v)
+{
     if (FULL || (live == 8 && S.vec)) {
         *reinterpret_cast<uint2 *>(q) = v;
     } else {
@@ -242,7 +275,37 @@ __device__ __forceinline__ void keep8(const Store &S, uint32_t row, uint32_t col
         for (int i = 0; i < 8; ++i)
             if (i < live) q[i] = static_cast<int8_t>((i < 4 ? v.x : v.y) >> (8 * (i & 3)));
     }
+}
+
+// Keeps a unit of a row, from `col` on, a multiple of 8, of which `live` values are the
+// row's.  All lanes of a warp call this together; four in a row hold a group.
+template <bool SR, int DT, bool FULL>
+__device__ __forceinline__ void keep8(const Store &S, uint32_t row, uint32_t col, int live, const Raw<DT> &raw)
+{
+    const uint32_t b = power_of(group_most<DT, 1>(&raw));
+    uint2 v = codes8<SR>(S, S.base + place(row, S.across, col >> 3), __uint_as_float((254u - b) << 23), raw);
+    if (b == 255u) v = make_uint2(0, 0);
+    store_codes<FULL>(S, S.q + place(row, S.q_ld, col), live, v);
     if ((FULL || live > 0) && (threadIdx.x & 3) == 0) S.power[place(row, S.power_ld, col >> 5)] = static_cast<uint8_t>(b);
+}
+
+// The same of two units side by side; two lanes hold a group.
+template <bool SR, int DT, bool FULL>
+__device__ __forceinline__ void keep16(const Store &S, uint32_t row, uint32_t col, int live, const Pair<DT> &raw)
+{
+    const uint32_t b = power_of(group_most<DT, 2>(raw.h));
+    const float up = __uint_as_float((254u - b) << 23);
+    const uint64_t at = S.base + place(row, S.across, col >> 3);        // even
+    uint2 v = codes8<SR>(S, at, up, raw.h[0]), z = codes8<SR>(S, at | 1, up, raw.h[1]);
+    if (b == 255u) v = z = make_uint2(0, 0);
+    int8_t *q = S.q + place(row, S.q_ld, col);
+    if (FULL || (live == 16 && S.vec == 2)) {
+        *reinterpret_cast<uint4 *>(q) = make_uint4(v.x, v.y, z.x, z.y);
+    } else {
+        store_codes<false>(S, q, half_of(live, 0), v);
+        store_codes<false>(S, q + 8, half_of(live, 1), z);
+    }
+    if ((FULL || live > 0) && (threadIdx.x & 1) == 0) S.power[place(row, S.power_ld, col >> 5)] = static_cast<uint8_t>(b);
 }
 
 // Codes and power of eight values, to be fetched ahead of their use.
@@ -265,6 +328,26 @@ __device__ __forceinline__ Codes fetch_codes(const Source &S, uint32_t row, uint
             if (i < live) (i < 4 ? c.v.x : c.v.y) |= static_cast<uint32_t>(static_cast<uint8_t>(q[i])) << (8 * (i & 3));
     }
     c.b = S.power[place(row, S.power_ld, col >> 5)];
+    return c;
+}
+
+struct Codes16 {
+    uint2 h[2];
+    uint32_t b;
+};
+
+template <bool FULL>
+__device__ __forceinline__ Codes16 fetch_codes16(const Source &S, uint32_t row, uint32_t col, int live)
+{
+    Codes16 c;
+    if (FULL || (live == 16 && S.vec == 2)) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(S.q + place(row, S.q_ld, col));
+        c.h[0] = make_uint2(v.x, v.y), c.h[1] = make_uint2(v.z, v.w);
+        c.b = S.power[place(row, S.power_ld, col >> 5)];
+        return c;
+    }
+    const Codes a = fetch_codes(S, row, col, half_of(live, 0)), b = fetch_codes(S, row, col + 8, half_of(live, 1));
+    c.h[0] = a.v, c.h[1] = b.v, c.b = a.b;
     return c;
 }
 
@@ -330,6 +413,24 @@ __device__ __forceinline__ void store8(const Out &O, uint32_t row, uint32_t col,
     }
 }
 
+// Sixteen out.
+template <int DT, bool FULL>
+__device__ __forceinline__ void store16(const Out &O, uint32_t row, uint32_t col, int live, uint32_t vec, const float v[2][8])
+{
+    if (DT == ASR_BF16 && (FULL || (vec == 2 && live == 16))) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[i >> 2][2 * (i & 3)], v[i >> 2][2 * (i & 3) + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        gemm::st_global_v8(static_cast<char *>(O.p) + place(row, O.ld, col) * 2, w);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) store8<DT>(O, row, col + 8 * h, half_of(live, h), vec, v[h]);
+    }
+}
+
 struct PackParams {
     Matrix x;
     uint32_t rows, cols;
@@ -340,28 +441,20 @@ struct PackParams {
 template <bool SR, int DT, bool FULL>
 __global__ void __launch_bounds__(kThreads) pack_kernel(const __grid_constant__ PackParams P, uint32_t spans)
 {
-    const uint32_t at = (threadIdx.x & 31) * 8;
-    Raw<DT> next[kUnits];
+    const uint32_t at = (threadIdx.x & 31) * 16;
+    Pair<DT> next;
     auto load = [&](const Walk &k) {
-        if (!k.more()) return;
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-            const uint32_t col = k.span * kSpan + u * 256 + at;
-            next[u] = fetch<DT, FULL>(P.x, k.row, col, FULL ? 8 : live_of(P.cols, col), P.x.vec);
-        }
+        const uint32_t col = k.span * kSpan + at;
+        if (k.more()) next = fetch16<DT, FULL>(P.x, k.row, col, FULL ? 16 : live_of(P.cols, col, 16), P.x.vec);
     };
     Walk k(P.rows, spans);
     load(k);
     while (k.more()) {
-        Raw<DT> x[kUnits];
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u) x[u] = next[u];
-        const uint32_t row = k.row, first = k.span * kSpan + at;
+        const Pair<DT> x = next;
+        const uint32_t row = k.row, col = k.span * kSpan + at;
         k.next();
         load(k);
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u)
-            keep8<SR, DT, FULL>(P.to, row, first + u * 256, FULL ? 8 : live_of(P.cols, first + u * 256), x[u]);
+        keep16<SR, DT, FULL>(P.to, row, col, FULL ? 16 : live_of(P.cols, col, 16), x);
     }
 }
 
@@ -374,31 +467,23 @@ struct UnpackParams {
 template <int DT, bool FULL>
 __global__ void __launch_bounds__(kThreads) unpack_kernel(const __grid_constant__ UnpackParams P, uint32_t spans)
 {
-    const uint32_t at = (threadIdx.x & 31) * 8;
-    Codes next[kUnits];
+    const uint32_t at = (threadIdx.x & 31) * 16;
+    Codes16 next;
     auto load = [&](const Walk &k) {
-        if (!k.more()) return;
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-            const uint32_t col = k.span * kSpan + u * 256 + at;
-            next[u] = fetch_codes<FULL>(P.from, k.row, col, FULL ? 8 : live_of(P.cols, col));
-        }
+        const uint32_t col = k.span * kSpan + at;
+        if (k.more()) next = fetch_codes16<FULL>(P.from, k.row, col, FULL ? 16 : live_of(P.cols, col, 16));
     };
     Walk k(P.rows, spans);
     load(k);
     while (k.more()) {
-        Codes c[kUnits];
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u) c[u] = next[u];
-        const uint32_t row = k.row, first = k.span * kSpan + at;
+        const Codes16 c = next;
+        const uint32_t row = k.row, col = k.span * kSpan + at;
         k.next();
         load(k);
+        float v[2][8];
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-            float v[8];
-            values(c[u], v);
-            store8<DT, FULL>(P.out, row, first + u * 256, FULL ? 8 : live_of(P.cols, first + u * 256), P.out.vec, v);
-        }
+        for (int h = 0; h < 2; ++h) values(Codes{c.h[h], c.b}, v[h]);
+        store16<DT, FULL>(P.out, row, col, FULL ? 16 : live_of(P.cols, col, 16), P.out.vec, v);
     }
 }
 
@@ -417,17 +502,24 @@ bool matrix_ok(const void *p, int32_t dtype, uint64_t ld, uint64_t cols)
     return p && muon::element_aligned(p, dtype) && pitch_ok(ld, cols);
 }
 
-Matrix matrix(const void *p, uint64_t ld)
+// How every row's units begin: on 32 bytes (2: eight f32 values or sixteen bf16 ones in
+// one access), on 16 bytes (1: eight bf16 values or four f32 ones), or not.
+uint32_t rows_vec(const void *p, uint64_t ld, int32_t dtype)
 {
-    return Matrix{p, static_cast<uint32_t>(ld), !muon::units_aligned(p, ld, 0) ? 0u : muon::aligned32(p) ? 2u : 1u};
+    const uint64_t off = reinterpret_cast<uintptr_t>(p) | ld * (dtype == ASR_BF16 ? 2 : 4);
+    return off % 32 == 0 ? 2 : off % 16 == 0 ? 1 : 0;
 }
 
-Out out(void *p, uint64_t ld)
-{
-    return Out{p, static_cast<uint32_t>(ld), !muon::units_aligned(p, ld, 0) ? 0u : muon::aligned32(p) ? 2u : 1u};
-}
+Matrix matrix(const void *p, uint64_t ld, int32_t dtype) { return Matrix{p, static_cast<uint32_t>(ld), rows_vec(p, ld, dtype)}; }
 
-bool aligned8(const void *p, uint64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0 && ld % 8 == 0; }
+Out out(void *p, uint64_t ld, int32_t dtype) { return Out{p, static_cast<uint32_t>(ld), rows_vec(p, ld, dtype)}; }
+
+// Codes of 16 values (2) or 8 (1) are aligned to their size.
+uint32_t codes_vec(const void *p, uint64_t ld)
+{
+    const uint64_t off = reinterpret_cast<uintptr_t>(p) | ld;
+    return off % 16 == 0 ? 2 : off % 8 == 0 ? 1 : 0;
+}
 
 uint64_t groups(uint64_t cols) { return (cols + kGroup - 1) / kGroup; }
 
@@ -449,7 +541,7 @@ asr_status writable(const asr_checkpoint &c, uint64_t rows, uint64_t cols)
 Source source(const asr_checkpoint &c)
 {
     return Source{c.q, c.power, static_cast<uint32_t>(c.q_ld), static_cast<uint32_t>(c.power_ld),
-                  aligned8(c.q, c.q_ld) ? 1u : 0u};
+                  codes_vec(c.q, c.q_ld)};
 }
 
 Store store(const asr_checkpoint &c, uint64_t cols)
@@ -461,7 +553,7 @@ Store store(const asr_checkpoint &c, uint64_t cols)
     S.power_ld = static_cast<uint32_t>(c.power_ld);
     S.base = c.base_index / 8;
     S.across = static_cast<uint32_t>(groups(cols) * (kGroup / 8));
-    S.vec = aligned8(c.q, c.q_ld);
+    S.vec = codes_vec(c.q, c.q_ld);
     S.step = c.step;
     S.keys = make_keys(c.seed);
     return S;
@@ -539,11 +631,11 @@ asr_status pack(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, uint
     if (st == ASR_OK) st = setup();
     if (st != ASR_OK) return st;
     PackParams P;
-    P.x = matrix(x, x_ld);
+    P.x = matrix(x, x_ld, dtype);
     P.rows = static_cast<uint32_t>(rows);
     P.cols = static_cast<uint32_t>(cols);
     P.to = store(*to, cols);
-    const bool sr = to->rounding == ASR_ROUND_SR, full = cols % kSpan == 0 && P.x.vec && P.to.vec;
+    const bool sr = to->rounding == ASR_ROUND_SR, full = cols % kSpan == 0 && P.x.vec == 2 && P.to.vec == 2;
     auto kernel = sr ? pack_kernel<true, ASR_F32, false> : pack_kernel<false, ASR_F32, false>;
     if (dtype == ASR_BF16)
         kernel = full ? (sr ? pack_kernel<true, ASR_BF16, true> : pack_kernel<false, ASR_BF16, true>)
@@ -563,10 +655,10 @@ asr_status unpack(const asr_checkpoint *from, uint64_t rows, uint64_t cols, void
     if (st != ASR_OK) return st;
     UnpackParams P;
     P.from = source(*from);
-    P.out = out(dst, ld);
+    P.out = out(dst, ld, dtype);
     P.rows = static_cast<uint32_t>(rows);
     P.cols = static_cast<uint32_t>(cols);
-    const bool full = cols % kSpan == 0 && P.from.vec && P.out.vec;
+    const bool full = cols % kSpan == 0 && P.from.vec == 2 && P.out.vec == 2;
     auto kernel = dtype != ASR_BF16 ? unpack_kernel<ASR_F32, false> : full ? unpack_kernel<ASR_BF16, true>
                                                                            : unpack_kernel<ASR_BF16, false>;
     return walk(ASR_KERNEL_CHECKPOINT, kernel, P, rows, cols, kSpan, stream);

@@ -74,25 +74,20 @@ struct LookupParams {
 template <int DT>
 __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant__ LookupParams P, uint32_t spans)
 {
-    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t lane = (threadIdx.x & 31) * 16;
     for (kept::Walk k(static_cast<uint32_t>(P.ids.n), spans); k.more(); k.next()) {
-        const uint32_t id = key_of(P.ids, k.row);
-        kept::Raw<DT> raw[kept::kUnits];
+        const uint32_t id = key_of(P.ids, k.row), col = k.span * kept::kSpan + lane;
+        const int live = live_of(P.dim, col, 16);
+        const kept::Pair<DT> raw = kept::fetch16<DT, false>(P.table, id, col, id < P.ids.vocab ? live : 0, P.table.vec);
+        float v[2][8];
 #pragma unroll
-        for (int u = 0; u < kept::kUnits; ++u) {
-            const uint32_t col = k.span * kept::kSpan + u * 256 + lane * 8;
-            raw[u] = kept::fetch<DT>(P.table, id, col, id < P.ids.vocab ? live_of(P.dim, col) : 0, P.table.vec);
-        }
-#pragma unroll
-        for (int u = 0; u < kept::kUnits; ++u) {
-            const uint32_t col = k.span * kept::kSpan + u * 256 + lane * 8;
-            float v[8];
-            kept::values(raw[u], v);
+        for (int h = 0; h < 2; ++h) {
+            kept::values(raw.h[h], v[h]);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                v[i] = id < P.ids.vocab ? __fmul_rn(v[i], P.scale) : __uint_as_float(0x7FC00000u);
-            kept::store8<DT>(P.y, k.row, col, live_of(P.dim, col), P.y.vec, v);
+                v[h][i] = id < P.ids.vocab ? __fmul_rn(v[h][i], P.scale) : __uint_as_float(0x7FC00000u);
         }
+        kept::store16<DT, false>(P.y, k.row, col, live, P.y.vec, v);
     }
 }
 
@@ -611,8 +606,8 @@ asr_status lookup(const void *ids, int32_t index, uint64_t tokens, const void *t
     if (st != ASR_OK) return st;
     LookupParams P;
     P.ids = ids_of(ids, index, tokens, vocab, -1);
-    P.table = kept::matrix(table, table_ld);
-    P.y = kept::out(y, y_ld);
+    P.table = kept::matrix(table, table_ld, dtype);
+    P.y = kept::out(y, y_ld, dtype);
     P.dim = static_cast<uint32_t>(dim);
     P.scale = static_cast<float>(scale);
     auto kernel = dtype == ASR_BF16 ? lookup_kernel<ASR_BF16> : lookup_kernel<ASR_F32>;
@@ -760,8 +755,8 @@ asr_status grads(const void *ids, int32_t index, uint64_t tokens, const void *dy
     P.vocab = static_cast<uint32_t>(vocab);
     P.dim = dim;
     P.pitch = muon::up(dim, 8);
-    P.dy = kept::matrix(dy, dy_ld);
-    P.out = kept::out(dtable, dim);
+    P.dy = kept::matrix(dy, dy_ld, dy_dtype);
+    P.out = kept::out(dtable, dim, dtable_dtype);
     P.head = reinterpret_cast<float *>(w + L.head);
     P.tail = reinterpret_cast<float *>(w + L.tail);
     P.arrived = words(L.arrived);

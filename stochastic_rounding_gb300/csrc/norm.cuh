@@ -782,8 +782,8 @@ asr_status forward(const asr_norm_params *p, const void *x, uint64_t x_ld, void 
     if (st == ASR_OK) st = setup();
     if (st != ASR_OK) return st;
     Params P = common(p);
-    P.x = kept::matrix(x, x_ld);
-    P.y = kept::out(y, y_ld);
+    P.x = kept::matrix(x, x_ld, p->dtype);
+    P.y = kept::out(y, y_ld, p->dtype);
     P.mean = mean;
     P.rstd = rstd;
     if (to) {
@@ -846,10 +846,10 @@ asr_status backward(const asr_norm_params *p, const void *dy, uint64_t dy_ld, co
     if (st != ASR_OK) return st;
     if (p->rows) {
         Params P = common(p);
-        P.dy = kept::matrix(dy, dy_ld);
-        if (dx) P.dx = kept::out(dx, dx_ld);
+        P.dy = kept::matrix(dy, dy_ld, p->dtype);
+        if (dx) P.dx = kept::out(dx, dx_ld, p->dtype);
         if (from) P.from = kept::source(*from);
-        else P.x = kept::matrix(x, x_ld);
+        else P.x = kept::matrix(x, x_ld, p->dtype);
         P.mean = const_cast<float *>(mean);
         P.rstd = const_cast<float *>(rstd);
         P.partial = static_cast<float *>(ws);
