@@ -188,6 +188,55 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
     }
 }
 
+// Rows off alignment.  Nothing is kept on the way where gated: that is a call of its own.
+template <int DT, bool GATED, int KEEP>
+__global__ void __launch_bounds__(kThreads) forward_loose_kernel(const __grid_constant__ Params P, uint32_t spans)
+{
+    __shared__ __align__(16) kept::Halves halves;
+    const bool gelu = P.gelu;
+    for (kept::Walk k(P.rows, spans); k.more(); k.next()) {
+        const uint32_t first = k.span * kept::kSpan;
+        float a[kept::kLoose], b[kept::kLoose];
+        kept::fetch_loose<DT>(P.x, k.row, first, P.cols, a);
+        if (GATED) kept::fetch_loose<DT>(P.x, k.row, P.cols + first, 2 * P.cols, b);
+        if (KEEP) kept::keep_loose<KEEP == 2>(P.to, halves.v[threadIdx.x >> 5], k.row, first, P.cols, a);
+#pragma unroll
+        for (int i = 0; i < kept::kLoose; ++i) {
+            const uint32_t col = first + 32 * i + (threadIdx.x & 31);
+            float y = value<DT>(a[i], gelu);
+            if (GATED) y = __fmul_rn(y, b[i]);
+            if (col < P.cols) kept::store1<DT>(P.y, k.row, col, y);
+        }
+    }
+}
+
+// KEPT: from codes.
+template <int DT, bool GATED, bool KEPT>
+__global__ void __launch_bounds__(kThreads) backward_loose_kernel(const __grid_constant__ Params P, uint32_t spans)
+{
+    const bool gelu = P.gelu;
+    for (kept::Walk k(P.rows, spans); k.more(); k.next()) {
+        const uint32_t first = k.span * kept::kSpan;
+        float a[kept::kLoose], b[kept::kLoose], g[kept::kLoose];
+        kept::fetch_loose<DT>(P.dy, k.row, first, P.cols, g);
+        if (KEPT) kept::restore_loose<true>(P.from, k.row, first, P.cols, a);
+        else kept::fetch_loose<DT>(P.x, k.row, first, P.cols, a);
+        if (GATED && KEPT) kept::restore_loose<false>(P.from, k.row, P.cols + first, 2 * P.cols, b);
+        else if (GATED) kept::fetch_loose<DT>(P.x, k.row, P.cols + first, 2 * P.cols, b);
+#pragma unroll
+        for (int i = 0; i < kept::kLoose; ++i) {
+            const uint32_t col = first + 32 * i + (threadIdx.x & 31);
+            float f, df;
+            value_and_slope<DT>(a[i], gelu, f, df);
+            if (GATED) df = __fmul_rn(df, b[i]);
+            if (col < P.cols) {
+                kept::store1<DT>(P.dx, k.row, col, __fmul_rn(g[i], df));
+                if (GATED) kept::store1<DT>(P.dx, k.row, P.cols + col, __fmul_rn(g[i], f));
+            }
+        }
+    }
+}
+
 // ------------------------------------------------------------------ host
 
 using Kernel = void (*)(const Params, uint32_t);
@@ -199,10 +248,21 @@ Kernel forward_of(int keep)
                                                                  : forward_kernel<DT, GATED, 0, FULL>;
 }
 
-Kernel forward_of(int32_t dtype, bool gated, int keep, bool full)
+template <int DT>
+Kernel loose_forward_of(bool gated, int keep)
 {
+    if (gated) return forward_loose_kernel<DT, true, 0>;
+    return keep == 2 ? forward_loose_kernel<DT, false, 2> : keep ? forward_loose_kernel<DT, false, 1>
+                                                                 : forward_loose_kernel<DT, false, 0>;
+}
+
+enum { kGeneral = 0, kFull = 1, kOff = 2 };     // how rows lie
+
+Kernel forward_of(int32_t dtype, bool gated, int keep, int how)
+{
+    if (how == kOff) return dtype == ASR_BF16 ? loose_forward_of<ASR_BF16>(gated, keep) : loose_forward_of<ASR_F32>(gated, keep);
     if (dtype != ASR_BF16) return gated ? forward_of<ASR_F32, true, false>(keep) : forward_of<ASR_F32, false, false>(keep);
-    if (full) return gated ? forward_of<ASR_BF16, true, true>(keep) : forward_of<ASR_BF16, false, true>(keep);
+    if (how == kFull) return gated ? forward_of<ASR_BF16, true, true>(keep) : forward_of<ASR_BF16, false, true>(keep);
     return gated ? forward_of<ASR_BF16, true, false>(keep) : forward_of<ASR_BF16, false, false>(keep);
 }
 
@@ -214,10 +274,18 @@ Kernel backward_of(bool gated, int codes)
     return codes ? backward_kernel<DT, true, 1, FULL> : backward_kernel<DT, true, 0, FULL>;
 }
 
-Kernel backward_of(int32_t dtype, bool gated, int codes, bool full)
+template <int DT>
+Kernel loose_backward_of(bool gated, int codes)
 {
+    if (gated) return codes ? backward_loose_kernel<DT, true, true> : backward_loose_kernel<DT, true, false>;
+    return codes ? backward_loose_kernel<DT, false, true> : backward_loose_kernel<DT, false, false>;
+}
+
+Kernel backward_of(int32_t dtype, bool gated, int codes, int how)
+{
+    if (how == kOff) return dtype == ASR_BF16 ? loose_backward_of<ASR_BF16>(gated, codes) : loose_backward_of<ASR_F32>(gated, codes);
     if (dtype != ASR_BF16) return backward_of<ASR_F32, false>(gated, codes);
-    return full ? backward_of<ASR_BF16, true>(gated, codes) : backward_of<ASR_BF16, false>(gated, codes);
+    return how == kFull ? backward_of<ASR_BF16, true>(gated, codes) : backward_of<ASR_BF16, false>(gated, codes);
 }
 
 asr_status setup()
@@ -228,11 +296,11 @@ asr_status setup()
     const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
     if (e == cudaSuccess && (ready.load(std::memory_order_acquire) & bit)) return ASR_OK;
     for (int32_t dtype : {ASR_F32, ASR_BF16})
-        for (int full = 0; full < 2; ++full)
+        for (int how : {kGeneral, kFull, kOff})
             for (int gated = 0; gated < 2; ++gated)
                 for (int form = 0; form < 3; ++form) {
-                    if (e == cudaSuccess) e = prod::load_kernel(forward_of(dtype, gated != 0, form, full != 0));
-                    if (e == cudaSuccess) e = prod::load_kernel(backward_of(dtype, gated != 0, form, full != 0));
+                    if (e == cudaSuccess) e = prod::load_kernel(forward_of(dtype, gated != 0, form, how));
+                    if (e == cudaSuccess) e = prod::load_kernel(backward_of(dtype, gated != 0, form, how));
                 }
     if (e != cudaSuccess) return cuda_fail(e);
     ready.fetch_or(bit, std::memory_order_release);
@@ -265,15 +333,17 @@ asr_status forward(const void *x, uint64_t x_ld, void *y, uint64_t y_ld, int32_t
     P.rows = static_cast<uint32_t>(rows);
     P.cols = static_cast<uint32_t>(cols);
     P.gelu = function == ASR_GELU;
+    int keep = 0, how = cols % kept::kSpan == 0 && P.x.vec == 2 && P.y.vec == 2 ? kFull : kGeneral;
+    if (!P.x.vec || !P.y.vec || (gated && cols % 8 != 0)) how = kOff;
+    if (to) P.to = kept::store(*to, width);
     // the kernel's lanes hold whole groups of both halves where they begin with the halves
-    const bool apart = to && gated && cols % kept::kGroup != 0;
-    int keep = 0;
+    const bool apart = to && gated && (cols % kept::kGroup != 0 || how == kOff || !P.to.vec);
     if (to && !apart) {
-        P.to = kept::store(*to, width);
         keep = to->rounding == ASR_ROUND_SR ? 2 : 1;
+        if (!P.to.vec) how = kOff;
+        else if (P.to.vec == 1 && how == kFull) how = kGeneral;
     }
-    const bool full = cols % kept::kSpan == 0 && P.x.vec == 2 && P.y.vec == 2 && (!keep || P.to.vec == 2);
-    st = kept::walk(ASR_KERNEL_ACTIVATION, forward_of(dtype, gated != 0, keep, full), P, rows, cols, kept::kSpan, stream);
+    st = kept::walk(ASR_KERNEL_ACTIVATION, forward_of(dtype, gated != 0, keep, how), P, rows, cols, kept::kSpan, stream);
     if (st == ASR_OK && apart) st = kept::pack(x, dtype, rows, width, x_ld, to, stream);
     return st;
 }
@@ -302,8 +372,10 @@ asr_status backward(const void *dy, uint64_t dy_ld, const void *x, uint64_t x_ld
     P.cols = static_cast<uint32_t>(cols);
     P.gelu = function == ASR_GELU;
     const int codes = !from ? 0 : gated && cols % kept::kGroup != 0 ? 2 : 1;
-    const bool full = cols % kept::kSpan == 0 && P.dy.vec == 2 && P.dx.vec == 2 && (from ? P.from.vec : P.x.vec) == 2;
-    return kept::walk(ASR_KERNEL_ACTIVATION, backward_of(dtype, gated != 0, codes, full), P, rows, cols, kept::kSpan, stream);
+    const uint32_t in = from ? P.from.vec : P.x.vec;
+    int how = cols % kept::kSpan == 0 && P.dy.vec == 2 && P.dx.vec == 2 && in == 2 ? kFull : kGeneral;
+    if (!P.dy.vec || !P.dx.vec || !in || (gated && cols % 8 != 0)) how = kOff;
+    return kept::walk(ASR_KERNEL_ACTIVATION, backward_of(dtype, gated != 0, codes, how), P, rows, cols, kept::kSpan, stream);
 }
 
 }  // namespace act

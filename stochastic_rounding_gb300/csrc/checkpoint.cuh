@@ -431,6 +431,113 @@ __device__ __forceinline__ void store16(const Out &O, uint32_t row, uint32_t col
     }
 }
 
+// ---- rows that begin off alignment
+//
+// A lane's sixteen values then lie 32 columns apart, the warp's side by side: every
+// access is of single values but of whole sectors, where units at any address would
+// take each sector several times (8,192 x 14,335: the gated activation's backward pass
+// @@A@@ us, 1,270 by units).  A group is a warp's values of one place.
+
+constexpr int kLoose = 16;
+
+template <int DT>
+__device__ __forceinline__ float load1(const Matrix &M, uint32_t row, uint32_t col)
+{
+    if (DT == ASR_F32) return static_cast<const float *>(M.p)[place(row, M.ld, col)];
+    return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(M.p)[place(row, M.ld, col)]) << 16);
+}
+
+template <int DT>
+__device__ __forceinline__ void store1(const Out &O, uint32_t row, uint32_t col, float v)
+{
+    if (DT == ASR_F32) static_cast<float *>(O.p)[place(row, O.ld, col)] = v;
+    else static_cast<__nv_bfloat16 *>(O.p)[place(row, O.ld, col)] = __float2bfloat16_rn(v);
+}
+
+// The values of columns first + 32 i + lane of a row.
+template <int DT>
+__device__ __forceinline__ void fetch_loose(const Matrix &M, uint32_t row, uint32_t first, uint32_t end, float x[kLoose])
+{
+#pragma unroll
+    for (int i = 0; i < kLoose; ++i) {
+        const uint32_t col = first + 32 * i + (threadIdx.x & 31);
+        x[i] = col < end ? load1<DT>(M, row, col) : 0.0f;
+    }
+}
+
+// A warp's random numbers: the outputs of 64 counters, whose halves in order are those
+// of its 512 values.  Counter k of them is base(k / 4) + k % 4.
+struct Halves {
+    uint16_t v[kThreads / 32][512];
+};
+
+template <typename F>
+__device__ __forceinline__ void draw_halves(const Store &S, uint16_t *to, F base)
+{
+    const uint32_t lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint64_t at = base(8 * h + (lane >> 2)) + (lane & 3);
+        uint32_t w[4];
+        philox4x32_10(static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32), S.step, kStream, S.keys, w);
+        reinterpret_cast<uint4 *>(to)[32 * h + lane] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+}
+
+// A code (its low byte) of one value, from its half.
+template <bool SR>
+__device__ __forceinline__ uint32_t code1(float x, float up, uint32_t half)
+{
+    if (SR) return __float_as_uint(__fadd_ru(__fmaf_ru(x, up, -__uint_as_float(0x43000000u | half)), 12583040.0f));
+    return __float_as_uint(__fmaf_rn(x, up, 12582912.0f));
+}
+
+// Power of the group that a warp holds a value of each of.
+__device__ __forceinline__ uint32_t warp_power(float x)
+{
+    return power_of(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x) & 0x7FFFFFFFu));
+}
+
+// Keeps a lane's sixteen values of a span that begins at column `first`, a multiple of 512.
+template <bool SR>
+__device__ __forceinline__ void keep_loose(const Store &S, uint16_t *halves, uint32_t row, uint32_t first, uint32_t cols,
+                                           const float x[kLoose])
+{
+    const uint32_t lane = threadIdx.x & 31;
+    if (SR) draw_halves(S, halves, [&](uint32_t g) { return S.base + place(row, S.across, first / 8 + 4 * g); });
+    uint32_t power = 0;
+#pragma unroll
+    for (int i = 0; i < kLoose; ++i) {
+        const uint32_t b = warp_power(x[i]), col = first + 32 * i + lane;
+        if (lane == i) power = b;
+        const uint32_t c = code1<SR>(x[i], __uint_as_float((254u - b) << 23), SR ? halves[32 * i + lane] : 0);
+        if (col < cols) S.q[place(row, S.q_ld, col)] = static_cast<int8_t>(b == 255u ? 0 : c);
+    }
+    if (lane < kLoose && first + 32 * lane < cols)
+        S.power[place(row, S.power_ld, first / 32 + lane)] = static_cast<uint8_t>(power);
+}
+
+__device__ __forceinline__ float value1(int8_t q, float scale) { return __fmul_rn(static_cast<float>(q), scale); }
+
+// The values that a span's codes stand for, as they lie (ALIGNED: groups begin with
+// the warp's values, else anywhere).
+template <bool ALIGNED>
+__device__ __forceinline__ void restore_loose(const Source &S, uint32_t row, uint32_t first, uint32_t end, float x[kLoose])
+{
+    const uint32_t lane = threadIdx.x & 31;
+    float mine = 0.0f;
+    if (ALIGNED && lane < kLoose && first + 32 * lane < end) mine = scale_of(S.power[place(row, S.power_ld, first / 32 + lane)]);
+#pragma unroll
+    for (int i = 0; i < kLoose; ++i) {
+        const uint32_t col = first + 32 * i + lane;
+        float scale = ALIGNED ? __shfl_sync(0xFFFFFFFFu, mine, i) : 0.0f;
+        if (!ALIGNED && col < end) scale = scale_of(S.power[place(row, S.power_ld, col >> 5)]);
+        x[i] = col < end ? value1(S.q[place(row, S.q_ld, col)], scale) : 0.0f;
+    }
+}
+
 struct PackParams {
     Matrix x;
     uint32_t rows, cols;
@@ -484,6 +591,31 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const __grid_constant_
 #pragma unroll
         for (int h = 0; h < 2; ++h) values(Codes{c.h[h], c.b}, v[h]);
         store16<DT, FULL>(P.out, row, col, FULL ? 16 : live_of(P.cols, col, 16), P.out.vec, v);
+    }
+}
+
+template <bool SR, int DT>
+__global__ void __launch_bounds__(kThreads) pack_loose_kernel(const __grid_constant__ PackParams P, uint32_t spans)
+{
+    __shared__ __align__(16) Halves halves;
+    for (Walk k(P.rows, spans); k.more(); k.next()) {
+        float x[kLoose];
+        fetch_loose<DT>(P.x, k.row, k.span * kSpan, P.cols, x);
+        keep_loose<SR>(P.to, halves.v[threadIdx.x >> 5], k.row, k.span * kSpan, P.cols, x);
+    }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads) unpack_loose_kernel(const __grid_constant__ UnpackParams P, uint32_t spans)
+{
+    for (Walk k(P.rows, spans); k.more(); k.next()) {
+        float x[kLoose];
+        restore_loose<true>(P.from, k.row, k.span * kSpan, P.cols, x);
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i) {
+            const uint32_t col = k.span * kSpan + 32 * i + (threadIdx.x & 31);
+            if (col < P.cols) store1<DT>(P.out, k.row, col, x[i]);
+        }
     }
 }
 
@@ -616,7 +748,9 @@ asr_status setup()
     return load_once(ready, pack_kernel<false, ASR_F32, false>, pack_kernel<false, ASR_BF16, false>,
                      pack_kernel<false, ASR_BF16, true>, pack_kernel<true, ASR_F32, false>,
                      pack_kernel<true, ASR_BF16, false>, pack_kernel<true, ASR_BF16, true>, unpack_kernel<ASR_F32, false>,
-                     unpack_kernel<ASR_BF16, false>, unpack_kernel<ASR_BF16, true>);
+                     unpack_kernel<ASR_BF16, false>, unpack_kernel<ASR_BF16, true>, pack_loose_kernel<false, ASR_F32>,
+                     pack_loose_kernel<false, ASR_BF16>, pack_loose_kernel<true, ASR_F32>, pack_loose_kernel<true, ASR_BF16>,
+                     unpack_loose_kernel<ASR_F32>, unpack_loose_kernel<ASR_BF16>);
 }
 
 asr_status pack(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, uint64_t x_ld, const asr_checkpoint *to,
@@ -640,6 +774,9 @@ asr_status pack(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, uint
     if (dtype == ASR_BF16)
         kernel = full ? (sr ? pack_kernel<true, ASR_BF16, true> : pack_kernel<false, ASR_BF16, true>)
                       : (sr ? pack_kernel<true, ASR_BF16, false> : pack_kernel<false, ASR_BF16, false>);
+    if (!P.x.vec || !P.to.vec)
+        kernel = dtype == ASR_BF16 ? (sr ? pack_loose_kernel<true, ASR_BF16> : pack_loose_kernel<false, ASR_BF16>)
+                                   : (sr ? pack_loose_kernel<true, ASR_F32> : pack_loose_kernel<false, ASR_F32>);
     return walk(ASR_KERNEL_CHECKPOINT, kernel, P, rows, cols, kSpan, stream);
 }
 
@@ -661,6 +798,7 @@ asr_status unpack(const asr_checkpoint *from, uint64_t rows, uint64_t cols, void
     const bool full = cols % kSpan == 0 && P.from.vec == 2 && P.out.vec == 2;
     auto kernel = dtype != ASR_BF16 ? unpack_kernel<ASR_F32, false> : full ? unpack_kernel<ASR_BF16, true>
                                                                            : unpack_kernel<ASR_BF16, false>;
+    if (!P.from.vec || !P.out.vec) kernel = dtype == ASR_BF16 ? unpack_loose_kernel<ASR_BF16> : unpack_loose_kernel<ASR_F32>;
     return walk(ASR_KERNEL_CHECKPOINT, kernel, P, rows, cols, kSpan, stream);
 }
 

@@ -91,6 +91,22 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant_
     }
 }
 
+template <int DT>
+__global__ void __launch_bounds__(kThreads) lookup_loose_kernel(const __grid_constant__ LookupParams P, uint32_t spans)
+{
+    for (kept::Walk k(static_cast<uint32_t>(P.ids.n), spans); k.more(); k.next()) {
+        const uint32_t id = key_of(P.ids, k.row), first = k.span * kept::kSpan;
+        float x[kept::kLoose];
+        kept::fetch_loose<DT>(P.table, id, first, id < P.ids.vocab ? P.dim : 0, x);
+#pragma unroll
+        for (int i = 0; i < kept::kLoose; ++i) {
+            const uint32_t col = first + 32 * i + (threadIdx.x & 31);
+            const float v = id < P.ids.vocab ? __fmul_rn(x[i], P.scale) : __uint_as_float(0x7FC00000u);
+            if (col < P.dim) kept::store1<DT>(P.y, k.row, col, v);
+        }
+    }
+}
+
 // ---- sort
 
 // Ranks of a block's keys by one digit.  Warp w holds keys w * rounds * 32 on, 32 a
@@ -133,7 +149,7 @@ __device__ __forceinline__ void rank_digits(const uint32_t key[ROUNDS], uint32_t
 struct ZeroParams {
     void *p;                                    // vocab x dim
     uint64_t dim;
-    uint32_t dtype, vec;
+    uint32_t dtype;
 };
 
 // Zeroes rows v0 .. v0 + rows - 1 of the table but those set in `taken`.
@@ -143,13 +159,18 @@ __device__ __forceinline__ void zero_rows(const ZeroParams &Z, uint64_t v0, uint
     const uint64_t size = Z.dtype == ASR_BF16 ? 2 : 4, bytes = Z.dim * size;
     for (uint32_t r = warp; r < rows; r += warps) {
         if ((taken[r >> 5] >> (r & 31)) & 1) continue;
-        char *p = static_cast<char *>(Z.p) + (v0 + r) * bytes;
-        if (Z.vec) {
-            for (uint64_t i = lane * 16ull; i < bytes; i += 512) *reinterpret_cast<uint4 *>(p + i) = make_uint4(0, 0, 0, 0);
-        } else if (Z.dtype == ASR_BF16) {
-            for (uint64_t i = lane; i < Z.dim; i += 32) reinterpret_cast<uint16_t *>(p)[i] = 0;
+        char *p = static_cast<char *>(Z.p) + (v0 + r) * bytes, *const end = p + bytes;
+        // up to 16 bytes' alignment value by value, then in 16 bytes, then the rest
+        char *const even = p + ((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15);
+        const uint64_t whole = even < end ? static_cast<uint64_t>(end - even) / 16 * 16 : 0;
+        for (uint64_t i = lane * 16ull; i < whole; i += 512) *reinterpret_cast<uint4 *>(even + i) = make_uint4(0, 0, 0, 0);
+        char *const rest = even + whole;        // past `end` where the row ends before its first 16 bytes
+        if (Z.dtype == ASR_BF16) {
+            if (p + lane * 2 < (even < end ? even : end)) reinterpret_cast<uint16_t *>(p)[lane] = 0;
+            if (rest + lane * 2 < end) reinterpret_cast<uint16_t *>(rest)[lane] = 0;
         } else {
-            for (uint64_t i = lane; i < Z.dim; i += 32) reinterpret_cast<float *>(p)[i] = 0.0f;
+            if (p + lane * 4 < (even < end ? even : end)) reinterpret_cast<float *>(p)[lane] = 0.0f;
+            if (rest + lane * 4 < end) reinterpret_cast<float *>(rest)[lane] = 0.0f;
         }
     }
 }
@@ -414,33 +435,58 @@ struct SumParams {
     ZeroParams zero;
 };
 
-template <int OT>
+// Eight of a row's columns: side by side from `col` on, `live` of them, or, LOOSE (rows
+// off alignment), at `col` and every blockDim.x-th behind it.
+template <int OT, bool LOOSE>
 __device__ __forceinline__ void store_row(const SumParams &P, uint32_t row, uint32_t col, int live, float v[8])
 {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], P.scale);
-    kept::store8<OT>(P.out, row, col, live, P.out.vec, v);
+    if (LOOSE) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col + i * blockDim.x < P.dim) kept::store1<OT>(P.out, row, col + i * blockDim.x, v[i]);
+    } else {
+        kept::store8<OT>(P.out, row, col, live, P.out.vec, v);
+    }
 }
 
-__device__ __forceinline__ void store_sum(float *p, const float v[8])
+// A row of sums in the workspace, of chunk c, whose columns lie as store_row's.
+template <bool LOOSE>
+__device__ __forceinline__ void store_sum(float *sums, const SumParams &P, uint32_t c, uint32_t col, const float v[8])
 {
-    __stcg(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
-    __stcg(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
+    float *p = sums + c * P.pitch + col;
+    if (LOOSE) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col + i * blockDim.x < P.dim) __stcg(p + i * blockDim.x, v[i]);
+    } else {
+        __stcg(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
+        __stcg(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
+    }
 }
 
-__device__ __forceinline__ void add_sum(float acc[8], const float *p)
+template <bool LOOSE>
+__device__ __forceinline__ void add_sum(float acc[8], const float *sums, const SumParams &P, uint32_t c, uint32_t col)
 {
-    const float4 a = __ldcg(reinterpret_cast<const float4 *>(p)), b = __ldcg(reinterpret_cast<const float4 *>(p) + 1);
-    acc[0] = __fadd_rn(acc[0], a.x), acc[1] = __fadd_rn(acc[1], a.y), acc[2] = __fadd_rn(acc[2], a.z);
-    acc[3] = __fadd_rn(acc[3], a.w), acc[4] = __fadd_rn(acc[4], b.x), acc[5] = __fadd_rn(acc[5], b.y);
-    acc[6] = __fadd_rn(acc[6], b.z), acc[7] = __fadd_rn(acc[7], b.w);
+    const float *p = sums + c * P.pitch + col;
+    if (LOOSE) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col + i * blockDim.x < P.dim) acc[i] = __fadd_rn(acc[i], __ldcg(p + i * blockDim.x));
+    } else {
+        const float4 a = __ldcg(reinterpret_cast<const float4 *>(p)), b = __ldcg(reinterpret_cast<const float4 *>(p) + 1);
+        acc[0] = __fadd_rn(acc[0], a.x), acc[1] = __fadd_rn(acc[1], a.y), acc[2] = __fadd_rn(acc[2], a.z);
+        acc[3] = __fadd_rn(acc[3], a.w), acc[4] = __fadd_rn(acc[4], b.x), acc[5] = __fadd_rn(acc[5], b.y);
+        acc[6] = __fadd_rn(acc[6], b.z), acc[7] = __fadd_rn(acc[7], b.w);
+    }
 }
 
 // Block c has left its sum of `row`, which reaches over chunks' ends (`began`: from
 // before this one).  The last one to do so adds them all up: of the chunk where the row
 // begins its tail, of the others their heads, in order.  All threads of the block come
 // here together.
-template <int OT>
+template <int OT, bool LOOSE>
 __device__ __forceinline__ void join(const SumParams &P, uint32_t c, uint32_t row, bool began, uint32_t slice, uint32_t col,
                                      int live)
 {
@@ -471,10 +517,10 @@ __device__ __forceinline__ void join(const SumParams &P, uint32_t c, uint32_t ro
     const uint32_t first = ends[0], last = ends[1];
     if (before != last - first || live == 0) return;
     float acc[8] = {};
-    add_sum(acc, P.tail + first * P.pitch + col);
-#pragma unroll 8
-    for (uint32_t d = first + 1; d <= last; ++d) add_sum(acc, P.head + d * P.pitch + col);
-    store_row<OT>(P, row, col, live, acc);
+    add_sum<LOOSE>(acc, P.tail, P, first, col);
+#pragma unroll(LOOSE ? 1 : 8)
+    for (uint32_t d = first + 1; d <= last; ++d) add_sum<LOOSE>(acc, P.head, P, d, col);
+    store_row<OT, LOOSE>(P, row, col, live, acc);
 }
 
 // A block a chunk and a slice of the columns, eight a thread; the blocks behind those
@@ -482,10 +528,10 @@ __device__ __forceinline__ void join(const SumParams &P, uint32_t c, uint32_t ro
 constexpr int kSumThreads = 128;                // at most
 constexpr int kPiece = 64;                      // tokens whose keys are at hand
 
-template <int DT, int OT>
-__global__ void __launch_bounds__(kSumThreads, 6) sum_kernel(const __grid_constant__ SumParams P)
+template <int DT, int OT, bool LOOSE>
+__global__ void __launch_bounds__(kSumThreads, LOOSE ? 4 : 6) sum_kernel(const __grid_constant__ SumParams P)
 {
-    constexpr int kAhead = DT == ASR_BF16 ? 8 : 4;          // rows fetched before they are added up
+    constexpr int kAhead = LOOSE ? 2 : DT == ASR_BF16 ? 8 : 4;      // rows fetched before they are added up
     __shared__ uint32_t key[kPiece + 2], order[kPiece];     // keys from the one before on
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t sums = P.chunks * P.slices;
@@ -511,7 +557,7 @@ __global__ void __launch_bounds__(kSumThreads, 6) sum_kernel(const __grid_consta
         return;
     }
     const uint32_t c = blockIdx.x / P.slices, slice = blockIdx.x % P.slices;
-    const uint32_t col = (slice * blockDim.x + threadIdx.x) * 8;
+    const uint32_t col = LOOSE ? slice * blockDim.x * 8 + threadIdx.x : (slice * blockDim.x + threadIdx.x) * 8;
     const int live = live_of(static_cast<uint32_t>(P.dim), col);
     const uint64_t begin = static_cast<uint64_t>(c) * P.chunk, end = begin + P.chunk < P.n ? begin + P.chunk : P.n;
     float acc[8] = {};
@@ -527,35 +573,43 @@ __global__ void __launch_bounds__(kSumThreads, 6) sum_kernel(const __grid_consta
             if (j < kPiece) order[j] = j < n ? P.order[i0 + j] : 0;
         }
         __syncthreads();
-        const uint32_t *const at = key + 1;
+        const uint32_t *const keys = key + 1;
         if (i0 == begin) {
-            front = at[0];
+            front = keys[0];
             began = begin > 0 && key[0] == front;
         }
-        back = at[n - 1];
-        goes_on = i0 + n < P.n && at[n] == back;
-        for (uint32_t a0 = 0; a0 < n && at[a0] < P.vocab; a0 += kAhead) {
+        back = keys[n - 1];
+        goes_on = i0 + n < P.n && keys[n] == back;
+        for (uint32_t a0 = 0; a0 < n && keys[a0] < P.vocab; a0 += kAhead) {
             kept::Raw<DT> raw[kAhead];
+            float loose[kAhead][8];
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
-                const bool in = a0 + a < n && at[a0 + a] < P.vocab;
-                raw[a] = kept::fetch<DT>(P.dy, in ? order[a0 + a] : 0, col, in ? live : 0, P.dy.vec);
+                const bool in = a0 + a < n && keys[a0 + a] < P.vocab;
+                if (LOOSE) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        loose[a][i] = in && col + i * blockDim.x < P.dim
+                                          ? kept::load1<DT>(P.dy, order[a0 + a], col + i * blockDim.x) : 0.0f;
+                } else {
+                    raw[a] = kept::fetch<DT>(P.dy, in ? order[a0 + a] : 0, col, in ? live : 0, P.dy.vec);
+                }
             }
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
-                if (a0 + a >= n || at[a0 + a] >= P.vocab) break;
+                if (a0 + a >= n || keys[a0 + a] >= P.vocab) break;
                 float v[8];
-                kept::values(raw[a], v);
+                if (!LOOSE) kept::values(raw[a], v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], v[i]);
+                for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], LOOSE ? loose[a][i] : v[i]);
                 const bool last = i0 + a0 + a + 1 == end;
-                if (!last && at[a0 + a + 1] == at[a0 + a]) continue;
+                if (!last && keys[a0 + a + 1] == keys[a0 + a]) continue;
                 if (first && began) {
-                    if (live) store_sum(P.head + c * P.pitch + col, acc);
+                    if (live) store_sum<LOOSE>(P.head, P, c, col, acc);
                 } else if (last && goes_on) {
-                    if (live) store_sum(P.tail + c * P.pitch + col, acc);
+                    if (live) store_sum<LOOSE>(P.tail, P, c, col, acc);
                 } else {
-                    store_row<OT>(P, at[a0 + a], col, live, acc);
+                    store_row<OT, LOOSE>(P, keys[a0 + a], col, live, acc);
                 }
                 first = false;
 #pragma unroll
@@ -564,8 +618,8 @@ __global__ void __launch_bounds__(kSumThreads, 6) sum_kernel(const __grid_consta
         }
     }
     // the chunk's first row, if it began before, and its last, if that goes on and is not the same
-    if (began && front < P.vocab) join<OT>(P, c, front, true, slice, col, live);
-    if (goes_on && back < P.vocab && !(began && front == back)) join<OT>(P, c, back, false, slice, col, live);
+    if (began && front < P.vocab) join<OT, LOOSE>(P, c, front, true, slice, col, live);
+    if (goes_on && back < P.vocab && !(began && front == back)) join<OT, LOOSE>(P, c, back, false, slice, col, live);
 }
 
 // ------------------------------------------------------------------ host
@@ -585,12 +639,29 @@ Ids ids_of(const void *ids, int32_t index, uint64_t tokens, uint64_t vocab, int6
                padding >= 0 && static_cast<uint64_t>(padding) < vocab ? static_cast<uint32_t>(padding) : 0xFFFFFFFFu};
 }
 
+using SumKernel = void (*)(const SumParams);
+
+template <int DT, bool LOOSE>
+SumKernel sums_of(int32_t out)
+{
+    return out == ASR_BF16 ? sum_kernel<DT, ASR_BF16, LOOSE> : sum_kernel<DT, ASR_F32, LOOSE>;
+}
+
+SumKernel sums_of(int32_t dy, int32_t out, bool loose)
+{
+    if (loose) return dy == ASR_BF16 ? sums_of<ASR_BF16, true>(out) : sums_of<ASR_F32, true>(out);
+    return dy == ASR_BF16 ? sums_of<ASR_BF16, false>(out) : sums_of<ASR_F32, false>(out);
+}
+
 asr_status setup()
 {
     static std::atomic<uint64_t> ready{0};
-    return kept::load_once(ready, lookup_kernel<ASR_F32>, lookup_kernel<ASR_BF16>, sort_kernel, tile_count_kernel,
-                           tile_scan_kernel, tile_move_kernel, sum_kernel<ASR_F32, ASR_F32>,
-                           sum_kernel<ASR_F32, ASR_BF16>, sum_kernel<ASR_BF16, ASR_F32>, sum_kernel<ASR_BF16, ASR_BF16>);
+    return kept::load_once(ready, lookup_kernel<ASR_F32>, lookup_kernel<ASR_BF16>, lookup_loose_kernel<ASR_F32>,
+                           lookup_loose_kernel<ASR_BF16>, sort_kernel, tile_count_kernel,
+                           tile_scan_kernel, tile_move_kernel, sums_of(ASR_F32, ASR_F32, false),
+                           sums_of(ASR_F32, ASR_BF16, false), sums_of(ASR_BF16, ASR_F32, false),
+                           sums_of(ASR_BF16, ASR_BF16, false), sums_of(ASR_F32, ASR_F32, true), sums_of(ASR_F32, ASR_BF16, true),
+                           sums_of(ASR_BF16, ASR_F32, true), sums_of(ASR_BF16, ASR_BF16, true));
 }
 
 asr_status lookup(const void *ids, int32_t index, uint64_t tokens, const void *table, uint64_t table_ld, uint64_t vocab,
@@ -611,6 +682,7 @@ asr_status lookup(const void *ids, int32_t index, uint64_t tokens, const void *t
     P.dim = static_cast<uint32_t>(dim);
     P.scale = static_cast<float>(scale);
     auto kernel = dtype == ASR_BF16 ? lookup_kernel<ASR_BF16> : lookup_kernel<ASR_F32>;
+    if ((vocab && !P.table.vec) || !P.y.vec) kernel = dtype == ASR_BF16 ? lookup_loose_kernel<ASR_BF16> : lookup_loose_kernel<ASR_F32>;
     return kept::walk(ASR_KERNEL_EMBEDDING, kernel, P, tokens, dim, kept::kSpan, stream);
 }
 
@@ -662,12 +734,6 @@ Layout layout(uint64_t tokens, uint64_t dim)
     return L;
 }
 
-template <int DT>
-void (*sums_of(bool bf))(const SumParams)
-{
-    return bf ? sum_kernel<DT, ASR_BF16> : sum_kernel<DT, ASR_F32>;
-}
-
 asr_status grads(const void *ids, int32_t index, uint64_t tokens, const void *dy, uint64_t dy_ld, int32_t dy_dtype,
                  uint64_t vocab, uint64_t dim, double scale, int64_t padding, void *dtable, int32_t dtable_dtype, void *ws,
                  uint64_t ws_bytes, cudaStream_t stream)
@@ -686,8 +752,7 @@ asr_status grads(const void *ids, int32_t index, uint64_t tokens, const void *dy
     char *w = static_cast<char *>(ws);
     auto words = [&](uint64_t at) { return reinterpret_cast<uint32_t *>(w + at); };
     const Ids I = ids_of(ids, index, tokens, vocab, padding);
-    const ZeroParams Z{dtable, dim, static_cast<uint32_t>(dtable_dtype),
-                       aligned16(dtable) && dim % (dtable_dtype == ASR_BF16 ? 8 : 4) == 0 ? 1u : 0u};
+    const ZeroParams Z{dtable, dim, static_cast<uint32_t>(dtable_dtype)};
     uint32_t bits = 1;
     while ((vocab >> bits) != 0) ++bits;
     const uint32_t passes = (bits + kDigitBits - 1) / kDigitBits, width = (bits + passes - 1) / passes;
@@ -765,9 +830,8 @@ asr_status grads(const void *ids, int32_t index, uint64_t tokens, const void *dy
     P.zero = Z;
     const unsigned threads = threads_of(dim), sums = P.chunks * P.slices;
     const unsigned zeros = static_cast<unsigned>((vocab - P.zero_from + kZeroRows - 1) / kZeroRows);
-    const bool bf = dtable_dtype == ASR_BF16;
-    return prod::launch_early(ASR_KERNEL_EMBEDDING, dy_dtype == ASR_BF16 ? sums_of<ASR_BF16>(bf) : sums_of<ASR_F32>(bf),
-                              dim3(sums + zeros), threads, P, stream);
+    return prod::launch_early(ASR_KERNEL_EMBEDDING, sums_of(dy_dtype, dtable_dtype, !P.dy.vec || !P.out.vec), dim3(sums + zeros),
+                              threads, P, stream);
 }
 
 }  // namespace embed

@@ -230,6 +230,104 @@ __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) forward_kernel(con
     }
 }
 
+// Rows that begin off alignment, a block each: a thread's sixteen values lie blockDim.x
+// columns apart (checkpoint.cuh says why), a warp's of one place side by side, a group.
+constexpr int kLoose = kept::kLoose;
+
+struct LooseHalves {
+    uint16_t v[32][512];
+};
+
+__device__ __forceinline__ float param1(const void *p, uint32_t dtype, uint32_t col, float none)
+{
+    if (!p) return none;
+    return dtype == ASR_BF16 ? bf16_lo(static_cast<const uint16_t *>(p)[col]) : static_cast<const float *>(p)[col];
+}
+
+template <int DT>
+__device__ __forceinline__ void fetch_loose(const kept::Matrix &M, uint32_t row, const Params &P, float x[kLoose])
+{
+#pragma unroll
+    for (int i = 0; i < kLoose; ++i) {
+        const uint32_t col = i * blockDim.x + threadIdx.x;
+        x[i] = col < P.cols ? kept::load1<DT>(M, row, col) : 0.0f;
+    }
+}
+
+template <int DT, bool KEEP>
+__global__ void __launch_bounds__(1024) forward_loose_kernel(const __grid_constant__ Params P)
+{
+    __shared__ Parts parts;
+    __shared__ __align__(16) LooseHalves halves;
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto in = [&](int i) { return i * blockDim.x + threadIdx.x < P.cols; };
+    float counts = 0.0f;                        // of warp `lane`
+    if (lane < blockDim.x >> 5)
+        for (int i = 0; i < kLoose; ++i) {
+            const uint32_t first = i * blockDim.x + lane * 32;
+            counts += first >= P.cols ? 0.0f : static_cast<float>(P.cols - first < 32 ? P.cols - first : 32);
+        }
+    const float own = __shfl_sync(0xFFFFFFFFu, counts, warp), over_own = own > 0.0f ? __frcp_rn(own) : 0.0f;
+    float next[kLoose];
+    fetch_loose<DT>(P.x, blockIdx.x, P, next);
+    uint32_t turn = 0;
+    for (uint32_t row = blockIdx.x; row < P.rows; row += gridDim.x, turn ^= 1) {
+        float x[kLoose], sum = 0.0f, squares = 0.0f, mean = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i) x[i] = next[i];
+        if (row + gridDim.x < P.rows) fetch_loose<DT>(P.x, row + gridDim.x, P, next);
+        if (P.centred) {
+#pragma unroll
+            for (int i = 0; i < kLoose; ++i) sum = __fadd_rn(sum, x[i]);
+            sum = warp_sum(sum);
+            mean = __fmul_rn(sum, over_own);
+        }
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i) {
+            const float d = in(i) ? __fsub_rn(x[i], mean) : 0.0f;
+            squares = __fmaf_rn(d, d, squares);
+        }
+        squares = warp_sum(squares);
+        const float2 p = exchange(parts, turn, make_float2(sum, squares));
+        squares = p.y;
+        if (P.centred) {
+            mean = __fmul_rn(warp_sum(p.x), P.over_n);
+            const float d = counts > 0.0f ? __fsub_rn(__fdiv_rn(p.x, counts), mean) : 0.0f;
+            squares = __fmaf_rn(__fmul_rn(d, d), counts, squares);
+        }
+        const float rstd = __frsqrt_rn(__fmaf_rn(warp_sum(squares), P.over_n, P.eps));
+        if (threadIdx.x == 0 && P.rstd) {
+            P.rstd[row] = rstd;
+            if (P.mean) P.mean[row] = mean;
+        }
+        if (KEEP) {
+            if (P.sr)
+                kept::draw_halves(P.to, halves.v[warp], [&](uint32_t g) {
+                    return P.to.base + kept::place(row, P.to.across, (g * blockDim.x + warp * 32) / 8);
+                });
+            uint32_t power = 0;
+#pragma unroll
+            for (int i = 0; i < kLoose; ++i) {
+                const uint32_t b = kept::warp_power(x[i]), col = i * blockDim.x + threadIdx.x;
+                const float up = __uint_as_float((254u - b) << 23);
+                if (lane == i) power = b;
+                const uint32_t c = P.sr ? kept::code1<true>(x[i], up, halves.v[warp][32 * i + lane]) : kept::code1<false>(x[i], up, 0);
+                if (in(i)) P.to.q[kept::place(row, P.to.q_ld, col)] = static_cast<int8_t>(b == 255u ? 0 : c);
+            }
+            const uint32_t first = lane * blockDim.x + warp * 32;
+            if (lane < kLoose && first < P.cols)
+                P.to.power[kept::place(row, P.to.power_ld, first / 32)] = static_cast<uint8_t>(power);
+        }
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i)
+            if (in(i)) {
+                const uint32_t col = i * blockDim.x + threadIdx.x;
+                kept::store1<DT>(P.y, row, col, __fmaf_rn(__fmul_rn(__fsub_rn(x[i], mean), rstd), param1(P.w, P.w_dtype, col, 1.0f),
+                                                          param1(P.b, P.b_dtype, col, 0.0f)));
+            }
+    }
+}
+
 // Sums over a block's threads, the same in all of them.
 __device__ __forceinline__ float block_sum(float v, float *part)
 {
@@ -520,6 +618,61 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
     }
 }
 
+// Rows off alignment.
+template <int DT, bool KEPT, int THREADS>
+__global__ void __launch_bounds__(THREADS) backward_loose_kernel(const __grid_constant__ Params P)
+{
+    __shared__ Parts parts;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto in = [&](int i) { return i * blockDim.x + threadIdx.x < P.cols; };
+    float dw[kLoose] = {}, db[kLoose] = {};
+    uint32_t turn = 0;
+    for (uint32_t row = blockIdx.x; row < P.rows; row += gridDim.x, turn ^= 1) {
+        float h[kLoose], g[kLoose], along = 0.0f, sum = 0.0f;
+        const float m = P.centred ? P.mean[row] : 0.0f, r = P.rstd[row];
+        fetch_loose<DT>(P.dy, row, P, g);
+        if (KEPT) {
+            const uint32_t first = lane * blockDim.x + warp * 32;
+            float mine = 0.0f;
+            if (lane < kLoose && first < P.cols) mine = kept::scale_of(P.from.power[kept::place(row, P.from.power_ld, first / 32)]);
+#pragma unroll
+            for (int i = 0; i < kLoose; ++i) {
+                const float scale = __shfl_sync(0xFFFFFFFFu, mine, i);
+                h[i] = in(i) ? kept::value1(P.from.q[kept::place(row, P.from.q_ld, i * blockDim.x + threadIdx.x)], scale) : 0.0f;
+            }
+        } else {
+            fetch_loose<DT>(P.x, row, P, h);
+        }
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i) {
+            h[i] = in(i) ? __fmul_rn(__fsub_rn(h[i], m), r) : 0.0f;
+            dw[i] = __fmaf_rn(g[i], h[i], dw[i]);
+            db[i] = __fadd_rn(db[i], g[i]);
+            if (in(i)) g[i] = __fmul_rn(g[i], param1(P.w, P.w_dtype, i * blockDim.x + threadIdx.x, 1.0f));
+            sum = __fadd_rn(sum, g[i]);
+            along = __fmaf_rn(g[i], h[i], along);
+        }
+        if (!P.dx.p) continue;
+        const float2 p = exchange(parts, turn, make_float2(warp_sum(sum), warp_sum(along)));
+        sum = P.centred ? __fmul_rn(__fmul_rn(warp_sum(p.x), P.over_n), r) : 0.0f;
+        along = __fmul_rn(__fmul_rn(warp_sum(p.y), P.over_n), r);
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i)
+            if (in(i))
+                kept::store1<DT>(P.dx, row, i * blockDim.x + threadIdx.x,
+                                 __fmaf_rn(-h[i], along, __fmaf_rn(g[i], r, -sum)));
+    }
+    if (!P.dw && !P.db) return;
+    float *to = P.partial + blockIdx.x * 2 * P.pitch;
+#pragma unroll
+    for (int i = 0; i < kLoose; ++i)
+        if (in(i)) {
+            to[i * blockDim.x + threadIdx.x] = dw[i];
+            if (P.db) to[P.pitch + i * blockDim.x + threadIdx.x] = db[i];
+        }
+}
+
 // Rows that do not fit: dx, a block a row, read twice.
 template <int DT, bool KEPT>
 __global__ void __launch_bounds__(kLongThreads) backward_long_kernel(const __grid_constant__ Params P)
@@ -645,8 +798,15 @@ Kernel forward_of(int shape)
                                                                                    : forward_long_kernel<DT, KEEP>;
 }
 
-Kernel forward_of(int32_t dtype, int shape, bool keep, bool full)
+enum { kGeneral = 0, kFull = 1, kOff = 2 };     // how rows lie; off alignment counts for a block's
+
+Kernel forward_of(int32_t dtype, int shape, bool keep, int how)
 {
+    const bool full = how == kFull;
+    if (how == kOff && shape == kBlock) {
+        if (dtype == ASR_BF16) return keep ? forward_loose_kernel<ASR_BF16, true> : forward_loose_kernel<ASR_BF16, false>;
+        return keep ? forward_loose_kernel<ASR_F32, true> : forward_loose_kernel<ASR_F32, false>;
+    }
     if (dtype != ASR_BF16) return keep ? forward_of<ASR_F32, true, false>(shape) : forward_of<ASR_F32, false, false>(shape);
     if (full) return keep ? forward_of<ASR_BF16, true, true>(shape) : forward_of<ASR_BF16, false, true>(shape);
     return keep ? forward_of<ASR_BF16, true, false>(shape) : forward_of<ASR_BF16, false, false>(shape);
@@ -687,8 +847,19 @@ Backward backward_of(int32_t dtype, int shape, unsigned threads, bool full)
     return full ? backward_of<ASR_BF16, KEPT, true>(shape, threads) : backward_of<ASR_BF16, KEPT, false>(shape, threads);
 }
 
-Backward backward_of(int32_t dtype, bool codes, int shape, unsigned threads, bool full)
+template <int DT, bool KEPT>
+Backward loose_of(unsigned threads)
 {
+    return Backward{threads <= 512 ? backward_loose_kernel<DT, KEPT, 512> : backward_loose_kernel<DT, KEPT, 1024>, 0};
+}
+
+Backward backward_of(int32_t dtype, bool codes, int shape, unsigned threads, int how)
+{
+    const bool full = how == kFull;
+    if (how == kOff && shape == kBlock) {
+        if (dtype == ASR_BF16) return codes ? loose_of<ASR_BF16, true>(threads) : loose_of<ASR_BF16, false>(threads);
+        return codes ? loose_of<ASR_F32, true>(threads) : loose_of<ASR_F32, false>(threads);
+    }
     return codes ? backward_of<true>(dtype, shape, threads, full) : backward_of<false>(dtype, shape, threads, full);
 }
 
@@ -714,13 +885,12 @@ asr_status setup()
     for (int32_t dtype : {ASR_F32, ASR_BF16})
         for (int kept = 0; kept < 2; ++kept) {
             if (e == cudaSuccess) e = prod::load_kernel(columns_of(dtype, kept != 0));
-            for (int form = 0; form < 6; ++form) {
-                const int shape = form % 3;
-                const bool full = form >= 3;
-                if (e == cudaSuccess) e = prod::load_kernel(forward_of(dtype, shape, kept != 0, full));
+            for (int form = 0; form < 9; ++form) {
+                const int shape = form % 3, how = form / 3;
+                if (e == cudaSuccess) e = prod::load_kernel(forward_of(dtype, shape, kept != 0, how));
                 for (unsigned threads : {512u, 1024u}) {
                     if (shape == kWarp) threads = kWarpThreads;
-                    const Backward k = backward_of(dtype, kept != 0, shape, threads, full);
+                    const Backward k = backward_of(dtype, kept != 0, shape, threads, how);
                     if (e == cudaSuccess && k.smem)
                         e = cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem));
                     if (e == cudaSuccess) e = prod::load_kernel(k.kernel);
@@ -792,8 +962,8 @@ asr_status forward(const asr_norm_params *p, const void *x, uint64_t x_ld, void 
     }
     const int shape = shape_of(p->cols);
     const unsigned threads = threads_of(p->cols);
-    const bool full = whole(p->cols) && P.x.vec && P.y.vec && (!to || P.to.vec);
-    auto kernel = forward_of(p->dtype, shape, to != nullptr, full);
+    const bool off = !P.x.vec || !P.y.vec || (to && !P.to.vec);
+    auto kernel = forward_of(p->dtype, shape, to != nullptr, off ? kOff : whole(p->cols) ? kFull : kGeneral);
     int most = 0;
     st = kept::resident(kernel, threads, 0, &most);
     if (st != ASR_OK) return st;
@@ -857,8 +1027,8 @@ asr_status backward(const asr_norm_params *p, const void *dy, uint64_t dy_ld, co
         P.db = dbias != nullptr;
         const int shape = shape_of(p->cols);
         const unsigned threads = threads_of(p->cols);
-        const bool full = whole(p->cols) && P.dy.vec && (!dx || P.dx.vec) && (from ? P.from.vec : P.x.vec);
-        const Backward k = backward_of(p->dtype, from != nullptr, shape, threads, full);
+        const bool off = !P.dy.vec || (dx && !P.dx.vec) || !(from ? P.from.vec : P.x.vec);
+        const Backward k = backward_of(p->dtype, from != nullptr, shape, threads, off ? kOff : whole(p->cols) ? kFull : kGeneral);
         int most = 0;
         st = kept::resident(k.kernel, static_cast<int>(threads), k.smem, &most);
         if (st != ASR_OK) return st;
