@@ -86,15 +86,16 @@ template <int DT, bool GATED, int KEEP, bool FULL>
 __global__ void __launch_bounds__(kThreads, DT == ASR_F32 ? 2 : GATED && KEEP == 2 ? 3 : 4) forward_kernel(const __grid_constant__ Params P, uint32_t spans)
 {
     constexpr int kHalves = GATED ? 2 : 1;      // of x
+    __shared__ kept::Stage stages[FULL ? 1 : kThreads / 32];
+    kept::Stage &stage = stages[FULL ? 0 : threadIdx.x >> 5];
     const bool gelu = P.gelu;
     const uint32_t vec1 = half_vec(P.x.vec, P.cols), lane = (threadIdx.x & 31) * 16;
     kept::Pair<DT> next[kHalves];
     auto load = [&](const kept::Walk &k) {
-        const uint32_t col = k.span * kept::kSpan + lane;
-        const int live = FULL ? 16 : live_of(P.cols, col, 16);
         if (!k.more()) return;
-        next[0] = kept::fetch16<DT, FULL>(P.x, k.row, col, live, P.x.vec);
-        if (GATED) next[kHalves - 1] = kept::fetch16<DT, FULL>(P.x, k.row, P.cols + col, live, vec1);
+        const uint32_t col = k.span * kept::kSpan + lane;
+        next[0] = kept::fetch16<DT, FULL>(P.x, k.row, col, P.cols, P.x.vec, stage);
+        if (GATED) next[kHalves - 1] = kept::fetch16<DT, FULL>(P.x, k.row, P.cols + col, 2 * P.cols, vec1, stage);
     };
     kept::Walk k(P.rows, spans);
     load(k);
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, DT == ASR_F32 ? 2 : GATED && KEEP ==
                 if (GATED) y[h][i] = __fmul_rn(y[h][i], b[i]);
             }
         }
-        kept::store16<DT, FULL>(P.y, row, col, live, P.y.vec, y);
+        kept::store16<DT, FULL>(P.y, row, col, P.cols, P.y.vec, y, stage);
     }
 }
 
@@ -132,28 +133,32 @@ template <int DT, bool GATED, int KEPT, bool FULL>
 __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constant__ Params P, uint32_t spans)
 {
     constexpr int kHalves = GATED ? 2 : 1;
+    __shared__ kept::Stage stages[FULL ? 1 : kThreads / 32];
+    kept::Stage &stage = stages[FULL ? 0 : threadIdx.x >> 5];
     const bool gelu = P.gelu;
     const uint32_t in1 = half_vec(P.x.vec, P.cols), out1 = half_vec(P.dx.vec, P.cols), lane = (threadIdx.x & 31) * 16;
     kept::Pair<DT> raw[kHalves], grad;
     kept::Codes16 codes[kHalves];
+    kept::CodesAcross across;
     auto load = [&](const kept::Walk &k) {
         if (!k.more()) return;
         const uint32_t col = k.span * kept::kSpan + lane;
         const int live = FULL ? 16 : live_of(P.cols, col, 16);
 #pragma unroll
         for (int u = 0; u < kHalves; ++u) {
-            if (!KEPT) raw[u] = kept::fetch16<DT, FULL>(P.x, k.row, u * P.cols + col, live, u ? in1 : P.x.vec);
+            if (!KEPT) raw[u] = kept::fetch16<DT, FULL>(P.x, k.row, u * P.cols + col, (u + 1) * P.cols, u ? in1 : P.x.vec, stage);
             else if (KEPT == 1 || u == 0) codes[u] = kept::fetch_codes16<FULL>(P.from, k.row, u * P.cols + col, live);
+            else across = kept::fetch_across(P.from, k.row, P.cols + col, 2 * P.cols, stage);
         }
-        grad = kept::fetch16<DT, FULL>(P.dy, k.row, col, live, P.dy.vec);
+        grad = kept::fetch16<DT, FULL>(P.dy, k.row, col, P.cols, P.dy.vec, stage);
     };
     kept::Walk k(P.rows, spans);
     load(k);
     while (k.more()) {
         const uint32_t row = k.row, col = k.span * kept::kSpan + lane;
-        const int live = FULL ? 16 : live_of(P.cols, col, 16);
         kept::Pair<DT> x0[kHalves], g0 = grad;
         kept::Codes16 c0[kHalves];
+        const kept::CodesAcross across0 = across;
 #pragma unroll
         for (int u = 0; u < kHalves; ++u) {
             if (!KEPT) x0[u] = raw[u];
@@ -170,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
             for (int u = 0; u < kHalves; ++u) {
                 if (!KEPT) kept::values(x0[u].h[h], x[u]);
                 else if (KEPT == 1 || u == 0) kept::values(Codes{c0[u].h[h], c0[u].b}, x[u]);
-                else kept::values_across(P.from, row, P.cols + col + 8 * h, kept::half_of(live, h), x[u]);
+                else kept::values(across0, h, x[u]);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -183,35 +188,31 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
                 da[h][i] = __fmul_rn(da[h][i], df);
             }
         }
-        kept::store16<DT, FULL>(P.dx, row, col, live, P.dx.vec, da);
-        if (GATED) kept::store16<DT, FULL>(P.dx, row, P.cols + col, live, out1, db);
+        kept::store16<DT, FULL>(P.dx, row, col, P.cols, P.dx.vec, da, stage);
+        if (GATED) kept::store16<DT, FULL>(P.dx, row, P.cols + col, 2 * P.cols, out1, db, stage);
     }
 }
 
-// Rows off alignment.  Nothing is kept on the way where gated: that is a call of its own.
-template <int DT, bool GATED, int KEEP>
+// Rows off alignment, nothing kept.
+template <int DT, bool GATED>
 __global__ void __launch_bounds__(kThreads) forward_loose_kernel(const __grid_constant__ Params P, uint32_t spans)
 {
-    __shared__ __align__(16) kept::Halves halves;
     const bool gelu = P.gelu;
     for (kept::Walk k(P.rows, spans); k.more(); k.next()) {
         const uint32_t first = k.span * kept::kSpan;
         float a[kept::kLoose], b[kept::kLoose];
         kept::fetch_loose<DT>(P.x, k.row, first, P.cols, a);
         if (GATED) kept::fetch_loose<DT>(P.x, k.row, P.cols + first, 2 * P.cols, b);
-        if (KEEP) kept::keep_loose<KEEP == 2>(P.to, halves.v[threadIdx.x >> 5], k.row, first, P.cols, a);
 #pragma unroll
         for (int i = 0; i < kept::kLoose; ++i) {
-            const uint32_t col = first + 32 * i + (threadIdx.x & 31);
-            float y = value<DT>(a[i], gelu);
-            if (GATED) y = __fmul_rn(y, b[i]);
-            if (col < P.cols) kept::store1<DT>(P.y, k.row, col, y);
+            a[i] = value<DT>(a[i], gelu);
+            if (GATED) a[i] = __fmul_rn(a[i], b[i]);
+            kept::store_loose1<DT>(P.y, k.row, first, P.cols, i, a[i]);
         }
     }
 }
 
-// KEPT: from codes.
-template <int DT, bool GATED, bool KEPT>
+template <int DT, bool GATED>
 __global__ void __launch_bounds__(kThreads) backward_loose_kernel(const __grid_constant__ Params P, uint32_t spans)
 {
     const bool gelu = P.gelu;
@@ -219,20 +220,15 @@ __global__ void __launch_bounds__(kThreads) backward_loose_kernel(const __grid_c
         const uint32_t first = k.span * kept::kSpan;
         float a[kept::kLoose], b[kept::kLoose], g[kept::kLoose];
         kept::fetch_loose<DT>(P.dy, k.row, first, P.cols, g);
-        if (KEPT) kept::restore_loose<true>(P.from, k.row, first, P.cols, a);
-        else kept::fetch_loose<DT>(P.x, k.row, first, P.cols, a);
-        if (GATED && KEPT) kept::restore_loose<false>(P.from, k.row, P.cols + first, 2 * P.cols, b);
-        else if (GATED) kept::fetch_loose<DT>(P.x, k.row, P.cols + first, 2 * P.cols, b);
+        kept::fetch_loose<DT>(P.x, k.row, first, P.cols, a);
+        if (GATED) kept::fetch_loose<DT>(P.x, k.row, P.cols + first, 2 * P.cols, b);
 #pragma unroll
         for (int i = 0; i < kept::kLoose; ++i) {
-            const uint32_t col = first + 32 * i + (threadIdx.x & 31);
             float f, df;
             value_and_slope<DT>(a[i], gelu, f, df);
             if (GATED) df = __fmul_rn(df, b[i]);
-            if (col < P.cols) {
-                kept::store1<DT>(P.dx, k.row, col, __fmul_rn(g[i], df));
-                if (GATED) kept::store1<DT>(P.dx, k.row, P.cols + col, __fmul_rn(g[i], f));
-            }
+            kept::store_loose1<DT>(P.dx, k.row, first, P.cols, i, __fmul_rn(g[i], df));
+            if (GATED) kept::store_loose1<DT>(P.dx, k.row, P.cols + first, 2 * P.cols, i, __fmul_rn(g[i], f));
         }
     }
 }
@@ -248,19 +244,14 @@ Kernel forward_of(int keep)
                                                                  : forward_kernel<DT, GATED, 0, FULL>;
 }
 
-template <int DT>
-Kernel loose_forward_of(bool gated, int keep)
-{
-    if (gated) return forward_loose_kernel<DT, true, 0>;
-    return keep == 2 ? forward_loose_kernel<DT, false, 2> : keep ? forward_loose_kernel<DT, false, 1>
-                                                                 : forward_loose_kernel<DT, false, 0>;
-}
-
-enum { kGeneral = 0, kFull = 1, kOff = 2 };     // how rows lie
+enum { kGeneral = 0, kFull = 1, kOff = 2 };     // how rows lie: whole and aligned, or off alignment
 
 Kernel forward_of(int32_t dtype, bool gated, int keep, int how)
 {
-    if (how == kOff) return dtype == ASR_BF16 ? loose_forward_of<ASR_BF16>(gated, keep) : loose_forward_of<ASR_F32>(gated, keep);
+    if (how == kOff && !keep) {
+        if (dtype == ASR_BF16) return gated ? forward_loose_kernel<ASR_BF16, true> : forward_loose_kernel<ASR_BF16, false>;
+        return gated ? forward_loose_kernel<ASR_F32, true> : forward_loose_kernel<ASR_F32, false>;
+    }
     if (dtype != ASR_BF16) return gated ? forward_of<ASR_F32, true, false>(keep) : forward_of<ASR_F32, false, false>(keep);
     if (how == kFull) return gated ? forward_of<ASR_BF16, true, true>(keep) : forward_of<ASR_BF16, false, true>(keep);
     return gated ? forward_of<ASR_BF16, true, false>(keep) : forward_of<ASR_BF16, false, false>(keep);
@@ -274,16 +265,12 @@ Kernel backward_of(bool gated, int codes)
     return codes ? backward_kernel<DT, true, 1, FULL> : backward_kernel<DT, true, 0, FULL>;
 }
 
-template <int DT>
-Kernel loose_backward_of(bool gated, int codes)
-{
-    if (gated) return codes ? backward_loose_kernel<DT, true, true> : backward_loose_kernel<DT, true, false>;
-    return codes ? backward_loose_kernel<DT, false, true> : backward_loose_kernel<DT, false, false>;
-}
-
 Kernel backward_of(int32_t dtype, bool gated, int codes, int how)
 {
-    if (how == kOff) return dtype == ASR_BF16 ? loose_backward_of<ASR_BF16>(gated, codes) : loose_backward_of<ASR_F32>(gated, codes);
+    if (how == kOff && !codes) {
+        if (dtype == ASR_BF16) return gated ? backward_loose_kernel<ASR_BF16, true> : backward_loose_kernel<ASR_BF16, false>;
+        return gated ? backward_loose_kernel<ASR_F32, true> : backward_loose_kernel<ASR_F32, false>;
+    }
     if (dtype != ASR_BF16) return backward_of<ASR_F32, false>(gated, codes);
     return how == kFull ? backward_of<ASR_BF16, true>(gated, codes) : backward_of<ASR_BF16, false>(gated, codes);
 }
@@ -333,17 +320,16 @@ asr_status forward(const void *x, uint64_t x_ld, void *y, uint64_t y_ld, int32_t
     P.rows = static_cast<uint32_t>(rows);
     P.cols = static_cast<uint32_t>(cols);
     P.gelu = function == ASR_GELU;
-    int keep = 0, how = cols % kept::kSpan == 0 && P.x.vec == 2 && P.y.vec == 2 ? kFull : kGeneral;
-    if (!P.x.vec || !P.y.vec || (gated && cols % 8 != 0)) how = kOff;
-    if (to) P.to = kept::store(*to, width);
     // the kernel's lanes hold whole groups of both halves where they begin with the halves
-    const bool apart = to && gated && (cols % kept::kGroup != 0 || how == kOff || !P.to.vec);
+    const bool apart = to && gated && cols % kept::kGroup != 0;
+    int keep = 0;
     if (to && !apart) {
+        P.to = kept::store(*to, width);
         keep = to->rounding == ASR_ROUND_SR ? 2 : 1;
-        if (!P.to.vec) how = kOff;
-        else if (P.to.vec == 1 && how == kFull) how = kGeneral;
     }
-    st = kept::walk(ASR_KERNEL_ACTIVATION, forward_of(dtype, gated != 0, keep, how), P, rows, cols, kept::kSpan, stream);
+    const bool full = cols % kept::kSpan == 0 && P.x.vec == 2 && P.y.vec == 2 && (!keep || P.to.vec == 2);
+    const bool off = !P.x.vec || !P.y.vec || (gated && cols % 8 != 0);
+    st = kept::walk(ASR_KERNEL_ACTIVATION, forward_of(dtype, gated != 0, keep, full ? kFull : off ? kOff : kGeneral), P, rows, cols, kept::kSpan, stream);
     if (st == ASR_OK && apart) st = kept::pack(x, dtype, rows, width, x_ld, to, stream);
     return st;
 }
@@ -372,10 +358,9 @@ asr_status backward(const void *dy, uint64_t dy_ld, const void *x, uint64_t x_ld
     P.cols = static_cast<uint32_t>(cols);
     P.gelu = function == ASR_GELU;
     const int codes = !from ? 0 : gated && cols % kept::kGroup != 0 ? 2 : 1;
-    const uint32_t in = from ? P.from.vec : P.x.vec;
-    int how = cols % kept::kSpan == 0 && P.dy.vec == 2 && P.dx.vec == 2 && in == 2 ? kFull : kGeneral;
-    if (!P.dy.vec || !P.dx.vec || !in || (gated && cols % 8 != 0)) how = kOff;
-    return kept::walk(ASR_KERNEL_ACTIVATION, backward_of(dtype, gated != 0, codes, how), P, rows, cols, kept::kSpan, stream);
+    const bool full = cols % kept::kSpan == 0 && P.dy.vec == 2 && P.dx.vec == 2 && (from ? P.from.vec : P.x.vec) == 2;
+    const bool off = !P.dy.vec || !P.dx.vec || (!from && !P.x.vec) || (gated && cols % 8 != 0);
+    return kept::walk(ASR_KERNEL_ACTIVATION, backward_of(dtype, gated != 0, codes, full ? kFull : off ? kOff : kGeneral), P, rows, cols, kept::kSpan, stream);
 }
 
 }  // namespace act

@@ -128,7 +128,7 @@ __device__ __forceinline__ void values(const Raw<DT> &r, float x[8])
                              : (i & 1) ? bf16_hi(r.w[DT == ASR_F32 ? 0 : i >> 1]) : bf16_lo(r.w[DT == ASR_F32 ? 0 : i >> 1]);
 }
 
-// Sixteen values of a lane: two units side by side.
+// Sixteen values of a lane: two units side by side, of a warp 512 columns.
 template <int DT>
 struct Pair {
     Raw<DT> h[2];
@@ -136,11 +136,83 @@ struct Pair {
 
 __device__ __forceinline__ int half_of(int live, int h) { return live - 8 * h < 0 ? 0 : live - 8 * h < 8 ? live - 8 * h : 8; }
 
+// Rows that begin off alignment come and go value by value, a warp's side by side, and
+// change hands in shared memory: units of such rows, taken lane by lane, would touch
+// every sector once for each of its values (8,192 x 14,335 bf16: unpack 86 us, 679
+// lane by lane).
+struct Stage {
+    uint4 w[128];                               // a warp's 512 values
+};
+
+template <int DT>
+struct WordOf {
+    using type = uint32_t;
+};
+template <>
+struct WordOf<ASR_BF16> {
+    using type = uint16_t;
+};
+
+// COUNT values a lane, in the order of `place_of`: where value e of the warp lies, or
+// null where there is none.
+template <int DT, int COUNT, typename F>
+__device__ __forceinline__ void stage_in(Stage &S, F place_of)
+{
+    using Word = typename WordOf<DT>::type;
+    const uint32_t lane = threadIdx.x & 31;
+    Word v[COUNT];
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+        const Word *p = static_cast<const Word *>(place_of(32 * i + lane));
+        v[i] = p ? *p : static_cast<Word>(0);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) reinterpret_cast<Word *>(S.w)[32 * i + lane] = v[i];
+    __syncwarp();
+}
+
+template <int DT, int COUNT, typename F>
+__device__ __forceinline__ void stage_out(const Stage &S, F place_of)
+{
+    using Word = typename WordOf<DT>::type;
+    const uint32_t lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+        Word *p = static_cast<Word *>(place_of(32 * i + lane));
+        if (p) *p = reinterpret_cast<const Word *>(S.w)[32 * i + lane];
+    }
+    __syncwarp();
+}
+
+template <int DT>
+__device__ __forceinline__ Raw<DT> staged(const Stage &S, uint32_t unit)
+{
+    Raw<DT> r;
+#pragma unroll
+    for (int i = 0; i < (DT == ASR_BF16 ? 1 : 2); ++i) {
+        const uint4 v = S.w[unit * (DT == ASR_BF16 ? 1 : 2) + i];
+        r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
+    }
+    return r;
+}
+
+// A lane's sixteen from column `col` on, the row ending at `end`; all lanes of a warp together.
 template <int DT, bool FULL>
-__device__ __forceinline__ Pair<DT> fetch16(const Matrix &M, uint32_t row, uint32_t col, int live, uint32_t vec)
+__device__ __forceinline__ Pair<DT> fetch16(const Matrix &M, uint32_t row, uint32_t col, uint32_t end, uint32_t vec, Stage &S)
 {
     Pair<DT> p;
-    if (DT == ASR_BF16 && (FULL || (vec == 2 && live == 16))) {
+    const int live = FULL ? 16 : live_of(end, col, 16);
+    if (!FULL && vec == 0) {
+        const uint32_t first = col - (threadIdx.x & 31) * 16;
+        stage_in<DT, 16>(S, [&](uint32_t e) -> const void * {
+            return first + e < end ? static_cast<const char *>(M.p) + place(row, M.ld, first + e) * sizeof(typename WordOf<DT>::type)
+                                   : nullptr;
+        });
+#pragma unroll
+        for (int h = 0; h < 2; ++h) p.h[h] = staged<DT>(S, (threadIdx.x & 31) * 2 + h);
+    } else if (DT == ASR_BF16 && (FULL || (vec == 2 && live == 16))) {
         uint32_t w[8];
         load32(static_cast<const char *>(M.p) + place(row, M.ld, col) * 2, w);
 #pragma unroll
@@ -369,13 +441,43 @@ __device__ __forceinline__ void values(const Codes &c, float x[8])
     }
 }
 
-// Eight values from any column on, whose group may end among them.
-__device__ __forceinline__ void values_across(const Source &S, uint32_t row, uint32_t col, int live, float x[8])
+// Codes of a lane's sixteen values from any column `col` on, and the powers of the two
+// groups that they may lie in.
+struct CodesAcross {
+    uint4 v;
+    uint32_t b[2];
+    uint32_t left;                              // values in the first group
+};
+
+__device__ __forceinline__ CodesAcross fetch_across(const Source &S, uint32_t row, uint32_t col, uint32_t end, Stage &T)
 {
+    const uint32_t lane = threadIdx.x & 31, first = col - lane * 16;
+    const int8_t *q = S.q + place(row, S.q_ld, first + lane);
+    int8_t c[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        x[i] = i < live ? __fmul_rn(static_cast<float>(S.q[place(row, S.q_ld, col + i)]),
-                                    scale_of(S.power[place(row, S.power_ld, (col + i) >> 5)])) : 0.0f;
+    for (int i = 0; i < 16; ++i) c[i] = first + 32 * i + lane < end ? q[32 * i] : 0;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) reinterpret_cast<int8_t *>(T.w)[32 * i + lane] = c[i];
+    __syncwarp();
+    CodesAcross r;
+    r.v = T.w[lane];
+    r.left = 32 - col % 32;
+    r.b[0] = col < end ? S.power[place(row, S.power_ld, col >> 5)] : 0;
+    r.b[1] = col + r.left < end ? S.power[place(row, S.power_ld, (col >> 5) + 1)] : 0;
+    return r;
+}
+
+__device__ __forceinline__ void values(const CodesAcross &c, int half, float x[8])
+{
+    const float near = scale_of(c.b[0]), far = scale_of(c.b[1]);
+    const uint32_t w[4] = {c.v.x, c.v.y, c.v.z, c.v.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int k = 8 * half + i;
+        const float q = static_cast<float>(static_cast<int8_t>(w[k >> 2] >> (8 * (k & 3))));
+        x[i] = __fmul_rn(q, k < c.left ? near : far);
+    }
 }
 
 // Eight values out, `live` of them, to nearest where they are bf16.
@@ -413,17 +515,45 @@ __device__ __forceinline__ void store8(const Out &O, uint32_t row, uint32_t col,
     }
 }
 
-// Sixteen out.
-template <int DT, bool FULL>
-__device__ __forceinline__ void store16(const Out &O, uint32_t row, uint32_t col, int live, uint32_t vec, const float v[2][8])
+// Values as they are stored, to nearest where they are bf16.
+template <int DT>
+__device__ __forceinline__ Raw<DT> rounded(const float v[8])
 {
-    if (DT == ASR_BF16 && (FULL || (vec == 2 && live == 16))) {
-        uint32_t w[8];
+    Raw<DT> r;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[i >> 2][2 * (i & 3)], v[i >> 2][2 * (i & 3) + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&h);
-        }
+    for (int i = 0; i < (DT == ASR_BF16 ? 4 : 8); ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[DT == ASR_BF16 ? 2 * i : i], v[DT == ASR_BF16 ? 2 * i + 1 : i]);
+        r.w[i] = DT == ASR_BF16 ? *reinterpret_cast<const uint32_t *>(&h) : __float_as_uint(v[i]);
+    }
+    return r;
+}
+
+template <int DT>
+__device__ __forceinline__ void put_staged(Stage &S, uint32_t unit, const Raw<DT> &r)
+{
+#pragma unroll
+    for (int i = 0; i < (DT == ASR_BF16 ? 1 : 2); ++i)
+        S.w[unit * (DT == ASR_BF16 ? 1 : 2) + i] = make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
+}
+
+// Sixteen out, as they come in.
+template <int DT, bool FULL>
+__device__ __forceinline__ void store16(const Out &O, uint32_t row, uint32_t col, uint32_t end, uint32_t vec, const float v[2][8],
+                                        Stage &S)
+{
+    const int live = FULL ? 16 : live_of(end, col, 16);
+    if (!FULL && vec == 0) {
+        const uint32_t first = col - (threadIdx.x & 31) * 16;
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) put_staged<DT>(S, (threadIdx.x & 31) * 2 + h, rounded<DT>(v[h]));
+        stage_out<DT, 16>(S, [&](uint32_t e) -> void * {
+            return first + e < end ? static_cast<char *>(O.p) + place(row, O.ld, first + e) * sizeof(typename WordOf<DT>::type)
+                                   : nullptr;
+        });
+    } else if (DT == ASR_BF16 && (FULL || (vec == 2 && live == 16))) {
+        const Raw<DT> a = rounded<DT>(v[0]), b = rounded<DT>(v[1]);
+        const uint32_t w[8] = {a.w[0], a.w[1], a.w[2], a.w[3], b.w[0], b.w[1], b.w[2], b.w[3]};
         gemm::st_global_v8(static_cast<char *>(O.p) + place(row, O.ld, col) * 2, w);
     } else {
 #pragma unroll
@@ -431,111 +561,32 @@ __device__ __forceinline__ void store16(const Out &O, uint32_t row, uint32_t col
     }
 }
 
-// ---- rows that begin off alignment
-//
-// A lane's sixteen values then lie 32 columns apart, the warp's side by side: every
-// access is of single values but of whole sectors, where units at any address would
-// take each sector several times (8,192 x 14,335: the gated activation's backward pass
-// @@A@@ us, 1,270 by units).  A group is a warp's values of one place.
-
+// Where every value goes its own way, rows off alignment need no such exchange: a lane
+// takes every 32nd of a span, and stores each as soon as it has it (8,192 x 14,335 bf16:
+// the gated activation 153 us, its backward pass 336, exchanged 256 and 423; the backward
+// pass with all of da stored before all of db 654).
 constexpr int kLoose = 16;
 
 template <int DT>
-__device__ __forceinline__ float load1(const Matrix &M, uint32_t row, uint32_t col)
-{
-    if (DT == ASR_F32) return static_cast<const float *>(M.p)[place(row, M.ld, col)];
-    return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(M.p)[place(row, M.ld, col)]) << 16);
-}
-
-template <int DT>
-__device__ __forceinline__ void store1(const Out &O, uint32_t row, uint32_t col, float v)
-{
-    if (DT == ASR_F32) static_cast<float *>(O.p)[place(row, O.ld, col)] = v;
-    else static_cast<__nv_bfloat16 *>(O.p)[place(row, O.ld, col)] = __float2bfloat16_rn(v);
-}
-
-// The values of columns first + 32 i + lane of a row.
-template <int DT>
 __device__ __forceinline__ void fetch_loose(const Matrix &M, uint32_t row, uint32_t first, uint32_t end, float x[kLoose])
 {
+    const char *p = static_cast<const char *>(M.p) + place(row, M.ld, first + (threadIdx.x & 31)) * (DT == ASR_BF16 ? 2 : 4);
 #pragma unroll
     for (int i = 0; i < kLoose; ++i) {
-        const uint32_t col = first + 32 * i + (threadIdx.x & 31);
-        x[i] = col < end ? load1<DT>(M, row, col) : 0.0f;
+        x[i] = 0.0f;
+        if (first + 32 * i + (threadIdx.x & 31) < end)
+            x[i] = DT == ASR_F32 ? reinterpret_cast<const float *>(p)[32 * i] : bf16_lo(reinterpret_cast<const uint16_t *>(p)[32 * i]);
     }
 }
 
-// A warp's random numbers: the outputs of 64 counters, whose halves in order are those
-// of its 512 values.  Counter k of them is base(k / 4) + k % 4.
-struct Halves {
-    uint16_t v[kThreads / 32][512];
-};
-
-template <typename F>
-__device__ __forceinline__ void draw_halves(const Store &S, uint16_t *to, F base)
+// The i-th of them.
+template <int DT>
+__device__ __forceinline__ void store_loose1(const Out &O, uint32_t row, uint32_t first, uint32_t end, int i, float x)
 {
-    const uint32_t lane = threadIdx.x & 31;
-    __syncwarp();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint64_t at = base(8 * h + (lane >> 2)) + (lane & 3);
-        uint32_t w[4];
-        philox4x32_10(static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32), S.step, kStream, S.keys, w);
-        reinterpret_cast<uint4 *>(to)[32 * h + lane] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    __syncwarp();
-}
-
-// A code (its low byte) of one value, from its half.
-template <bool SR>
-__device__ __forceinline__ uint32_t code1(float x, float up, uint32_t half)
-{
-    if (SR) return __float_as_uint(__fadd_ru(__fmaf_ru(x, up, -__uint_as_float(0x43000000u | half)), 12583040.0f));
-    return __float_as_uint(__fmaf_rn(x, up, 12582912.0f));
-}
-
-// Power of the group that a warp holds a value of each of.
-__device__ __forceinline__ uint32_t warp_power(float x)
-{
-    return power_of(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x) & 0x7FFFFFFFu));
-}
-
-// Keeps a lane's sixteen values of a span that begins at column `first`, a multiple of 512.
-template <bool SR>
-__device__ __forceinline__ void keep_loose(const Store &S, uint16_t *halves, uint32_t row, uint32_t first, uint32_t cols,
-                                           const float x[kLoose])
-{
-    const uint32_t lane = threadIdx.x & 31;
-    if (SR) draw_halves(S, halves, [&](uint32_t g) { return S.base + place(row, S.across, first / 8 + 4 * g); });
-    uint32_t power = 0;
-#pragma unroll
-    for (int i = 0; i < kLoose; ++i) {
-        const uint32_t b = warp_power(x[i]), col = first + 32 * i + lane;
-        if (lane == i) power = b;
-        const uint32_t c = code1<SR>(x[i], __uint_as_float((254u - b) << 23), SR ? halves[32 * i + lane] : 0);
-        if (col < cols) S.q[place(row, S.q_ld, col)] = static_cast<int8_t>(b == 255u ? 0 : c);
-    }
-    if (lane < kLoose && first + 32 * lane < cols)
-        S.power[place(row, S.power_ld, first / 32 + lane)] = static_cast<uint8_t>(power);
-}
-
-__device__ __forceinline__ float value1(int8_t q, float scale) { return __fmul_rn(static_cast<float>(q), scale); }
-
-// The values that a span's codes stand for, as they lie (ALIGNED: groups begin with
-// the warp's values, else anywhere).
-template <bool ALIGNED>
-__device__ __forceinline__ void restore_loose(const Source &S, uint32_t row, uint32_t first, uint32_t end, float x[kLoose])
-{
-    const uint32_t lane = threadIdx.x & 31;
-    float mine = 0.0f;
-    if (ALIGNED && lane < kLoose && first + 32 * lane < end) mine = scale_of(S.power[place(row, S.power_ld, first / 32 + lane)]);
-#pragma unroll
-    for (int i = 0; i < kLoose; ++i) {
-        const uint32_t col = first + 32 * i + lane;
-        float scale = ALIGNED ? __shfl_sync(0xFFFFFFFFu, mine, i) : 0.0f;
-        if (!ALIGNED && col < end) scale = scale_of(S.power[place(row, S.power_ld, col >> 5)]);
-        x[i] = col < end ? value1(S.q[place(row, S.q_ld, col)], scale) : 0.0f;
-    }
+    const uint32_t col = first + 32 * i + (threadIdx.x & 31);
+    if (col >= end) return;
+    if (DT == ASR_F32) static_cast<float *>(O.p)[place(row, O.ld, col)] = x;
+    else static_cast<__nv_bfloat16 *>(O.p)[place(row, O.ld, col)] = __float2bfloat16_rn(x);
 }
 
 struct PackParams {
@@ -548,11 +599,12 @@ struct PackParams {
 template <bool SR, int DT, bool FULL>
 __global__ void __launch_bounds__(kThreads) pack_kernel(const __grid_constant__ PackParams P, uint32_t spans)
 {
+    __shared__ Stage stages[FULL ? 1 : kThreads / 32];
+    Stage &stage = stages[FULL ? 0 : threadIdx.x >> 5];
     const uint32_t at = (threadIdx.x & 31) * 16;
     Pair<DT> next;
     auto load = [&](const Walk &k) {
-        const uint32_t col = k.span * kSpan + at;
-        if (k.more()) next = fetch16<DT, FULL>(P.x, k.row, col, FULL ? 16 : live_of(P.cols, col, 16), P.x.vec);
+        if (k.more()) next = fetch16<DT, FULL>(P.x, k.row, k.span * kSpan + at, P.cols, P.x.vec, stage);
     };
     Walk k(P.rows, spans);
     load(k);
@@ -574,6 +626,8 @@ struct UnpackParams {
 template <int DT, bool FULL>
 __global__ void __launch_bounds__(kThreads) unpack_kernel(const __grid_constant__ UnpackParams P, uint32_t spans)
 {
+    __shared__ Stage stages[FULL ? 1 : kThreads / 32];
+    Stage &stage = stages[FULL ? 0 : threadIdx.x >> 5];
     const uint32_t at = (threadIdx.x & 31) * 16;
     Codes16 next;
     auto load = [&](const Walk &k) {
@@ -590,32 +644,7 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const __grid_constant_
         float v[2][8];
 #pragma unroll
         for (int h = 0; h < 2; ++h) values(Codes{c.h[h], c.b}, v[h]);
-        store16<DT, FULL>(P.out, row, col, FULL ? 16 : live_of(P.cols, col, 16), P.out.vec, v);
-    }
-}
-
-template <bool SR, int DT>
-__global__ void __launch_bounds__(kThreads) pack_loose_kernel(const __grid_constant__ PackParams P, uint32_t spans)
-{
-    __shared__ __align__(16) Halves halves;
-    for (Walk k(P.rows, spans); k.more(); k.next()) {
-        float x[kLoose];
-        fetch_loose<DT>(P.x, k.row, k.span * kSpan, P.cols, x);
-        keep_loose<SR>(P.to, halves.v[threadIdx.x >> 5], k.row, k.span * kSpan, P.cols, x);
-    }
-}
-
-template <int DT>
-__global__ void __launch_bounds__(kThreads) unpack_loose_kernel(const __grid_constant__ UnpackParams P, uint32_t spans)
-{
-    for (Walk k(P.rows, spans); k.more(); k.next()) {
-        float x[kLoose];
-        restore_loose<true>(P.from, k.row, k.span * kSpan, P.cols, x);
-#pragma unroll
-        for (int i = 0; i < kLoose; ++i) {
-            const uint32_t col = k.span * kSpan + 32 * i + (threadIdx.x & 31);
-            if (col < P.cols) store1<DT>(P.out, k.row, col, x[i]);
-        }
+        store16<DT, FULL>(P.out, row, col, P.cols, P.out.vec, v, stage);
     }
 }
 
@@ -706,7 +735,8 @@ asr_status load_once(std::atomic<uint64_t> &ready, K... kernels)
     return ASR_OK;
 }
 
-// How many blocks of a kernel the current device holds at once.
+// How many blocks of a kernel the current device holds at once.  A kernel and its
+// threads settle its shared memory, if it has any in this call.
 template <typename K>
 asr_status resident(K kernel, int threads, size_t smem, int *blocks)
 {
@@ -714,7 +744,7 @@ asr_status resident(K kernel, int threads, size_t smem, int *blocks)
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
     const uint64_t key = (static_cast<uint64_t>(dev) << 48) ^ reinterpret_cast<uintptr_t>(kernel) ^
-                         (static_cast<uint64_t>(threads / 32) << 54);
+                         (static_cast<uint64_t>(threads / 32) << 54) ^ (static_cast<uint64_t>(smem != 0) << 60);
     std::lock_guard<std::mutex> lk(g_grid_mu);
     auto it = g_grid_cache.find(key);
     if (it != g_grid_cache.end()) {
@@ -748,9 +778,7 @@ asr_status setup()
     return load_once(ready, pack_kernel<false, ASR_F32, false>, pack_kernel<false, ASR_BF16, false>,
                      pack_kernel<false, ASR_BF16, true>, pack_kernel<true, ASR_F32, false>,
                      pack_kernel<true, ASR_BF16, false>, pack_kernel<true, ASR_BF16, true>, unpack_kernel<ASR_F32, false>,
-                     unpack_kernel<ASR_BF16, false>, unpack_kernel<ASR_BF16, true>, pack_loose_kernel<false, ASR_F32>,
-                     pack_loose_kernel<false, ASR_BF16>, pack_loose_kernel<true, ASR_F32>, pack_loose_kernel<true, ASR_BF16>,
-                     unpack_loose_kernel<ASR_F32>, unpack_loose_kernel<ASR_BF16>);
+                     unpack_kernel<ASR_BF16, false>, unpack_kernel<ASR_BF16, true>);
 }
 
 asr_status pack(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, uint64_t x_ld, const asr_checkpoint *to,
@@ -774,9 +802,6 @@ asr_status pack(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, uint
     if (dtype == ASR_BF16)
         kernel = full ? (sr ? pack_kernel<true, ASR_BF16, true> : pack_kernel<false, ASR_BF16, true>)
                       : (sr ? pack_kernel<true, ASR_BF16, false> : pack_kernel<false, ASR_BF16, false>);
-    if (!P.x.vec || !P.to.vec)
-        kernel = dtype == ASR_BF16 ? (sr ? pack_loose_kernel<true, ASR_BF16> : pack_loose_kernel<false, ASR_BF16>)
-                                   : (sr ? pack_loose_kernel<true, ASR_F32> : pack_loose_kernel<false, ASR_F32>);
     return walk(ASR_KERNEL_CHECKPOINT, kernel, P, rows, cols, kSpan, stream);
 }
 
@@ -798,7 +823,6 @@ asr_status unpack(const asr_checkpoint *from, uint64_t rows, uint64_t cols, void
     const bool full = cols % kSpan == 0 && P.from.vec == 2 && P.out.vec == 2;
     auto kernel = dtype != ASR_BF16 ? unpack_kernel<ASR_F32, false> : full ? unpack_kernel<ASR_BF16, true>
                                                                            : unpack_kernel<ASR_BF16, false>;
-    if (!P.from.vec || !P.out.vec) kernel = dtype == ASR_BF16 ? unpack_loose_kernel<ASR_BF16> : unpack_loose_kernel<ASR_F32>;
     return walk(ASR_KERNEL_CHECKPOINT, kernel, P, rows, cols, kSpan, stream);
 }
 

@@ -74,11 +74,11 @@ struct LookupParams {
 template <int DT>
 __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant__ LookupParams P, uint32_t spans)
 {
+    __shared__ kept::Stage stage;               // rows are aligned: not used
     const uint32_t lane = (threadIdx.x & 31) * 16;
     for (kept::Walk k(static_cast<uint32_t>(P.ids.n), spans); k.more(); k.next()) {
         const uint32_t id = key_of(P.ids, k.row), col = k.span * kept::kSpan + lane;
-        const int live = live_of(P.dim, col, 16);
-        const kept::Pair<DT> raw = kept::fetch16<DT, false>(P.table, id, col, id < P.ids.vocab ? live : 0, P.table.vec);
+        const kept::Pair<DT> raw = kept::fetch16<DT, false>(P.table, id, col, id < P.ids.vocab ? P.dim : 0, P.table.vec, stage);
         float v[2][8];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -87,10 +87,11 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant_
             for (int i = 0; i < 8; ++i)
                 v[h][i] = id < P.ids.vocab ? __fmul_rn(v[h][i], P.scale) : __uint_as_float(0x7FC00000u);
         }
-        kept::store16<DT, false>(P.y, k.row, col, live, P.y.vec, v);
+        kept::store16<DT, false>(P.y, k.row, col, P.dim, P.y.vec, v, stage);
     }
 }
 
+// Rows off alignment.
 template <int DT>
 __global__ void __launch_bounds__(kThreads) lookup_loose_kernel(const __grid_constant__ LookupParams P, uint32_t spans)
 {
@@ -99,11 +100,8 @@ __global__ void __launch_bounds__(kThreads) lookup_loose_kernel(const __grid_con
         float x[kept::kLoose];
         kept::fetch_loose<DT>(P.table, id, first, id < P.ids.vocab ? P.dim : 0, x);
 #pragma unroll
-        for (int i = 0; i < kept::kLoose; ++i) {
-            const uint32_t col = first + 32 * i + (threadIdx.x & 31);
-            const float v = id < P.ids.vocab ? __fmul_rn(x[i], P.scale) : __uint_as_float(0x7FC00000u);
-            if (col < P.dim) kept::store1<DT>(P.y, k.row, col, v);
-        }
+        for (int i = 0; i < kept::kLoose; ++i)
+            kept::store_loose1<DT>(P.y, k.row, first, P.dim, i, id < P.ids.vocab ? __fmul_rn(x[i], P.scale) : __uint_as_float(0x7FC00000u));
     }
 }
 
@@ -435,60 +433,46 @@ struct SumParams {
     ZeroParams zero;
 };
 
-// Eight of a row's columns: side by side from `col` on, `live` of them, or, LOOSE (rows
-// off alignment), at `col` and every blockDim.x-th behind it.
-template <int OT, bool LOOSE>
-__device__ __forceinline__ void store_row(const SumParams &P, uint32_t row, uint32_t col, int live, float v[8])
+// A warp's 256 columns of a row, eight a lane from `col` on.  OFF: rows off alignment.
+template <int OT, bool OFF>
+__device__ __forceinline__ void store_row(const SumParams &P, uint32_t row, uint32_t col, int live, float v[8], kept::Stage &S)
 {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], P.scale);
-    if (LOOSE) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (col + i * blockDim.x < P.dim) kept::store1<OT>(P.out, row, col + i * blockDim.x, v[i]);
+    if (OFF) {
+        const uint32_t lane = threadIdx.x & 31, first = col - lane * 8;
+        __syncwarp();
+        kept::put_staged<OT>(S, lane, kept::rounded<OT>(v));
+        kept::stage_out<OT, 8>(S, [&](uint32_t e) -> void * {
+            return first + e < P.dim ? static_cast<char *>(P.out.p) + kept::place(row, P.out.ld, first + e) * (OT == ASR_BF16 ? 2 : 4)
+                                     : nullptr;
+        });
     } else {
         kept::store8<OT>(P.out, row, col, live, P.out.vec, v);
     }
 }
 
-// A row of sums in the workspace, of chunk c, whose columns lie as store_row's.
-template <bool LOOSE>
-__device__ __forceinline__ void store_sum(float *sums, const SumParams &P, uint32_t c, uint32_t col, const float v[8])
+__device__ __forceinline__ void store_sum(float *p, const float v[8])
 {
-    float *p = sums + c * P.pitch + col;
-    if (LOOSE) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (col + i * blockDim.x < P.dim) __stcg(p + i * blockDim.x, v[i]);
-    } else {
-        __stcg(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
-        __stcg(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
-    }
+    __stcg(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
+    __stcg(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
 }
 
-template <bool LOOSE>
-__device__ __forceinline__ void add_sum(float acc[8], const float *sums, const SumParams &P, uint32_t c, uint32_t col)
+__device__ __forceinline__ void add_sum(float acc[8], const float *p)
 {
-    const float *p = sums + c * P.pitch + col;
-    if (LOOSE) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (col + i * blockDim.x < P.dim) acc[i] = __fadd_rn(acc[i], __ldcg(p + i * blockDim.x));
-    } else {
-        const float4 a = __ldcg(reinterpret_cast<const float4 *>(p)), b = __ldcg(reinterpret_cast<const float4 *>(p) + 1);
-        acc[0] = __fadd_rn(acc[0], a.x), acc[1] = __fadd_rn(acc[1], a.y), acc[2] = __fadd_rn(acc[2], a.z);
-        acc[3] = __fadd_rn(acc[3], a.w), acc[4] = __fadd_rn(acc[4], b.x), acc[5] = __fadd_rn(acc[5], b.y);
-        acc[6] = __fadd_rn(acc[6], b.z), acc[7] = __fadd_rn(acc[7], b.w);
-    }
+    const float4 a = __ldcg(reinterpret_cast<const float4 *>(p)), b = __ldcg(reinterpret_cast<const float4 *>(p) + 1);
+    acc[0] = __fadd_rn(acc[0], a.x), acc[1] = __fadd_rn(acc[1], a.y), acc[2] = __fadd_rn(acc[2], a.z);
+    acc[3] = __fadd_rn(acc[3], a.w), acc[4] = __fadd_rn(acc[4], b.x), acc[5] = __fadd_rn(acc[5], b.y);
+    acc[6] = __fadd_rn(acc[6], b.z), acc[7] = __fadd_rn(acc[7], b.w);
 }
 
 // Block c has left its sum of `row`, which reaches over chunks' ends (`began`: from
 // before this one).  The last one to do so adds them all up: of the chunk where the row
 // begins its tail, of the others their heads, in order.  All threads of the block come
 // here together.
-template <int OT, bool LOOSE>
+template <int OT, bool OFF>
 __device__ __forceinline__ void join(const SumParams &P, uint32_t c, uint32_t row, bool began, uint32_t slice, uint32_t col,
-                                     int live)
+                                     int live, kept::Stage &S)
 {
     __shared__ uint32_t ends[2], before;
     __threadfence();                            // what this thread has left, before its block is counted
@@ -515,12 +499,14 @@ __device__ __forceinline__ void join(const SumParams &P, uint32_t c, uint32_t ro
     }
     __syncthreads();
     const uint32_t first = ends[0], last = ends[1];
-    if (before != last - first || live == 0) return;
+    if (before != last - first) return;
     float acc[8] = {};
-    add_sum<LOOSE>(acc, P.tail, P, first, col);
-#pragma unroll(LOOSE ? 1 : 8)
-    for (uint32_t d = first + 1; d <= last; ++d) add_sum<LOOSE>(acc, P.head, P, d, col);
-    store_row<OT, LOOSE>(P, row, col, live, acc);
+    if (live) {
+        add_sum(acc, P.tail + first * P.pitch + col);
+#pragma unroll 8
+        for (uint32_t d = first + 1; d <= last; ++d) add_sum(acc, P.head + d * P.pitch + col);
+    }
+    store_row<OT, OFF>(P, row, col, live, acc, S);
 }
 
 // A block a chunk and a slice of the columns, eight a thread; the blocks behind those
@@ -528,10 +514,12 @@ __device__ __forceinline__ void join(const SumParams &P, uint32_t c, uint32_t ro
 constexpr int kSumThreads = 128;                // at most
 constexpr int kPiece = 64;                      // tokens whose keys are at hand
 
-template <int DT, int OT, bool LOOSE>
-__global__ void __launch_bounds__(kSumThreads, LOOSE ? 4 : 6) sum_kernel(const __grid_constant__ SumParams P)
+template <int DT, int OT, bool OFF>
+__global__ void __launch_bounds__(kSumThreads, OFF ? 4 : 6) sum_kernel(const __grid_constant__ SumParams P)
 {
-    constexpr int kAhead = LOOSE ? 2 : DT == ASR_BF16 ? 8 : 4;      // rows fetched before they are added up
+    constexpr int kAhead = DT == ASR_BF16 && !OFF ? 8 : 4;          // rows fetched before they are added up
+    __shared__ kept::Stage stages[OFF ? kSumThreads / 32 : 1];
+    kept::Stage &stage = stages[OFF ? threadIdx.x >> 5 : 0];
     __shared__ uint32_t key[kPiece + 2], order[kPiece];     // keys from the one before on
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t sums = P.chunks * P.slices;
@@ -557,7 +545,7 @@ __global__ void __launch_bounds__(kSumThreads, LOOSE ? 4 : 6) sum_kernel(const _
         return;
     }
     const uint32_t c = blockIdx.x / P.slices, slice = blockIdx.x % P.slices;
-    const uint32_t col = LOOSE ? slice * blockDim.x * 8 + threadIdx.x : (slice * blockDim.x + threadIdx.x) * 8;
+    const uint32_t col = (slice * blockDim.x + threadIdx.x) * 8, warp_col = col - (threadIdx.x & 31) * 8;
     const int live = live_of(static_cast<uint32_t>(P.dim), col);
     const uint64_t begin = static_cast<uint64_t>(c) * P.chunk, end = begin + P.chunk < P.n ? begin + P.chunk : P.n;
     float acc[8] = {};
@@ -582,16 +570,32 @@ __global__ void __launch_bounds__(kSumThreads, LOOSE ? 4 : 6) sum_kernel(const _
         goes_on = i0 + n < P.n && keys[n] == back;
         for (uint32_t a0 = 0; a0 < n && keys[a0] < P.vocab; a0 += kAhead) {
             kept::Raw<DT> raw[kAhead];
-            float loose[kAhead][8];
+            if (OFF) {
+                // all rows' values side by side first, then each in turn through shared memory
+                using Word = typename kept::WordOf<DT>::type;
+                Word v[kAhead][8];
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                const bool in = a0 + a < n && keys[a0 + a] < P.vocab;
-                if (LOOSE) {
+                for (int a = 0; a < kAhead; ++a) {
+                    const bool in = a0 + a < n && keys[a0 + a] < P.vocab;
+                    const Word *from = static_cast<const Word *>(P.dy.p) + kept::place(in ? order[a0 + a] : 0, P.dy.ld, warp_col);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        loose[a][i] = in && col + i * blockDim.x < P.dim
-                                          ? kept::load1<DT>(P.dy, order[a0 + a], col + i * blockDim.x) : 0.0f;
-                } else {
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t e = 32 * i + (threadIdx.x & 31);
+                        v[a][i] = in && warp_col + e < P.dim ? from[e] : static_cast<Word>(0);
+                    }
+                }
+#pragma unroll
+                for (int a = 0; a < kAhead; ++a) {
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) reinterpret_cast<Word *>(stage.w)[32 * i + (threadIdx.x & 31)] = v[a][i];
+                    __syncwarp();
+                    raw[a] = kept::staged<DT>(stage, threadIdx.x & 31);
+                }
+            } else {
+#pragma unroll
+                for (int a = 0; a < kAhead; ++a) {
+                    const bool in = a0 + a < n && keys[a0 + a] < P.vocab;
                     raw[a] = kept::fetch<DT>(P.dy, in ? order[a0 + a] : 0, col, in ? live : 0, P.dy.vec);
                 }
             }
@@ -599,17 +603,17 @@ __global__ void __launch_bounds__(kSumThreads, LOOSE ? 4 : 6) sum_kernel(const _
             for (int a = 0; a < kAhead; ++a) {
                 if (a0 + a >= n || keys[a0 + a] >= P.vocab) break;
                 float v[8];
-                if (!LOOSE) kept::values(raw[a], v);
+                kept::values(raw[a], v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], LOOSE ? loose[a][i] : v[i]);
+                for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], v[i]);
                 const bool last = i0 + a0 + a + 1 == end;
                 if (!last && keys[a0 + a + 1] == keys[a0 + a]) continue;
                 if (first && began) {
-                    if (live) store_sum<LOOSE>(P.head, P, c, col, acc);
+                    if (live) store_sum(P.head + c * P.pitch + col, acc);
                 } else if (last && goes_on) {
-                    if (live) store_sum<LOOSE>(P.tail, P, c, col, acc);
+                    if (live) store_sum(P.tail + c * P.pitch + col, acc);
                 } else {
-                    store_row<OT, LOOSE>(P, keys[a0 + a], col, live, acc);
+                    store_row<OT, OFF>(P, keys[a0 + a], col, live, acc, stage);
                 }
                 first = false;
 #pragma unroll
@@ -618,8 +622,8 @@ __global__ void __launch_bounds__(kSumThreads, LOOSE ? 4 : 6) sum_kernel(const _
         }
     }
     // the chunk's first row, if it began before, and its last, if that goes on and is not the same
-    if (began && front < P.vocab) join<OT, LOOSE>(P, c, front, true, slice, col, live);
-    if (goes_on && back < P.vocab && !(began && front == back)) join<OT, LOOSE>(P, c, back, false, slice, col, live);
+    if (began && front < P.vocab) join<OT, OFF>(P, c, front, true, slice, col, live, stage);
+    if (goes_on && back < P.vocab && !(began && front == back)) join<OT, OFF>(P, c, back, false, slice, col, live, stage);
 }
 
 // ------------------------------------------------------------------ host
@@ -641,15 +645,15 @@ Ids ids_of(const void *ids, int32_t index, uint64_t tokens, uint64_t vocab, int6
 
 using SumKernel = void (*)(const SumParams);
 
-template <int DT, bool LOOSE>
+template <int DT, bool OFF>
 SumKernel sums_of(int32_t out)
 {
-    return out == ASR_BF16 ? sum_kernel<DT, ASR_BF16, LOOSE> : sum_kernel<DT, ASR_F32, LOOSE>;
+    return out == ASR_BF16 ? sum_kernel<DT, ASR_BF16, OFF> : sum_kernel<DT, ASR_F32, OFF>;
 }
 
-SumKernel sums_of(int32_t dy, int32_t out, bool loose)
+SumKernel sums_of(int32_t dy, int32_t out, bool off)
 {
-    if (loose) return dy == ASR_BF16 ? sums_of<ASR_BF16, true>(out) : sums_of<ASR_F32, true>(out);
+    if (off) return dy == ASR_BF16 ? sums_of<ASR_BF16, true>(out) : sums_of<ASR_F32, true>(out);
     return dy == ASR_BF16 ? sums_of<ASR_BF16, false>(out) : sums_of<ASR_F32, false>(out);
 }
 
@@ -682,7 +686,7 @@ asr_status lookup(const void *ids, int32_t index, uint64_t tokens, const void *t
     P.dim = static_cast<uint32_t>(dim);
     P.scale = static_cast<float>(scale);
     auto kernel = dtype == ASR_BF16 ? lookup_kernel<ASR_BF16> : lookup_kernel<ASR_F32>;
-    if ((vocab && !P.table.vec) || !P.y.vec) kernel = dtype == ASR_BF16 ? lookup_loose_kernel<ASR_BF16> : lookup_loose_kernel<ASR_F32>;
+    if (!P.table.vec || !P.y.vec) kernel = dtype == ASR_BF16 ? lookup_loose_kernel<ASR_BF16> : lookup_loose_kernel<ASR_F32>;
     return kept::walk(ASR_KERNEL_EMBEDDING, kernel, P, tokens, dim, kept::kSpan, stream);
 }
 

@@ -103,11 +103,27 @@ struct Place {
             live[u] = FULL ? 8 : live_of(P.cols, col[u]);
         }
     }
+    // where value e of the warp's 256 of unit u lies in a matrix, null where there is none; `first`: the warp's first row
+    template <int DT, typename T>
+    __device__ T *value(const Params &P, T *matrix, uint32_t ld, int u, uint32_t first, uint32_t e) const
+    {
+        using Char = typename std::conditional<std::is_const<T>::value, const char, char>::type;
+        const uint32_t lane = e >> 3, lanes = WARP ? P.lanes : 32, r = WARP ? first + lane / lanes : first;
+        const uint32_t c = col[u] - at8() + lane % lanes * 8 + (e & 7);
+        return r < P.rows && c < P.cols ? static_cast<Char *>(matrix) + kept::place(r, ld, c) * (DT == ASR_BF16 ? 2 : 4) : nullptr;
+    }
+    // the caller's place among its warp's columns of a row
+    __device__ uint32_t at8() const { return (WARP ? at : at & 31) * 8; }
     __device__ uint32_t row() const { return base + sub; }
     __device__ int of(int u, uint32_t row, uint32_t rows) const
     {
         return FULL && !WARP ? 8 : row < rows ? live[u] : 0;
     }
+};
+
+// For rows off alignment: a warp's 256 values (the first half of a kept::Stage).
+struct __align__(16) HalfStage {
+    uint4 w[64];
 };
 
 // Sums of a block's warps: `part` holds theirs, `turn` says which half of it this row
@@ -141,6 +157,8 @@ template <int DT, bool WARP, bool KEEP, bool FULL>
 __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) forward_kernel(const __grid_constant__ Params P)
 {
     __shared__ Parts parts;
+    extern __shared__ HalfStage stages[];       // one a warp, where rows are off alignment
+    kept::Stage &stage = reinterpret_cast<kept::Stage &>(stages[threadIdx.x >> 5]);
     Place<WARP, FULL> at(P);
     float counts = 0.0f, own = 0.0f;            // of warp `lane`, of the caller's
     if (!WARP) {
@@ -154,7 +172,12 @@ __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) forward_kernel(con
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             const int live = at.of(u, at.row(), P.rows);
-            next[u] = kept::fetch<DT, FULL && !WARP>(P.x, at.row(), at.col[u], live, P.x.vec);
+            if (!FULL && P.x.vec == 0) {
+                kept::stage_in<DT, 8>(stage, [&](uint32_t e) { return at.template value<DT>(P, P.x.p, P.x.ld, u, at.base, e); });
+                next[u] = kept::staged<DT>(stage, threadIdx.x & 31);
+            } else {
+                next[u] = kept::fetch<DT, FULL && !WARP>(P.x, at.row(), at.col[u], live, P.x.vec);
+            }
         }
     };
     load();
@@ -214,7 +237,7 @@ __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) forward_kernel(con
                 if (P.sr) kept::keep8<true, DT, FULL && !WARP>(P.to, row, at.col[u], live, raw[u]);
                 else kept::keep8<false, DT, FULL && !WARP>(P.to, row, at.col[u], live, raw[u]);
             }
-            if (!(FULL && !WARP) && live == 0) continue;
+            if ((FULL || P.y.vec) && !(FULL && !WARP) && live == 0) continue;
             float w[8], b[8];
             params8(P.w, P.w_dtype, at.col[u], live, P.w_vec, 1.0f, w);
             if (P.b) {
@@ -225,106 +248,14 @@ __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) forward_kernel(con
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[u][i] = __fmul_rn(__fmul_rn(__fsub_rn(x[u][i], mean), rstd), w[i]);
             }
-            kept::store8<DT, FULL && !WARP>(P.y, row, at.col[u], live, P.y.vec, x[u]);
-        }
-    }
-}
-
-// Rows that begin off alignment, a block each: a thread's sixteen values lie blockDim.x
-// columns apart (checkpoint.cuh says why), a warp's of one place side by side, a group.
-constexpr int kLoose = kept::kLoose;
-
-struct LooseHalves {
-    uint16_t v[32][512];
-};
-
-__device__ __forceinline__ float param1(const void *p, uint32_t dtype, uint32_t col, float none)
-{
-    if (!p) return none;
-    return dtype == ASR_BF16 ? bf16_lo(static_cast<const uint16_t *>(p)[col]) : static_cast<const float *>(p)[col];
-}
-
-template <int DT>
-__device__ __forceinline__ void fetch_loose(const kept::Matrix &M, uint32_t row, const Params &P, float x[kLoose])
-{
-#pragma unroll
-    for (int i = 0; i < kLoose; ++i) {
-        const uint32_t col = i * blockDim.x + threadIdx.x;
-        x[i] = col < P.cols ? kept::load1<DT>(M, row, col) : 0.0f;
-    }
-}
-
-template <int DT, bool KEEP>
-__global__ void __launch_bounds__(1024) forward_loose_kernel(const __grid_constant__ Params P)
-{
-    __shared__ Parts parts;
-    __shared__ __align__(16) LooseHalves halves;
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    auto in = [&](int i) { return i * blockDim.x + threadIdx.x < P.cols; };
-    float counts = 0.0f;                        // of warp `lane`
-    if (lane < blockDim.x >> 5)
-        for (int i = 0; i < kLoose; ++i) {
-            const uint32_t first = i * blockDim.x + lane * 32;
-            counts += first >= P.cols ? 0.0f : static_cast<float>(P.cols - first < 32 ? P.cols - first : 32);
-        }
-    const float own = __shfl_sync(0xFFFFFFFFu, counts, warp), over_own = own > 0.0f ? __frcp_rn(own) : 0.0f;
-    float next[kLoose];
-    fetch_loose<DT>(P.x, blockIdx.x, P, next);
-    uint32_t turn = 0;
-    for (uint32_t row = blockIdx.x; row < P.rows; row += gridDim.x, turn ^= 1) {
-        float x[kLoose], sum = 0.0f, squares = 0.0f, mean = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kLoose; ++i) x[i] = next[i];
-        if (row + gridDim.x < P.rows) fetch_loose<DT>(P.x, row + gridDim.x, P, next);
-        if (P.centred) {
-#pragma unroll
-            for (int i = 0; i < kLoose; ++i) sum = __fadd_rn(sum, x[i]);
-            sum = warp_sum(sum);
-            mean = __fmul_rn(sum, over_own);
-        }
-#pragma unroll
-        for (int i = 0; i < kLoose; ++i) {
-            const float d = in(i) ? __fsub_rn(x[i], mean) : 0.0f;
-            squares = __fmaf_rn(d, d, squares);
-        }
-        squares = warp_sum(squares);
-        const float2 p = exchange(parts, turn, make_float2(sum, squares));
-        squares = p.y;
-        if (P.centred) {
-            mean = __fmul_rn(warp_sum(p.x), P.over_n);
-            const float d = counts > 0.0f ? __fsub_rn(__fdiv_rn(p.x, counts), mean) : 0.0f;
-            squares = __fmaf_rn(__fmul_rn(d, d), counts, squares);
-        }
-        const float rstd = __frsqrt_rn(__fmaf_rn(warp_sum(squares), P.over_n, P.eps));
-        if (threadIdx.x == 0 && P.rstd) {
-            P.rstd[row] = rstd;
-            if (P.mean) P.mean[row] = mean;
-        }
-        if (KEEP) {
-            if (P.sr)
-                kept::draw_halves(P.to, halves.v[warp], [&](uint32_t g) {
-                    return P.to.base + kept::place(row, P.to.across, (g * blockDim.x + warp * 32) / 8);
-                });
-            uint32_t power = 0;
-#pragma unroll
-            for (int i = 0; i < kLoose; ++i) {
-                const uint32_t b = kept::warp_power(x[i]), col = i * blockDim.x + threadIdx.x;
-                const float up = __uint_as_float((254u - b) << 23);
-                if (lane == i) power = b;
-                const uint32_t c = P.sr ? kept::code1<true>(x[i], up, halves.v[warp][32 * i + lane]) : kept::code1<false>(x[i], up, 0);
-                if (in(i)) P.to.q[kept::place(row, P.to.q_ld, col)] = static_cast<int8_t>(b == 255u ? 0 : c);
+            if (!FULL && P.y.vec == 0) {
+                __syncwarp();
+                kept::put_staged<DT>(stage, threadIdx.x & 31, kept::rounded<DT>(x[u]));
+                kept::stage_out<DT, 8>(stage, [&](uint32_t e) { return at.template value<DT>(P, P.y.p, P.y.ld, u, row - at.sub, e); });
+            } else {
+                kept::store8<DT, FULL && !WARP>(P.y, row, at.col[u], live, P.y.vec, x[u]);
             }
-            const uint32_t first = lane * blockDim.x + warp * 32;
-            if (lane < kLoose && first < P.cols)
-                P.to.power[kept::place(row, P.to.power_ld, first / 32)] = static_cast<uint8_t>(power);
         }
-#pragma unroll
-        for (int i = 0; i < kLoose; ++i)
-            if (in(i)) {
-                const uint32_t col = i * blockDim.x + threadIdx.x;
-                kept::store1<DT>(P.y, row, col, __fmaf_rn(__fmul_rn(__fsub_rn(x[i], mean), rstd), param1(P.w, P.w_dtype, col, 1.0f),
-                                                          param1(P.b, P.b_dtype, col, 0.0f)));
-            }
     }
 }
 
@@ -474,16 +405,58 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
     Place<WARP, FULL> at(P);
     const uint32_t step = blockDim.x;
     uint4 *const mine = ring + threadIdx.x;
-    auto bring_row = [&](uint32_t row, uint32_t slot) {
+    // Rows off alignment: value e of the warp's 256 of unit u, in words of 16 bytes that
+    // its lanes have side by side.
+    auto word_of = [&](uint4 *to, uint32_t e) {
+        uint4 *const warp = to - (threadIdx.x & 31);
+        return reinterpret_cast<uint32_t *>(warp + (e >> 2 & 1) * step + (e >> 3)) + (e & 3);
+    };
+    auto bring_off = [&](uint4 *to, const kept::Matrix &M, uint32_t first) {
+        if (DT == ASR_BF16) {                   // nothing smaller than four bytes is copied asynchronously
+            uint16_t v[kUnits][8];
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const void *from = at.template value<DT>(P, M.p, M.ld, u, first, 32 * i + (threadIdx.x & 31));
+                    v[u][i] = from ? *static_cast<const uint16_t *>(from) : static_cast<uint16_t>(0);
+                }
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    reinterpret_cast<uint16_t *>(to + u * step - (threadIdx.x & 31))[32 * i + (threadIdx.x & 31)] = v[u][i];
+        } else {
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t e = 32 * i + (threadIdx.x & 31);
+                    uint32_t *w = word_of(to + 2 * u * step, e);
+                    const void *from = at.template value<DT>(P, M.p, M.ld, u, first, e);
+                    if (from) copy_async<4>(w, from);
+                    else *w = 0;
+                }
+        }
+    };
+    // `first`: the warp's first row
+    auto bring_row = [&](uint32_t first, uint32_t slot) {
+        const uint32_t row = first + at.sub;
         uint4 *to = mine + (4 + slot * S::kWords) * step;
-        if (row < P.rows)
+        if (!FULL) __syncwarp();                // lanes may write for one another what was read a row ago
+        if (!FULL && first < P.rows) {
+            if (P.dy.vec == 0) bring_off(to, P.dy, first);
+            if (!KEPT && P.x.vec == 0) bring_off(to + S::kDy * step, P.x, first);
+        }
+        if (first < P.rows)
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             const int live = at.of(u, row, P.rows);
-            if (!FULL && live == 0) continue;
-            bring<DT, FULL>(to + u * (S::kDy / kUnits) * step, step, P.dy, row, at.col[u], live);
+            if (!(FULL && !WARP) && live == 0) continue;
+            if (FULL || P.dy.vec) bring<DT, FULL>(to + u * (S::kDy / kUnits) * step, step, P.dy, row, at.col[u], live);
             if (!KEPT) {
-                bring<DT, FULL>(to + (S::kDy + u * (S::kDy / kUnits)) * step, step, P.x, row, at.col[u], live);
+                if (FULL || P.x.vec)
+                    bring<DT, FULL>(to + (S::kDy + u * (S::kDy / kUnits)) * step, step, P.x, row, at.col[u], live);
             } else {
                 uint2 *q = reinterpret_cast<uint2 *>(to + S::kDy * step) + u;
                 if (FULL || (P.from.vec && live == 8)) copy_async<8>(q, P.from.q + kept::place(row, P.from.q_ld, at.col[u]));
@@ -506,7 +479,7 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
     };
     if constexpr (kStages > 1) {
 #pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) bring_row(at.row() + s * at.stride, s);
+        for (int s = 0; s < kStages - 1; ++s) bring_row(at.base + s * at.stride, s);
     }
     fetch_rest(at.row());
 #pragma unroll
@@ -521,8 +494,9 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
     uint32_t slot = 0;
     for (uint32_t turn = 0; at.base < P.rows; turn ^= 1) {
         const uint32_t row = at.row();
-        bring_row(row + (kStages - 1) * at.stride, slot ? slot - 1 : kStages - 1);
+        bring_row(at.base + (kStages - 1) * at.stride, slot ? slot - 1 : kStages - 1);
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        if (!FULL) __syncwarp();
         const uint4 *from = mine + (4 + slot * S::kWords) * step;
         slot = slot + 1 == kStages ? 0 : slot + 1;
         const float m = mean, r = rstd;
@@ -565,11 +539,29 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             const int live = at.of(u, row, P.rows);
-            if (!(FULL && !WARP) && live == 0) continue;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 g[u][i] = __fmaf_rn(-h[u][i], along, __fmaf_rn(g[u][i], r, -sum));
-            kept::store8<DT, FULL && !WARP>(P.dx, row, at.col[u], live, P.dx.vec, g[u]);
+            if (!FULL && P.dx.vec == 0) {
+                // through the words that this row's dy came in
+                uint4 *const mine_dy = const_cast<uint4 *>(from) + u * (S::kDy / kUnits) * step, *const warp = mine_dy - (threadIdx.x & 31);
+                const kept::Raw<DT> v = kept::rounded<DT>(g[u]);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < S::kDy / kUnits; ++i)
+                    mine_dy[i * step] = make_uint4(v.w[4 * i], v.w[4 * i + 1], v.w[4 * i + 2], v.w[4 * i + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t e = 32 * i + (threadIdx.x & 31);
+                    void *dst = at.template value<DT>(P, P.dx.p, P.dx.ld, u, row - at.sub, e);
+                    if (!dst) continue;
+                    if (DT == ASR_BF16) *static_cast<uint16_t *>(dst) = reinterpret_cast<const uint16_t *>(warp)[e];
+                    else *static_cast<uint32_t *>(dst) = *word_of(mine_dy, e);
+                }
+            } else if ((FULL && !WARP) || live) {
+                kept::store8<DT, FULL && !WARP>(P.dx, row, at.col[u], live, P.dx.vec, g[u]);
+            }
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -616,61 +608,6 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
             }
         }
     }
-}
-
-// Rows off alignment.
-template <int DT, bool KEPT, int THREADS>
-__global__ void __launch_bounds__(THREADS) backward_loose_kernel(const __grid_constant__ Params P)
-{
-    __shared__ Parts parts;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    auto in = [&](int i) { return i * blockDim.x + threadIdx.x < P.cols; };
-    float dw[kLoose] = {}, db[kLoose] = {};
-    uint32_t turn = 0;
-    for (uint32_t row = blockIdx.x; row < P.rows; row += gridDim.x, turn ^= 1) {
-        float h[kLoose], g[kLoose], along = 0.0f, sum = 0.0f;
-        const float m = P.centred ? P.mean[row] : 0.0f, r = P.rstd[row];
-        fetch_loose<DT>(P.dy, row, P, g);
-        if (KEPT) {
-            const uint32_t first = lane * blockDim.x + warp * 32;
-            float mine = 0.0f;
-            if (lane < kLoose && first < P.cols) mine = kept::scale_of(P.from.power[kept::place(row, P.from.power_ld, first / 32)]);
-#pragma unroll
-            for (int i = 0; i < kLoose; ++i) {
-                const float scale = __shfl_sync(0xFFFFFFFFu, mine, i);
-                h[i] = in(i) ? kept::value1(P.from.q[kept::place(row, P.from.q_ld, i * blockDim.x + threadIdx.x)], scale) : 0.0f;
-            }
-        } else {
-            fetch_loose<DT>(P.x, row, P, h);
-        }
-#pragma unroll
-        for (int i = 0; i < kLoose; ++i) {
-            h[i] = in(i) ? __fmul_rn(__fsub_rn(h[i], m), r) : 0.0f;
-            dw[i] = __fmaf_rn(g[i], h[i], dw[i]);
-            db[i] = __fadd_rn(db[i], g[i]);
-            if (in(i)) g[i] = __fmul_rn(g[i], param1(P.w, P.w_dtype, i * blockDim.x + threadIdx.x, 1.0f));
-            sum = __fadd_rn(sum, g[i]);
-            along = __fmaf_rn(g[i], h[i], along);
-        }
-        if (!P.dx.p) continue;
-        const float2 p = exchange(parts, turn, make_float2(warp_sum(sum), warp_sum(along)));
-        sum = P.centred ? __fmul_rn(__fmul_rn(warp_sum(p.x), P.over_n), r) : 0.0f;
-        along = __fmul_rn(__fmul_rn(warp_sum(p.y), P.over_n), r);
-#pragma unroll
-        for (int i = 0; i < kLoose; ++i)
-            if (in(i))
-                kept::store1<DT>(P.dx, row, i * blockDim.x + threadIdx.x,
-                                 __fmaf_rn(-h[i], along, __fmaf_rn(g[i], r, -sum)));
-    }
-    if (!P.dw && !P.db) return;
-    float *to = P.partial + blockIdx.x * 2 * P.pitch;
-#pragma unroll
-    for (int i = 0; i < kLoose; ++i)
-        if (in(i)) {
-            to[i * blockDim.x + threadIdx.x] = dw[i];
-            if (P.db) to[P.pitch + i * blockDim.x + threadIdx.x] = db[i];
-        }
 }
 
 // Rows that do not fit: dx, a block a row, read twice.
@@ -798,15 +735,8 @@ Kernel forward_of(int shape)
                                                                                    : forward_long_kernel<DT, KEEP>;
 }
 
-enum { kGeneral = 0, kFull = 1, kOff = 2 };     // how rows lie; off alignment counts for a block's
-
-Kernel forward_of(int32_t dtype, int shape, bool keep, int how)
+Kernel forward_of(int32_t dtype, int shape, bool keep, bool full)
 {
-    const bool full = how == kFull;
-    if (how == kOff && shape == kBlock) {
-        if (dtype == ASR_BF16) return keep ? forward_loose_kernel<ASR_BF16, true> : forward_loose_kernel<ASR_BF16, false>;
-        return keep ? forward_loose_kernel<ASR_F32, true> : forward_loose_kernel<ASR_F32, false>;
-    }
     if (dtype != ASR_BF16) return keep ? forward_of<ASR_F32, true, false>(shape) : forward_of<ASR_F32, false, false>(shape);
     if (full) return keep ? forward_of<ASR_BF16, true, true>(shape) : forward_of<ASR_BF16, false, true>(shape);
     return keep ? forward_of<ASR_BF16, true, false>(shape) : forward_of<ASR_BF16, false, false>(shape);
@@ -847,19 +777,8 @@ Backward backward_of(int32_t dtype, int shape, unsigned threads, bool full)
     return full ? backward_of<ASR_BF16, KEPT, true>(shape, threads) : backward_of<ASR_BF16, KEPT, false>(shape, threads);
 }
 
-template <int DT, bool KEPT>
-Backward loose_of(unsigned threads)
+Backward backward_of(int32_t dtype, bool codes, int shape, unsigned threads, bool full)
 {
-    return Backward{threads <= 512 ? backward_loose_kernel<DT, KEPT, 512> : backward_loose_kernel<DT, KEPT, 1024>, 0};
-}
-
-Backward backward_of(int32_t dtype, bool codes, int shape, unsigned threads, int how)
-{
-    const bool full = how == kFull;
-    if (how == kOff && shape == kBlock) {
-        if (dtype == ASR_BF16) return codes ? loose_of<ASR_BF16, true>(threads) : loose_of<ASR_BF16, false>(threads);
-        return codes ? loose_of<ASR_F32, true>(threads) : loose_of<ASR_F32, false>(threads);
-    }
     return codes ? backward_of<true>(dtype, shape, threads, full) : backward_of<false>(dtype, shape, threads, full);
 }
 
@@ -885,12 +804,13 @@ asr_status setup()
     for (int32_t dtype : {ASR_F32, ASR_BF16})
         for (int kept = 0; kept < 2; ++kept) {
             if (e == cudaSuccess) e = prod::load_kernel(columns_of(dtype, kept != 0));
-            for (int form = 0; form < 9; ++form) {
-                const int shape = form % 3, how = form / 3;
-                if (e == cudaSuccess) e = prod::load_kernel(forward_of(dtype, shape, kept != 0, how));
+            for (int form = 0; form < 6; ++form) {
+                const int shape = form % 3;
+                const bool full = form >= 3;
+                if (e == cudaSuccess) e = prod::load_kernel(forward_of(dtype, shape, kept != 0, full));
                 for (unsigned threads : {512u, 1024u}) {
                     if (shape == kWarp) threads = kWarpThreads;
-                    const Backward k = backward_of(dtype, kept != 0, shape, threads, how);
+                    const Backward k = backward_of(dtype, kept != 0, shape, threads, full);
                     if (e == cudaSuccess && k.smem)
                         e = cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem));
                     if (e == cudaSuccess) e = prod::load_kernel(k.kernel);
@@ -962,13 +882,14 @@ asr_status forward(const asr_norm_params *p, const void *x, uint64_t x_ld, void 
     }
     const int shape = shape_of(p->cols);
     const unsigned threads = threads_of(p->cols);
-    const bool off = !P.x.vec || !P.y.vec || (to && !P.to.vec);
-    auto kernel = forward_of(p->dtype, shape, to != nullptr, off ? kOff : whole(p->cols) ? kFull : kGeneral);
+    const bool full = whole(p->cols) && P.x.vec && P.y.vec && (!to || P.to.vec);
+    auto kernel = forward_of(p->dtype, shape, to != nullptr, full);
+    const size_t smem = shape != kLong && (!P.x.vec || !P.y.vec) ? threads / 32 * sizeof(HalfStage) : 0;
     int most = 0;
-    st = kept::resident(kernel, threads, 0, &most);
+    st = kept::resident(kernel, threads, smem, &most);
     if (st != ASR_OK) return st;
     const unsigned grid = int8::blocks_for(p->rows, shape == kWarp ? kWarpThreads / P.lanes : 1, static_cast<uint64_t>(most));
-    kernel<<<grid, threads, 0, stream>>>(P);
+    kernel<<<grid, threads, smem, stream>>>(P);
     return launched(ASR_KERNEL_NORM);
 }
 
@@ -1027,8 +948,8 @@ asr_status backward(const asr_norm_params *p, const void *dy, uint64_t dy_ld, co
         P.db = dbias != nullptr;
         const int shape = shape_of(p->cols);
         const unsigned threads = threads_of(p->cols);
-        const bool off = !P.dy.vec || (dx && !P.dx.vec) || !(from ? P.from.vec : P.x.vec);
-        const Backward k = backward_of(p->dtype, from != nullptr, shape, threads, off ? kOff : whole(p->cols) ? kFull : kGeneral);
+        const bool full = whole(p->cols) && P.dy.vec && (!dx || P.dx.vec) && (from ? P.from.vec : P.x.vec);
+        const Backward k = backward_of(p->dtype, from != nullptr, shape, threads, full);
         int most = 0;
         st = kept::resident(k.kernel, static_cast<int>(threads), k.smem, &most);
         if (st != ASR_OK) return st;
