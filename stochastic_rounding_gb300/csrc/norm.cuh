@@ -13,7 +13,7 @@
 // mean about the row's added), so nothing cancels.  Blocks walk over rows, the next
 // row's values fetched before the current one's are worked on.
 //
-// The backward kernel keeps its columns' sums for dw and db in registers (up to 608
+// The backward kernel keeps its columns' sums for dw and db in registers (up to 1,216
 // blocks leave theirs, and a second kernel adds them up, in one order), which leaves
 // too few warps to hide memory behind: each thread copies its own values of the next
 // rows into shared memory, asynchronously, and reads them back itself, so the ring
@@ -893,16 +893,15 @@ asr_status forward(const asr_norm_params *p, const void *x, uint64_t x_ld, void 
     return launched(ASR_KERNEL_NORM);
 }
 
-// Blocks that leave sums of a backward pass at most: enough to fill the GPU, and four
-// steps' rows each where there are fewer, since each leaves 2 x cols of them.  Of rows
-// that do not fit, 64, with 32 rows each.
-constexpr uint64_t kMostGroups = 152 * 4;
-
+// Blocks that leave sums of a backward pass at most: enough to fill the GPU, more where
+// they are small, and four steps' rows each where there are fewer, since each leaves
+// 2 x cols of them.  Of rows that do not fit, 64, with 32 rows each.
 uint64_t groups_of(uint64_t rows, uint64_t cols)
 {
     const int shape = shape_of(cols);
     const uint64_t each = shape == kLong ? 32 : 4 * (shape == kWarp ? kWarpThreads / lanes_of(cols) : 1);
-    const uint64_t want = (rows + each - 1) / each, most = shape == kLong ? 64 : kMostGroups;
+    const uint64_t per_sm = threads_of(cols) < 128 ? 512 / threads_of(cols) : 4;
+    const uint64_t want = (rows + each - 1) / each, most = shape == kLong ? 64 : 152 * per_sm;
     return want < most ? want : most;
 }
 
