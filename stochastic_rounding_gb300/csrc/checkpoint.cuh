@@ -74,6 +74,34 @@ __device__ __forceinline__ void load32(const void *p, uint32_t w[8])
                  : "l"(p));
 }
 
+// Two binary32 numbers at once, each rounded as by itself.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d)
+        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)),
+          "l"(reinterpret_cast<const uint64_t &>(c)));
+    return reinterpret_cast<const float2 &>(d);
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d)
+        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)));
+    return reinterpret_cast<const float2 &>(d);
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d)
+        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)));
+    return reinterpret_cast<const float2 &>(d);
+}
+
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
 __device__ __forceinline__ uint64_t place(uint32_t row, uint32_t ld, uint32_t col)
 {
     return static_cast<uint64_t>(row) * ld + col;
@@ -680,6 +708,12 @@ uint32_t codes_vec(const void *p, uint64_t ld)
 {
     const uint64_t off = reinterpret_cast<uintptr_t>(p) | ld;
     return off % 16 == 0 ? 2 : off % 8 == 0 ? 1 : 0;
+}
+
+// Whether a row's powers are aligned words of four.
+bool powers_whole(const asr_checkpoint &c, uint64_t cols)
+{
+    return ((reinterpret_cast<uintptr_t>(c.power) | c.power_ld) & 3u) == 0 && cols % (4 * kGroup) == 0;
 }
 
 uint64_t groups(uint64_t cols) { return (cols + kGroup - 1) / kGroup; }

@@ -126,18 +126,49 @@ struct __align__(16) HalfStage {
     uint4 w[64];
 };
 
-// Sums of a block's warps: `part` holds theirs, `turn` says which half of it this row
-// uses, so that one barrier a row is enough.
+// Two sums over a warp: lanes below 16 get the first, the others the second.
+__device__ __forceinline__ float half_sums(float a, float b)
+{
+    const bool high = threadIdx.x & 16;
+    float v = __fadd_rn(high ? b : a, __shfl_xor_sync(0xFFFFFFFFu, high ? a : b, 16));
+#pragma unroll
+    for (int d = 8; d; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+    return v;
+}
+
+// Sums of a block's warps, two of each; `turn` says which half a row uses, so that one
+// barrier a row is enough.
 struct Parts {
-    float2 v[2][32];
+    float v[2][2][32];
 };
 
+// Every lane gets warp `lane`'s two.
 __device__ __forceinline__ float2 exchange(Parts &parts, uint32_t turn, float2 mine)
 {
     const uint32_t lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    if (lane == 0) parts.v[turn][threadIdx.x >> 5] = mine;
+    if (lane == 0) {
+        parts.v[turn][0][threadIdx.x >> 5] = mine.x;
+        parts.v[turn][1][threadIdx.x >> 5] = mine.y;
+    }
     __syncthreads();
-    return lane < warps ? parts.v[turn][lane] : make_float2(0.0f, 0.0f);
+    return lane < warps ? make_float2(parts.v[turn][0][lane], parts.v[turn][1][lane]) : make_float2(0.0f, 0.0f);
+}
+
+// Two sums over a block, of what its threads hold: half the shuffles of one after the
+// other, and as many steps as one takes.
+__device__ __forceinline__ float2 block_sums(Parts &parts, uint32_t turn, float a, float b)
+{
+    const uint32_t lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    float v = half_sums(a, b);
+    if ((lane & 15) == 0) parts.v[turn][lane >> 4][threadIdx.x >> 5] = v;
+    __syncthreads();
+    const float *part = parts.v[turn][lane >> 4];
+    v = (lane & 15) < warps ? part[lane & 15] : 0.0f;
+    if (warps > 16) v = __fadd_rn(v, (lane & 15) + 16 < warps ? part[(lane & 15) + 16] : 0.0f);
+#pragma unroll
+    for (int d = 8; d; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+    return lane & 16 ? make_float2(other, v) : make_float2(v, other);
 }
 
 // How many of a row's values warp `lane` of the block holds.
@@ -165,7 +196,7 @@ __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) forward_kernel(con
         counts = count_of(P.cols);
         own = __shfl_sync(0xFFFFFFFFu, counts, threadIdx.x >> 5);
     }
-    const float over_own = own > 0.0f ? __frcp_rn(own) : 0.0f;
+    const float over_own = own > 0.0f ? __frcp_rn(own) : 0.0f, over_counts = counts > 0.0f ? __frcp_rn(counts) : 0.0f;
     kept::Raw<DT> next[kUnits];
     auto load = [&]() {
         if (at.base >= P.rows) return;
@@ -192,35 +223,41 @@ __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) forward_kernel(con
         }
         at.base += at.stride;
         load();
+        float2 two = kept::both(0.0f);
         if (P.centred) {
 #pragma unroll
             for (int u = 0; u < kUnits; ++u)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum = __fadd_rn(sum, x[u][i]);
+                for (int i = 0; i < 8; i += 2) two = kept::add2(two, make_float2(x[u][i], x[u][i + 1]));
+            sum = __fadd_rn(two.x, two.y);
             sum = WARP ? lane_sum(sum, P.lanes) : warp_sum(sum);
             mean = __fmul_rn(sum, WARP ? P.over_n : over_own);
-        }
-        if (P.centred) {
+            two = kept::both(0.0f);
 #pragma unroll
             for (int u = 0; u < kUnits; ++u)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float d = FULL || i < at.live[u] ? __fsub_rn(x[u][i], mean) : 0.0f;
-                    squares = __fmaf_rn(d, d, squares);
+                for (int i = 0; i < 8; i += 2) {
+                    float2 d = kept::add2(make_float2(x[u][i], x[u][i + 1]), kept::both(-mean));
+                    if (!FULL) d = make_float2(i < at.live[u] ? d.x : 0.0f, i + 1 < at.live[u] ? d.y : 0.0f);
+                    two = kept::fma2(d, d, two);
                 }
         } else {
 #pragma unroll
             for (int u = 0; u < kUnits; ++u)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) squares = __fmaf_rn(x[u][i], x[u][i], squares);
+                for (int i = 0; i < 8; i += 2) {
+                    const float2 d = make_float2(x[u][i], x[u][i + 1]);
+                    two = kept::fma2(d, d, two);
+                }
         }
+        squares = __fadd_rn(two.x, two.y);
         squares = WARP ? lane_sum(squares, P.lanes) : warp_sum(squares);
         if (!WARP) {
             const float2 p = exchange(parts, turn, make_float2(sum, squares));
             squares = p.y;
             if (P.centred) {
                 mean = __fmul_rn(warp_sum(p.x), P.over_n);
-                const float d = counts > 0.0f ? __fsub_rn(__fdiv_rn(p.x, counts), mean) : 0.0f;
+                const float d = counts > 0.0f ? __fsub_rn(__fmul_rn(p.x, over_counts), mean) : 0.0f;    // the warp's own mean again
                 squares = __fmaf_rn(__fmul_rn(d, d), counts, squares);
             }
             squares = warp_sum(squares);
@@ -240,13 +277,16 @@ __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) forward_kernel(con
             if ((FULL || P.y.vec) && !(FULL && !WARP) && live == 0) continue;
             float w[8], b[8];
             params8(P.w, P.w_dtype, at.col[u], live, P.w_vec, 1.0f, w);
-            if (P.b) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                float2 &h = reinterpret_cast<float2 &>(x[u][i]);
+                h = kept::mul2(kept::add2(h, kept::both(-mean)), kept::both(rstd));
+                h = kept::mul2(h, make_float2(w[i], w[i + 1]));
+            }
+            if (P.b) {                          // behind the weight, and not with it, for want of registers
                 muon::load8(P.b, P.b_dtype, at.col[u], live, P.b_vec, b);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[u][i] = __fmaf_rn(__fmul_rn(__fsub_rn(x[u][i], mean), rstd), w[i], b[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[u][i] = __fmul_rn(__fmul_rn(__fsub_rn(x[u][i], mean), rstd), w[i]);
+                for (int i = 0; i < 8; ++i) x[u][i] = __fadd_rn(x[u][i], b[i]);
             }
             if (!FULL && P.y.vec == 0) {
                 __syncwarp();
@@ -337,16 +377,15 @@ __device__ __forceinline__ void copy_async(void *to, const void *from)
 }
 
 // Eight values of a matrix, from memory to a thread's place in shared memory (words
-// `step` apart for 16 bytes each): asynchronously, in 16 bytes or, off alignment, f32
-// by one; bf16 off alignment at once.
+// `step` apart for 16 bytes each), asynchronously in 16 bytes; of a row's last ones f32
+// by one, bf16 at once.
 template <int DT, bool FULL>
 __device__ __forceinline__ void bring(uint4 *to, uint32_t step, const kept::Matrix &M, uint32_t row, uint32_t col, int live)
 {
-    constexpr int kWords = DT == ASR_BF16 ? 1 : 2;
     const char *from = static_cast<const char *>(M.p) + kept::place(row, M.ld, col) * (DT == ASR_BF16 ? 2 : 4);
     if (FULL || (M.vec && live == 8)) {
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) copy_async<16>(to + i * step, from + 16 * i);
+        for (int i = 0; i < (DT == ASR_BF16 ? 1 : 2); ++i) copy_async<16>(to + i * step, from + 16 * i);
     } else if (DT == ASR_F32) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -381,25 +420,29 @@ struct Stage {
 };
 static_assert(kUnits == 2, "codes of two units fill a word");
 
-// Stages of the ring: four, fewer where a block's values and weight would not leave
-// room (227 KB) for them.
-template <int DT, bool KEPT, int THREADS>
+// Stages of the ring: four, fewer where the values and weights of BLOCKS blocks would
+// not leave room (227 KB) for them.
+template <int DT, bool KEPT, int THREADS, int BLOCKS = 1>
 struct Ring {
-    static constexpr int kRoom = 220 * 1024 - THREADS * 64;
+    static constexpr int kRoom = 220 * 1024 / BLOCKS - THREADS * 64;
     static constexpr int kFit = kRoom / (THREADS * Stage<DT, KEPT>::kWords * 16);
     static constexpr int kStages = kFit < 1 ? 1 : kFit > 4 ? 4 : kFit;
-    static size_t bytes(unsigned threads) { return (static_cast<size_t>(kStages) * Stage<DT, KEPT>::kWords + 4) * 16 * threads; }
+    static size_t bytes(unsigned threads) { return ((static_cast<size_t>(kStages) * Stage<DT, KEPT>::kWords + 4) * 16 + kStages) * threads; }
 };
 
-// What a norm that is not centred, or has no bias, does not need is computed all the
-// same: a form without it had a quarter fewer instructions and took as long (8,192 x
-// 4,096 from codes 49 us, 46 to 48 as it is).
-template <int DT, bool WARP, bool KEPT, int THREADS, bool FULL>
-__global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant__ Params P)
+// LEAN: without a mean and a bias's gradient, whose sums' registers make room for a third
+// block of up to 256 threads an SM.  From codes only (8,192 x 4,096 bf16, one launch
+// after another: 38.9 -> 37.2 us); from x three blocks leave the ring two stages (37.0,
+// 40.1 with three).
+constexpr int kLeanBlocks = 3;
+
+template <int DT, bool WARP, bool KEPT, int THREADS, bool FULL, bool LEAN = false>
+__global__ void __launch_bounds__(THREADS, LEAN ? kLeanBlocks : THREADS == 256 ? 2 : 1) backward_kernel(const __grid_constant__ Params P)
 {
     using S = Stage<DT, KEPT>;
-    constexpr int kStages = Ring<DT, KEPT, THREADS>::kStages;
-    extern __shared__ __align__(16) uint4 ring[];           // [weight: 4][stage][word][thread]
+    constexpr bool kPower = KEPT && !WARP && FULL;           // whole words of powers
+    constexpr int kStages = Ring<DT, KEPT, THREADS, LEAN ? kLeanBlocks : 1>::kStages;
+    extern __shared__ __align__(16) uint4 ring[];           // [weight: 4 | stages' words][thread], [stage][warp][8]
     __shared__ Parts parts;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     Place<WARP, FULL> at(P);
@@ -439,11 +482,28 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
                 }
         }
     };
+    // A row's rstd, mean and words of powers come through the ring too, a lane a word of
+    // the warp's: in registers, a row ahead, they came too late (8,192 x 4,096 bf16 from x
+    // 44.5 -> 40.4 us, from codes 44.0 -> 37.0).
+    const uint32_t lane = threadIdx.x & 31;
+    const char *stat = nullptr;
+    uint32_t stat_step = 4;
+    if (!WARP) {
+        if (lane == 0) stat = reinterpret_cast<const char *>(P.rstd);
+        if (!LEAN && lane == 1 && P.centred) stat = reinterpret_cast<const char *>(P.mean);
+        if (kPower && lane >= 2 && lane < 6) {
+            stat = reinterpret_cast<const char *>(P.from.power) + ((lane >= 4 ? at.col[1] : at.col[0]) - at.at8()) / 32 + (lane & 1) * 4;
+            stat_step = P.from.power_ld;
+        }
+    }
+    auto rest_of = [&](uint32_t slot) {
+        return reinterpret_cast<uint32_t *>(ring + (4 + kStages * S::kWords) * step) + (slot * (step >> 5) + (threadIdx.x >> 5)) * 8;
+    };
     // `first`: the warp's first row
     auto bring_row = [&](uint32_t first, uint32_t slot) {
         const uint32_t row = first + at.sub;
         uint4 *to = mine + (4 + slot * S::kWords) * step;
-        if (!FULL) __syncwarp();                // lanes may write for one another what was read a row ago
+        if (!(FULL && WARP)) __syncwarp();      // lanes may write for one another what was read a row ago
         if (!FULL && first < P.rows) {
             if (P.dy.vec == 0) bring_off(to, P.dy, first);
             if (!KEPT && P.x.vec == 0) bring_off(to + S::kDy * step, P.x, first);
@@ -463,16 +523,19 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
                 else *q = kept::fetch_codes(P.from, row, at.col[u], live).v;
             }
         }
+        if (!WARP && stat && row < P.rows) copy_async<4>(rest_of(slot) + lane, stat + static_cast<uint64_t>(row) * stat_step);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    // what is too little for the ring is fetched a row ahead
+    // what does not come through the ring is fetched a row ahead
     float mean = 0.0f, rstd = 0.0f;
     uint32_t power[kUnits] = {};
     auto fetch_rest = [&](uint32_t row) {
         if (row >= P.rows) return;
-        rstd = P.rstd[row];
-        if (P.centred) mean = P.mean[row];
-        if (KEPT)
+        if (WARP) {
+            rstd = P.rstd[row];
+            if (P.centred) mean = P.mean[row];
+        }
+        if (KEPT && !kPower)
 #pragma unroll
             for (int u = 0; u < kUnits; ++u)
                 if (FULL || at.live[u]) power[u] = P.from.power[kept::place(row, P.from.power_ld, at.col[u] >> 5)];
@@ -496,14 +559,23 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
         const uint32_t row = at.row();
         bring_row(at.base + (kStages - 1) * at.stride, slot ? slot - 1 : kStages - 1);
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-        if (!FULL) __syncwarp();
+        if (!(FULL && WARP)) __syncwarp();
         const uint4 *from = mine + (4 + slot * S::kWords) * step;
+        float m = mean, r = rstd;
+        uint32_t b[kUnits] = {power[0], power[1]};
+        if (!WARP) {
+            const uint32_t *rest = rest_of(slot);
+            r = __uint_as_float(rest[0]);
+            m = !LEAN && P.centred ? __uint_as_float(rest[1]) : 0.0f;
+            if (kPower)
+#pragma unroll
+                for (int u = 0; u < kUnits; ++u) b[u] = rest[2 + 2 * u + (lane >> 4)] >> (lane * 2 & 24) & 255;
+        }
         slot = slot + 1 == kStages ? 0 : slot + 1;
-        const float m = mean, r = rstd;
-        const uint32_t b[kUnits] = {power[0], power[1]};
         at.base += at.stride;
         fetch_rest(at.row());
-        float h[kUnits][8], g[kUnits][8], along = 0.0f, sum = 0.0f;
+        float h[kUnits][8], g[kUnits][8];
+        float2 along2 = kept::both(0.0f), sum2 = kept::both(0.0f);
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             if (at.of(u, row, P.rows) == 0) {
@@ -515,33 +587,41 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
             if (KEPT) kept::values(kept::Codes{*(reinterpret_cast<const uint2 *>(from + S::kDy * step) + u), b[u]}, h[u]);
             else taken<DT>(from + (S::kDy + u * (S::kDy / kUnits)) * step, step, h[u]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 8; i += 2) {
                 const float4 w4 = *reinterpret_cast<const float4 *>(mine + (2 * u + (i >> 2)) * step);
-                const float w = (i & 3) == 0 ? w4.x : (i & 3) == 1 ? w4.y : (i & 3) == 2 ? w4.z : w4.w;
-                h[u][i] = __fmul_rn(__fsub_rn(h[u][i], m), r);
-                dw[u][i] = __fmaf_rn(g[u][i], h[u][i], dw[u][i]);
-                db[u][i] = __fadd_rn(db[u][i], g[u][i]);
-                g[u][i] = __fmul_rn(g[u][i], w);
-                sum = __fadd_rn(sum, g[u][i]);
-                along = __fmaf_rn(g[u][i], h[u][i], along);
+                float2 &h2 = reinterpret_cast<float2 &>(h[u][i]), &g2 = reinterpret_cast<float2 &>(g[u][i]);
+                float2 &dw2 = reinterpret_cast<float2 &>(dw[u][i]), &db2 = reinterpret_cast<float2 &>(db[u][i]);
+                if (!LEAN) h2 = kept::add2(h2, kept::both(-m));
+                h2 = kept::mul2(h2, kept::both(r));
+                dw2 = kept::fma2(g2, h2, dw2);
+                if (!LEAN) db2 = kept::add2(db2, g2);
+                g2 = kept::mul2(g2, i & 2 ? make_float2(w4.z, w4.w) : make_float2(w4.x, w4.y));
+                if (!LEAN) sum2 = kept::add2(sum2, g2);
+                along2 = kept::fma2(g2, h2, along2);
             }
         }
+        float along = __fadd_rn(along2.x, along2.y), sum = __fadd_rn(sum2.x, sum2.y);
         if (!P.dx.p) continue;
-        sum = WARP ? lane_sum(sum, P.lanes) : warp_sum(sum);
-        along = WARP ? lane_sum(along, P.lanes) : warp_sum(along);
-        if (!WARP) {
-            const float2 p = exchange(parts, turn, make_float2(sum, along));
-            sum = warp_sum(p.x);
-            along = warp_sum(p.y);
+        if (WARP) {
+            sum = lane_sum(sum, P.lanes);
+            along = lane_sum(along, P.lanes);
+        } else {
+            const float2 p = block_sums(parts, turn, sum, along);
+            sum = p.x;
+            along = p.y;
         }
-        sum = !P.centred ? 0.0f : __fmul_rn(__fmul_rn(sum, P.over_n), r);
+        sum = LEAN || !P.centred ? 0.0f : __fmul_rn(__fmul_rn(sum, P.over_n), r);
         along = __fmul_rn(__fmul_rn(along, P.over_n), r);
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             const int live = at.of(u, row, P.rows);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                g[u][i] = __fmaf_rn(-h[u][i], along, __fmaf_rn(g[u][i], r, -sum));
+            for (int i = 0; i < 8; i += 2) {
+                float2 &g2 = reinterpret_cast<float2 &>(g[u][i]);
+                const float2 h2 = reinterpret_cast<const float2 &>(h[u][i]);
+                g2 = LEAN ? kept::mul2(g2, kept::both(r)) : kept::fma2(g2, kept::both(r), kept::both(-sum));
+                g2 = kept::fma2(h2, kept::both(-along), g2);
+            }
             if (!FULL && P.dx.vec == 0) {
                 // through the words that this row's dy came in
                 uint4 *const mine_dy = const_cast<uint4 *>(from) + u * (S::kDy / kUnits) * step, *const warp = mine_dy - (threadIdx.x & 31);
@@ -570,7 +650,6 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
     if constexpr (WARP) {
         // a row's lanes, then the warps, one after another, in the first rows of the ring
         float *const sums = reinterpret_cast<float *>(ring);
-        const uint32_t lane = threadIdx.x & 31;
 #pragma unroll
         for (int u = 0; u < kUnits; ++u)
 #pragma unroll
@@ -604,7 +683,7 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
             for (int i = 0; i < 2; ++i) {
                 float4 *p = reinterpret_cast<float4 *>(to + at.col[u]) + i;
                 *p = make_float4(dw[u][4 * i], dw[u][4 * i + 1], dw[u][4 * i + 2], dw[u][4 * i + 3]);
-                if (P.db) p[P.pitch / 4] = make_float4(db[u][4 * i], db[u][4 * i + 1], db[u][4 * i + 2], db[u][4 * i + 3]);
+                if (!LEAN && P.db) p[P.pitch / 4] = make_float4(db[u][4 * i], db[u][4 * i + 1], db[u][4 * i + 2], db[u][4 * i + 3]);
             }
         }
     }
@@ -763,23 +842,27 @@ Backward backward_at(unsigned threads)
 }
 
 template <int DT, bool KEPT, bool FULL>
-Backward backward_of(int shape, unsigned threads)
+Backward backward_of(int shape, unsigned threads, bool lean)
 {
+    if constexpr (FULL) {
+        if (KEPT && lean && shape == kBlock && threads <= 256)
+            return Backward{backward_kernel<DT, false, KEPT, 256, true, true>, Ring<DT, KEPT, 256, kLeanBlocks>::bytes(threads)};
+    }
     if (shape == kWarp) return backward_at<DT, KEPT, true, kWarpThreads, FULL>(threads);
     if (shape == kLong) return Backward{backward_long_kernel<DT, KEPT>, 0};
     return threads <= 512 ? backward_at<DT, KEPT, false, 512, FULL>(threads) : backward_at<DT, KEPT, false, 1024, FULL>(threads);
 }
 
 template <bool KEPT>
-Backward backward_of(int32_t dtype, int shape, unsigned threads, bool full)
+Backward backward_of(int32_t dtype, int shape, unsigned threads, bool full, bool lean)
 {
-    if (dtype != ASR_BF16) return backward_of<ASR_F32, KEPT, false>(shape, threads);
-    return full ? backward_of<ASR_BF16, KEPT, true>(shape, threads) : backward_of<ASR_BF16, KEPT, false>(shape, threads);
+    if (dtype != ASR_BF16) return backward_of<ASR_F32, KEPT, false>(shape, threads, lean);
+    return full ? backward_of<ASR_BF16, KEPT, true>(shape, threads, lean) : backward_of<ASR_BF16, KEPT, false>(shape, threads, lean);
 }
 
-Backward backward_of(int32_t dtype, bool codes, int shape, unsigned threads, bool full)
+Backward backward_of(int32_t dtype, bool codes, int shape, unsigned threads, bool full, bool lean)
 {
-    return codes ? backward_of<true>(dtype, shape, threads, full) : backward_of<false>(dtype, shape, threads, full);
+    return codes ? backward_of<true>(dtype, shape, threads, full, lean) : backward_of<false>(dtype, shape, threads, full, lean);
 }
 
 template <int DT>
@@ -808,9 +891,9 @@ asr_status setup()
                 const int shape = form % 3;
                 const bool full = form >= 3;
                 if (e == cudaSuccess) e = prod::load_kernel(forward_of(dtype, shape, kept != 0, full));
-                for (unsigned threads : {512u, 1024u}) {
+                for (unsigned threads : {256u, 512u, 1024u}) {
                     if (shape == kWarp) threads = kWarpThreads;
-                    const Backward k = backward_of(dtype, kept != 0, shape, threads, full);
+                    const Backward k = backward_of(dtype, kept != 0, shape, threads, full, threads == 256);
                     if (e == cudaSuccess && k.smem)
                         e = cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem));
                     if (e == cudaSuccess) e = prod::load_kernel(k.kernel);
@@ -947,8 +1030,8 @@ asr_status backward(const asr_norm_params *p, const void *dy, uint64_t dy_ld, co
         P.db = dbias != nullptr;
         const int shape = shape_of(p->cols);
         const unsigned threads = threads_of(p->cols);
-        const bool full = whole(p->cols) && P.dy.vec && (!dx || P.dx.vec) && (from ? P.from.vec : P.x.vec);
-        const Backward k = backward_of(p->dtype, from != nullptr, shape, threads, full);
+        const bool full = whole(p->cols) && P.dy.vec && (!dx || P.dx.vec) && (from ? P.from.vec && kept::powers_whole(*from, p->cols) : P.x.vec);
+        const Backward k = backward_of(p->dtype, from != nullptr, shape, threads, full, !p->centred && !dbias);
         int most = 0;
         st = kept::resident(k.kernel, static_cast<int>(threads), k.smem, &most);
         if (st != ASR_OK) return st;

@@ -319,6 +319,33 @@ def test_norm(asr, rows, cols, dtype, centred):
                 assert torch.equal(only[0], dx)
 
 
+@pytest.mark.parametrize("rows,cols", [(2, 512), (1500, 1024), (3001, 2560), (2100, 4096), (40, 4608)])
+def test_norm_gradients_from_codes_without_a_bias(asr, rows, cols):
+    """The same gradients whether a bias's is wanted, and however the powers lie; many rows to a block."""
+    import torch
+    x, dy = make(rows, cols, "bf16", rows), make(rows, cols, "bf16", cols, 1e-3)
+    w = (1 + 0.3 * torch.randn(cols, generator=torch.Generator().manual_seed(cols))).to(torch.bfloat16).cuda()
+    _, saved = asr.layer_norm(x, w, centred=False, save="int8")
+    dx, dw, none = asr.layer_norm_grads(dy, saved, w, need_dbias=False)
+    assert none is None
+    at, rstd = asr.restore_int8(saved.input, torch.float32), saved.rstd.double()[:, None]
+    ha = at.double() * rstd                     # rstd as it is saved: h has a rounding, a product with dy another in its sum
+    bound = (128 * U * (dy.double() * ha).abs()).sum(0)
+    close(dw, (dy.double() * ha).sum(0), bound, "dw")
+    full = asr.layer_norm_grads(dy, saved, w)
+    assert torch.equal(full[0], dx)
+    close(full[1], (dy.double() * ha).sum(0), bound, "dw with db")
+    q, power = saved.input.q, saved.input.power
+    groups = cols // 32
+    for off, ld in ((0, groups), (1, groups + 4), (4, groups + 1)):
+        buf = torch.zeros(off + rows * ld + 8, dtype=torch.uint8, device="cuda")
+        p = buf[off:off + rows * ld].view(rows, ld)[:, :groups].copy_(power)
+        dx2, dw2 = torch.empty_like(dx), torch.empty_like(dw)
+        asr.asr_layer_norm_grads(dy, None, w, None, saved.rstd, dx2, dw2, None, centred=False, kept=(q, p))
+        assert torch.equal(dx2, dx)
+        close(dw2, (dy.double() * ha).sum(0), bound, "dw")
+
+
 @pytest.mark.parametrize("centred", [True, False])
 @pytest.mark.parametrize("cols", [40, 1500, 20000])
 def test_norm_without_parameters_and_without_rows(asr, centred, cols):
