@@ -420,28 +420,25 @@ struct Stage {
 };
 static_assert(kUnits == 2, "codes of two units fill a word");
 
-// Stages of the ring: four, fewer where the values and weights of BLOCKS blocks would
-// not leave room (227 KB) for them.
-template <int DT, bool KEPT, int THREADS, int BLOCKS = 1>
+// Stages of the ring: four, fewer where a block's values and weight would not leave
+// room (227 KB) for them.
+template <int DT, bool KEPT, int THREADS>
 struct Ring {
-    static constexpr int kRoom = 220 * 1024 / BLOCKS - THREADS * 64;
+    static constexpr int kRoom = 220 * 1024 - THREADS * 64;
     static constexpr int kFit = kRoom / (THREADS * Stage<DT, KEPT>::kWords * 16);
     static constexpr int kStages = kFit < 1 ? 1 : kFit > 4 ? 4 : kFit;
     static size_t bytes(unsigned threads) { return ((static_cast<size_t>(kStages) * Stage<DT, KEPT>::kWords + 4) * 16 + kStages) * threads; }
 };
 
-// LEAN: without a mean and a bias's gradient, whose sums' registers make room for a third
-// block of up to 256 threads an SM.  From codes only (8,192 x 4,096 bf16, one launch
-// after another: 38.9 -> 37.2 us); from x three blocks leave the ring two stages (37.0,
-// 40.1 with three).
-constexpr int kLeanBlocks = 3;
-
+// LEAN: without a mean and a bias's gradient, a quarter fewer instructions, for up to 512
+// threads (bf16 from codes, one launch after another: 8,192 x 4,096 38.9 -> 35.0 us,
+// 4,096 x 8,192 42.6 -> 38.9; from x it gains nothing, 37.0 and 37.3).
 template <int DT, bool WARP, bool KEPT, int THREADS, bool FULL, bool LEAN = false>
-__global__ void __launch_bounds__(THREADS, LEAN ? kLeanBlocks : THREADS == 256 ? 2 : 1) backward_kernel(const __grid_constant__ Params P)
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) backward_kernel(const __grid_constant__ Params P)
 {
     using S = Stage<DT, KEPT>;
     constexpr bool kPower = KEPT && !WARP && FULL;           // whole words of powers
-    constexpr int kStages = Ring<DT, KEPT, THREADS, LEAN ? kLeanBlocks : 1>::kStages;
+    constexpr int kStages = Ring<DT, KEPT, THREADS>::kStages;
     extern __shared__ __align__(16) uint4 ring[];           // [weight: 4 | stages' words][thread], [stage][warp][8]
     __shared__ Parts parts;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -844,9 +841,9 @@ Backward backward_at(unsigned threads)
 template <int DT, bool KEPT, bool FULL>
 Backward backward_of(int shape, unsigned threads, bool lean)
 {
-    if constexpr (FULL) {
-        if (KEPT && lean && shape == kBlock && threads <= 256)
-            return Backward{backward_kernel<DT, false, KEPT, 256, true, true>, Ring<DT, KEPT, 256, kLeanBlocks>::bytes(threads)};
+    if constexpr (FULL && KEPT) {
+        if (lean && shape == kBlock && threads <= 512)
+            return Backward{backward_kernel<DT, false, true, 512, true, true>, Ring<DT, true, 512>::bytes(threads)};
     }
     if (shape == kWarp) return backward_at<DT, KEPT, true, kWarpThreads, FULL>(threads);
     if (shape == kLong) return Backward{backward_long_kernel<DT, KEPT>, 0};
@@ -891,9 +888,9 @@ asr_status setup()
                 const int shape = form % 3;
                 const bool full = form >= 3;
                 if (e == cudaSuccess) e = prod::load_kernel(forward_of(dtype, shape, kept != 0, full));
-                for (unsigned threads : {256u, 512u, 1024u}) {
-                    if (shape == kWarp) threads = kWarpThreads;
-                    const Backward k = backward_of(dtype, kept != 0, shape, threads, full, threads == 256);
+                for (int block = 0; block < 3; ++block) {
+                    const unsigned threads = shape == kWarp ? kWarpThreads : block == 2 ? 1024 : 512;
+                    const Backward k = backward_of(dtype, kept != 0, shape, threads, full, block == 1);
                     if (e == cudaSuccess && k.smem)
                         e = cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem));
                     if (e == cudaSuccess) e = prod::load_kernel(k.kernel);
