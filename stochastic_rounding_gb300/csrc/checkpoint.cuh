@@ -14,6 +14,11 @@
 // above 127 2^e; 32 values rather than a row keep a strong channel from costing the
 // others theirs.
 //
+// Bound by bytes, but for the stochastic form of bf16, which is by Philox's
+// multiplications (8,192 x 14,336 bf16, one launch after another, at 6,697 GB/s 53 us:
+// pack 56, stochastic 75, restore 59).  Pairs of values go through the conversions
+// together (fma.f32x2; pack, stochastic, 82 without).
+//
 // Random bits: eight values to a Philox counter, sixteen bits each, where the
 // optimizers take four: the generator is a third of the stochastic form's
 // instructions, and the third counter word sets these numbers apart from theirs.
@@ -45,8 +50,9 @@ struct Source {
 // Whether kernels look at a unit's bounds: FULL is for matrices of whole spans whose
 // units are all aligned, as the widths of layers are, and leaves out the tests and the
 // element by element accesses.  Only for bf16, whose kernels are bound by their
-// instructions (8,192 x 14,336: pack 67 -> 59 us, unpack 68 -> 57 us, the gated
-// activation's backward pass from codes 197 -> 168 us); f32's are bound by bytes.
+// instructions (pack, stochastic: 8,192 x 14,336 84 us, 8,192 x 14,352 without FULL 90;
+// the gated activation's backward pass from codes at 0.96 of the copy rate, 0.88 without
+// at 8,192 x 11,008); f32's are bound by bytes.
 __device__ __forceinline__ int live_of(uint32_t cols, uint32_t col, uint32_t most = 8)
 {
     return col >= cols ? 0 : static_cast<int>(cols - col < most ? cols - col : most);

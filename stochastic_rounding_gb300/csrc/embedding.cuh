@@ -21,6 +21,10 @@
 // memory (by one block alone 8,192 tokens took 20 us: its instructions); more are cut
 // into tiles of 4,096, with a launch each for their counts, the tiles' places, and the
 // moves.
+//
+// Bound by bytes: 8,192 tokens of a bf16 table of 128,256 x 4,096, with the time of its
+// bytes at 6,697 GB/s: lookup 20.5 us (20.1), gradient 179 (167), 8 of them the sort's,
+// with zeros beside it.
 
 namespace embed {
 
