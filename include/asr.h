@@ -436,7 +436,7 @@ typedef struct {
 } asr_checkpoint;
 
 /* Makes the checkpoint of x (x_ld elements between rows); bytes between a row's end
- * and the next are not written.  rows at most 2^30, cols at most 2^24. */
+ * and the next are not written.  rows at most 2^30, cols at most 2^25. */
 asr_status asr_checkpoint_int8(const void *x, int32_t x_dtype, uint64_t rows, uint64_t cols, uint64_t x_ld,
                                const asr_checkpoint *to, asr_stream_t stream);
 
@@ -447,7 +447,8 @@ asr_status asr_restore_int8(const asr_checkpoint *from, uint64_t rows, uint64_t 
 /* A layer's activation: f(a) = a s(u), s(u) = 1 / (1 + e^-u), with u = a (ASR_SILU) or
  * u = sqrt(8/pi) (a + 0.044715 a^3) (ASR_GELU, its tanh form).  gated == 0: x is rows x
  * cols and y = f(x).  gated == 1: x is rows x 2 cols, [a | b], and y = f(a) b.
- * x and y of one dtype.  keep, if not NULL, receives x's checkpoint (of all its columns). */
+ * x and y of one dtype.  keep, if not NULL, receives x's checkpoint (of all its columns).
+ * rows at most 2^30, cols at most 2^24. */
 typedef enum { ASR_SILU = 0, ASR_GELU = 1 } asr_function;
 
 asr_status asr_activation(const void *x, uint64_t x_ld, void *y, uint64_t y_ld, int32_t dtype, uint64_t rows,

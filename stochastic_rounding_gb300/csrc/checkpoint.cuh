@@ -711,8 +711,9 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const __grid_constant_
 // ------------------------------------------------------------------ host
 
 constexpr uint64_t kMaxRows = 1ull << 30, kMaxCols = 1ull << 24;
+constexpr uint64_t kMaxWidth = 2 * kMaxCols;    // of a checkpoint: both halves of a gated activation's input
 
-bool sizes_ok(uint64_t rows, uint64_t cols) { return rows <= kMaxRows && cols <= kMaxCols; }
+bool sizes_ok(uint64_t rows, uint64_t cols, uint64_t most = kMaxCols) { return rows <= kMaxRows && cols <= most; }
 
 bool dtype_ok(int32_t dtype) { return dtype == ASR_F32 || dtype == ASR_BF16; }
 
@@ -859,7 +860,7 @@ asr_status pack(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, uint
     if (!to) return ASR_ERR_INVALID_VALUE;
     if (to->rounding != ASR_ROUND_SR && to->rounding != ASR_ROUND_RNE) return ASR_ERR_UNSUPPORTED_DTYPE;
     if (rows == 0 || cols == 0) return ASR_OK;
-    if (!sizes_ok(rows, cols) || !matrix_ok(x, dtype, x_ld, cols)) return ASR_ERR_INVALID_VALUE;
+    if (!sizes_ok(rows, cols, kMaxWidth) || !matrix_ok(x, dtype, x_ld, cols)) return ASR_ERR_INVALID_VALUE;
     asr_status st = writable(*to, rows, cols);
     if (st == ASR_OK) st = setup();
     if (st != ASR_OK) return st;
@@ -883,7 +884,7 @@ asr_status unpack(const asr_checkpoint *from, uint64_t rows, uint64_t cols, void
     if (!dtype_ok(dtype)) return ASR_ERR_UNSUPPORTED_DTYPE;
     if (!from) return ASR_ERR_INVALID_VALUE;
     if (rows == 0 || cols == 0) return ASR_OK;
-    if (!sizes_ok(rows, cols) || !matrix_ok(dst, dtype, ld, cols)) return ASR_ERR_INVALID_VALUE;
+    if (!sizes_ok(rows, cols, kMaxWidth) || !matrix_ok(dst, dtype, ld, cols)) return ASR_ERR_INVALID_VALUE;
     asr_status st = readable(*from, cols);
     if (st == ASR_OK) st = setup();
     if (st != ASR_OK) return st;
