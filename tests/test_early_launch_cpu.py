@@ -17,3 +17,22 @@ def test_no_read_only_loads_beside_early_launches(name):
     with open(os.path.join(CSRC, name)) as f:
         code = re.sub(r"//[^\n]*", "", f.read())
     assert not re.search(r"__ldg\s*\(|\bld\.global(\.\w+)*\.nc\b|__restrict__", code)
+
+
+@pytest.mark.parametrize("name", ["common.cuh", "checkpoint.cuh", "norm.cuh", "embedding.cuh", "gemm_sr.cuh"])
+def test_no_read_only_loads_in_the_sums_that_start_early(name):
+    """The norm's and the embedding's sums start while the kernel ahead writes what they add up, and the bf16 product may
+    start while its operands are written; the checkpoint's functions are what the sums load and store with."""
+    test_no_read_only_loads_beside_early_launches(name)
+
+
+def test_every_file_with_early_launches_is_looked_at():
+    """All but the 8-bit product of few tokens, whose read-only loads are of the weight and its scales, older than the
+    kernel that it may overlap."""
+    looked_at = {"product.cuh", "int8_product.cuh", "muon.cuh", "skinny.cuh", "int8.cuh", "norm.cuh", "embedding.cuh", "gemm_sr.cuh"}
+    early = set()
+    for name in os.listdir(CSRC):
+        with open(os.path.join(CSRC, name)) as f:
+            if re.search(r"griddepcontrol|launch_early\(", f.read()):
+                early.add(name)
+    assert early - {"int8_few.cuh"} <= looked_at
