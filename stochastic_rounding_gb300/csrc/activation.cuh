@@ -304,15 +304,21 @@ asr_status kind_ok(int32_t dtype, uint32_t function)
     return kept::dtype_ok(dtype) && (function == ASR_SILU || function == ASR_GELU) ? ASR_OK : ASR_ERR_UNSUPPORTED_DTYPE;
 }
 
-// Blocks an SM at most (kept::walk), of bf16; measured at 8,192 x 14,336, us: gated 3:
-// 105, 4: 112; its input kept to nearest, gated, whole rows 2: 153, 3: 164, 4: 170 (but
-// 8,192 x 11,008 2: 157, 4: 127); not gated 3: 94, 2: 105, 4: 105.  Kept stochastically,
-// or not gated and not kept, as many as fit.
+// Blocks an SM at most (kept::walk), of bf16 where rows are whole spans; us of 8,192 rows,
+// capped and as many as fit (four):
+//                                 4,096          8,192          14,336         28,672 (4,096 rows)
+//   gated, 3                      33.3 / 33.2    61.8 / 63.5    104.9 / 111.4  105.0 / 111.4
+//   gated, codes to nearest, 2    47.6 / 51.0    89.9 / 98.7    152.6 / 170.1  152.1 / 169.7
+//   not gated, codes to nearest, 3  30.7 / 30.0  55.6 / 61.6    94.0 / 105.3   94.0 / 105.4
+// (1,024 x 14,336, 0.1 to 2 us the other way).  Rows that end inside a span leave lanes
+// idle, for which more warps make up: 16,384 x 2,752 57.8 / 45.1, 90.1 / 70.8 and 56.0 /
+// 42.8, 8,192 x 6,912 55.4 / 54.1, 102.4 / 82.1 and 51.2 / 47.8, 8,192 x 11,008 83.9 / 85.0,
+// 156.8 / 127.3 and 77.0 / 77.8.  Kept stochastically, or not gated and not kept, as many
+// as fit.
 int forward_limit(int32_t dtype, bool gated, int keep, int how)
 {
-    if (dtype != ASR_BF16 || keep == 2 || (how == kOff && !keep)) return 32;
-    if (gated) return keep == 0 ? 3 : how == kFull ? 2 : 32;
-    return keep ? 3 : 32;
+    if (dtype != ASR_BF16 || how != kFull || keep == 2 || (!gated && !keep)) return 32;
+    return gated && keep ? 2 : 3;
 }
 
 asr_status forward(const void *x, uint64_t x_ld, void *y, uint64_t y_ld, int32_t dtype, uint64_t rows, uint64_t cols,
@@ -379,7 +385,8 @@ asr_status backward(const void *dy, uint64_t dy_ld, const void *x, uint64_t x_ld
     const bool full = cols % kept::kSpan == 0 && P.dy.vec == 2 && P.dx.vec == 2 && (from ? P.from.vec : P.x.vec) == 2;
     const bool off = !P.dy.vec || !P.dx.vec || (!from && !P.x.vec) || (gated && cols % 8 != 0);
     const int how = full ? kFull : off ? kOff : kGeneral;
-    // gated, 8,192 x 11,008 bf16, two blocks: 137 us, three 159; wherever three fit, they do not help
+    // gated from x, bf16, rows that end inside a span: two blocks and three, 8,192 x 11,008 137.5 and 159 us, 8,192 x 6,912
+    // 90.2 and 100, 16,384 x 2,752 79.8 and 94.7, 1,024 x 11,008 22.4 and 21.5; of whole rows either gives the same
     const int limit = dtype == ASR_BF16 && gated && !from && how == kGeneral ? 2 : 32;
     return kept::walk(ASR_KERNEL_ACTIVATION, backward_of(dtype, gated != 0, codes, how), P, rows, cols, kept::kSpan, stream, limit);
 }

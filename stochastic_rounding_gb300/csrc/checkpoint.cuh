@@ -47,12 +47,13 @@ struct Source {
     uint32_t vec;
 };
 
-// Whether kernels look at a unit's bounds: FULL is for matrices of whole spans whose
-// units are all aligned, as the widths of layers are, and leaves out the tests and the
-// element by element accesses.  Only for bf16, whose kernels are bound by their
-// instructions (pack, stochastic: 8,192 x 14,336 84 us, 8,192 x 14,352 without FULL 90;
-// the gated activation's backward pass from codes at 0.96 of the copy rate, 0.88 without
-// at 8,192 x 11,008); f32's are bound by bytes.
+// How many of a unit's values, `most` at most, a row of `cols` has from `col` on.  Kernels
+// have a form, FULL, that does not ask: for matrices of whole spans whose units are all
+// aligned, as the widths of layers are, without the tests and the element by element
+// accesses.  Only for bf16, whose kernels are bound by their instructions (pack,
+// stochastic: 8,192 x 14,336 75 us, 8,192 x 14,352 without FULL 84; the gated activation's
+// backward pass from codes at 0.96 of the copy rate, 0.88 without at 8,192 x 11,008);
+// f32's are bound by bytes.
 __device__ __forceinline__ int live_of(uint32_t cols, uint32_t col, uint32_t most = 8)
 {
     return col >= cols ? 0 : static_cast<int>(cols - col < most ? cols - col : most);
@@ -874,7 +875,8 @@ asr_status pack(const void *x, int32_t dtype, uint64_t rows, uint64_t cols, uint
     if (dtype == ASR_BF16)
         kernel = full ? (sr ? pack_kernel<true, ASR_BF16, true> : pack_kernel<false, ASR_BF16, true>)
                       : (sr ? pack_kernel<true, ASR_BF16, false> : pack_kernel<false, ASR_BF16, false>);
-    // 8,192 x 14,336 bf16: 56.1 us, eight blocks 57.2, four 59.5
+    // bf16, 8,192 rows of 4,096, 8,192, 11,008, 14,336, us: six blocks 18.6, 34.0, 45.2, 55.9, four 20.5, 36.3, 48.1, 59.4, as many
+    // as fit 18.5, 34.1, 45.2, 57.2; stochastic the same from four on
     return walk(ASR_KERNEL_CHECKPOINT, kernel, P, rows, cols, kSpan, stream, 6);
 }
 
@@ -896,7 +898,8 @@ asr_status unpack(const asr_checkpoint *from, uint64_t rows, uint64_t cols, void
     const bool full = cols % kSpan == 0 && P.from.vec == 2 && P.out.vec == 2;
     auto kernel = dtype != ASR_BF16 ? unpack_kernel<ASR_F32, false> : full ? unpack_kernel<ASR_BF16, true>
                                                                            : unpack_kernel<ASR_BF16, false>;
-    // 8,192 x 14,336 bf16: five blocks 58.8 us, eight 63.4, four 61.5; 4,096 x 14,336 f32: three 49.0, six 51.7
+    // 8,192 rows of 4,096, 8,192, 11,008, 14,336, us; bf16: five blocks 20.5, 35.1, 46.8, 58.6, as many as fit 19.2, 37.1, 46.2,
+    // 63.5, four 20.7, 36.9, 49.2, 61.4; f32: three 30.5, 55.2, 71.9, 92.8, as many as fit 30.3, 61.2, 82.6, 104
     return walk(ASR_KERNEL_CHECKPOINT, kernel, P, rows, cols, kSpan, stream, dtype == ASR_BF16 ? 5 : 3);
 }
 
