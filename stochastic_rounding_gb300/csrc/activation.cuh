@@ -11,10 +11,12 @@
 // 2^-24, and |u| 2^-24 from the exponent's rounding) are far below their rounding;
 // f32 results take the library's.  Below u = -87, where e^-u leaves binary32, s is 0.
 //
-// Bound by bytes: an element of x and y each once, the kept form on the way; kept
-// stochastically, by Philox.  Gated silu of 8,192 x 14,336 bf16, one launch after another,
-// with the time of its bytes at 6,697 GB/s: 105 us (105), codes to nearest 153 (141),
-// stochastic 204 (141), backward 181 (175), from codes 147.5 (141).
+// Bound by bytes: an element of x and y each once, the kept form on the way (x is read once
+// more where a gated half is no whole number of groups); kept stochastically, by
+// instructions, 2.5 times as many (issue 62 %, memory 51).  Gated silu of 8,192 x 14,336
+// bf16, one launch after another, with the time of its bytes at 6,697 GB/s: 105 us (105),
+// codes to nearest 153 (141), stochastic 204 (141), backward 181 (175), from codes 147.5
+// (141).
 
 namespace act {
 
@@ -86,7 +88,7 @@ __device__ __forceinline__ uint32_t half_vec(uint32_t vec, uint32_t cols)
 // KEEP: 0 nothing, 1 to nearest, 2 stochastically.  A span is 512 columns of y; the
 // next one's values are fetched before the current one's are worked on.  Registers for
 // four blocks an SM, for three where Philox's come on top, for two of f32 with its values
-// twice as wide.
+// twice as wide; the gated bf16 ones with codes spill 12 to 60 bytes at that.
 template <int DT, bool GATED, int KEEP, bool FULL>
 __global__ void __launch_bounds__(kThreads, DT == ASR_F32 ? 2 : GATED && KEEP == 2 ? 3 : 4) forward_kernel(const __grid_constant__ Params P, uint32_t spans)
 {

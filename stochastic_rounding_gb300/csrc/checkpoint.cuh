@@ -14,10 +14,11 @@
 // above 127 2^e; 32 values rather than a row keep a strong channel from costing the
 // others theirs.
 //
-// Bound by bytes, but for the stochastic form of bf16, which is by Philox's
-// multiplications (8,192 x 14,336 bf16, one launch after another, at 6,697 GB/s 53 us:
-// pack 56, stochastic 75, restore 59).  Pairs of values go through the conversions
-// together (fma.f32x2; pack, stochastic, 82 without).
+// Bound by bytes, but for the stochastic form of bf16, which is by its instructions, twice
+// the other's (8,192 x 14,336 bf16, one launch after another, at 6,697 GB/s 53 us: pack
+// 56, stochastic 75, restore 59): no pipe is full (multiplications 48 %, logic 57, issue
+// 59), but warps come to Philox's multiplications together and wait for that pipe.  Pairs
+// of values go through the conversions together (fma.f32x2; pack, stochastic, 82 without).
 //
 // Random bits: eight values to a Philox counter, sixteen bits each, where the
 // optimizers take four: the generator is a third of the stochastic form's

@@ -23,8 +23,11 @@
 // moves.
 //
 // Bound by bytes: 8,192 tokens of a bf16 table of 128,256 x 4,096, with the time of its
-// bytes at 6,697 GB/s: lookup 20.5 us (20.1), gradient 179 (167), 8 of them the sort's,
-// with zeros beside it.
+// bytes at 6,697 GB/s: lookup 20.5 us (20.1), gradient 178 (167), 8 of them the sort's,
+// with zeros beside it; 32,768 tokens 254 (197), the sort's launches and one block's
+// sums of all counts in front of everything; 262,144 tokens of 1,024 columns 217 to 221
+// (120).  Tokens of one id only have the last block of each slice add up all chunks: 8,192
+// tokens 199, 262,144 tokens 956.
 
 namespace embed {
 
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(kScanThreads) tile_scan_kernel(const __grid_co
     const uint64_t n = static_cast<uint64_t>(P.bins) * P.tiles;
     uint32_t carry = 0;
     for (uint64_t at = 0; at < n; at += kScanThreads * 4) {
-        const uint64_t i = at + threadIdx.x * 4;            // n is a multiple of 4 or less than it
+        const uint64_t i = at + threadIdx.x * 4;            // n may end within the four: two bins of an odd number of tiles
         uint32_t c[4] = {};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -694,10 +697,11 @@ asr_status lookup(const void *ids, int32_t index, uint64_t tokens, const void *t
     return kept::walk(ASR_KERNEL_EMBEDDING, kernel, P, tokens, dim, kept::kSpan, stream);
 }
 
-// Columns go to blocks of up to 128 threads, and tokens to chunks that make 1,216
-// blocks (eight an SM) or more, of 8 to 64 tokens: shorter ones leave more sums in the
-// workspace, longer ones are too few.  Never more than 8,192 chunks, each of which
-// takes two rows of sums.
+// Columns go to blocks of up to 128 threads, and tokens to chunks of 8 to 64, in eights,
+// that make about 1,216 blocks (eight an SM; of 8,192 x 4,096 tokens 32 make 1,024):
+// shorter ones leave more sums in the workspace, longer ones are too few.  More than
+// 524,288 tokens go to longer chunks, of any length: never more than 8,192 of them, each of
+// which takes two rows of sums.
 unsigned threads_of(uint64_t dim)
 {
     return dim >= kSumThreads * 8 ? kSumThreads : static_cast<unsigned>((dim + 255) / 256 * 32);

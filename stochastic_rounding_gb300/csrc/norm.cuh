@@ -20,10 +20,14 @@
 // needs no barrier but the warp's.  Rows that do not fit a block of 1,024 threads are
 // read anew for each sum.
 //
-// Bound by a row's two sums, one behind the other, and by their instructions: bf16 8,192 x
-// 4,096, one launch after another, with the time of its bytes at 6,697 GB/s: norm 26.7 us
-// (20.0), layer norm 30.8, with codes 32.8 and 39.5 (25.2); backward from x 37.0 and 38.1
-// (30.1), from codes 35.0 and 39.6 (25.2), of which the sums of dw take 4.
+// bf16 8,192 x 4,096, one launch after another, with the time of its bytes at 6,697 GB/s:
+// norm 26.6 us (20.0), layer norm 30.8, with codes 32.7 and 39.1 (25.2); backward from x
+// 37.0 and 37.8 (30.1), from codes 35.1 and 39.1 (25.2), of which the sums of dw take 4.
+// Bound forward by instructions, 16 a value, 23 with a mean and 31 with codes too: issue
+// slots are 69 to 73 % full with the memory at 35 to 47 %.  Backward by waiting: two blocks
+// an SM (23 % of its warps) issue in 43 to 52 % of cycles, held up by shared memory and
+// the row's barrier.  f32 from x, 8,192 x 4,096, 104 us (60), by the ring: two rows of it
+// fit, and issue is at 26 %, what is waited for being memory.
 
 namespace norm {
 

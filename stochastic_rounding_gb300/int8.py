@@ -224,7 +224,10 @@ class Int8Linear(_CountedModule):
 
     ``save="int8"`` keeps the input in 8 bits for the backward pass, rounded
     stochastically, in place of the input itself: a little over half of a bf16
-    input's memory, and a weight's gradient that is right on average.
+    input's memory, and a weight's gradient that is right on average.  The forward pass
+    reads the input once more for it, and the backward pass restores the whole input in
+    bf16 for as long as its products take (a step of 8,192 tokens of 4,096 x 4,096 bf16:
+    695 us, 653 with the input itself).
 
     The random bits of an output gradient's element are those of its index in
     (tokens, out_features), from position 0 on, under (seed, pass).  Layers that share a

@@ -8,8 +8,10 @@ package's optimizers.  Nothing here has a second derivative.
 
 A pass that is kept in 8 bits and rounded stochastically takes its random numbers from
 (seed, step), the same for every call with these: modules count their passes (``calls``)
-and go on counting from a state dict.  These numbers are not an optimizer's, nor those
-of ``Int8Linear``'s gradients, whatever the seed; modules that share a seed share them.
+and go on counting from a state dict.  A pass captured into a CUDA graph keeps its
+number, and every replay its random numbers.  These numbers are not an optimizer's, nor
+those of ``Int8Linear``'s gradients, whatever the seed; modules that share a seed share
+them.
 """
 from __future__ import annotations
 
@@ -37,7 +39,8 @@ def activation(x, function="silu", *, gated=False, save=None, rounding="rne", st
     """f(x) for ``x`` (rows, columns), or, ``gated``, f of its first half of columns
     times its second half.  ``function``: "silu", or "gelu" (its tanh form).  With
     ``save`` returns (y, saved) for ``activation_grads``: "input" saves x itself,
-    "int8" its 8-bit checkpoint, made in the same pass."""
+    "int8" its 8-bit checkpoint, made in the same pass (in one of its own where a gated
+    half is no multiple of 32 columns)."""
     _check_save(save)
     _lib._check_rounding(rounding)
     code = _lib._function(function)
@@ -329,7 +332,9 @@ class _EmbeddingFunction(torch.autograd.Function):
 class Embedding(torch.nn.Module):
     """``torch.nn.Embedding`` with a factor on what is looked up (``scale``, such as the
     root of ``dim``).  Its gradient is dense, for this package's optimizers; tokens of
-    ``padding_idx`` add nothing to it."""
+    ``padding_idx`` add nothing to it.  That row is drawn like the others (from a normal
+    distribution of deviation 0.02), and not zeros as in ``torch.nn.Embedding``: zero it,
+    or load a table, where its values matter."""
 
     def __init__(self, vocab: int, dim: int, *, scale: float = 1.0, padding_idx: Optional[int] = None, device=None,
                  dtype=torch.bfloat16):
