@@ -160,3 +160,34 @@ def test_activation_far_from_zero(asr, function, dtype):
     one = u > 25
     assert int(one.sum()) > 1500
     assert torch.equal(y[one], x[one]) and (dx[one] == 1).all()
+
+
+# ------------------------------------------------------------------ in place
+
+@pytest.mark.parametrize("rows,cols", [(9, 24), (1300, 72), (700, 512), (5, 515), (300, 4096), (40, 4104), (2500, 1032), (3, 16384),
+                                       (5, 20001)])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_the_norm_in_place(asr, rows, cols, dtype):
+    """y may be x, with and without codes, of rows with a gap and of either alignment: the same bits, and nothing written
+    between the rows."""
+    import torch
+    g = torch.Generator("cuda").manual_seed(cols)
+    dt = getattr(torch, dtype)
+    x = torch.randn(rows, cols, device="cuda", generator=g).to(dt)
+    w, b = (torch.randn(cols, device="cuda", generator=g).to(dt) for _ in range(2))
+    for centred in (True, False):
+        want, saved = asr.layer_norm(x, w, b, centred=centred, save="int8", rounding="sr", step=2, seed=1)
+        for off, gap in ((0, 0), (0, 32), (1, 3)):
+            buf = torch.full((off + rows * (cols + gap),), 7.0, dtype=dt, device="cuda")
+            z = buf[off:].view(rows, cols + gap)[:, :cols]
+            for keep in (False, True):
+                z.copy_(x)
+                q = torch.empty(rows, cols, dtype=torch.int8, device="cuda")
+                power = torch.empty(rows, -(-cols // 32), dtype=torch.uint8, device="cuda")
+                rstd = torch.empty(rows, device="cuda")
+                asr.asr_layer_norm(z, w, b, z, None, rstd, centred=centred, keep=(q, power) if keep else None, rounding="sr",
+                                   step=2, seed=1)
+                assert torch.equal(z, want) and torch.equal(rstd, saved.rstd)
+                assert (buf[:off] == 7).all() and (buf[off:].view(rows, cols + gap)[:, cols:] == 7).all()
+                if keep:
+                    assert torch.equal(q, saved.input.q) and torch.equal(power, saved.input.power)
